@@ -55,6 +55,11 @@ extern "C" {
                       2.2): 0.5 instead of 1 byte per weight, unpacked by the
                       GEMM.  Results are bit-identical to QMM_Q4_K's. */
 
+/* Element types of activation tensors. */
+#define QMM_F32 0
+#define QMM_F16 1
+#define QMM_BF16 2
+
 /* Return codes. */
 #define QMM_OK 0
 #define QMM_EINVAL (-1) /* bad argument: type, size, null or misaligned pointer */
@@ -72,6 +77,9 @@ extern "C" {
 
 /* Compute units a launch plan (qmm_mmq_plan) may be asked for: 1 .. QMM_MAX_CUS. */
 #define QMM_MAX_CUS 65536
+
+/* Largest stride (in elements) from row to row of a strided tensor. */
+#define QMM_MAX_STRIDE (1 << 24)
 
 /* Tokens are padded to a multiple of this many in the qact buffer. */
 #define QMM_TOKEN_PAD 128
@@ -197,6 +205,78 @@ size_t qmm_qact_bytes(int64_t n_tok, int64_t id);
  */
 int qmm_quantize_activations(const float *x, int64_t n_tok, int64_t id, void *qact,
                              size_t qact_bytes, void *stream);
+
+/*
+ * qmm_dequantize_activations -- read a qact buffer back: out[t][k] = dh * q, the
+ * number each code stands for, rounded once to the element type (a product of
+ * an f16 and a 7-bit integer: exact in f32).
+ *   qact, qact_bytes  a buffer for these n_tok and id, 16-byte aligned
+ *   type        QMM_F32, QMM_F16 or QMM_BF16
+ *   out         device [n_tok] rows of id elements, out_stride elements from
+ *               row to row (>= id, a multiple of 4); 16-byte aligned.  Padding
+ *               tokens are not written.  Must not overlap qact.
+ * Errors: QMM_EINVAL, QMM_EHIP.
+ */
+int qmm_dequantize_activations(const void *qact, size_t qact_bytes, int64_t n_tok, int64_t id,
+                               int type, void *out, int64_t out_stride, void *stream);
+
+/* Norm kinds: over a row x of id elements,
+ *   QMM_NORM_RMS    x_k / sqrt(mean(x^2) + eps) * weight_k + bias_k
+ *   QMM_NORM_LAYER  (x_k - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight_k + bias_k */
+#define QMM_NORM_RMS 0
+#define QMM_NORM_LAYER 1
+
+/* What qmm_norm_quantize works on.  Zero the struct, then set what is wanted.
+ * Tensors are device memory of n_tok rows of id elements of `type`, a stride
+ * (in elements) from row to row: a multiple of 4 in [id, QMM_MAX_STRIDE];
+ * pointers 16-byte aligned.  The vectors are f32 [id], 16-byte aligned. */
+typedef struct {
+    int32_t type;             /* QMM_F32, QMM_F16 or QMM_BF16: h, y, gate, h_out, normed */
+    int32_t kind;             /* QMM_NORM_RMS or QMM_NORM_LAYER, both norms */
+    float eps;                /* > 0, finite */
+    float residual_scale;     /* rs: factor of h in the sum */
+    float block_scale;        /* bs: factor of the block's part in the sum */
+    const void *h;            /* the residual stream */
+    int64_t h_stride;
+    const void *y;            /* the block's output, or NULL: nothing is added */
+    int64_t y_stride;
+    const float *post_weight; /* norm after the block, of y: its weight, or NULL: y as it is */
+    const float *post_bias;   /* its bias or NULL (only with post_weight) */
+    const void *gate;         /* factor of the block's part, or NULL (only with y): */
+    int64_t gate_stride;      /* 0: one row for every token, else a row per token */
+    const float *weight;      /* norm before the next block, of the sum: its weight ... */
+    const float *bias;        /* ... and bias, or NULL */
+    void *h_out;              /* receives the sum, or NULL */
+    int64_t h_out_stride;
+    void *normed;             /* receives the norm of the sum, or NULL */
+    int64_t normed_stride;
+    void *qact;               /* receives the norm of the sum as q8 blocks, or NULL */
+    size_t qact_bytes;        /* qmm_qact_bytes(n_tok, id), or 0 without qact */
+} qmm_norm;
+
+/*
+ * qmm_norm_quantize -- what stands between two blocks of a layer, in one pass
+ * per row: the norm after a block, its gate, the scaled residual sum, the norm
+ * before the next block and its quantization for the next qmm_mmq.
+ *   u      = gate * norm(y; post_weight, post_bias)   (each step where given)
+ *   s      = rs * h + bs * u, rounded once to `type`  (rs * h without y)
+ *   h_out  = s
+ *   n      = norm(s; weight, bias)
+ *   normed = n rounded to `type`;  qact = the q8 blocks of n, not of its
+ *            rounding, as qmm_quantize_activations writes them (padding
+ *            tokens zero; |n| <= 2046 as there)
+ * At least one of h_out, normed and qact is given; everything is computed in
+ * f32, and the second norm is that of s as `type` holds it, whether h_out is
+ * stored or not.  A row's result does not depend on the other rows or on which
+ * outputs are wanted.  Values whose squares overflow f32 when summed give
+ * infinities or NaN in their own row only.
+ * An output may be one of the inputs in place (same pointer and stride): h_out
+ * may be h or y; normed may be y, or h where h_out is NULL.  Any other overlap
+ * of an output with h, y, gate or another output is refused.
+ * No workspace; can be captured into a graph.
+ * Errors: QMM_EINVAL, QMM_EHIP.  n_tok == 0 is an empty batch.
+ */
+int qmm_norm_quantize(const qmm_norm *args, int64_t n_tok, int64_t id, void *stream);
 
 /*
  * qmm_mmq -- the GEMM: out[t][j] = sum over 32-blocks c of

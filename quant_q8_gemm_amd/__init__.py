@@ -8,11 +8,17 @@ built, importing this package raises immediately -- there is no other path.
     w = qmm.register_weights(qmm.Q6_K, od, id, raw_bytes)      # numpy uint8
     qact = qmm.quantize_activations(x)                          # x: cuda f32 [T][id]
     out = qmm.mmq(w, qact, n_tok)                               # cuda f32 [T][od]
+
+and what stands between the products of a layer:
+
+    r = qmm.norm_quantize(h, weight, y=out)                     # r.h = h + out, r.qact = q8(norm(r.h))
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -46,8 +52,13 @@ BLOCK_BYTES = {Q4_K: 144, Q4_K_PACKED: 144, Q6_K: 210}
 # The full list of entry points include/qmm.h declares.
 EXPORTS = ("qmm_register_weights", "qmm_weights_info", "qmm_weights_export", "qmm_release_weights",
            "qmm_set_memory_cap", "qmm_qact_bytes", "qmm_quantize_activations", "qmm_mmq",
-           "qmm_mmq_noalloc", "qmm_stream_release", "qmm_mmq_plan", "qmm_mmq_plan_work", "qmm_last_error")
+           "qmm_mmq_noalloc", "qmm_stream_release", "qmm_mmq_plan", "qmm_mmq_plan_work", "qmm_last_error",
+           "qmm_dequantize_activations", "qmm_norm_quantize")
 MAX_CUS = 65536
+# element types of activation tensors
+F32, F16, BF16 = 0, 1, 2
+ELEM_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+NORM_KINDS = {"rms": 0, "layer": 1}
 
 
 class Info(ctypes.Structure):
@@ -63,6 +74,17 @@ class Plan(ctypes.Structure):
                 ("tile_tokens", ctypes.c_int32), ("k_groups", ctypes.c_int32), ("per_cu", ctypes.c_int32),
                 ("row_tiles", ctypes.c_int32), ("tok_tiles", ctypes.c_int32), ("dp_row_tiles", ctypes.c_int32),
                 ("n_tail", ctypes.c_int32), ("split", ctypes.c_int32), ("nsb", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("kind", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("h", ctypes.c_void_p), ("h_stride", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("y_stride", ctypes.c_int64), ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("h_out", ctypes.c_void_p), ("h_out_stride", ctypes.c_int64),
+                ("normed", ctypes.c_void_p), ("normed_stride", ctypes.c_int64), ("qact", ctypes.c_void_p),
+                ("qact_bytes", ctypes.c_size_t)]
 
 
 _P = ctypes.c_void_p
@@ -93,6 +115,10 @@ _lib.qmm_mmq_plan.restype = ctypes.c_int
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _lib.qmm_mmq_plan_work.argtypes = [ctypes.POINTER(Plan), _I64, _I32P, _I32P, _I32P, _I32P]
 _lib.qmm_mmq_plan_work.restype = ctypes.c_int
+_lib.qmm_dequantize_activations.argtypes = [_P, _SZ, _I64, _I64, ctypes.c_int, _P, _I64, _P]
+_lib.qmm_dequantize_activations.restype = ctypes.c_int
+_lib.qmm_norm_quantize.argtypes = [ctypes.POINTER(Norm), _I64, _I64, _P]
+_lib.qmm_norm_quantize.restype = ctypes.c_int
 _lib.qmm_last_error.argtypes = []
 _lib.qmm_last_error.restype = ctypes.c_char_p
 
@@ -255,3 +281,123 @@ def mmq_plan_work(plan: Plan, wg: int):
     out = [ctypes.c_int32() for _ in range(4)]
     _check(_lib.qmm_mmq_plan_work(ctypes.byref(plan), int(wg), *[ctypes.byref(o) for o in out]))
     return tuple(o.value for o in out)
+
+
+# ---- what stands between the products ----
+
+def _elem(dtype, what: str = "dtype") -> int:
+    t = ELEM_TYPES.get(dtype)
+    if t is None:
+        raise QmmError(EINVAL, f"{what} must be float32, float16 or bfloat16, got {dtype}")
+    return t
+
+
+def _device(t, what: str) -> int:
+    """The index of t's device, which has to be the current one."""
+    if not t.is_cuda:
+        raise QmmError(EINVAL, f"{what} must be a cuda tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise QmmError(EINVAL, f"{what} is on device {t.get_device()} but device {torch.cuda.current_device()} is current")
+    return t.get_device()
+
+
+def _rows(t, what: str, shape, dtype=None):
+    """(address, stride) of a tensor of rows with adjacent elements; the library checks the rest."""
+    if t is None:
+        return None, 0
+    _device(t, what)
+    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+        raise QmmError(EINVAL, f"{what} must be {list(shape)} {dtype or ''}, got {list(t.shape)} {t.dtype}")
+    if t.stride(1) != 1 and shape[1] > 1:
+        raise QmmError(EINVAL, f"{what} must have adjacent elements in a row")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t, what: str, n: int):
+    if t is None:
+        return None
+    _device(t, what)
+    if t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise QmmError(EINVAL, f"{what} must be a contiguous float32 [{n}] tensor")
+    return t.data_ptr()
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream it is written on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def dequantize_activations(qact, n_tok: int, id_: int, dtype=torch.float32, out=None, stream=None):
+    """The numbers a qact buffer stands for: [n_tok][id] of dtype (float32, float16 or bfloat16)."""
+    _check_qact(qact)
+    _device(qact, "qact")
+    if out is None:
+        _elem(dtype)
+        out = _empty((n_tok, id_), dtype, qact.device, stream)
+    ptr, stride = _rows(out, "out", (n_tok, id_))
+    _check(_lib.qmm_dequantize_activations(qact.data_ptr(), qact.numel(), n_tok, id_, _elem(out.dtype, "out"), ptr,
+                                           stride, _stream(stream)))
+    return out
+
+
+class NormResult(NamedTuple):
+    h: object       # the sum, or None
+    normed: object  # its norm as numbers, or None
+    qact: object    # its norm as q8 blocks, or None
+
+
+def norm_quantize(h, weight, *, y=None, bias=None, post_weight=None, post_bias=None, gate=None,
+                  residual_scale: float = 1.0, block_scale: float = 1.0, kind: str = "rms", eps: float = 1e-5,
+                  h_out=True, normed=False, qact=True, stream=None) -> NormResult:
+    """Norm after a block, gate, scaled residual sum, norm before the next block and its q8 blocks in one pass:
+
+        s = residual_scale * h + block_scale * gate * norm(y; post_weight, post_bias),  n = norm(s; weight, bias)
+
+    h, y: cuda [n_tok][id] of float32, float16 or bfloat16 (rows may be strided); gate: [id] or [n_tok][id] of the
+    same type; weights and biases float32 [id]; kind "rms" or "layer".  h_out (s), normed (n) and qact (n quantized):
+    True for a new tensor, a tensor to write into, or False.  h_out may be h or y itself."""
+    if h.dim() != 2:
+        raise QmmError(EINVAL, "h must be [n_tok][id]")
+    n_tok, id_ = h.shape
+    device, dtype = h.device, h.dtype
+    a = Norm(type=_elem(dtype, "h"), eps=eps, residual_scale=residual_scale, block_scale=block_scale)
+    if kind not in NORM_KINDS:
+        raise QmmError(EINVAL, f"kind must be 'rms' or 'layer', got {kind!r}")
+    a.kind = NORM_KINDS[kind]
+    shape = (n_tok, id_)
+    a.h, a.h_stride = _rows(h, "h", shape)
+    if y is not None:
+        a.y, a.y_stride = _rows(y, "y", shape, dtype)
+    a.weight = _vector(weight, "weight", id_)
+    if bias is not None:
+        a.bias = _vector(bias, "bias", id_)
+    if post_weight is not None:
+        a.post_weight = _vector(post_weight, "post_weight", id_)
+    if post_bias is not None:
+        a.post_bias = _vector(post_bias, "post_bias", id_)
+    if gate is not None:
+        if gate.dim() == 1:
+            a.gate, a.gate_stride = _rows(gate.unsqueeze(0), "gate", (1, id_), dtype)[0], 0
+        else:
+            a.gate, a.gate_stride = _rows(gate, "gate", shape, dtype)
+    h_out = _empty(shape, dtype, device, stream) if h_out is True else None if h_out is False else h_out
+    if h_out is not None:
+        a.h_out, a.h_out_stride = _rows(h_out, "h_out", shape, dtype)
+    normed = _empty(shape, dtype, device, stream) if normed is True else None if normed is False else normed
+    if normed is not None:
+        a.normed, a.normed_stride = _rows(normed, "normed", shape, dtype)
+    if qact is True:
+        qact = _empty((qact_bytes(n_tok, id_),), torch.uint8, device, stream)
+    elif qact is False:
+        qact = None
+    if qact is not None:
+        _check_qact(qact)
+        _device(qact, "qact")
+        a.qact, a.qact_bytes = qact.data_ptr(), qact.numel()
+    _check(_lib.qmm_norm_quantize(ctypes.byref(a), n_tok, id_, _stream(stream)))
+    return NormResult(h_out, normed, qact)

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -276,6 +277,155 @@ int qmm_quantize_activations(const float* x, int64_t n_tok, int64_t id, void* qa
   hipError_t e = qmm::launch_quantize(x, n_tok, token_pad(n_tok), id, (uint8_t*)qact,
                                       (hipStream_t)stream);
   if (e != hipSuccess) return fail_hip(e, "quantize launch");
+  ok();
+  return QMM_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- qmm_norm_quantize, qmm_dequantize_activations ----
+
+int check_elem(const char* what, int type) {
+  if (type != QMM_F32 && type != QMM_F16 && type != QMM_BF16)
+    return fail(QMM_EINVAL, "%s must be QMM_F32 (%d), QMM_F16 (%d) or QMM_BF16 (%d), got %d", what, QMM_F32, QMM_F16,
+                QMM_BF16, type);
+  return QMM_OK;
+}
+
+size_t elem_bytes(int type) { return type == QMM_F32 ? 4 : 2; }
+
+// Rows of `cols` elements, `stride` elements apart, accessed four elements at a time.
+int check_rows(const char* what, const void* p, int64_t stride, int64_t cols) {
+  if (!aligned(p, 16)) return fail(QMM_EINVAL, "%s must be 16-byte aligned", what);
+  if (stride < cols || stride % 4 != 0 || stride > QMM_MAX_STRIDE)
+    return fail(QMM_EINVAL, "%s_stride must be a multiple of 4 in [%lld, %lld], got %lld", what, (long long)cols,
+                (long long)QMM_MAX_STRIDE, (long long)stride);
+  return QMM_OK;
+}
+
+// A range of device bytes with the layout of its rows.
+struct Range {
+  const char* what;
+  const void* p;
+  int64_t stride;  // bytes from row to row
+  size_t bytes;    // from the first byte to the last
+};
+
+Range rows_range(const char* what, const void* p, int64_t stride, int64_t rows, int64_t cols, size_t elem) {
+  if (p == nullptr) return {what, p, 0, 0};
+  return {what, p, stride * (int64_t)elem, (size_t)((rows - 1) * stride + cols) * elem};
+}
+
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.p != nullptr && b.p != nullptr && x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether an output that overlaps an input is that input in place.
+bool same_rows(const Range& a, const Range& b) { return a.p == b.p && a.stride == b.stride && a.bytes == b.bytes; }
+
+int refuse_overlap(const Range& a, const Range& b) {
+  return fail(QMM_EINVAL, "%s overlaps %s", a.what, b.what);
+}
+
+int check_vector(const char* what, const float* p) {
+  return aligned(p, 16) ? QMM_OK : fail(QMM_EINVAL, "%s must be 16-byte aligned", what);
+}
+
+}  // namespace
+
+extern "C" {
+
+int qmm_dequantize_activations(const void* qact, size_t qact_bytes, int64_t n_tok, int64_t id, int type, void* out,
+                               int64_t out_stride, void* stream) {
+  if (int rc = check_tokens(n_tok)) return rc;
+  if (int rc = check_id(id)) return rc;
+  if (int rc = check_elem("type", type)) return rc;
+  const size_t need = qmm_qact_bytes(n_tok, id);
+  if (qact_bytes != need)
+    return fail(QMM_EINVAL, "qact_bytes %zu != qmm_qact_bytes(%lld, %lld) = %zu", qact_bytes, (long long)n_tok,
+                (long long)id, need);
+  if (n_tok == 0) {
+    ok();
+    return QMM_OK;
+  }
+  if (qact == nullptr || out == nullptr) return fail(QMM_EINVAL, "qact or out is NULL");
+  if (!aligned(qact, 16)) return fail(QMM_EINVAL, "qact must be 16-byte aligned");
+  if (int rc = check_rows("out", out, out_stride, id)) return rc;
+  const Range r = rows_range("out", out, out_stride, n_tok, id, elem_bytes(type)), q{"qact", qact, 0, qact_bytes};
+  if (overlap(r, q)) return refuse_overlap(r, q);
+  hipError_t e = qmm::launch_dequantize((const uint8_t*)qact, n_tok, token_pad(n_tok), id, type, out, out_stride,
+                                        (hipStream_t)stream);
+  if (e != hipSuccess) return fail_hip(e, "dequantize launch");
+  ok();
+  return QMM_OK;
+}
+
+int qmm_norm_quantize(const qmm_norm* args, int64_t n_tok, int64_t id, void* stream) {
+  if (args == nullptr) return fail(QMM_EINVAL, "args is NULL");
+  const qmm_norm& a = *args;
+  if (int rc = check_tokens(n_tok)) return rc;
+  if (int rc = check_id(id)) return rc;
+  if (int rc = check_elem("type", a.type)) return rc;
+  if (a.kind != QMM_NORM_RMS && a.kind != QMM_NORM_LAYER)
+    return fail(QMM_EINVAL, "kind must be QMM_NORM_RMS (%d) or QMM_NORM_LAYER (%d), got %d", QMM_NORM_RMS,
+                QMM_NORM_LAYER, a.kind);
+  if (!(a.eps > 0.0f) || !std::isfinite(a.eps)) return fail(QMM_EINVAL, "eps must be positive and finite");
+  if (!std::isfinite(a.residual_scale) || !std::isfinite(a.block_scale))
+    return fail(QMM_EINVAL, "residual_scale and block_scale must be finite");
+  const size_t need = a.qact != nullptr ? qmm_qact_bytes(n_tok, id) : 0;
+  if (a.qact_bytes != need)
+    return fail(QMM_EINVAL, "qact_bytes %zu != %zu for n_tok=%lld id=%lld %s", a.qact_bytes, need, (long long)n_tok,
+                (long long)id, a.qact != nullptr ? "" : "without qact");
+  if (n_tok == 0) {  // empty batch: no rows, pointers are not used
+    ok();
+    return QMM_OK;
+  }
+  if (a.h == nullptr || a.weight == nullptr) return fail(QMM_EINVAL, "h or weight is NULL");
+  if (a.h_out == nullptr && a.normed == nullptr && a.qact == nullptr)
+    return fail(QMM_EINVAL, "no output: h_out, normed and qact are NULL");
+  if (a.y == nullptr && (a.post_weight != nullptr || a.gate != nullptr))
+    return fail(QMM_EINVAL, "post_weight and gate need y");
+  if (a.post_weight == nullptr && a.post_bias != nullptr) return fail(QMM_EINVAL, "post_bias needs post_weight");
+  if (int rc = check_rows("h", a.h, a.h_stride, id)) return rc;
+  if (a.y != nullptr)
+    if (int rc = check_rows("y", a.y, a.y_stride, id)) return rc;
+  if (a.gate != nullptr)  // a single row of any stride stands for every token when its stride is 0
+    if (int rc = check_rows("gate", a.gate, a.gate_stride == 0 ? id : a.gate_stride, id)) return rc;
+  if (a.h_out != nullptr)
+    if (int rc = check_rows("h_out", a.h_out, a.h_out_stride, id)) return rc;
+  if (a.normed != nullptr)
+    if (int rc = check_rows("normed", a.normed, a.normed_stride, id)) return rc;
+  if (!aligned(a.qact, 16)) return fail(QMM_EINVAL, "qact must be 16-byte aligned");
+  if (int rc = check_vector("weight", a.weight)) return rc;
+  if (int rc = check_vector("bias", a.bias)) return rc;
+  if (int rc = check_vector("post_weight", a.post_weight)) return rc;
+  if (int rc = check_vector("post_bias", a.post_bias)) return rc;
+  const size_t eb = elem_bytes(a.type);
+  const Range h = rows_range("h", a.h, a.h_stride, n_tok, id, eb), y = rows_range("y", a.y, a.y_stride, n_tok, id, eb);
+  const Range outs[] = {rows_range("h_out", a.h_out, a.h_out_stride, n_tok, id, eb),
+                        rows_range("normed", a.normed, a.normed_stride, n_tok, id, eb),
+                        {"qact", a.qact, 0, need}};
+  const Range fixed[] = {rows_range("gate", a.gate, a.gate_stride, a.gate_stride == 0 ? 1 : n_tok, id, eb),
+                         {"weight", a.weight, 0, (size_t)id * 4},
+                         {"bias", a.bias, 0, (size_t)id * 4},
+                         {"post_weight", a.post_weight, 0, (size_t)id * 4},
+                         {"post_bias", a.post_bias, 0, (size_t)id * 4}};
+  for (int i = 0; i < 3; ++i) {
+    const bool rows = i < 2;  // h_out and normed may be computed in place
+    const bool in_h = rows && (i == 0 || a.h_out == nullptr) && same_rows(outs[i], h);
+    const bool in_y = rows && same_rows(outs[i], y);
+    if (overlap(outs[i], h) && !in_h) return refuse_overlap(outs[i], h);
+    if (overlap(outs[i], y) && !in_y) return refuse_overlap(outs[i], y);
+    for (const Range& f : fixed)
+      if (overlap(outs[i], f)) return refuse_overlap(outs[i], f);
+    for (int k = 0; k < i; ++k)
+      if (overlap(outs[i], outs[k])) return refuse_overlap(outs[i], outs[k]);
+  }
+  hipError_t e = qmm::launch_norm(a, n_tok, a.qact != nullptr ? token_pad(n_tok) : 0, id, (hipStream_t)stream);
+  if (e != hipSuccess) return fail_hip(e, "norm launch");
   ok();
   return QMM_OK;
 }

@@ -32,4 +32,32 @@ __device__ __forceinline__ float f16_bits_to_float(uint32_t bits) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
 }
 
+// Activations of the element types QMM_F32, QMM_F16 and QMM_BF16 (0, 1, 2),
+// always computed on as f32: a conversion to f32 is exact, one back rounds to
+// nearest even, once, where the value is stored.
+template <int TYPE>
+struct Elem;
+template <>
+struct Elem<0> { typedef float type; };
+template <>
+struct Elem<1> { typedef _Float16 type; };
+template <>
+struct Elem<2> { typedef __bf16 type; };
+template <int TYPE>
+using elem_t = typename Elem<TYPE>::type;
+
+// Four consecutive elements at p[i] .. p[i + 3]; p + i is aligned to four of them.
+template <int TYPE>
+__device__ __forceinline__ float4 load4(const void* p, int64_t i) {
+  typedef elem_t<TYPE> v4 __attribute__((ext_vector_type(4)));
+  const v4 v = *(const v4*)((const elem_t<TYPE>*)p + i);
+  return make_float4((float)v.x, (float)v.y, (float)v.z, (float)v.w);
+}
+template <int TYPE>
+__device__ __forceinline__ void store4(void* p, int64_t i, const float4& f) {
+  typedef elem_t<TYPE> T;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  *(v4*)((T*)p + i) = v4{(T)f.x, (T)f.y, (T)f.z, (T)f.w};
+}
+
 }  // namespace qmm

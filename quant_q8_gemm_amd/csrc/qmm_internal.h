@@ -6,6 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "../../include/qmm.h"
+
 namespace qmm {
 
 // Device planes of one registered weight matrix (layout documented in
@@ -45,6 +47,11 @@ size_t wsm_bytes(int type, int64_t od_pad, int64_t id);
 hipError_t launch_repack(const uint8_t* raw, const Planes& p, hipStream_t s);
 hipError_t launch_quantize(const float* x, int64_t n_tok, int64_t t_pad, int64_t id,
                            uint8_t* qact, hipStream_t s);
+// The norms and residual sum of qmm_norm_quantize on checked arguments
+// (t_pad: the tokens of the qact buffer, 0 without one).
+hipError_t launch_norm(const qmm_norm& a, int64_t n_tok, int64_t t_pad, int64_t id, hipStream_t s);
+hipError_t launch_dequantize(const uint8_t* qact, int64_t n_tok, int64_t t_pad, int64_t id, int type, void* out,
+                             int64_t out_stride, hipStream_t s);
 // MMQ launch plan: tile geometry, and for a ragged last wave the K split of the
 // tail tiles and the scratch they need (n_tail tiles x split partials).
 struct MmqPlan {

@@ -3,6 +3,7 @@
 // MFMA fragment order the MMQ reads.
 #include "qmm_internal.h"
 #include "qmm_common.h"
+#include "qmm_quant.h"
 
 #include "../../include/qmm.h"
 
@@ -18,62 +19,6 @@ namespace qmm {
 // (DPP moves).
 // ---------------------------------------------------------------------------
 constexpr int kQuantChunks = 2;
-
-// DPP controls: swap neighbours in a quad, swap pairs in a quad, and mirror
-// each half-row of 8 lanes (lane i <-> 7 - i).  After the two quad steps every
-// lane of a quad holds the quad's result, so the mirror step combines the two
-// quads of an aligned group of 8 lanes.
-constexpr int kDppQuadXor1 = 0xB1;     // quad_perm [1, 0, 3, 2]
-constexpr int kDppQuadXor2 = 0x4E;     // quad_perm [2, 3, 0, 1]
-constexpr int kDppHalfMirror = 0x141;  // row_half_mirror
-
-template <int CTRL>
-__device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
-}
-
-// Maximum of non-negative finite floats over the 8 lanes, on their bit patterns
-// (ordered like the values), so each step is one integer max.
-__device__ __forceinline__ float max8(float v) {
-  uint32_t u = __builtin_bit_cast(uint32_t, v);
-  u = max(u, (uint32_t)dpp<kDppQuadXor1>((int)u));
-  u = max(u, (uint32_t)dpp<kDppQuadXor2>((int)u));
-  u = max(u, (uint32_t)dpp<kDppHalfMirror>((int)u));
-  return __builtin_bit_cast(float, u);
-}
-
-__device__ __forceinline__ int sum8(int v) {
-  v += dpp<kDppQuadXor1>(v);
-  v += dpp<kDppQuadXor2>(v);
-  return v + dpp<kDppHalfMirror>(v);
-}
-
-// q = clamp(rint(v / dh), -127, 127) where v / dh is the correctly rounded f32
-// quotient (IEEE division) and rint rounds half to even.  The correctly rounded
-// division costs about a dozen instructions, so the quotient is first formed as
-// v * rcp(dh): with |v / dh| <= 127.1 (|v| <= amax, dh = f16(amax/127)) the
-// reciprocal (1 ulp) and the product (0.5 ulp) put it within 2.3e-5 of the
-// exact quotient, and the correctly rounded quotient is within 3.8e-6 of it.
-// So unless the product lies within 1e-4 of a half-integer, both round to the
-// same integer; when one of a lane's four products does, the lane divides all
-// four exactly.  With dh == 0 the reciprocal is taken as 0, which gives q = 0.
-__device__ __forceinline__ void quant4(const float4& v, float dhf, float inv, int q[4]) {
-  const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-  float n[4], e[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    n[i] = __builtin_rintf(r[i]);
-    e[i] = fabsf(r[i] - n[i]);
-  }
-  if (fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > 0.5f - 1e-4f) {
-    n[0] = __builtin_rintf(v.x / dhf);
-    n[1] = __builtin_rintf(v.y / dhf);
-    n[2] = __builtin_rintf(v.z / dhf);
-    n[3] = __builtin_rintf(v.w / dhf);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = (int)__builtin_amdgcn_fmed3f(n[i], -127.0f, 127.0f);
-}
 
 __global__ void __launch_bounds__(256)
 quantize_kernel(const float* __restrict__ x, int n_tok, int id, int nchunk, int chunk_major,
@@ -100,23 +45,10 @@ quantize_kernel(const float* __restrict__ x, int n_tok, int id, int nchunk, int 
     const int c = c0 + i;
     if (c >= nchunk) break;
     if (!block_full && !live) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float amax = max8(fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)),
-                                  fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
-    const float d32 = amax / 127.0f;
-    const _Float16 dh = (_Float16)d32;  // round to nearest even
-    const float dhf = (float)dh;
-    const float inv = dhf == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(dhf);
-    int q[4];
-    quant4(v[i], dhf, inv, q);
-    const int S = sum8(q[0] + q[1] + q[2] + q[3]);
-    const _Float16 sh = (_Float16)(dhf * (float)S);  // the product is exact in f32
-    const uint32_t packed = (uint32_t)(q[0] & 255) | ((uint32_t)(q[1] & 255) << 8) |
-                            ((uint32_t)(q[2] & 255) << 16) | ((uint32_t)(q[3] & 255) << 24);
+    const Q8Quad r = quant_quad(v[i]);
     const int64_t frag = (int64_t)tb * nchunk + c;
-    *(uint32_t*)(qq + frag * 1024 + (sub >> 2) * 512 + tt * 16 + (sub & 3) * 4) = packed;
-    if (sub == 0)
-      *(uint32_t*)(qs + frag * 128 + tt * 4) =
-          (uint32_t)__builtin_bit_cast(uint16_t, dh) | ((uint32_t)__builtin_bit_cast(uint16_t, sh) << 16);
+    *(uint32_t*)(qq + frag * 1024 + (sub >> 2) * 512 + tt * 16 + (sub & 3) * 4) = r.codes;
+    if (sub == 0) *(uint32_t*)(qs + frag * 128 + tt * 4) = r.pair();
   }
 }
 
@@ -133,6 +65,42 @@ hipError_t launch_quantize(const float* x, int64_t n_tok, int64_t t_pad, int64_t
   const dim3 grid = chunk_major ? dim3(n_cg, n_tb) : dim3(n_tb, n_cg);
   quantize_kernel<<<grid, dim3(256), 0, s>>>(x, (int)n_tok, (int)id, (int)nchunk, chunk_major, qact,
                                              qact + (size_t)t_pad * (size_t)id);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Reading a qact buffer back: a thread per four codes of one token and chunk, in
+// the prepass's mapping (its fragment words back into rows of numbers).
+// ---------------------------------------------------------------------------
+template <int TYPE>
+__global__ void __launch_bounds__(256)
+dequantize_kernel(const uint8_t* __restrict__ qq, const uint8_t* __restrict__ qs, int n_tok, int nchunk,
+                  void* __restrict__ out, int64_t out_stride) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tt = wave * 8 + (lane >> 3), sub = lane & 7;
+  const int64_t t = (int64_t)blockIdx.y * 32 + tt;
+  if (t >= n_tok) return;
+#pragma unroll
+  for (int i = 0; i < kQuantChunks; ++i) {
+    const int c = blockIdx.x * kQuantChunks + i;
+    if (c >= nchunk) break;
+    const int64_t frag = (int64_t)blockIdx.y * nchunk + c;
+    const int q = *(const int*)(qq + frag * 1024 + (sub >> 2) * 512 + tt * 16 + (sub & 3) * 4);
+    const float dh = f16_bits_to_float(*(const uint32_t*)(qs + frag * 128 + tt * 4) & 0xFFFF);
+    store4<TYPE>(out, t * out_stride + 32 * c + 4 * sub,
+                 make_float4(dh * (float)(int8_t)q, dh * (float)(int8_t)(q >> 8), dh * (float)(int8_t)(q >> 16),
+                             dh * (float)(q >> 24)));
+  }
+}
+
+hipError_t launch_dequantize(const uint8_t* qact, int64_t n_tok, int64_t t_pad, int64_t id, int type, void* out,
+                             int64_t out_stride, hipStream_t s) {
+  const int64_t nchunk = id / 32;
+  const dim3 grid((unsigned)((nchunk + kQuantChunks - 1) / kQuantChunks), (unsigned)((n_tok + 31) / 32));
+  const uint8_t* qs = qact + (size_t)t_pad * (size_t)id;
+  const auto kernel = type == QMM_F32 ? dequantize_kernel<QMM_F32>
+                    : type == QMM_F16 ? dequantize_kernel<QMM_F16> : dequantize_kernel<QMM_BF16>;
+  kernel<<<grid, dim3(256), 0, s>>>(qact, qs, (int)n_tok, (int)nchunk, out, out_stride);
   return hipGetLastError();
 }
 

@@ -1,0 +1,97 @@
+// qmm_quant.h -- the arithmetic of one q8 block of 32 activations, shared by every
+// kernel that writes such blocks: eight lanes hold a block, four consecutive
+// values each (lanes 8i .. 8i + 7 of a wave).
+#pragma once
+
+#include "qmm_common.h"
+
+namespace qmm {
+
+// DPP controls: swap neighbours in a quad, swap pairs in a quad, and mirror
+// each half-row of 8 lanes (lane i <-> 7 - i).  After the two quad steps every
+// lane of a quad holds the quad's result, so the mirror step combines the two
+// quads of an aligned group of 8 lanes.
+constexpr int kDppQuadXor1 = 0xB1;     // quad_perm [1, 0, 3, 2]
+constexpr int kDppQuadXor2 = 0x4E;     // quad_perm [2, 3, 0, 1]
+constexpr int kDppHalfMirror = 0x141;  // row_half_mirror
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+}
+
+// Maximum of non-negative finite floats over the 8 lanes, on their bit patterns
+// (ordered like the values), so each step is one integer max.
+__device__ __forceinline__ float max8(float v) {
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  u = max(u, (uint32_t)dpp<kDppQuadXor1>((int)u));
+  u = max(u, (uint32_t)dpp<kDppQuadXor2>((int)u));
+  u = max(u, (uint32_t)dpp<kDppHalfMirror>((int)u));
+  return __builtin_bit_cast(float, u);
+}
+
+__device__ __forceinline__ int sum8(int v) {
+  v += dpp<kDppQuadXor1>(v);
+  v += dpp<kDppQuadXor2>(v);
+  return v + dpp<kDppHalfMirror>(v);
+}
+
+// q = clamp(rint(v / dh), -127, 127) where v / dh is the correctly rounded f32
+// quotient (IEEE division) and rint rounds half to even.  The correctly rounded
+// division costs about a dozen instructions, so the quotient is first formed as
+// v * rcp(dh): with |v / dh| <= 127.1 (|v| <= amax, dh = f16(amax/127)) the
+// reciprocal (1 ulp) and the product (0.5 ulp) put it within 2.3e-5 of the
+// exact quotient, and the correctly rounded quotient is within 3.8e-6 of it.
+// So unless the product lies within 1e-4 of a half-integer, both round to the
+// same integer; when one of a lane's four products does, the lane divides all
+// four exactly.  With dh == 0 the reciprocal is taken as 0, which gives q = 0.
+__device__ __forceinline__ void quant4(const float4& v, float dhf, float inv, int q[4]) {
+  const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+  float n[4], e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    n[i] = __builtin_rintf(r[i]);
+    e[i] = fabsf(r[i] - n[i]);
+  }
+  if (fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > 0.5f - 1e-4f) {
+    n[0] = __builtin_rintf(v.x / dhf);
+    n[1] = __builtin_rintf(v.y / dhf);
+    n[2] = __builtin_rintf(v.z / dhf);
+    n[3] = __builtin_rintf(v.w / dhf);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = (int)__builtin_amdgcn_fmed3f(n[i], -127.0f, 127.0f);
+}
+
+// One lane's part of a q8 block: its four codes, one per byte, and the block's
+// scale dh and scaled sum s (the same in all eight lanes).
+struct Q8Quad {
+  uint32_t codes;
+  _Float16 dh, s;
+  // the (dh, s) word of the scale plane
+  __device__ __forceinline__ uint32_t pair() const {
+    return (uint32_t)__builtin_bit_cast(uint16_t, dh) | ((uint32_t)__builtin_bit_cast(uint16_t, s) << 16);
+  }
+};
+
+__device__ __forceinline__ uint32_t pack4(const int q[4]) {
+  return (uint32_t)(q[0] & 255) | ((uint32_t)(q[1] & 255) << 8) | ((uint32_t)(q[2] & 255) << 16) |
+         ((uint32_t)(q[3] & 255) << 24);
+}
+
+__device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
+  const float amax = max8(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+  const float d32 = amax / 127.0f;
+  Q8Quad r;
+  r.dh = (_Float16)d32;  // round to nearest even
+  const float dhf = (float)r.dh;
+  const float inv = dhf == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(dhf);
+  int q[4];
+  quant4(v, dhf, inv, q);
+  const int S = sum8(q[0] + q[1] + q[2] + q[3]);
+  r.s = (_Float16)(dhf * (float)S);  // the product is exact in f32
+  r.codes = pack4(q);
+  return r;
+}
+
+}  // namespace qmm
