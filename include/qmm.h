@@ -59,6 +59,7 @@ extern "C" {
 #define QMM_F32 0
 #define QMM_F16 1
 #define QMM_BF16 2
+#define QMM_Q8 3 /* as the output of a product: q8 blocks, a qact buffer */
 
 /* Return codes. */
 #define QMM_OK 0
@@ -340,6 +341,57 @@ int qmm_stream_release(void *stream, size_t *freed_bytes);
  */
 int qmm_mmq_noalloc(const qmm_weights *w, const void *qact, size_t qact_bytes, int64_t n_tok,
                     float *out, void *stream);
+
+/* Activations of an epilogue. */
+#define QMM_ACT_NONE 0
+#define QMM_ACT_RELU 1
+#define QMM_ACT_SILU 2      /* x / (1 + exp(-x)) */
+#define QMM_ACT_GELU 3      /* x * (1 + erf(x / sqrt(2))) / 2 */
+#define QMM_ACT_GELU_TANH 4 /* x * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))) / 2 */
+
+/* What happens to a product's f32 sum v of (token t, row j) before it is stored:
+ *   scale * mul[t][j] * act(v + bias[j]) + residual_scale * residual[t][j]
+ * each part where given, in f32, rounded once.  Zero the struct, set scale to 1
+ * and then what is wanted. */
+typedef struct {
+    const float *bias;     /* f32 [od], 4-byte aligned, or NULL */
+    int32_t act;           /* QMM_ACT_* */
+    int32_t type;          /* element type of mul and residual: QMM_F32, QMM_F16, QMM_BF16 */
+    float scale;           /* finite */
+    float residual_scale;  /* finite */
+    const void *mul;       /* device [n_tok] rows of od elements, or NULL */
+    int64_t mul_stride;    /* elements from row to row, in [od, QMM_MAX_STRIDE] */
+    const void *residual;  /* device [n_tok] rows of od elements, or NULL */
+    int64_t residual_stride;
+} qmm_epilogue;
+
+/*
+ * qmm_mmq_epilogue -- qmm_mmq with an epilogue on its sums, stored in the type
+ * and place the next step reads: one kernel instead of the product and an
+ * elementwise pass over its output.  The sums are qmm_mmq's, bit for bit.
+ *   w, qact, qact_bytes, n_tok, stream  as for qmm_mmq
+ *   ep          the epilogue, or NULL: the sums themselves, rounded to out_type
+ *   out_type    QMM_F32, QMM_F16 or QMM_BF16: out is device [n_tok] rows of od
+ *               elements, out_stride elements from row to row (in [od,
+ *               QMM_MAX_STRIDE]), aligned to its element.  Only the n_tok x od
+ *               elements are written.
+ *               QMM_Q8: out is a qact buffer of qmm_qact_bytes(n_tok, od) bytes
+ *               (od % 256 == 0; 16-byte aligned) and out_stride is that number;
+ *               it receives the q8 blocks of the values, as
+ *               qmm_quantize_activations makes them of f32 values, padding
+ *               tokens zero -- the next product's input (|values| <= 2046).
+ *   work        device memory for the tail partials (see qmm_mmq), 16-byte
+ *               aligned, work_bytes of it, at least the plan's scratch_bytes
+ *               (qmm_mmq_plan): the call then allocates nothing and can be
+ *               captured, and calls with work memory of their own may overlap.
+ *               NULL with work_bytes 0: the stream's scratch, as qmm_mmq.
+ * out may be mul or residual in place (same pointer, stride and type); any
+ * other overlap of out or work with an input is refused.
+ * Errors: as qmm_mmq.
+ */
+int qmm_mmq_epilogue(const qmm_weights *w, const void *qact, size_t qact_bytes, int64_t n_tok,
+                     const qmm_epilogue *ep, int out_type, void *out, int64_t out_stride,
+                     void *work, size_t work_bytes, void *stream);
 
 /* The launch plan of one MMQ (qmm_mmq, qmm_mmq_noalloc): how its output tiles
  * map onto work-groups on a GPU of a given size, and the tail partials it needs.

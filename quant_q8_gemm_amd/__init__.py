@@ -53,12 +53,14 @@ BLOCK_BYTES = {Q4_K: 144, Q4_K_PACKED: 144, Q6_K: 210}
 EXPORTS = ("qmm_register_weights", "qmm_weights_info", "qmm_weights_export", "qmm_release_weights",
            "qmm_set_memory_cap", "qmm_qact_bytes", "qmm_quantize_activations", "qmm_mmq",
            "qmm_mmq_noalloc", "qmm_stream_release", "qmm_mmq_plan", "qmm_mmq_plan_work", "qmm_last_error",
-           "qmm_dequantize_activations", "qmm_norm_quantize")
+           "qmm_dequantize_activations", "qmm_norm_quantize", "qmm_mmq_epilogue")
 MAX_CUS = 65536
 # element types of activation tensors
 F32, F16, BF16 = 0, 1, 2
 ELEM_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 NORM_KINDS = {"rms": 0, "layer": 1}
+Q8 = 3  # as the output of a product: q8 blocks
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
 class Info(ctypes.Structure):
@@ -85,6 +87,12 @@ class Norm(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("h_out", ctypes.c_void_p), ("h_out_stride", ctypes.c_int64),
                 ("normed", ctypes.c_void_p), ("normed_stride", ctypes.c_int64), ("qact", ctypes.c_void_p),
                 ("qact_bytes", ctypes.c_size_t)]
+
+
+class Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("act", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("residual_scale", ctypes.c_float), ("mul", ctypes.c_void_p),
+                ("mul_stride", ctypes.c_int64), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -119,6 +127,8 @@ _lib.qmm_dequantize_activations.argtypes = [_P, _SZ, _I64, _I64, ctypes.c_int, _
 _lib.qmm_dequantize_activations.restype = ctypes.c_int
 _lib.qmm_norm_quantize.argtypes = [ctypes.POINTER(Norm), _I64, _I64, _P]
 _lib.qmm_norm_quantize.restype = ctypes.c_int
+_lib.qmm_mmq_epilogue.argtypes = [_P, _P, _SZ, _I64, ctypes.POINTER(Epilogue), ctypes.c_int, _P, _I64, _P, _SZ, _P]
+_lib.qmm_mmq_epilogue.restype = ctypes.c_int
 _lib.qmm_last_error.argtypes = []
 _lib.qmm_last_error.restype = ctypes.c_char_p
 
@@ -401,3 +411,59 @@ def norm_quantize(h, weight, *, y=None, bias=None, post_weight=None, post_bias=N
         a.qact, a.qact_bytes = qact.data_ptr(), qact.numel()
     _check(_lib.qmm_norm_quantize(ctypes.byref(a), n_tok, id_, _stream(stream)))
     return NormResult(h_out, normed, qact)
+
+
+def _epilogue(n_tok: int, od: int, bias, act: str, mul, residual, scale: float, residual_scale: float) -> Epilogue:
+    ep = Epilogue(scale=scale, residual_scale=residual_scale)
+    if act not in ACTS:
+        raise QmmError(EINVAL, f"act must be one of {sorted(ACTS)}, got {act!r}")
+    ep.act = ACTS[act]
+    if bias is not None:
+        ep.bias = _vector(bias, "bias", od)
+    if mul is not None:
+        ep.type = _elem(mul.dtype, "mul")
+        ep.mul, ep.mul_stride = _rows(mul, "mul", (n_tok, od))
+    if residual is not None:
+        if mul is not None and residual.dtype != mul.dtype:
+            raise QmmError(EINVAL, f"mul is {mul.dtype} but residual is {residual.dtype}")
+        ep.type = _elem(residual.dtype, "residual")
+        ep.residual, ep.residual_stride = _rows(residual, "residual", (n_tok, od))
+    return ep
+
+
+def mmq_epilogue(w: Weights, qact, n_tok: int, *, bias=None, act: str = "none", mul=None, residual=None,
+                 scale: float = 1.0, residual_scale: float = 1.0, dtype=torch.float32, out=None, work=None,
+                 stream=None):
+    """The product of mmq with an epilogue, in one kernel:
+
+        scale * mul * act(x @ W^T + bias) + residual_scale * residual
+
+    bias: float32 [od]; mul, residual: [n_tok][od] of one type (rows may be strided); act: "none", "relu", "silu",
+    "gelu" or "gelu_tanh".  The result is [n_tok][od] of `dtype`, or with dtype "q8" the qact buffer of the values
+    (the next product's input; od % 256 == 0).  out: a tensor to write into; it may be mul or residual itself.
+    work: a uint8 tensor for the split tails (mmq_plan(...).scratch_bytes), for graph capture; the stream's own
+    scratch without it."""
+    _check_qact(qact)
+    _device(qact, "qact")
+    ep = _epilogue(n_tok, w.od, bias, act, mul, residual, scale, residual_scale)
+    if dtype == "q8":
+        if out is None:
+            out = _empty((qact_bytes(n_tok, w.od),), torch.uint8, qact.device, stream)
+        _check_qact(out)
+        _device(out, "out")
+        out_type, ptr, stride = Q8, out.data_ptr(), out.numel()
+    else:
+        if out is None:
+            _elem(dtype)
+            out = _empty((n_tok, w.od), dtype, qact.device, stream)
+        out_type = _elem(out.dtype, "out")
+        ptr, stride = _rows(out, "out", (n_tok, w.od))
+    work_ptr, work_bytes = None, 0
+    if work is not None and work.numel():
+        if work.dtype != torch.uint8 or not work.is_contiguous():
+            raise QmmError(EINVAL, "work must be a contiguous cuda uint8 tensor")
+        _device(work, "work")
+        work_ptr, work_bytes = work.data_ptr(), work.numel()
+    _check(_lib.qmm_mmq_epilogue(w.handle, qact.data_ptr(), qact.numel(), n_tok, ctypes.byref(ep), out_type, ptr,
+                                 stride, work_ptr, work_bytes, _stream(stream)))
+    return out

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/qmm.h"
+#include "qmm_epilogue.h"
 #include "qmm_internal.h"
 
 struct qmm_weights {
@@ -311,16 +312,23 @@ struct Range {
   const void* p;
   int64_t stride;  // bytes from row to row
   size_t bytes;    // from the first byte to the last
+  size_t row = 0;  // bytes of a row (rows only)
 };
 
 Range rows_range(const char* what, const void* p, int64_t stride, int64_t rows, int64_t cols, size_t elem) {
   if (p == nullptr) return {what, p, 0, 0};
-  return {what, p, stride * (int64_t)elem, (size_t)((rows - 1) * stride + cols) * elem};
+  return {what, p, stride * (int64_t)elem, (size_t)((rows - 1) * stride + cols) * elem, (size_t)cols * elem};
 }
 
 bool overlap(const Range& a, const Range& b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  return a.p != nullptr && b.p != nullptr && x < y + b.bytes && y < x + a.bytes;
+  if (a.p == nullptr || b.p == nullptr || x >= y + b.bytes || y >= x + a.bytes) return false;
+  if (a.row > 0 && b.row > 0 && a.stride == b.stride && a.stride > 0) {
+    // columns of one wider tensor: where b's row starts inside a's stride
+    const size_t stride = (size_t)a.stride, at = y >= x ? (y - x) % stride : (stride - (x - y) % stride) % stride;
+    return at < a.row || at + b.row > stride;
+  }
+  return true;
 }
 
 // Whether an output that overlaps an input is that input in place.
@@ -434,6 +442,96 @@ int qmm_norm_quantize(const qmm_norm* args, int64_t n_tok, int64_t id, void* str
 
 namespace {
 
+// The parts of an epilogue that do not depend on the product's sizes.
+int check_epilogue(const qmm_epilogue* ep, int out_type) {
+  if (out_type != QMM_Q8)
+    if (int rc = check_elem("out_type", out_type)) return rc;
+  if (ep == nullptr) return QMM_OK;
+  if (ep->act < QMM_ACT_NONE || ep->act > QMM_ACT_GELU_TANH)
+    return fail(QMM_EINVAL, "act must be one of QMM_ACT_* (0 to %d), got %d", QMM_ACT_GELU_TANH, ep->act);
+  if (int rc = check_elem("type of mul and residual", ep->type)) return rc;
+  if (!std::isfinite(ep->scale) || !std::isfinite(ep->residual_scale))
+    return fail(QMM_EINVAL, "scale and residual_scale must be finite");
+  if (!aligned(ep->bias, 4)) return fail(QMM_EINVAL, "bias must be 4-byte aligned");
+  const size_t eb = elem_bytes(ep->type);
+  if (!aligned(ep->mul, eb) || !aligned(ep->residual, eb))
+    return fail(QMM_EINVAL, "mul and residual must be aligned to their element");
+  return QMM_OK;
+}
+
+int check_stride(const char* what, int64_t stride, int64_t cols) {
+  if (stride < cols || stride > QMM_MAX_STRIDE)
+    return fail(QMM_EINVAL, "%s_stride must be in [%lld, %lld], got %lld", what, (long long)cols,
+                (long long)QMM_MAX_STRIDE, (long long)stride);
+  return QMM_OK;
+}
+
+// Checks the epilogue and output of a product of n_tok > 0 tokens by od rows and
+// writes the kernels' form of them.  `in`: the product's other inputs; *written:
+// the range of out.
+int resolve_epilogue(const qmm_epilogue* ep, int64_t n_tok, int64_t od, int out_type, void* out, int64_t out_stride,
+                     const Range& in, qmm::Epilogue* r, Range* written) {
+  static const qmm_epilogue kNone = {nullptr, QMM_ACT_NONE, QMM_F32, 1.0f, 0.0f, nullptr, 0, nullptr, 0};
+  if (ep == nullptr) ep = &kNone;
+  if (out == nullptr) return fail(QMM_EINVAL, "out is NULL");
+  if (out_type == QMM_Q8) {
+    const size_t need = qmm_qact_bytes(n_tok, od);
+    if (need == 0) return fail(QMM_EINVAL, "a q8 output needs od %% 256 == 0, got od=%lld", (long long)od);
+    if (out_stride < 0 || (size_t)out_stride != need)
+      return fail(QMM_EINVAL, "out_stride %lld != qmm_qact_bytes(%lld, %lld) = %zu", (long long)out_stride,
+                  (long long)n_tok, (long long)od, need);
+    if (!aligned(out, 16)) return fail(QMM_EINVAL, "a q8 output must be 16-byte aligned");
+    *written = {"out", out, 0, need};
+  } else {
+    if (int rc = check_stride("out", out_stride, od)) return rc;
+    if (!aligned(out, elem_bytes(out_type))) return fail(QMM_EINVAL, "out must be aligned to its element");
+    *written = rows_range("out", out, out_stride, n_tok, od, elem_bytes(out_type));
+  }
+  const size_t eb = elem_bytes(ep->type);
+  if (ep->mul != nullptr)
+    if (int rc = check_stride("mul", ep->mul_stride, od)) return rc;
+  if (ep->residual != nullptr)
+    if (int rc = check_stride("residual", ep->residual_stride, od)) return rc;
+  if (overlap(*written, in)) return refuse_overlap(*written, in);
+  const Range bias{"bias", ep->bias, 0, (size_t)od * 4};
+  if (overlap(*written, bias)) return refuse_overlap(*written, bias);
+  for (const Range& side : {rows_range("mul", ep->mul, ep->mul_stride, n_tok, od, eb),
+                            rows_range("residual", ep->residual, ep->residual_stride, n_tok, od, eb)})
+    if (overlap(*written, side) && !(out_type == ep->type && same_rows(*written, side)))
+      return refuse_overlap(*written, side);
+  const auto quads = [&](const void* p, int64_t stride, size_t elem) {
+    return p == nullptr || (aligned(p, 4 * elem) && stride % 4 == 0);
+  };
+  r->bias = ep->bias;
+  r->mul = ep->mul;
+  r->residual = ep->residual;
+  r->out = out;
+  r->mul_stride = ep->mul_stride;
+  r->residual_stride = ep->residual_stride;
+  r->out_stride = out_stride;
+  r->t_pad = token_pad(n_tok);
+  r->scale = ep->scale;
+  r->residual_scale = ep->residual_scale;
+  r->act = ep->act;
+  r->side_type = ep->type;
+  r->out_type = out_type;
+  r->vec = od % 4 == 0 && quads(ep->bias, 0, 4) && quads(ep->mul, ep->mul_stride, eb) &&
+           quads(ep->residual, ep->residual_stride, eb) &&
+           (out_type == QMM_Q8 || quads(out, out_stride, elem_bytes(out_type)));
+  return QMM_OK;
+}
+
+// The current device, which has to be the handle's, and its compute units.
+int current_device(const qmm_weights* w, int* device, int* num_cus) {
+  hipError_t e = hipGetDevice(device);
+  if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
+  if (*device != w->device)
+    return fail(QMM_EINVAL, "handle belongs to device %d but device %d is current", w->device, *device);
+  e = hipDeviceGetAttribute(num_cus, hipDeviceAttributeMultiprocessorCount, *device);
+  if (e != hipSuccess) return fail_hip(e, "hipDeviceGetAttribute(multiprocessor count)");
+  return QMM_OK;
+}
+
 // Validation and launch plan shared by qmm_mmq and qmm_mmq_noalloc.  Returns
 // QMM_OK with *launch false for an empty batch (nothing to launch).
 int prepare_mmq(const qmm_weights* w, const void* qact, size_t qact_bytes, int64_t n_tok, const float* out,
@@ -452,15 +550,27 @@ int prepare_mmq(const qmm_weights* w, const void* qact, size_t qact_bytes, int64
   if (qact_bytes != need)
     return fail(QMM_ESHAPE, "qact_bytes %zu does not match n_tok=%lld and the handle's id=%lld (%zu)",
                 qact_bytes, (long long)n_tok, (long long)w->p.id, need);
-  hipError_t e = hipGetDevice(device);
-  if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
-  if (*device != w->device)
-    return fail(QMM_EINVAL, "handle belongs to device %d but device %d is current", w->device, *device);
-  e = hipDeviceGetAttribute(num_cus, hipDeviceAttributeMultiprocessorCount, *device);
-  if (e != hipSuccess) return fail_hip(e, "hipDeviceGetAttribute(multiprocessor count)");
+  if (int rc = current_device(w, device, num_cus)) return rc;
   *plan = qmm::plan_mmq(w->p, n_tok, *num_cus);
   if (int rc = check_launch(*plan, n_tok, w->p.od, *num_cus)) return rc;
   *launch = true;
+  return QMM_OK;
+}
+
+// The tail-partials scratch of (device, stream), allocated by its first call.
+int stream_scratch(int device, int num_cus, hipStream_t s, void** scratch) {
+  const size_t max_bytes = qmm::mmq_scratch_max_bytes(num_cus);
+  std::lock_guard<std::mutex> lock(g_scratch_mu);
+  for (const Scratch& sc : g_scratch)
+    if (sc.device == device && sc.stream == s) *scratch = sc.ptr;
+  if (*scratch != nullptr) return QMM_OK;
+  hipError_t e = hipMalloc(scratch, max_bytes);
+  if (e != hipSuccess) {
+    (void)hipGetLastError();  // leave no sticky error for the caller's next HIP call
+    return e == hipErrorOutOfMemory ? fail(QMM_ENOMEM, "hipMalloc(%zu) for the tail partials failed", max_bytes)
+                                    : fail_hip(e, "hipMalloc(tail partials)");
+  }
+  g_scratch.push_back({device, s, *scratch, max_bytes});
   return QMM_OK;
 }
 
@@ -480,22 +590,8 @@ int qmm_mmq(const qmm_weights* w, const void* qact, size_t qact_bytes, int64_t n
   }
   const hipStream_t s = (hipStream_t)stream;
   void* scratch = nullptr;
-  if (plan.scratch_bytes > 0) {
-    const size_t max_bytes = qmm::mmq_scratch_max_bytes(num_cus);
-    std::lock_guard<std::mutex> lock(g_scratch_mu);
-    for (const Scratch& sc : g_scratch)
-      if (sc.device == device && sc.stream == s) scratch = sc.ptr;
-    if (scratch == nullptr) {
-      hipError_t e = hipMalloc(&scratch, max_bytes);
-      if (e != hipSuccess) {
-        (void)hipGetLastError();  // leave no sticky error for the caller's next HIP call
-        return e == hipErrorOutOfMemory
-                   ? fail(QMM_ENOMEM, "hipMalloc(%zu) for the tail partials failed", max_bytes)
-                   : fail_hip(e, "hipMalloc(tail partials)");
-      }
-      g_scratch.push_back({device, s, scratch, max_bytes});
-    }
-  }
+  if (plan.scratch_bytes > 0)
+    if (int rc = stream_scratch(device, num_cus, s, &scratch)) return rc;
   hipError_t e = qmm::launch_mmq(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), out,
                                  (float*)scratch, s);
   if (e != hipSuccess) return fail_hip(e, "mmq launch");
@@ -553,6 +649,53 @@ int qmm_mmq_noalloc(const qmm_weights* w, const void* qact, size_t qact_bytes, i
   }
   hipError_t e = qmm::launch_mmq(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), out, part,
                                  (hipStream_t)stream);
+  if (e != hipSuccess) return fail_hip(e, "mmq launch");
+  ok();
+  return QMM_OK;
+}
+
+int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, int64_t n_tok, const qmm_epilogue* ep,
+                     int out_type, void* out, int64_t out_stride, void* work, size_t work_bytes, void* stream) {
+  if (int rc = check_epilogue(ep, out_type)) return rc;
+  if ((work == nullptr) != (work_bytes == 0) || !aligned(work, 16))
+    return fail(QMM_EINVAL, "work must be 16-byte aligned and come with its size (NULL with 0)");
+  if (w == nullptr) return fail(QMM_EINVAL, "NULL weights handle");
+  if (int rc = check_tokens(n_tok)) return rc;
+  const size_t need = qmm_qact_bytes(n_tok, w->p.id);
+  if (qact_bytes != need)
+    return fail(QMM_ESHAPE, "qact_bytes %zu does not match n_tok=%lld and the handle's id=%lld (%zu)", qact_bytes,
+                (long long)n_tok, (long long)w->p.id, need);
+  if (n_tok == 0) {  // empty batch: an empty output, nothing launched
+    ok();
+    return QMM_OK;
+  }
+  if (qact == nullptr) return fail(QMM_EINVAL, "qact is NULL");
+  if (!aligned(qact, 16)) return fail(QMM_EINVAL, "qact must be 16-byte aligned");
+  const Range in{"qact", qact, 0, need}, own{"work", work, 0, work_bytes};
+  qmm::Epilogue r{};
+  Range written{};
+  if (int rc = resolve_epilogue(ep, n_tok, w->p.od, out_type, out, out_stride, in, &r, &written)) return rc;
+  if (overlap(own, in)) return refuse_overlap(own, in);
+  if (overlap(own, written)) return refuse_overlap(own, written);
+  if (ep != nullptr)
+    for (const Range& side : {Range{"bias", ep->bias, 0, (size_t)w->p.od * 4},
+                              rows_range("mul", ep->mul, ep->mul_stride, n_tok, w->p.od, elem_bytes(ep->type)),
+                              rows_range("residual", ep->residual, ep->residual_stride, n_tok, w->p.od,
+                                         elem_bytes(ep->type))})
+      if (overlap(own, side)) return refuse_overlap(own, side);
+  int device = -1, num_cus = 0;
+  if (int rc = current_device(w, &device, &num_cus)) return rc;
+  const qmm::MmqPlan plan = qmm::plan_mmq(w->p, n_tok, num_cus);
+  if (int rc = check_launch(plan, n_tok, w->p.od, num_cus)) return rc;
+  if (work != nullptr && work_bytes < plan.scratch_bytes)
+    return fail(QMM_EINVAL, "work_bytes %zu, but this launch needs %zu bytes of tail scratch", work_bytes,
+                plan.scratch_bytes);
+  const hipStream_t s = (hipStream_t)stream;
+  void* scratch = work;
+  if (scratch == nullptr && plan.scratch_bytes > 0)
+    if (int rc = stream_scratch(device, num_cus, s, &scratch)) return rc;
+  hipError_t e = qmm::launch_mmq_epilogue(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), r,
+                                          (float*)scratch, s);
   if (e != hipSuccess) return fail_hip(e, "mmq launch");
   ok();
   return QMM_OK;

@@ -46,6 +46,14 @@ struct Elem<2> { typedef __bf16 type; };
 template <int TYPE>
 using elem_t = typename Elem<TYPE>::type;
 
+template <int TYPE>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  return (float)((const elem_t<TYPE>*)p)[i];
+}
+template <int TYPE>
+__device__ __forceinline__ void store1(void* p, int64_t i, float f) {
+  ((elem_t<TYPE>*)p)[i] = (elem_t<TYPE>)f;
+}
 // Four consecutive elements at p[i] .. p[i + 3]; p + i is aligned to four of them.
 template <int TYPE>
 __device__ __forceinline__ float4 load4(const void* p, int64_t i) {

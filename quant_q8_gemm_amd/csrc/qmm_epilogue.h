@@ -1,0 +1,104 @@
+// qmm_epilogue.h -- the epilogue of a product, shared by the MMQ and the
+// few-token product: from the f32 sum v of output element (token t, row j),
+//
+//   scale * mul[t][j] * act(v + bias[j]) + residual_scale * residual[t][j]
+//
+// in f32, rounded once to the output's type (or quantized with its 32-block).
+#pragma once
+
+#include "qmm_common.h"
+#include "qmm_quant.h"
+
+#include "../../include/qmm.h"
+
+namespace qmm {
+
+// A kernel without an epilogue: its outputs are the f32 sums themselves.
+struct NoEpilogue {
+  static constexpr bool kOn = false;
+};
+
+// The caller's epilogue and output, checked; strides in elements.
+struct Epilogue {
+  static constexpr bool kOn = true;
+  const float* bias;     // or nullptr
+  const void* mul;       // or nullptr
+  const void* residual;  // or nullptr
+  void* out;
+  int64_t mul_stride, residual_stride, out_stride;
+  int64_t t_pad;  // QMM_Q8: tokens of the output's qact buffer
+  float scale, residual_scale;
+  int act;
+  int side_type;  // element type of mul and residual
+  int out_type;   // element type of out, or QMM_Q8
+  int vec;        // rows can be accessed four elements at a time everywhere
+};
+
+// The sigmoid forms have no cancellation on either side: exp(-x) overflows to
+// infinity for large negative x and the quotient is then -0.
+__device__ __forceinline__ float activate(float x, int act) {
+  switch (act) {
+    case QMM_ACT_RELU: return fmaxf(x, 0.0f);
+    case QMM_ACT_SILU: return x / (1.0f + __expf(-x));
+    case QMM_ACT_GELU: return 0.5f * x * erfcf(-0.70710678f * x);
+    case QMM_ACT_GELU_TANH:  // 0.5*x*(1 + tanh(z)) = x*sigmoid(2z), z = sqrt(2/pi)*(x + 0.044715*x^3)
+      return x / (1.0f + __expf(-1.5957691f * (x + 0.044715f * x * x * x)));
+    default: return x;
+  }
+}
+
+// Rows j .. j + 3 of a token's row of mul, residual or out, at element offset i;
+// n of them exist (1 to 4), all four where the access is one vector.
+__device__ __forceinline__ float4 load_side(const void* p, int type, int64_t i, int vec, int n) {
+  if (vec)
+    return type == QMM_F32 ? load4<QMM_F32>(p, i) : type == QMM_F16 ? load4<QMM_F16>(p, i) : load4<QMM_BF16>(p, i);
+  float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < n)
+      f[k] = type == QMM_F32   ? load1<QMM_F32>(p, i + k)
+             : type == QMM_F16 ? load1<QMM_F16>(p, i + k)
+                               : load1<QMM_BF16>(p, i + k);
+  return make_float4(f[0], f[1], f[2], f[3]);
+}
+
+// The epilogue of rows j .. j + 3 of one token, n of which exist.
+__device__ __forceinline__ float4 finish(const Epilogue& ep, float4 v, int64_t t, int j, int n) {
+  if (ep.bias != nullptr) {
+    const float4 b = load_side(ep.bias, QMM_F32, j, ep.vec, n);
+    v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+  }
+  if (ep.act != QMM_ACT_NONE)
+    v = make_float4(activate(v.x, ep.act), activate(v.y, ep.act), activate(v.z, ep.act), activate(v.w, ep.act));
+  v = make_float4(v.x * ep.scale, v.y * ep.scale, v.z * ep.scale, v.w * ep.scale);
+  if (ep.mul != nullptr) {
+    const float4 m = load_side(ep.mul, ep.side_type, t * ep.mul_stride + j, ep.vec, n);
+    v = make_float4(v.x * m.x, v.y * m.y, v.z * m.z, v.w * m.w);
+  }
+  if (ep.residual != nullptr) {
+    const float4 r = load_side(ep.residual, ep.side_type, t * ep.residual_stride + j, ep.vec, n);
+    const float s = ep.residual_scale;
+    v = make_float4(fmaf(s, r.x, v.x), fmaf(s, r.y, v.y), fmaf(s, r.z, v.z), fmaf(s, r.w, v.w));
+  }
+  return v;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void put_typed(const Epilogue& ep, float4 v, int64_t i, int n) {
+  if (ep.vec) {
+    store4<TYPE>(ep.out, i, v);
+  } else {
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) store1<TYPE>(ep.out, i + k, f[k]);
+  }
+}
+__device__ __forceinline__ void put(const Epilogue& ep, float4 v, int64_t t, int j, int n) {
+  const int64_t i = t * ep.out_stride + j;
+  if (ep.out_type == QMM_F32) put_typed<QMM_F32>(ep, v, i, n);
+  else if (ep.out_type == QMM_F16) put_typed<QMM_F16>(ep, v, i, n);
+  else put_typed<QMM_BF16>(ep, v, i, n);
+}
+
+}  // namespace qmm

@@ -76,6 +76,9 @@ void plan_work(const MmqPlan& plan, int nsb, int64_t wg, int* rt, int* tt, int* 
 size_t mmq_scratch_max_bytes(int num_cus);
 hipError_t launch_mmq(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok,
                       int64_t t_pad, float* out, float* part, hipStream_t s);
+struct Epilogue;  // qmm_epilogue.h
+hipError_t launch_mmq_epilogue(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok,
+                               int64_t t_pad, const Epilogue& ep, float* part, hipStream_t s);
 // The allocation-free entry point's tail scratch: a static device array of
 // this many bytes per GPU (64 KiB per compute unit of a 256-CU MI355X).
 constexpr size_t kStaticScratchBytes = (size_t)16 << 20;

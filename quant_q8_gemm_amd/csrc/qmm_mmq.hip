@@ -30,6 +30,7 @@
 //    f16 scaled sums, times dmin.
 #include "qmm_internal.h"
 #include "qmm_common.h"
+#include "qmm_epilogue.h"
 
 #include <algorithm>
 #include <mutex>
@@ -333,6 +334,52 @@ __device__ __forceinline__ void store_block(float* __restrict__ out, const v16f&
                lane, q, od, n_tok, vec_store);
 }
 
+// The same block through an epilogue.  The lane's sums pass through the wave's
+// own LDS region as [token][row], so that afterwards eight lanes hold the 32 rows
+// of one token, four each: mul, residual and out are accessed in runs of a
+// token's row, and the eight lanes are a q8 block as the prepass has it.
+// Token rows are 36 floats apart: both sides access 16 bytes per lane without
+// bank conflicts.  The loop is kept rolled: the epilogue is long and runs once
+// per tile.
+constexpr int kEpRow = 36;
+constexpr int kEpWave = 32 * kEpRow;  // floats per wave
+
+// four codes and, from the eight lanes' first, the (dh, s) pair of token t, chunk
+// `block` of the next product's qact (od/32 chunks)
+__device__ __forceinline__ void put_q8(const Epilogue& ep, const Q8Quad& r, int t, int block, int od, int quad) {
+  const int64_t frag = (int64_t)(t >> 5) * (od >> 5) + block;
+  *(uint32_t*)((uint8_t*)ep.out + frag * 1024 + (quad >> 2) * 512 + (t & 31) * 16 + (quad & 3) * 4) = r.codes;
+  if (quad == 0) *(uint32_t*)((uint8_t*)ep.out + ep.t_pad * od + frag * 128 + (t & 31) * 4) = r.pair;
+}
+
+__device__ __forceinline__ void finish_block(const Epilogue& ep, const v16f& acc, float* lds, int rblock, int tblock,
+                                             int lane, int od, int n_tok) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *(float4*)(lds + (lane & 31) * kEpRow + 8 * q + 4 * (lane >> 5)) =
+        make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+  const int quad = lane & 7, j = rblock * 32 + 4 * quad;
+  const int n = min(od - j, 4);  // rows of the quad that exist
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int tl = 8 * k + (lane >> 3), t = tblock * 32 + tl;
+    const bool live = t < n_tok && n > 0;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);  // q8: what padding tokens get
+    if (live) v = finish(ep, *(const float4*)(lds + tl * kEpRow + 4 * quad), t, j, n);
+    if (ep.out_type == QMM_Q8)  // od % 256 == 0: the eight lanes hold a whole block
+      put_q8(ep, quant_quad(v), t, rblock, od, quad);
+    else if (live)
+      put(ep, v, t, j, n);
+  }
+}
+
+// Zeros of a chunk of 32 padding tokens that no tile covers.
+__device__ __forceinline__ void zero_block(const Epilogue& ep, int rblock, int tblock, int lane, int od) {
+  const int64_t frag = (int64_t)tblock * (od >> 5) + rblock;
+  *(uint4*)((uint8_t*)ep.out + frag * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
+  if (lane < 32) *(uint32_t*)((uint8_t*)ep.out + ep.t_pad * od + frag * 128 + lane * 4) = 0;
+}
+
 // Ragged second wave ("tail").  When the tiles fill the resident work-group
 // slots once and a few more, the first wave's worth of row tiles run whole
 // (data-parallel) and each of the remaining tail tiles is split along K into
@@ -342,13 +389,13 @@ __device__ __forceinline__ void store_block(float* __restrict__ out, const v16f&
 // tail is whole row tiles at the end, so the rows before it keep exactly the
 // summation order they have without a tail.
 // Every launch shape runs 16 waves per CU, 4 per SIMD: at most 128 VGPRs.
-template <int TYPE, int WR, int WT, int KC, int KS>
+template <int TYPE, int WR, int WT, int KC, int KS, class EP>
 __global__ void __launch_bounds__(64 * WR * WT * KS) __attribute__((amdgpu_waves_per_eu(4, 4)))
 mmq_kernel(const int8_t* __restrict__ wq, const float* __restrict__ wd,
            const uint8_t* __restrict__ wsm, const uint8_t* __restrict__ qq,
            const uint8_t* __restrict__ qs, int nchunk, int nsb, int od, int n_tok,
            int tok_tiles, int dp_row_tiles, int split, int vec_store, float* __restrict__ out,
-           float* __restrict__ part) {
+           float* __restrict__ part, EP ep) {
   using St = Stage<TYPE, WR, WT, KC>;
   using W = WeightOps<TYPE>;
   constexpr int kWaves = WR * WT;
@@ -644,7 +691,20 @@ mmq_kernel(const int8_t* __restrict__ wq, const float* __restrict__ wd,
     }
   }
 
-  if (tail_idx < 0 && !vec_store) {
+  if constexpr (EP::kOn) {
+    if (tail_idx < 0) {
+      // LDS after the k-group combine's region, or with one k-group once every
+      // wave is done with the stage buffers
+      constexpr size_t kRed = KS > 1 ? (size_t)kWaves * 1024 : 0;
+      static_assert((kRed + (size_t)kWaves * kEpWave) * sizeof(float) <= KS * 2 * sizeof(St), "room for the epilogue");
+      if (KS == 1) __syncthreads();
+      if (ks != 0) return;
+      finish_block(ep, acc, (float*)stage_all + kRed + wave * kEpWave, rb0 + wr, tb0 + wt, lane, od, n_tok);
+      if (ep.out_type == QMM_Q8 && tt == tok_tiles - 1)
+        for (int tb = tb0 + wt + WT; tb * 32 < ep.t_pad; tb += WT) zero_block(ep, rb0 + wr, tb, lane, od);
+      return;
+    }
+  } else if (tail_idx < 0 && !vec_store) {
     // Without 16-byte stores (od % 4 != 0), through LDS: after the k-group
     // combine's region (kWaves x 4 KiB), or with one k-group once every wave
     // is done with the stage buffers.  od 4097 x 11008 at 509 tokens: 4-5%
@@ -677,10 +737,10 @@ mmq_kernel(const int8_t* __restrict__ wq, const float* __restrict__ wd,
 // slice; the adds keep slice order.
 constexpr int kFixBatch = 8;
 
-template <int WR, int WT>
+template <int WR, int WT, class EP>
 __global__ void __launch_bounds__(256)
 mmq_fixup_kernel(const float* __restrict__ part, int split, int dp_row_tiles, int tok_tiles, int od,
-                 int n_tok, int vec_store, float* __restrict__ out) {
+                 int n_tok, int vec_store, float* __restrict__ out, EP ep) {
   constexpr int kWaves = WR * WT;
   constexpr size_t kSlice = (size_t)kWaves * 1024;  // floats per slice of one tile
   const int u = blockIdx.x / kWaves, w = blockIdx.x % kWaves;
@@ -709,24 +769,46 @@ mmq_fixup_kernel(const float* __restrict__ part, int split, int dp_row_tiles, in
     }
   }
   const int rt = dp_row_tiles + u / tok_tiles, tt = u % tok_tiles;
-  store_quad(out, v, rt * WR + w / WT, tt * WT + w % WT, lane, q, od, n_tok, vec_store);
+  const int rblock = rt * WR + w / WT, tblock = tt * WT + w % WT;
+  if constexpr (EP::kOn) {
+    // to the epilogue's layout, as finish_block has it: this wave takes tokens
+    // 8q .. 8q + 7 of the block
+    __shared__ float lds[kEpWave];
+    *(float4*)(lds + (lane & 31) * kEpRow + 8 * q + 4 * (lane >> 5)) = v;
+    __syncthreads();
+    const int quad = lane & 7, j = rblock * 32 + 4 * quad;
+    const int tl = 8 * q + (lane >> 3), t = tblock * 32 + tl;
+    const int n = min(od - j, 4);
+    const bool live = t < n_tok && n > 0;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) f = finish(ep, *(const float4*)(lds + tl * kEpRow + 4 * quad), t, j, n);
+    if (ep.out_type == QMM_Q8) {
+      put_q8(ep, quant_quad(f), t, rblock, od, quad);
+      if (q == 0 && tt == tok_tiles - 1)
+        for (int tb = tblock + WT; tb * 32 < ep.t_pad; tb += WT) zero_block(ep, rblock, tb, lane, od);
+    } else if (live) {
+      put(ep, f, t, j, n);
+    }
+  } else {
+    store_quad(out, v, rblock, tblock, lane, q, od, n_tok, vec_store);
+  }
 }
 
-template <int TYPE, int WR, int WT, int KC, int KS>
+template <int TYPE, int WR, int WT, int KC, int KS, class EP>
 static hipError_t launch_tiled(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok,
-                               int64_t t_pad, float* out, float* part, hipStream_t s) {
+                               int64_t t_pad, float* out, float* part, const EP& ep, hipStream_t s) {
   static_assert(kRowPad % (32 * WR) == 0 && kTokenPad % (32 * WT) == 0,
                 "tiles must divide the row and token padding");
   const uint8_t* qs = qact + (size_t)t_pad * (size_t)p.id;
   const int vec_store = (p.od % 4 == 0) && ((uintptr_t)out % 16 == 0);
   const int64_t wgs = plan.work_groups;
-  mmq_kernel<TYPE, WR, WT, KC, KS><<<dim3((unsigned)wgs), dim3(64 * WR * WT * KS), 0, s>>>(
+  mmq_kernel<TYPE, WR, WT, KC, KS, EP><<<dim3((unsigned)wgs), dim3(64 * WR * WT * KS), 0, s>>>(
       p.wq, p.wd, p.wsm, qact, qs, (int)p.nchunk, (int)p.nsb, (int)p.od, (int)n_tok, plan.tok_tiles,
-      plan.dp_row_tiles, plan.split, vec_store, out, part);
+      plan.dp_row_tiles, plan.split, vec_store, out, part, ep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.n_tail == 0) return e;
-  mmq_fixup_kernel<WR, WT><<<dim3((unsigned)(plan.n_tail * WR * WT)), dim3(256), 0, s>>>(
-      part, plan.split, plan.dp_row_tiles, plan.tok_tiles, (int)p.od, (int)n_tok, vec_store, out);
+  mmq_fixup_kernel<WR, WT, EP><<<dim3((unsigned)(plan.n_tail * WR * WT)), dim3(256), 0, s>>>(
+      part, plan.split, plan.dp_row_tiles, plan.tok_tiles, (int)p.od, (int)n_tok, vec_store, out, ep);
   return hipGetLastError();
 }
 
@@ -836,19 +918,31 @@ void plan_work(const MmqPlan& plan, int nsb, int64_t wg, int* rt, int* tt, int* 
 // at most 64 KiB per CU in every shape (scratch_fits).
 size_t mmq_scratch_max_bytes(int num_cus) { return (size_t)num_cus * 64 * 1024; }
 
-hipError_t launch_mmq(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok,
-                      int64_t t_pad, float* out, float* part, hipStream_t s) {
+template <class EP>
+static hipError_t launch_any(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok, int64_t t_pad,
+                             float* out, float* part, const EP& ep, hipStream_t s) {
   constexpr Geometry q6 = kQ6Many, q4 = kQ4Many, f = kFew;
   if (p.type == QMM_Q6_K)
-    return plan.many ? launch_tiled<QMM_Q6_K, q6.wr, q6.wt, q6.kc, q6.ks>(p, plan, qact, n_tok, t_pad, out, part, s)
-                     : launch_tiled<QMM_Q6_K, f.wr, f.wt, f.kc, f.ks>(p, plan, qact, n_tok, t_pad, out, part, s);
+    return plan.many
+               ? launch_tiled<QMM_Q6_K, q6.wr, q6.wt, q6.kc, q6.ks>(p, plan, qact, n_tok, t_pad, out, part, ep, s)
+               : launch_tiled<QMM_Q6_K, f.wr, f.wt, f.kc, f.ks>(p, plan, qact, n_tok, t_pad, out, part, ep, s);
   if (p.type == QMM_Q4_K_PACKED)
-    return plan.many ? launch_tiled<QMM_Q4_K_PACKED, q4.wr, q4.wt, q4.kc, q4.ks>(p, plan, qact, n_tok, t_pad, out,
-                                                                               part, s)
-                     : launch_tiled<QMM_Q4_K_PACKED, f.wr, f.wt, f.kc, f.ks>(p, plan, qact, n_tok, t_pad, out,
-                                                                           part, s);
-  return plan.many ? launch_tiled<QMM_Q4_K, q4.wr, q4.wt, q4.kc, q4.ks>(p, plan, qact, n_tok, t_pad, out, part, s)
-                   : launch_tiled<QMM_Q4_K, f.wr, f.wt, f.kc, f.ks>(p, plan, qact, n_tok, t_pad, out, part, s);
+    return plan.many
+               ? launch_tiled<QMM_Q4_K_PACKED, q4.wr, q4.wt, q4.kc, q4.ks>(p, plan, qact, n_tok, t_pad, out, part, ep, s)
+               : launch_tiled<QMM_Q4_K_PACKED, f.wr, f.wt, f.kc, f.ks>(p, plan, qact, n_tok, t_pad, out, part, ep, s);
+  return plan.many
+             ? launch_tiled<QMM_Q4_K, q4.wr, q4.wt, q4.kc, q4.ks>(p, plan, qact, n_tok, t_pad, out, part, ep, s)
+             : launch_tiled<QMM_Q4_K, f.wr, f.wt, f.kc, f.ks>(p, plan, qact, n_tok, t_pad, out, part, ep, s);
+}
+
+hipError_t launch_mmq(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok, int64_t t_pad,
+                      float* out, float* part, hipStream_t s) {
+  return launch_any(p, plan, qact, n_tok, t_pad, out, part, NoEpilogue{}, s);
+}
+
+hipError_t launch_mmq_epilogue(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok, int64_t t_pad,
+                               const Epilogue& ep, float* part, hipStream_t s) {
+  return launch_any(p, plan, qact, n_tok, t_pad, (float*)nullptr, part, ep, s);
 }
 
 // The tail partials of the allocation-free entry point (qmm_mmq_noalloc): one

@@ -89,7 +89,7 @@ __device__ __forceinline__ void store_q8(uint8_t* qact, int64_t t_pad, int id, i
   const int sub = threadIdx.x & 7, tt = (int)(t & 31);
   const int64_t frag = (t >> 5) * (id >> 5) + (e >> 5);
   *(uint32_t*)(qact + frag * 1024 + (sub >> 2) * 512 + tt * 16 + (sub & 3) * 4) = r.codes;
-  if (sub == 0) *(uint32_t*)(qact + t_pad * id + frag * 128 + tt * 4) = r.pair();
+  if (sub == 0) *(uint32_t*)(qact + t_pad * id + frag * 128 + tt * 4) = r.pair;
 }
 
 // A padding token's zeros.

@@ -48,7 +48,7 @@ quantize_kernel(const float* __restrict__ x, int n_tok, int id, int nchunk, int 
     const Q8Quad r = quant_quad(v[i]);
     const int64_t frag = (int64_t)tb * nchunk + c;
     *(uint32_t*)(qq + frag * 1024 + (sub >> 2) * 512 + tt * 16 + (sub & 3) * 4) = r.codes;
-    if (sub == 0) *(uint32_t*)(qs + frag * 128 + tt * 4) = r.pair();
+    if (sub == 0) *(uint32_t*)(qs + frag * 128 + tt * 4) = r.pair;
   }
 }
 

@@ -63,13 +63,22 @@ __device__ __forceinline__ void quant4(const float4& v, float dhf, float inv, in
   for (int i = 0; i < 4; ++i) q[i] = (int)__builtin_amdgcn_fmed3f(n[i], -127.0f, 127.0f);
 }
 
-// One lane's part of a q8 block: its four codes, one per byte, and the block's
-// scale dh and scaled sum s (the same in all eight lanes).
-struct Q8Quad {
-  uint32_t codes;
-  _Float16 dh, s;
-  // the (dh, s) word of the scale plane
-  __device__ __forceinline__ uint32_t pair() const {
+// A float's magnitude as a bit pattern, ordered like the values (max8 above).
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+
+// The scale of a block whose largest magnitude is amax.
+struct Q8Scale {
+  _Float16 dh;
+  float dhf, inv;
+  __device__ __forceinline__ explicit Q8Scale(float amax) {
+    const float d32 = amax / 127.0f;
+    dh = (_Float16)d32;  // round to nearest even
+    dhf = (float)dh;
+    inv = dhf == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(dhf);
+  }
+  // the (dh, s) word of the scale plane; S is the sum of the block's codes
+  __device__ __forceinline__ uint32_t pair(int S) const {
+    const _Float16 s = (_Float16)(dhf * (float)S);  // the product is exact in f32
     return (uint32_t)__builtin_bit_cast(uint16_t, dh) | ((uint32_t)__builtin_bit_cast(uint16_t, s) << 16);
   }
 };
@@ -79,19 +88,17 @@ __device__ __forceinline__ uint32_t pack4(const int q[4]) {
          ((uint32_t)(q[3] & 255) << 24);
 }
 
+// One lane's part of a q8 block: its four codes, one per byte, and the block's
+// (dh, s) word (the same in all eight lanes).
+struct Q8Quad {
+  uint32_t codes, pair;
+};
+
 __device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
-  const float amax = max8(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-  const float d32 = amax / 127.0f;
-  Q8Quad r;
-  r.dh = (_Float16)d32;  // round to nearest even
-  const float dhf = (float)r.dh;
-  const float inv = dhf == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(dhf);
+  const Q8Scale sc(max8(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)))));
   int q[4];
-  quant4(v, dhf, inv, q);
-  const int S = sum8(q[0] + q[1] + q[2] + q[3]);
-  r.s = (_Float16)(dhf * (float)S);  // the product is exact in f32
-  r.codes = pack4(q);
-  return r;
+  quant4(v, sc.dhf, sc.inv, q);
+  return {pack4(q), sc.pair(sum8(q[0] + q[1] + q[2] + q[3]))};
 }
 
 }  // namespace qmm
