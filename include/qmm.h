@@ -55,6 +55,12 @@ extern "C" {
                       2.2): 0.5 instead of 1 byte per weight, unpacked by the
                       GEMM.  Results are bit-identical to QMM_Q4_K's. */
 
+/* The rows forms: the same blocks registered for qmm_mmv, kept row by row at the
+ * blocks' own size (0.5625 and 0.8203 bytes per weight).  The MMQ needs the
+ * types above; a program that runs both registers a matrix twice. */
+#define QMM_Q4_K_ROWS 24
+#define QMM_Q6_K_ROWS 26
+
 /* Element types of activation tensors. */
 #define QMM_F32 0
 #define QMM_F16 1
@@ -82,21 +88,26 @@ extern "C" {
 /* Largest stride (in elements) from row to row of a strided tensor. */
 #define QMM_MAX_STRIDE (1 << 24)
 
+/* Most tokens of one qmm_mmv. */
+#define QMM_MV_MAX_TOKENS 8
+
 /* Tokens are padded to a multiple of this many in the qact buffer. */
 #define QMM_TOKEN_PAD 128
 
 typedef struct qmm_weights qmm_weights;
 
 typedef struct {
-    int type;            /* QMM_Q4_K, QMM_Q4_K_PACKED or QMM_Q6_K */
+    int type;            /* QMM_Q4_K, QMM_Q4_K_PACKED, QMM_Q6_K, QMM_Q4_K_ROWS or QMM_Q6_K_ROWS */
     int64_t od;          /* output rows */
     int64_t id;          /* inner dimension */
-    int64_t od_pad;      /* rows padded with zeros to the row tile */
+    int64_t od_pad;      /* rows padded with zeros to the row tile (rows forms: od) */
     size_t raw_bytes;    /* od * (id/256) * (144 or 210): the k-quant bytes */
     size_t plane_bytes;  /* device memory the handle holds */
-    size_t wd_offset;    /* byte offset of the d plane (q6_K; q4_K: == plane_bytes) */
+    size_t wd_offset;    /* byte offset of the d plane (q6_K; q4_K: == plane_bytes);
+                            rows forms: of the plane after the codes */
     size_t sm_offset;    /* byte offset of the stage-record plane of scales, mins,
-                            d and dmin (q4_K; q6_K: == plane_bytes) */
+                            d and dmin (q4_K; q6_K: == plane_bytes); q6_K rows:
+                            of the scales (q4_K rows: == plane_bytes) */
 } qmm_info;
 
 /*
@@ -104,7 +115,8 @@ typedef struct {
  * expand it once into the planes the GEMM reads (the registration-time planes
  * of r56 section 2.2 and r58 section 3.2; layout: see qmm_weights_export).
  *   type        QMM_Q4_K, QMM_Q4_K_PACKED (q4_K blocks, codes kept packed on
- *               the device) or QMM_Q6_K
+ *               the device) or QMM_Q6_K for the MMQ; QMM_Q4_K_ROWS or
+ *               QMM_Q6_K_ROWS for qmm_mmv
  *   od, id      the weight is od rows of id weights; id % 256 == 0.  Any od >= 1
  *               (odd included) is valid: rows are padded with zeros internally.
  *   host_bytes  host memory, od rows * (id/256) blocks, row major, exactly
@@ -157,6 +169,20 @@ int qmm_weights_info(const qmm_weights *w, qmm_info *out);
  *                       exact in binary32, zeros stored as +0
  *                 (the two records of a super-block both hold its mins, d and
  *                 dmin)
+ * Rows forms, planes of [od][nsb] blocks without padding rows, each starting at a
+ * multiple of 256 bytes:
+ *   at 0          128 bytes per block: q4_K the code bytes, q6_K the low code bits
+ *   at wd_offset  q4_K 16 bytes per block: for each pair of 32-blocks (2i, 2i + 1)
+ *                 24 bits (three bytes, little endian) of scale and min of 2i,
+ *                 scale and min of 2i + 1, six bits each from the lowest; then
+ *                 binary16 d and dmin
+ *                 q6_K 64 bytes per block: for each group p of 16 low bytes eight
+ *                 bytes of high code bits: bits 2j, 2j + 1 of byte b are those of
+ *                 the code in the low nibble (b < 4) or the high nibble (b >= 4)
+ *                 of the group's byte 4j + b%4, the upper one inverted
+ *   at sm_offset  q6_K 16 bytes per block: for each p the int8 scale of the low
+ *                 nibbles' weights and that of the high ones'
+ *   after it      q6_K binary16 d per block
  * Errors: QMM_EINVAL (null pointers, bytes mismatch), QMM_EHIP.
  */
 int qmm_weights_export(const qmm_weights *w, void *host, size_t bytes);
@@ -392,6 +418,24 @@ typedef struct {
 int qmm_mmq_epilogue(const qmm_weights *w, const void *qact, size_t qact_bytes, int64_t n_tok,
                      const qmm_epilogue *ep, int out_type, void *out, int64_t out_stride,
                      void *work, size_t work_bytes, void *stream);
+
+/*
+ * qmm_mmv -- the product for up to QMM_MV_MAX_TOKENS tokens straight from the
+ * activations, in one kernel: decode steps, a few sequences at once.  The
+ * numbers are the MMQ's: x is quantized to the q8 blocks that
+ * qmm_quantize_activations writes, block dots are exact, scales are applied and
+ * summed in f32 (in another order than qmm_mmq's).
+ *   w           a handle of a rows form (current device = its device)
+ *   x, x_type   device [n_tok] rows of id activations, QMM_F32, QMM_F16 or
+ *               QMM_BF16, x_stride elements from row to row (a multiple of 4 in
+ *               [id, QMM_MAX_STRIDE]); aligned to four elements; |x| <= 2046
+ *   ep, out_type, out, out_stride  as for qmm_mmq_epilogue, without QMM_Q8
+ * No workspace; can be captured into a graph.  Deterministic; a token's result
+ * may depend in its last bits on how many tokens the call has.
+ * Errors: QMM_EINVAL, QMM_EHIP.  n_tok == 0 is an empty batch.
+ */
+int qmm_mmv(const qmm_weights *w, const void *x, int x_type, int64_t x_stride, int64_t n_tok,
+            const qmm_epilogue *ep, int out_type, void *out, int64_t out_stride, void *stream);
 
 /* The launch plan of one MMQ (qmm_mmq, qmm_mmq_noalloc): how its output tiles
  * map onto work-groups on a GPU of a given size, and the tail partials it needs.

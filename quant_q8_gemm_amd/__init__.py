@@ -12,6 +12,8 @@ built, importing this package raises immediately -- there is no other path.
 and what stands between the products of a layer:
 
     r = qmm.norm_quantize(h, weight, y=out)                     # r.h = h + out, r.qact = q8(norm(r.h))
+    out = qmm.mmq_epilogue(w, r.qact, n_tok, act="silu", dtype=torch.float16)
+    out = qmm.mmv(w_rows, x, residual=h)                        # up to 8 tokens, w_rows: a rows-form handle
 """
 from __future__ import annotations
 
@@ -47,13 +49,16 @@ ESHAPE = -2
 ENOMEM = -3
 EHIP = -4
 TOKEN_PAD = 128
-BLOCK_BYTES = {Q4_K: 144, Q4_K_PACKED: 144, Q6_K: 210}
+Q4_K_ROWS = 24  # the rows forms, for mmv
+Q6_K_ROWS = 26
+MV_MAX_TOKENS = 8
+BLOCK_BYTES = {Q4_K: 144, Q4_K_PACKED: 144, Q6_K: 210, Q4_K_ROWS: 144, Q6_K_ROWS: 210}
 
 # The full list of entry points include/qmm.h declares.
 EXPORTS = ("qmm_register_weights", "qmm_weights_info", "qmm_weights_export", "qmm_release_weights",
            "qmm_set_memory_cap", "qmm_qact_bytes", "qmm_quantize_activations", "qmm_mmq",
            "qmm_mmq_noalloc", "qmm_stream_release", "qmm_mmq_plan", "qmm_mmq_plan_work", "qmm_last_error",
-           "qmm_dequantize_activations", "qmm_norm_quantize", "qmm_mmq_epilogue")
+           "qmm_dequantize_activations", "qmm_norm_quantize", "qmm_mmq_epilogue", "qmm_mmv")
 MAX_CUS = 65536
 # element types of activation tensors
 F32, F16, BF16 = 0, 1, 2
@@ -129,6 +134,8 @@ _lib.qmm_norm_quantize.argtypes = [ctypes.POINTER(Norm), _I64, _I64, _P]
 _lib.qmm_norm_quantize.restype = ctypes.c_int
 _lib.qmm_mmq_epilogue.argtypes = [_P, _P, _SZ, _I64, ctypes.POINTER(Epilogue), ctypes.c_int, _P, _I64, _P, _SZ, _P]
 _lib.qmm_mmq_epilogue.restype = ctypes.c_int
+_lib.qmm_mmv.argtypes = [_P, _P, ctypes.c_int, _I64, _I64, ctypes.POINTER(Epilogue), ctypes.c_int, _P, _I64, _P]
+_lib.qmm_mmv.restype = ctypes.c_int
 _lib.qmm_last_error.argtypes = []
 _lib.qmm_last_error.restype = ctypes.c_char_p
 
@@ -466,4 +473,27 @@ def mmq_epilogue(w: Weights, qact, n_tok: int, *, bias=None, act: str = "none", 
         work_ptr, work_bytes = work.data_ptr(), work.numel()
     _check(_lib.qmm_mmq_epilogue(w.handle, qact.data_ptr(), qact.numel(), n_tok, ctypes.byref(ep), out_type, ptr,
                                  stride, work_ptr, work_bytes, _stream(stream)))
+    return out
+
+
+def mmv(w: Weights, x, *, bias=None, act: str = "none", mul=None, residual=None, scale: float = 1.0,
+        residual_scale: float = 1.0, dtype=torch.float32, out=None, stream=None):
+    """The product for up to MV_MAX_TOKENS tokens straight from the activations, with mmq_epilogue's epilogue:
+
+        scale * mul * act(x @ W^T + bias) + residual_scale * residual
+
+    w: a handle of Q4_K_ROWS or Q6_K_ROWS; x: [n_tok][id] of float32, float16 or bfloat16 (rows may be strided).
+    The result is [n_tok][od] of `dtype`, or `out`."""
+    if x.dim() != 2:
+        raise QmmError(EINVAL, "x must be [n_tok][id]")
+    n_tok = x.shape[0]
+    x_type = _elem(x.dtype, "x")
+    x_ptr, x_stride = _rows(x, "x", (n_tok, w.id))
+    ep = _epilogue(n_tok, w.od, bias, act, mul, residual, scale, residual_scale)
+    if out is None:
+        _elem(dtype)
+        out = _empty((n_tok, w.od), dtype, x.device, stream)
+    out_ptr, out_stride = _rows(out, "out", (n_tok, w.od))
+    _check(_lib.qmm_mmv(w.handle, x_ptr, x_type, x_stride, n_tok, ctypes.byref(ep), _elem(out.dtype, "out"), out_ptr,
+                        out_stride, _stream(stream)))
     return out

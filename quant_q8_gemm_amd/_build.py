@@ -7,7 +7,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-KERNELS = ["qmm_repack.hip", "qmm_prepass.hip", "qmm_norm.hip", "qmm_mmq.hip"]
+KERNELS = ["qmm_repack.hip", "qmm_prepass.hip", "qmm_norm.hip", "qmm_mmq.hip", "qmm_mmv.hip"]
 SOURCES = [os.path.join(CSRC, "qmm_api.cpp")] + [os.path.join(CSRC, k) for k in KERNELS]
 LIB = os.path.join(HERE, "libqmm.so")
 # calibration kernels for the benchmark's measured rooflines (not part of the ABI),

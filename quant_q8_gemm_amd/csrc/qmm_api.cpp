@@ -63,10 +63,14 @@ void ok() { g_last_error.clear(); }
 
 size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
 
-size_t block_bytes(int type) { return qmm::is_q4k(type) ? 144 : 210; }
+size_t block_bytes(int type) { return qmm::is_q4k(type) || type == QMM_Q4_K_ROWS ? 144 : 210; }
 
 const char* type_name(int type) {
-  return type == QMM_Q6_K ? "q6_K" : type == QMM_Q4_K ? "q4_K" : "q4_K (codes packed)";
+  return type == QMM_Q6_K          ? "q6_K"
+         : type == QMM_Q4_K        ? "q4_K"
+         : type == QMM_Q4_K_PACKED ? "q4_K (codes packed)"
+         : type == QMM_Q4_K_ROWS   ? "q4_K (rows)"
+                                   : "q6_K (rows)";
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -89,8 +93,8 @@ int64_t token_pad(int64_t n_tok) { return (n_tok + qmm::kTokenPad - 1) / qmm::kT
 
 int check_type(int type) {
   if (type != QMM_Q4_K && type != QMM_Q4_K_PACKED && type != QMM_Q6_K)
-    return fail(QMM_EINVAL, "type must be QMM_Q4_K (%d), QMM_Q4_K_PACKED (%d) or QMM_Q6_K (%d), got %d",
-                QMM_Q4_K, QMM_Q4_K_PACKED, QMM_Q6_K, type);
+    return fail(QMM_EINVAL, "type must be QMM_Q4_K (%d), QMM_Q4_K_PACKED (%d) or QMM_Q6_K (%d)%s, got %d", QMM_Q4_K,
+                QMM_Q4_K_PACKED, QMM_Q6_K, qmm::is_rows(type) ? " (a rows form has no MMQ)" : "", type);
   return QMM_OK;
 }
 
@@ -139,7 +143,9 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
                          void* stream, qmm_weights** out) {
   if (out == nullptr) return fail(QMM_EINVAL, "out is NULL");
   *out = nullptr;
-  if (int rc = check_type(type)) return rc;
+  const bool rows = qmm::is_rows(type);
+  if (!rows)
+    if (int rc = check_type(type)) return rc;
   if (int rc = check_od(od)) return rc;
   if (int rc = check_id(id)) return rc;
   if (host_bytes == nullptr) return fail(QMM_EINVAL, "host_bytes is NULL");
@@ -151,7 +157,11 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
   // q6_K: codes, d; q4_K: codes, stage records (one of the last two is empty)
   const size_t off_wd = round_up(qmm::wq_bytes(type, p.od_pad, id), 256);
   const size_t off_sm = off_wd + round_up(qmm::wd_bytes(type, p.od_pad, id), 256);
-  const size_t plane_bytes = off_sm + round_up(qmm::wsm_bytes(type, p.od_pad, id), 256);
+  size_t plane_bytes = off_sm + round_up(qmm::wsm_bytes(type, p.od_pad, id), 256);
+  if (rows) {
+    p.od_pad = od;
+    p.rows = qmm::row_planes(type, od, id, nullptr, &plane_bytes);
+  }
   // reserve the bytes against the cap before allocating, atomically, so that
   // registrations on several threads cannot overshoot it together; every
   // failure below gives them back
@@ -188,13 +198,18 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
     return e == hipErrorOutOfMemory ? fail(QMM_ENOMEM, "hipMalloc(%zu) failed: out of memory", nbytes)
                                     : fail_hip(e, "hipMalloc(raw)");
   }
-  p.wq = (int8_t*)alloc;
-  p.wd = qmm::is_q4k(type) ? nullptr : (float*)((char*)alloc + off_wd);
-  p.wsm = qmm::is_q4k(type) ? (uint8_t*)alloc + off_sm : nullptr;
+  if (rows) {
+    p.rows = qmm::row_planes(type, od, id, alloc, &plane_bytes);
+  } else {
+    p.wq = (int8_t*)alloc;
+    p.wd = qmm::is_q4k(type) ? nullptr : (float*)((char*)alloc + off_wd);
+    p.wsm = qmm::is_q4k(type) ? (uint8_t*)alloc + off_sm : nullptr;
+  }
   int rc = QMM_OK;
   if ((e = hipMemcpyAsync(raw, host_bytes, nbytes, hipMemcpyHostToDevice, s)) != hipSuccess)
     rc = fail_hip(e, "hipMemcpyAsync(weights)");
-  else if ((e = qmm::launch_repack((const uint8_t*)raw, p, s)) != hipSuccess)
+  else if ((e = rows ? qmm::launch_repack_rows((const uint8_t*)raw, type, od, id, p.rows, s)
+                     : qmm::launch_repack((const uint8_t*)raw, p, s)) != hipSuccess)
     rc = fail_hip(e, "repack launch");
   else if ((e = hipStreamSynchronize(s)) != hipSuccess)
     rc = fail_hip(e, "hipStreamSynchronize(registration)");
@@ -209,8 +224,9 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
   w->device = device;
   w->raw_bytes = nbytes;
   w->plane_bytes = plane_bytes;
-  w->wd_offset = qmm::is_q4k(type) ? plane_bytes : off_wd;
-  w->sm_offset = qmm::is_q4k(type) ? off_sm : plane_bytes;
+  w->wd_offset = rows ? p.rows.heads_offset : qmm::is_q4k(type) ? plane_bytes : off_wd;
+  w->sm_offset = type == QMM_Q6_K_ROWS                 ? p.rows.scales_offset
+                 : qmm::is_q4k(type) && !rows ? off_sm : plane_bytes;
   w->alloc = alloc;
   if (getenv("QMM_LOG") != nullptr)
     fprintf(stderr, "qmm: registered %s od=%lld id=%lld od_pad=%lld raw=%zu planes=%zu device=%d\n",
@@ -521,6 +537,13 @@ int resolve_epilogue(const qmm_epilogue* ep, int64_t n_tok, int64_t od, int out_
   return QMM_OK;
 }
 
+int check_mmq_handle(const qmm_weights* w) {
+  if (w == nullptr) return fail(QMM_EINVAL, "NULL weights handle");
+  if (qmm::is_rows(w->p.type))
+    return fail(QMM_EINVAL, "the handle holds %s weights, the form of qmm_mmv", type_name(w->p.type));
+  return QMM_OK;
+}
+
 // The current device, which has to be the handle's, and its compute units.
 int current_device(const qmm_weights* w, int* device, int* num_cus) {
   hipError_t e = hipGetDevice(device);
@@ -537,7 +560,7 @@ int current_device(const qmm_weights* w, int* device, int* num_cus) {
 int prepare_mmq(const qmm_weights* w, const void* qact, size_t qact_bytes, int64_t n_tok, const float* out,
                 qmm::MmqPlan* plan, int* device, int* num_cus, bool* launch) {
   *launch = false;
-  if (w == nullptr) return fail(QMM_EINVAL, "NULL weights handle");
+  if (int rc = check_mmq_handle(w)) return rc;
   if (int rc = check_tokens(n_tok)) return rc;
   if (n_tok == 0) {  // empty batch: an empty output, nothing launched
     if (qact_bytes != 0) return fail(QMM_ESHAPE, "qact_bytes %zu != 0 for n_tok = 0", qact_bytes);
@@ -659,7 +682,7 @@ int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, 
   if (int rc = check_epilogue(ep, out_type)) return rc;
   if ((work == nullptr) != (work_bytes == 0) || !aligned(work, 16))
     return fail(QMM_EINVAL, "work must be 16-byte aligned and come with its size (NULL with 0)");
-  if (w == nullptr) return fail(QMM_EINVAL, "NULL weights handle");
+  if (int rc = check_mmq_handle(w)) return rc;
   if (int rc = check_tokens(n_tok)) return rc;
   const size_t need = qmm_qact_bytes(n_tok, w->p.id);
   if (qact_bytes != need)
@@ -697,6 +720,38 @@ int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, 
   hipError_t e = qmm::launch_mmq_epilogue(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), r,
                                           (float*)scratch, s);
   if (e != hipSuccess) return fail_hip(e, "mmq launch");
+  ok();
+  return QMM_OK;
+}
+
+int qmm_mmv(const qmm_weights* w, const void* x, int x_type, int64_t x_stride, int64_t n_tok, const qmm_epilogue* ep,
+            int out_type, void* out, int64_t out_stride, void* stream) {
+  if (int rc = check_elem("out_type", out_type)) return rc;
+  if (int rc = check_epilogue(ep, out_type)) return rc;
+  if (int rc = check_elem("x_type", x_type)) return rc;
+  if (n_tok < 0 || n_tok > QMM_MV_MAX_TOKENS)
+    return fail(QMM_EINVAL, "n_tok must be in [0, %d], got %lld", QMM_MV_MAX_TOKENS, (long long)n_tok);
+  if (n_tok > 0 && x == nullptr) return fail(QMM_EINVAL, "x is NULL");
+  const size_t xb = elem_bytes(x_type);
+  if (!aligned(x, 4 * xb) || x_stride % 4 != 0)
+    return fail(QMM_EINVAL, "x and its rows must be aligned to four elements");
+  if (w == nullptr) return fail(QMM_EINVAL, "NULL weights handle");
+  if (!qmm::is_rows(w->p.type))
+    return fail(QMM_EINVAL, "the handle holds %s weights, qmm_mmv reads the rows forms", type_name(w->p.type));
+  if (n_tok == 0) {  // empty batch: an empty output, nothing launched
+    ok();
+    return QMM_OK;
+  }
+  if (int rc = check_stride("x", x_stride, w->p.id)) return rc;
+  qmm::Epilogue r{};
+  Range written{};
+  if (int rc = resolve_epilogue(ep, n_tok, w->p.od, out_type, out, out_stride,
+                                rows_range("x", x, x_stride, n_tok, w->p.id, xb), &r, &written))
+    return rc;
+  int device = -1, num_cus = 0;
+  if (int rc = current_device(w, &device, &num_cus)) return rc;
+  hipError_t e = qmm::launch_mmv(w->p, x, x_type, x_stride, (int)n_tok, r, num_cus, (hipStream_t)stream);
+  if (e != hipSuccess) return fail_hip(e, "mmv launch");
   ok();
   return QMM_OK;
 }

@@ -10,10 +10,19 @@
 
 namespace qmm {
 
+// The planes of a rows-form matrix (layout documented in qmm_mmv.hip).
+struct RowPlanes {
+  uint8_t* codes;   // 128 bytes per block
+  uint8_t* heads;   // q4_K scales, mins, d, dmin; q6_K high code bits
+  uint8_t* scales;  // q6_K scales
+  uint16_t* d;      // q6_K d
+  size_t heads_offset, scales_offset, d_offset;  // bytes from codes
+};
+
 // Device planes of one registered weight matrix (layout documented in
 // qmm_repack.hip next to the repack kernel).
 struct Planes {
-  int type;          // QMM_Q4_K, QMM_Q4_K_PACKED or QMM_Q6_K
+  int type;          // QMM_Q4_K, QMM_Q4_K_PACKED, QMM_Q6_K; QMM_Q4_K_ROWS, QMM_Q6_K_ROWS
   int64_t od, id;    // logical shape
   int64_t od_pad;    // rows padded to kRowPad
   int64_t nsb;       // id / 256
@@ -22,6 +31,7 @@ struct Planes {
   float* wd;         // q6_K: d per (row, super-block); else nullptr
   uint8_t* wsm;      // q4_K: one 1 KiB record per (32-row block, 4-chunk stage) of the
                      // stage's scales and its super-block's mins, d*2^25 and -dmin; else nullptr
+  RowPlanes rows;    // the rows form, instead of the three above
 };
 
 constexpr int kRowPad = 128;     // weight rows are padded to a multiple of this
@@ -31,6 +41,7 @@ constexpr int kQ4PackedFrag = 512; // the same, packed: two codes per byte
 
 // Both q4_K registrations share every plane but the codes'.
 constexpr bool is_q4k(int type) { return type == 4 || type == 14; }  // QMM_Q4_K, QMM_Q4_K_PACKED
+constexpr bool is_rows(int type) { return type == QMM_Q4_K_ROWS || type == QMM_Q6_K_ROWS; }
 
 // q4_K's per-stage record: the 4 scales of each of the 32 rows (f16 integers,
 // [row][chunk]), the 8 mins of the stage's super-block ([chunk/4][row][chunk%4],
@@ -47,6 +58,13 @@ size_t wsm_bytes(int type, int64_t od_pad, int64_t id);
 hipError_t launch_repack(const uint8_t* raw, const Planes& p, hipStream_t s);
 hipError_t launch_quantize(const float* x, int64_t n_tok, int64_t t_pad, int64_t id,
                            uint8_t* qact, hipStream_t s);
+// The rows form's planes at `base` and the bytes they need.
+RowPlanes row_planes(int type, int64_t od, int64_t id, void* base, size_t* bytes);
+hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t id, const RowPlanes& r, hipStream_t s);
+struct Epilogue;  // qmm_epilogue.h
+// The product of 1 to QMM_MV_MAX_TOKENS tokens with a rows-form matrix.
+hipError_t launch_mmv(const Planes& p, const void* x, int x_type, int64_t x_stride, int n_tok, const Epilogue& ep,
+                      int num_cus, hipStream_t s);
 // The norms and residual sum of qmm_norm_quantize on checked arguments
 // (t_pad: the tokens of the qact buffer, 0 without one).
 hipError_t launch_norm(const qmm_norm& a, int64_t n_tok, int64_t t_pad, int64_t id, hipStream_t s);
@@ -76,7 +94,6 @@ void plan_work(const MmqPlan& plan, int nsb, int64_t wg, int* rt, int* tt, int* 
 size_t mmq_scratch_max_bytes(int num_cus);
 hipError_t launch_mmq(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok,
                       int64_t t_pad, float* out, float* part, hipStream_t s);
-struct Epilogue;  // qmm_epilogue.h
 hipError_t launch_mmq_epilogue(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok,
                                int64_t t_pad, const Epilogue& ep, float* part, hipStream_t s);
 // The allocation-free entry point's tail scratch: a static device array of

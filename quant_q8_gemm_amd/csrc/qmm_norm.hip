@@ -24,7 +24,6 @@ constexpr int kMaxWaves = kMaxThreads / 64;
 
 // Sum over the wave's 64 lanes, in every lane: four DPP steps give each row of
 // 16 its sum, the four rows are added in order.
-constexpr int kDppMirror = 0x140;  // row_mirror: lane i <-> 15 - i
 __device__ __forceinline__ float dpp_add(float v, int moved) { return v + __builtin_bit_cast(float, moved); }
 __device__ __forceinline__ float wave_sum(float v) {
   v = dpp_add(v, dpp<kDppQuadXor1>(__builtin_bit_cast(int, v)));

@@ -14,6 +14,7 @@ namespace qmm {
 constexpr int kDppQuadXor1 = 0xB1;     // quad_perm [1, 0, 3, 2]
 constexpr int kDppQuadXor2 = 0x4E;     // quad_perm [2, 3, 0, 1]
 constexpr int kDppHalfMirror = 0x141;  // row_half_mirror
+constexpr int kDppMirror = 0x140;      // row_mirror: lane i <-> 15 - i of each row of 16
 
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {

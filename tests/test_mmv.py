@@ -1,0 +1,260 @@
+"""qmm_mmv and the rows forms: refusals on the CPU; on the GPU the registered bytes,
+the sums against the oracle and the epilogue on them against its formula in 64 bits.
+
+Tolerance of the sums: integer dots are exact; a term of the oracle's sum (a
+32-block's scaled dot, its min) meets at most five roundings on its way into a
+lane's sum and then one addition per block of that lane, two per super-block, six
+over the wave and eight over the waves: K = 2*ceil(nsb/8) + 20 units of 2^-24 of
+the sum of the terms' magnitudes."""
+import ctypes
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import oracle  # noqa: E402
+import quant_q8_gemm_amd as qmm  # noqa: E402
+import synth  # noqa: E402
+from tests.test_mmq_epilogue import ACTS, TYPES, U, check, device, sides  # noqa: E402,F401
+
+gpu = pytest.mark.gpu
+ROWS = {synth.Q4_K: qmm.Q4_K_ROWS, synth.Q6_K: qmm.Q6_K_ROWS}
+
+
+# ---- on the CPU ----
+
+def test_refusals_that_need_no_handle():
+    L, x, o = qmm._lib, 1 << 20, 1 << 21
+
+    def call(n_tok=2, x_ptr=x, x_type=0, x_stride=512, out_type=0, **kw):
+        ep = qmm.Epilogue(**{"scale": 1.0, **kw})
+        return L.qmm_mmv(None, x_ptr, x_type, x_stride, n_tok, ctypes.byref(ep), out_type, o, 16, None)
+
+    for change, word in (({"n_tok": -1}, "n_tok"), ({"n_tok": 9}, "n_tok"), ({"x_type": 3}, "x_type"), ({"x_ptr": None}, "x is"),
+                         ({"x_ptr": x + 8}, "aligned"), ({"x_ptr": x + 4, "x_type": 1}, "aligned"),
+                         ({"x_stride": 514}, "aligned"), ({"out_type": 3}, "out_type"), ({"act": 7}, "act"),
+                         ({"scale": float("inf")}, "finite"), ({}, "handle")):
+        assert call(**change) == qmm.EINVAL, change
+        assert word in qmm.last_error(), (change, qmm.last_error())
+
+
+def test_rows_forms_have_no_plan():
+    for t in (qmm.Q4_K_ROWS, qmm.Q6_K_ROWS):
+        with pytest.raises(qmm.QmmError) as e:
+            qmm.mmq_plan(t, 256, 256, 1, 256)
+        assert e.value.code == qmm.EINVAL
+    h = ctypes.c_void_p()
+    buf = ctypes.create_string_buffer(840)
+    f = qmm._lib.qmm_register_weights
+    assert f(qmm.Q4_K_ROWS, 4, 256, buf, 4 * 210, None, ctypes.byref(h)) == qmm.EINVAL
+    assert f(qmm.Q6_K_ROWS, 4, 256, buf, 4 * 144, None, ctypes.byref(h)) == qmm.EINVAL
+
+
+# ---- on the GPU ----
+
+def read_rows(buf, type_, od, id_, wd, sm):
+    """The exported rows form back into block bytes, from the header's description."""
+    nb = od * id_ // 256
+    out = np.zeros((nb, 144 if type_ == synth.Q4_K else 210), np.uint8)
+    codes = buf[:nb * 128].reshape(nb, 128)
+    if type_ == synth.Q4_K:
+        assert sm == buf.size
+        head = buf[wd:wd + nb * 16].reshape(nb, 16).astype(np.int64)
+        out[:, 0:4], out[:, 16:] = head[:, 12:], codes
+        sc, mn = np.zeros((nb, 8), np.int64), np.zeros((nb, 8), np.int64)
+        for i in range(4):
+            f = head[:, 3 * i] | head[:, 3 * i + 1] << 8 | head[:, 3 * i + 2] << 16
+            sc[:, 2 * i], mn[:, 2 * i], sc[:, 2 * i + 1], mn[:, 2 * i + 1] = f & 63, f >> 6 & 63, f >> 12 & 63, f >> 18
+        out[:, 4:8] = sc[:, :4] | (sc[:, 4:] >> 4) << 6
+        out[:, 8:12] = mn[:, :4] | (mn[:, 4:] >> 4) << 6
+        out[:, 12:16] = (sc[:, 4:] & 15) | (mn[:, 4:] & 15) << 4
+        return out
+    out[:, :128] = codes
+    high = buf[wd:wd + nb * 64].reshape(nb, 8, 2, 4).astype(np.int64)  # [p][nibble][b]
+    qh = np.zeros((nb, 2, 32), np.int64)
+    for p in range(8):
+        half, m2, lh = p // 4, p // 2 % 2, p % 2
+        for nib in range(2):
+            for j in range(4):
+                bits = (high[:, p, nib] >> 2 * j & 3) ^ 2
+                qh[:, half, 16 * lh + 4 * j:16 * lh + 4 * j + 4] |= bits << 2 * (m2 + 2 * nib)
+    out[:, 128:192] = qh.reshape(nb, 64)
+    scales = buf[sm:sm + nb * 16].reshape(nb, 8, 2)
+    for p in range(8):
+        out[:, 192 + p + 4 * (p // 4)], out[:, 192 + p + 4 * (p // 4) + 4] = scales[:, p, 0], scales[:, p, 1]
+    at = sm + (nb * 16 + 255) // 256 * 256
+    out[:, 208:] = buf[at:at + nb * 2].reshape(nb, 2)
+    return out
+
+
+@gpu
+@pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K])
+@pytest.mark.parametrize("od,id_", [(1, 256), (7, 768), (130, 1024), (20001, 256)])
+def test_registered_rows_are_the_blocks(device, type_, od, id_):  # noqa: F811
+    """The rows form holds every bit of the blocks: read back, it is the input, byte for byte."""
+    rng = np.random.default_rng(od)
+    bb = synth.BLOCK_BYTES[type_]
+    raw = rng.integers(0, 256, od * id_ // 256 * bb, dtype=np.uint8)
+    w = qmm.register_weights(ROWS[type_], od, id_, raw)
+    assert (w.type, w.od, w.id, w.od_pad, w.raw_bytes) == (ROWS[type_], od, id_, od, raw.size)
+    assert w.plane_bytes <= raw.size + 4 * 256
+    assert np.array_equal(read_rows(w.export(), type_, od, id_, w.wd_offset, w.sm_offset).reshape(-1), raw)
+    w.release()
+
+
+def sums_ok(got, raw, type_, od, id_, x):
+    q, dh, s = oracle.quantize(np.ascontiguousarray(x.float().cpu().numpy()))
+    ref, A = oracle.mmq_parallel(type_, raw, od, id_, q, dh, s)
+    K = 2 * ((id_ // 256 + 7) // 8) + 20
+    bad = ~(np.abs(got.cpu().numpy() - ref) <= K * U * A)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:3])
+
+
+SHAPES = [(1, 256), (3, 768), (64, 512), (131, 2048), (1030, 4096), (257, 11008), (4096, 2304), (20001, 512), (5, 65536)]
+
+
+@gpu
+@pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K], ids=["q4_K", "q6_K"])
+@pytest.mark.parametrize("od,id_", SHAPES)
+def test_mmv_against_oracle_and_formula(device, type_, od, id_):  # noqa: F811
+    print(f"mmv {synth.TYPE_NAMES[type_]} {od}x{id_}", flush=True)
+    for n_tok in (1, 2, 3, 4, 5, 6, 7, 8):
+        xt = TYPES[n_tok % 3]
+        raw, x = synth.case(type_, od, id_, n_tok, seed=od + n_tok, outliers=n_tok % 2 == 0)
+        x = torch.from_numpy(x).to(device).to(xt)
+        if n_tok in (1, 5):
+            w = qmm.register_weights(ROWS[type_], od, id_, raw)
+            kept = raw
+        got = qmm.mmv(w, x)
+        sums_ok(got, kept, type_, od, id_, x)
+        assert torch.equal(got, qmm.mmv(w, x)), "a repeat differs"
+        for i, act in enumerate(ACTS[n_tok % 2::2]):
+            c = sides(device, n_tok, od, TYPES[i % 3], i)
+            ep = {**c, "act": act, "scale": 0.5, "residual_scale": -1.25}
+            check(qmm.mmv(w, x, dtype=TYPES[(i + n_tok) % 3], **ep), got, ep)
+            ep = {("bias", "mul", "residual")[i % 3]: c[("bias", "mul", "residual")[i % 3]], "act": act}
+            check(qmm.mmv(w, x, **ep), got, ep)
+
+
+@gpu
+@pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K], ids=["q4_K", "q6_K"])
+def test_longest_rows_in_tiles(device, type_):  # noqa: F811
+    """Rows whose activations do not fit the LDS at once: the inner dimension in tiles, the last one short."""
+    for od, id_, n_tok in ((6, 1 << 20, 1), (37, 256 * 131, 8), (300, 256 * 61, 8)):
+        raw, x = synth.case(type_, od, id_, n_tok, seed=od)
+        w = qmm.register_weights(ROWS[type_], od, id_, raw)
+        x = torch.from_numpy(x).to(device)
+        sums_ok(qmm.mmv(w, x), raw, type_, od, id_, x)
+        w.release()
+
+
+@gpu
+@pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K], ids=["q4_K", "q6_K"])
+def test_extreme_blocks(device, type_):  # noqa: F811
+    """Full-range codes and scales, d and dmin of either sign, zero, subnormal and huge, activations with
+    vanishing scales: within the same tolerance."""
+    rng = np.random.default_rng(3)
+    od, id_, T = 70, 1024, 4
+    nb = od * id_ // 256
+    blk = rng.integers(0, 256, (nb, synth.BLOCK_BYTES[type_]), dtype=np.uint8)
+    halves = np.array([0x0000, 0x8000, 0x0001, 0x83FF, 0x7B53, 0xFB53, 0x1400, 0x9400], np.uint16)
+    for at in ((0, 2) if type_ == synth.Q4_K else (208,)):
+        blk[:, at:at + 2] = halves[rng.integers(0, 8, nb)].view(np.uint8).reshape(nb, 2)
+    x = synth.activations(rng, T, id_)
+    x[1] = 2046 * np.sign(x[1])
+    x[2] *= 1e-6
+    x[3, ::2] = 0
+    w = qmm.register_weights(ROWS[type_], od, id_, blk.reshape(-1))
+    x = torch.from_numpy(x).to(device)
+    sums_ok(qmm.mmv(w, x), blk.reshape(-1), type_, od, id_, x)
+    w.release()
+
+
+@gpu
+def test_mmv_numbers_are_the_mmqs(device):  # noqa: F811
+    """The same product through the prefill path: both within f32 rounding of each other's terms."""
+    for type_ in (synth.Q4_K, synth.Q6_K):
+        raw, x = synth.case(type_, 515, 1280, 6, seed=11)
+        w, wr = qmm.register_weights(type_, 515, 1280, raw), qmm.register_weights(ROWS[type_], 515, 1280, raw)
+        x = torch.from_numpy(x).to(device)
+        a, b = qmm.mmq(w, qmm.quantize_activations(x), 6), qmm.mmv(wr, x)
+        q, dh, s = oracle.quantize(x.cpu().numpy())
+        _, A = oracle.mmq(type_, raw, 515, 1280, q, dh, s)
+        assert np.all(np.abs((a - b).cpu().numpy()) <= 2e-5 * A)
+
+
+@gpu
+def test_mmv_strides_places_streams_and_graphs(device):  # noqa: F811
+    od, id_, T = 1030, 1024, 5
+    raw, x = synth.case(synth.Q6_K, od, id_, T, seed=4)
+    w = qmm.register_weights(qmm.Q6_K_ROWS, od, id_, raw)
+    x = torch.from_numpy(x).to(device).half()
+    c = sides(device, T, od, torch.bfloat16, 2)
+    ep = {**c, "act": "gelu"}
+    ref = qmm.mmv(w, x, dtype=torch.bfloat16, **ep)
+    wx = torch.full((T, id_ + 8), float("nan"), dtype=x.dtype, device=device)
+    wx[:, 4:-4] = x
+    wo = torch.full((T, od + 7), float("nan"), dtype=torch.bfloat16, device=device)
+    qmm.mmv(w, wx[:, 4:-4], out=wo[:, 3:-4], **ep)
+    assert torch.equal(wo[:, 3:-4], ref) and torch.isnan(wo[:, :3]).all() and torch.isnan(wo[:, -4:]).all()
+    for name in ("mul", "residual"):
+        place = c[name].clone()
+        qmm.mmv(w, x, out=place, **{**ep, name: place})
+        assert torch.equal(place, ref)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        outs = [qmm.mmv(w, x, dtype=torch.bfloat16, stream=s, **ep) for s in streams]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, ref) for o in outs)
+    out = torch.empty_like(ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qmm.mmv(w, x, out=out, **ep)
+    for i in range(3):
+        x.normal_()
+        want = qmm.mmv(w, x, dtype=torch.bfloat16, **ep)
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {i}"
+    del graph
+    w.release()
+
+
+@gpu
+def test_mmv_refusals_with_a_handle(device):  # noqa: F811
+    od, id_, T = 130, 512, 3
+    raw, x = synth.case(synth.Q4_K, od, id_, T, seed=1)
+    w, wm = qmm.register_weights(qmm.Q4_K_ROWS, od, id_, raw), qmm.register_weights(qmm.Q4_K, od, id_, raw)
+    x = torch.from_numpy(x).to(device)
+    c = sides(device, T, od, torch.float32, 1)
+
+    def refused(h=w, xx=x, **kw):
+        with pytest.raises(qmm.QmmError) as e:
+            qmm.mmv(h, xx, **kw)
+        assert e.value.code == qmm.EINVAL, e.value
+
+    refused(h=wm)
+    with pytest.raises(qmm.QmmError) as e:  # and the MMQ does not take a rows form
+        qmm.mmq(w, qmm.quantize_activations(x), T)
+    assert e.value.code == qmm.EINVAL
+    with pytest.raises(qmm.QmmError):
+        qmm.mmq_epilogue(w, qmm.quantize_activations(x), T)
+    refused(xx=torch.zeros(9, id_, device=device))
+    refused(xx=x[:, :256])
+    refused(xx=x.double())
+    refused(xx=x.cpu())
+    refused(xx=torch.zeros(T, id_ + 4, device=device)[:, 1:-3])
+    refused(xx=torch.zeros(T, id_ + 2, device=device)[:, :-2])
+    refused(xx=x[:1].expand(T, id_))
+    refused(dtype=torch.float64)
+    refused(mul=c["mul"].half(), residual=c["residual"])
+    refused(out=torch.empty(T, od + 1, device=device))
+    both = torch.zeros(T * id_ + 64, device=device)
+    refused(xx=both[:T * id_].view(T, id_), out=both[64:64 + T * od].view(T, od))
+    assert qmm.mmv(w, x[:0]).shape == (0, od)
+    w.release()
+    wm.release()
