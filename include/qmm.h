@@ -55,8 +55,8 @@ extern "C" {
                       2.2): 0.5 instead of 1 byte per weight, unpacked by the
                       GEMM.  Results are bit-identical to QMM_Q4_K's. */
 
-/* The rows forms: the same blocks registered for qmm_mmv, kept row by row at the
- * blocks' own size (0.5625 and 0.8203 bytes per weight).  The MMQ needs the
+/* The rows forms: the same blocks registered for qmm_mmv, kept at the blocks' own
+ * size (0.5625 and 0.8203 bytes per weight).  The MMQ needs the
  * types above; a program that runs both registers a matrix twice. */
 #define QMM_Q4_K_ROWS 24
 #define QMM_Q6_K_ROWS 26
@@ -100,7 +100,7 @@ typedef struct {
     int type;            /* QMM_Q4_K, QMM_Q4_K_PACKED, QMM_Q6_K, QMM_Q4_K_ROWS or QMM_Q6_K_ROWS */
     int64_t od;          /* output rows */
     int64_t id;          /* inner dimension */
-    int64_t od_pad;      /* rows padded with zeros to the row tile (rows forms: od) */
+    int64_t od_pad;      /* rows padded with zeros to the row tile (rows forms: to 16) */
     size_t raw_bytes;    /* od * (id/256) * (144 or 210): the k-quant bytes */
     size_t plane_bytes;  /* device memory the handle holds */
     size_t wd_offset;    /* byte offset of the d plane (q6_K; q4_K: == plane_bytes);
@@ -169,20 +169,20 @@ int qmm_weights_info(const qmm_weights *w, qmm_info *out);
  *                       exact in binary32, zeros stored as +0
  *                 (the two records of a super-block both hold its mins, d and
  *                 dmin)
- * Rows forms, planes of [od][nsb] blocks without padding rows, each starting at a
- * multiple of 256 bytes:
- *   at 0          128 bytes per block: q4_K the code bytes, q6_K the low code bits
- *   at wd_offset  q4_K 16 bytes per block: for each pair of 32-blocks (2i, 2i + 1)
- *                 24 bits (three bytes, little endian) of scale and min of 2i,
- *                 scale and min of 2i + 1, six bits each from the lowest; then
- *                 binary16 d and dmin
- *                 q6_K 64 bytes per block: for each group p of 16 low bytes eight
- *                 bytes of high code bits: bits 2j, 2j + 1 of byte b are those of
- *                 the code in the low nibble (b < 4) or the high nibble (b >= 4)
- *                 of the group's byte 4j + b%4, the upper one inverted
- *   at sm_offset  q6_K 16 bytes per block: for each p the int8 scale of the low
- *                 nibbles' weights and that of the high ones'
- *   after it      q6_K binary16 d per block
+ * Rows forms: tiles of 16 rows (row j is row n = j%16 of its tile) by nsb blocks;
+ * planes start at multiples of 256 bytes.  Byte group g of half h of a block is
+ * bytes 64h + 16g .. + 15 of its 128 code bytes.
+ *   at 0          [od_pad/16][nsb][h][g][n][16 bytes]: the code bytes, q6_K the low
+ *                 code bits
+ *   at wd_offset  q4_K [od_pad/16][nsb][n][4 words]: word i from its lowest bit: the
+ *                 six-bit scale and min of 32-block 2i, scale and min of 2i + 1, then
+ *                 byte i of the block's binary16 d and dmin
+ *                 q6_K [od_pad/16][nsb][g][n][h][8 bytes]: the high code bits: bits
+ *                 2j, 2j + 1 of byte b are those of the code in the low nibble
+ *                 (b < 4) or the high nibble (b >= 4) of the byte group's byte
+ *                 4j + b%4, the upper one inverted
+ *   at sm_offset  q6_K [od_pad/16][nsb][n][16]: the int8 scales plus 128
+ *   after it      q6_K [od_pad/16][nsb][n]: binary16 d
  * Errors: QMM_EINVAL (null pointers, bytes mismatch), QMM_EHIP.
  */
 int qmm_weights_export(const qmm_weights *w, void *host, size_t bytes);

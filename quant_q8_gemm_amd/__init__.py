@@ -17,7 +17,6 @@ and what stands between the products of a layer:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple
@@ -309,34 +308,38 @@ def _elem(dtype, what: str = "dtype") -> int:
     return t
 
 
-def _device(t, what: str) -> int:
+def _current(t, what: str) -> int:
     """The index of t's device, which has to be the current one."""
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0:
         raise QmmError(EINVAL, f"{what} must be a cuda tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise QmmError(EINVAL, f"{what} is on device {t.get_device()} but device {torch.cuda.current_device()} is current")
-    return t.get_device()
+    if device != torch.cuda.current_device():
+        raise QmmError(EINVAL, f"{what} is on device {device} but device {torch.cuda.current_device()} is current")
+    return device
 
 
-def _rows(t, what: str, shape, dtype=None):
+def _rows(t, what: str, shape, device: int, dtype=None):
     """(address, stride) of a tensor of rows with adjacent elements; the library checks the rest."""
-    if t is None:
-        return None, 0
-    _device(t, what)
-    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+    if t.get_device() != device:
+        raise QmmError(EINVAL, f"{what} must be on device {device}, got {t.device}")
+    if t.shape != shape or (dtype is not None and t.dtype != dtype):
         raise QmmError(EINVAL, f"{what} must be {list(shape)} {dtype or ''}, got {list(t.shape)} {t.dtype}")
-    if t.stride(1) != 1 and shape[1] > 1:
+    if shape[1] > 1 and t.stride(1) != 1:
         raise QmmError(EINVAL, f"{what} must have adjacent elements in a row")
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
 
 
-def _vector(t, what: str, n: int):
-    if t is None:
-        return None
-    _device(t, what)
-    if t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise QmmError(EINVAL, f"{what} must be a contiguous float32 [{n}] tensor")
+def _vector(t, what: str, n: int, device: int):
+    if t.get_device() != device or t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        raise QmmError(EINVAL, f"{what} must be a contiguous float32 [{n}] tensor on device {device}")
     return t.data_ptr()
+
+
+def _bytes(t, what: str, device: int):
+    """(address, size) of a flat byte tensor."""
+    if t.get_device() != device or t.dtype != torch.uint8 or t.dim() != 1 or not t.is_contiguous():
+        raise QmmError(EINVAL, f"{what} must be a contiguous one-dimensional uint8 tensor on device {device}")
+    return t.data_ptr(), t.numel()
 
 
 def _empty(shape, dtype, device, stream):
@@ -349,16 +352,23 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _raw_stream(stream, device: int):
+    """The hipStream_t of `stream` (None: torch's current one), as _stream without its detours."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def dequantize_activations(qact, n_tok: int, id_: int, dtype=torch.float32, out=None, stream=None):
     """The numbers a qact buffer stands for: [n_tok][id] of dtype (float32, float16 or bfloat16)."""
-    _check_qact(qact)
-    _device(qact, "qact")
+    device = _current(qact, "qact")
+    q_ptr, q_bytes = _bytes(qact, "qact", device)
     if out is None:
         _elem(dtype)
         out = _empty((n_tok, id_), dtype, qact.device, stream)
-    ptr, stride = _rows(out, "out", (n_tok, id_))
-    _check(_lib.qmm_dequantize_activations(qact.data_ptr(), qact.numel(), n_tok, id_, _elem(out.dtype, "out"), ptr,
-                                           stride, _stream(stream)))
+    ptr, stride = _rows(out, "out", (n_tok, id_), device)
+    _check(_lib.qmm_dequantize_activations(q_ptr, q_bytes, n_tok, id_, _elem(out.dtype, "out"), ptr, stride,
+                                           _raw_stream(stream, device)))
     return out
 
 
@@ -380,61 +390,57 @@ def norm_quantize(h, weight, *, y=None, bias=None, post_weight=None, post_bias=N
     True for a new tensor, a tensor to write into, or False.  h_out may be h or y itself."""
     if h.dim() != 2:
         raise QmmError(EINVAL, "h must be [n_tok][id]")
-    n_tok, id_ = h.shape
-    device, dtype = h.device, h.dtype
-    a = Norm(type=_elem(dtype, "h"), eps=eps, residual_scale=residual_scale, block_scale=block_scale)
+    shape, dtype = h.shape, h.dtype
+    n_tok, id_ = shape
+    elem = _elem(dtype, "h")
     if kind not in NORM_KINDS:
         raise QmmError(EINVAL, f"kind must be 'rms' or 'layer', got {kind!r}")
-    a.kind = NORM_KINDS[kind]
-    shape = (n_tok, id_)
-    a.h, a.h_stride = _rows(h, "h", shape)
+    device = _current(h, "h")
+    a = Norm(elem, NORM_KINDS[kind], eps, residual_scale, block_scale, *_rows(h, "h", shape, device))
     if y is not None:
-        a.y, a.y_stride = _rows(y, "y", shape, dtype)
-    a.weight = _vector(weight, "weight", id_)
+        a.y, a.y_stride = _rows(y, "y", shape, device, dtype)
+    a.weight = _vector(weight, "weight", id_, device)
     if bias is not None:
-        a.bias = _vector(bias, "bias", id_)
+        a.bias = _vector(bias, "bias", id_, device)
     if post_weight is not None:
-        a.post_weight = _vector(post_weight, "post_weight", id_)
+        a.post_weight = _vector(post_weight, "post_weight", id_, device)
     if post_bias is not None:
-        a.post_bias = _vector(post_bias, "post_bias", id_)
+        a.post_bias = _vector(post_bias, "post_bias", id_, device)
     if gate is not None:
         if gate.dim() == 1:
-            a.gate, a.gate_stride = _rows(gate.unsqueeze(0), "gate", (1, id_), dtype)[0], 0
+            a.gate, a.gate_stride = _rows(gate.unsqueeze(0), "gate", (1, id_), device, dtype)[0], 0
         else:
-            a.gate, a.gate_stride = _rows(gate, "gate", shape, dtype)
-    h_out = _empty(shape, dtype, device, stream) if h_out is True else None if h_out is False else h_out
-    if h_out is not None:
-        a.h_out, a.h_out_stride = _rows(h_out, "h_out", shape, dtype)
-    normed = _empty(shape, dtype, device, stream) if normed is True else None if normed is False else normed
-    if normed is not None:
-        a.normed, a.normed_stride = _rows(normed, "normed", shape, dtype)
+            a.gate, a.gate_stride = _rows(gate, "gate", shape, device, dtype)
+    if h_out is True:
+        h_out = _empty(shape, dtype, h.device, stream)
+    if h_out is not False:
+        a.h_out, a.h_out_stride = _rows(h_out, "h_out", shape, device, dtype)
+    if normed is True:
+        normed = _empty(shape, dtype, h.device, stream)
+    if normed is not False:
+        a.normed, a.normed_stride = _rows(normed, "normed", shape, device, dtype)
     if qact is True:
-        qact = _empty((qact_bytes(n_tok, id_),), torch.uint8, device, stream)
-    elif qact is False:
-        qact = None
-    if qact is not None:
-        _check_qact(qact)
-        _device(qact, "qact")
-        a.qact, a.qact_bytes = qact.data_ptr(), qact.numel()
-    _check(_lib.qmm_norm_quantize(ctypes.byref(a), n_tok, id_, _stream(stream)))
-    return NormResult(h_out, normed, qact)
+        qact = _empty((qact_bytes(n_tok, id_),), torch.uint8, h.device, stream)
+    if qact is not False:
+        a.qact, a.qact_bytes = _bytes(qact, "qact", device)
+    _check(_lib.qmm_norm_quantize(a, n_tok, id_, _raw_stream(stream, device)))
+    return NormResult(*(None if v is False else v for v in (h_out, normed, qact)))
 
 
-def _epilogue(n_tok: int, od: int, bias, act: str, mul, residual, scale: float, residual_scale: float) -> Epilogue:
-    ep = Epilogue(scale=scale, residual_scale=residual_scale)
-    if act not in ACTS:
+def _epilogue(shape, device: int, bias, act: str, mul, residual, scale: float, residual_scale: float) -> Epilogue:
+    ep = Epilogue(None, ACTS.get(act, -1), F32, scale, residual_scale)
+    if ep.act < 0:
         raise QmmError(EINVAL, f"act must be one of {sorted(ACTS)}, got {act!r}")
-    ep.act = ACTS[act]
     if bias is not None:
-        ep.bias = _vector(bias, "bias", od)
+        ep.bias = _vector(bias, "bias", shape[1], device)
     if mul is not None:
         ep.type = _elem(mul.dtype, "mul")
-        ep.mul, ep.mul_stride = _rows(mul, "mul", (n_tok, od))
+        ep.mul, ep.mul_stride = _rows(mul, "mul", shape, device)
     if residual is not None:
         if mul is not None and residual.dtype != mul.dtype:
             raise QmmError(EINVAL, f"mul is {mul.dtype} but residual is {residual.dtype}")
         ep.type = _elem(residual.dtype, "residual")
-        ep.residual, ep.residual_stride = _rows(residual, "residual", (n_tok, od))
+        ep.residual, ep.residual_stride = _rows(residual, "residual", shape, device)
     return ep
 
 
@@ -450,29 +456,22 @@ def mmq_epilogue(w: Weights, qact, n_tok: int, *, bias=None, act: str = "none", 
     (the next product's input; od % 256 == 0).  out: a tensor to write into; it may be mul or residual itself.
     work: a uint8 tensor for the split tails (mmq_plan(...).scratch_bytes), for graph capture; the stream's own
     scratch without it."""
-    _check_qact(qact)
-    _device(qact, "qact")
-    ep = _epilogue(n_tok, w.od, bias, act, mul, residual, scale, residual_scale)
+    device = _current(qact, "qact")
+    q_ptr, q_bytes = _bytes(qact, "qact", device)
+    shape = (n_tok, w.od)
+    ep = _epilogue(shape, device, bias, act, mul, residual, scale, residual_scale)
     if dtype == "q8":
         if out is None:
             out = _empty((qact_bytes(n_tok, w.od),), torch.uint8, qact.device, stream)
-        _check_qact(out)
-        _device(out, "out")
-        out_type, ptr, stride = Q8, out.data_ptr(), out.numel()
+        out_type, (ptr, stride) = Q8, _bytes(out, "out", device)
     else:
         if out is None:
             _elem(dtype)
-            out = _empty((n_tok, w.od), dtype, qact.device, stream)
-        out_type = _elem(out.dtype, "out")
-        ptr, stride = _rows(out, "out", (n_tok, w.od))
-    work_ptr, work_bytes = None, 0
-    if work is not None and work.numel():
-        if work.dtype != torch.uint8 or not work.is_contiguous():
-            raise QmmError(EINVAL, "work must be a contiguous cuda uint8 tensor")
-        _device(work, "work")
-        work_ptr, work_bytes = work.data_ptr(), work.numel()
-    _check(_lib.qmm_mmq_epilogue(w.handle, qact.data_ptr(), qact.numel(), n_tok, ctypes.byref(ep), out_type, ptr,
-                                 stride, work_ptr, work_bytes, _stream(stream)))
+            out = _empty(shape, dtype, qact.device, stream)
+        out_type, (ptr, stride) = _elem(out.dtype, "out"), _rows(out, "out", shape, device)
+    work_ptr, work_bytes = _bytes(work, "work", device) if work is not None and work.numel() else (None, 0)
+    _check(_lib.qmm_mmq_epilogue(w.handle, q_ptr, q_bytes, n_tok, ep, out_type, ptr, stride, work_ptr, work_bytes,
+                                 _raw_stream(stream, device)))
     return out
 
 
@@ -486,14 +485,16 @@ def mmv(w: Weights, x, *, bias=None, act: str = "none", mul=None, residual=None,
     The result is [n_tok][od] of `dtype`, or `out`."""
     if x.dim() != 2:
         raise QmmError(EINVAL, "x must be [n_tok][id]")
-    n_tok = x.shape[0]
+    n_tok, od = x.shape[0], w.od
     x_type = _elem(x.dtype, "x")
-    x_ptr, x_stride = _rows(x, "x", (n_tok, w.id))
-    ep = _epilogue(n_tok, w.od, bias, act, mul, residual, scale, residual_scale)
+    device = _current(x, "x")
+    x_ptr, x_stride = _rows(x, "x", (n_tok, w.id), device)
+    shape = (n_tok, od)
+    ep = _epilogue(shape, device, bias, act, mul, residual, scale, residual_scale)
     if out is None:
         _elem(dtype)
-        out = _empty((n_tok, w.od), dtype, x.device, stream)
-    out_ptr, out_stride = _rows(out, "out", (n_tok, w.od))
-    _check(_lib.qmm_mmv(w.handle, x_ptr, x_type, x_stride, n_tok, ctypes.byref(ep), _elem(out.dtype, "out"), out_ptr,
-                        out_stride, _stream(stream)))
+        out = _empty(shape, dtype, x.device, stream)
+    out_ptr, out_stride = _rows(out, "out", shape, device)
+    _check(_lib.qmm_mmv(w.handle, x_ptr, x_type, x_stride, n_tok, ep, _elem(out.dtype, "out"), out_ptr, out_stride,
+                        _raw_stream(stream, device)))
     return out

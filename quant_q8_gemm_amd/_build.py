@@ -1,8 +1,10 @@
 """Build libqmm.so (the C-ABI library) for gfx950 with hipcc, in-tree."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -29,9 +31,15 @@ MAX_ILP = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
 LIB_FLAGS = DEVICE_FLAGS + MAX_ILP
 
 
-def _hipcc(sources, out: str, verbose: bool, flags=None) -> str:
-    cmd = [HIPCC, *(LIB_FLAGS if flags is None else flags), "-fPIC", "-shared", "-Wall", "-I",
-           os.path.join(ROOT, "include"), *sources, "-o", out + ".tmp"]
+def _flags(source: str):
+    """The few-token product keeps the default strategy: it needs its registers for
+    the loads in flight, and max-ILP spills them."""
+    return DEVICE_FLAGS if os.path.basename(source) == "qmm_mmv.hip" else LIB_FLAGS
+
+
+def _hipcc(sources, out: str, verbose: bool, flags, shared: bool = True) -> str:
+    cmd = [HIPCC, *flags, "-fPIC", "-shared" if shared else "-c", "-Wall", "-I", os.path.join(ROOT, "include"),
+           *sources, "-o", out + ".tmp"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     msgs = [ln for ln in (r.stdout + r.stderr).splitlines() if noise not in ln and ln.strip()]
@@ -44,9 +52,14 @@ def _hipcc(sources, out: str, verbose: bool, flags=None) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    _hipcc(SOURCES, LIB, verbose)
-    _hipcc([PEAK_SRC], PEAK_LIB, verbose, DEVICE_FLAGS)
-    _hipcc([PEAK_SRC], PEAK_LIB_ILP, verbose, DEVICE_FLAGS + MAX_ILP)
+    with tempfile.TemporaryDirectory() as tmp, concurrent.futures.ThreadPoolExecutor(8) as pool:
+        objects = [pool.submit(_hipcc, [src], os.path.join(tmp, os.path.basename(src) + ".o"), verbose, _flags(src), False)
+                   for src in SOURCES]
+        peaks = [pool.submit(_hipcc, [PEAK_SRC], PEAK_LIB, verbose, DEVICE_FLAGS),
+                 pool.submit(_hipcc, [PEAK_SRC], PEAK_LIB_ILP, verbose, LIB_FLAGS)]
+        _hipcc([o.result() for o in objects], LIB, verbose, ["--offload-arch=gfx950"])
+        for p in peaks:
+            p.result()
     return LIB
 
 
@@ -56,7 +69,7 @@ def device_asm(out_path: str) -> str:
     parts = []
     for k in KERNELS + ["qmm_peak.hip"]:
         tmp = out_path + "." + k + ".s"
-        cmd = [HIPCC, *(DEVICE_FLAGS if k == "qmm_peak.hip" else LIB_FLAGS), "--cuda-device-only", "-S", "-I",
+        cmd = [HIPCC, *(DEVICE_FLAGS if k == "qmm_peak.hip" else _flags(k)), "--cuda-device-only", "-S", "-I",
                os.path.join(ROOT, "include"), os.path.join(CSRC, k), "-o", tmp]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

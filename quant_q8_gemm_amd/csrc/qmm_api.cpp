@@ -159,7 +159,7 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
   const size_t off_sm = off_wd + round_up(qmm::wd_bytes(type, p.od_pad, id), 256);
   size_t plane_bytes = off_sm + round_up(qmm::wsm_bytes(type, p.od_pad, id), 256);
   if (rows) {
-    p.od_pad = od;
+    p.od_pad = qmm::row_pad(od);
     p.rows = qmm::row_planes(type, od, id, nullptr, &plane_bytes);
   }
   // reserve the bytes against the cap before allocating, atomically, so that

@@ -58,6 +58,8 @@ size_t wsm_bytes(int type, int64_t od_pad, int64_t id);
 hipError_t launch_repack(const uint8_t* raw, const Planes& p, hipStream_t s);
 hipError_t launch_quantize(const float* x, int64_t n_tok, int64_t t_pad, int64_t id,
                            uint8_t* qact, hipStream_t s);
+// Rows of a rows form, padded to its tile of 16.
+int64_t row_pad(int64_t od);
 // The rows form's planes at `base` and the bytes they need.
 RowPlanes row_planes(int type, int64_t od, int64_t id, void* base, size_t* bytes);
 hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t id, const RowPlanes& r, hipStream_t s);

@@ -9,16 +9,17 @@
 // With so few tokens the weights' bytes bound the product, so they are kept as
 // small as the k-quant blocks are (the rows form: 0.5625 bytes per q4_K weight,
 // 0.8203 per q6_K weight, where the MMQ's planes have 1.25 and 2.02) and every
-// byte is read once, in rows, 16 code bytes per lane: eight lanes hold a
-// super-block, a wave eight consecutive ones.  Dots are 4-element integer dot
-// products on the vector ALU: the matrix core's tiles of 16 or 32 tokens would
-// be mostly empty.
+// byte is read once, straight into registers, 16 code bytes per lane.
 //
-// A work-group first quantizes the tokens' activations into LDS (the whole inner
-// dimension, where it fits), then walks row groups: each of its waves takes kRows
-// rows, so that an activation read from LDS serves kRows rows, over its share of
-// the super-blocks; a row group's shares are added through LDS in a fixed order
-// and go through the epilogue.
+// The dots run on the matrix core although at most 8 of its 16 token rows could be
+// filled: on the vector ALU the 4-element dots of 8 tokens alone cost 64 cycles
+// per 16 rows and 32 weights, four times the memory's pace (32000 x 4096 q6_K, 8
+// tokens: 58 us, 57% of them issuing vector instructions).  The spare token rows
+// do a second job.  A scale applies to 16 (q6_K) or 32 (q4_K) weights, while one
+// MFMA sums 64; so the activations are laid out block-diagonally: token rows
+// 0.. see one scale group's activations and zeros elsewhere, the next token rows
+// the next group's.  One 16x16x64 MFMA of 16 weight rows then gives the separate
+// dots of four groups for up to four tokens, or of two for up to eight.
 #include "qmm_internal.h"
 #include "qmm_common.h"
 #include "qmm_epilogue.h"
@@ -29,22 +30,28 @@
 namespace qmm {
 
 // ---------------------------------------------------------------------------
-// The rows form of a weight matrix of od rows and nsb super-blocks per row,
-// planes in this order, each starting at a multiple of 256 bytes:
-//   q4_K  codes  [od][nsb][128]: the block's 128 code bytes
-//         heads  [od][nsb][16]: for each pair i of 32-blocks (2i, 2i + 1) three
-//                bytes, 24 bits from the lowest: scale and min of block 2i, scale
-//                and min of block 2i + 1, six bits each; then f16 d, f16 dmin
-//   q6_K  low    [od][nsb][128]: the block's 128 bytes of low code bits
-//         high   [od][nsb][8][8]: for byte group p (the 16 low bytes 16p ..) the
-//                high bits of its 32 codes: byte b of the first (second) four
-//                bytes holds in bits 2j, 2j + 1 those of the low (high) nibble's
-//                code 4j + b, the upper of the two inverted
-//         scales [od][nsb][8][2]: the int8 scales of byte group p's low nibbles
-//                and of its high nibbles
-//         d      [od][nsb] f16
+// The rows form of a weight matrix: tiles of kTile rows (padding rows all zero)
+// by nsb super-blocks, planes in this order, each starting at a multiple of 256
+// bytes.  Byte group g (0..3) of half h (0, 1) of a block is bytes 64h + 16g ..
+// + 15 of its 128 code bytes: 16 codes in the low nibbles and 16 in the high
+// ones.  n is the row in its tile.
+//   q4_K  codes  [tiles][nsb][h][g][n][16]
+//         heads  [tiles][nsb][n][4 words]: word i holds the six-bit scale and min
+//                of 32-block 2i and scale and min of 2i + 1 from its lowest bit,
+//                and in its top byte one byte of f16 d (i = 0, 1) or dmin (2, 3),
+//                the lower one first
+//   q6_K  low    [tiles][nsb][h][g][n][16]: the block's low code bits
+//         high   [tiles][nsb][g][n][h][8]: the high bits of the byte group's 32
+//                codes: byte b of the first (second) four bytes holds in bits 2j,
+//                2j + 1 those of the low (high) nibble's code 4j + b, the upper of
+//                the two inverted
+//         scales [tiles][nsb][n][16]: the int8 scales plus 128
+//         d      [tiles][nsb][n] f16
+// A wave's loads are whole contiguous runs: 1 KiB of codes, 1 KiB of high bits.
 // ---------------------------------------------------------------------------
 namespace {
+
+constexpr int kTile = 16;
 
 constexpr size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -57,48 +64,54 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p) {  // 16 bytes at an e
 }
 
 __device__ __forceinline__ uint4 q4k_head(const uint8_t* B) {
-  uint32_t pair[4];
+  const uint8_t* P = B + 4;
+  uint32_t word[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t six[4];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int c = 2 * i + k;
-      const uint8_t* P = B + 4;
       six[2 * k] = c < 4 ? P[c] & 63 : (P[c + 4] & 15) | ((P[c - 4] >> 6) << 4);
       six[2 * k + 1] = c < 4 ? P[c + 4] & 63 : (P[c + 4] >> 4) | ((P[c] >> 6) << 4);
     }
-    pair[i] = six[0] | (six[1] << 6) | (six[2] << 12) | (six[3] << 18);
+    word[i] = six[0] | (six[1] << 6) | (six[2] << 12) | (six[3] << 18) | ((uint32_t)B[i] << 24);
   }
-  return make_uint4(pair[0] | (pair[1] << 24), (pair[1] >> 8) | (pair[2] << 16), (pair[2] >> 16) | (pair[3] << 8),
-                    (uint32_t)B[0] | ((uint32_t)B[1] << 8) | ((uint32_t)B[2] << 16) | ((uint32_t)B[3] << 24));
+  return make_uint4(word[0], word[1], word[2], word[3]);
 }
 
-// One thread per (super-block, byte group p), striding over a capped grid.
+// One thread per (tile, super-block, half, byte group, row), striding over a
+// capped grid.
 __global__ void __launch_bounds__(256)
-repack_rows_kernel(const uint8_t* __restrict__ raw, int q6, int64_t total, RowPlanes r) {
+repack_rows_kernel(const uint8_t* __restrict__ raw, int q6, int od, int nsb, int64_t total, RowPlanes r) {
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t b = i >> 3;
-    const int p = (int)(i & 7);
+    const int n = (int)(i & 15), g = (int)(i >> 4) & 3, h = (int)(i >> 6) & 1;
+    const int64_t ts = i >> 7;  // tile * nsb + super-block
+    const int64_t row = ts / nsb * kTile + n;
+    const bool real = row < od;
+    const int64_t b = (real ? row : 0) * nsb + ts % nsb;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     if (q6) {
       const uint8_t* B = raw + b * 210;
-      *(uint4*)(r.codes + b * 128 + 16 * p) = load16(B + 16 * p);
-      const int shift = 2 * ((p >> 1) & 1);
-      const uint8_t* qh = B + 128 + 32 * (p >> 2) + 16 * (p & 1);
+      *(uint4*)(r.codes + i * 16) = real ? load16(B + 64 * h + 16 * g) : zero;
+      const uint8_t* qh = B + 128 + 32 * h + 16 * (g & 1);
       uint32_t high[2] = {0, 0};
+#pragma unroll
       for (int k = 0; k < 16; ++k)
-        for (int n = 0; n < 2; ++n)
-          high[n] |= (uint32_t)(((qh[k] >> (shift + 4 * n)) & 3) ^ 2) << (8 * (k & 3) + 2 * (k >> 2));
-      *(uint2*)(r.heads + b * 64 + 8 * p) = make_uint2(high[0], high[1]);
-      const int g = p + 4 * (p >> 2);  // the 16-weight group of the low nibbles; the high ones' is 4 further
-      r.scales[b * 16 + 2 * p] = B[192 + g];
-      r.scales[b * 16 + 2 * p + 1] = B[192 + g + 4];
-      if (p == 0) r.d[b] = (uint16_t)(B[208] | (B[209] << 8));
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          high[m] |= (uint32_t)(((qh[k] >> (2 * (g >> 1) + 4 * m)) & 3) ^ 2) << (8 * (k & 3) + 2 * (k >> 2));
+      *(uint2*)(r.heads + ((ts * 4 + g) * kTile + n) * 16 + 8 * h) = real ? make_uint2(high[0], high[1]) : make_uint2(0, 0);
+      if (h == 0 && g == 0) {
+        uint8_t* const s = r.scales + (ts * kTile + n) * 16;
+        for (int k = 0; k < 16; ++k) s[k] = real ? (uint8_t)(B[192 + k] + 128) : 0;
+        r.d[ts * kTile + n] = real ? (uint16_t)(B[208] | (B[209] << 8)) : 0;
+      }
     } else {
       const uint8_t* B = raw + b * 144;
-      *(uint4*)(r.codes + b * 128 + 16 * p) = *(const uint4*)(B + 16 + 16 * p);
-      if (p == 0) *(uint4*)(r.heads + b * 16) = q4k_head(B);
+      *(uint4*)(r.codes + i * 16) = real ? *(const uint4*)(B + 16 + 64 * h + 16 * g) : zero;
+      if (h == 0 && g == 0) *(uint4*)(r.heads + (ts * kTile + n) * 16) = real ? q4k_head(B) : zero;
     }
   }
 }
@@ -106,7 +119,7 @@ repack_rows_kernel(const uint8_t* __restrict__ raw, int q6, int64_t total, RowPl
 }  // namespace
 
 RowPlanes row_planes(int type, int64_t od, int64_t id, void* base, size_t* bytes) {
-  const size_t nb = (size_t)od * (size_t)(id / 256);
+  const size_t nb = (size_t)((od + kTile - 1) / kTile * kTile) * (size_t)(id / 256);
   const bool q6 = type == QMM_Q6_K_ROWS;
   RowPlanes r{};
   r.heads_offset = round256(nb * 128);
@@ -120,30 +133,41 @@ RowPlanes row_planes(int type, int64_t od, int64_t id, void* base, size_t* bytes
   return r;
 }
 
+int64_t row_pad(int64_t od) { return (od + kTile - 1) / kTile * kTile; }
+
 hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t id, const RowPlanes& r, hipStream_t s) {
-  const int64_t total = od * (id / 256) * 8;
+  const int64_t total = row_pad(od) * (id / 256) * 8;
   const int64_t blocks = std::min<int64_t>((total + 255) / 256, 1 << 14);
-  repack_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(raw, type == QMM_Q6_K_ROWS, total, r);
+  repack_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(raw, type == QMM_Q6_K_ROWS, (int)od, (int)(id / 256),
+                                                                 total, r);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
-// The product.
+// The product.  A work-group of kWaves waves first quantizes the activations into
+// LDS, the whole inner dimension where it fits; then it walks row tiles: kg of its
+// waves share a tile, each over its share of the super-blocks, and the tile's
+// partial sums meet in LDS, are added in wave order and go through the epilogue.
+//
+// The MFMA's A operand are the activations (row m: lane & 15, k group: lane >> 4,
+// 16 bytes), B the weights (row n of the tile: lane & 15, the same k groups: the
+// four byte groups of a half block).  Lane (n, G) of the result holds token rows
+// m = 4G .. 4G + 3 of weight row n:
+//   up to 4 tokens (WIDE false): m = 4*group + token: lane group G has tokens 0..3
+//     of byte group G;
+//   up to 8 (WIDE): m = 8*half + token.  q4_K: the halves are the two 32-blocks of
+//     the half block (byte groups 0, 1 and 2, 3); q6_K: two byte groups, and a
+//     second MFMA with the other two.
+// A lane's scales are those of its own row n, and of its own byte group or pair.
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kRows = 4;  // rows a wave takes at once
-constexpr int kItem = 8;  // super-blocks a wave reads at once
+constexpr int kWaves = 16;
 
-// Activations in LDS, per token and super-block: 256 code bytes as [low, high][8
-// byte groups][16], the codes that meet the low and the high nibbles of weight
-// byte group p; and per pair of 32-blocks the f32 scales: q4_K (dh, s) of the
-// low nibbles' block and of the high ones', q6_K both dh.
+// LDS per super-block: codes [h][nibble][g][token][16], n_tok tokens; then f32 dh
+// [32-block][8 tokens] and for q4_K s [32-block][8 tokens].
 template <bool Q6>
-constexpr int kScaleBytes = Q6 ? 32 : 64;
-template <bool Q6>
-constexpr int kSbBytes = 256 + kScaleBytes<Q6>;
+constexpr int kScaleBytes = Q6 ? 256 : 512;
 
 struct MvArgs {
   RowPlanes w;
@@ -151,262 +175,285 @@ struct MvArgs {
   int64_t x_stride;
   int x_type, n_tok, od, nsb;
   int tile_sb;  // super-blocks quantized at a time
-  int kg;       // waves that share a row group, each over its share of the super-blocks
-  int steps;    // row-group sets: ceil(od / (kWaves / kg * kRows))
+  int kg;       // waves that share a row tile
+  int steps;    // sets of kWaves/kg row tiles
 };
 
-// A lane's weights of one row: 32 codes and what scales them.
-struct Q4Lane {
-  uint4 code, head;
+// A lane's weights of one super-block as loaded, and the f32 factors of its dots.
+template <bool Q6>
+struct Raw;
+template <>
+struct Raw<false> {
+  uint4 code[2], head;
+  // ts: tile*nsb + super-block (uniform)
+  __device__ __forceinline__ void load(const RowPlanes& w, int64_t ts, uint32_t lane) {
+    code[0] = *(const uint4*)(w.codes + ts * 2048 + lane * 16);
+    code[1] = *(const uint4*)(w.codes + ts * 2048 + 1024 + lane * 16);
+    head = *(const uint4*)(w.heads + ts * 256 + (lane & 15) * 16);
+  }
 };
-struct Q6Lane {
-  uint4 low;
-  uint2 high;
-  uint32_t scales, d;  // two int8; f16
+template <>
+struct Raw<true> {
+  uint4 code[2], high, scales;
+  uint32_t d;
+  __device__ __forceinline__ void load(const RowPlanes& w, int64_t ts, uint32_t lane) {
+    code[0] = *(const uint4*)(w.codes + ts * 2048 + lane * 16);
+    code[1] = *(const uint4*)(w.codes + ts * 2048 + 1024 + lane * 16);
+    high = *(const uint4*)(w.heads + ts * 1024 + lane * 16);
+    scales = *(const uint4*)(w.scales + ts * 256 + (lane & 15) * 16);
+    d = *(w.d + ts * 16 + (lane & 15));
+  }
 };
 
-__device__ __forceinline__ int dot16(const uint32_t (&a)[4], const v4i& b) {
-  int s = __builtin_amdgcn_sdot4((int)a[0], b[0], 0, false);
-  s = __builtin_amdgcn_sdot4((int)a[1], b[1], s, false);
-  s = __builtin_amdgcn_sdot4((int)a[2], b[2], s, false);
-  return __builtin_amdgcn_sdot4((int)a[3], b[3], s, false);
+__device__ __forceinline__ v4i mfma(v4i a, v4i b) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, v4i{0, 0, 0, 0}, 0, 0, 0);
 }
 
-template <int NT>
-__device__ __forceinline__ void add_row(const Q4Lane& w, const v4i (&qa)[NT], const v4i (&qb)[NT],
-                                        const float4 (&sc)[NT], int pair, float (&acc)[NT]) {
-  uint32_t lo[4], hi[4];
-  const uint32_t c[4] = {w.code.x, w.code.y, w.code.z, w.code.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[i] = c[i] & 0x0F0F0F0Fu;
-    hi[i] = (c[i] >> 4) & 0x0F0F0F0Fu;
-  }
-  // the pair's 24 bits: bytes 3*pair .. of the head's first twelve
-  const uint32_t h0 = w.head.x, h1 = w.head.y, h2 = w.head.z;
-  const uint32_t low = pair < 2 ? h0 : pair == 2 ? h1 : h2, up = pair < 2 ? h1 : h2;
-  const uint32_t f = __builtin_amdgcn_alignbit(up, low, (24u * (uint32_t)pair) & 31u);
-  const int sa = (int)(f & 63), sb = (int)((f >> 12) & 63);
-  const float ma = (float)((f >> 6) & 63), mb = (float)((f >> 18) & 63);
-  const float d = f16_bits_to_float(w.head.w & 0xFFFF);
-  const float m = -0.5f * f16_bits_to_float(w.head.w >> 16);  // both lanes of a pair add the min term
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const float da = (float)__mul24(sa, dot16(lo, qa[t])), db = (float)__mul24(sb, dot16(hi, qb[t]));
-    acc[t] = fmaf(d, fmaf(da, sc[t].x, db * sc[t].z), acc[t]);
-    acc[t] = fmaf(m, fmaf(ma, sc[t].y, mb * sc[t].w), acc[t]);
-  }
+// acc[i] += f * (dh[i] * dot[i]): one scale group's dots of four tokens
+__device__ __forceinline__ void add_dots(float (&acc)[4], const v4i& dot, float f, const float4& dh) {
+  acc[0] = fmaf((float)dot[0] * dh.x, f, acc[0]);
+  acc[1] = fmaf((float)dot[1] * dh.y, f, acc[1]);
+  acc[2] = fmaf((float)dot[2] * dh.z, f, acc[2]);
+  acc[3] = fmaf((float)dot[3] * dh.w, f, acc[3]);
+}
+__device__ __forceinline__ void add_min(float (&acc)[4], float f, const float4& s) {
+  acc[0] = fmaf(s.x, f, acc[0]);
+  acc[1] = fmaf(s.y, f, acc[1]);
+  acc[2] = fmaf(s.z, f, acc[2]);
+  acc[3] = fmaf(s.w, f, acc[3]);
 }
 
-// q6_K codes as four times (code - 32): the six bits, the top one inverted, in a
-// byte's upper bits are that as an int8; the 4 is taken off d.
-template <int NT>
-__device__ __forceinline__ void add_row(const Q6Lane& w, const v4i (&qa)[NT], const v4i (&qb)[NT],
-                                        const float2 (&sc)[NT], int, float (&acc)[NT]) {
-  uint32_t lo[4], hi[4];
-  const uint32_t c[4] = {w.low.x, w.low.y, w.low.z, w.low.w};
+// One super-block of q4_K.  codes(h, nibble): the A operand; dh, s: the f32 scales
+// of four of the lane's tokens, of 32-block c at [8c].
+template <bool WIDE, class Codes>
+__device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[4], int G, Codes&& codes,
+                                          const float* dh, const float* s) {
+  const bool second = G >= 2;  // the lane's pair of 32-blocks in a half block
+  const float d = f16_bits_to_float(__builtin_amdgcn_perm(w.head.y, w.head.x, 0x0C0C0703u));
+  const float m = -f16_bits_to_float(__builtin_amdgcn_perm(w.head.w, w.head.z, 0x0C0C0703u));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[i] = ((c[i] << 2) & 0x3C3C3C3Cu) | ((w.high.x << (6 - 2 * i)) & 0xC0C0C0C0u);
-    hi[i] = ((c[i] >> 2) & 0x3C3C3C3Cu) | ((w.high.y << (6 - 2 * i)) & 0xC0C0C0C0u);
-  }
-  const int sa = (int)(int8_t)w.scales, sb = (int)(int8_t)(w.scales >> 8);
-  const float d = 0.25f * f16_bits_to_float(w.d);
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c[4] = {w.code[h].x, w.code[h].y, w.code[h].z, w.code[h].w};
+    v4i lo, hi;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const float da = (float)__mul24(sa, dot16(lo, qa[t])), db = (float)__mul24(sb, dot16(hi, qb[t]));
-    acc[t] = fmaf(d, fmaf(da, sc[t].x, db * sc[t].y), acc[t]);
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = (int)(c[i] & 0x0F0F0F0Fu);
+      hi[i] = (int)((c[i] >> 4) & 0x0F0F0F0Fu);
+    }
+    const uint32_t f = h == 0 ? (second ? w.head.y : w.head.x) : (second ? w.head.w : w.head.z);
+    const float* const dhp = dh + 32 * h + (second ? 16 : 0);
+    const float* const sp = s + 32 * h + (second ? 16 : 0);
+    add_dots(acc, mfma(codes(h, 0), lo), d * (float)(f & 63), *(const float4*)dhp);
+    add_dots(acc, mfma(codes(h, 1), hi), d * (float)((f >> 12) & 63), *(const float4*)(dhp + 8));
+    if (WIDE) {
+      add_min(acc, m * (float)((f >> 6) & 63), *(const float4*)sp);
+      add_min(acc, m * (float)((f >> 18) & 63), *(const float4*)(sp + 8));
+    } else {  // two lane groups share the pair: each adds one block's min term
+      add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), *(const float4*)(sp + (G & 1 ? 8 : 0)));
+    }
   }
 }
 
-// Sums over the wave of N values per lane.  Two values share a register after
-// the halves are swapped and added, four after the rows of 16 are, so the last
-// four steps run on N/4 registers.  Row r of register k ends with the sum of value
-// 4k + {0, 2, 1, 3}[r], in all of its lanes.
-template <int N>
-__device__ __forceinline__ void wave_sums(float (&v)[N], float (&w)[(N + 3) / 4]) {
-  float h[(N + 3) / 4 * 2];
+// One super-block of q6_K.  A code as four times (code - 32): its six bits, the top
+// one inverted, in a byte's upper bits are that as an int8; the 4 is taken off d.
+template <bool WIDE, class Codes>
+__device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[4], int G, Codes&& codes,
+                                          const float* dh, const float*) {
+  const float d = 0.25f * f16_bits_to_float(w.d), d128 = -128.0f * d;
 #pragma unroll
-  for (int i = 0; i < (N + 3) / 4 * 2; ++i) {
-    const uint32_t a = 2 * i < N ? __builtin_bit_cast(uint32_t, v[2 * i < N ? 2 * i : 0]) : 0;
-    const uint32_t b = 2 * i + 1 < N ? __builtin_bit_cast(uint32_t, v[2 * i + 1 < N ? 2 * i + 1 : 0]) : 0;
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    h[i] = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
-  }
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c[4] = {w.code[h].x, w.code[h].y, w.code[h].z, w.code[h].w};
+    const uint32_t top[2] = {h ? w.high.z : w.high.x, h ? w.high.w : w.high.y};
+    v4i b[2];
 #pragma unroll
-  for (int k = 0; k < (N + 3) / 4; ++k) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, h[2 * k]),
-                                                    __builtin_bit_cast(uint32_t, h[2 * k + 1]), false, false);
-    float s = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
-    s += __builtin_bit_cast(float, dpp<kDppQuadXor1>(__builtin_bit_cast(int, s)));
-    s += __builtin_bit_cast(float, dpp<kDppQuadXor2>(__builtin_bit_cast(int, s)));
-    s += __builtin_bit_cast(float, dpp<kDppHalfMirror>(__builtin_bit_cast(int, s)));
-    w[k] = s + __builtin_bit_cast(float, dpp<kDppMirror>(__builtin_bit_cast(int, s)));
-  }
-}
-
-// Quantizes super-blocks [sb0, sb0 + n) of every token into LDS: a thread per
-// four activations, eight lanes per 32-block, as the prepass.
-template <bool Q6, int NT>
-__device__ __forceinline__ void quantize_tile(const MvArgs& a, uint8_t* lds, int sb0, int n) {
-  const int per_tok = n * 64;  // quads of a token: whole waves
-  for (int i = threadIdx.x; i < NT * per_tok; i += 64 * kWaves) {
-    const int t = i / per_tok, k = i % per_tok;  // t is uniform over the wave
-    const int64_t at = t * a.x_stride + (int64_t)sb0 * 256 + 4 * k;
-    const float4 v = a.x_type == QMM_F32   ? load4<QMM_F32>(a.x, at)
-                     : a.x_type == QMM_F16 ? load4<QMM_F16>(a.x, at)
-                                           : load4<QMM_BF16>(a.x, at);
-    const Q8Quad r = quant_quad(v);
-    const int sb = k >> 6, g = (k >> 2) & 15;  // 16-code group of the super-block
-    // its place: which nibbles it meets, and of which byte group
-    const int hi = Q6 ? (g >> 2) & 1 : (g >> 1) & 1;
-    const int p = Q6 ? 4 * (g >> 3) + (g & 3) : 2 * (g >> 2) + (g & 1);
-    uint8_t* const q = lds + (t * a.tile_sb + sb) * kSbBytes<Q6>;
-    *(uint32_t*)(q + hi * 128 + p * 16 + (k & 3) * 4) = r.codes;
-    if ((k & 7) == 0) {
-      const int c = (k >> 3) & 7;  // 32-block of the super-block
-      float* const s = (float*)(q + 256);
-      if (Q6) {  // pair 2*(c/4) + c%2, nibble (c/2)%2
-        s[2 * (2 * (c >> 2) + (c & 1)) + ((c >> 1) & 1)] = f16_bits_to_float(r.pair & 0xFFFF);
+    for (int i = 0; i < 4; ++i) {
+      b[0][i] = (int)(((c[i] << 2) & 0x3C3C3C3Cu) | ((top[0] << (6 - 2 * i)) & 0xC0C0C0C0u));
+      b[1][i] = (int)(((c[i] >> 2) & 0x3C3C3C3Cu) | ((top[1] << (6 - 2 * i)) & 0xC0C0C0C0u));
+    }
+    const uint32_t sc[2] = {h ? w.scales.z : w.scales.x, h ? w.scales.w : w.scales.y};
+#pragma unroll
+    for (int nib = 0; nib < 2; ++nib) {
+      // byte group g is 16-group 2*(32-block) + g%2, of 32-block 4h + 2*nib + g/2
+      if (WIDE) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t u = (sc[nib] >> (8 * (G >> 1) + 16 * k)) & 255;
+          add_dots(acc, mfma(codes(h, nib, k), b[nib]), fmaf(d, (float)u, d128),
+                   *(const float4*)(dh + 8 * (4 * h + 2 * nib + k)));
+        }
       } else {
-        *(float2*)(s + 2 * c) = make_float2(f16_bits_to_float(r.pair & 0xFFFF), f16_bits_to_float(r.pair >> 16));
+        const uint32_t u = (sc[nib] >> (8 * G)) & 255;
+        add_dots(acc, mfma(codes(h, nib), b[nib]), fmaf(d, (float)u, d128),
+                 *(const float4*)(dh + 8 * (4 * h + 2 * nib) + 8 * (G >> 1)));
       }
     }
   }
 }
 
-template <bool Q6, int NT>
+// Quantizes super-blocks [sb0, sb0 + n) of every token into LDS: eight activations
+// per lane, four lanes per 32-block.
+template <bool Q6>
+__device__ __forceinline__ void quantize_tile(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0, int n) {
+  const int per_tok = n * 32;
+  for (int i = threadIdx.x; i < a.n_tok * per_tok; i += 64 * kWaves) {
+    const int t = i / per_tok, k = i - t * per_tok;
+    const int64_t at = t * a.x_stride + (int64_t)sb0 * 256 + 8 * k;
+    float4 v[2];
+    if (a.x_type == QMM_F32) {
+      v[0] = load4<QMM_F32>(a.x, at);
+      v[1] = load4<QMM_F32>(a.x, at + 4);
+    } else if (a.x_type == QMM_F16) {
+      v[0] = load4<QMM_F16>(a.x, at);
+      v[1] = load4<QMM_F16>(a.x, at + 4);
+    } else {
+      v[0] = load4<QMM_BF16>(a.x, at);
+      v[1] = load4<QMM_BF16>(a.x, at + 4);
+    }
+    const Q8Oct r = quant_oct(v[0], v[1]);
+    const int sb = k >> 5, c = (k >> 2) & 7, half16 = (k >> 1) & 1;
+    // 32-block c -> (half, nibble, byte group)
+    const int h = c >> 2, nib = Q6 ? (c >> 1) & 1 : c & 1, g = 2 * (Q6 ? c & 1 : (c >> 1) & 1) + half16;
+    uint8_t* const q = lds + sb * sb_bytes;
+    *(uint2*)(q + (((2 * h + nib) * 4 + g) * a.n_tok + t) * 16 + (k & 1) * 8) = make_uint2(r.codes[0], r.codes[1]);
+    if ((k & 3) == 0) {
+      float* const s = (float*)(q + 256 * a.n_tok) + 8 * c + t;
+      s[0] = f16_bits_to_float(r.pair & 0xFFFF);
+      if (!Q6) s[64] = f16_bits_to_float(r.pair >> 16);
+    }
+  }
+}
+
+template <bool Q6, bool WIDE>
 __global__ void __launch_bounds__(64 * kWaves)
 mmv_kernel(MvArgs a, Epilogue ep) {
+  constexpr int kTok = WIDE ? 8 : 4;
   extern __shared__ uint4 lds_raw[];
   uint8_t* const lds = (uint8_t*)lds_raw;
-  float* const red = (float*)(lds + (size_t)NT * a.tile_sb * kSbBytes<Q6>);  // [2][wave][NT][kRows]
-  constexpr int kVals = NT * kRows;
+  const int sb_bytes = 256 * a.n_tok + kScaleBytes<Q6>;
+  // the partial sums [2][wave][token][kTile], and 16 bytes of zeros
+  float* const red = (float*)(lds + (size_t)a.tile_sb * sb_bytes);
+  uint4* const zeros = (uint4*)(red + 2 * kWaves * kTok * kTile);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rg = wave / a.kg, kg = wave % a.kg, groups = kWaves / a.kg;
-  const int p = lane & 7, sbl = lane >> 3;
+  const int tiles = (a.od + kTile - 1) / kTile;
   const bool one_tile = a.tile_sb == a.nsb;
-  if (one_tile) quantize_tile<Q6, NT>(a, lds, 0, a.nsb);
-  if (one_tile) __syncthreads();
+  const int m = lane & 15, G = lane >> 4;
+
+  Raw<Q6> next;
+  auto fetch = [&](int step, int sb) __attribute__((always_inline)) {
+    next.load(a.w, (int64_t)min(step * groups + rg, tiles - 1) * a.nsb + sb, (uint32_t)lane);
+  };
+  fetch(blockIdx.x, min(kg, a.nsb - 1));
+  if (threadIdx.x == 0) *zeros = make_uint4(0, 0, 0, 0);
+  if (one_tile) quantize_tile<Q6>(a, lds, sb_bytes, 0, a.nsb);
+  __syncthreads();
+
+  // The lane's A operand: its token's codes of its byte group, or zeros (always
+  // the same ones) where the group is not its row's.  q6_K with eight tokens: for
+  // the MFMA of byte groups 0, 1 and for that of 2, 3.
+  const int tok = WIDE ? m & 7 : m & 3;
+  const bool own = tok < a.n_tok && (WIDE ? (m >> 3) == (Q6 ? G & 1 : G >> 1) : (m >> 2) == G);
+  const uint32_t at = (uint32_t)(G * a.n_tok + tok) * 16, step_nib = (uint32_t)a.n_tok * 64;
+  const uint32_t zero_at = (uint32_t)((uint8_t*)zeros - lds);
+  const float* const scales = (const float*)(lds + 256 * a.n_tok) + (WIDE ? 4 * (G & 1) : 0);
+
   int buf = 0;
   for (int step = blockIdx.x; step < a.steps; step += gridDim.x, buf ^= 1) {
-    const int r0 = (step * groups + rg) * kRows;
-    float acc[kRows][NT];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[r][t] = 0.0f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int sb0 = 0; sb0 < a.nsb; sb0 += a.tile_sb) {
       const int n = min(a.tile_sb, a.nsb - sb0);
       if (!one_tile) {
         __syncthreads();  // the last tile's readers are done
-        quantize_tile<Q6, NT>(a, lds, sb0, n);
+        quantize_tile<Q6>(a, lds, sb_bytes, sb0, n);
         __syncthreads();
       }
-      if (r0 < a.od)
-        for (int it = kg * kItem; it < n; it += a.kg * kItem) {
-          const int sb = it + sbl;
-          if (sb < n) {
-            typedef typename std::conditional<Q6, Q6Lane, Q4Lane>::type Lane;
-            typedef typename std::conditional<Q6, float2, float4>::type Scale;
-            Lane w[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {  // rows past the end read the last one
-              const int64_t b = (int64_t)min(r0 + r, a.od - 1) * a.nsb + sb0 + sb;
-              if constexpr (Q6) {
-                w[r].low = *(const uint4*)(a.w.codes + b * 128 + 16 * p);
-                w[r].high = *(const uint2*)(a.w.heads + b * 64 + 8 * p);
-                w[r].scales = *(const uint16_t*)(a.w.scales + b * 16 + 2 * p);
-                w[r].d = a.w.d[b];
-              } else {
-                w[r].code = *(const uint4*)(a.w.codes + b * 128 + 16 * p);
-                w[r].head = *(const uint4*)(a.w.heads + b * 16);
-              }
-            }
-            v4i qa[NT], qb[NT];
-            Scale sc[NT];
-            const int pair = Q6 ? 2 * (p >> 2) + ((p >> 1) & 1) : p >> 1;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint8_t* const q = lds + (t * a.tile_sb + sb) * kSbBytes<Q6>;
-              qa[t] = *(const v4i*)(q + 16 * p);
-              qb[t] = *(const v4i*)(q + 128 + 16 * p);
-              sc[t] = *(const Scale*)(q + 256 + sizeof(Scale) * pair);
-            }
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) add_row<NT>(w[r], qa, qb, sc, pair, acc[r]);
-          }
-        }
+      for (int sb = kg; sb < n; sb += a.kg) {
+        const Raw<Q6> w = next;
+        // the next super-block: of this part, of the next one, of the next row tile
+        const bool same = sb + a.kg < n;
+        const int left = a.nsb - sb0 - n;  // super-blocks after this part
+        const bool same_row = same || kg < left;
+        fetch(same_row ? step : min(step + (int)gridDim.x, a.steps - 1),
+              same ? sb0 + sb + a.kg : same_row ? sb0 + n + kg : min(kg, a.nsb - 1));
+        const uint32_t base = (uint32_t)(sb * sb_bytes);
+        const float* const dh = (const float*)((const uint8_t*)scales + base);
+        auto codes = [&](int h, int nib, int k = 0) __attribute__((always_inline)) {
+          const bool live = Q6 && WIDE ? own && (G >> 1) == k : own;
+          return *(const v4i*)(lds + (live ? base + at + (uint32_t)(2 * h + nib) * step_nib : zero_at));
+        };
+        add_block<WIDE>(w, acc, G, codes, dh, dh + 64);
+      }
     }
-    // the wave's sums, then the row group's over its waves in order
-    float v[kVals], s[(kVals + 3) / 4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) v[t * kRows + r] = acc[r][t];
-    wave_sums<kVals>(v, s);
-    float* const out = red + ((size_t)buf * kWaves + wave) * kVals;
-    if ((lane & 15) == 0) {
-      const int row = lane >> 4, order = row == 1 ? 2 : row == 2 ? 1 : row;
-#pragma unroll
-      for (int k = 0; k < kVals / 4; ++k) out[4 * k + order] = s[k];
+    // the lane groups' sums; then lane (n, G) holds one token's (two if WIDE)
+    const auto s01 = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, acc[0]),
+                                                      __builtin_bit_cast(uint32_t, acc[1]), false, false);
+    const auto s23 = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, acc[2]),
+                                                      __builtin_bit_cast(uint32_t, acc[3]), false, false);
+    const float x = __builtin_bit_cast(float, (uint32_t)s01[0]) + __builtin_bit_cast(float, (uint32_t)s01[1]);
+    const float y = __builtin_bit_cast(float, (uint32_t)s23[0]) + __builtin_bit_cast(float, (uint32_t)s23[1]);
+    float* const out = red + ((size_t)buf * kWaves + wave) * (kTok * kTile);
+    if (WIDE) {  // lower half of the wave: tokens 4*(G&1) and + 2, upper: + 1 and + 3
+      const int t0 = 4 * (G & 1) + (G >> 1);
+      out[t0 * kTile + m] = x;
+      out[(t0 + 2) * kTile + m] = y;
+    } else {  // the odd rows of 16 of x and the even ones of y change places
+      const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                      __builtin_bit_cast(uint32_t, y), false, false);
+      out[((G >> 1) + 2 * (G & 1)) * kTile + m] =
+          __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
     }
     __syncthreads();
     // two buffers: the next step's sums do not overwrite these, the one after has
-    // passed the next barrier
-    if (kg == 0 && lane < a.n_tok && r0 < a.od) {
-      float4 f = *(const float4*)(out + lane * kRows);
+    // passed the next barrier.  A thread per four rows of a token.
+    const int per_group = 4 * a.n_tok;
+    if ((int)threadIdx.x < groups * per_group) {
+      const int gr = threadIdx.x / per_group, at4 = threadIdx.x - gr * per_group;
+      const int t = at4 >> 2, row = (step * groups + gr) * kTile + 4 * (at4 & 3);
+      const float* p = red + ((size_t)buf * kWaves + gr * a.kg) * (kTok * kTile) + t * kTile + 4 * (at4 & 3);
+      float4 f = *(const float4*)p;
       for (int k = 1; k < a.kg; ++k) {
-        const float4 g = *(const float4*)(out + k * kVals + lane * kRows);
-        f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
+        const float4 e = *(const float4*)(p + (size_t)k * (kTok * kTile));
+        f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
       }
-      const int n = min(a.od - r0, kRows);
-      put(ep, finish(ep, f, lane, r0, n), lane, r0, n);
+      const int left = min(a.od - row, 4);
+      if (left > 0) put(ep, finish(ep, f, t, row, left), t, row, left);
     }
   }
 }
 
-template <bool Q6, int NT>
-hipError_t launch_mmv_tokens(const MvArgs& in, const Epilogue& ep, int num_cus, hipStream_t s) {
+template <bool Q6, bool WIDE>
+hipError_t launch_typed(const MvArgs& in, const Epilogue& ep, int num_cus, hipStream_t s) {
   MvArgs a = in;
-  // LDS: the whole inner dimension where it fits 150 of the CU's 160 KB, else
-  // tiles of it, quantized again for every row-group set
-  constexpr size_t kRed = 2 * kWaves * NT * kRows * sizeof(float);
-  constexpr size_t kMost = 150 * 1024;
-  const size_t per_sb = (size_t)NT * kSbBytes<Q6>;
+  // LDS: the whole inner dimension where it fits the CU's 160 KB, else parts of it,
+  // quantized again for every set of row tiles
+  constexpr size_t kMost = 160 * 1024;
+  constexpr size_t kRed = (size_t)2 * kWaves * (WIDE ? 8 : 4) * kTile * sizeof(float) + 16;
+  const size_t per_sb = (size_t)256 * a.n_tok + kScaleBytes<Q6>;
   a.tile_sb = (int)std::min<size_t>(a.nsb, (kMost - kRed) / per_sb);
   const size_t lds = a.tile_sb * per_sb + kRed;
-  // Waves per row group: enough to fill the GPU with 16 waves per CU, each with a
-  // whole item of its own.
-  const int64_t row_groups = (a.od + kRows - 1) / kRows;
-  a.kg = 1;
-  while (a.kg < kWaves && row_groups * a.kg < 16 * (int64_t)num_cus && a.nsb >= 2 * a.kg * kItem) a.kg *= 2;
-  const int groups = kWaves / a.kg;
-  a.steps = (int)((row_groups + groups - 1) / groups);
-  const int per_cu = (int)std::max<size_t>(1, std::min<size_t>(2, (160 * 1024) / lds));
-  const int grid = std::min(a.steps, num_cus * per_cu);
+  // One work-group per CU.  Waves per row tile: as few as fill the GPU's CUs with
+  // row tiles of their own, and the fewest rounds of them, counted in the
+  // super-blocks that each wave walks (and half of one for the sums).
+  const int64_t tiles = (a.od + kTile - 1) / kTile;
+  double best = 0;
+  for (int kg = 1; kg <= kWaves && (kg == 1 || kg <= a.nsb); kg *= 2) {
+    const int64_t steps = (tiles + kWaves / kg - 1) / (kWaves / kg);
+    const double cost = (double)((steps + num_cus - 1) / num_cus) * ((a.nsb + kg - 1) / kg + 0.5);
+    if (kg == 1 || cost < best) {
+      best = cost;
+      a.kg = kg;
+      a.steps = (int)steps;
+    }
+  }
+  const int grid = (int)std::min<int64_t>(a.steps, num_cus);
   if (lds > 64 * 1024) {
-    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, NT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, WIDE>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)lds);
     if (e != hipSuccess) return e;
   }
-  mmv_kernel<Q6, NT><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
+  mmv_kernel<Q6, WIDE><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
   return hipGetLastError();
-}
-
-template <bool Q6>
-hipError_t launch_mmv_type(const MvArgs& a, const Epilogue& ep, int num_cus, hipStream_t s) {
-  switch (a.n_tok) {
-    case 1: return launch_mmv_tokens<Q6, 1>(a, ep, num_cus, s);
-    case 2: return launch_mmv_tokens<Q6, 2>(a, ep, num_cus, s);
-    case 3: return launch_mmv_tokens<Q6, 3>(a, ep, num_cus, s);
-    case 4: return launch_mmv_tokens<Q6, 4>(a, ep, num_cus, s);
-    case 5: return launch_mmv_tokens<Q6, 5>(a, ep, num_cus, s);
-    case 6: return launch_mmv_tokens<Q6, 6>(a, ep, num_cus, s);
-    case 7: return launch_mmv_tokens<Q6, 7>(a, ep, num_cus, s);
-    default: return launch_mmv_tokens<Q6, 8>(a, ep, num_cus, s);
-  }
 }
 
 }  // namespace
@@ -421,7 +468,9 @@ hipError_t launch_mmv(const Planes& p, const void* x, int x_type, int64_t x_stri
   a.n_tok = n_tok;
   a.od = (int)p.od;
   a.nsb = (int)p.nsb;
-  return p.type == QMM_Q6_K_ROWS ? launch_mmv_type<true>(a, ep, num_cus, s) : launch_mmv_type<false>(a, ep, num_cus, s);
+  if (p.type == QMM_Q6_K_ROWS)
+    return n_tok > 4 ? launch_typed<true, true>(a, ep, num_cus, s) : launch_typed<true, false>(a, ep, num_cus, s);
+  return n_tok > 4 ? launch_typed<false, true>(a, ep, num_cus, s) : launch_typed<false, false>(a, ep, num_cus, s);
 }
 
 }  // namespace qmm

@@ -102,4 +102,53 @@ __device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
   return {pack4(q), sc.pair(sum8(q[0] + q[1] + q[2] + q[3]))};
 }
 
+// The same block with eight consecutive values per lane, four lanes (4i .. 4i + 3):
+// half the shared work per value.  Codes are rounded by adding 1.5 * 2^23, whose
+// sum holds the integer (half to even) in its low bits.
+struct Q8Oct {
+  uint32_t codes[2], pair;
+};
+
+__device__ __forceinline__ float max4lanes(float v) {
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  u = max(u, (uint32_t)dpp<kDppQuadXor1>((int)u));
+  u = max(u, (uint32_t)dpp<kDppQuadXor2>((int)u));
+  return __builtin_bit_cast(float, u);
+}
+
+__device__ __forceinline__ Q8Oct quant_oct(const float4& v0, const float4& v1) {
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+  const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+  const Q8Scale sc(max4lanes(top));
+  float n[8], far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = __builtin_amdgcn_fmed3f(v[i] * sc.inv, -127.0f, 127.0f);
+    n[i] = r + kRound;
+    far = fmaxf(far, fabsf(r - (n[i] - kRound)));
+  }
+  if (far > 0.5f - 1e-4f) {  // as in quant4: next to a tie the quotients are formed exactly
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = __builtin_amdgcn_fmed3f(v[i] / sc.dhf, -127.0f, 127.0f) + kRound;
+  }
+  Q8Oct r;
+  int S = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t a = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, n[4 * k + 1]),
+                                             __builtin_bit_cast(uint32_t, n[4 * k]), 0x0C0C0400u);
+    const uint32_t b = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, n[4 * k + 3]),
+                                             __builtin_bit_cast(uint32_t, n[4 * k + 2]), 0x04000C0Cu);
+    r.codes[k] = a | b;
+    S = __builtin_amdgcn_sdot4((int)r.codes[k], 0x01010101, S, false);
+  }
+  S += dpp<kDppQuadXor1>(S);
+  S += dpp<kDppQuadXor2>(S);
+  r.pair = sc.pair(S);
+  return r;
+}
+
 }  // namespace qmm
