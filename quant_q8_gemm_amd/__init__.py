@@ -162,8 +162,7 @@ def _check_qact(qact) -> None:
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -320,13 +319,13 @@ def _current(t, what: str) -> int:
 
 def _rows(t, what: str, shape, device: int, dtype=None):
     """(address, stride) of a tensor of rows with adjacent elements; the library checks the rest."""
-    if t.get_device() != device:
-        raise QmmError(EINVAL, f"{what} must be on device {device}, got {t.device}")
-    if t.shape != shape or (dtype is not None and t.dtype != dtype):
-        raise QmmError(EINVAL, f"{what} must be {list(shape)} {dtype or ''}, got {list(t.shape)} {t.dtype}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    if t.get_device() == device and t.shape == shape and (dtype is None or t.dtype == dtype):
+        strides = t.stride()
+        if strides[1] == 1 or shape[1] == 1:
+            return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1]
         raise QmmError(EINVAL, f"{what} must have adjacent elements in a row")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    raise QmmError(EINVAL, f"{what} must be {list(shape)} {dtype or ''} on device {device}, got {list(t.shape)} "
+                           f"{t.dtype} on {t.device}")
 
 
 def _vector(t, what: str, n: int, device: int):
@@ -342,14 +341,14 @@ def _bytes(t, what: str, device: int):
     return t.data_ptr(), t.numel()
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor that belongs to the stream it is written on."""
+def _empty(like, shape, dtype, stream):
+    """A new tensor on like's device that belongs to the stream it is written on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _raw_stream(stream, device: int):
@@ -365,7 +364,7 @@ def dequantize_activations(qact, n_tok: int, id_: int, dtype=torch.float32, out=
     q_ptr, q_bytes = _bytes(qact, "qact", device)
     if out is None:
         _elem(dtype)
-        out = _empty((n_tok, id_), dtype, qact.device, stream)
+        out = _empty(qact, (n_tok, id_), dtype, stream)
     ptr, stride = _rows(out, "out", (n_tok, id_), device)
     _check(_lib.qmm_dequantize_activations(q_ptr, q_bytes, n_tok, id_, _elem(out.dtype, "out"), ptr, stride,
                                            _raw_stream(stream, device)))
@@ -412,19 +411,27 @@ def norm_quantize(h, weight, *, y=None, bias=None, post_weight=None, post_bias=N
         else:
             a.gate, a.gate_stride = _rows(gate, "gate", shape, device, dtype)
     if h_out is True:
-        h_out = _empty(shape, dtype, h.device, stream)
-    if h_out is not False:
+        h_out = _empty(h, shape, dtype, stream)
+        a.h_out, a.h_out_stride = h_out.data_ptr(), id_
+    elif h_out is False:
+        h_out = None
+    else:
         a.h_out, a.h_out_stride = _rows(h_out, "h_out", shape, device, dtype)
     if normed is True:
-        normed = _empty(shape, dtype, h.device, stream)
-    if normed is not False:
+        normed = _empty(h, shape, dtype, stream)
+        a.normed, a.normed_stride = normed.data_ptr(), id_
+    elif normed is False:
+        normed = None
+    else:
         a.normed, a.normed_stride = _rows(normed, "normed", shape, device, dtype)
     if qact is True:
-        qact = _empty((qact_bytes(n_tok, id_),), torch.uint8, h.device, stream)
-    if qact is not False:
+        qact = _empty(h, (qact_bytes(n_tok, id_),), torch.uint8, stream)
+    if qact is False:
+        qact = None
+    else:
         a.qact, a.qact_bytes = _bytes(qact, "qact", device)
     _check(_lib.qmm_norm_quantize(a, n_tok, id_, _raw_stream(stream, device)))
-    return NormResult(*(None if v is False else v for v in (h_out, normed, qact)))
+    return NormResult(h_out, normed, qact)
 
 
 def _epilogue(shape, device: int, bias, act: str, mul, residual, scale: float, residual_scale: float) -> Epilogue:
@@ -462,12 +469,12 @@ def mmq_epilogue(w: Weights, qact, n_tok: int, *, bias=None, act: str = "none", 
     ep = _epilogue(shape, device, bias, act, mul, residual, scale, residual_scale)
     if dtype == "q8":
         if out is None:
-            out = _empty((qact_bytes(n_tok, w.od),), torch.uint8, qact.device, stream)
+            out = _empty(qact, (qact_bytes(n_tok, w.od),), torch.uint8, stream)
         out_type, (ptr, stride) = Q8, _bytes(out, "out", device)
     else:
         if out is None:
             _elem(dtype)
-            out = _empty(shape, dtype, qact.device, stream)
+            out = _empty(qact, shape, dtype, stream)
         out_type, (ptr, stride) = _elem(out.dtype, "out"), _rows(out, "out", shape, device)
     work_ptr, work_bytes = _bytes(work, "work", device) if work is not None and work.numel() else (None, 0)
     _check(_lib.qmm_mmq_epilogue(w.handle, q_ptr, q_bytes, n_tok, ep, out_type, ptr, stride, work_ptr, work_bytes,
@@ -493,7 +500,7 @@ def mmv(w: Weights, x, *, bias=None, act: str = "none", mul=None, residual=None,
     ep = _epilogue(shape, device, bias, act, mul, residual, scale, residual_scale)
     if out is None:
         _elem(dtype)
-        out = _empty(shape, dtype, x.device, stream)
+        out = _empty(x, shape, dtype, stream)
     out_ptr, out_stride = _rows(out, "out", shape, device)
     _check(_lib.qmm_mmv(w.handle, x_ptr, x_type, x_stride, n_tok, ep, _elem(out.dtype, "out"), out_ptr, out_stride,
                         _raw_stream(stream, device)))

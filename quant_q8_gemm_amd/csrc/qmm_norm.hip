@@ -54,41 +54,71 @@ struct Stats {
   float mean, rstd;
 };
 
-__device__ __forceinline__ float4 operator+(float4 a, float4 b) {
-  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+// Eight consecutive elements of a row in one thread.
+struct Oct {
+  float4 a, b;
+};
+template <class F>
+__device__ __forceinline__ Oct each(const Oct& x, F&& f) {
+  return {make_float4(f(x.a.x), f(x.a.y), f(x.a.z), f(x.a.w)), make_float4(f(x.b.x), f(x.b.y), f(x.b.z), f(x.b.w))};
 }
-__device__ __forceinline__ float4 operator*(float4 a, float4 b) {
-  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+template <class F>
+__device__ __forceinline__ Oct each(const Oct& x, const Oct& y, F&& f) {
+  return {make_float4(f(x.a.x, y.a.x), f(x.a.y, y.a.y), f(x.a.z, y.a.z), f(x.a.w, y.a.w)),
+          make_float4(f(x.b.x, y.b.x), f(x.b.y, y.b.y), f(x.b.z, y.b.z), f(x.b.w, y.b.w))};
 }
-__device__ __forceinline__ float4 operator*(float4 a, float b) {
-  return make_float4(a.x * b, a.y * b, a.z * b, a.w * b);
+__device__ __forceinline__ Oct operator*(const Oct& x, const Oct& y) {
+  return each(x, y, [](float p, float q) { return p * q; });
 }
-__device__ __forceinline__ float4 operator-(float4 a, float b) {
-  return make_float4(a.x - b, a.y - b, a.z - b, a.w - b);
+__device__ __forceinline__ Oct operator+(const Oct& x, const Oct& y) {
+  return each(x, y, [](float p, float q) { return p + q; });
 }
-__device__ __forceinline__ float sum4(float4 a) { return (a.x + a.y) + (a.z + a.w); }
+__device__ __forceinline__ float sum8(const Oct& x) {
+  return ((x.a.x + x.a.y) + (x.a.z + x.a.w)) + ((x.b.x + x.b.y) + (x.b.z + x.b.w));
+}
 
-// (x - mean)*rstd*weight + bias of elements e .. e + 3
-__device__ __forceinline__ float4 apply(float4 x, const Stats& st, const float* __restrict__ weight,
-                                        const float* __restrict__ bias, int64_t e) {
-  float4 n = (x - st.mean) * st.rstd * *(const float4*)(weight + e);
-  if (bias != nullptr) n = n + *(const float4*)(bias + e);
-  return n;
+template <int TYPE>
+__device__ __forceinline__ Oct load8(const void* p, int64_t i) {
+  return {load4<TYPE>(p, i), load4<TYPE>(p, i + 4)};
+}
+template <int TYPE>
+__device__ __forceinline__ void store8(void* p, int64_t i, const Oct& x) {
+  store4<TYPE>(p, i, x.a);
+  store4<TYPE>(p, i + 4, x.b);
+}
+
+// (x - mean)*rstd*weight + bias
+__device__ __forceinline__ Oct apply(const Oct& x, const Stats& st, const Oct& weight) {
+  return each(x, [&](float v) { return (v - st.mean) * st.rstd; }) * weight;
+}
+__device__ __forceinline__ Oct apply(const Oct& x, const Stats& st, const float* __restrict__ weight,
+                                     const float* __restrict__ bias, int64_t e) {
+  const Oct n = apply(x, st, load8<QMM_F32>(weight, e));
+  return bias == nullptr ? n : n + load8<QMM_F32>(bias, e);
+}
+
+__device__ __forceinline__ float squares(const Oct& x, float mean) {
+  return sum8(each(x, [&](float v) { return (v - mean) * (v - mean); }));
 }
 
 // What the type holds of x.
 template <int TYPE>
-__device__ __forceinline__ float4 rounded(float4 x) {
-  typedef elem_t<TYPE> T;
-  return make_float4((float)(T)x.x, (float)(T)x.y, (float)(T)x.z, (float)(T)x.w);
+__device__ __forceinline__ Oct rounded(const Oct& x) {
+  return each(x, [](float v) { return (float)(elem_t<TYPE>)v; });
 }
 
-__device__ __forceinline__ void store_q8(uint8_t* qact, int64_t t_pad, int id, int64_t t, int e, float4 n) {
-  const Q8Quad r = quant_quad(n);
-  const int sub = threadIdx.x & 7, tt = (int)(t & 31);
+// Elements e .. e + 7 of token t: four lanes hold a q8 block.
+__device__ __forceinline__ void store_q8(uint8_t* qact, int64_t t_pad, int id, int64_t t, int e, const Oct& n) {
+  const Q8Oct r = quant_oct(n.a, n.b);
+  const int sub = threadIdx.x & 3, tt = (int)(t & 31);
   const int64_t frag = (t >> 5) * (id >> 5) + (e >> 5);
-  *(uint32_t*)(qact + frag * 1024 + (sub >> 2) * 512 + tt * 16 + (sub & 3) * 4) = r.codes;
+  *(uint2*)(qact + frag * 1024 + (sub >> 1) * 512 + tt * 16 + (sub & 1) * 8) = make_uint2(r.codes[0], r.codes[1]);
   if (sub == 0) *(uint32_t*)(qact + t_pad * id + frag * 128 + tt * 4) = r.pair;
+}
+
+// rs*p + bs*q, in the same two roundings wherever it is formed
+__device__ __forceinline__ float sum(const qmm_norm& a, float p, float q) {
+  return fmaf(a.residual_scale, p, a.block_scale * q);
 }
 
 // A padding token's zeros.
@@ -115,9 +145,11 @@ struct Reduce {
   float sums[4][kMaxWaves];  // one row per sum over the work-group
 };
 
-// The row in registers: V times four elements per thread, element
-// 4*(v*threads + thread).  A wave's four-element groups cover 256 elements, and
-// id is a multiple of 256, so a wave is inside the row or outside it whole.
+// The row in registers: V times eight elements per thread, element
+// 8*(v*threads + thread); id is a multiple of 256, so the four lanes of a q8 block
+// are inside the row or outside it together.  Everything the row needs is loaded
+// before the first reduction, at V = 1 the weights too, so that no load waits behind
+// a barrier (at V = 2 their registers would halve the rows in flight).
 template <int TYPE, int V>
 __global__ void __launch_bounds__(kMaxThreads)
 norm_kernel(qmm_norm a, int64_t t_pad, int n_tok, int id) {
@@ -128,67 +160,79 @@ norm_kernel(qmm_norm a, int64_t t_pad, int n_tok, int id) {
     zero_q8(qact, t_pad, id, t);
     return;
   }
-  const bool layer = a.kind == QMM_NORM_LAYER;
+  constexpr bool kAhead = V == 1;
+  const bool layer = a.kind == QMM_NORM_LAYER, out = a.normed != nullptr || qact != nullptr;
   const float inv_id = 1.0f / (float)id;
-  const int e0 = 4 * threadIdx.x, step = 4 * blockDim.x;
-  auto stats = [&](const float4(&x)[V], int at) __attribute__((always_inline)) {
+  const int e0 = 8 * threadIdx.x, step = 8 * blockDim.x;
+  auto stats = [&](const Oct(&x)[V], int at) __attribute__((always_inline)) {
     Stats st{0.0f, 0.0f};
     if (layer) {
       float s = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (e0 + v * step < id) s += sum4(x[v]);
+        if (e0 + v * step < id) s += sum8(x[v]);
       st.mean = group_sum(s, red.sums[at]) * inv_id;
     }
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (e0 + v * step < id) s += sum4((x[v] - st.mean) * (x[v] - st.mean));
+      if (e0 + v * step < id) s += squares(x[v], st.mean);
     st.rstd = rsqrtf(group_sum(s, red.sums[at + 1]) * inv_id + a.eps);
     return st;
   };
 
-  float4 s[V], u[V];
+  Oct s[V], u[V], w[V], pw[V], gt[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = e0 + v * step;
     if (e < id) {
-      s[v] = load4<TYPE>(a.h, t * a.h_stride + e);
-      if (a.y != nullptr) u[v] = load4<TYPE>(a.y, t * a.y_stride + e);
+      s[v] = load8<TYPE>(a.h, t * a.h_stride + e);
+      if (a.y != nullptr) u[v] = load8<TYPE>(a.y, t * a.y_stride + e);
+      if (kAhead) {
+        if (a.post_weight != nullptr) pw[v] = load8<QMM_F32>(a.post_weight, e);
+        if (a.gate != nullptr) gt[v] = load8<TYPE>(a.gate, t * a.gate_stride + e);
+        if (out) w[v] = load8<QMM_F32>(a.weight, e);
+      }
     }
   }
   if (a.y != nullptr) {
     if (a.post_weight != nullptr) {
       const Stats st = stats(u, 0);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e0 + v * step < id) u[v] = apply(u[v], st, a.post_weight, a.post_bias, e0 + v * step);
+      for (int v = 0; v < V; ++v) {
+        const int e = e0 + v * step;
+        if (e < id) {
+          u[v] = apply(u[v], st, kAhead ? pw[v] : load8<QMM_F32>(a.post_weight, e));
+          if (a.post_bias != nullptr) u[v] = u[v] + load8<QMM_F32>(a.post_bias, e);
+        }
+      }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = e0 + v * step;
       if (e < id) {
-        if (a.gate != nullptr) u[v] = u[v] * load4<TYPE>(a.gate, t * a.gate_stride + e);
-        s[v] = rounded<TYPE>(s[v] * a.residual_scale + u[v] * a.block_scale);
+        if (a.gate != nullptr) u[v] = u[v] * (kAhead ? gt[v] : load8<TYPE>(a.gate, t * a.gate_stride + e));
+        s[v] = rounded<TYPE>(each(s[v], u[v], [&](float p, float q) { return sum(a, p, q); }));
       }
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = rounded<TYPE>(s[v] * a.residual_scale);
+    for (int v = 0; v < V; ++v) s[v] = rounded<TYPE>(each(s[v], [&](float p) { return p * a.residual_scale; }));
   }
   if (a.h_out != nullptr) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (e0 + v * step < id) store4<TYPE>(a.h_out, t * a.h_out_stride + e0 + v * step, s[v]);
+      if (e0 + v * step < id) store8<TYPE>(a.h_out, t * a.h_out_stride + e0 + v * step, s[v]);
   }
-  if (a.normed == nullptr && qact == nullptr) return;
+  if (!out) return;
   const Stats st = stats(s, 2);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = e0 + v * step;
     if (e < id) {
-      const float4 n = apply(s[v], st, a.weight, a.bias, e);
-      if (a.normed != nullptr) store4<TYPE>(a.normed, t * a.normed_stride + e, n);
+      Oct n = apply(s[v], st, kAhead ? w[v] : load8<QMM_F32>(a.weight, e));
+      if (a.bias != nullptr) n = n + load8<QMM_F32>(a.bias, e);
+      if (a.normed != nullptr) store8<TYPE>(a.normed, t * a.normed_stride + e, n);
       if (qact != nullptr) store_q8(qact, t_pad, id, t, e, n);
     }
   }
@@ -209,45 +253,40 @@ norm_long_kernel(qmm_norm a, int64_t t_pad, int n_tok, int id) {
   }
   const bool layer = a.kind == QMM_NORM_LAYER;
   const float inv_id = 1.0f / (float)id;
-  const int e0 = 4 * threadIdx.x, step = 4 * blockDim.x;
+  const int e0 = 8 * threadIdx.x, step = 8 * blockDim.x;
   auto stats = [&](auto&& get, int at) __attribute__((always_inline)) {
     Stats st{0.0f, 0.0f};
     if (layer) {
       float s = 0.0f;
-      for (int e = e0; e < id; e += step) s += sum4(get(e));
+      for (int e = e0; e < id; e += step) s += sum8(get(e));
       st.mean = group_sum(s, red.sums[at]) * inv_id;
     }
     float s = 0.0f;
-    for (int e = e0; e < id; e += step) {
-      const float4 d = get(e) - st.mean;
-      s += sum4(d * d);
-    }
+    for (int e = e0; e < id; e += step) s += squares(get(e), st.mean);
     st.rstd = rsqrtf(group_sum(s, red.sums[at + 1]) * inv_id + a.eps);
     return st;
   };
   Stats post{0.0f, 0.0f};
   if (a.y != nullptr && a.post_weight != nullptr)
-    post = stats([&](int e) { return load4<TYPE>(a.y, t * a.y_stride + e); }, 0);
+    post = stats([&](int e) { return load8<TYPE>(a.y, t * a.y_stride + e); }, 0);
   auto form = [&](int e) __attribute__((always_inline)) {
-    float4 s = load4<TYPE>(a.h, t * a.h_stride + e) * a.residual_scale;
-    if (a.y != nullptr) {
-      float4 u = load4<TYPE>(a.y, t * a.y_stride + e);
-      if (a.post_weight != nullptr) u = apply(u, post, a.post_weight, a.post_bias, e);
-      if (a.gate != nullptr) u = u * load4<TYPE>(a.gate, t * a.gate_stride + e);
-      s = s + u * a.block_scale;
-    }
-    return rounded<TYPE>(s);
+    Oct s = load8<TYPE>(a.h, t * a.h_stride + e);
+    if (a.y == nullptr) return rounded<TYPE>(each(s, [&](float p) { return p * a.residual_scale; }));
+    Oct u = load8<TYPE>(a.y, t * a.y_stride + e);
+    if (a.post_weight != nullptr) u = apply(u, post, a.post_weight, a.post_bias, e);
+    if (a.gate != nullptr) u = u * load8<TYPE>(a.gate, t * a.gate_stride + e);
+    return rounded<TYPE>(each(s, u, [&](float p, float q) { return sum(a, p, q); }));
   };
   if (a.h_out != nullptr)
-    for (int e = e0; e < id; e += step) store4<TYPE>(a.h_out, t * a.h_out_stride + e, form(e));
+    for (int e = e0; e < id; e += step) store8<TYPE>(a.h_out, t * a.h_out_stride + e, form(e));
   if (a.normed == nullptr && qact == nullptr) return;
-  auto sum = [&](int e) __attribute__((always_inline)) {
-    return a.h_out != nullptr ? load4<TYPE>(a.h_out, t * a.h_out_stride + e) : form(e);
+  auto kept = [&](int e) __attribute__((always_inline)) {
+    return a.h_out != nullptr ? load8<TYPE>(a.h_out, t * a.h_out_stride + e) : form(e);
   };
-  const Stats st = stats(sum, 2);
+  const Stats st = stats(kept, 2);
   for (int e = e0; e < id; e += step) {
-    const float4 n = apply(sum(e), st, a.weight, a.bias, e);
-    if (a.normed != nullptr) store4<TYPE>(a.normed, t * a.normed_stride + e, n);
+    const Oct n = apply(kept(e), st, a.weight, a.bias, e);
+    if (a.normed != nullptr) store8<TYPE>(a.normed, t * a.normed_stride + e, n);
     if (qact != nullptr) store_q8(qact, t_pad, id, t, e, n);
   }
 }
@@ -255,14 +294,16 @@ norm_long_kernel(qmm_norm a, int64_t t_pad, int n_tok, int id) {
 template <int TYPE>
 hipError_t launch_typed(const qmm_norm& a, int64_t n_tok, int64_t t_pad, int64_t id, hipStream_t s) {
   const dim3 grid((unsigned)std::max(n_tok, t_pad));
-  // threads for V groups of four per thread, in whole waves
-  const auto threads = [&](int v) { return dim3((unsigned)((id / 4 + v * 64 - 1) / (v * 64) * 64)); };
-  if (id > 8 * 4 * kMaxThreads)
+  // threads for V groups of eight per thread, in whole waves
+  const auto threads = [&](int v) { return dim3((unsigned)((id / 8 + v * 64 - 1) / (v * 64) * 64)); };
+  if (id > 4 * 8 * kMaxThreads)
     norm_long_kernel<TYPE><<<grid, dim3(kMaxThreads), 0, s>>>(a, t_pad, (int)n_tok, (int)id);
-  else if (id > 4 * 4 * kMaxThreads)
-    norm_kernel<TYPE, 8><<<grid, threads(8), 0, s>>>(a, t_pad, (int)n_tok, (int)id);
-  else
+  else if (id > 2 * 8 * kMaxThreads)
     norm_kernel<TYPE, 4><<<grid, threads(4), 0, s>>>(a, t_pad, (int)n_tok, (int)id);
+  else if (id > 8 * kMaxThreads)
+    norm_kernel<TYPE, 2><<<grid, threads(2), 0, s>>>(a, t_pad, (int)n_tok, (int)id);
+  else
+    norm_kernel<TYPE, 1><<<grid, threads(1), 0, s>>>(a, t_pad, (int)n_tok, (int)id);
   return hipGetLastError();
 }
 
