@@ -65,7 +65,7 @@ extern "C" {
 #define QMM_F32 0
 #define QMM_F16 1
 #define QMM_BF16 2
-#define QMM_Q8 3 /* as the output of a product: q8 blocks, a qact buffer */
+#define QMM_Q8 3 /* as the output or input of a product: q8 blocks, a qact buffer */
 
 /* Return codes. */
 #define QMM_OK 0
@@ -428,11 +428,16 @@ int qmm_mmq_epilogue(const qmm_weights *w, const void *qact, size_t qact_bytes, 
  *   w           a handle of a rows form (current device = its device)
  *   x, x_type   device [n_tok] rows of id activations, QMM_F32, QMM_F16 or
  *               QMM_BF16, x_stride elements from row to row (a multiple of 4 in
- *               [id, QMM_MAX_STRIDE]); aligned to four elements; |x| <= 2046
+ *               [id, QMM_MAX_STRIDE]); aligned to four elements; |x| <= 2046.
+ *               Or QMM_Q8: the qact buffer of these tokens (16-byte aligned), as
+ *               qmm_norm_quantize and qmm_quantize_activations write it, and
+ *               x_stride its qmm_qact_bytes(n_tok, id) bytes; the same results
+ *               as from the numbers it was made of
  *   ep, out_type, out, out_stride  as for qmm_mmq_epilogue, without QMM_Q8
  * No workspace; can be captured into a graph.  Deterministic; a token's result
  * may depend in its last bits on how many tokens the call has.
- * Errors: QMM_EINVAL, QMM_EHIP.  n_tok == 0 is an empty batch.
+ * Errors: QMM_EINVAL, QMM_ESHAPE (a qact of another size), QMM_EHIP.  n_tok == 0 is
+ * an empty batch.
  */
 int qmm_mmv(const qmm_weights *w, const void *x, int x_type, int64_t x_stride, int64_t n_tok,
             const qmm_epilogue *ep, int out_type, void *out, int64_t out_stride, void *stream);

@@ -342,13 +342,14 @@ def _bytes(t, what: str, device: int):
 
 
 def _empty(like, shape, dtype, stream):
-    """A new tensor on like's device that belongs to the stream it is written on."""
+    """A new contiguous tensor on like's device that belongs to the stream it is written on."""
+    strides = (shape[1], 1) if len(shape) == 2 else (1,)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
 
 
 def _raw_stream(stream, device: int):
@@ -473,7 +474,7 @@ def mmq_epilogue(w: Weights, qact, n_tok: int, *, bias=None, act: str = "none", 
         out_type, (ptr, stride) = Q8, _bytes(out, "out", device)
     else:
         if out is None:
-            _elem(dtype)
+            _elem(dtype)  # before the allocation
             out = _empty(qact, shape, dtype, stream)
         out_type, (ptr, stride) = _elem(out.dtype, "out"), _rows(out, "out", shape, device)
     work_ptr, work_bytes = _bytes(work, "work", device) if work is not None and work.numel() else (None, 0)
@@ -482,26 +483,30 @@ def mmq_epilogue(w: Weights, qact, n_tok: int, *, bias=None, act: str = "none", 
     return out
 
 
-def mmv(w: Weights, x, *, bias=None, act: str = "none", mul=None, residual=None, scale: float = 1.0,
+def mmv(w: Weights, x, n_tok: int = None, *, bias=None, act: str = "none", mul=None, residual=None, scale: float = 1.0,
         residual_scale: float = 1.0, dtype=torch.float32, out=None, stream=None):
     """The product for up to MV_MAX_TOKENS tokens straight from the activations, with mmq_epilogue's epilogue:
 
         scale * mul * act(x @ W^T + bias) + residual_scale * residual
 
-    w: a handle of Q4_K_ROWS or Q6_K_ROWS; x: [n_tok][id] of float32, float16 or bfloat16 (rows may be strided).
-    The result is [n_tok][od] of `dtype`, or `out`."""
-    if x.dim() != 2:
-        raise QmmError(EINVAL, "x must be [n_tok][id]")
-    n_tok, od = x.shape[0], w.od
-    x_type = _elem(x.dtype, "x")
+    w: a handle of Q4_K_ROWS or Q6_K_ROWS; x: [n_tok][id] of float32, float16 or bfloat16 (rows may be strided), or
+    the qact buffer of n_tok tokens.  The result is [n_tok][od] of `dtype`, or `out`."""
     device = _current(x, "x")
-    x_ptr, x_stride = _rows(x, "x", (n_tok, w.id), device)
-    shape = (n_tok, od)
+    if n_tok is not None:
+        x_type, (x_ptr, x_stride) = Q8, _bytes(x, "x", device)
+    elif x.dim() == 2:
+        n_tok, x_type = x.shape[0], _elem(x.dtype, "x")
+        x_ptr, x_stride = _rows(x, "x", (n_tok, w.id), device)
+    else:
+        raise QmmError(EINVAL, "x must be [n_tok][id], or a qact buffer with n_tok")
+    shape = (n_tok, w.od)
     ep = _epilogue(shape, device, bias, act, mul, residual, scale, residual_scale)
     if out is None:
-        _elem(dtype)
+        out_type = _elem(dtype)
         out = _empty(x, shape, dtype, stream)
-    out_ptr, out_stride = _rows(out, "out", shape, device)
-    _check(_lib.qmm_mmv(w.handle, x_ptr, x_type, x_stride, n_tok, ep, _elem(out.dtype, "out"), out_ptr, out_stride,
+        out_ptr, out_stride = out.data_ptr(), w.od
+    else:
+        out_type, (out_ptr, out_stride) = _elem(out.dtype, "out"), _rows(out, "out", shape, device)
+    _check(_lib.qmm_mmv(w.handle, x_ptr, x_type, x_stride, n_tok, ep, out_type, out_ptr, out_stride,
                         _raw_stream(stream, device)))
     return out

@@ -728,29 +728,39 @@ int qmm_mmv(const qmm_weights* w, const void* x, int x_type, int64_t x_stride, i
             int out_type, void* out, int64_t out_stride, void* stream) {
   if (int rc = check_elem("out_type", out_type)) return rc;
   if (int rc = check_epilogue(ep, out_type)) return rc;
-  if (int rc = check_elem("x_type", x_type)) return rc;
+  if (x_type != QMM_Q8)
+    if (int rc = check_elem("x_type", x_type)) return rc;
   if (n_tok < 0 || n_tok > QMM_MV_MAX_TOKENS)
     return fail(QMM_EINVAL, "n_tok must be in [0, %d], got %lld", QMM_MV_MAX_TOKENS, (long long)n_tok);
   if (n_tok > 0 && x == nullptr) return fail(QMM_EINVAL, "x is NULL");
-  const size_t xb = elem_bytes(x_type);
-  if (!aligned(x, 4 * xb) || x_stride % 4 != 0)
-    return fail(QMM_EINVAL, "x and its rows must be aligned to four elements");
+  const bool q8 = x_type == QMM_Q8;
+  const size_t xb = q8 ? 1 : elem_bytes(x_type);
+  if (q8 ? !aligned(x, 16) : !aligned(x, 4 * xb) || x_stride % 4 != 0)
+    return fail(QMM_EINVAL, "x and its rows must be aligned to four elements, a q8 x to 16 bytes");
   if (w == nullptr) return fail(QMM_EINVAL, "NULL weights handle");
   if (!qmm::is_rows(w->p.type))
     return fail(QMM_EINVAL, "the handle holds %s weights, qmm_mmv reads the rows forms", type_name(w->p.type));
+  Range in = rows_range("x", x, x_stride, n_tok, w->p.id, xb);
+  if (q8) {
+    const size_t need = qmm_qact_bytes(n_tok, w->p.id);
+    if (x_stride < 0 || (size_t)x_stride != need)
+      return fail(QMM_ESHAPE, "x_stride %lld does not match a qact of n_tok=%lld and the handle's id=%lld (%zu bytes)",
+                  (long long)x_stride, (long long)n_tok, (long long)w->p.id, need);
+    in = {"x", x, 0, need};
+  }
   if (n_tok == 0) {  // empty batch: an empty output, nothing launched
     ok();
     return QMM_OK;
   }
-  if (int rc = check_stride("x", x_stride, w->p.id)) return rc;
+  if (!q8)
+    if (int rc = check_stride("x", x_stride, w->p.id)) return rc;
   qmm::Epilogue r{};
   Range written{};
-  if (int rc = resolve_epilogue(ep, n_tok, w->p.od, out_type, out, out_stride,
-                                rows_range("x", x, x_stride, n_tok, w->p.id, xb), &r, &written))
-    return rc;
+  if (int rc = resolve_epilogue(ep, n_tok, w->p.od, out_type, out, out_stride, in, &r, &written)) return rc;
   int device = -1, num_cus = 0;
   if (int rc = current_device(w, &device, &num_cus)) return rc;
-  hipError_t e = qmm::launch_mmv(w->p, x, x_type, x_stride, (int)n_tok, r, num_cus, (hipStream_t)stream);
+  hipError_t e = qmm::launch_mmv(w->p, x, x_type, q8 ? token_pad(n_tok) * w->p.id : x_stride, (int)n_tok, r, num_cus,
+                                 (hipStream_t)stream);
   if (e != hipSuccess) return fail_hip(e, "mmv launch");
   ok();
   return QMM_OK;

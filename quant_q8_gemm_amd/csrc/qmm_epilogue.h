@@ -34,15 +34,39 @@ struct Epilogue {
   int vec;        // rows can be accessed four elements at a time everywhere
 };
 
-// The sigmoid forms have no cancellation on either side: exp(-x) overflows to
-// infinity for large negative x and the quotient is then -0.
+// x * sigmoid(z).  No cancellation on either side: exp(-z) overflows to infinity for
+// large negative z and its reciprocal is then 0.
+__device__ __forceinline__ float times_sigmoid(float x, float z) {
+  return x * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+// x * Phi(x), Phi the normal distribution function.  For a = |x|, Phi(-a) =
+// exp(-a^2/2) * R(a) with a smooth R, fitted as t*P(t), t = 1/(1 + 0.3a), P of degree
+// 7 with the least relative error over 0 <= a <= 14.5 (1.7e-7; beyond, the
+// exponential is zero in f32), so the negative tail keeps its relative accuracy.
+// The library's erfc cost 9% of a product of 11008 x 4096 by 3314 tokens.
+__device__ __forceinline__ float gelu(float x) {
+  const float a = fabsf(x);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, a, 1.0f));
+  float p = 3.542385948e-02f;
+  p = fmaf(p, t, -1.561589360e-01f);
+  p = fmaf(p, t, 2.045575700e-01f);
+  p = fmaf(p, t, -5.203468462e-02f);
+  p = fmaf(p, t, 1.276920947e-01f);
+  p = fmaf(p, t, 1.001758594e-01f);
+  p = fmaf(p, t, 1.207121488e-01f);
+  p = fmaf(p, t, 1.196320065e-01f);
+  const float tail = p * t * __expf(-0.5f * a * a);
+  return x * (x < 0.0f ? tail : 1.0f - tail);
+}
+
 __device__ __forceinline__ float activate(float x, int act) {
   switch (act) {
     case QMM_ACT_RELU: return fmaxf(x, 0.0f);
-    case QMM_ACT_SILU: return x / (1.0f + __expf(-x));
-    case QMM_ACT_GELU: return 0.5f * x * erfcf(-0.70710678f * x);
+    case QMM_ACT_SILU: return times_sigmoid(x, x);
+    case QMM_ACT_GELU: return gelu(x);
     case QMM_ACT_GELU_TANH:  // 0.5*x*(1 + tanh(z)) = x*sigmoid(2z), z = sqrt(2/pi)*(x + 0.044715*x^3)
-      return x / (1.0f + __expf(-1.5957691f * (x + 0.044715f * x * x * x)));
+      return times_sigmoid(x, 1.5957691f * (x + 0.044715f * x * x * x));
     default: return x;
   }
 }
@@ -62,23 +86,29 @@ __device__ __forceinline__ float4 load_side(const void* p, int type, int64_t i, 
   return make_float4(f[0], f[1], f[2], f[3]);
 }
 
-// The epilogue of rows j .. j + 3 of one token, n of which exist.
-__device__ __forceinline__ float4 finish(const Epilogue& ep, float4 v, int64_t t, int j, int n) {
-  if (ep.bias != nullptr) {
-    const float4 b = load_side(ep.bias, QMM_F32, j, ep.vec, n);
-    v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
-  }
+// What the epilogue of rows j .. j + 3 of one token reads, n of which exist.
+struct Sides {
+  float4 bias, mul, residual;
+};
+__device__ __forceinline__ Sides load_sides(const Epilogue& ep, int64_t t, int j, int n) {
+  Sides s = {};
+  if (ep.bias != nullptr) s.bias = load_side(ep.bias, QMM_F32, j, ep.vec, n);
+  if (ep.mul != nullptr) s.mul = load_side(ep.mul, ep.side_type, t * ep.mul_stride + j, ep.vec, n);
+  if (ep.residual != nullptr) s.residual = load_side(ep.residual, ep.side_type, t * ep.residual_stride + j, ep.vec, n);
+  return s;
+}
+
+// The epilogue of those rows' sums.
+__device__ __forceinline__ float4 finish(const Epilogue& ep, float4 v, const Sides& side) {
+  if (ep.bias != nullptr) v = make_float4(v.x + side.bias.x, v.y + side.bias.y, v.z + side.bias.z, v.w + side.bias.w);
   if (ep.act != QMM_ACT_NONE)
     v = make_float4(activate(v.x, ep.act), activate(v.y, ep.act), activate(v.z, ep.act), activate(v.w, ep.act));
   v = make_float4(v.x * ep.scale, v.y * ep.scale, v.z * ep.scale, v.w * ep.scale);
-  if (ep.mul != nullptr) {
-    const float4 m = load_side(ep.mul, ep.side_type, t * ep.mul_stride + j, ep.vec, n);
-    v = make_float4(v.x * m.x, v.y * m.y, v.z * m.z, v.w * m.w);
-  }
+  if (ep.mul != nullptr) v = make_float4(v.x * side.mul.x, v.y * side.mul.y, v.z * side.mul.z, v.w * side.mul.w);
   if (ep.residual != nullptr) {
-    const float4 r = load_side(ep.residual, ep.side_type, t * ep.residual_stride + j, ep.vec, n);
     const float s = ep.residual_scale;
-    v = make_float4(fmaf(s, r.x, v.x), fmaf(s, r.y, v.y), fmaf(s, r.z, v.z), fmaf(s, r.w, v.w));
+    v = make_float4(fmaf(s, side.residual.x, v.x), fmaf(s, side.residual.y, v.y), fmaf(s, side.residual.z, v.z),
+                    fmaf(s, side.residual.w, v.w));
   }
   return v;
 }

@@ -64,7 +64,8 @@ int64_t row_pad(int64_t od);
 RowPlanes row_planes(int type, int64_t od, int64_t id, void* base, size_t* bytes);
 hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t id, const RowPlanes& r, hipStream_t s);
 struct Epilogue;  // qmm_epilogue.h
-// The product of 1 to QMM_MV_MAX_TOKENS tokens with a rows-form matrix.
+// The product of 1 to QMM_MV_MAX_TOKENS tokens with a rows-form matrix; x_stride
+// of a qact buffer (x_type QMM_Q8): the bytes of its code plane.
 hipError_t launch_mmv(const Planes& p, const void* x, int x_type, int64_t x_stride, int n_tok, const Epilogue& ep,
                       int num_cus, hipStream_t s);
 // The norms and residual sum of qmm_norm_quantize on checked arguments

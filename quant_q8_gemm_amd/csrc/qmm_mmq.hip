@@ -365,7 +365,7 @@ __device__ __forceinline__ void finish_block(const Epilogue& ep, const v16f& acc
     const int tl = 8 * k + (lane >> 3), t = tblock * 32 + tl;
     const bool live = t < n_tok && n > 0;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);  // q8: what padding tokens get
-    if (live) v = finish(ep, *(const float4*)(lds + tl * kEpRow + 4 * quad), t, j, n);
+    if (live) v = finish(ep, *(const float4*)(lds + tl * kEpRow + 4 * quad), load_sides(ep, t, j, n));
     if (ep.out_type == QMM_Q8)  // od % 256 == 0: the eight lanes hold a whole block
       put_q8(ep, quant_quad(v), t, rblock, od, quad);
     else if (live)
@@ -781,7 +781,7 @@ mmq_fixup_kernel(const float* __restrict__ part, int split, int dp_row_tiles, in
     const int n = min(od - j, 4);
     const bool live = t < n_tok && n > 0;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) f = finish(ep, *(const float4*)(lds + tl * kEpRow + 4 * quad), t, j, n);
+    if (live) f = finish(ep, *(const float4*)(lds + tl * kEpRow + 4 * quad), load_sides(ep, t, j, n));
     if (ep.out_type == QMM_Q8) {
       put_q8(ep, quant_quad(f), t, rblock, od, quad);
       if (q == 0 && tt == tok_tiles - 1)

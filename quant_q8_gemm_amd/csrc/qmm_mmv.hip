@@ -172,7 +172,7 @@ constexpr int kScaleBytes = Q6 ? 256 : 512;
 struct MvArgs {
   RowPlanes w;
   const void* x;
-  int64_t x_stride;
+  int64_t x_stride;  // elements; of a qact buffer: bytes of its code plane
   int x_type, n_tok, od, nsb;
   int tile_sb;  // super-blocks quantized at a time
   int kg;       // waves that share a row tile
@@ -290,40 +290,100 @@ __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[4], i
   }
 }
 
-// Quantizes super-blocks [sb0, sb0 + n) of every token into LDS: eight activations
-// per lane, four lanes per 32-block.
+// Where eight codes of a token go: k counts eights from the first of the part.
 template <bool Q6>
-__device__ __forceinline__ void quantize_tile(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0, int n) {
-  const int per_tok = n * 32;
-  for (int i = threadIdx.x; i < a.n_tok * per_tok; i += 64 * kWaves) {
-    const int t = i / per_tok, k = i - t * per_tok;
-    const int64_t at = t * a.x_stride + (int64_t)sb0 * 256 + 8 * k;
-    float4 v[2];
-    if (a.x_type == QMM_F32) {
-      v[0] = load4<QMM_F32>(a.x, at);
-      v[1] = load4<QMM_F32>(a.x, at + 4);
-    } else if (a.x_type == QMM_F16) {
-      v[0] = load4<QMM_F16>(a.x, at);
-      v[1] = load4<QMM_F16>(a.x, at + 4);
-    } else {
-      v[0] = load4<QMM_BF16>(a.x, at);
-      v[1] = load4<QMM_BF16>(a.x, at + 4);
-    }
-    const Q8Oct r = quant_oct(v[0], v[1]);
-    const int sb = k >> 5, c = (k >> 2) & 7, half16 = (k >> 1) & 1;
-    // 32-block c -> (half, nibble, byte group)
-    const int h = c >> 2, nib = Q6 ? (c >> 1) & 1 : c & 1, g = 2 * (Q6 ? c & 1 : (c >> 1) & 1) + half16;
-    uint8_t* const q = lds + sb * sb_bytes;
-    *(uint2*)(q + (((2 * h + nib) * 4 + g) * a.n_tok + t) * 16 + (k & 1) * 8) = make_uint2(r.codes[0], r.codes[1]);
-    if ((k & 3) == 0) {
-      float* const s = (float*)(q + 256 * a.n_tok) + 8 * c + t;
-      s[0] = f16_bits_to_float(r.pair & 0xFFFF);
-      if (!Q6) s[64] = f16_bits_to_float(r.pair >> 16);
-    }
-  }
+__device__ __forceinline__ uint8_t* place(uint8_t* lds, int sb_bytes, int n_tok, int t, int k) {
+  const int c = (k >> 2) & 7, half16 = (k >> 1) & 1;  // 32-block, its 16 codes
+  const int h = c >> 2, nib = Q6 ? (c >> 1) & 1 : c & 1, g = 2 * (Q6 ? c & 1 : (c >> 1) & 1) + half16;
+  return lds + (k >> 5) * sb_bytes + (((2 * h + nib) * 4 + g) * n_tok + t) * 16 + (k & 1) * 8;
+}
+template <bool Q6>
+__device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int n_tok, int t, int k, uint32_t pair) {
+  float* const s = (float*)(lds + (k >> 5) * sb_bytes + 256 * n_tok) + 8 * ((k >> 2) & 7) + t;
+  s[0] = f16_bits_to_float(pair & 0xFFFF);
+  if (!Q6) s[64] = f16_bits_to_float(pair >> 16);
 }
 
-template <bool Q6, bool WIDE>
+// The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
+// numbers: eight per thread, four threads per 32-block, the next eight loaded
+// while these are quantized; begin() loads the first ones, so that the caller can
+// put other loads behind them.
+template <bool Q6, int XT>
+struct Quantizer {
+  float4 v0, v1;
+  int t, k, per_tok, dt, dk;
+  __device__ __forceinline__ void fetch(const MvArgs& a, int sb0) {
+    if (t < a.n_tok) {
+      const int64_t at = t * a.x_stride + (sb0 * 256 + 8 * k);
+      v0 = load4<XT>(a.x, at);
+      v1 = load4<XT>(a.x, at + 4);
+    }
+  }
+  __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
+    per_tok = n * 32;
+    t = threadIdx.x / per_tok;
+    k = threadIdx.x - t * per_tok;
+    dt = 64 * kWaves / per_tok;  // the threads' stride in tokens and eights
+    dk = 64 * kWaves - dt * per_tok;
+    fetch(a, sb0);
+  }
+  __device__ __forceinline__ void run(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0) {
+    while (t < a.n_tok) {
+      const float4 c0 = v0, c1 = v1;
+      const int tok = t, at = k;
+      k += dk;
+      t += dt;
+      if (k >= per_tok) {
+        k -= per_tok;
+        ++t;
+      }
+      fetch(a, sb0);
+      const Q8Oct r = quant_oct(c0, c1);
+      *(uint2*)place<Q6>(lds, sb_bytes, a.n_tok, tok, at) = make_uint2(r.codes[0], r.codes[1]);
+      if ((at & 3) == 0) place_scales<Q6>(lds, sb_bytes, a.n_tok, tok, at, r.pair);
+    }
+  }
+};
+
+// From a qact buffer (one token block: n_tok <= 8): 16 codes, half a 32-block, per
+// thread, in a slot per token (1, 2, 4 or 8 of them).
+template <bool Q6>
+struct Quantizer<Q6, QMM_Q8> {
+  uint4 codes;
+  uint32_t pair;
+  int t, half, halves, slots;
+  __device__ __forceinline__ void fetch(const MvArgs& a, int sb0) {
+    if (half < halves && t < a.n_tok) {
+      const uint8_t* const q = (const uint8_t*)a.x;
+      const uint32_t c = (uint32_t)(sb0 * 8 + (half >> 1));
+      codes = *(const uint4*)(q + (size_t)c * 1024 + (half & 1) * 512 + t * 16);
+      if ((half & 1) == 0) pair = *(const uint32_t*)(q + a.x_stride + (size_t)c * 128 + t * 4);
+    }
+  }
+  __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
+    const int bits = a.n_tok > 4 ? 3 : a.n_tok > 2 ? 2 : a.n_tok > 1 ? 1 : 0;
+    slots = 1 << bits;
+    t = threadIdx.x & (slots - 1);
+    half = threadIdx.x >> bits;
+    halves = n * 16;
+    fetch(a, sb0);
+  }
+  __device__ __forceinline__ void run(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0) {
+    while (half < halves) {
+      const uint4 c = codes;
+      const uint32_t pr = pair;
+      const int at = 2 * half;
+      half += 64 * kWaves / slots;
+      fetch(a, sb0);
+      if (t < a.n_tok) {
+        *(uint4*)place<Q6>(lds, sb_bytes, a.n_tok, t, at) = c;
+        if ((at & 2) == 0) place_scales<Q6>(lds, sb_bytes, a.n_tok, t, at, pr);
+      }
+    }
+  }
+};
+
+template <bool Q6, bool WIDE, int XT>
 __global__ void __launch_bounds__(64 * kWaves)
 mmv_kernel(MvArgs a, Epilogue ep) {
   constexpr int kTok = WIDE ? 8 : 4;
@@ -340,13 +400,27 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   const bool one_tile = a.tile_sb == a.nsb;
   const int m = lane & 15, G = lane >> 4;
 
-  Raw<Q6> next;
-  auto fetch = [&](int step, int sb) __attribute__((always_inline)) {
-    next.load(a.w, (int64_t)min(step * groups + rg, tiles - 1) * a.nsb + sb, (uint32_t)lane);
+  // Loads return in order, so the activations' go first.
+  Quantizer<Q6, XT> quant;
+  quant.begin(a, 0, a.tile_sb);
+  // The wave's weights, kAhead super-blocks ahead: super-blocks kg, kg + a.kg, ... of
+  // its tile of this step, then of the next step's (past the last step: the last
+  // step's again, unused).
+  constexpr int kAhead = Q6 ? 1 : 2;
+  Raw<Q6> ahead[kAhead];
+  int f_step = blockIdx.x, f_sb = kg;
+  auto fetch = [&](Raw<Q6>& to) __attribute__((always_inline)) {
+    to.load(a.w, (int64_t)min(f_step * groups + rg, tiles - 1) * a.nsb + f_sb, (uint32_t)lane);
+    f_sb += a.kg;
+    if (f_sb >= a.nsb) {
+      f_sb = kg;
+      f_step = min(f_step + (int)gridDim.x, a.steps - 1);
+    }
   };
-  fetch(blockIdx.x, min(kg, a.nsb - 1));
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(ahead[i]);
   if (threadIdx.x == 0) *zeros = make_uint4(0, 0, 0, 0);
-  if (one_tile) quantize_tile<Q6>(a, lds, sb_bytes, 0, a.nsb);
+  if (one_tile) quant.run(a, lds, sb_bytes, 0);
   __syncthreads();
 
   // The lane's A operand: its token's codes of its byte group, or zeros (always
@@ -357,25 +431,31 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   const uint32_t at = (uint32_t)(G * a.n_tok + tok) * 16, step_nib = (uint32_t)a.n_tok * 64;
   const uint32_t zero_at = (uint32_t)((uint8_t*)zeros - lds);
   const float* const scales = (const float*)(lds + 256 * a.n_tok) + (WIDE ? 4 * (G & 1) : 0);
+  // The thread that finishes four rows of a token: of which wave group's tile
+  const int per_group = 4 * a.n_tok;
+  const int e_group = (int)threadIdx.x / per_group, e_at = (int)threadIdx.x - e_group * per_group;
+  const int e_tok = e_at >> 2, e_row = 4 * (e_at & 3);
 
   int buf = 0;
   for (int step = blockIdx.x; step < a.steps; step += gridDim.x, buf ^= 1) {
+    const int row = (step * groups + e_group) * kTile + e_row;
+    const int left = e_group < groups ? min(a.od - row, 4) : 0;
+    Sides side = {};
+    if (left > 0) side = load_sides(ep, e_tok, row, left);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int sb0 = 0; sb0 < a.nsb; sb0 += a.tile_sb) {
       const int n = min(a.tile_sb, a.nsb - sb0);
       if (!one_tile) {
-        __syncthreads();  // the last tile's readers are done
-        quantize_tile<Q6>(a, lds, sb_bytes, sb0, n);
+        if (sb0 > 0 || step != (int)blockIdx.x) quant.begin(a, sb0, n);
+        __syncthreads();  // the last part's readers are done
+        quant.run(a, lds, sb_bytes, sb0);
         __syncthreads();
       }
       for (int sb = kg; sb < n; sb += a.kg) {
-        const Raw<Q6> w = next;
-        // the next super-block: of this part, of the next one, of the next row tile
-        const bool same = sb + a.kg < n;
-        const int left = a.nsb - sb0 - n;  // super-blocks after this part
-        const bool same_row = same || kg < left;
-        fetch(same_row ? step : min(step + (int)gridDim.x, a.steps - 1),
-              same ? sb0 + sb + a.kg : same_row ? sb0 + n + kg : min(kg, a.nsb - 1));
+        const Raw<Q6> w = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+        fetch(ahead[kAhead - 1]);
         const uint32_t base = (uint32_t)(sb * sb_bytes);
         const float* const dh = (const float*)((const uint8_t*)scales + base);
         auto codes = [&](int h, int nib, int k = 0) __attribute__((always_inline)) {
@@ -405,25 +485,21 @@ mmv_kernel(MvArgs a, Epilogue ep) {
     }
     __syncthreads();
     // two buffers: the next step's sums do not overwrite these, the one after has
-    // passed the next barrier.  A thread per four rows of a token.
-    const int per_group = 4 * a.n_tok;
-    if ((int)threadIdx.x < groups * per_group) {
-      const int gr = threadIdx.x / per_group, at4 = threadIdx.x - gr * per_group;
-      const int t = at4 >> 2, row = (step * groups + gr) * kTile + 4 * (at4 & 3);
-      const float* p = red + ((size_t)buf * kWaves + gr * a.kg) * (kTok * kTile) + t * kTile + 4 * (at4 & 3);
+    // passed the next barrier
+    if (left > 0) {
+      const float* p = red + ((size_t)buf * kWaves + e_group * a.kg) * (kTok * kTile) + e_tok * kTile + e_row;
       float4 f = *(const float4*)p;
       for (int k = 1; k < a.kg; ++k) {
         const float4 e = *(const float4*)(p + (size_t)k * (kTok * kTile));
         f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
       }
-      const int left = min(a.od - row, 4);
-      if (left > 0) put(ep, finish(ep, f, t, row, left), t, row, left);
+      put(ep, finish(ep, f, side), e_tok, row, left);
     }
   }
 }
 
-template <bool Q6, bool WIDE>
-hipError_t launch_typed(const MvArgs& in, const Epilogue& ep, int num_cus, hipStream_t s) {
+template <bool Q6, bool WIDE, int XT>
+hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipStream_t s) {
   MvArgs a = in;
   // LDS: the whole inner dimension where it fits the CU's 160 KB, else parts of it,
   // quantized again for every set of row tiles
@@ -431,6 +507,7 @@ hipError_t launch_typed(const MvArgs& in, const Epilogue& ep, int num_cus, hipSt
   constexpr size_t kRed = (size_t)2 * kWaves * (WIDE ? 8 : 4) * kTile * sizeof(float) + 16;
   const size_t per_sb = (size_t)256 * a.n_tok + kScaleBytes<Q6>;
   a.tile_sb = (int)std::min<size_t>(a.nsb, (kMost - kRed) / per_sb);
+  if (a.tile_sb < a.nsb) a.tile_sb = a.tile_sb / kWaves * kWaves;  // a wave's super-blocks go on across parts
   const size_t lds = a.tile_sb * per_sb + kRed;
   // One work-group per CU.  Waves per row tile: as few as fill the GPU's CUs with
   // row tiles of their own, and the fewest rounds of them, counted in the
@@ -448,12 +525,20 @@ hipError_t launch_typed(const MvArgs& in, const Epilogue& ep, int num_cus, hipSt
   }
   const int grid = (int)std::min<int64_t>(a.steps, num_cus);
   if (lds > 64 * 1024) {
-    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, WIDE>, hipFuncAttributeMaxDynamicSharedMemorySize,
+    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, WIDE, XT>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)lds);
     if (e != hipSuccess) return e;
   }
-  mmv_kernel<Q6, WIDE><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
+  mmv_kernel<Q6, WIDE, XT><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
   return hipGetLastError();
+}
+
+template <bool Q6, bool WIDE>
+hipError_t launch_typed(const MvArgs& a, const Epilogue& ep, int num_cus, hipStream_t s) {
+  return a.x_type == QMM_F32    ? launch_kernel<Q6, WIDE, QMM_F32>(a, ep, num_cus, s)
+         : a.x_type == QMM_F16  ? launch_kernel<Q6, WIDE, QMM_F16>(a, ep, num_cus, s)
+         : a.x_type == QMM_BF16 ? launch_kernel<Q6, WIDE, QMM_BF16>(a, ep, num_cus, s)
+                                : launch_kernel<Q6, WIDE, QMM_Q8>(a, ep, num_cus, s);
 }
 
 }  // namespace

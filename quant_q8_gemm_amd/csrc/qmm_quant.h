@@ -71,9 +71,9 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_ca
 struct Q8Scale {
   _Float16 dh;
   float dhf, inv;
-  __device__ __forceinline__ explicit Q8Scale(float amax) {
-    const float d32 = amax / 127.0f;
-    dh = (_Float16)d32;  // round to nearest even
+  __device__ __forceinline__ explicit Q8Scale(float amax) : Q8Scale((_Float16)(amax / 127.0f)) {}  // nearest even
+  __device__ __forceinline__ explicit Q8Scale(_Float16 scale) {
+    dh = scale;
     dhf = (float)dh;
     inv = dhf == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(dhf);
   }
@@ -103,36 +103,45 @@ __device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
 }
 
 // The same block with eight consecutive values per lane, four lanes (4i .. 4i + 3):
-// half the shared work per value.  Codes are rounded by adding 1.5 * 2^23, whose
-// sum holds the integer (half to even) in its low bits.
+// half the shared work per value, and cheaper forms of the same numbers:
+//  * amax/127 with one Newton step on the quotient's remainder, q + (a - 127q)/127
+//    (Markstein): the correctly rounded quotient for every finite f32 whose
+//    quotient is normal (checked for every significand; smaller ones round to a
+//    scale of zero either way);
+//  * codes rounded by adding 1.5 * 2^23, whose sum holds the integer (half to
+//    even) in its low bits;
+//  * no clamp where dh is a normal f16: dh is then amax/127 to 2^-11, so that no
+//    quotient exceeds 127.07 and rounds above 127.
 struct Q8Oct {
   uint32_t codes[2], pair;
 };
 
-__device__ __forceinline__ float max4lanes(float v) {
-  uint32_t u = __builtin_bit_cast(uint32_t, v);
+__device__ __forceinline__ Q8Oct quant_oct(const float4& v0, const float4& v1) {
+  constexpr float kRound = 12582912.0f;      // 1.5 * 2^23
+  constexpr float kHalfMin = 6.103515625e-5f;  // the smallest normal f16
+  const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  float top = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+  uint32_t u = __builtin_bit_cast(uint32_t, top);
   u = max(u, (uint32_t)dpp<kDppQuadXor1>((int)u));
   u = max(u, (uint32_t)dpp<kDppQuadXor2>((int)u));
-  return __builtin_bit_cast(float, u);
-}
-
-__device__ __forceinline__ Q8Oct quant_oct(const float4& v0, const float4& v1) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
-  const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-  float top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
-  const Q8Scale sc(max4lanes(top));
+  const float amax = __builtin_bit_cast(float, u);
+  const float q0 = amax * (1.0f / 127.0f);
+  const Q8Scale sc((_Float16)fmaf(fmaf(-127.0f, q0, amax), 1.0f / 127.0f, q0));
   float n[8], far = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float r = __builtin_amdgcn_fmed3f(v[i] * sc.inv, -127.0f, 127.0f);
+    const float r = v[i] * sc.inv;
     n[i] = r + kRound;
     far = fmaxf(far, fabsf(r - (n[i] - kRound)));
   }
-  if (far > 0.5f - 1e-4f) {  // as in quant4: next to a tie the quotients are formed exactly
+  if (!(far <= 0.5f - 1e-4f) || sc.dhf < kHalfMin) {  // as in quant4: next to a tie the quotients are formed exactly
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = __builtin_amdgcn_fmed3f(v[i] / sc.dhf, -127.0f, 127.0f) + kRound;
+    for (int i = 0; i < 8; ++i) {
+      const float r = sc.dhf == 0.0f ? 0.0f : v[i] / sc.dhf;
+      n[i] = __builtin_amdgcn_fmed3f(r, -127.0f, 127.0f) + kRound;
+    }
   }
   Q8Oct r;
   int S = 0;

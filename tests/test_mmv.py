@@ -32,7 +32,7 @@ def test_refusals_that_need_no_handle():
         ep = qmm.Epilogue(**{"scale": 1.0, **kw})
         return L.qmm_mmv(None, x_ptr, x_type, x_stride, n_tok, ctypes.byref(ep), out_type, o, 16, None)
 
-    for change, word in (({"n_tok": -1}, "n_tok"), ({"n_tok": 9}, "n_tok"), ({"x_type": 3}, "x_type"), ({"x_ptr": None}, "x is"),
+    for change, word in (({"n_tok": -1}, "n_tok"), ({"n_tok": 9}, "n_tok"), ({"x_type": 4}, "x_type"), ({"x_type": 3, "x_ptr": x + 8}, "aligned"), ({"x_ptr": None}, "x is"),
                          ({"x_ptr": x + 8}, "aligned"), ({"x_ptr": x + 4, "x_type": 1}, "aligned"),
                          ({"x_stride": 514}, "aligned"), ({"out_type": 3}, "out_type"), ({"act": 7}, "act"),
                          ({"scale": float("inf")}, "finite"), ({}, "handle")):
@@ -131,6 +131,8 @@ def test_mmv_against_oracle_and_formula(device, type_, od, id_):  # noqa: F811
         got = qmm.mmv(w, x)
         sums_ok(got, kept, type_, od, id_, x)
         assert torch.equal(got, qmm.mmv(w, x)), "a repeat differs"
+        qact = qmm.quantize_activations(x.float())
+        assert torch.equal(got, qmm.mmv(w, qact, n_tok)), "from its q8 blocks it differs"
         for i, act in enumerate(ACTS[n_tok % 2::2]):
             c = sides(device, n_tok, od, TYPES[i % 3], i)
             ep = {**c, "act": act, "scale": 0.5, "residual_scale": -1.25}
@@ -147,7 +149,9 @@ def test_longest_rows_in_tiles(device, type_):  # noqa: F811
         raw, x = synth.case(type_, od, id_, n_tok, seed=od)
         w = qmm.register_weights(ROWS[type_], od, id_, raw)
         x = torch.from_numpy(x).to(device)
-        sums_ok(qmm.mmv(w, x), raw, type_, od, id_, x)
+        got = qmm.mmv(w, x)
+        sums_ok(got, raw, type_, od, id_, x)
+        assert torch.equal(got, qmm.mmv(w, qmm.quantize_activations(x), n_tok))
         w.release()
 
 
@@ -169,7 +173,38 @@ def test_extreme_blocks(device, type_):  # noqa: F811
     x[3, ::2] = 0
     w = qmm.register_weights(ROWS[type_], od, id_, blk.reshape(-1))
     x = torch.from_numpy(x).to(device)
-    sums_ok(qmm.mmv(w, x), blk.reshape(-1), type_, od, id_, x)
+    got = qmm.mmv(w, x)
+    sums_ok(got, blk.reshape(-1), type_, od, id_, x)
+    assert torch.equal(got, qmm.mmv(w, qmm.quantize_activations(x), T))  # the prepass's codes, ties and subnormals too
+    w.release()
+
+
+@gpu
+def test_quantized_in_the_kernel_as_by_the_prepass(device):  # noqa: F811
+    """Values a few ulps either side of half-integer quotients and on them, vanishing and subnormal scales: the
+    same bits from the numbers and from the prepass's blocks of them."""
+    rng = np.random.default_rng(11)
+    T, id_ = 8, 1024
+    x = np.zeros((T, id_), np.float32)
+    xb = x.reshape(T, -1, 32)
+    steps = (np.abs(rng.standard_normal(xb.shape[:2])) * 0.05 + 1e-3).astype(np.float16).astype(np.float32)
+    steps[6] = np.float32(2.0 ** -24) * rng.integers(1, 40, steps.shape[1])  # subnormal scales
+    steps[7, ::2] = 1e-9                                                      # vanishing ones
+    xb[:, :, 0] = 127 * steps
+    k = rng.integers(-126, 126, size=xb[:, :, 1:].shape).astype(np.float32)
+    ulps = rng.integers(-3, 4, size=k.shape)
+    target = ((k + 0.5) * steps[:, :, None]).astype(np.float32)
+    xb[:, :, 1:] = np.nextafter(target, np.where(ulps > 0, np.inf, -np.inf).astype(np.float32))
+    xb[:, :, 1:] = np.where(ulps == 0, target, xb[:, :, 1:])
+    xb[6, :, 31] = 1.49 * 127 * steps[6]  # dh rounds down by up to a third: the clamp
+    raw = synth.q6k_weights(rng, 200, id_)
+    w = qmm.register_weights(qmm.Q6_K_ROWS, 200, id_, raw)
+    xt = torch.from_numpy(x).to(device)
+    got = qmm.mmv(w, xt)
+    assert torch.equal(got, qmm.mmv(w, qmm.quantize_activations(xt), T))
+    sums_ok(got, raw, synth.Q6_K, 200, id_, xt)
+    r = qmm.norm_quantize(xt, torch.ones(id_, device=device), normed=True)  # the norm's blocks are made the same way
+    assert torch.equal(r.qact, qmm.quantize_activations(r.normed))
     w.release()
 
 
@@ -253,6 +288,10 @@ def test_mmv_refusals_with_a_handle(device):  # noqa: F811
     refused(xx=torch.zeros(T, id_ + 2, device=device)[:, :-2])
     refused(xx=x[:1].expand(T, id_))
     refused(dtype=torch.float64)
+    with pytest.raises(qmm.QmmError) as e:
+        qmm.mmv(w, qmm.quantize_activations(x)[:-16], T)
+    assert e.value.code == qmm.ESHAPE
+    refused(xx=x.view(-1))
     refused(mul=c["mul"].half(), residual=c["residual"])
     refused(out=torch.empty(T, od + 1, device=device))
     both = torch.zeros(T * id_ + 64, device=device)
