@@ -410,7 +410,9 @@ typedef struct {
  *               aligned, work_bytes of it, at least the plan's scratch_bytes
  *               (qmm_mmq_plan): the call then allocates nothing and can be
  *               captured, and calls with work memory of their own may overlap.
- *               NULL with work_bytes 0: the stream's scratch, as qmm_mmq.
+ *               NULL with work_bytes 0: the stream's scratch, as qmm_mmq; a
+ *               captured call that needs scratch is then refused, since graphs
+ *               replayed side by side would share it.
  * out may be mul or residual in place (same pointer, stride and type); any
  * other overlap of out or work with an input is refused.
  * Errors: as qmm_mmq.

@@ -492,7 +492,8 @@ int resolve_epilogue(const qmm_epilogue* ep, int64_t n_tok, int64_t od, int out_
   if (out == nullptr) return fail(QMM_EINVAL, "out is NULL");
   if (out_type == QMM_Q8) {
     const size_t need = qmm_qact_bytes(n_tok, od);
-    if (need == 0) return fail(QMM_EINVAL, "a q8 output needs od %% 256 == 0, got od=%lld", (long long)od);
+    if (need == 0)
+      return fail(QMM_EINVAL, "a q8 output needs od %% 256 == 0 and od <= %d, got od=%lld", QMM_MAX_ID, (long long)od);
     if (out_stride < 0 || (size_t)out_stride != need)
       return fail(QMM_EINVAL, "out_stride %lld != qmm_qact_bytes(%lld, %lld) = %zu", (long long)out_stride,
                   (long long)n_tok, (long long)od, need);
@@ -515,9 +516,6 @@ int resolve_epilogue(const qmm_epilogue* ep, int64_t n_tok, int64_t od, int out_
                             rows_range("residual", ep->residual, ep->residual_stride, n_tok, od, eb)})
     if (overlap(*written, side) && !(out_type == ep->type && same_rows(*written, side)))
       return refuse_overlap(*written, side);
-  const auto quads = [&](const void* p, int64_t stride, size_t elem) {
-    return p == nullptr || (aligned(p, 4 * elem) && stride % 4 == 0);
-  };
   r->bias = ep->bias;
   r->mul = ep->mul;
   r->residual = ep->residual;
@@ -531,9 +529,6 @@ int resolve_epilogue(const qmm_epilogue* ep, int64_t n_tok, int64_t od, int out_
   r->act = ep->act;
   r->side_type = ep->type;
   r->out_type = out_type;
-  r->vec = od % 4 == 0 && quads(ep->bias, 0, 4) && quads(ep->mul, ep->mul_stride, eb) &&
-           quads(ep->residual, ep->residual_stride, eb) &&
-           (out_type == QMM_Q8 || quads(out, out_stride, elem_bytes(out_type)));
   return QMM_OK;
 }
 
@@ -715,8 +710,15 @@ int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, 
                 plan.scratch_bytes);
   const hipStream_t s = (hipStream_t)stream;
   void* scratch = work;
-  if (scratch == nullptr && plan.scratch_bytes > 0)
+  if (scratch == nullptr && plan.scratch_bytes > 0) {
+    // a captured launch outlives the stream's turn: two graphs would share its scratch
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(s, &capture) != hipSuccess) (void)hipGetLastError();
+    if (capture != hipStreamCaptureStatusNone)
+      return fail(QMM_EINVAL, "a captured call of this shape needs %zu bytes of work memory of its own",
+                  plan.scratch_bytes);
     if (int rc = stream_scratch(device, num_cus, s, &scratch)) return rc;
+  }
   hipError_t e = qmm::launch_mmq_epilogue(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), r,
                                           (float*)scratch, s);
   if (e != hipSuccess) return fail_hip(e, "mmq launch");

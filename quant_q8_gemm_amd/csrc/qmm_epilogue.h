@@ -31,7 +31,6 @@ struct Epilogue {
   int act;
   int side_type;  // element type of mul and residual
   int out_type;   // element type of out, or QMM_Q8
-  int vec;        // rows can be accessed four elements at a time everywhere
 };
 
 // x * sigmoid(z).  No cancellation on either side: exp(-z) overflows to infinity for
@@ -71,19 +70,21 @@ __device__ __forceinline__ float activate(float x, int act) {
   }
 }
 
-// Rows j .. j + 3 of a token's row of mul, residual or out, at element offset i;
-// n of them exist (1 to 4), all four where the access is one vector.
-__device__ __forceinline__ float4 load_side(const void* p, int type, int64_t i, int vec, int n) {
-  if (vec)
-    return type == QMM_F32 ? load4<QMM_F32>(p, i) : type == QMM_F16 ? load4<QMM_F16>(p, i) : load4<QMM_BF16>(p, i);
-  float f[4] = {0.f, 0.f, 0.f, 0.f};
+// Rows j .. j + 3 of a token's row of mul, residual or out, at element offset i, of
+// any alignment; n of them exist: one access where all four do, else one each.
+template <int TYPE>
+__device__ __forceinline__ float4 load_typed(const void* p, int64_t i, int n) {
+  if (n == 4) return load4_any<TYPE>(p, i);
+  float f[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < n)
-      f[k] = type == QMM_F32   ? load1<QMM_F32>(p, i + k)
-             : type == QMM_F16 ? load1<QMM_F16>(p, i + k)
-                               : load1<QMM_BF16>(p, i + k);
-  return make_float4(f[0], f[1], f[2], f[3]);
+  for (int k = 0; k < 3; ++k)
+    if (k < n) f[k] = load1<TYPE>(p, i + k);
+  return make_float4(f[0], f[1], f[2], 0.0f);
+}
+__device__ __forceinline__ float4 load_side(const void* p, int type, int64_t i, int n) {
+  return type == QMM_F32   ? load_typed<QMM_F32>(p, i, n)
+         : type == QMM_F16 ? load_typed<QMM_F16>(p, i, n)
+                           : load_typed<QMM_BF16>(p, i, n);
 }
 
 // What the epilogue of rows j .. j + 3 of one token reads, n of which exist.
@@ -92,9 +93,9 @@ struct Sides {
 };
 __device__ __forceinline__ Sides load_sides(const Epilogue& ep, int64_t t, int j, int n) {
   Sides s = {};
-  if (ep.bias != nullptr) s.bias = load_side(ep.bias, QMM_F32, j, ep.vec, n);
-  if (ep.mul != nullptr) s.mul = load_side(ep.mul, ep.side_type, t * ep.mul_stride + j, ep.vec, n);
-  if (ep.residual != nullptr) s.residual = load_side(ep.residual, ep.side_type, t * ep.residual_stride + j, ep.vec, n);
+  if (ep.bias != nullptr) s.bias = load_typed<QMM_F32>(ep.bias, j, n);
+  if (ep.mul != nullptr) s.mul = load_side(ep.mul, ep.side_type, t * ep.mul_stride + j, n);
+  if (ep.residual != nullptr) s.residual = load_side(ep.residual, ep.side_type, t * ep.residual_stride + j, n);
   return s;
 }
 
@@ -114,21 +115,21 @@ __device__ __forceinline__ float4 finish(const Epilogue& ep, float4 v, const Sid
 }
 
 template <int TYPE>
-__device__ __forceinline__ void put_typed(const Epilogue& ep, float4 v, int64_t i, int n) {
-  if (ep.vec) {
-    store4<TYPE>(ep.out, i, v);
+__device__ __forceinline__ void put_typed(void* p, const float4& v, int64_t i, int n) {
+  if (n == 4) {
+    store4_any<TYPE>(p, i, v);
   } else {
-    const float f[4] = {v.x, v.y, v.z, v.w};
+    const float f[3] = {v.x, v.y, v.z};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < n) store1<TYPE>(ep.out, i + k, f[k]);
+    for (int k = 0; k < 3; ++k)
+      if (k < n) store1<TYPE>(p, i + k, f[k]);
   }
 }
 __device__ __forceinline__ void put(const Epilogue& ep, float4 v, int64_t t, int j, int n) {
   const int64_t i = t * ep.out_stride + j;
-  if (ep.out_type == QMM_F32) put_typed<QMM_F32>(ep, v, i, n);
-  else if (ep.out_type == QMM_F16) put_typed<QMM_F16>(ep, v, i, n);
-  else put_typed<QMM_BF16>(ep, v, i, n);
+  if (ep.out_type == QMM_F32) put_typed<QMM_F32>(ep.out, v, i, n);
+  else if (ep.out_type == QMM_F16) put_typed<QMM_F16>(ep.out, v, i, n);
+  else put_typed<QMM_BF16>(ep.out, v, i, n);
 }
 
 }  // namespace qmm

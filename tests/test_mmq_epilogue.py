@@ -273,6 +273,14 @@ def test_work_memory_streams_and_graphs(device):
 
     chain(works[2])
     torch.cuda.synchronize()
+    if need:  # without work memory of its own a split call is not captured
+        refused = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(refused):
+            out.zero_()
+            with pytest.raises(qmm.QmmError) as e:
+                qmm.mmq_epilogue(w, q_in, T, out=torch.empty((T, od), device=device))
+        assert e.value.code == qmm.EINVAL
+        del refused
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         chain(works[2])
