@@ -89,7 +89,7 @@ extern "C" {
 #define QMM_MAX_STRIDE (1 << 24)
 
 /* Most tokens of one qmm_mmv. */
-#define QMM_MV_MAX_TOKENS 8
+#define QMM_MV_MAX_TOKENS 16
 
 /* Tokens are padded to a multiple of this many in the qact buffer. */
 #define QMM_TOKEN_PAD 128

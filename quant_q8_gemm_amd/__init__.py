@@ -13,7 +13,7 @@ and what stands between the products of a layer:
 
     r = qmm.norm_quantize(h, weight, y=out)                     # r.h = h + out, r.qact = q8(norm(r.h))
     out = qmm.mmq_epilogue(w, r.qact, n_tok, act="silu", dtype=torch.float16)
-    out = qmm.mmv(w_rows, x, residual=h)                        # up to 8 tokens, w_rows: a rows-form handle
+    out = qmm.mmv(w_rows, x, residual=h)                        # up to 16 tokens, w_rows: a rows-form handle
 """
 from __future__ import annotations
 
@@ -50,7 +50,7 @@ EHIP = -4
 TOKEN_PAD = 128
 Q4_K_ROWS = 24  # the rows forms, for mmv
 Q6_K_ROWS = 26
-MV_MAX_TOKENS = 8
+MV_MAX_TOKENS = 16
 BLOCK_BYTES = {Q4_K: 144, Q4_K_PACKED: 144, Q6_K: 210, Q4_K_ROWS: 144, Q6_K_ROWS: 210}
 
 # The full list of entry points include/qmm.h declares.

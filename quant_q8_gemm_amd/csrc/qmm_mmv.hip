@@ -1,4 +1,4 @@
-// qmm_mmv.hip -- the product for one to eight tokens (decode steps, speculative
+// qmm_mmv.hip -- the product for one to sixteen tokens (decode steps, speculative
 // tokens, small batches), straight from the activations:
 //
 //   out[t][j] = epilogue( sum over 32-blocks of weight block j x q8 block of x[t] )
@@ -11,15 +11,15 @@
 // 0.8203 per q6_K weight, where the MMQ's planes have 1.25 and 2.02) and every
 // byte is read once, straight into registers, 16 code bytes per lane.
 //
-// The dots run on the matrix core although at most 8 of its 16 token rows could be
-// filled: on the vector ALU the 4-element dots of 8 tokens alone cost 64 cycles
-// per 16 rows and 32 weights, four times the memory's pace (32000 x 4096 q6_K, 8
-// tokens: 58 us, 57% of them issuing vector instructions).  The spare token rows
-// do a second job.  A scale applies to 16 (q6_K) or 32 (q4_K) weights, while one
-// MFMA sums 64; so the activations are laid out block-diagonally: token rows
-// 0.. see one scale group's activations and zeros elsewhere, the next token rows
-// the next group's.  One 16x16x64 MFMA of 16 weight rows then gives the separate
-// dots of four groups for up to four tokens, or of two for up to eight.
+// The dots run on the matrix core although few of its 16 token rows are filled: on
+// the vector ALU the 4-element dots of 8 tokens alone cost 64 cycles per 16 rows
+// and 32 weights, four times the memory's pace (32000 x 4096 q6_K, 8 tokens: 58 us,
+// 57% of them issuing vector instructions).  The spare token rows do a second job.
+// A scale applies to 16 (q6_K) or 32 (q4_K) weights, while one MFMA sums 64; so the
+// activations are laid out block-diagonally: token rows 0.. see one scale group's
+// activations and zeros elsewhere, the next token rows the next group's.  One
+// 16x16x64 MFMA of 16 weight rows then gives the separate dots of four groups for
+// up to four tokens, of two for up to eight, of one for up to sixteen.
 #include "qmm_internal.h"
 #include "qmm_common.h"
 #include "qmm_epilogue.h"
@@ -153,21 +153,27 @@ hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t 
 // 16 bytes), B the weights (row n of the tile: lane & 15, the same k groups: the
 // four byte groups of a half block).  Lane (n, G) of the result holds token rows
 // m = 4G .. 4G + 3 of weight row n:
-//   up to 4 tokens (WIDE false): m = 4*group + token: lane group G has tokens 0..3
-//     of byte group G;
-//   up to 8 (WIDE): m = 8*half + token.  q4_K: the halves are the two 32-blocks of
-//     the half block (byte groups 0, 1 and 2, 3); q6_K: two byte groups, and a
-//     second MFMA with the other two.
-// A lane's scales are those of its own row n, and of its own byte group or pair.
+//   TOK = 4 (up to 4 tokens): m = 4*group + token: lane group G has tokens 0..3 of
+//     byte group G;
+//   TOK = 8: m = 8*half + token.  q4_K: the halves are the two 32-blocks of the half
+//     block (byte groups 0, 1 and 2, 3); q6_K: two byte groups, and a second MFMA
+//     with the other two;
+//   TOK = 16: m = token, an MFMA per 32-block (q4_K) or byte group (q6_K).
+// A lane's scales are those of its own row n.
 // ---------------------------------------------------------------------------
 namespace {
 
 constexpr int kWaves = 16;
 
 // LDS per super-block: codes [h][nibble][g][token][16], n_tok tokens; then f32 dh
-// [32-block][8 tokens] and for q4_K s [32-block][8 tokens].
-template <bool Q6>
-constexpr int kScaleBytes = Q6 ? 256 : 512;
+// [32-block][token] and for q4_K s [32-block][token], for kSlots tokens.
+template <int TOK>
+constexpr int kSlots = TOK == 16 ? 16 : 8;
+template <bool Q6, int TOK>
+constexpr int kScaleBytes = (Q6 ? 1 : 2) * 8 * kSlots<TOK> * 4;
+// MFMAs per 64 weights of a row.
+template <bool Q6, int TOK>
+constexpr int kPasses = Q6 ? (TOK == 16 ? 4 : TOK == 8 ? 2 : 1) : (TOK == 16 ? 2 : 1);
 
 struct MvArgs {
   RowPlanes w;
@@ -223,12 +229,12 @@ __device__ __forceinline__ void add_min(float (&acc)[4], float f, const float4& 
   acc[3] = fmaf(s.w, f, acc[3]);
 }
 
-// One super-block of q4_K.  codes(h, nibble): the A operand; dh, s: the f32 scales
-// of four of the lane's tokens, of 32-block c at [8c].
-template <bool WIDE, class Codes>
+// One super-block of q4_K.  codes(h, nibble, pass): the A operand; dh, s: the f32
+// scales of four of the lane's tokens, of 32-block c at [c*kSlots].
+template <int TOK, class Codes>
 __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[4], int G, Codes&& codes,
                                           const float* dh, const float* s) {
-  const bool second = G >= 2;  // the lane's pair of 32-blocks in a half block
+  constexpr int kS = kSlots<TOK>;
   const float d = f16_bits_to_float(__builtin_amdgcn_perm(w.head.y, w.head.x, 0x0C0C0703u));
   const float m = -f16_bits_to_float(__builtin_amdgcn_perm(w.head.w, w.head.z, 0x0C0C0703u));
 #pragma unroll
@@ -240,23 +246,27 @@ __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[4], 
       lo[i] = (int)(c[i] & 0x0F0F0F0Fu);
       hi[i] = (int)((c[i] >> 4) & 0x0F0F0F0Fu);
     }
-    const uint32_t f = h == 0 ? (second ? w.head.y : w.head.x) : (second ? w.head.w : w.head.z);
-    const float* const dhp = dh + 32 * h + (second ? 16 : 0);
-    const float* const sp = s + 32 * h + (second ? 16 : 0);
-    add_dots(acc, mfma(codes(h, 0), lo), d * (float)(f & 63), *(const float4*)dhp);
-    add_dots(acc, mfma(codes(h, 1), hi), d * (float)((f >> 12) & 63), *(const float4*)(dhp + 8));
-    if (WIDE) {
-      add_min(acc, m * (float)((f >> 6) & 63), *(const float4*)sp);
-      add_min(acc, m * (float)((f >> 18) & 63), *(const float4*)(sp + 8));
-    } else {  // two lane groups share the pair: each adds one block's min term
-      add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), *(const float4*)(sp + (G & 1 ? 8 : 0)));
+#pragma unroll
+    for (int k = 0; k < kPasses<false, TOK>; ++k) {
+      const int pair = TOK == 16 ? k : G >> 1;  // of 32-blocks: 4h + 2*pair and the next
+      const uint32_t f = h == 0 ? (pair ? w.head.y : w.head.x) : (pair ? w.head.w : w.head.z);
+      const float* const dhp = dh + kS * (4 * h + 2 * pair);
+      const float* const sp = s + kS * (4 * h + 2 * pair);
+      add_dots(acc, mfma(codes(h, 0, k), lo), d * (float)(f & 63), *(const float4*)dhp);
+      add_dots(acc, mfma(codes(h, 1, k), hi), d * (float)((f >> 12) & 63), *(const float4*)(dhp + kS));
+      if (TOK == 4) {  // two lane groups share the pair: each adds one block's min term
+        add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), *(const float4*)(sp + (G & 1 ? kS : 0)));
+      } else {
+        add_min(acc, m * (float)((f >> 6) & 63), *(const float4*)sp);
+        add_min(acc, m * (float)((f >> 18) & 63), *(const float4*)(sp + kS));
+      }
     }
   }
 }
 
 // One super-block of q6_K.  A code as four times (code - 32): its six bits, the top
 // one inverted, in a byte's upper bits are that as an int8; the 4 is taken off d.
-template <bool WIDE, class Codes>
+template <int TOK, class Codes>
 __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[4], int G, Codes&& codes,
                                           const float* dh, const float*) {
   const float d = 0.25f * f16_bits_to_float(w.d), d128 = -128.0f * d;
@@ -273,18 +283,13 @@ __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[4], i
     const uint32_t sc[2] = {h ? w.scales.z : w.scales.x, h ? w.scales.w : w.scales.y};
 #pragma unroll
     for (int nib = 0; nib < 2; ++nib) {
-      // byte group g is 16-group 2*(32-block) + g%2, of 32-block 4h + 2*nib + g/2
-      if (WIDE) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t u = (sc[nib] >> (8 * (G >> 1) + 16 * k)) & 255;
-          add_dots(acc, mfma(codes(h, nib, k), b[nib]), fmaf(d, (float)u, d128),
-                   *(const float4*)(dh + 8 * (4 * h + 2 * nib + k)));
-        }
-      } else {
-        const uint32_t u = (sc[nib] >> (8 * G)) & 255;
-        add_dots(acc, mfma(codes(h, nib), b[nib]), fmaf(d, (float)u, d128),
-                 *(const float4*)(dh + 8 * (4 * h + 2 * nib) + 8 * (G >> 1)));
+      for (int k = 0; k < kPasses<true, TOK>; ++k) {
+        // byte group g: 16-group 8h + 4*nib + g, in 32-block 4h + 2*nib + g/2
+        const int g = TOK == 16 ? k : TOK == 8 ? 2 * k + (G >> 1) : G;
+        const uint32_t u = (sc[nib] >> (8 * g)) & 255;
+        add_dots(acc, mfma(codes(h, nib, k), b[nib]), fmaf(d, (float)u, d128),
+                 *(const float4*)(dh + kSlots<TOK> * (4 * h + 2 * nib + (g >> 1))));
       }
     }
   }
@@ -297,18 +302,18 @@ __device__ __forceinline__ uint8_t* place(uint8_t* lds, int sb_bytes, int n_tok,
   const int h = c >> 2, nib = Q6 ? (c >> 1) & 1 : c & 1, g = 2 * (Q6 ? c & 1 : (c >> 1) & 1) + half16;
   return lds + (k >> 5) * sb_bytes + (((2 * h + nib) * 4 + g) * n_tok + t) * 16 + (k & 1) * 8;
 }
-template <bool Q6>
+template <bool Q6, int TOK>
 __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int n_tok, int t, int k, uint32_t pair) {
-  float* const s = (float*)(lds + (k >> 5) * sb_bytes + 256 * n_tok) + 8 * ((k >> 2) & 7) + t;
+  float* const s = (float*)(lds + (k >> 5) * sb_bytes + 256 * n_tok) + kSlots<TOK> * ((k >> 2) & 7) + t;
   s[0] = f16_bits_to_float(pair & 0xFFFF);
-  if (!Q6) s[64] = f16_bits_to_float(pair >> 16);
+  if (!Q6) s[8 * kSlots<TOK>] = f16_bits_to_float(pair >> 16);
 }
 
 // The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
 // numbers: eight per thread, four threads per 32-block, the next eight loaded
 // while these are quantized; begin() loads the first ones, so that the caller can
 // put other loads behind them.
-template <bool Q6, int XT>
+template <bool Q6, int TOK, int XT>
 struct Quantizer {
   float4 v0, v1;
   int t, k, per_tok, dt, dk;
@@ -340,15 +345,15 @@ struct Quantizer {
       fetch(a, sb0);
       const Q8Oct r = quant_oct(c0, c1);
       *(uint2*)place<Q6>(lds, sb_bytes, a.n_tok, tok, at) = make_uint2(r.codes[0], r.codes[1]);
-      if ((at & 3) == 0) place_scales<Q6>(lds, sb_bytes, a.n_tok, tok, at, r.pair);
+      if ((at & 3) == 0) place_scales<Q6, TOK>(lds, sb_bytes, a.n_tok, tok, at, r.pair);
     }
   }
 };
 
-// From a qact buffer (one token block: n_tok <= 8): 16 codes, half a 32-block, per
-// thread, in a slot per token (1, 2, 4 or 8 of them).
-template <bool Q6>
-struct Quantizer<Q6, QMM_Q8> {
+// From a qact buffer (one block of 32 tokens): 16 codes, half a 32-block, per thread,
+// in a slot per token (1, 2, 4, 8 or 16 of them).
+template <bool Q6, int TOK>
+struct Quantizer<Q6, TOK, QMM_Q8> {
   uint4 codes;
   uint32_t pair;
   int t, half, halves, slots;
@@ -361,7 +366,7 @@ struct Quantizer<Q6, QMM_Q8> {
     }
   }
   __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
-    const int bits = a.n_tok > 4 ? 3 : a.n_tok > 2 ? 2 : a.n_tok > 1 ? 1 : 0;
+    const int bits = a.n_tok > 8 ? 4 : a.n_tok > 4 ? 3 : a.n_tok > 2 ? 2 : a.n_tok > 1 ? 1 : 0;
     slots = 1 << bits;
     t = threadIdx.x & (slots - 1);
     half = threadIdx.x >> bits;
@@ -377,22 +382,28 @@ struct Quantizer<Q6, QMM_Q8> {
       fetch(a, sb0);
       if (t < a.n_tok) {
         *(uint4*)place<Q6>(lds, sb_bytes, a.n_tok, t, at) = c;
-        if ((at & 2) == 0) place_scales<Q6>(lds, sb_bytes, a.n_tok, t, at, pr);
+        if ((at & 2) == 0) place_scales<Q6, TOK>(lds, sb_bytes, a.n_tok, t, at, pr);
       }
     }
   }
 };
 
-template <bool Q6, bool WIDE, int XT>
+// The sum over both halves of the wave of a in the lower half, of b in the upper.
+__device__ __forceinline__ float halves_sum(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                                                  false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+template <bool Q6, int TOK, int XT>
 __global__ void __launch_bounds__(64 * kWaves)
 mmv_kernel(MvArgs a, Epilogue ep) {
-  constexpr int kTok = WIDE ? 8 : 4;
   extern __shared__ uint4 lds_raw[];
   uint8_t* const lds = (uint8_t*)lds_raw;
-  const int sb_bytes = 256 * a.n_tok + kScaleBytes<Q6>;
+  const int sb_bytes = 256 * a.n_tok + kScaleBytes<Q6, TOK>;
   // the partial sums [2][wave][token][kTile], and 16 bytes of zeros
   float* const red = (float*)(lds + (size_t)a.tile_sb * sb_bytes);
-  uint4* const zeros = (uint4*)(red + 2 * kWaves * kTok * kTile);
+  uint4* const zeros = (uint4*)(red + 2 * kWaves * TOK * kTile);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rg = wave / a.kg, kg = wave % a.kg, groups = kWaves / a.kg;
@@ -401,7 +412,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   const int m = lane & 15, G = lane >> 4;
 
   // Loads return in order, so the activations' go first.
-  Quantizer<Q6, XT> quant;
+  Quantizer<Q6, TOK, XT> quant;
   quant.begin(a, 0, a.tile_sb);
   // The wave's weights, kAhead super-blocks ahead: super-blocks kg, kg + a.kg, ... of
   // its tile of this step, then of the next step's (past the last step: the last
@@ -423,14 +434,14 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   if (one_tile) quant.run(a, lds, sb_bytes, 0);
   __syncthreads();
 
-  // The lane's A operand: its token's codes of its byte group, or zeros (always
-  // the same ones) where the group is not its row's.  q6_K with eight tokens: for
-  // the MFMA of byte groups 0, 1 and for that of 2, 3.
-  const int tok = WIDE ? m & 7 : m & 3;
-  const bool own = tok < a.n_tok && (WIDE ? (m >> 3) == (Q6 ? G & 1 : G >> 1) : (m >> 2) == G);
+  // The lane's A operand: its token's codes of its byte group G, or zeros (always the
+  // same ones) where G is not what its row sees in the pass.
+  const int tok = m & (TOK - 1);
+  const bool own = tok < a.n_tok && (TOK == 16 || (TOK == 8 ? (m >> 3) == (Q6 ? G & 1 : G >> 1) : (m >> 2) == G));
+  const int pass = Q6 && TOK == 16 ? G : G >> 1;  // the lane's, of several
   const uint32_t at = (uint32_t)(G * a.n_tok + tok) * 16, step_nib = (uint32_t)a.n_tok * 64;
   const uint32_t zero_at = (uint32_t)((uint8_t*)zeros - lds);
-  const float* const scales = (const float*)(lds + 256 * a.n_tok) + (WIDE ? 4 * (G & 1) : 0);
+  const float* const scales = (const float*)(lds + 256 * a.n_tok) + (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
   // The thread that finishes four rows of a token: of which wave group's tile
   const int per_group = 4 * a.n_tok;
   const int e_group = (int)threadIdx.x / per_group, e_at = (int)threadIdx.x - e_group * per_group;
@@ -458,39 +469,39 @@ mmv_kernel(MvArgs a, Epilogue ep) {
         fetch(ahead[kAhead - 1]);
         const uint32_t base = (uint32_t)(sb * sb_bytes);
         const float* const dh = (const float*)((const uint8_t*)scales + base);
-        auto codes = [&](int h, int nib, int k = 0) __attribute__((always_inline)) {
-          const bool live = Q6 && WIDE ? own && (G >> 1) == k : own;
+        auto codes = [&](int h, int nib, int k) __attribute__((always_inline)) {
+          const bool live = kPasses<Q6, TOK> > 1 ? own && pass == k : own;
           return *(const v4i*)(lds + (live ? base + at + (uint32_t)(2 * h + nib) * step_nib : zero_at));
         };
-        add_block<WIDE>(w, acc, G, codes, dh, dh + 64);
+        add_block<TOK>(w, acc, G, codes, dh, dh + 8 * kSlots<TOK>);
       }
     }
-    // the lane groups' sums; then lane (n, G) holds one token's (two if WIDE)
-    const auto s01 = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, acc[0]),
-                                                      __builtin_bit_cast(uint32_t, acc[1]), false, false);
-    const auto s23 = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, acc[2]),
-                                                      __builtin_bit_cast(uint32_t, acc[3]), false, false);
-    const float x = __builtin_bit_cast(float, (uint32_t)s01[0]) + __builtin_bit_cast(float, (uint32_t)s01[1]);
-    const float y = __builtin_bit_cast(float, (uint32_t)s23[0]) + __builtin_bit_cast(float, (uint32_t)s23[1]);
-    float* const out = red + ((size_t)buf * kWaves + wave) * (kTok * kTile);
-    if (WIDE) {  // lower half of the wave: tokens 4*(G&1) and + 2, upper: + 1 and + 3
-      const int t0 = 4 * (G & 1) + (G >> 1);
-      out[t0 * kTile + m] = x;
-      out[(t0 + 2) * kTile + m] = y;
-    } else {  // the odd rows of 16 of x and the even ones of y change places
-      const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
-                                                      __builtin_bit_cast(uint32_t, y), false, false);
-      out[((G >> 1) + 2 * (G & 1)) * kTile + m] =
-          __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+    // the sums of the lane groups that share tokens, into [token][row]
+    float* const out = red + ((size_t)buf * kWaves + wave) * (TOK * kTile) + m;
+    if constexpr (TOK == 16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[(4 * G + i) * kTile] = acc[i];
+    } else {
+      const float x = halves_sum(acc[0], acc[1]), y = halves_sum(acc[2], acc[3]);
+      if constexpr (TOK == 8) {  // lower half of the wave: tokens 4*(G&1) and + 2, upper: + 1 and + 3
+        const int t0 = 4 * (G & 1) + (G >> 1);
+        out[t0 * kTile] = x;
+        out[(t0 + 2) * kTile] = y;
+      } else {  // the odd rows of 16 lanes of x and the even ones of y change places
+        const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                        __builtin_bit_cast(uint32_t, y), false, false);
+        out[((G >> 1) + 2 * (G & 1)) * kTile] =
+            __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+      }
     }
     __syncthreads();
     // two buffers: the next step's sums do not overwrite these, the one after has
     // passed the next barrier
     if (left > 0) {
-      const float* p = red + ((size_t)buf * kWaves + e_group * a.kg) * (kTok * kTile) + e_tok * kTile + e_row;
+      const float* p = red + ((size_t)buf * kWaves + e_group * a.kg) * (TOK * kTile) + e_tok * kTile + e_row;
       float4 f = *(const float4*)p;
       for (int k = 1; k < a.kg; ++k) {
-        const float4 e = *(const float4*)(p + (size_t)k * (kTok * kTile));
+        const float4 e = *(const float4*)(p + (size_t)k * (TOK * kTile));
         f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
       }
       put(ep, finish(ep, f, side), e_tok, row, left);
@@ -498,14 +509,14 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   }
 }
 
-template <bool Q6, bool WIDE, int XT>
+template <bool Q6, int TOK, int XT>
 hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipStream_t s) {
   MvArgs a = in;
   // LDS: the whole inner dimension where it fits the CU's 160 KB, else parts of it,
   // quantized again for every set of row tiles
   constexpr size_t kMost = 160 * 1024;
-  constexpr size_t kRed = (size_t)2 * kWaves * (WIDE ? 8 : 4) * kTile * sizeof(float) + 16;
-  const size_t per_sb = (size_t)256 * a.n_tok + kScaleBytes<Q6>;
+  constexpr size_t kRed = (size_t)2 * kWaves * TOK * kTile * sizeof(float) + 16;
+  const size_t per_sb = (size_t)256 * a.n_tok + kScaleBytes<Q6, TOK>;
   a.tile_sb = (int)std::min<size_t>(a.nsb, (kMost - kRed) / per_sb);
   if (a.tile_sb < a.nsb) a.tile_sb = a.tile_sb / kWaves * kWaves;  // a wave's super-blocks go on across parts
   const size_t lds = a.tile_sb * per_sb + kRed;
@@ -525,20 +536,27 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   }
   const int grid = (int)std::min<int64_t>(a.steps, num_cus);
   if (lds > 64 * 1024) {
-    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, WIDE, XT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, TOK, XT>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)lds);
     if (e != hipSuccess) return e;
   }
-  mmv_kernel<Q6, WIDE, XT><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
+  mmv_kernel<Q6, TOK, XT><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
   return hipGetLastError();
 }
 
-template <bool Q6, bool WIDE>
+template <bool Q6, int TOK>
 hipError_t launch_typed(const MvArgs& a, const Epilogue& ep, int num_cus, hipStream_t s) {
-  return a.x_type == QMM_F32    ? launch_kernel<Q6, WIDE, QMM_F32>(a, ep, num_cus, s)
-         : a.x_type == QMM_F16  ? launch_kernel<Q6, WIDE, QMM_F16>(a, ep, num_cus, s)
-         : a.x_type == QMM_BF16 ? launch_kernel<Q6, WIDE, QMM_BF16>(a, ep, num_cus, s)
-                                : launch_kernel<Q6, WIDE, QMM_Q8>(a, ep, num_cus, s);
+  return a.x_type == QMM_F32    ? launch_kernel<Q6, TOK, QMM_F32>(a, ep, num_cus, s)
+         : a.x_type == QMM_F16  ? launch_kernel<Q6, TOK, QMM_F16>(a, ep, num_cus, s)
+         : a.x_type == QMM_BF16 ? launch_kernel<Q6, TOK, QMM_BF16>(a, ep, num_cus, s)
+                                : launch_kernel<Q6, TOK, QMM_Q8>(a, ep, num_cus, s);
+}
+
+template <bool Q6>
+hipError_t launch_tokens(const MvArgs& a, const Epilogue& ep, int num_cus, hipStream_t s) {
+  return a.n_tok > 8   ? launch_typed<Q6, 16>(a, ep, num_cus, s)
+         : a.n_tok > 4 ? launch_typed<Q6, 8>(a, ep, num_cus, s)
+                       : launch_typed<Q6, 4>(a, ep, num_cus, s);
 }
 
 }  // namespace
@@ -553,9 +571,7 @@ hipError_t launch_mmv(const Planes& p, const void* x, int x_type, int64_t x_stri
   a.n_tok = n_tok;
   a.od = (int)p.od;
   a.nsb = (int)p.nsb;
-  if (p.type == QMM_Q6_K_ROWS)
-    return n_tok > 4 ? launch_typed<true, true>(a, ep, num_cus, s) : launch_typed<true, false>(a, ep, num_cus, s);
-  return n_tok > 4 ? launch_typed<false, true>(a, ep, num_cus, s) : launch_typed<false, false>(a, ep, num_cus, s);
+  return p.type == QMM_Q6_K_ROWS ? launch_tokens<true>(a, ep, num_cus, s) : launch_tokens<false>(a, ep, num_cus, s);
 }
 
 }  // namespace qmm

@@ -32,7 +32,7 @@ def test_refusals_that_need_no_handle():
         ep = qmm.Epilogue(**{"scale": 1.0, **kw})
         return L.qmm_mmv(None, x_ptr, x_type, x_stride, n_tok, ctypes.byref(ep), out_type, o, 16, None)
 
-    for change, word in (({"n_tok": -1}, "n_tok"), ({"n_tok": 9}, "n_tok"), ({"x_type": 4}, "x_type"), ({"x_type": 3, "x_ptr": x + 8}, "aligned"), ({"x_ptr": None}, "x is"),
+    for change, word in (({"n_tok": -1}, "n_tok"), ({"n_tok": 17}, "n_tok"), ({"x_type": 4}, "x_type"), ({"x_type": 3, "x_ptr": x + 8}, "aligned"), ({"x_ptr": None}, "x is"),
                          ({"x_ptr": x + 8}, "aligned"), ({"x_ptr": x + 4, "x_type": 1}, "aligned"),
                          ({"x_stride": 514}, "aligned"), ({"out_type": 3}, "out_type"), ({"act": 7}, "act"),
                          ({"scale": float("inf")}, "finite"), ({}, "handle")):
@@ -121,15 +121,13 @@ SHAPES = [(1, 256), (3, 768), (64, 512), (131, 2048), (1030, 4096), (257, 11008)
 @pytest.mark.parametrize("od,id_", SHAPES)
 def test_mmv_against_oracle_and_formula(device, type_, od, id_):  # noqa: F811
     print(f"mmv {synth.TYPE_NAMES[type_]} {od}x{id_}", flush=True)
-    for n_tok in (1, 2, 3, 4, 5, 6, 7, 8):
-        xt = TYPES[n_tok % 3]
-        raw, x = synth.case(type_, od, id_, n_tok, seed=od + n_tok, outliers=n_tok % 2 == 0)
-        x = torch.from_numpy(x).to(device).to(xt)
-        if n_tok in (1, 5):
-            w = qmm.register_weights(ROWS[type_], od, id_, raw)
-            kept = raw
+    raw = synth.weights(np.random.default_rng(od), type_, od, id_)
+    w = qmm.register_weights(ROWS[type_], od, id_, raw)
+    for n_tok in (1, 2, 3, 4, 5, 6, 7, 8, 9, 13, 16):
+        x = synth.activations(np.random.default_rng(n_tok), n_tok, id_, outliers=n_tok % 2 == 0)
+        x = torch.from_numpy(x).to(device).to(TYPES[n_tok % 3])
         got = qmm.mmv(w, x)
-        sums_ok(got, kept, type_, od, id_, x)
+        sums_ok(got, raw, type_, od, id_, x)
         assert torch.equal(got, qmm.mmv(w, x)), "a repeat differs"
         qact = qmm.quantize_activations(x.float())
         assert torch.equal(got, qmm.mmv(w, qact, n_tok)), "from its q8 blocks it differs"
@@ -139,13 +137,14 @@ def test_mmv_against_oracle_and_formula(device, type_, od, id_):  # noqa: F811
             check(qmm.mmv(w, x, dtype=TYPES[(i + n_tok) % 3], **ep), got, ep)
             ep = {("bias", "mul", "residual")[i % 3]: c[("bias", "mul", "residual")[i % 3]], "act": act}
             check(qmm.mmv(w, x, **ep), got, ep)
+    w.release()
 
 
 @gpu
 @pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K], ids=["q4_K", "q6_K"])
 def test_longest_rows_in_tiles(device, type_):  # noqa: F811
     """Rows whose activations do not fit the LDS at once: the inner dimension in tiles, the last one short."""
-    for od, id_, n_tok in ((6, 1 << 20, 1), (37, 256 * 131, 8), (300, 256 * 61, 8)):
+    for od, id_, n_tok in ((6, 1 << 20, 1), (37, 256 * 131, 8), (300, 256 * 61, 8), (50, 256 * 43, 16), (33, 256 * 29, 11)):
         raw, x = synth.case(type_, od, id_, n_tok, seed=od)
         w = qmm.register_weights(ROWS[type_], od, id_, raw)
         x = torch.from_numpy(x).to(device)
@@ -280,7 +279,7 @@ def test_mmv_refusals_with_a_handle(device):  # noqa: F811
     assert e.value.code == qmm.EINVAL
     with pytest.raises(qmm.QmmError):
         qmm.mmq_epilogue(w, qmm.quantize_activations(x), T)
-    refused(xx=torch.zeros(9, id_, device=device))
+    refused(xx=torch.zeros(17, id_, device=device))
     refused(xx=x[:, :256])
     refused(xx=x.double())
     refused(xx=x.cpu())
