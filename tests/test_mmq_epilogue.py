@@ -340,3 +340,26 @@ def test_refusals_with_a_handle(device):
     assert wide(*args) == qmm.EINVAL and "out" in qmm.last_error()
     assert qmm.mmq_epilogue(w, torch.empty(0, dtype=torch.uint8, device=device), 0).shape == (0, od)
     w.release()
+
+
+@gpu
+def test_outputs_past_32_bits(device):
+    """Outputs of more than 2^32 elements (f16, in place of the residual) and of more than 2^32 bytes of q8
+    blocks: the last tokens equal a call with only them."""
+    od, id_, T, last = 1 << 20, 256, 4200, 130
+    raw, x = synth.case(synth.Q4_K, od, id_, T, seed=3)
+    w = qmm.register_weights(synth.Q4_K_PACKED, od, id_, raw)
+    x = torch.from_numpy(x).to(device)
+    qact, tail = qmm.quantize_activations(x), qmm.quantize_activations(x[-last:].contiguous())
+    out = torch.zeros((T, od), dtype=torch.float16, device=device)
+    out[-last:] = 0.5
+    want = qmm.mmq_epilogue(w, tail, last, dtype=torch.float16, act="relu", residual=out[-last:].clone())
+    qmm.mmq_epilogue(w, qact, T, act="relu", residual=out, out=out)
+    assert torch.equal(out[-last:], want)
+    del out, want
+    q8 = qmm.mmq_epilogue(w, qact, T, dtype="q8", scale=0.125)
+    assert q8.numel() > 1 << 32
+    want = qmm.dequantize_activations(qmm.mmq_epilogue(w, tail, last, dtype="q8", scale=0.125), last, od, torch.float16)
+    got = qmm.dequantize_activations(q8, T, od, torch.float16)
+    assert torch.equal(got[-last:], want)
+    w.release()

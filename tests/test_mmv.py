@@ -298,3 +298,51 @@ def test_mmv_refusals_with_a_handle(device):  # noqa: F811
     assert qmm.mmv(w, x[:0]).shape == (0, od)
     w.release()
     wm.release()
+
+
+@gpu
+def test_largest_matrices(device):  # noqa: F811
+    """The most rows the ABI takes (the last ones against the oracle), and a wide row with sixteen tokens whose
+    LDS is past 64 KiB, captured into a graph."""
+    od, id_, T = 1 << 21, 256, 2
+    raw, x = synth.case(synth.Q6_K, od, id_, T, seed=5)
+    w = qmm.register_weights(qmm.Q6_K_ROWS, od, id_, raw)
+    x = torch.from_numpy(x).to(device)
+    got = qmm.mmv(w, x, dtype=torch.float32)
+    for lo in (0, od - 100):
+        sums_ok(got[:, lo:lo + 100], raw[lo * 210:(lo + 100) * 210], synth.Q6_K, 100, id_, x)
+    w.release()
+    raw, x = synth.case(synth.Q4_K, 600, 5120, 16, seed=6)
+    w = qmm.register_weights(qmm.Q4_K_ROWS, 600, 5120, raw)
+    x = torch.from_numpy(x).to(device)
+    want = qmm.mmv(w, x)
+    sums_ok(want, raw, synth.Q4_K, 600, 5120, x)
+    out = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qmm.mmv(w, x, out=out)
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    del graph
+    w.release()
+
+
+@gpu
+def test_infinities_and_nan_stay_in_their_token(device):  # noqa: F811
+    """Values outside the q8 range are not specified, but they do not reach the other tokens of the call."""
+    for type_ in (synth.Q4_K, synth.Q6_K):
+        for T in (3, 7, 12):
+            raw, x = synth.case(type_, 100, 768, T, seed=T)
+            w = qmm.register_weights(ROWS[type_], 100, 768, raw)
+            x = torch.from_numpy(x).to(device)
+            ref = qmm.mmv(w, x)
+            bad = x.clone()
+            bad[1, 5], bad[1, 700], bad[2, 300] = float("nan"), float("inf"), 1e30
+            got = qmm.mmv(w, bad)
+            keep = [t for t in range(T) if t not in (1, 2)]
+            assert torch.equal(got[keep], ref[keep])
+            w.release()
