@@ -435,7 +435,7 @@ int qmm_mmq_epilogue(const qmm_weights *w, const void *qact, size_t qact_bytes, 
  *               qmm_norm_quantize and qmm_quantize_activations write it, and
  *               x_stride its qmm_qact_bytes(n_tok, id) bytes; the same results
  *               as from the numbers it was made of
- *   ep, out_type, out, out_stride  as for qmm_mmq_epilogue, without QMM_Q8
+ *   ep, out_type, out, out_stride  as for qmm_mmq_epilogue
  * No workspace; can be captured into a graph.  Deterministic; a token's result
  * may depend in its last bits on how many tokens the call has.
  * Errors: QMM_EINVAL, QMM_ESHAPE (a qact of another size), QMM_EHIP.  n_tok == 0 is

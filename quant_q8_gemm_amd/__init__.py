@@ -34,7 +34,7 @@ if not os.path.exists(LIB_PATH):
 # One HIP runtime per process: PyTorch ships its own libamdhip64 under the same
 # soname.  Loading torch first makes libqmm bind to that runtime; loading libqmm
 # first would pull in a second runtime that cannot see the device.
-import torch  # noqa: E402,F401
+import torch  # noqa: E402
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -155,7 +155,6 @@ def _check(rc: int) -> None:
 
 
 def _check_qact(qact) -> None:
-    import torch
     if qact.dtype != torch.uint8 or not qact.is_cuda or qact.dim() != 1 or not qact.is_contiguous():
         raise QmmError(EINVAL, "qact must be a contiguous one-dimensional cuda uint8 tensor")
 
@@ -231,24 +230,20 @@ def register_weights(type_: int, od: int, id_: int, raw, stream=None) -> Weights
 
 def quantize_activations(x, qact=None, stream=None):
     """x: cuda float32 [n_tok][id] contiguous -> qact (cuda uint8, qact_bytes)."""
-    import torch
     if x.dtype != torch.float32 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise QmmError(EINVAL, "x must be a contiguous cuda float32 [n_tok][id] tensor")
     n_tok, id_ = x.shape
-    nb = qact_bytes(n_tok, id_)
     if qact is None:
+        nb = qact_bytes(n_tok, id_)
         if nb == 0 and n_tok != 0:
             raise QmmError(EINVAL, f"bad shape n_tok={n_tok} id={id_}")
-        qact = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        qact = torch.empty_strided((nb,), (1,), dtype=torch.uint8, device=x.device)
     _check_qact(qact)
-    _check(_lib.qmm_quantize_activations(ctypes.c_void_p(x.data_ptr()), n_tok, id_,
-                                         ctypes.c_void_p(qact.data_ptr()), qact.numel(),
-                                         _stream(stream)))
+    _check(_lib.qmm_quantize_activations(x.data_ptr(), n_tok, id_, qact.data_ptr(), qact.numel(), _stream(stream)))
     return qact
 
 
 def _mmq_args(w: Weights, qact, n_tok: int, out):
-    import torch
     _check_qact(qact)
     if out is None:
         out = torch.empty((n_tok, w.od), dtype=torch.float32, device=qact.device)
@@ -490,7 +485,8 @@ def mmv(w: Weights, x, n_tok: int = None, *, bias=None, act: str = "none", mul=N
         scale * mul * act(x @ W^T + bias) + residual_scale * residual
 
     w: a handle of Q4_K_ROWS or Q6_K_ROWS; x: [n_tok][id] of float32, float16 or bfloat16 (rows may be strided), or
-    the qact buffer of n_tok tokens.  The result is [n_tok][od] of `dtype`, or `out`."""
+    the qact buffer of n_tok tokens.  The result is [n_tok][od] of `dtype`, or its qact buffer with dtype "q8" (od %
+    256 == 0), or `out`."""
     device = _current(x, "x")
     if n_tok is not None:
         x_type, (x_ptr, x_stride) = Q8, _bytes(x, "x", device)
@@ -501,7 +497,11 @@ def mmv(w: Weights, x, n_tok: int = None, *, bias=None, act: str = "none", mul=N
         raise QmmError(EINVAL, "x must be [n_tok][id], or a qact buffer with n_tok")
     shape = (n_tok, w.od)
     ep = _epilogue(shape, device, bias, act, mul, residual, scale, residual_scale)
-    if out is None:
+    if dtype == "q8":
+        if out is None:
+            out = _empty(x, (qact_bytes(n_tok, w.od),), torch.uint8, stream)
+        out_type, (out_ptr, out_stride) = Q8, _bytes(out, "out", device)
+    elif out is None:
         out_type = _elem(dtype)
         out = _empty(x, shape, dtype, stream)
         out_ptr, out_stride = out.data_ptr(), w.od

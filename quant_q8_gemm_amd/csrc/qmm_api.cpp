@@ -728,7 +728,6 @@ int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, 
 
 int qmm_mmv(const qmm_weights* w, const void* x, int x_type, int64_t x_stride, int64_t n_tok, const qmm_epilogue* ep,
             int out_type, void* out, int64_t out_stride, void* stream) {
-  if (int rc = check_elem("out_type", out_type)) return rc;
   if (int rc = check_epilogue(ep, out_type)) return rc;
   if (x_type != QMM_Q8)
     if (int rc = check_elem("x_type", x_type)) return rc;

@@ -132,4 +132,19 @@ __device__ __forceinline__ void put(const Epilogue& ep, float4 v, int64_t t, int
   else put_typed<QMM_BF16>(ep.out, v, i, n);
 }
 
+// Into the next product's qact (od/32 chunks): one lane's four codes of rows
+// 32*block + 4*quad .. of token t, and from quad 0 the chunk's (dh, s) pair.
+__device__ __forceinline__ void put_q8(const Epilogue& ep, const Q8Quad& r, int t, int block, int od, int quad) {
+  const int64_t frag = (int64_t)(t >> 5) * (od >> 5) + block;
+  *(uint32_t*)((uint8_t*)ep.out + frag * 1024 + (quad >> 2) * 512 + (t & 31) * 16 + (quad & 3) * 4) = r.codes;
+  if (quad == 0) *(uint32_t*)((uint8_t*)ep.out + ep.t_pad * od + frag * 128 + (t & 31) * 4) = r.pair;
+}
+
+// The zeros of padding token t there: half of its codes, and with half 0 its pair.
+__device__ __forceinline__ void zero_q8(const Epilogue& ep, int t, int block, int od, int half) {
+  const int64_t frag = (int64_t)(t >> 5) * (od >> 5) + block;
+  *(uint4*)((uint8_t*)ep.out + frag * 1024 + half * 512 + (t & 31) * 16) = make_uint4(0, 0, 0, 0);
+  if (half == 0) *(uint32_t*)((uint8_t*)ep.out + ep.t_pad * od + frag * 128 + (t & 31) * 4) = 0;
+}
+
 }  // namespace qmm

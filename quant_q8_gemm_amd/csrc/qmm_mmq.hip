@@ -344,14 +344,6 @@ __device__ __forceinline__ void store_block(float* __restrict__ out, const v16f&
 constexpr int kEpRow = 36;
 constexpr int kEpWave = 32 * kEpRow;  // floats per wave
 
-// four codes and, from the eight lanes' first, the (dh, s) pair of token t, chunk
-// `block` of the next product's qact (od/32 chunks)
-__device__ __forceinline__ void put_q8(const Epilogue& ep, const Q8Quad& r, int t, int block, int od, int quad) {
-  const int64_t frag = (int64_t)(t >> 5) * (od >> 5) + block;
-  *(uint32_t*)((uint8_t*)ep.out + frag * 1024 + (quad >> 2) * 512 + (t & 31) * 16 + (quad & 3) * 4) = r.codes;
-  if (quad == 0) *(uint32_t*)((uint8_t*)ep.out + ep.t_pad * od + frag * 128 + (t & 31) * 4) = r.pair;
-}
-
 __device__ __forceinline__ void finish_block(const Epilogue& ep, const v16f& acc, float* lds, int rblock, int tblock,
                                              int lane, int od, int n_tok) {
 #pragma unroll

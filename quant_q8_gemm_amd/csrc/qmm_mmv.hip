@@ -395,7 +395,9 @@ __device__ __forceinline__ float halves_sum(float a, float b) {
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-template <bool Q6, int TOK, int XT>
+// OUT8: the output is kept as q8 blocks (its code beside the other outputs' cost
+// every call 0.9 us).
+template <bool Q6, int TOK, int XT, bool OUT8>
 __global__ void __launch_bounds__(64 * kWaves)
 mmv_kernel(MvArgs a, Epilogue ep) {
   extern __shared__ uint4 lds_raw[];
@@ -442,17 +444,19 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   const uint32_t at = (uint32_t)(G * a.n_tok + tok) * 16, step_nib = (uint32_t)a.n_tok * 64;
   const uint32_t zero_at = (uint32_t)((uint8_t*)zeros - lds);
   const float* const scales = (const float*)(lds + 256 * a.n_tok) + (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
-  // The thread that finishes four rows of a token: of which wave group's tile
-  const int per_group = 4 * a.n_tok;
-  const int e_group = (int)threadIdx.x / per_group, e_at = (int)threadIdx.x - e_group * per_group;
-  const int e_tok = e_at >> 2, e_row = 4 * (e_at & 3);
+  // The thread that finishes four rows of a token: of which unit, a row tile or, for
+  // a q8 output, a pair of them (a 32-block: eight threads).
+  constexpr int kUnit = OUT8 ? 2 : 1, kQuads = 4 * kUnit;
+  const int units = groups / kUnit, per_unit = kQuads * a.n_tok;
+  const int e_unit = (int)threadIdx.x / per_unit, e_at = (int)threadIdx.x - e_unit * per_unit;
+  const int e_tok = e_at / kQuads, e_quad = e_at % kQuads;
 
   int buf = 0;
   for (int step = blockIdx.x; step < a.steps; step += gridDim.x, buf ^= 1) {
-    const int row = (step * groups + e_group) * kTile + e_row;
-    const int left = e_group < groups ? min(a.od - row, 4) : 0;
+    const int row = (step * groups + e_unit * kUnit) * kTile + 4 * e_quad;
+    const int left = e_unit < units ? min(a.od - row, 4) : 0;
     Sides side = {};
-    if (left > 0) side = load_sides(ep, e_tok, row, left);
+    if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);  // early, where the registers hold them
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int sb0 = 0; sb0 < a.nsb; sb0 += a.tile_sb) {
       const int n = min(a.tile_sb, a.nsb - sb0);
@@ -498,18 +502,28 @@ mmv_kernel(MvArgs a, Epilogue ep) {
     // two buffers: the next step's sums do not overwrite these, the one after has
     // passed the next barrier
     if (left > 0) {
-      const float* p = red + ((size_t)buf * kWaves + e_group * a.kg) * (TOK * kTile) + e_tok * kTile + e_row;
+      const int tile = e_unit * kUnit + (e_quad >> 2);  // of the set
+      const float* p = red + ((size_t)buf * kWaves + tile * a.kg) * (TOK * kTile) + e_tok * kTile + 4 * (e_quad & 3);
       float4 f = *(const float4*)p;
       for (int k = 1; k < a.kg; ++k) {
         const float4 e = *(const float4*)(p + (size_t)k * (TOK * kTile));
         f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
       }
-      put(ep, finish(ep, f, side), e_tok, row, left);
+      f = finish(ep, f, OUT8 ? load_sides(ep, e_tok, row, 4) : side);
+      if constexpr (OUT8)
+        put_q8(ep, quant_quad(f), e_tok, row >> 5, a.od, e_quad);
+      else
+        put(ep, f, e_tok, row, left);
     }
+    if constexpr (OUT8)
+      for (int i = threadIdx.x; i < units * 2 * (int)ep.t_pad; i += 64 * kWaves) {  // the padding tokens' zeros
+        const int t = (i >> 1) & ((int)ep.t_pad - 1), block = step * groups / 2 + i / (2 * (int)ep.t_pad);
+        if (t >= a.n_tok) zero_q8(ep, t, block, a.od, i & 1);
+      }
   }
 }
 
-template <bool Q6, int TOK, int XT>
+template <bool Q6, int TOK, int XT, bool OUT8>
 hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipStream_t s) {
   MvArgs a = in;
   // LDS: the whole inner dimension where it fits the CU's 160 KB, else parts of it,
@@ -524,8 +538,9 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   // row tiles of their own, and the fewest rounds of them, counted in the
   // super-blocks that each wave walks (and half of one for the sums).
   const int64_t tiles = (a.od + kTile - 1) / kTile;
+  const int most = OUT8 ? kWaves / 2 : kWaves;  // q8: row tiles in pairs
   double best = 0;
-  for (int kg = 1; kg <= kWaves && (kg == 1 || kg <= a.nsb); kg *= 2) {
+  for (int kg = 1; kg <= most && (kg == 1 || kg <= a.nsb); kg *= 2) {
     const int64_t steps = (tiles + kWaves / kg - 1) / (kWaves / kg);
     const double cost = (double)((steps + num_cus - 1) / num_cus) * ((a.nsb + kg - 1) / kg + 0.5);
     if (kg == 1 || cost < best) {
@@ -536,20 +551,26 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   }
   const int grid = (int)std::min<int64_t>(a.steps, num_cus);
   if (lds > 64 * 1024) {
-    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, TOK, XT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+    hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, TOK, XT, OUT8>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)lds);
     if (e != hipSuccess) return e;
   }
-  mmv_kernel<Q6, TOK, XT><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
+  mmv_kernel<Q6, TOK, XT, OUT8><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
   return hipGetLastError();
+}
+
+template <bool Q6, int TOK, int XT>
+hipError_t launch_out(const MvArgs& a, const Epilogue& ep, int num_cus, hipStream_t s) {
+  return ep.out_type == QMM_Q8 ? launch_kernel<Q6, TOK, XT, true>(a, ep, num_cus, s)
+                               : launch_kernel<Q6, TOK, XT, false>(a, ep, num_cus, s);
 }
 
 template <bool Q6, int TOK>
 hipError_t launch_typed(const MvArgs& a, const Epilogue& ep, int num_cus, hipStream_t s) {
-  return a.x_type == QMM_F32    ? launch_kernel<Q6, TOK, QMM_F32>(a, ep, num_cus, s)
-         : a.x_type == QMM_F16  ? launch_kernel<Q6, TOK, QMM_F16>(a, ep, num_cus, s)
-         : a.x_type == QMM_BF16 ? launch_kernel<Q6, TOK, QMM_BF16>(a, ep, num_cus, s)
-                                : launch_kernel<Q6, TOK, QMM_Q8>(a, ep, num_cus, s);
+  return a.x_type == QMM_F32    ? launch_out<Q6, TOK, QMM_F32>(a, ep, num_cus, s)
+         : a.x_type == QMM_F16  ? launch_out<Q6, TOK, QMM_F16>(a, ep, num_cus, s)
+         : a.x_type == QMM_BF16 ? launch_out<Q6, TOK, QMM_BF16>(a, ep, num_cus, s)
+                                : launch_out<Q6, TOK, QMM_Q8>(a, ep, num_cus, s);
 }
 
 template <bool Q6>

@@ -92,8 +92,10 @@ def _decode(w, v, h, from_q8):
     a = qmm.norm_quantize(h, v["norm"], h_out=False, normed=not from_q8, qact=from_q8)
     x = (a.qact, T) if from_q8 else (a.normed,)
     g = qmm.mmv(w["gate"], *x, bias=v["bias"], act="silu", dtype=torch.float16)
-    u = qmm.mmv(w["up"], *x, mul=g)
-    y = qmm.mmv(w["down"], u, dtype=torch.float16)
+    if from_q8:  # q8 blocks from the first norm to the down product
+        y = qmm.mmv(w["down"], qmm.mmv(w["up"], *x, mul=g, dtype="q8"), T, dtype=torch.float16)
+    else:
+        y = qmm.mmv(w["down"], qmm.mmv(w["up"], *x, mul=g), dtype=torch.float16)
     return qmm.norm_quantize(h, v["next"], y=y, post_weight=v["post"], gate=v["gate"].half(), residual_scale=0.5,
                              block_scale=0.8, normed=True, qact=False)
 

@@ -17,7 +17,8 @@ torch = pytest.importorskip("torch")
 import oracle  # noqa: E402
 import quant_q8_gemm_amd as qmm  # noqa: E402
 import synth  # noqa: E402
-from tests.test_mmq_epilogue import ACTS, TYPES, U, check, device, sides  # noqa: E402,F401
+from tests import layouts  # noqa: E402
+from tests.test_mmq_epilogue import ACTS, TYPES, U, check, check_q8, device, sides  # noqa: E402,F401
 
 gpu = pytest.mark.gpu
 ROWS = {synth.Q4_K: qmm.Q4_K_ROWS, synth.Q6_K: qmm.Q6_K_ROWS}
@@ -34,7 +35,7 @@ def test_refusals_that_need_no_handle():
 
     for change, word in (({"n_tok": -1}, "n_tok"), ({"n_tok": 17}, "n_tok"), ({"x_type": 4}, "x_type"), ({"x_type": 3, "x_ptr": x + 8}, "aligned"), ({"x_ptr": None}, "x is"),
                          ({"x_ptr": x + 8}, "aligned"), ({"x_ptr": x + 4, "x_type": 1}, "aligned"),
-                         ({"x_stride": 514}, "aligned"), ({"out_type": 3}, "out_type"), ({"act": 7}, "act"),
+                         ({"x_stride": 514}, "aligned"), ({"out_type": 4}, "out_type"), ({"act": 7}, "act"),
                          ({"scale": float("inf")}, "finite"), ({}, "handle")):
         assert call(**change) == qmm.EINVAL, change
         assert word in qmm.last_error(), (change, qmm.last_error())
@@ -137,6 +138,38 @@ def test_mmv_against_oracle_and_formula(device, type_, od, id_):  # noqa: F811
             check(qmm.mmv(w, x, dtype=TYPES[(i + n_tok) % 3], **ep), got, ep)
             ep = {("bias", "mul", "residual")[i % 3]: c[("bias", "mul", "residual")[i % 3]], "act": act}
             check(qmm.mmv(w, x, **ep), got, ep)
+    w.release()
+
+
+@gpu
+@pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K], ids=["q4_K", "q6_K"])
+@pytest.mark.parametrize("od,id_", [(256, 256), (512, 4096), (4096, 2304), (11008, 1024), (20480, 512), (256, 65536)])
+def test_q8_output_is_the_prepass_of_the_values(device, type_, od, id_):  # noqa: F811
+    """The output kept as q8 blocks: the next product's, from one to sixteen tokens, into a buffer that held other
+    bytes; in the same order of sums as the numbers' where both share the waves per row tile."""
+    print(f"mmv q8 {synth.TYPE_NAMES[type_]} {od}x{id_}", flush=True)
+    raw = synth.weights(np.random.default_rng(od), type_, od, id_)
+    w = qmm.register_weights(ROWS[type_], od, id_, raw)
+    for n_tok in (1, 4, 6, 11, 16):
+        x = torch.from_numpy(synth.activations(np.random.default_rng(n_tok), n_tok, id_)).to(device)
+        c = sides(device, n_tok, od, torch.float16, 3)
+        ep = {**c, "act": "silu", "scale": 2.0 ** -8}
+        out = torch.full((qmm.qact_bytes(n_tok, od),), 0x5A, dtype=torch.uint8, device=device)
+        assert qmm.mmv(w, x, dtype="q8", out=out, **ep) is out
+        values = qmm.mmv(w, x, **ep)
+        q, dh, s = layouts.read_qact(out.cpu().numpy(), n_tok, od)
+        assert not q[n_tok:].any() and not dh[n_tok:].any() and not s[n_tok:].any(), "padding not zero"
+        # the blocks' sums are f32 sums in another order where the waves per tile differ: K units of the terms
+        # apart, far less than a step; codes may differ by one next to a border, rarely
+        oq, odh, _ = oracle.quantize(values.cpu().numpy())
+        d, od_ = (v[:n_tok].view(np.float16).astype(np.float64) for v in (dh, odh))
+        assert np.all(np.abs(d - od_) <= 2.0 ** -10 * od_ + 2.0 ** -24)
+        off = q[:n_tok].astype(int) != oq
+        assert np.abs(q[:n_tok].astype(int) - oq).max() <= 1 and off.mean() <= 0.01
+        sums = (d.astype(np.float32) * q[:n_tok].reshape(n_tok, -1, 32).sum(2).astype(np.float32)).astype(np.float16)
+        assert np.array_equal(s[:n_tok], sums.view(np.uint16).reshape(s[:n_tok].shape))
+        if od >= 20480:  # the same waves per tile: bit for bit
+            check_q8(out, values)
     w.release()
 
 
@@ -287,6 +320,7 @@ def test_mmv_refusals_with_a_handle(device):  # noqa: F811
     refused(xx=torch.zeros(T, id_ + 2, device=device)[:, :-2])
     refused(xx=x[:1].expand(T, id_))
     refused(dtype=torch.float64)
+    refused(dtype="q8")                                              # od % 256 != 0
     with pytest.raises(qmm.QmmError) as e:
         qmm.mmv(w, qmm.quantize_activations(x)[:-16], T)
     assert e.value.code == qmm.ESHAPE
