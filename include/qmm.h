@@ -394,7 +394,10 @@ typedef struct {
 /*
  * qmm_mmq_epilogue -- qmm_mmq with an epilogue on its sums, stored in the type
  * and place the next step reads: one kernel instead of the product and an
- * elementwise pass over its output.  The sums are qmm_mmq's, bit for bit.
+ * elementwise pass over its output.  The sums are qmm_mmq's: bit for bit where
+ * its tiled kernel runs, in another order of their f32 additions for few tokens
+ * (up to 32, or a launch that small), which have a kernel of their own.  The same
+ * call gives the same bits.
  *   w, qact, qact_bytes, n_tok, stream  as for qmm_mmq
  *   ep          the epilogue, or NULL: the sums themselves, rounded to out_type
  *   out_type    QMM_F32, QMM_F16 or QMM_BF16: out is device [n_tok] rows of od
@@ -408,7 +411,7 @@ typedef struct {
  *               tokens zero -- the next product's input (|values| <= 2046).
  *   work        device memory for the tail partials (see qmm_mmq), 16-byte
  *               aligned, work_bytes of it, at least the plan's scratch_bytes
- *               (qmm_mmq_plan): the call then allocates nothing and can be
+ *               (qmm_mmq_plan; few tokens need none): the call then allocates nothing and can be
  *               captured, and calls with work memory of their own may overlap.
  *               NULL with work_bytes 0: the stream's scratch, as qmm_mmq; a
  *               captured call that needs scratch is then refused, since graphs

@@ -9,7 +9,7 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-KERNELS = ["qmm_repack.hip", "qmm_prepass.hip", "qmm_norm.hip", "qmm_mmq.hip", "qmm_mmv.hip"]
+KERNELS = ["qmm_repack.hip", "qmm_prepass.hip", "qmm_norm.hip", "qmm_mmq.hip", "qmm_mmq_few.hip", "qmm_mmv.hip"]
 SOURCES = [os.path.join(CSRC, "qmm_api.cpp")] + [os.path.join(CSRC, k) for k in KERNELS]
 LIB = os.path.join(HERE, "libqmm.so")
 # calibration kernels for the benchmark's measured rooflines (not part of the ABI),
@@ -32,9 +32,9 @@ LIB_FLAGS = DEVICE_FLAGS + MAX_ILP
 
 
 def _flags(source: str):
-    """The few-token product keeps the default strategy: it needs its registers for
+    """The few-token kernels keep the default strategy: they need their registers for
     the loads in flight, and max-ILP spills them."""
-    return DEVICE_FLAGS if os.path.basename(source) == "qmm_mmv.hip" else LIB_FLAGS
+    return DEVICE_FLAGS if os.path.basename(source) in ("qmm_mmv.hip", "qmm_mmq_few.hip") else LIB_FLAGS
 
 
 def _hipcc(sources, out: str, verbose: bool, flags, shared: bool = True) -> str:

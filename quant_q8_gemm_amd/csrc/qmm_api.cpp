@@ -703,12 +703,18 @@ int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, 
       if (overlap(own, side)) return refuse_overlap(own, side);
   int device = -1, num_cus = 0;
   if (int rc = current_device(w, &device, &num_cus)) return rc;
+  const hipStream_t s = (hipStream_t)stream;
+  if (qmm::mmq_few_applies(w->p, n_tok, num_cus)) {  // no scratch
+    hipError_t e = qmm::launch_mmq_few(w->p, (const uint8_t*)qact, n_tok, token_pad(n_tok), r, num_cus, s);
+    if (e != hipSuccess) return fail_hip(e, "mmq launch");
+    ok();
+    return QMM_OK;
+  }
   const qmm::MmqPlan plan = qmm::plan_mmq(w->p, n_tok, num_cus);
   if (int rc = check_launch(plan, n_tok, w->p.od, num_cus)) return rc;
   if (work != nullptr && work_bytes < plan.scratch_bytes)
     return fail(QMM_EINVAL, "work_bytes %zu, but this launch needs %zu bytes of tail scratch", work_bytes,
                 plan.scratch_bytes);
-  const hipStream_t s = (hipStream_t)stream;
   void* scratch = work;
   if (scratch == nullptr && plan.scratch_bytes > 0) {
     // a captured launch outlives the stream's turn: two graphs would share its scratch

@@ -1,0 +1,239 @@
+// qmm_mmq_few.hip -- the MMQ with an epilogue for few tokens (short prompts, batches
+// too large for the few-token product on the rows form): one block of 32 tokens
+// per work-group, straight from the MMQ's planes.
+//
+// With so few tokens the planes' bytes bound the product (q4_K 1.25, packed 0.75,
+// q6_K 2.02 bytes per weight), and every weight fragment meets one token block, so
+// that staging it in LDS shares it with nobody.  A wave owns 32 rows and a share of
+// the super-blocks and loads its operands straight into registers, kAhead chunks
+// ahead; the waves of a row block add their sums in LDS, in order, where the tiled
+// MMQ splits a launch this small along the inner dimension into partial tiles that a
+// second kernel adds.  The block dots, scales and their order within a super-block
+// are the tiled MMQ's.
+#include "qmm_internal.h"
+#include "qmm_common.h"
+#include "qmm_epilogue.h"
+#include "qmm_mmq_ops.h"
+
+#include <algorithm>
+
+namespace qmm {
+
+namespace {
+
+constexpr int kWaves = 16;
+
+struct FewArgs {
+  const int8_t* wq;
+  const float* wd;
+  const uint8_t* wsm;
+  const uint8_t* qq;
+  const uint8_t* qs;
+  int nchunk, nsb, od, n_tok;
+  int kg;  // waves that share a row block
+};
+
+// Chunks loaded ahead: what 128 registers hold beside the sums (16 waves x 2 chunks
+// keep 32 to 64 KiB of weights per CU in flight; four chunks spill: 11008 x 4096
+// q4_K, 32 tokens: 17.0 instead of 13.0 us).
+constexpr int kAhead = 2;
+
+// A super-block's scales, mins and d (q6_K: d only).
+template <int TYPE>
+struct Small {
+  v2i sc[2], mins;
+  float d;
+};
+
+template <int TYPE>
+__global__ void __launch_bounds__(64 * kWaves)
+mmq_few_kernel(FewArgs a, Epilogue ep) {
+  using W = WeightOps<TYPE>;
+  constexpr bool kQ4 = is_q4k(TYPE);
+  __shared__ float red[kWaves * kEpWave];
+  __shared__ float dd_all[kWaves][64];  // a super-block's d of 32 rows; q4_K: d*2^25, then -dmin
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave / a.kg, kg = wave % a.kg, groups = kWaves / a.kg;
+  const int rblocks = (a.od + 31) / 32;
+  const int rb = min((int)blockIdx.x * groups + group, rblocks - 1);  // past the last: the last again, not stored
+  const int row = lane & 31;
+  const int tb = blockIdx.y;
+  const int sb0 = kg * a.nsb / a.kg, sb1 = (kg + 1) * a.nsb / a.kg;
+  float* const dd = dd_all[wave];
+
+  const int8_t* const pa = a.wq + (int64_t)rb * a.nchunk * kFragA<TYPE>;
+  const uint8_t* const pb = a.qq + (int64_t)tb * a.nchunk * 1024;
+  const uint8_t* const ps = a.qs + (int64_t)tb * a.nchunk * 128;
+  const uint8_t* const pr = a.wsm + (int64_t)rb * (a.nchunk / 4) * kQ4RecBytes;  // q4_K
+  const float* const pd = a.wd + (int64_t)rb * a.nsb * 32;                        // q6_K
+
+  typename W::A qa[kAhead];
+  v4i qb[kAhead];
+  uint32_t pair[kAhead];
+  const int last = sb1 * 8 - 1;  // the last chunk of the wave's share
+  auto load = [&](int slot, int c) __attribute__((always_inline)) {
+    c = min(c, last);
+    qa[slot] = W::load(pa + (int64_t)c * kFragA<TYPE>, lane);
+    qb[slot] = *(const v4i*)(pb + (int64_t)c * 1024 + lane * 16);
+    pair[slot] = *(const uint32_t*)(ps + (int64_t)c * 128 + (lane & 31) * 4);
+  };
+  auto small = [&](int sb) __attribute__((always_inline)) {
+    Small<TYPE> r{};
+    if constexpr (kQ4) {
+      const uint8_t* const rec = pr + (int64_t)sb * 2 * kQ4RecBytes;
+      r.sc[0] = *(const v2i*)(rec + kQ4RecScOff + row * 8);
+      r.sc[1] = *(const v2i*)(rec + kQ4RecBytes + kQ4RecScOff + row * 8);
+      r.mins = *(const v2i*)(rec + kQ4RecMnOff + lane * 8);
+      r.d = *(const float*)(rec + kQ4RecDOff + lane * 4);
+    } else {
+      r.d = pd[sb * 32 + (lane & 31)];
+    }
+    return r;
+  };
+  Small<TYPE> next{};
+  if (!kQ4) next = small(sb0);  // q6_K's one register a super-block ahead
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i, sb0 * 8 + i);
+
+  float acc[16], inner[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+  const bool lane_hi = lane >= 32;
+  for (int sb = sb0; sb < sb1; ++sb) {
+    const Small<TYPE> now = kQ4 ? small(sb) : next;
+    if (!kQ4) next = small(min(sb + 1, sb1 - 1));
+    v2i bs = {};
+    uint32_t even = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int slot = c % kAhead;
+      const typename W::D dot = W::mma(qa[slot], qb[slot]);
+      const uint32_t pr_c = pair[slot];
+      load(slot, sb * 8 + c + kAhead);
+      v16f sd;
+      float dh = 0.0f;
+      if constexpr (kQ4) {
+        sd = scale_outer(now.sc[c >> 2], pr_c, c & 3);
+        if (c & 1) {  // the scaled sums of chunks c - 1 and c
+          const int two = (int)__builtin_amdgcn_perm(pr_c, even, 0x07060302u);
+          if (lane_hi == (c >= 4)) bs[(c & 3) >> 1] = two;
+        } else {
+          even = pr_c;
+        }
+      } else {
+        dh = f16_bits_to_float(pr_c & 0xFFFF);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float s = kQ4 ? sd[i] : dh;
+        inner[i] = c == 0 ? W::val(dot, i) * s : fmaf(W::val(dot, i), s, inner[i]);
+        pin(inner[i]);
+      }
+      // a chunk at a time: the loads ahead need the other registers
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    dd[lane] = now.d;
+    v16f mt;
+    if constexpr (kQ4) {
+      typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+      const v16f zero = {};
+      mt = __builtin_amdgcn_mfma_f32_32x32x8f16(__builtin_bit_cast(v4h, now.mins), __builtin_bit_cast(v4h, bs), zero, 0,
+                                                0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 f = *(const float4*)(dd + 8 * q + 4 * (lane >> 5));
+      acc[4 * q + 0] = fmaf(inner[4 * q + 0], f.x, acc[4 * q + 0]);
+      acc[4 * q + 1] = fmaf(inner[4 * q + 1], f.y, acc[4 * q + 1]);
+      acc[4 * q + 2] = fmaf(inner[4 * q + 2], f.z, acc[4 * q + 2]);
+      acc[4 * q + 3] = fmaf(inner[4 * q + 3], f.w, acc[4 * q + 3]);
+      if constexpr (kQ4) {
+        const float4 m = *(const float4*)(dd + 32 + 8 * q + 4 * (lane >> 5));
+        acc[4 * q + 0] = fmaf(mt[4 * q + 0], m.x, acc[4 * q + 0]);
+        acc[4 * q + 1] = fmaf(mt[4 * q + 1], m.y, acc[4 * q + 1]);
+        acc[4 * q + 2] = fmaf(mt[4 * q + 2], m.z, acc[4 * q + 2]);
+        acc[4 * q + 3] = fmaf(mt[4 * q + 3], m.w, acc[4 * q + 3]);
+      }
+    }
+  }
+
+  float* const mine = red + wave * kEpWave;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *(float4*)(mine + (lane & 31) * kEpRow + 8 * q + 4 * (lane >> 5)) =
+        make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+  __syncthreads();
+  // four rows of a token per thread: eight threads hold a token's 32 rows
+  const bool q8 = ep.out_type == QMM_Q8;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < groups * 256; i += 64 * kWaves) {
+    const int g = i >> 8, tl = (i >> 3) & 31, quad = i & 7;
+    const int b = (int)blockIdx.x * groups + g, j = b * 32 + 4 * quad, t = tb * 32 + tl;
+    const int n = min(a.od - j, 4);
+    const bool live = t < a.n_tok && n > 0;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      const Sides side = load_sides(ep, t, j, n);
+      const float* p = red + g * a.kg * kEpWave + tl * kEpRow + 4 * quad;
+      v = *(const float4*)p;
+      for (int k = 1; k < a.kg; ++k) {
+        const float4 e = *(const float4*)(p + k * kEpWave);
+        v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
+      }
+      v = finish(ep, v, side);
+    }
+    if (q8 && b < rblocks)  // od % 256 == 0: whole blocks; padding tokens are zeros
+      put_q8(ep, quant_quad(v), t, b, a.od, quad);
+    else if (live)
+      put(ep, v, t, j, n);
+  }
+  if (q8 && blockIdx.y + 1 == gridDim.y && kg == 0 && (int)blockIdx.x * groups + group < rblocks)
+    for (int b = tb + 1; b * 32 < ep.t_pad; ++b) zero_block(ep, rb, b, lane, a.od);
+}
+
+template <int TYPE>
+hipError_t launch_typed(const Planes& p, const uint8_t* qact, int64_t n_tok, int64_t t_pad, const Epilogue& ep,
+                        int num_cus, hipStream_t s) {
+  FewArgs a{p.wq, p.wd, p.wsm, qact, qact + (size_t)t_pad * (size_t)p.id, (int)p.nchunk, (int)p.nsb, (int)p.od,
+            (int)n_tok, 1};
+  // Waves per row block: the fewest rounds of work-groups (one per CU), counted in
+  // the super-blocks that each wave walks (and half of one for the sums).
+  const int64_t rblocks = (p.od + 31) / 32, tblocks = (n_tok + 31) / 32;
+  double best = 0;
+  for (int kg = 1; kg <= kWaves && (kg == 1 || kg <= a.nsb); kg *= 2) {
+    const int64_t wgs = (rblocks + kWaves / kg - 1) / (kWaves / kg) * tblocks;
+    const double cost = (double)((wgs + num_cus - 1) / num_cus) * ((a.nsb + kg - 1) / kg + 0.5);
+    if (kg == 1 || cost < best) {
+      best = cost;
+      a.kg = kg;
+    }
+  }
+  const int groups = kWaves / a.kg;
+  mmq_few_kernel<TYPE><<<dim3((unsigned)((rblocks + groups - 1) / groups), (unsigned)tblocks), dim3(64 * kWaves), 0,
+                         s>>>(a, ep);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Measured against the tiled MMQ (in a graph, us, few / tiled): one token block is
+// always worth it (4096 x 4096 q4_K 7.7 / 15.7, 32000 x 4096 q6_K 42.6 / 63.4, 32
+// tokens).  More read the weights once each, mostly from cache, and win while the
+// work-groups fit one round of the CUs (4096 x 11008 q6_K, 64 tokens: 18.3 / 27.3),
+// with short rows two (4096 x 4096 q4_K, 128 tokens: 10.0 / 15.7; 4096 x 11008 q6_K:
+// 29.3 / 27.7), or three for two token blocks (11008 x 4096 q4_K, 64 tokens: 21.7 /
+// 24.5; 96: 37.1 / 24.8).
+bool mmq_few_applies(const Planes& p, int64_t n_tok, int num_cus) {
+  const int64_t tblocks = (n_tok + 31) / 32, blocks = (p.od + 31) / 32 * tblocks;
+  return tblocks == 1 || blocks <= num_cus || (p.nsb <= 32 && blocks <= (tblocks == 2 ? 3 : 2) * (int64_t)num_cus);
+}
+
+hipError_t launch_mmq_few(const Planes& p, const uint8_t* qact, int64_t n_tok, int64_t t_pad, const Epilogue& ep,
+                          int num_cus, hipStream_t s) {
+  return p.type == QMM_Q6_K   ? launch_typed<QMM_Q6_K>(p, qact, n_tok, t_pad, ep, num_cus, s)
+         : p.type == QMM_Q4_K ? launch_typed<QMM_Q4_K>(p, qact, n_tok, t_pad, ep, num_cus, s)
+                              : launch_typed<QMM_Q4_K_PACKED>(p, qact, n_tok, t_pad, ep, num_cus, s);
+}
+
+}  // namespace qmm

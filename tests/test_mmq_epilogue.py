@@ -1,8 +1,11 @@
-"""qmm_mmq_epilogue: refusals on the CPU; on the GPU its sums against qmm_mmq bit for
-bit, qmm_mmq against the oracle, and the epilogue on those sums against its formula
-in 64 bits.
+"""qmm_mmq_epilogue: refusals on the CPU; on the GPU its sums against the oracle (and
+against qmm_mmq bit for bit where the tiled kernel runs), and the epilogue on those
+sums against its formula in 64 bits.
 
-Tolerances, from the arithmetic (u = 2^-24, half a step of f32): the bias add, the
+Tolerances, from the arithmetic (u = 2^-24, half a step of f32): a term of a sum meets
+eight additions of its super-block (two roundings each), one per super-block and one
+per wave that shares the row: K = 20 + 2*nsb + 16 units of the terms' magnitudes.  In
+the epilogue the bias add, the
 scale, the factor and the residual's fused add round once each; exp of an argument z
 is off by |z| units of u and a few ulp, erfc of y by its ulps and 2*y^2 times the
 argument's error; act' is below 1.2 everywhere.  A stored value adds half a step of
@@ -135,7 +138,10 @@ SHAPES = [  # every geometry, split tails, all-split launches, odd rows and toke
     (synth.Q6_K, 256, 512, 64), (synth.Q4_K, 131, 768, 37), (synth.Q4_K, 1, 256, 1), (synth.Q6_K, 33, 1024, 129),
     (synth.Q6_K, 4097, 2048, 509), (synth.Q4_K, 512, 2816, 300), (synth.Q4_K_PACKED, 4160, 1024, 512),
     (synth.Q4_K, 8192, 1024, 560), (synth.Q6_K, 8192, 512, 600), (synth.Q4_K_PACKED, 8192, 512, 650),
-    (synth.Q4_K, 4099, 256, 2111)]
+    (synth.Q4_K, 4099, 256, 2111),
+    # few tokens: one block of them, several, odd rows; one to sixteen waves per row, some with more super-blocks
+    (synth.Q4_K, 300, 11008, 17), (synth.Q4_K_PACKED, 1000, 4096, 32), (synth.Q6_K, 515, 11008, 33), (synth.Q6_K, 97, 1280, 100),
+    (synth.Q4_K, 2048, 2304, 129), (synth.Q4_K_PACKED, 70, 256, 200), (synth.Q6_K, 20001, 768, 9), (synth.Q4_K, 40000, 512, 5)]
 
 
 @gpu
@@ -143,12 +149,14 @@ SHAPES = [  # every geometry, split tails, all-split launches, odd rows and toke
 def test_epilogue_against_the_formula(device, type_, od, id_, T):
     print(f"epilogue {synth.TYPE_NAMES[type_]} {od}x{id_} T={T}", flush=True)
     w, qact, raw, x = make(device, type_, od, id_, T, seed=od + T)
-    sums = qmm.mmq(w, qact, T)
-    if od * T < 200_000:
+    sums = qmm.mmq_epilogue(w, qact, T)
+    if od * T < 500_000:
         q, dh, s = oracle.quantize(x)
-        ref, A = oracle.mmq(synth.block_format(type_), raw, od, id_, q, dh, s)
-        assert np.all(np.abs(sums.cpu().numpy() - ref) <= 1e-4 * A)
-    assert torch.equal(qmm.mmq_epilogue(w, qact, T).view(torch.int32), sums.view(torch.int32)), "the sums differ"
+        ref, A = oracle.mmq_parallel(synth.block_format(type_), raw, od, id_, q, dh, s)
+        assert np.all(np.abs(sums.cpu().numpy() - ref) <= (36 + 2 * (id_ // 256)) * U * A)
+    if -(-od // 32) * -(-T // 32) > 768:  # more than three rounds of the GPU: the tiled kernel
+        assert torch.equal(sums.view(torch.int32), qmm.mmq(w, qact, T).view(torch.int32)), "not qmm_mmq's sums"
+    assert torch.equal(sums, qmm.mmq_epilogue(w, qact, T)), "a repeat differs"
     for i, act in enumerate(ACTS):
         side, out = TYPES[i % 3], TYPES[(i + 1) % 3]
         c = sides(device, T, od, side, i)
@@ -164,7 +172,8 @@ def test_epilogue_against_the_formula(device, type_, od, id_, T):
 @pytest.mark.parametrize("type_,od,id_,T", [
     (synth.Q6_K, 256, 512, 64), (synth.Q4_K, 256, 256, 1), (synth.Q4_K, 512, 2816, 300), (synth.Q6_K, 4352, 2048, 509),
     (synth.Q4_K, 8192, 1024, 560), (synth.Q6_K, 8192, 512, 600), (synth.Q4_K_PACKED, 8192, 512, 650),
-    (synth.Q4_K, 4096, 256, 2111), (synth.Q4_K_PACKED, 1024, 768, 130)])
+    (synth.Q4_K, 4096, 256, 2111), (synth.Q4_K_PACKED, 1024, 768, 130), (synth.Q6_K, 512, 2816, 1), (synth.Q4_K, 768, 4096, 31),
+    (synth.Q4_K_PACKED, 20480, 512, 32), (synth.Q6_K, 1024, 1024, 97)])
 def test_q8_output_is_the_prepass_of_the_values(device, type_, od, id_, T):
     """The output kept as q8 blocks equals the prepass's blocks of the f32 output, with and
     without the vector path, into a buffer that held other bytes."""
@@ -186,7 +195,7 @@ def test_q8_output_is_the_prepass_of_the_values(device, type_, od, id_, T):
 
 
 @gpu
-@pytest.mark.parametrize("type_,od,id_,T", [(synth.Q4_K, 260, 512, 70), (synth.Q6_K, 4097, 2048, 509)])
+@pytest.mark.parametrize("type_,od,id_,T", [(synth.Q4_K, 260, 512, 70), (synth.Q6_K, 4097, 2048, 509), (synth.Q4_K, 1001, 1024, 20)])
 def test_strides_places_and_repeats(device, type_, od, id_, T):
     """Strided rows at any alignment, columns of one tensor, in place, and nothing written outside."""
     w, qact, _, _ = make(device, type_, od, id_, T, seed=9)
@@ -340,6 +349,35 @@ def test_refusals_with_a_handle(device):
     assert wide(*args) == qmm.EINVAL and "out" in qmm.last_error()
     assert qmm.mmq_epilogue(w, torch.empty(0, dtype=torch.uint8, device=device), 0).shape == (0, od)
     w.release()
+
+
+@gpu
+def test_few_tokens_on_streams_and_in_a_graph(device):
+    """The few-token kernel needs no work memory: two streams at once, and captured without any."""
+    for type_, T in ((synth.Q4_K, 32), (synth.Q6_K, 90)):
+        w, qact, _, _ = make(device, type_, 1100, 2816, T, seed=T)
+        c = sides(device, T, 1100, torch.float16, 3)
+        ref = qmm.mmq_epilogue(w, qact, T, **c)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        for _ in range(3):
+            outs = [qmm.mmq_epilogue(w, qact, T, stream=s, **c) for s in streams]
+            torch.cuda.synchronize()
+            assert all(torch.equal(o, ref) for o in outs)
+        out = torch.empty_like(ref)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            qmm.mmq_epilogue(w, qact, T, out=out, **c)
+        for i in range(3):
+            c["residual"].normal_()
+            want = qmm.mmq_epilogue(w, qact, T, **c)
+            out.fill_(float("nan"))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want), f"replay {i}"
+        del graph
+        w.release()
 
 
 @gpu
