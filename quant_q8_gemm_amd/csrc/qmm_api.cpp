@@ -158,9 +158,10 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
   const size_t off_wd = round_up(qmm::wq_bytes(type, p.od_pad, id), 256);
   const size_t off_sm = off_wd + round_up(qmm::wd_bytes(type, p.od_pad, id), 256);
   size_t plane_bytes = off_sm + round_up(qmm::wsm_bytes(type, p.od_pad, id), 256);
+  const qmm::RowOffsets at = qmm::row_offsets(type, od, id);
   if (rows) {
     p.od_pad = qmm::row_pad(od);
-    p.rows = qmm::row_planes(type, od, id, nullptr, &plane_bytes);
+    plane_bytes = at.bytes;
   }
   // reserve the bytes against the cap before allocating, atomically, so that
   // registrations on several threads cannot overshoot it together; every
@@ -199,7 +200,8 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
                                     : fail_hip(e, "hipMalloc(raw)");
   }
   if (rows) {
-    p.rows = qmm::row_planes(type, od, id, alloc, &plane_bytes);
+    uint8_t* const base = (uint8_t*)alloc;
+    p.rows = {base, base + at.heads, base + at.scales, (uint16_t*)(base + at.d)};
   } else {
     p.wq = (int8_t*)alloc;
     p.wd = qmm::is_q4k(type) ? nullptr : (float*)((char*)alloc + off_wd);
@@ -224,9 +226,8 @@ int qmm_register_weights(int type, int64_t od, int64_t id, const void* host_byte
   w->device = device;
   w->raw_bytes = nbytes;
   w->plane_bytes = plane_bytes;
-  w->wd_offset = rows ? p.rows.heads_offset : qmm::is_q4k(type) ? plane_bytes : off_wd;
-  w->sm_offset = type == QMM_Q6_K_ROWS                 ? p.rows.scales_offset
-                 : qmm::is_q4k(type) && !rows ? off_sm : plane_bytes;
+  w->wd_offset = rows ? at.heads : qmm::is_q4k(type) ? plane_bytes : off_wd;
+  w->sm_offset = type == QMM_Q6_K_ROWS ? at.scales : qmm::is_q4k(type) ? off_sm : plane_bytes;
   w->alloc = alloc;
   if (getenv("QMM_LOG") != nullptr)
     fprintf(stderr, "qmm: registered %s od=%lld id=%lld od_pad=%lld raw=%zu planes=%zu device=%d\n",
@@ -747,7 +748,7 @@ int qmm_mmv(const qmm_weights* w, const void* x, int x_type, int64_t x_stride, i
   if (w == nullptr) return fail(QMM_EINVAL, "NULL weights handle");
   if (!qmm::is_rows(w->p.type))
     return fail(QMM_EINVAL, "the handle holds %s weights, qmm_mmv reads the rows forms", type_name(w->p.type));
-  Range in = rows_range("x", x, x_stride, n_tok, w->p.id, xb);
+  Range in{};
   if (q8) {
     const size_t need = qmm_qact_bytes(n_tok, w->p.id);
     if (x_stride < 0 || (size_t)x_stride != need)
@@ -759,8 +760,10 @@ int qmm_mmv(const qmm_weights* w, const void* x, int x_type, int64_t x_stride, i
     ok();
     return QMM_OK;
   }
-  if (!q8)
+  if (!q8) {
     if (int rc = check_stride("x", x_stride, w->p.id)) return rc;
+    in = rows_range("x", x, x_stride, n_tok, w->p.id, xb);
+  }
   qmm::Epilogue r{};
   Range written{};
   if (int rc = resolve_epilogue(ep, n_tok, w->p.od, out_type, out, out_stride, in, &r, &written)) return rc;

@@ -16,7 +16,6 @@ struct RowPlanes {
   uint8_t* heads;   // q4_K scales, mins, d, dmin; q6_K high code bits
   uint8_t* scales;  // q6_K scales
   uint16_t* d;      // q6_K d
-  size_t heads_offset, scales_offset, d_offset;  // bytes from codes
 };
 
 // Device planes of one registered weight matrix (layout documented in
@@ -60,8 +59,11 @@ hipError_t launch_quantize(const float* x, int64_t n_tok, int64_t t_pad, int64_t
                            uint8_t* qact, hipStream_t s);
 // Rows of a rows form, padded to its tile of 16.
 int64_t row_pad(int64_t od);
-// The rows form's planes at `base` and the bytes they need.
-RowPlanes row_planes(int type, int64_t od, int64_t id, void* base, size_t* bytes);
+// Where the rows form's planes start, in bytes from the codes, and where they end.
+struct RowOffsets {
+  size_t heads, scales, d, bytes;
+};
+RowOffsets row_offsets(int type, int64_t od, int64_t id);
 hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t id, const RowPlanes& r, hipStream_t s);
 struct Epilogue;  // qmm_epilogue.h
 // The product of 1 to QMM_MV_MAX_TOKENS tokens with a rows-form matrix; x_stride

@@ -118,22 +118,18 @@ repack_rows_kernel(const uint8_t* __restrict__ raw, int q6, int od, int nsb, int
 
 }  // namespace
 
-RowPlanes row_planes(int type, int64_t od, int64_t id, void* base, size_t* bytes) {
-  const size_t nb = (size_t)((od + kTile - 1) / kTile * kTile) * (size_t)(id / 256);
+int64_t row_pad(int64_t od) { return (od + kTile - 1) / kTile * kTile; }
+
+RowOffsets row_offsets(int type, int64_t od, int64_t id) {
+  const size_t nb = (size_t)row_pad(od) * (size_t)(id / 256);
   const bool q6 = type == QMM_Q6_K_ROWS;
-  RowPlanes r{};
-  r.heads_offset = round256(nb * 128);
-  r.scales_offset = r.heads_offset + round256(nb * (q6 ? 64 : 16));
-  r.d_offset = r.scales_offset + (q6 ? round256(nb * 16) : 0);
-  *bytes = r.d_offset + (q6 ? round256(nb * 2) : 0);
-  r.codes = (uint8_t*)base;
-  r.heads = r.codes + r.heads_offset;
-  r.scales = r.codes + r.scales_offset;
-  r.d = (uint16_t*)(r.codes + r.d_offset);
+  RowOffsets r;
+  r.heads = round256(nb * 128);
+  r.scales = r.heads + round256(nb * (q6 ? 64 : 16));
+  r.d = r.scales + (q6 ? round256(nb * 16) : 0);
+  r.bytes = r.d + (q6 ? round256(nb * 2) : 0);
   return r;
 }
-
-int64_t row_pad(int64_t od) { return (od + kTile - 1) / kTile * kTile; }
 
 hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t id, const RowPlanes& r, hipStream_t s) {
   const int64_t total = row_pad(od) * (id / 256) * 8;

@@ -77,6 +77,13 @@ def main():
     h, buf = P(), ctypes.create_string_buffer(840)
     for t, n in ((24, 840), (26, 576), (25, 840), (24, 0)):
         expect(f"register {t}", L.qmm_register_weights(t, 4, 256, buf, n, None, ctypes.byref(h)))
+    for t, n in ((24, 576), (26, 840)):  # valid: refused only for want of a GPU, nothing left held
+        L.qmm_set_memory_cap(ctypes.c_size_t(1))
+        expect(f"cap {t}", L.qmm_register_weights(t, 4, 256, buf, n, None, ctypes.byref(h)), -3)
+        L.qmm_set_memory_cap(ctypes.c_size_t(0))
+        rc = L.qmm_register_weights(t, 4, 256, buf, n, None, ctypes.byref(h))
+        if rc not in (OK, -4) or (rc == OK) != bool(h.value):
+            bad.append(f"valid registration {t}: {rc}")
     if bad:
         print("\n".join(bad))
     return 1 if bad else 0
