@@ -396,7 +396,7 @@ typedef struct {
  * and place the next step reads: one kernel instead of the product and an
  * elementwise pass over its output.  The sums are qmm_mmq's: bit for bit where
  * its tiled kernel runs, in another order of their f32 additions for few tokens
- * (up to 32, or a launch that small), which have a kernel of their own.  The same
+ * (up to 64, or a launch that small), which have a kernel of their own.  The same
  * call gives the same bits.
  *   w, qact, qact_bytes, n_tok, stream  as for qmm_mmq
  *   ep          the epilogue, or NULL: the sums themselves, rounded to out_type
@@ -411,8 +411,9 @@ typedef struct {
  *               tokens zero -- the next product's input (|values| <= 2046).
  *   work        device memory for the tail partials (see qmm_mmq), 16-byte
  *               aligned, work_bytes of it, at least the plan's scratch_bytes
- *               (qmm_mmq_plan; few tokens need none): the call then allocates nothing and can be
- *               captured, and calls with work memory of their own may overlap.
+ *               (qmm_mmq_plan; few tokens need none): the call then allocates
+ *               nothing and can be captured, and calls with work memory of their
+ *               own may overlap.
  *               NULL with work_bytes 0: the stream's scratch, as qmm_mmq; a
  *               captured call that needs scratch is then refused, since graphs
  *               replayed side by side would share it.

@@ -705,7 +705,7 @@ int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, 
   int device = -1, num_cus = 0;
   if (int rc = current_device(w, &device, &num_cus)) return rc;
   const hipStream_t s = (hipStream_t)stream;
-  if (qmm::mmq_few_applies(w->p, n_tok, num_cus)) {  // no scratch
+  if (qmm::mmq_few_blocks(w->p, n_tok, num_cus) > 0) {  // no scratch
     hipError_t e = qmm::launch_mmq_few(w->p, (const uint8_t*)qact, n_tok, token_pad(n_tok), r, num_cus, s);
     if (e != hipSuccess) return fail_hip(e, "mmq launch");
     ok();

@@ -101,9 +101,9 @@ hipError_t launch_mmq(const Planes& p, const MmqPlan& plan, const uint8_t* qact,
                       int64_t t_pad, float* out, float* part, hipStream_t s);
 hipError_t launch_mmq_epilogue(const Planes& p, const MmqPlan& plan, const uint8_t* qact, int64_t n_tok,
                                int64_t t_pad, const Epilogue& ep, float* part, hipStream_t s);
-// The same product for few tokens, without scratch (sums in another order), and
-// where it is the faster one.
-bool mmq_few_applies(const Planes& p, int64_t n_tok, int num_cus);
+// The same product for few tokens, without scratch (sums in another order); and the
+// token blocks its waves take, 0 where the tiled MMQ is the faster one.
+int mmq_few_blocks(const Planes& p, int64_t n_tok, int num_cus);
 hipError_t launch_mmq_few(const Planes& p, const uint8_t* qact, int64_t n_tok, int64_t t_pad, const Epilogue& ep,
                           int num_cus, hipStream_t s);
 // The allocation-free entry point's tail scratch: a static device array of
