@@ -127,6 +127,7 @@ WORKLOADS = {
 # only while the kernel source is the one they were taken with.
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "mmq_traffic.json")
 KERNEL_SRC = os.path.join(ROOT, "quant_q8_gemm_amd", "csrc", "qmm_mmq.hip")
+KERNEL_OPS = os.path.join(ROOT, "quant_q8_gemm_amd", "csrc", "qmm_mmq_ops.h")  # the weight types' part of it
 
 
 def _parse():
@@ -213,7 +214,8 @@ def kernel_hash() -> str:
     spec = importlib.util.spec_from_file_location("qmm_build", os.path.join(ROOT, "quant_q8_gemm_amd", "_build.py"))
     build = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(build)
-    code = re.sub(r"//[^\n]*|/\*.*?\*/", " ", open(KERNEL_SRC).read(), flags=re.S)
+    text = open(KERNEL_SRC).read() + open(KERNEL_OPS).read()
+    code = re.sub(r"//[^\n]*|/\*.*?\*/", " ", text, flags=re.S)
     h = hashlib.sha256(" ".join(code.split()).encode())
     h.update(" ".join(build.LIB_FLAGS).encode())
     return h.hexdigest()[:16]
