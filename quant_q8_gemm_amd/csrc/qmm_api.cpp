@@ -521,9 +521,9 @@ int resolve_epilogue(const qmm_epilogue* ep, int64_t n_tok, int64_t od, int out_
   r->mul = ep->mul;
   r->residual = ep->residual;
   r->out = out;
-  r->mul_stride = ep->mul_stride;
-  r->residual_stride = ep->residual_stride;
-  r->out_stride = out_stride;
+  r->mul_stride = (int)ep->mul_stride;
+  r->residual_stride = (int)ep->residual_stride;
+  r->out_stride = out_type == QMM_Q8 ? 0 : (int)out_stride;
   r->t_pad = token_pad(n_tok);
   r->scale = ep->scale;
   r->residual_scale = ep->residual_scale;

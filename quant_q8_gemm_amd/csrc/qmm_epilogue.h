@@ -18,15 +18,15 @@ struct NoEpilogue {
   static constexpr bool kOn = false;
 };
 
-// The caller's epilogue and output, checked; strides in elements.
+// The caller's epilogue and output, checked; strides in elements (up to 2^24).
 struct Epilogue {
   static constexpr bool kOn = true;
   const float* bias;     // or nullptr
   const void* mul;       // or nullptr
   const void* residual;  // or nullptr
   void* out;
-  int64_t mul_stride, residual_stride, out_stride;
   int64_t t_pad;  // QMM_Q8: tokens of the output's qact buffer
+  int mul_stride, residual_stride, out_stride;
   float scale, residual_scale;
   int act;
   int side_type;  // element type of mul and residual
@@ -91,11 +91,11 @@ __device__ __forceinline__ float4 load_side(const void* p, int type, int64_t i, 
 struct Sides {
   float4 bias, mul, residual;
 };
-__device__ __forceinline__ Sides load_sides(const Epilogue& ep, int64_t t, int j, int n) {
+__device__ __forceinline__ Sides load_sides(const Epilogue& ep, int t, int j, int n) {
   Sides s = {};
   if (ep.bias != nullptr) s.bias = load_typed<QMM_F32>(ep.bias, j, n);
-  if (ep.mul != nullptr) s.mul = load_side(ep.mul, ep.side_type, t * ep.mul_stride + j, n);
-  if (ep.residual != nullptr) s.residual = load_side(ep.residual, ep.side_type, t * ep.residual_stride + j, n);
+  if (ep.mul != nullptr) s.mul = load_side(ep.mul, ep.side_type, (int64_t)t * ep.mul_stride + j, n);
+  if (ep.residual != nullptr) s.residual = load_side(ep.residual, ep.side_type, (int64_t)t * ep.residual_stride + j, n);
   return s;
 }
 
@@ -125,8 +125,8 @@ __device__ __forceinline__ void put_typed(void* p, const float4& v, int64_t i, i
       if (k < n) store1<TYPE>(p, i + k, f[k]);
   }
 }
-__device__ __forceinline__ void put(const Epilogue& ep, float4 v, int64_t t, int j, int n) {
-  const int64_t i = t * ep.out_stride + j;
+__device__ __forceinline__ void put(const Epilogue& ep, float4 v, int t, int j, int n) {
+  const int64_t i = (int64_t)t * ep.out_stride + j;
   if (ep.out_type == QMM_F32) put_typed<QMM_F32>(ep.out, v, i, n);
   else if (ep.out_type == QMM_F16) put_typed<QMM_F16>(ep.out, v, i, n);
   else put_typed<QMM_BF16>(ep.out, v, i, n);

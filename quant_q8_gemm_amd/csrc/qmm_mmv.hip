@@ -149,8 +149,8 @@ hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t 
 // 16 bytes), B the weights (row n of the tile: lane & 15, the same k groups: the
 // four byte groups of a half block).  Lane (n, G) of the result holds token rows
 // m = 4G .. 4G + 3 of weight row n:
-//   TOK = 4 (up to 4 tokens): m = 4*group + token: lane group G has tokens 0..3 of
-//     byte group G;
+//   TOK = 1, 2, 4 (up to as many tokens): m = 4*group + token: lane group G has the
+//     tokens of byte group G, again in its other rows;
 //   TOK = 8: m = 8*half + token.  q4_K: the halves are the two 32-blocks of the half
 //     block (byte groups 0, 1 and 2, 3); q6_K: two byte groups, and a second MFMA
 //     with the other two;
@@ -161,12 +161,18 @@ namespace {
 
 constexpr int kWaves = 16;
 
-// LDS per super-block: codes [h][nibble][g][token][16], n_tok tokens; then f32 dh
-// [32-block][token] and for q4_K s [32-block][token], for kSlots tokens.
+// LDS per super-block: codes [h][nibble][g][token][16]; then f32 dh [32-block][token]
+// and for q4_K s [32-block][token].  TOK tokens, so that a lane's addresses differ by
+// constants; codes of n_tok tokens with TOK = 16, where the room is wanted.
 template <int TOK>
-constexpr int kSlots = TOK == 16 ? 16 : 8;
+__device__ __host__ __forceinline__ int code_slots(int n_tok) {
+  return TOK == 16 ? n_tok : TOK;
+}
+// Tokens whose sums a lane holds.
+template <int TOK>
+constexpr int kAcc = TOK < 4 ? TOK : 4;
 template <bool Q6, int TOK>
-constexpr int kScaleBytes = (Q6 ? 1 : 2) * 8 * kSlots<TOK> * 4;
+constexpr int kScaleBytes = (Q6 ? 1 : 2) * 8 * TOK * 4;
 // MFMAs per 64 weights of a row.
 template <bool Q6, int TOK>
 constexpr int kPasses = Q6 ? (TOK == 16 ? 4 : TOK == 8 ? 2 : 1) : (TOK == 16 ? 2 : 1);
@@ -174,12 +180,20 @@ constexpr int kPasses = Q6 ? (TOK == 16 ? 4 : TOK == 8 ? 2 : 1) : (TOK == 16 ? 2
 struct MvArgs {
   RowPlanes w;
   const void* x;
-  int64_t x_stride;  // elements; of a qact buffer: bytes of its code plane
+  int x_stride;  // elements; of a qact buffer: bytes of its code plane (128 tokens)
   int x_type, n_tok, od, nsb;
   int tile_sb;  // super-blocks quantized at a time
   int kg;       // waves that share a row tile
+  uint32_t over_per_tok, over_per_unit;  // see over()
+  int dt;  // threads / eights of a token
   int steps;    // sets of kWaves/kg row tiles
 };
+
+// n / d for n < 1024 and d >= 1, from over(d) = ceil(2^20 / d): the product's excess
+// over n / d, n / 2^20, is below 1/d, d up to 1024, and with larger d the quotient 0
+// stays below 1.
+inline uint32_t over(int64_t d) { return (uint32_t)(((1 << 20) + d - 1) / d); }
+__device__ __forceinline__ int divide(int n, uint32_t over_d) { return (int)(__umul24(n, over_d) >> 20); }
 
 // A lane's weights of one super-block as loaded, and the f32 factors of its dots.
 template <bool Q6>
@@ -207,30 +221,34 @@ struct Raw<true> {
   }
 };
 
+template <int N>
+struct alignas(4 * N) Vec {
+  float f[N];
+};
+
 __device__ __forceinline__ v4i mfma(v4i a, v4i b) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, v4i{0, 0, 0, 0}, 0, 0, 0);
 }
 
-// acc[i] += f * (dh[i] * dot[i]): one scale group's dots of four tokens
-__device__ __forceinline__ void add_dots(float (&acc)[4], const v4i& dot, float f, const float4& dh) {
-  acc[0] = fmaf((float)dot[0] * dh.x, f, acc[0]);
-  acc[1] = fmaf((float)dot[1] * dh.y, f, acc[1]);
-  acc[2] = fmaf((float)dot[2] * dh.z, f, acc[2]);
-  acc[3] = fmaf((float)dot[3] * dh.w, f, acc[3]);
+// acc[i] += f * (dh[i] * dot[i]): one scale group's dots of the lane's tokens
+template <int N>
+__device__ __forceinline__ void add_dots(float (&acc)[N], const v4i& dot, float f, const float* dh) {
+  const Vec<N> v = *(const Vec<N>*)dh;
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = fmaf((float)dot[i] * v.f[i], f, acc[i]);
 }
-__device__ __forceinline__ void add_min(float (&acc)[4], float f, const float4& s) {
-  acc[0] = fmaf(s.x, f, acc[0]);
-  acc[1] = fmaf(s.y, f, acc[1]);
-  acc[2] = fmaf(s.z, f, acc[2]);
-  acc[3] = fmaf(s.w, f, acc[3]);
+template <int N>
+__device__ __forceinline__ void add_min(float (&acc)[N], float f, const float* s) {
+  const Vec<N> v = *(const Vec<N>*)s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = fmaf(v.f[i], f, acc[i]);
 }
 
 // One super-block of q4_K.  codes(h, nibble, pass): the A operand; dh, s: the f32
 // scales of four of the lane's tokens, of 32-block c at [c*kSlots].
 template <int TOK, class Codes>
-__device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[4], int G, Codes&& codes,
+__device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc<TOK>], int G, Codes&& codes,
                                           const float* dh, const float* s) {
-  constexpr int kS = kSlots<TOK>;
   const float d = f16_bits_to_float(__builtin_amdgcn_perm(w.head.y, w.head.x, 0x0C0C0703u));
   const float m = -f16_bits_to_float(__builtin_amdgcn_perm(w.head.w, w.head.z, 0x0C0C0703u));
 #pragma unroll
@@ -246,15 +264,15 @@ __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[4], 
     for (int k = 0; k < kPasses<false, TOK>; ++k) {
       const int pair = TOK == 16 ? k : G >> 1;  // of 32-blocks: 4h + 2*pair and the next
       const uint32_t f = h == 0 ? (pair ? w.head.y : w.head.x) : (pair ? w.head.w : w.head.z);
-      const float* const dhp = dh + kS * (4 * h + 2 * pair);
-      const float* const sp = s + kS * (4 * h + 2 * pair);
-      add_dots(acc, mfma(codes(h, 0, k), lo), d * (float)(f & 63), *(const float4*)dhp);
-      add_dots(acc, mfma(codes(h, 1, k), hi), d * (float)((f >> 12) & 63), *(const float4*)(dhp + kS));
-      if (TOK == 4) {  // two lane groups share the pair: each adds one block's min term
-        add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), *(const float4*)(sp + (G & 1 ? kS : 0)));
+      const float* const dhp = dh + TOK * (4 * h + 2 * pair);
+      const float* const sp = s + TOK * (4 * h + 2 * pair);
+      add_dots(acc, mfma(codes(h, 0, k), lo), d * (float)(f & 63), dhp);
+      add_dots(acc, mfma(codes(h, 1, k), hi), d * (float)((f >> 12) & 63), dhp + TOK);
+      if (TOK <= 4) {  // two lane groups share the pair: each adds one block's min term
+        add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), sp + (G & 1 ? TOK : 0));
       } else {
-        add_min(acc, m * (float)((f >> 6) & 63), *(const float4*)sp);
-        add_min(acc, m * (float)((f >> 18) & 63), *(const float4*)(sp + kS));
+        add_min(acc, m * (float)((f >> 6) & 63), sp);
+        add_min(acc, m * (float)((f >> 18) & 63), sp + TOK);
       }
     }
   }
@@ -263,7 +281,7 @@ __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[4], 
 // One super-block of q6_K.  A code as four times (code - 32): its six bits, the top
 // one inverted, in a byte's upper bits are that as an int8; the 4 is taken off d.
 template <int TOK, class Codes>
-__device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[4], int G, Codes&& codes,
+__device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[kAcc<TOK>], int G, Codes&& codes,
                                           const float* dh, const float*) {
   const float d = 0.25f * f16_bits_to_float(w.d), d128 = -128.0f * d;
 #pragma unroll
@@ -285,7 +303,7 @@ __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[4], i
         const int g = TOK == 16 ? k : TOK == 8 ? 2 * k + (G >> 1) : G;
         const uint32_t u = (sc[nib] >> (8 * g)) & 255;
         add_dots(acc, mfma(codes(h, nib, k), b[nib]), fmaf(d, (float)u, d128),
-                 *(const float4*)(dh + kSlots<TOK> * (4 * h + 2 * nib + (g >> 1))));
+                 dh + TOK * (4 * h + 2 * nib + (g >> 1)));
       }
     }
   }
@@ -293,16 +311,16 @@ __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[4], i
 
 // Where eight codes of a token go: k counts eights from the first of the part.
 template <bool Q6>
-__device__ __forceinline__ uint8_t* place(uint8_t* lds, int sb_bytes, int n_tok, int t, int k) {
+__device__ __forceinline__ uint8_t* place(uint8_t* lds, int sb_bytes, int slots, int t, int k) {
   const int c = (k >> 2) & 7, half16 = (k >> 1) & 1;  // 32-block, its 16 codes
   const int h = c >> 2, nib = Q6 ? (c >> 1) & 1 : c & 1, g = 2 * (Q6 ? c & 1 : (c >> 1) & 1) + half16;
-  return lds + (k >> 5) * sb_bytes + (((2 * h + nib) * 4 + g) * n_tok + t) * 16 + (k & 1) * 8;
+  return lds + (k >> 5) * sb_bytes + (((2 * h + nib) * 4 + g) * slots + t) * 16 + (k & 1) * 8;
 }
 template <bool Q6, int TOK>
-__device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int n_tok, int t, int k, uint32_t pair) {
-  float* const s = (float*)(lds + (k >> 5) * sb_bytes + 256 * n_tok) + kSlots<TOK> * ((k >> 2) & 7) + t;
+__device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slots, int t, int k, uint32_t pair) {
+  float* const s = (float*)(lds + (k >> 5) * sb_bytes + 256 * slots) + TOK * ((k >> 2) & 7) + t;
   s[0] = f16_bits_to_float(pair & 0xFFFF);
-  if (!Q6) s[8 * kSlots<TOK>] = f16_bits_to_float(pair >> 16);
+  if (!Q6) s[8 * TOK] = f16_bits_to_float(pair >> 16);
 }
 
 // The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
@@ -312,19 +330,20 @@ __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int n_t
 template <bool Q6, int TOK, int XT>
 struct Quantizer {
   float4 v0, v1;
-  int t, k, per_tok, dt, dk;
+  int t, k, live, per_tok, dt, dk;  // a thread's token and eight of the part; live of per_tok, the others the last again
   __device__ __forceinline__ void fetch(const MvArgs& a, int sb0) {
     if (t < a.n_tok) {
-      const int64_t at = t * a.x_stride + (sb0 * 256 + 8 * k);
+      const int64_t at = (int64_t)t * a.x_stride + (sb0 * 256 + 8 * min(k, live - 1));
       v0 = load4<XT>(a.x, at);
       v1 = load4<XT>(a.x, at + 4);
     }
   }
   __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
-    per_tok = n * 32;
-    t = threadIdx.x / per_tok;
-    k = threadIdx.x - t * per_tok;
-    dt = 64 * kWaves / per_tok;  // the threads' stride in tokens and eights
+    live = n * 32;
+    per_tok = a.tile_sb * 32;
+    t = divide(threadIdx.x, a.over_per_tok);
+    k = threadIdx.x - __umul24(t, per_tok);
+    dt = a.dt;  // the threads' stride in tokens and eights
     dk = 64 * kWaves - dt * per_tok;
     fetch(a, sb0);
   }
@@ -340,8 +359,9 @@ struct Quantizer {
       }
       fetch(a, sb0);
       const Q8Oct r = quant_oct(c0, c1);
-      *(uint2*)place<Q6>(lds, sb_bytes, a.n_tok, tok, at) = make_uint2(r.codes[0], r.codes[1]);
-      if ((at & 3) == 0) place_scales<Q6, TOK>(lds, sb_bytes, a.n_tok, tok, at, r.pair);
+      const int slots = code_slots<TOK>(a.n_tok);
+      *(uint2*)place<Q6>(lds, sb_bytes, slots, tok, at) = make_uint2(r.codes[0], r.codes[1]);
+      if ((at & 3) == 0) place_scales<Q6, TOK>(lds, sb_bytes, slots, tok, at, r.pair);
     }
   }
 };
@@ -377,8 +397,9 @@ struct Quantizer<Q6, TOK, QMM_Q8> {
       half += 64 * kWaves / slots;
       fetch(a, sb0);
       if (t < a.n_tok) {
-        *(uint4*)place<Q6>(lds, sb_bytes, a.n_tok, t, at) = c;
-        if ((at & 2) == 0) place_scales<Q6, TOK>(lds, sb_bytes, a.n_tok, t, at, pr);
+        const int n = code_slots<TOK>(a.n_tok);
+        *(uint4*)place<Q6>(lds, sb_bytes, n, t, at) = c;
+        if ((at & 2) == 0) place_scales<Q6, TOK>(lds, sb_bytes, n, t, at, pr);
       }
     }
   }
@@ -391,6 +412,13 @@ __device__ __forceinline__ float halves_sum(float a, float b) {
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
+// Of each half of the wave: the sum over its two rows of 16 lanes.
+__device__ __forceinline__ float quarters_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                                  false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
 // OUT8: the output is kept as q8 blocks (its code beside the other outputs' cost
 // every call 0.9 us).
 template <bool Q6, int TOK, int XT, bool OUT8>
@@ -398,8 +426,9 @@ __global__ void __launch_bounds__(64 * kWaves)
 mmv_kernel(MvArgs a, Epilogue ep) {
   extern __shared__ uint4 lds_raw[];
   uint8_t* const lds = (uint8_t*)lds_raw;
-  const int sb_bytes = 256 * a.n_tok + kScaleBytes<Q6, TOK>;
-  // the partial sums [2][wave][token][kTile], and 16 bytes of zeros
+  const int slots = code_slots<TOK>(a.n_tok);
+  const int sb_bytes = 256 * slots + kScaleBytes<Q6, TOK>;
+  // the partial sums [2][wave][token][kTile], and the codes of a super-block as zeros
   float* const red = (float*)(lds + (size_t)a.tile_sb * sb_bytes);
   uint4* const zeros = (uint4*)(red + 2 * kWaves * TOK * kTile);
   const int lane = threadIdx.x & 63;
@@ -428,23 +457,32 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch(ahead[i]);
-  if (threadIdx.x == 0) *zeros = make_uint4(0, 0, 0, 0);
+  if ((int)threadIdx.x < 16 * slots) zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);
   if (one_tile) quant.run(a, lds, sb_bytes, 0);
   __syncthreads();
 
-  // The lane's A operand: its token's codes of its byte group G, or zeros (always the
-  // same ones) where G is not what its row sees in the pass.
+  // The lane's A operand: its token's codes of its byte group G, or zeros where G is
+  // not what its row sees in the pass.
   const int tok = m & (TOK - 1);
   const bool own = tok < a.n_tok && (TOK == 16 || (TOK == 8 ? (m >> 3) == (Q6 ? G & 1 : G >> 1) : (m >> 2) == G));
   const int pass = Q6 && TOK == 16 ? G : G >> 1;  // the lane's, of several
-  const uint32_t at = (uint32_t)(G * a.n_tok + tok) * 16, step_nib = (uint32_t)a.n_tok * 64;
-  const uint32_t zero_at = (uint32_t)((uint8_t*)zeros - lds);
-  const float* const scales = (const float*)(lds + 256 * a.n_tok) + (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
+  constexpr int kPass = kPasses<Q6, TOK>;
+  const uint8_t* first[kPass];  // of the wave's first super-block
+  int step_sb[kPass];           // to its next one
+#pragma unroll
+  for (int k = 0; k < kPass; ++k) {
+    const bool live = own && (kPass == 1 || pass == k);
+    first[k] = live ? lds + kg * sb_bytes + (G * slots + tok) * 16 : (const uint8_t*)zeros;
+    step_sb[k] = live ? a.kg * sb_bytes : 0;
+  }
+  const float* const scales =
+      (const float*)(lds + kg * sb_bytes + 256 * slots) + (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
   // The thread that finishes four rows of a token: of which unit, a row tile or, for
   // a q8 output, a pair of them (a 32-block: eight threads).
   constexpr int kUnit = OUT8 ? 2 : 1, kQuads = 4 * kUnit;
   const int units = groups / kUnit, per_unit = kQuads * a.n_tok;
-  const int e_unit = (int)threadIdx.x / per_unit, e_at = (int)threadIdx.x - e_unit * per_unit;
+  const int e_unit = divide(threadIdx.x, a.over_per_unit);
+  const uint32_t e_at = threadIdx.x - __umul24(e_unit, per_unit);
   const int e_tok = e_at / kQuads, e_quad = e_at % kQuads;
 
   int buf = 0;
@@ -453,7 +491,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
     const int left = e_unit < units ? min(a.od - row, 4) : 0;
     Sides side = {};
     if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);  // early, where the registers hold them
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc[kAcc<TOK>] = {};
     for (int sb0 = 0; sb0 < a.nsb; sb0 += a.tile_sb) {
       const int n = min(a.tile_sb, a.nsb - sb0);
       if (!one_tile) {
@@ -462,18 +500,22 @@ mmv_kernel(MvArgs a, Epilogue ep) {
         quant.run(a, lds, sb_bytes, sb0);
         __syncthreads();
       }
+      const uint8_t* at[kPass];
+#pragma unroll
+      for (int k = 0; k < kPass; ++k) at[k] = first[k];
+      const float* dh = scales;
       for (int sb = kg; sb < n; sb += a.kg) {
         const Raw<Q6> w = ahead[0];
 #pragma unroll
         for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
         fetch(ahead[kAhead - 1]);
-        const uint32_t base = (uint32_t)(sb * sb_bytes);
-        const float* const dh = (const float*)((const uint8_t*)scales + base);
         auto codes = [&](int h, int nib, int k) __attribute__((always_inline)) {
-          const bool live = kPasses<Q6, TOK> > 1 ? own && pass == k : own;
-          return *(const v4i*)(lds + (live ? base + at + (uint32_t)(2 * h + nib) * step_nib : zero_at));
+          return *(const v4i*)(at[k] + (2 * h + nib) * 64 * slots);
         };
-        add_block<TOK>(w, acc, G, codes, dh, dh + 8 * kSlots<TOK>);
+        add_block<TOK>(w, acc, G, codes, dh, dh + 8 * TOK);
+#pragma unroll
+        for (int k = 0; k < kPass; ++k) at[k] += step_sb[k];
+        dh += a.kg * sb_bytes / 4;
       }
     }
     // the sums of the lane groups that share tokens, into [token][row]
@@ -481,6 +523,9 @@ mmv_kernel(MvArgs a, Epilogue ep) {
     if constexpr (TOK == 16) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) out[(4 * G + i) * kTile] = acc[i];
+    } else if constexpr (TOK <= 2) {
+      const float x = quarters_sum(halves_sum(acc[0], acc[TOK - 1]));  // upper half of the wave: the second token
+      if ((G & 1) == 0) out[TOK == 2 ? (G >> 1) * kTile : 0] = x;
     } else {
       const float x = halves_sum(acc[0], acc[1]), y = halves_sum(acc[2], acc[3]);
       if constexpr (TOK == 8) {  // lower half of the wave: tokens 4*(G&1) and + 2, upper: + 1 and + 3
@@ -525,11 +570,14 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   // LDS: the whole inner dimension where it fits the CU's 160 KB, else parts of it,
   // quantized again for every set of row tiles
   constexpr size_t kMost = 160 * 1024;
-  constexpr size_t kRed = (size_t)2 * kWaves * TOK * kTile * sizeof(float) + 16;
-  const size_t per_sb = (size_t)256 * a.n_tok + kScaleBytes<Q6, TOK>;
+  constexpr size_t kRed = (size_t)2 * kWaves * TOK * kTile * sizeof(float) + 256 * TOK;
+  const size_t per_sb = (size_t)256 * code_slots<TOK>(a.n_tok) + kScaleBytes<Q6, TOK>;
   a.tile_sb = (int)std::min<size_t>(a.nsb, (kMost - kRed) / per_sb);
   if (a.tile_sb < a.nsb) a.tile_sb = a.tile_sb / kWaves * kWaves;  // a wave's super-blocks go on across parts
   const size_t lds = a.tile_sb * per_sb + kRed;
+  a.over_per_tok = over((int64_t)a.tile_sb * 32);
+  a.dt = 64 * kWaves / (a.tile_sb * 32);
+  a.over_per_unit = over((OUT8 ? 8 : 4) * a.n_tok);
   // One work-group per CU.  Waves per row tile: as few as fill the GPU's CUs with
   // row tiles of their own, and the fewest rounds of them, counted in the
   // super-blocks that each wave walks (and half of one for the sums).
@@ -573,7 +621,9 @@ template <bool Q6>
 hipError_t launch_tokens(const MvArgs& a, const Epilogue& ep, int num_cus, hipStream_t s) {
   return a.n_tok > 8   ? launch_typed<Q6, 16>(a, ep, num_cus, s)
          : a.n_tok > 4 ? launch_typed<Q6, 8>(a, ep, num_cus, s)
-                       : launch_typed<Q6, 4>(a, ep, num_cus, s);
+         : a.n_tok > 2 ? launch_typed<Q6, 4>(a, ep, num_cus, s)
+         : a.n_tok > 1 ? launch_typed<Q6, 2>(a, ep, num_cus, s)
+                       : launch_typed<Q6, 1>(a, ep, num_cus, s);
 }
 
 }  // namespace
@@ -583,7 +633,7 @@ hipError_t launch_mmv(const Planes& p, const void* x, int x_type, int64_t x_stri
   MvArgs a{};
   a.w = p.rows;
   a.x = x;
-  a.x_stride = x_stride;
+  a.x_stride = (int)x_stride;
   a.x_type = x_type;
   a.n_tok = n_tok;
   a.od = (int)p.od;

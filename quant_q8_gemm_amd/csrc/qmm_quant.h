@@ -108,6 +108,14 @@ __device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
 //    (Markstein): the correctly rounded quotient for every finite f32 whose
 //    quotient is normal (checked for every significand; smaller ones round to a
 //    scale of zero either way);
+//  * v/dh with the same step from r = v * inv, which is 2.5 units of its last place
+//    (ulp) off at most.  The remainder e = v - r*dh is exact: with dh's 11-bit
+//    significand it is a few thousand times the product of the two last places.  So
+//    r + e*inv is the quotient to 2^-20 ulp before its rounding, while a quotient of
+//    24 by 11 bits is never a midpoint of two f32 and at least 2^-12 ulp away from
+//    one: rounded once, it is the correctly rounded quotient.  (e underflows only
+//    where |v| is far below dh/2 and the code is 0.)  Asking instead whether any
+//    value is near a tie costs as much and sends most work-groups through a division;
 //  * codes rounded by adding 1.5 * 2^23, whose sum holds the integer (half to
 //    even) in its low bits;
 //  * no clamp where dh is a normal f16: dh is then amax/127 to 2^-11, so that no
@@ -129,20 +137,18 @@ __device__ __forceinline__ Q8Oct quant_oct(const float4& v0, const float4& v1) {
   const float amax = __builtin_bit_cast(float, u);
   const float q0 = amax * (1.0f / 127.0f);
   const Q8Scale sc((_Float16)fmaf(fmaf(-127.0f, q0, amax), 1.0f / 127.0f, q0));
-  float n[8], far = 0.0f;
+  float n[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float r = v[i] * sc.inv;
-    n[i] = r + kRound;
-    far = fmaxf(far, fabsf(r - (n[i] - kRound)));
+    n[i] = fmaf(fmaf(-r, sc.dhf, v[i]), sc.inv, r);
   }
-  if (!(far <= 0.5f - 1e-4f) || sc.dhf < kHalfMin) {  // as in quant4: next to a tie the quotients are formed exactly
+  if (sc.dhf < kHalfMin) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float r = sc.dhf == 0.0f ? 0.0f : v[i] / sc.dhf;
-      n[i] = __builtin_amdgcn_fmed3f(r, -127.0f, 127.0f) + kRound;
-    }
+    for (int i = 0; i < 8; ++i) n[i] = __builtin_amdgcn_fmed3f(n[i], -127.0f, 127.0f);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) n[i] += kRound;
   Q8Oct r;
   int S = 0;
 #pragma unroll
