@@ -11,6 +11,8 @@
 
 #include "../../include/qmm.h"
 
+#include <type_traits>
+
 namespace qmm {
 
 // A kernel without an epilogue: its outputs are the f32 sums themselves.
@@ -71,28 +73,63 @@ __device__ __forceinline__ float activate(float x, int act) {
 }
 
 // Rows j .. j + 3 of a token's row of mul, residual or out, at element offset i, of
-// any alignment; n of them exist: one access where all four do, else one each.
+// any alignment; n of them exist: one access where all four do, else one each.  As
+// loaded, one element per word or, all four of 16 bits, two: a conversion would wait
+// for the load where it stands.  Words without an element stay unset, as a zero would
+// wait for loads in flight to the same register.
+struct Side {
+  uint32_t w[4];
+};
 template <int TYPE>
-__device__ __forceinline__ float4 load_typed(const void* p, int64_t i, int n) {
-  if (n == 4) return load4_any<TYPE>(p, i);
-  float f[3] = {0.f, 0.f, 0.f};
+__device__ __forceinline__ Side load_typed(const void* p, int64_t i, int n) {
+  typedef std::conditional_t<TYPE == QMM_F32, uint32_t, uint16_t> B;
+  typedef B v4 __attribute__((ext_vector_type(4)));
+  typedef v4 any __attribute__((aligned(sizeof(B))));
+  const B* const q = (const B*)p + i;
+  Side s;
+  if (n == 4) {
+    const v4 v = *(const any*)q;
+    if constexpr (TYPE == QMM_F32) {
+      s.w[0] = v.x;
+      s.w[1] = v.y;
+      s.w[2] = v.z;
+      s.w[3] = v.w;
+    } else {
+      const uint2 u = __builtin_bit_cast(uint2, v);
+      s.w[0] = u.x;
+      s.w[1] = u.y;
+    }
+  } else {
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
-    if (k < n) f[k] = load1<TYPE>(p, i + k);
-  return make_float4(f[0], f[1], f[2], 0.0f);
+    for (int k = 0; k < 3; ++k)
+      if (k < n) s.w[k] = q[k];
+  }
+  return s;
 }
-__device__ __forceinline__ float4 load_side(const void* p, int type, int64_t i, int n) {
-  return type == QMM_F32   ? load_typed<QMM_F32>(p, i, n)
-         : type == QMM_F16 ? load_typed<QMM_F16>(p, i, n)
-                           : load_typed<QMM_BF16>(p, i, n);
+__device__ __forceinline__ Side load_side(const void* p, int type, int64_t i, int n) {
+  return type == QMM_F32 ? load_typed<QMM_F32>(p, i, n) : load_typed<QMM_F16>(p, i, n);  // bf16: the same bits
+}
+__device__ __forceinline__ float side_value(uint32_t w, int type, int half) {
+  if (type == QMM_BF16) return __uint_as_float(half ? w & 0xFFFF0000u : w << 16);
+  return f16_bits_to_float((half ? w >> 16 : w) & 0xFFFF);
+}
+__device__ __forceinline__ float4 side_values(const Side& s, int type, int n) {
+  if (type == QMM_F32)
+    return make_float4(__uint_as_float(s.w[0]), __uint_as_float(s.w[1]), __uint_as_float(s.w[2]), __uint_as_float(s.w[3]));
+  const bool two = n == 4;
+  return make_float4(side_value(s.w[0], type, 0), two ? side_value(s.w[0], type, 1) : side_value(s.w[1], type, 0),
+                     side_value(two ? s.w[1] : s.w[2], type, 0), side_value(s.w[1], type, 1));
 }
 
-// What the epilogue of rows j .. j + 3 of one token reads, n of which exist.
+// What the epilogue of rows j .. j + 3 of one token reads, n of which exist; parts that
+// the epilogue has not stay unset.
 struct Sides {
-  float4 bias, mul, residual;
+  Side bias, mul, residual;
+  int n;
 };
 __device__ __forceinline__ Sides load_sides(const Epilogue& ep, int t, int j, int n) {
-  Sides s = {};
+  Sides s;
+  s.n = n;
   if (ep.bias != nullptr) s.bias = load_typed<QMM_F32>(ep.bias, j, n);
   if (ep.mul != nullptr) s.mul = load_side(ep.mul, ep.side_type, (int64_t)t * ep.mul_stride + j, n);
   if (ep.residual != nullptr) s.residual = load_side(ep.residual, ep.side_type, (int64_t)t * ep.residual_stride + j, n);
@@ -101,15 +138,21 @@ __device__ __forceinline__ Sides load_sides(const Epilogue& ep, int t, int j, in
 
 // The epilogue of those rows' sums.
 __device__ __forceinline__ float4 finish(const Epilogue& ep, float4 v, const Sides& side) {
-  if (ep.bias != nullptr) v = make_float4(v.x + side.bias.x, v.y + side.bias.y, v.z + side.bias.z, v.w + side.bias.w);
+  if (ep.bias != nullptr) {
+    const float4 b = side_values(side.bias, QMM_F32, side.n);
+    v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+  }
   if (ep.act != QMM_ACT_NONE)
     v = make_float4(activate(v.x, ep.act), activate(v.y, ep.act), activate(v.z, ep.act), activate(v.w, ep.act));
   v = make_float4(v.x * ep.scale, v.y * ep.scale, v.z * ep.scale, v.w * ep.scale);
-  if (ep.mul != nullptr) v = make_float4(v.x * side.mul.x, v.y * side.mul.y, v.z * side.mul.z, v.w * side.mul.w);
+  if (ep.mul != nullptr) {
+    const float4 m = side_values(side.mul, ep.side_type, side.n);
+    v = make_float4(v.x * m.x, v.y * m.y, v.z * m.z, v.w * m.w);
+  }
   if (ep.residual != nullptr) {
     const float s = ep.residual_scale;
-    v = make_float4(fmaf(s, side.residual.x, v.x), fmaf(s, side.residual.y, v.y), fmaf(s, side.residual.z, v.z),
-                    fmaf(s, side.residual.w, v.w));
+    const float4 r = side_values(side.residual, ep.side_type, side.n);
+    v = make_float4(fmaf(s, r.x, v.x), fmaf(s, r.y, v.y), fmaf(s, r.z, v.z), fmaf(s, r.w, v.w));
   }
   return v;
 }

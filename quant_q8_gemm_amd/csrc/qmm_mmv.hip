@@ -329,13 +329,14 @@ __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slo
 // put other loads behind them.
 template <bool Q6, int TOK, int XT>
 struct Quantizer {
-  float4 v0, v1;
+  typedef elem_t<XT> Eight __attribute__((ext_vector_type(8)));
+  Eight v;      // as loaded: a conversion would wait here
   int t, k, live, per_tok, dt, dk;  // a thread's token and eight of the part; live of per_tok, the others the last again
   __device__ __forceinline__ void fetch(const MvArgs& a, int sb0) {
     if (t < a.n_tok) {
       const int64_t at = (int64_t)t * a.x_stride + (sb0 * 256 + 8 * min(k, live - 1));
-      v0 = load4<XT>(a.x, at);
-      v1 = load4<XT>(a.x, at + 4);
+      typedef Eight Rows __attribute__((aligned(4 * sizeof(elem_t<XT>))));  // rows start at fours
+      v = *(const Rows*)((const elem_t<XT>*)a.x + at);
     }
   }
   __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
@@ -349,7 +350,8 @@ struct Quantizer {
   }
   __device__ __forceinline__ void run(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0) {
     while (t < a.n_tok) {
-      const float4 c0 = v0, c1 = v1;
+      const float4 c0 = make_float4((float)v[0], (float)v[1], (float)v[2], (float)v[3]);
+      const float4 c1 = make_float4((float)v[4], (float)v[5], (float)v[6], (float)v[7]);
       const int tok = t, at = k;
       k += dk;
       t += dt;
@@ -457,10 +459,6 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch(ahead[i]);
-  if ((int)threadIdx.x < 16 * slots) zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);
-  if (one_tile) quant.run(a, lds, sb_bytes, 0);
-  __syncthreads();
-
   // The lane's A operand: its token's codes of its byte group G, or zeros where G is
   // not what its row sees in the pass.
   const int tok = m & (TOK - 1);
@@ -485,12 +483,19 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   const uint32_t e_at = threadIdx.x - __umul24(e_unit, per_unit);
   const int e_tok = e_at / kQuads, e_quad = e_at % kQuads;
 
+  // Its sides, early: behind the first step's weights, and a step ahead of the others'.
+  auto row_of = [&](int step) __attribute__((always_inline)) { return (step * groups + e_unit * kUnit) * kTile + 4 * e_quad; };
+  auto left_of = [&](int row) __attribute__((always_inline)) { return e_unit < units ? min(a.od - row, 4) : 0; };
+  int row = row_of(blockIdx.x), left = left_of(row);
+  Sides side;
+  if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);
+
+  if ((int)threadIdx.x < 16 * slots) zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  if (one_tile) quant.run(a, lds, sb_bytes, 0);
+  __syncthreads();
+
   int buf = 0;
   for (int step = blockIdx.x; step < a.steps; step += gridDim.x, buf ^= 1) {
-    const int row = (step * groups + e_unit * kUnit) * kTile + 4 * e_quad;
-    const int left = e_unit < units ? min(a.od - row, 4) : 0;
-    Sides side = {};
-    if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);  // early, where the registers hold them
     float acc[kAcc<TOK>] = {};
     for (int sb0 = 0; sb0 < a.nsb; sb0 += a.tile_sb) {
       const int n = min(a.tile_sb, a.nsb - sb0);
@@ -561,6 +566,9 @@ mmv_kernel(MvArgs a, Epilogue ep) {
         const int t = (i >> 1) & ((int)ep.t_pad - 1), block = step * groups / 2 + i / (2 * (int)ep.t_pad);
         if (t >= a.n_tok) zero_q8(ep, t, block, a.od, i & 1);
       }
+    row = row_of(step + gridDim.x);
+    left = left_of(row);
+    if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);
   }
 }
 
