@@ -183,7 +183,7 @@ struct MvArgs {
   int x_stride;  // elements; of a qact buffer: bytes of its code plane (128 tokens)
   int x_type, n_tok, od, nsb;
   int tile_sb;  // super-blocks quantized at a time
-  int kg;       // waves that share a row tile
+  int kg_bits;  // 2^kg_bits waves share a row tile
   uint32_t over_per_tok, over_per_unit;  // see over()
   int dt;  // threads / eights of a token
   int steps;    // sets of kWaves/kg row tiles
@@ -222,9 +222,16 @@ struct Raw<true> {
 };
 
 template <int N>
-struct alignas(4 * N) Vec {
-  float f[N];
-};
+using Vec = float __attribute__((ext_vector_type(N)));
+
+// LDS by its address, so that addresses can be pinned (computed where they stand).
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
+template <class T>
+__device__ __forceinline__ const __attribute__((address_space(3))) T* lds_at(uint32_t address) {
+  return (const __attribute__((address_space(3))) T*)(uintptr_t)address;
+}
 
 __device__ __forceinline__ v4i mfma(v4i a, v4i b) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, v4i{0, 0, 0, 0}, 0, 0, 0);
@@ -232,23 +239,23 @@ __device__ __forceinline__ v4i mfma(v4i a, v4i b) {
 
 // acc[i] += f * (dh[i] * dot[i]): one scale group's dots of the lane's tokens
 template <int N>
-__device__ __forceinline__ void add_dots(float (&acc)[N], const v4i& dot, float f, const float* dh) {
-  const Vec<N> v = *(const Vec<N>*)dh;
+__device__ __forceinline__ void add_dots(float (&acc)[N], const v4i& dot, float f, uint32_t dh) {
+  const Vec<N> v = *lds_at<Vec<N>>(dh);
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = fmaf((float)dot[i] * v.f[i], f, acc[i]);
+  for (int i = 0; i < N; ++i) acc[i] = fmaf((float)dot[i] * v[i], f, acc[i]);
 }
 template <int N>
-__device__ __forceinline__ void add_min(float (&acc)[N], float f, const float* s) {
-  const Vec<N> v = *(const Vec<N>*)s;
+__device__ __forceinline__ void add_min(float (&acc)[N], float f, uint32_t s) {
+  const Vec<N> v = *lds_at<Vec<N>>(s);
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = fmaf(v.f[i], f, acc[i]);
+  for (int i = 0; i < N; ++i) acc[i] = fmaf(v[i], f, acc[i]);
 }
 
 // One super-block of q4_K.  codes(h, nibble, pass): the A operand; dh, s: the f32
 // scales of four of the lane's tokens, of 32-block c at [c*kSlots].
 template <int TOK, class Codes>
 __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc<TOK>], int G, Codes&& codes,
-                                          const float* dh, const float* s) {
+                                          uint32_t dh, uint32_t s) {
   const float d = f16_bits_to_float(__builtin_amdgcn_perm(w.head.y, w.head.x, 0x0C0C0703u));
   const float m = -f16_bits_to_float(__builtin_amdgcn_perm(w.head.w, w.head.z, 0x0C0C0703u));
 #pragma unroll
@@ -264,15 +271,15 @@ __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc
     for (int k = 0; k < kPasses<false, TOK>; ++k) {
       const int pair = TOK == 16 ? k : G >> 1;  // of 32-blocks: 4h + 2*pair and the next
       const uint32_t f = h == 0 ? (pair ? w.head.y : w.head.x) : (pair ? w.head.w : w.head.z);
-      const float* const dhp = dh + TOK * (4 * h + 2 * pair);
-      const float* const sp = s + TOK * (4 * h + 2 * pair);
+      const uint32_t dhp = dh + 4 * TOK * (4 * h + 2 * pair);
+      const uint32_t sp = s + 4 * TOK * (4 * h + 2 * pair);
       add_dots(acc, mfma(codes(h, 0, k), lo), d * (float)(f & 63), dhp);
-      add_dots(acc, mfma(codes(h, 1, k), hi), d * (float)((f >> 12) & 63), dhp + TOK);
+      add_dots(acc, mfma(codes(h, 1, k), hi), d * (float)((f >> 12) & 63), dhp + 4 * TOK);
       if (TOK <= 4) {  // two lane groups share the pair: each adds one block's min term
-        add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), sp + (G & 1 ? TOK : 0));
+        add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), sp + (G & 1 ? 4 * TOK : 0));
       } else {
         add_min(acc, m * (float)((f >> 6) & 63), sp);
-        add_min(acc, m * (float)((f >> 18) & 63), sp + TOK);
+        add_min(acc, m * (float)((f >> 18) & 63), sp + 4 * TOK);
       }
     }
   }
@@ -282,7 +289,7 @@ __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc
 // one inverted, in a byte's upper bits are that as an int8; the 4 is taken off d.
 template <int TOK, class Codes>
 __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[kAcc<TOK>], int G, Codes&& codes,
-                                          const float* dh, const float*) {
+                                          uint32_t dh, uint32_t) {
   const float d = 0.25f * f16_bits_to_float(w.d), d128 = -128.0f * d;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -303,7 +310,7 @@ __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[kAcc<
         const int g = TOK == 16 ? k : TOK == 8 ? 2 * k + (G >> 1) : G;
         const uint32_t u = (sc[nib] >> (8 * g)) & 255;
         add_dots(acc, mfma(codes(h, nib, k), b[nib]), fmaf(d, (float)u, d128),
-                 dh + TOK * (4 * h + 2 * nib + (g >> 1)));
+                 dh + 4 * TOK * (4 * h + 2 * nib + (g >> 1)));
       }
     }
   }
@@ -435,7 +442,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   uint4* const zeros = (uint4*)(red + 2 * kWaves * TOK * kTile);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rg = wave / a.kg, kg = wave % a.kg, groups = kWaves / a.kg;
+  const int kgs = 1 << a.kg_bits, rg = wave >> a.kg_bits, kg = wave & (kgs - 1), groups = kWaves >> a.kg_bits;
   const int tiles = (a.od + kTile - 1) / kTile;
   const bool one_tile = a.tile_sb == a.nsb;
   const int m = lane & 15, G = lane >> 4;
@@ -443,7 +450,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   // Loads return in order, so the activations' go first.
   Quantizer<Q6, TOK, XT> quant;
   quant.begin(a, 0, a.tile_sb);
-  // The wave's weights, kAhead super-blocks ahead: super-blocks kg, kg + a.kg, ... of
+  // The wave's weights, kAhead super-blocks ahead: super-blocks kg, kg + kgs, ... of
   // its tile of this step, then of the next step's (past the last step: the last
   // step's again, unused).
   constexpr int kAhead = Q6 ? 1 : 2;
@@ -451,7 +458,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   int f_step = blockIdx.x, f_sb = kg;
   auto fetch = [&](Raw<Q6>& to) __attribute__((always_inline)) {
     to.load(a.w, (int64_t)min(f_step * groups + rg, tiles - 1) * a.nsb + f_sb, (uint32_t)lane);
-    f_sb += a.kg;
+    f_sb += kgs;
     if (f_sb >= a.nsb) {
       f_sb = kg;
       f_step = min(f_step + (int)gridDim.x, a.steps - 1);
@@ -465,16 +472,18 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   const bool own = tok < a.n_tok && (TOK == 16 || (TOK == 8 ? (m >> 3) == (Q6 ? G & 1 : G >> 1) : (m >> 2) == G));
   const int pass = Q6 && TOK == 16 ? G : G >> 1;  // the lane's, of several
   constexpr int kPass = kPasses<Q6, TOK>;
-  const uint8_t* first[kPass];  // of the wave's first super-block
-  int step_sb[kPass];           // to its next one
+  uint32_t first[kPass];  // LDS address, of the wave's first super-block
+  int step_sb[kPass];     // to its next one
 #pragma unroll
   for (int k = 0; k < kPass; ++k) {
     const bool live = own && (kPass == 1 || pass == k);
-    first[k] = live ? lds + kg * sb_bytes + (G * slots + tok) * 16 : (const uint8_t*)zeros;
-    step_sb[k] = live ? a.kg * sb_bytes : 0;
+    first[k] = live ? lds_address(lds) + kg * sb_bytes + (G * slots + tok) * 16 : lds_address(zeros);
+    step_sb[k] = live ? kgs * sb_bytes : 0;
+    pin(first[k]);
+    pin(step_sb[k]);
   }
-  const float* const scales =
-      (const float*)(lds + kg * sb_bytes + 256 * slots) + (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
+  uint32_t scales = lds_address(lds) + kg * sb_bytes + 256 * slots + 4 * (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
+  pin(scales);
   // The thread that finishes four rows of a token: of which unit, a row tile or, for
   // a q8 output, a pair of them (a 32-block: eight threads).
   constexpr int kUnit = OUT8 ? 2 : 1, kQuads = 4 * kUnit;
@@ -505,22 +514,22 @@ mmv_kernel(MvArgs a, Epilogue ep) {
         quant.run(a, lds, sb_bytes, sb0);
         __syncthreads();
       }
-      const uint8_t* at[kPass];
+      uint32_t at[kPass];
 #pragma unroll
       for (int k = 0; k < kPass; ++k) at[k] = first[k];
-      const float* dh = scales;
-      for (int sb = kg; sb < n; sb += a.kg) {
+      uint32_t dh = scales;
+      for (int sb = kg; sb < n; sb += kgs) {
         const Raw<Q6> w = ahead[0];
 #pragma unroll
         for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
         fetch(ahead[kAhead - 1]);
         auto codes = [&](int h, int nib, int k) __attribute__((always_inline)) {
-          return *(const v4i*)(at[k] + (2 * h + nib) * 64 * slots);
+          return *lds_at<v4i>(at[k] + (2 * h + nib) * 64 * slots);
         };
-        add_block<TOK>(w, acc, G, codes, dh, dh + 8 * TOK);
+        add_block<TOK>(w, acc, G, codes, dh, dh + 32 * TOK);
 #pragma unroll
         for (int k = 0; k < kPass; ++k) at[k] += step_sb[k];
-        dh += a.kg * sb_bytes / 4;
+        dh += kgs * sb_bytes;
       }
     }
     // the sums of the lane groups that share tokens, into [token][row]
@@ -549,9 +558,9 @@ mmv_kernel(MvArgs a, Epilogue ep) {
     // passed the next barrier
     if (left > 0) {
       const int tile = e_unit * kUnit + (e_quad >> 2);  // of the set
-      const float* p = red + ((size_t)buf * kWaves + tile * a.kg) * (TOK * kTile) + e_tok * kTile + 4 * (e_quad & 3);
+      const float* p = red + ((size_t)buf * kWaves + (tile << a.kg_bits)) * (TOK * kTile) + e_tok * kTile + 4 * (e_quad & 3);
       float4 f = *(const float4*)p;
-      for (int k = 1; k < a.kg; ++k) {
+      for (int k = 1; k < kgs; ++k) {
         const float4 e = *(const float4*)(p + (size_t)k * (TOK * kTile));
         f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
       }
@@ -592,12 +601,12 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   const int64_t tiles = (a.od + kTile - 1) / kTile;
   const int most = OUT8 ? kWaves / 2 : kWaves;  // q8: row tiles in pairs
   double best = 0;
-  for (int kg = 1; kg <= most && (kg == 1 || kg <= a.nsb); kg *= 2) {
+  for (int bits = 0, kg = 1; kg <= most && (kg == 1 || kg <= a.nsb); kg = 1 << ++bits) {
     const int64_t steps = (tiles + kWaves / kg - 1) / (kWaves / kg);
     const double cost = (double)((steps + num_cus - 1) / num_cus) * ((a.nsb + kg - 1) / kg + 0.5);
     if (kg == 1 || cost < best) {
       best = cost;
-      a.kg = kg;
+      a.kg_bits = bits;
       a.steps = (int)steps;
     }
   }
