@@ -48,7 +48,7 @@ struct FewArgs {
   const uint8_t* qq;
   const uint8_t* qs;
   int nchunk, nsb, od, n_tok;
-  int kg;  // waves that share a row block
+  int kg_bits, groups;  // 2^kg_bits waves share a row block, groups of them in a work-group
 };
 
 // Chunks loaded ahead: what the registers hold beside the sums (32 to 64 KiB of
@@ -75,12 +75,13 @@ mmq_few_kernel(FewArgs a, Epilogue ep) {
   __shared__ float dd_all[kWaves][64];  // a super-block's d of 32 rows; q4_K: d*2^25, then -dmin
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = wave / a.kg, kg = wave % a.kg, groups = kWaves / a.kg;
+  const int kgs = 1 << a.kg_bits;
+  const int group = wave >> a.kg_bits, kg = wave & (kgs - 1), groups = a.groups;
   const int rblocks = (a.od + 31) / 32;
   const int rb = min((int)blockIdx.x * groups + group, rblocks - 1);  // past the last: the last again, not stored
   const int row = lane & 31;
   const int tb0 = blockIdx.y * WT;
-  const int sb0 = kg * a.nsb / a.kg, sb1 = (kg + 1) * a.nsb / a.kg;
+  const int sb0 = kg * a.nsb >> a.kg_bits, sb1 = (kg + 1) * a.nsb >> a.kg_bits;
   float* const dd = dd_all[wave];
 
   const int8_t* const pa = a.wq + (int64_t)rb * a.nchunk * kFragA<TYPE>;
@@ -214,7 +215,7 @@ mmq_few_kernel(FewArgs a, Epilogue ep) {
   // four rows of a token per thread: eight threads hold a token's 32 rows
   const bool q8 = ep.out_type == QMM_Q8;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < groups * WT * 256; i += 64 * kWaves) {
+  for (int i = threadIdx.x; i < groups * WT * 256; i += blockDim.x) {
     const int g = i / (WT * 256), w = (i >> 8) % WT, tl = (i >> 3) & 31, quad = i & 7;
     const int b = (int)blockIdx.x * groups + g, j = b * 32 + 4 * quad, t = (tb0 + w) * 32 + tl;
     const int n = min(a.od - j, 4);
@@ -222,9 +223,9 @@ mmq_few_kernel(FewArgs a, Epilogue ep) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
       const Sides side = load_sides(ep, t, j, n);
-      const float* p = red + (g * a.kg * WT + w) * kEpWave + tl * kEpRow + 4 * quad;
+      const float* p = red + ((g << a.kg_bits) * WT + w) * kEpWave + tl * kEpRow + 4 * quad;
       v = *(const float4*)p;
-      for (int k = 1; k < a.kg; ++k) {
+      for (int k = 1; k < kgs; ++k) {
         const float4 e = *(const float4*)(p + k * WT * kEpWave);
         v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
       }
@@ -240,30 +241,32 @@ mmq_few_kernel(FewArgs a, Epilogue ep) {
 }
 
 // Waves per row block: the fewest rounds of work-groups (one per CU), counted in the
-// super-blocks that each wave walks (and half of one for the sums).
+// super-blocks that each wave walks (and half of one for the sums).  Row blocks per
+// work-group: as few as leave no more work-groups than CUs.
 template <int TYPE, int WT>
 void launch_blocks(FewArgs a, int64_t tgroups, const Epilogue& ep, int num_cus, hipStream_t s) {
   constexpr int kWaves = waves_of(WT);
   const int64_t rblocks = (a.od + 31) / 32;
   double best = 0;
-  for (int kg = 1; kg <= kWaves && (kg == 1 || kg <= a.nsb); kg *= 2) {
+  for (int bits = 0, kg = 1; kg <= kWaves && (kg == 1 || kg <= a.nsb); kg = 1 << ++bits) {
     const int64_t wgs = (rblocks + kWaves / kg - 1) / (kWaves / kg) * tgroups;
     const double cost = (double)((wgs + num_cus - 1) / num_cus) * ((a.nsb + kg - 1) / kg + 0.5);
     if (kg == 1 || cost < best) {
       best = cost;
-      a.kg = kg;
+      a.kg_bits = bits;
     }
   }
-  const int groups = kWaves / a.kg;
-  mmq_few_kernel<TYPE, WT><<<dim3((unsigned)((rblocks + groups - 1) / groups), (unsigned)tgroups), dim3(64 * kWaves), 0,
-                             s>>>(a, ep);
+  a.groups = kWaves >> a.kg_bits;
+  while (a.groups > 1 && (rblocks + a.groups / 2 - 1) / (a.groups / 2) * tgroups <= num_cus) a.groups /= 2;
+  mmq_few_kernel<TYPE, WT><<<dim3((unsigned)((rblocks + a.groups - 1) / a.groups), (unsigned)tgroups),
+                             dim3((64 * a.groups) << a.kg_bits), 0, s>>>(a, ep);
 }
 
 template <int TYPE>
 hipError_t launch_typed(const Planes& p, const uint8_t* qact, int64_t n_tok, int64_t t_pad, const Epilogue& ep,
                         int num_cus, hipStream_t s) {
   FewArgs a{p.wq, p.wd, p.wsm, qact, qact + (size_t)t_pad * (size_t)p.id, (int)p.nchunk, (int)p.nsb, (int)p.od,
-            (int)n_tok, 1};
+            (int)n_tok, 0, 1};
   const int64_t tblocks = (n_tok + 31) / 32;
   if (mmq_few_blocks(p, n_tok, num_cus) == 2)
     launch_blocks<TYPE, 2>(a, 1, ep, num_cus, s);
