@@ -140,7 +140,7 @@ hipError_t launch_repack_rows(const uint8_t* raw, int type, int64_t od, int64_t 
 }
 
 // ---------------------------------------------------------------------------
-// The product.  A work-group of kWaves waves first quantizes the activations into
+// The product.  A work-group of up to kWaves waves first quantizes the activations into
 // LDS, the whole inner dimension where it fits; then it walks row tiles: kg of its
 // waves share a tile, each over its share of the super-blocks, and the tile's
 // partial sums meet in LDS, are added in wave order and go through the epilogue.
@@ -183,10 +183,11 @@ struct MvArgs {
   int x_stride;  // elements; of a qact buffer: bytes of its code plane (128 tokens)
   int x_type, n_tok, od, nsb;
   int tile_sb;  // super-blocks quantized at a time
-  int kg_bits;  // 2^kg_bits waves share a row tile
+  int kg_bits;  // 2^kg_bits waves share a row tile,
+  int groups;   // groups of them in a work-group
   uint32_t over_per_tok, over_per_unit;  // see over()
   int dt;  // threads / eights of a token
-  int steps;    // sets of kWaves/kg row tiles
+  int steps;    // sets of so many row tiles
 };
 
 // n / d for n < 1024 and d >= 1, from over(d) = ceil(2^20 / d): the product's excess
@@ -194,6 +195,8 @@ struct MvArgs {
 // stays below 1.
 inline uint32_t over(int64_t d) { return (uint32_t)(((1 << 20) + d - 1) / d); }
 __device__ __forceinline__ int divide(int n, uint32_t over_d) { return (int)(__umul24(n, over_d) >> 20); }
+
+__device__ __host__ __forceinline__ int threads_of(const MvArgs& a) { return (64 << a.kg_bits) * a.groups; }
 
 // A lane's weights of one super-block as loaded, and the f32 factors of its dots.
 template <bool Q6>
@@ -352,7 +355,7 @@ struct Quantizer {
     t = divide(threadIdx.x, a.over_per_tok);
     k = threadIdx.x - __umul24(t, per_tok);
     dt = a.dt;  // the threads' stride in tokens and eights
-    dk = 64 * kWaves - dt * per_tok;
+    dk = threads_of(a) - dt * per_tok;
     fetch(a, sb0);
   }
   __device__ __forceinline__ void run(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0) {
@@ -381,7 +384,7 @@ template <bool Q6, int TOK>
 struct Quantizer<Q6, TOK, QMM_Q8> {
   uint4 codes;
   uint32_t pair;
-  int t, half, halves, slots;
+  int t, half, halves, bits;
   __device__ __forceinline__ void fetch(const MvArgs& a, int sb0) {
     if (half < halves && t < a.n_tok) {
       const uint8_t* const q = (const uint8_t*)a.x;
@@ -391,9 +394,8 @@ struct Quantizer<Q6, TOK, QMM_Q8> {
     }
   }
   __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
-    const int bits = a.n_tok > 8 ? 4 : a.n_tok > 4 ? 3 : a.n_tok > 2 ? 2 : a.n_tok > 1 ? 1 : 0;
-    slots = 1 << bits;
-    t = threadIdx.x & (slots - 1);
+    bits = a.n_tok > 8 ? 4 : a.n_tok > 4 ? 3 : a.n_tok > 2 ? 2 : a.n_tok > 1 ? 1 : 0;
+    t = threadIdx.x & ((1 << bits) - 1);
     half = threadIdx.x >> bits;
     halves = n * 16;
     fetch(a, sb0);
@@ -403,7 +405,7 @@ struct Quantizer<Q6, TOK, QMM_Q8> {
       const uint4 c = codes;
       const uint32_t pr = pair;
       const int at = 2 * half;
-      half += 64 * kWaves / slots;
+      half += threads_of(a) >> bits;
       fetch(a, sb0);
       if (t < a.n_tok) {
         const int n = code_slots<TOK>(a.n_tok);
@@ -442,7 +444,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   uint4* const zeros = (uint4*)(red + 2 * kWaves * TOK * kTile);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kgs = 1 << a.kg_bits, rg = wave >> a.kg_bits, kg = wave & (kgs - 1), groups = kWaves >> a.kg_bits;
+  const int kgs = 1 << a.kg_bits, rg = wave >> a.kg_bits, kg = wave & (kgs - 1), groups = a.groups;
   const int tiles = (a.od + kTile - 1) / kTile;
   const bool one_tile = a.tile_sb == a.nsb;
   const int m = lane & 15, G = lane >> 4;
@@ -499,7 +501,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   Sides side;
   if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);
 
-  if ((int)threadIdx.x < 16 * slots) zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < 16 * slots; i += threads_of(a)) zeros[i] = make_uint4(0, 0, 0, 0);
   if (one_tile) quant.run(a, lds, sb_bytes, 0);
   __syncthreads();
 
@@ -571,7 +573,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
         put(ep, f, e_tok, row, left);
     }
     if constexpr (OUT8)
-      for (int i = threadIdx.x; i < units * 2 * (int)ep.t_pad; i += 64 * kWaves) {  // the padding tokens' zeros
+      for (int i = threadIdx.x; i < units * 2 * (int)ep.t_pad; i += threads_of(a)) {  // the padding tokens' zeros
         const int t = (i >> 1) & ((int)ep.t_pad - 1), block = step * groups / 2 + i / (2 * (int)ep.t_pad);
         if (t >= a.n_tok) zero_q8(ep, t, block, a.od, i & 1);
       }
@@ -592,9 +594,6 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   a.tile_sb = (int)std::min<size_t>(a.nsb, (kMost - kRed) / per_sb);
   if (a.tile_sb < a.nsb) a.tile_sb = a.tile_sb / kWaves * kWaves;  // a wave's super-blocks go on across parts
   const size_t lds = a.tile_sb * per_sb + kRed;
-  a.over_per_tok = over((int64_t)a.tile_sb * 32);
-  a.dt = 64 * kWaves / (a.tile_sb * 32);
-  a.over_per_unit = over((OUT8 ? 8 : 4) * a.n_tok);
   // One work-group per CU.  Waves per row tile: as few as fill the GPU's CUs with
   // row tiles of their own, and the fewest rounds of them, counted in the
   // super-blocks that each wave walks (and half of one for the sums).
@@ -607,16 +606,22 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
     if (kg == 1 || cost < best) {
       best = cost;
       a.kg_bits = bits;
-      a.steps = (int)steps;
     }
   }
+  // Row tiles per work-group: as few as leave no more work-groups than CUs.
+  a.groups = kWaves >> a.kg_bits;
+  while (a.groups > (OUT8 ? 2 : 1) && (tiles + a.groups / 2 - 1) / (a.groups / 2) <= num_cus) a.groups /= 2;
+  a.steps = (int)((tiles + a.groups - 1) / a.groups);
+  a.over_per_tok = over((int64_t)a.tile_sb * 32);
+  a.dt = threads_of(a) / (a.tile_sb * 32);
+  a.over_per_unit = over((OUT8 ? 8 : 4) * a.n_tok);
   const int grid = (int)std::min<int64_t>(a.steps, num_cus);
   if (lds > 64 * 1024) {
     hipError_t e = hipFuncSetAttribute((const void*)mmv_kernel<Q6, TOK, XT, OUT8>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)lds);
     if (e != hipSuccess) return e;
   }
-  mmv_kernel<Q6, TOK, XT, OUT8><<<dim3((unsigned)grid), dim3(64 * kWaves), lds, s>>>(a, ep);
+  mmv_kernel<Q6, TOK, XT, OUT8><<<dim3((unsigned)grid), dim3((unsigned)threads_of(a)), lds, s>>>(a, ep);
   return hipGetLastError();
 }
 
