@@ -9,6 +9,11 @@
 // passes.  The mean square (RMS) or the mean and then the mean of the squared
 // deviations (layer) are summed in f32: per thread, over the wave, over the
 // waves, always in the same order.
+//
+// Its bytes bound it, of one row the launch.  In a graph, without a post-norm: 3314 x
+// 4096 f32 to the sum and q8 blocks, 178 MB, 28.8 us (35.9 at a copy's 4.96 TB/s from
+// memory; part of it comes from the cache); 509 x 11008 f16 layer norm to the sum and
+// numbers, 45 MB, 9.3; one row of 4096 2.9 (an empty launch: 2.1).
 #include "qmm_internal.h"
 #include "qmm_common.h"
 #include "qmm_quant.h"
