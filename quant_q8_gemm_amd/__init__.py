@@ -307,7 +307,7 @@ def _current(t, what: str) -> int:
     device = t.get_device()
     if device < 0:
         raise QmmError(EINVAL, f"{what} must be a cuda tensor")
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():  # torch.cuda.current_device without its detours: t is a cuda tensor
         raise QmmError(EINVAL, f"{what} is on device {device} but device {torch.cuda.current_device()} is current")
     return device
 
