@@ -13,8 +13,8 @@
 //
 // Measured in a graph, 32 tokens: 11008 x 4096 packed (34 MB) 10.2 us, q4_K (56 MB)
 // 12.4, q6_K (91 MB) 20.5, a copy's rate being 4.96 TB/s; 4096 x 4096 q4_K 7.6, 256 x
-// 512 q6_K 4.0.  4096 x 11008 q6_K takes 24.3: its 128 row blocks leave half of the
-// CUs idle, and a CU's share of the memory's rate is what bounds it.
+// 512 q6_K 4.0.  4096 x 11008 q6_K, 91 MB as well, takes 24.3: its 128 row blocks leave
+// half of the CUs idle.
 #include "qmm_internal.h"
 #include "qmm_common.h"
 #include "qmm_epilogue.h"

@@ -194,8 +194,8 @@ struct MvArgs {
   int tile_sb;  // super-blocks quantized at a time
   int kg_bits;  // 2^kg_bits waves share a row tile,
   int groups;   // groups of them in a work-group
-  uint32_t over_per_tok, over_per_unit;  // see over()
-  int dt;  // threads / eights of a token
+  uint32_t over_n_tok, over_per_unit;  // see over()
+  int db;  // threads / 4 / n_tok
   int steps;    // sets of so many row tiles
 };
 
@@ -343,40 +343,41 @@ __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slo
 }
 
 // The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
-// numbers: eight per thread, four threads per 32-block, the next eight loaded
-// while these are quantized; begin() loads the first ones, so that the caller can
-// put other loads behind them.
+// numbers: eight per thread, four threads per 32-block, the tokens of a block next to
+// each other, as LDS has them (4096 x 11008 q4_K, 16 tokens: 27.0 us; the blocks of a
+// token next to each other, in the same banks: 28.8); the next eight are loaded while
+// these are quantized; begin() loads the first ones, so that the caller can put other
+// loads behind them.
 template <bool Q6, int TOK, int XT>
 struct Quantizer {
   typedef elem_t<XT> Eight __attribute__((ext_vector_type(8)));
-  Eight v;      // as loaded: a conversion would wait here
-  int t, k, live, per_tok, dt, dk;  // a thread's token and eight of the part; live of per_tok, the others the last again
+  Eight v;                       // as loaded: a conversion would wait here
+  int t, b, blocks, dt, db;      // a thread's token and 32-block of the part
   __device__ __forceinline__ void fetch(const MvArgs& a, int sb0) {
-    if (t < a.n_tok) {
-      const int64_t at = (int64_t)t * a.x_stride + (sb0 * 256 + 8 * min(k, live - 1));
+    if (b < blocks) {
+      const int64_t at = (int64_t)t * a.x_stride + (sb0 * 256 + 32 * b + 8 * (int)(threadIdx.x & 3));
       typedef Eight Rows __attribute__((aligned(4 * sizeof(elem_t<XT>))));  // rows start at fours
       v = *(const Rows*)((const elem_t<XT>*)a.x + at);
     }
   }
   __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
-    live = n * 32;
-    per_tok = a.tile_sb * 32;
-    t = divide(threadIdx.x, a.over_per_tok);
-    k = threadIdx.x - __umul24(t, per_tok);
-    dt = a.dt;  // the threads' stride in tokens and eights
-    dk = threads_of(a) - dt * per_tok;
+    blocks = n * 8;
+    b = divide(threadIdx.x >> 2, a.over_n_tok);
+    t = (threadIdx.x >> 2) - __umul24(b, a.n_tok);
+    db = a.db;  // the threads' stride in blocks and tokens
+    dt = threads_of(a) / 4 - db * a.n_tok;
     fetch(a, sb0);
   }
   __device__ __forceinline__ void run(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0) {
-    while (t < a.n_tok) {
+    while (b < blocks) {
       const float4 c0 = make_float4((float)v[0], (float)v[1], (float)v[2], (float)v[3]);
       const float4 c1 = make_float4((float)v[4], (float)v[5], (float)v[6], (float)v[7]);
-      const int tok = t, at = k;
-      k += dk;
+      const int tok = t, at = 4 * b + (threadIdx.x & 3);
+      b += db;
       t += dt;
-      if (k >= per_tok) {
-        k -= per_tok;
-        ++t;
+      if (t >= a.n_tok) {
+        t -= a.n_tok;
+        ++b;
       }
       fetch(a, sb0);
       const Q8Oct r = quant_oct(c0, c1);
@@ -621,8 +622,8 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   a.groups = kWaves >> a.kg_bits;
   while (a.groups > (OUT8 ? 2 : 1) && (tiles + a.groups / 2 - 1) / (a.groups / 2) <= num_cus) a.groups /= 2;
   a.steps = (int)((tiles + a.groups - 1) / a.groups);
-  a.over_per_tok = over((int64_t)a.tile_sb * 32);
-  a.dt = threads_of(a) / (a.tile_sb * 32);
+  a.over_n_tok = over(a.n_tok);
+  a.db = threads_of(a) / 4 / a.n_tok;
   a.over_per_unit = over((OUT8 ? 8 : 4) * a.n_tok);
   const int grid = (int)std::min<int64_t>(a.steps, num_cus);
   if (lds > 64 * 1024) {
