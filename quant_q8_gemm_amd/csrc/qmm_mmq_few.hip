@@ -261,8 +261,7 @@ void launch_blocks(FewArgs a, int64_t tgroups, const Epilogue& ep, int num_cus, 
       a.kg_bits = bits;
     }
   }
-  a.groups = kWaves >> a.kg_bits;
-  while (a.groups > 1 && (rblocks + a.groups / 2 - 1) / (a.groups / 2) * tgroups <= num_cus) a.groups /= 2;
+  a.groups = (int)std::min<int64_t>(kWaves >> a.kg_bits, (rblocks * tgroups + num_cus - 1) / num_cus);
   mmq_few_kernel<TYPE, WT><<<dim3((unsigned)((rblocks + a.groups - 1) / a.groups), (unsigned)tgroups),
                              dim3((64 * a.groups) << a.kg_bits), 0, s>>>(a, ep);
 }

@@ -585,7 +585,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
     if constexpr (OUT8)
       for (int i = threadIdx.x; i < units * 2 * (int)ep.t_pad; i += threads_of(a)) {  // the padding tokens' zeros
         const int t = (i >> 1) & ((int)ep.t_pad - 1), block = step * groups / 2 + i / (2 * (int)ep.t_pad);
-        if (t >= a.n_tok) zero_q8(ep, t, block, a.od, i & 1);
+        if (t >= a.n_tok && block < a.od >> 5) zero_q8(ep, t, block, a.od, i & 1);
       }
     row = row_of(step + gridDim.x);
     left = left_of(row);
@@ -619,8 +619,8 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
     }
   }
   // Row tiles per work-group: as few as leave no more work-groups than CUs.
-  a.groups = kWaves >> a.kg_bits;
-  while (a.groups > (OUT8 ? 2 : 1) && (tiles + a.groups / 2 - 1) / (a.groups / 2) <= num_cus) a.groups /= 2;
+  const int64_t share = (tiles + num_cus - 1) / num_cus;
+  a.groups = (int)std::min<int64_t>(kWaves >> a.kg_bits, OUT8 ? (share + 1) / 2 * 2 : share);
   a.steps = (int)((tiles + a.groups - 1) / a.groups);
   a.over_n_tok = over(a.n_tok);
   a.db = threads_of(a) / 4 / a.n_tok;
