@@ -171,7 +171,7 @@ namespace {
 constexpr int kWaves = 16;
 
 // LDS per super-block: codes [h][nibble][g][token][16]; then f32 dh [32-block][token]
-// and for q4_K s [32-block][token].  TOK tokens, so that a lane's addresses differ by
+// and for q4_K s, f32 [32-block][token] or f16 [token][32-block] (kMinMma).  TOK tokens, so that a lane's addresses differ by
 // constants; codes of n_tok tokens with TOK = 16, where the room is wanted.
 template <int TOK>
 __device__ __host__ __forceinline__ int code_slots(int n_tok) {
@@ -180,8 +180,13 @@ __device__ __host__ __forceinline__ int code_slots(int n_tok) {
 // Tokens whose sums a lane holds.
 template <int TOK>
 constexpr int kAcc = TOK < 4 ? TOK : 4;
+// q4_K's min terms on the matrix core, from s as f16 [token][32-block]: a super-block's
+// eight mins of a row times eight s are one MFMA for all tokens.  Up to four tokens
+// the vector ALU needs no more instructions than the operands would.
 template <bool Q6, int TOK>
-constexpr int kScaleBytes = (Q6 ? 1 : 2) * 8 * TOK * 4;
+constexpr bool kMinMma = !Q6 && TOK >= 8;
+template <bool Q6, int TOK>
+constexpr int kScaleBytes = Q6 ? 8 * TOK * 4 : 8 * TOK * (kMinMma<Q6, TOK> ? 6 : 8);
 // MFMAs per 64 weights of a row.
 template <bool Q6, int TOK>
 constexpr int kPasses = Q6 ? (TOK == 16 ? 4 : TOK == 8 ? 2 : 1) : (TOK == 16 ? 2 : 1);
@@ -264,7 +269,8 @@ __device__ __forceinline__ void add_min(float (&acc)[N], float f, uint32_t s) {
 }
 
 // One super-block of q4_K.  codes(h, nibble, pass): the A operand; dh, s: the f32
-// scales of four of the lane's tokens, of 32-block c at [c*kSlots].
+// scales of the lane's tokens (addresses), of 32-block c at [c*TOK]; s with kMinMma the
+// lane's four f16.
 template <int TOK, class Codes>
 __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc<TOK>], int G, Codes&& codes,
                                           uint32_t dh, uint32_t s) {
@@ -284,16 +290,26 @@ __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc
       const int pair = TOK == 16 ? k : G >> 1;  // of 32-blocks: 4h + 2*pair and the next
       const uint32_t f = h == 0 ? (pair ? w.head.y : w.head.x) : (pair ? w.head.w : w.head.z);
       const uint32_t dhp = dh + 4 * TOK * (4 * h + 2 * pair);
-      const uint32_t sp = s + 4 * TOK * (4 * h + 2 * pair);
+      const uint32_t sp = s + 4 * TOK * (4 * h + 2 * pair);  // (f32 s)
       add_dots(acc, mfma(codes(h, 0, k), lo), d * (float)(f & 63), dhp);
       add_dots(acc, mfma(codes(h, 1, k), hi), d * (float)((f >> 12) & 63), dhp + 4 * TOK);
-      if (TOK <= 4) {  // two lane groups share the pair: each adds one block's min term
+      if (!kMinMma<false, TOK>)  // two lane groups share the pair: each adds one block's min term
         add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), sp + (G & 1 ? 4 * TOK : 0));
-      } else {
-        add_min(acc, m * (float)((f >> 6) & 63), sp);
-        add_min(acc, m * (float)((f >> 18) & 63), sp + 4 * TOK);
-      }
     }
+  }
+  if constexpr (kMinMma<false, TOK>) {
+    // B: lane groups 0 and 1 hold the mins of 32-blocks 0..3 and 4..7 of their row, as
+    // f16 subnormals (a code's bits are code * 2^-24); A: the same blocks' s of token m,
+    // zeros in the other groups and rows.  The products are exact.
+    const uint32_t a = G & 1 ? w.head.z : w.head.x, b = G & 1 ? w.head.w : w.head.y;
+    const uint2 mins = make_uint2(((a >> 6) & 0x3Fu) | ((a >> 2) & 0x3F0000u), ((b >> 6) & 0x3Fu) | ((b >> 2) & 0x3F0000u));
+    typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+    typedef float v4f __attribute__((ext_vector_type(4)));
+    const v4f t = __builtin_amdgcn_mfma_f32_16x16x16f16(*lds_at<v4h>(s), __builtin_bit_cast(v4h, mins),
+                                                        v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+    const float f = m * 16777216.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], f, acc[i]);
   }
 }
 
@@ -339,7 +355,10 @@ template <bool Q6, int TOK>
 __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slots, int t, int k, uint32_t pair) {
   float* const s = (float*)(lds + (k >> 5) * sb_bytes + 256 * slots) + TOK * ((k >> 2) & 7) + t;
   s[0] = f16_bits_to_float(pair & 0xFFFF);
-  if (!Q6) s[8 * TOK] = f16_bits_to_float(pair >> 16);
+  if constexpr (kMinMma<Q6, TOK>)
+    *(uint16_t*)(lds + (k >> 5) * sb_bytes + 256 * slots + 32 * TOK + t * 16 + ((k >> 2) & 7) * 2) = (uint16_t)(pair >> 16);
+  else if (!Q6)
+    s[8 * TOK] = f16_bits_to_float(pair >> 16);
 }
 
 // The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
@@ -496,6 +515,16 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   }
   uint32_t scales = lds_address(lds) + kg * sb_bytes + 256 * slots + 4 * (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
   pin(scales);
+  uint32_t s_first = lds_address(zeros);  // kMinMma: the lane's four f16 s
+  int s_step = 0;
+  if constexpr (kMinMma<Q6, TOK>) {
+    if (G < 2 && m < TOK && m < a.n_tok) {
+      s_first = lds_address(lds) + kg * sb_bytes + 256 * slots + 32 * TOK + m * 16 + G * 8;
+      s_step = kgs * sb_bytes;
+    }
+    pin(s_first);
+    pin(s_step);
+  }
   // The thread that finishes four rows of a token: of which unit, a row tile or, for
   // a q8 output, a pair of them (a 32-block: eight threads).
   constexpr int kUnit = OUT8 ? 2 : 1, kQuads = 4 * kUnit;
@@ -529,7 +558,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
       uint32_t at[kPass];
 #pragma unroll
       for (int k = 0; k < kPass; ++k) at[k] = first[k];
-      uint32_t dh = scales;
+      uint32_t dh = scales, s_at = s_first;
       for (int sb = kg; sb < n; sb += kgs) {
         const Raw<Q6> w = ahead[0];
 #pragma unroll
@@ -538,10 +567,11 @@ mmv_kernel(MvArgs a, Epilogue ep) {
         auto codes = [&](int h, int nib, int k) __attribute__((always_inline)) {
           return *lds_at<v4i>(at[k] + (2 * h + nib) * 64 * slots);
         };
-        add_block<TOK>(w, acc, G, codes, dh, dh + 32 * TOK);
+        add_block<TOK>(w, acc, G, codes, dh, kMinMma<Q6, TOK> ? s_at : dh + 32 * TOK);
 #pragma unroll
         for (int k = 0; k < kPass; ++k) at[k] += step_sb[k];
         dh += kgs * sb_bytes;
+        s_at += s_step;
       }
     }
     // the sums of the lane groups that share tokens, into [token][row]
