@@ -170,9 +170,10 @@ namespace {
 
 constexpr int kWaves = 16;
 
-// LDS per super-block: codes [h][nibble][g][token][16]; then f32 dh [32-block][token]
-// and for q4_K s, f32 [32-block][token] or f16 [token][32-block] (kMinMma).  TOK tokens, so that a lane's addresses differ by
-// constants; codes of n_tok tokens with TOK = 16, where the room is wanted.
+// LDS per super-block: codes [h][nibble][g][token][16]; then for q6_K f32 dh
+// [32-block][token], for q4_K the prepass's pairs, f16 (dh, s) [token][32-block].  TOK
+// tokens, so that a lane's addresses differ by constants; codes of n_tok tokens with
+// TOK = 16, where the room is wanted.
 template <int TOK>
 __device__ __host__ __forceinline__ int code_slots(int n_tok) {
   return TOK == 16 ? n_tok : TOK;
@@ -180,13 +181,8 @@ __device__ __host__ __forceinline__ int code_slots(int n_tok) {
 // Tokens whose sums a lane holds.
 template <int TOK>
 constexpr int kAcc = TOK < 4 ? TOK : 4;
-// q4_K's min terms on the matrix core, from s as f16 [token][32-block]: a super-block's
-// eight mins of a row times eight s are one MFMA for all tokens.  Up to four tokens
-// the vector ALU needs no more instructions than the operands would.
-template <bool Q6, int TOK>
-constexpr bool kMinMma = !Q6 && TOK >= 8;
-template <bool Q6, int TOK>
-constexpr int kScaleBytes = Q6 ? 8 * TOK * 4 : 8 * TOK * (kMinMma<Q6, TOK> ? 6 : 8);
+template <int TOK>
+constexpr int kScaleBytes = 32 * TOK;
 // MFMAs per 64 weights of a row.
 template <bool Q6, int TOK>
 constexpr int kPasses = Q6 ? (TOK == 16 ? 4 : TOK == 8 ? 2 : 1) : (TOK == 16 ? 2 : 1);
@@ -261,21 +257,37 @@ __device__ __forceinline__ void add_dots(float (&acc)[N], const v4i& dot, float 
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = fmaf((float)dot[i] * v[i], f, acc[i]);
 }
-template <int N>
-__device__ __forceinline__ void add_min(float (&acc)[N], float f, uint32_t s) {
-  const Vec<N> v = *lds_at<Vec<N>>(s);
-#pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = fmaf(v[i], f, acc[i]);
-}
-
-// One super-block of q4_K.  codes(h, nibble, pass): the A operand; dh, s: the f32
-// scales of the lane's tokens (addresses), of 32-block c at [c*TOK]; s with kMinMma the
-// lane's four f16.
+// One super-block of q4_K.  codes(h, nibble, pass): the A operand of the dots; pairs:
+// the address of the lane's (dh, s) pairs of token m and 32-blocks 2G and 2G + 1, or of
+// zeros where row m does not see these (m >> 3 the pair of 32-blocks a row sees, but
+// with TOK = 16 all).
+//
+// A dot's factor scale * dh is an outer product over rows and tokens, and the min terms
+// are a product over the eight 32-blocks: an MFMA each, with k = 4G + (dh, s, dh, s), B
+// the scales (zeros but for the dot's 32-blocks) or the mins of a lane's two 32-blocks.
+// Their six bits stand for themselves as f16 subnormals, code * 2^-24; the products are
+// exact.  The vector ALU is left with two instructions per dot and token.
 template <int TOK, class Codes>
 __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc<TOK>], int G, Codes&& codes,
-                                          uint32_t dh, uint32_t s) {
-  const float d = f16_bits_to_float(__builtin_amdgcn_perm(w.head.y, w.head.x, 0x0C0C0703u));
-  const float m = -f16_bits_to_float(__builtin_amdgcn_perm(w.head.w, w.head.z, 0x0C0C0703u));
+                                          uint32_t pairs) {
+  typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+  typedef float v4f __attribute__((ext_vector_type(4)));
+  constexpr int kN = kAcc<TOK>;
+  const v4h a = *lds_at<v4h>(pairs);
+  auto outer = [&](uint32_t b0, uint32_t b1) __attribute__((always_inline)) {
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(a, __builtin_bit_cast(v4h, make_uint2(b0, b1)),
+                                                 v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+  };
+  // scales and mins of 32-blocks 2G and 2G + 1, see q4k_head
+  const uint32_t h0 = w.head.x, h1 = w.head.y, h2 = w.head.z, h3 = w.head.w;
+  const uint32_t word = G & 2 ? (G & 1 ? h3 : h2) : (G & 1 ? h1 : h0);
+  const uint32_t sc0 = word & 63, sc1 = (word >> 12) & 63;
+  const v4f mins = outer((word << 10) & 0x3F0000u, (word >> 2) & 0x3F0000u);
+  const float d = 16777216.0f * f16_bits_to_float(__builtin_amdgcn_perm(w.head.y, w.head.x, 0x0C0C0703u));
+  // up to four tokens two lane groups see the same pair
+  const float m = (TOK <= 4 ? -8388608.0f : -16777216.0f) *
+                  f16_bits_to_float(__builtin_amdgcn_perm(w.head.w, w.head.z, 0x0C0C0703u));
+  float inner[kN] = {};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t c[4] = {w.code[h].x, w.code[h].y, w.code[h].z, w.code[h].w};
@@ -287,37 +299,23 @@ __device__ __forceinline__ void add_block(const Raw<false>& w, float (&acc)[kAcc
     }
 #pragma unroll
     for (int k = 0; k < kPasses<false, TOK>; ++k) {
-      const int pair = TOK == 16 ? k : G >> 1;  // of 32-blocks: 4h + 2*pair and the next
-      const uint32_t f = h == 0 ? (pair ? w.head.y : w.head.x) : (pair ? w.head.w : w.head.z);
-      const uint32_t dhp = dh + 4 * TOK * (4 * h + 2 * pair);
-      const uint32_t sp = s + 4 * TOK * (4 * h + 2 * pair);  // (f32 s)
-      add_dots(acc, mfma(codes(h, 0, k), lo), d * (float)(f & 63), dhp);
-      add_dots(acc, mfma(codes(h, 1, k), hi), d * (float)((f >> 12) & 63), dhp + 4 * TOK);
-      if (!kMinMma<false, TOK>)  // two lane groups share the pair: each adds one block's min term
-        add_min(acc, m * (float)((f >> (G & 1 ? 18 : 6)) & 63), sp + (G & 1 ? 4 * TOK : 0));
+      const bool mine = TOK == 16 ? G == 2 * h + k : G >> 1 == h;
+      const v4f f0 = outer(mine ? sc0 : 0, 0), f1 = outer(0, mine ? sc1 : 0);
+      const v4i d0 = mfma(codes(h, 0, k), lo), d1 = mfma(codes(h, 1, k), hi);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) inner[i] = fmaf((float)d1[i], f1[i], fmaf((float)d0[i], f0[i], inner[i]));
+      if (TOK == 16) __builtin_amdgcn_sched_barrier(0);  // a pass at a time: else registers spill
     }
   }
-  if constexpr (kMinMma<false, TOK>) {
-    // B: lane groups 0 and 1 hold the mins of 32-blocks 0..3 and 4..7 of their row, as
-    // f16 subnormals (a code's bits are code * 2^-24); A: the same blocks' s of token m,
-    // zeros in the other groups and rows.  The products are exact.
-    const uint32_t a = G & 1 ? w.head.z : w.head.x, b = G & 1 ? w.head.w : w.head.y;
-    const uint2 mins = make_uint2(((a >> 6) & 0x3Fu) | ((a >> 2) & 0x3F0000u), ((b >> 6) & 0x3Fu) | ((b >> 2) & 0x3F0000u));
-    typedef _Float16 v4h __attribute__((ext_vector_type(4)));
-    typedef float v4f __attribute__((ext_vector_type(4)));
-    const v4f t = __builtin_amdgcn_mfma_f32_16x16x16f16(*lds_at<v4h>(s), __builtin_bit_cast(v4h, mins),
-                                                        v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-    const float f = m * 16777216.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], f, acc[i]);
-  }
+  for (int i = 0; i < kN; ++i) acc[i] = fmaf(mins[i], m, fmaf(inner[i], d, acc[i]));
 }
 
 // One super-block of q6_K.  A code as four times (code - 32): its six bits, the top
 // one inverted, in a byte's upper bits are that as an int8; the 4 is taken off d.
 template <int TOK, class Codes>
 __device__ __forceinline__ void add_block(const Raw<true>& w, float (&acc)[kAcc<TOK>], int G, Codes&& codes,
-                                          uint32_t dh, uint32_t) {
+                                          uint32_t dh) {
   const float d = 0.25f * f16_bits_to_float(w.d), d128 = -128.0f * d;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -353,12 +351,12 @@ __device__ __forceinline__ uint8_t* place(uint8_t* lds, int sb_bytes, int slots,
 }
 template <bool Q6, int TOK>
 __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slots, int t, int k, uint32_t pair) {
-  float* const s = (float*)(lds + (k >> 5) * sb_bytes + 256 * slots) + TOK * ((k >> 2) & 7) + t;
-  s[0] = f16_bits_to_float(pair & 0xFFFF);
-  if constexpr (kMinMma<Q6, TOK>)
-    *(uint16_t*)(lds + (k >> 5) * sb_bytes + 256 * slots + 32 * TOK + t * 16 + ((k >> 2) & 7) * 2) = (uint16_t)(pair >> 16);
-  else if (!Q6)
-    s[8 * TOK] = f16_bits_to_float(pair >> 16);
+  uint8_t* const s = lds + (k >> 5) * sb_bytes + 256 * slots;
+  const int c = (k >> 2) & 7;
+  if (Q6)
+    ((float*)s)[TOK * c + t] = f16_bits_to_float(pair & 0xFFFF);
+  else
+    ((uint32_t*)s)[8 * t + c] = pair;
 }
 
 // The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
@@ -467,7 +465,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   extern __shared__ uint4 lds_raw[];
   uint8_t* const lds = (uint8_t*)lds_raw;
   const int slots = code_slots<TOK>(a.n_tok);
-  const int sb_bytes = 256 * slots + kScaleBytes<Q6, TOK>;
+  const int sb_bytes = 256 * slots + kScaleBytes<TOK>;
   // the partial sums [2][wave][token][kTile], and the codes of a super-block as zeros
   float* const red = (float*)(lds + (size_t)a.tile_sb * sb_bytes);
   uint4* const zeros = (uint4*)(red + 2 * kWaves * TOK * kTile);
@@ -513,18 +511,18 @@ mmv_kernel(MvArgs a, Epilogue ep) {
     pin(first[k]);
     pin(step_sb[k]);
   }
-  uint32_t scales = lds_address(lds) + kg * sb_bytes + 256 * slots + 4 * (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
-  pin(scales);
-  uint32_t s_first = lds_address(zeros);  // kMinMma: the lane's four f16 s
-  int s_step = 0;
-  if constexpr (kMinMma<Q6, TOK>) {
-    if (G < 2 && m < TOK && m < a.n_tok) {
-      s_first = lds_address(lds) + kg * sb_bytes + 256 * slots + 32 * TOK + m * 16 + G * 8;
-      s_step = kgs * sb_bytes;
-    }
-    pin(s_first);
-    pin(s_step);
+  // Its scales: q6_K of the tokens whose sums it holds, q4_K see add_block.
+  uint32_t scales = lds_address(lds) + kg * sb_bytes + 256 * slots;
+  int scale_step = kgs * sb_bytes;
+  if constexpr (Q6) {
+    scales += 4 * (TOK == 16 ? 4 * G : TOK == 8 ? 4 * (G & 1) : 0);
+  } else {
+    const bool live = tok < a.n_tok && (TOK == 16 || m >> 3 == (G & 1));
+    scales = live ? scales + tok * 32 + G * 8 : lds_address(zeros);
+    scale_step = live ? scale_step : 0;
+    pin(scale_step);
   }
+  pin(scales);
   // The thread that finishes four rows of a token: of which unit, a row tile or, for
   // a q8 output, a pair of them (a 32-block: eight threads).
   constexpr int kUnit = OUT8 ? 2 : 1, kQuads = 4 * kUnit;
@@ -558,7 +556,7 @@ mmv_kernel(MvArgs a, Epilogue ep) {
       uint32_t at[kPass];
 #pragma unroll
       for (int k = 0; k < kPass; ++k) at[k] = first[k];
-      uint32_t dh = scales, s_at = s_first;
+      uint32_t scales_at = scales;
       for (int sb = kg; sb < n; sb += kgs) {
         const Raw<Q6> w = ahead[0];
 #pragma unroll
@@ -567,11 +565,10 @@ mmv_kernel(MvArgs a, Epilogue ep) {
         auto codes = [&](int h, int nib, int k) __attribute__((always_inline)) {
           return *lds_at<v4i>(at[k] + (2 * h + nib) * 64 * slots);
         };
-        add_block<TOK>(w, acc, G, codes, dh, kMinMma<Q6, TOK> ? s_at : dh + 32 * TOK);
+        add_block<TOK>(w, acc, G, codes, scales_at);
 #pragma unroll
         for (int k = 0; k < kPass; ++k) at[k] += step_sb[k];
-        dh += kgs * sb_bytes;
-        s_at += s_step;
+        scales_at += scale_step;
       }
     }
     // the sums of the lane groups that share tokens, into [token][row]
@@ -630,7 +627,7 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   // quantized again for every set of row tiles
   constexpr size_t kMost = 160 * 1024;
   constexpr size_t kRed = (size_t)2 * kWaves * TOK * kTile * sizeof(float) + 256 * TOK;
-  const size_t per_sb = (size_t)256 * code_slots<TOK>(a.n_tok) + kScaleBytes<Q6, TOK>;
+  const size_t per_sb = (size_t)256 * code_slots<TOK>(a.n_tok) + kScaleBytes<TOK>;
   a.tile_sb = (int)std::min<size_t>(a.nsb, (kMost - kRed) / per_sb);
   if (a.tile_sb < a.nsb) a.tile_sb = a.tile_sb / kWaves * kWaves;  // a wave's super-blocks go on across parts
   const size_t lds = a.tile_sb * per_sb + kRed;
