@@ -21,14 +21,14 @@
 // 16x16x64 MFMA of 16 weight rows then gives the separate dots of four groups for
 // up to four tokens, of two for up to eight, of one for up to sixteen.
 //
-// What bounds it: a large matrix its bytes (32000 x 4096 q6_K, 108 MB: 20.1 us with
-// one token, 22.3 with five, a copy's rate is 4.96 TB/s); one that the CUs hold in a
+// What bounds it: a large matrix its bytes (32000 x 4096 q6_K, 108 MB: 20.4 us with
+// one token, 23.0 with five, a copy's rate is 4.96 TB/s); one that the CUs hold in a
 // round the path of a wave, since with sixteen of them on a CU each vector
-// instruction takes 7 ns (4096 x 4096 q4_K, 9.4 MB: 4.6 us, of which the launch 2.1
-// and the bytes 1.9; 11008 x 4096: 6.9).  From numbers, every work-group quantizes the
-// activations anew, 0.3 us per 4096 values: with many tokens and long rows q8 blocks
-// as the input are faster (16 x 4096 values, 4096 rows: 11.2 and 6.4 us, 5 x 4096: 6.3
-// and 5.3; the blocks themselves take a launch of 2.5).
+// instruction takes 7 ns (4096 x 4096 q4_K, 9.4 MB: 4.7 us, of which the launch 2.1
+// and the bytes 1.9; 11008 x 4096: 6.8, with five tokens 8.5).  From numbers, every
+// work-group quantizes the activations anew, 0.3 us per 4096 values: with many tokens
+// and long rows q8 blocks as the input are faster (16 x 4096 values, 4096 rows: 10.8
+// and 6.1 us, 5 x 4096: 6.2 and 5.2; the blocks themselves take a launch of 2.5).
 #include "qmm_internal.h"
 #include "qmm_common.h"
 #include "qmm_epilogue.h"
@@ -361,10 +361,10 @@ __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slo
 
 // The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
 // numbers: eight per thread, four threads per 32-block, the tokens of a block next to
-// each other, as LDS has them (4096 x 11008 q4_K, 16 tokens: 27.0 us; the blocks of a
-// token next to each other, in the same banks: 28.8); the next eight are loaded while
-// these are quantized; begin() loads the first ones, so that the caller can put other
-// loads behind them.
+// each other, as LDS has them (4096 x 11008 q4_K, 16 tokens, 25.8 us: 1.8 less than with
+// the blocks of a token next to each other, in the same banks); the next eight are
+// loaded while these are quantized; begin() loads the first ones, so that the caller
+// can put other loads behind them.
 template <bool Q6, int TOK, int XT>
 struct Quantizer {
   typedef elem_t<XT> Eight __attribute__((ext_vector_type(8)));
