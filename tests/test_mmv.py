@@ -177,7 +177,8 @@ def test_q8_output_is_the_prepass_of_the_values(device, type_, od, id_):  # noqa
 @pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K], ids=["q4_K", "q6_K"])
 def test_longest_rows_in_tiles(device, type_):  # noqa: F811
     """Rows whose activations do not fit the LDS at once: the inner dimension in tiles, the last one short."""
-    for od, id_, n_tok in ((6, 1 << 20, 1), (37, 256 * 131, 8), (300, 256 * 61, 8), (50, 256 * 43, 16), (33, 256 * 29, 11)):
+    for od, id_, n_tok in ((6, 1 << 20, 1), (37, 256 * 131, 8), (300, 256 * 61, 8), (50, 256 * 43, 16), (33, 256 * 29, 11),
+                          (7, 256 * 300, 2), (21, 256 * 150, 3), (600, 256 * 70, 7)):
         raw, x = synth.case(type_, od, id_, n_tok, seed=od)
         w = qmm.register_weights(ROWS[type_], od, id_, raw)
         x = torch.from_numpy(x).to(device)
@@ -185,6 +186,36 @@ def test_longest_rows_in_tiles(device, type_):  # noqa: F811
         sums_ok(got, raw, type_, od, id_, x)
         assert torch.equal(got, qmm.mmv(w, qmm.quantize_activations(x), n_tok))
         w.release()
+
+
+@gpu
+@pytest.mark.parametrize("type_", [synth.Q4_K, synth.Q6_K], ids=["q4_K", "q6_K"])
+@pytest.mark.parametrize("od,id_", [(4101, 256), (8197, 512), (12300, 256), (17000, 768), (24577, 256), (36865, 512)])
+def test_any_share_of_row_tiles(device, type_, od, id_):  # noqa: F811
+    """One to sixteen row tiles per work-group, odd numbers of them and a last group that is not full, as numbers and
+    (the largest multiple of 256 rows) as q8 blocks."""
+    od8 = od // 256 * 256
+    raw = synth.weights(np.random.default_rng(od), type_, od, id_)
+    w = qmm.register_weights(ROWS[type_], od, id_, raw)
+    w8 = qmm.register_weights(ROWS[type_], od8, id_, raw[:raw.size // od * od8])
+    scale = 2.0 ** -8  # the blocks' range
+    for n_tok in (1, 2, 4, 7, 16):
+        x = synth.activations(np.random.default_rng(n_tok), n_tok, id_)
+        ref, A = oracle.mmq_parallel(type_, raw, od, id_, *oracle.quantize(x))
+        E = (8 * (id_ // 256) + 23) * U * A
+        x = torch.from_numpy(x).to(device)
+        assert (np.abs(qmm.mmv(w, x).cpu().numpy() - ref) <= E).all()
+        buf = torch.full((qmm.qact_bytes(n_tok, od8) + 4096,), 77, dtype=torch.uint8, device=device)
+        qmm.mmv(w8, x, dtype="q8", out=buf[:-4096], scale=scale)
+        assert (buf[-4096:] == 77).all(), "written behind the blocks"
+        back = qmm.dequantize_activations(buf[:-4096], n_tok, od8).cpu().numpy().astype(np.float64)
+        ref, E = ref[:, :od8] * scale, E[:, :od8] * scale
+        # half a step of the block's largest value, or 0.07 steps where its stored scale (2^-11 off, or 2^-25 where
+        # it is subnormal) is below a 127th of it
+        top = (np.abs(ref) + E).reshape(n_tok, -1, 32).max(-1).repeat(32, -1)
+        assert (np.abs(back - ref) <= 0.58 / 127 * top * (1 + 2.0 ** -10) + E + 127 * 2.0 ** -25).all()
+    w.release()
+    w8.release()
 
 
 @gpu
