@@ -25,10 +25,11 @@
 // one token, 23.0 with five, a copy's rate is 4.96 TB/s); one that the CUs hold in a
 // round the path of a wave, since with sixteen of them on a CU each vector
 // instruction takes 7 ns (4096 x 4096 q4_K, 9.4 MB: 4.7 us, of which the launch 2.1
-// and the bytes 1.9; 11008 x 4096: 6.8, with five tokens 8.5).  From numbers, every
-// work-group quantizes the activations anew, 0.3 us per 4096 values: with many tokens
-// and long rows q8 blocks as the input are faster (16 x 4096 values, 4096 rows: 10.8
-// and 6.1 us, 5 x 4096: 6.2 and 5.2; the blocks themselves take a launch of 2.5).
+// and the bytes 1.9; 11008 x 4096: 6.7, with five tokens 8.3).  From numbers, every
+// work-group quantizes the activations anew, 0.2 us (16 bits) or 0.3 (f32) per 4096
+// values: with many tokens and long rows q8 blocks as the input are faster (16 x 4096
+// values, 4096 rows: 9.3 or 10.7 and 6.1 us, 5 x 4096: 5.8 or 6.3 and 5.2; the blocks
+// themselves take a launch of 2.5).
 #include "qmm_internal.h"
 #include "qmm_common.h"
 #include "qmm_epilogue.h"
@@ -196,7 +197,7 @@ struct MvArgs {
   int kg_bits;  // 2^kg_bits waves share a row tile,
   int groups;   // groups of them in a work-group
   uint32_t over_n_tok, over_per_unit;  // see over()
-  int db;  // threads / 4 / n_tok
+  int db;  // threads / 2 / n_tok
   int steps;    // sets of so many row tiles
 };
 
@@ -360,36 +361,38 @@ __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slo
 }
 
 // The activations of super-blocks [sb0, sb0 + n) of every token into LDS.  From
-// numbers: eight per thread, four threads per 32-block, the tokens of a block next to
-// each other, as LDS has them (4096 x 11008 q4_K, 16 tokens, 25.8 us: 1.8 less than with
-// the blocks of a token next to each other, in the same banks); the next eight are
-// loaded while these are quantized; begin() loads the first ones, so that the caller
-// can put other loads behind them.
+// numbers: sixteen per thread, two threads per 32-block, the tokens of a block next to
+// each other, as LDS has them; the next sixteen are loaded while these are quantized;
+// begin() loads the first ones, so that the caller can put other loads behind them.
+// Eight per thread repeat more of the shared work (4096 x 11008 q4_K, 16 tokens of bf16:
+// 26.1 instead of 20.7 us, 5 of f32: 11.7 and 11.1; one token of 2048: 3.7 and 3.8).
 template <bool Q6, int TOK, int XT>
 struct Quantizer {
-  typedef elem_t<XT> Eight __attribute__((ext_vector_type(8)));
-  Eight v;                       // as loaded: a conversion would wait here
-  int t, b, blocks, dt, db;      // a thread's token and 32-block of the part
+  static constexpr int kPer = 16;
+  typedef elem_t<XT> Part __attribute__((ext_vector_type(kPer)));
+  Part v;                    // as loaded: a conversion would wait here
+  int t, b, blocks, dt, db;  // a thread's token and 32-block of the part
   __device__ __forceinline__ void fetch(const MvArgs& a, int sb0) {
     if (b < blocks) {
-      const int64_t at = (int64_t)t * a.x_stride + (sb0 * 256 + 32 * b + 8 * (int)(threadIdx.x & 3));
-      typedef Eight Rows __attribute__((aligned(4 * sizeof(elem_t<XT>))));  // rows start at fours
+      const int64_t at = (int64_t)t * a.x_stride + (sb0 * 256 + 32 * b + kPer * (int)(threadIdx.x & 1));
+      typedef Part Rows __attribute__((aligned(4 * sizeof(elem_t<XT>))));  // rows start at fours
       v = *(const Rows*)((const elem_t<XT>*)a.x + at);
     }
   }
   __device__ __forceinline__ void begin(const MvArgs& a, int sb0, int n) {
     blocks = n * 8;
-    b = divide(threadIdx.x >> 2, a.over_n_tok);
-    t = (threadIdx.x >> 2) - __umul24(b, a.n_tok);
+    b = divide(threadIdx.x >> 1, a.over_n_tok);
+    t = (threadIdx.x >> 1) - __umul24(b, a.n_tok);
     db = a.db;  // the threads' stride in blocks and tokens
-    dt = threads_of(a) / 4 - db * a.n_tok;
+    dt = threads_of(a) / 2 - db * a.n_tok;
     fetch(a, sb0);
   }
   __device__ __forceinline__ void run(const MvArgs& a, uint8_t* lds, int sb_bytes, int sb0) {
     while (b < blocks) {
-      const float4 c0 = make_float4((float)v[0], (float)v[1], (float)v[2], (float)v[3]);
-      const float4 c1 = make_float4((float)v[4], (float)v[5], (float)v[6], (float)v[7]);
-      const int tok = t, at = 4 * b + (threadIdx.x & 3);
+      float c[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = (float)v[i];
+      const int tok = t, at = 4 * b + 2 * (threadIdx.x & 1);
       b += db;
       t += dt;
       if (t >= a.n_tok) {
@@ -397,10 +400,10 @@ struct Quantizer {
         ++b;
       }
       fetch(a, sb0);
-      const Q8Oct r = quant_oct(c0, c1);
+      const Q8Part<kPer> r = quant_part(c);
       const int slots = code_slots<TOK>(a.n_tok);
-      *(uint2*)place<Q6>(lds, sb_bytes, slots, tok, at) = make_uint2(r.codes[0], r.codes[1]);
-      if ((at & 3) == 0) place_scales<Q6, TOK>(lds, sb_bytes, slots, tok, at, r.pair);
+      *(uint4*)place<Q6>(lds, sb_bytes, slots, tok, at) = make_uint4(r.codes[0], r.codes[1], r.codes[2], r.codes[3]);
+      if ((at & 2) == 0) place_scales<Q6, TOK>(lds, sb_bytes, slots, tok, at, r.pair);
     }
   }
 };
@@ -531,15 +534,16 @@ mmv_kernel(MvArgs a, Epilogue ep) {
   const uint32_t e_at = threadIdx.x - __umul24(e_unit, per_unit);
   const int e_tok = e_at / kQuads, e_quad = e_at % kQuads;
 
-  // Its sides, early: behind the first step's weights, and a step ahead of the others'.
+  // Its sides, early: a step ahead, in front of the first with no quantizing to come,
+  // whose registers they would take.
   auto row_of = [&](int step) __attribute__((always_inline)) { return (step * groups + e_unit * kUnit) * kTile + 4 * e_quad; };
   auto left_of = [&](int row) __attribute__((always_inline)) { return e_unit < units ? min(a.od - row, 4) : 0; };
   int row = row_of(blockIdx.x), left = left_of(row);
   Sides side;
-  if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);
 
   for (int i = threadIdx.x; i < 16 * slots; i += threads_of(a)) zeros[i] = make_uint4(0, 0, 0, 0);
   if (one_tile) quant.run(a, lds, sb_bytes, 0);
+  if (!OUT8 && left > 0) side = load_sides(ep, e_tok, row, left);
   __syncthreads();
 
   int buf = 0;
@@ -650,7 +654,7 @@ hipError_t launch_kernel(const MvArgs& in, const Epilogue& ep, int num_cus, hipS
   a.groups = (int)std::min<int64_t>(kWaves >> a.kg_bits, OUT8 ? (share + 1) / 2 * 2 : share);
   a.steps = (int)((tiles + a.groups - 1) / a.groups);
   a.over_n_tok = over(a.n_tok);
-  a.db = threads_of(a) / 4 / a.n_tok;
+  a.db = threads_of(a) / 2 / a.n_tok;
   a.over_per_unit = over((OUT8 ? 8 : 4) * a.n_tok);
   const int grid = (int)std::min<int64_t>(a.steps, num_cus);
   if (lds > 64 * 1024) {

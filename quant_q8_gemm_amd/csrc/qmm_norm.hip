@@ -114,7 +114,8 @@ __device__ __forceinline__ Oct rounded(const Oct& x) {
 
 // Elements e .. e + 7 of token t: four lanes hold a q8 block.
 __device__ __forceinline__ void store_q8(uint8_t* qact, int64_t t_pad, int id, int64_t t, int e, const Oct& n) {
-  const Q8Oct r = quant_oct(n.a, n.b);
+  const float v[8] = {n.a.x, n.a.y, n.a.z, n.a.w, n.b.x, n.b.y, n.b.z, n.b.w};
+  const Q8Part<8> r = quant_part(v);
   const int sub = threadIdx.x & 3, tt = (int)(t & 31);
   const int64_t frag = (t >> 5) * (id >> 5) + (e >> 5);
   *(uint2*)(qact + frag * 1024 + (sub >> 1) * 512 + tt * 16 + (sub & 1) * 8) = make_uint2(r.codes[0], r.codes[1]);

@@ -102,8 +102,8 @@ __device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
   return {pack4(q), sc.pair(sum8(q[0] + q[1] + q[2] + q[3]))};
 }
 
-// The same block with eight consecutive values per lane, four lanes (4i .. 4i + 3):
-// half the shared work per value, and cheaper forms of the same numbers:
+// The same block with N = 8 consecutive values per lane, four lanes (4i .. 4i + 3), or
+// 16, two lanes: less shared work per value, and cheaper forms of the same numbers:
 //  * amax/127 with one Newton step on the quotient's remainder, q + (a - 127q)/127
 //    (Markstein): the correctly rounded quotient for every finite f32 whose
 //    quotient is normal (checked for every significand; smaller ones round to a
@@ -120,39 +120,41 @@ __device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
 //    even) in its low bits;
 //  * no clamp where dh is a normal f16: dh is then amax/127 to 2^-11, so that no
 //    quotient exceeds 127.07 and rounds above 127.
-struct Q8Oct {
-  uint32_t codes[2], pair;
+template <int N>
+struct Q8Part {
+  uint32_t codes[N / 4], pair;
 };
 
-__device__ __forceinline__ Q8Oct quant_oct(const float4& v0, const float4& v1) {
+template <int N>
+__device__ __forceinline__ Q8Part<N> quant_part(const float (&v)[N]) {
+  static_assert(N == 8 || N == 16, "four or two lanes");
   constexpr float kRound = 12582912.0f;      // 1.5 * 2^23
   constexpr float kHalfMin = 6.103515625e-5f;  // the smallest normal f16
-  const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
   float top = fabsf(v[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+  for (int i = 1; i < N; ++i) top = fmaxf(top, fabsf(v[i]));
   uint32_t u = __builtin_bit_cast(uint32_t, top);
   u = max(u, (uint32_t)dpp<kDppQuadXor1>((int)u));
-  u = max(u, (uint32_t)dpp<kDppQuadXor2>((int)u));
+  if (N == 8) u = max(u, (uint32_t)dpp<kDppQuadXor2>((int)u));
   const float amax = __builtin_bit_cast(float, u);
   const float q0 = amax * (1.0f / 127.0f);
   const Q8Scale sc((_Float16)fmaf(fmaf(-127.0f, q0, amax), 1.0f / 127.0f, q0));
-  float n[8];
+  float n[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < N; ++i) {
     const float r = v[i] * sc.inv;
     n[i] = fmaf(fmaf(-r, sc.dhf, v[i]), sc.inv, r);
   }
   if (sc.dhf < kHalfMin) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = __builtin_amdgcn_fmed3f(n[i], -127.0f, 127.0f);
+    for (int i = 0; i < N; ++i) n[i] = __builtin_amdgcn_fmed3f(n[i], -127.0f, 127.0f);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) n[i] += kRound;
-  Q8Oct r;
+  for (int i = 0; i < N; ++i) n[i] += kRound;
+  Q8Part<N> r;
   int S = 0;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < N / 4; ++k) {
     const uint32_t a = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, n[4 * k + 1]),
                                              __builtin_bit_cast(uint32_t, n[4 * k]), 0x0C0C0400u);
     const uint32_t b = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, n[4 * k + 3]),
@@ -161,7 +163,7 @@ __device__ __forceinline__ Q8Oct quant_oct(const float4& v0, const float4& v1) {
     S = __builtin_amdgcn_sdot4((int)r.codes[k], 0x01010101, S, false);
   }
   S += dpp<kDppQuadXor1>(S);
-  S += dpp<kDppQuadXor2>(S);
+  if (N == 8) S += dpp<kDppQuadXor2>(S);
   r.pair = sc.pair(S);
   return r;
 }
