@@ -325,8 +325,11 @@ int qmm_norm_quantize(const qmm_norm *args, int64_t n_tok, int64_t id, void *str
  * scratch is one device buffer per (device, stream) of 64 KiB per compute unit
  * (16 MiB on MI355X), allocated with hipMalloc by the first call on that stream
  * that needs it and kept until qmm_stream_release or the end of the process;
- * calls on one stream share it in stream order.  Synchronize a stream before destroying it if an MMQ on it
- * may still run.  Results are deterministic: the same call gives the same bits.
+ * calls on one stream share it in stream order, also when several threads make
+ * them (a call's two kernels are enqueued with nothing in between).  For
+ * hipStreamPerThread it is one buffer per (device, thread).  Synchronize a stream
+ * before destroying it if an MMQ on it may still run.  Results are deterministic:
+ * the same call gives the same bits.
  * Errors: QMM_EINVAL (also for a shape whose tiles exceed one launch: n_tok * od
  * beyond about 6.9e10, i.e. an output of 275 GB), QMM_ESHAPE, QMM_ENOMEM (the
  * scratch), QMM_EHIP.
@@ -338,7 +341,8 @@ int qmm_mmq(const qmm_weights *w, const void *qact, size_t qact_bytes, int64_t n
  * qmm_stream_release -- give back the device memory qmm_mmq keeps for `stream`
  * (the tail-partials scratch above, on every device it was allocated for), for
  * callers that create and destroy streams: call it before destroying the
- * stream.  It synchronizes `stream` first (an MMQ on it may still read the
+ * stream, with hipStreamPerThread before the thread ends (it gives back the calling
+ * thread's).  It synchronizes `stream` first (an MMQ on it may still read the
  * partials), then frees; a later qmm_mmq on the same stream allocates again.
  *   freed_bytes  NULL, or receives the bytes freed (0 if the stream held none).
  * A stream that holds nothing returns QMM_OK without any HIP call.  Not safe
@@ -358,7 +362,8 @@ int qmm_stream_release(void *stream, size_t *freed_bytes);
  * looked up (hipGetSymbolAddress) on the first call on each device.
  *   - Every call on one GPU shares that GPU's array and leaves the last call's
  *     partials in it: calls that may overlap on one GPU (different streams
- *     without ordering between them) race.  Calls on one stream are ordered.
+ *     without ordering between them) race.  Calls on one stream are ordered, from
+ *     one thread or several.
  *   - Nothing in the array needs clearing: each partial is written whole
  *     before it is read.
  *   - A launch that needs more than 16 MiB of partials (only on GPUs with more
@@ -413,7 +418,8 @@ typedef struct {
  *               aligned, work_bytes of it, at least the plan's scratch_bytes
  *               (qmm_mmq_plan; few tokens need none): the call then allocates
  *               nothing and can be captured, and calls with work memory of their
- *               own may overlap.
+ *               own may overlap.  Calls that share it have to be on one stream (or
+ *               ordered otherwise).
  *               NULL with work_bytes 0: the stream's scratch, as qmm_mmq; a
  *               captured call that needs scratch is then refused, since graphs
  *               replayed side by side would share it.

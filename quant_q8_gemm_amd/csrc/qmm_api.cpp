@@ -39,11 +39,31 @@ std::atomic<size_t> g_cap{0};   // 0 = no cap
 struct Scratch {
   int device;
   hipStream_t stream;
+  uint64_t thread;  // hipStreamPerThread: whose stream (this_thread), else 0
   void* ptr;
   size_t bytes;
 };
 std::mutex g_scratch_mu;
 std::vector<Scratch> g_scratch;
+
+// hipStreamPerThread is one handle for a stream of each thread, whose work
+// overlaps.  Numbers are not used again (a thread's scratch may outlive it).
+uint64_t this_thread(hipStream_t s) {
+  static std::atomic<uint64_t> last{0};
+  thread_local const uint64_t mine = ++last;
+  return s == hipStreamPerThread ? mine : 0;
+}
+
+// Held while a product with a split tail and the kernel that adds its partials
+// are enqueued: with another call's product between the two on the stream, the
+// second would add that call's partials.  A stream always takes the same one of
+// these; two streams that share one wait for each other's launches only.
+std::unique_lock<std::mutex> launch_turn(hipStream_t s, size_t scratch_bytes) {
+  static std::mutex turns[64];
+  if (scratch_bytes == 0) return {};
+  const uintptr_t v = (uintptr_t)s;
+  return std::unique_lock<std::mutex>(turns[(v ^ (v >> 6) ^ (v >> 12)) % 64]);
+}
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -581,7 +601,7 @@ int stream_scratch(int device, int num_cus, hipStream_t s, void** scratch) {
   const size_t max_bytes = qmm::mmq_scratch_max_bytes(num_cus);
   std::lock_guard<std::mutex> lock(g_scratch_mu);
   for (const Scratch& sc : g_scratch)
-    if (sc.device == device && sc.stream == s) *scratch = sc.ptr;
+    if (sc.device == device && sc.stream == s && sc.thread == this_thread(s)) *scratch = sc.ptr;
   if (*scratch != nullptr) return QMM_OK;
   hipError_t e = hipMalloc(scratch, max_bytes);
   if (e != hipSuccess) {
@@ -589,7 +609,7 @@ int stream_scratch(int device, int num_cus, hipStream_t s, void** scratch) {
     return e == hipErrorOutOfMemory ? fail(QMM_ENOMEM, "hipMalloc(%zu) for the tail partials failed", max_bytes)
                                     : fail_hip(e, "hipMalloc(tail partials)");
   }
-  g_scratch.push_back({device, s, *scratch, max_bytes});
+  g_scratch.push_back({device, s, this_thread(s), *scratch, max_bytes});
   return QMM_OK;
 }
 
@@ -611,6 +631,7 @@ int qmm_mmq(const qmm_weights* w, const void* qact, size_t qact_bytes, int64_t n
   void* scratch = nullptr;
   if (plan.scratch_bytes > 0)
     if (int rc = stream_scratch(device, num_cus, s, &scratch)) return rc;
+  const auto turn = launch_turn(s, plan.scratch_bytes);
   hipError_t e = qmm::launch_mmq(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), out,
                                  (float*)scratch, s);
   if (e != hipSuccess) return fail_hip(e, "mmq launch");
@@ -625,7 +646,7 @@ int qmm_stream_release(void* stream, size_t* freed_bytes) {
   bool synced = false;
   int cur = -1;
   for (size_t i = 0; i < g_scratch.size();) {
-    if (g_scratch[i].stream != s) {
+    if (g_scratch[i].stream != s || g_scratch[i].thread != this_thread(s)) {
       ++i;
       continue;
     }
@@ -666,6 +687,7 @@ int qmm_mmq_noalloc(const qmm_weights* w, const void* qact, size_t qact_bytes, i
     hipError_t e = qmm::static_scratch(device, &part);
     if (e != hipSuccess) return fail_hip(e, "hipGetSymbolAddress(static tail scratch)");
   }
+  const auto turn = launch_turn((hipStream_t)stream, plan.scratch_bytes);
   hipError_t e = qmm::launch_mmq(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), out, part,
                                  (hipStream_t)stream);
   if (e != hipSuccess) return fail_hip(e, "mmq launch");
@@ -726,6 +748,7 @@ int qmm_mmq_epilogue(const qmm_weights* w, const void* qact, size_t qact_bytes, 
                   plan.scratch_bytes);
     if (int rc = stream_scratch(device, num_cus, s, &scratch)) return rc;
   }
+  const auto turn = launch_turn(s, plan.scratch_bytes);
   hipError_t e = qmm::launch_mmq_epilogue(w->p, plan, (const uint8_t*)qact, n_tok, token_pad(n_tok), r,
                                           (float*)scratch, s);
   if (e != hipSuccess) return fail_hip(e, "mmq launch");
