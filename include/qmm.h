@@ -295,8 +295,9 @@ typedef struct {
  * At least one of h_out, normed and qact is given; everything is computed in
  * f32, and the second norm is that of s as `type` holds it, whether h_out is
  * stored or not.  A row's result does not depend on the other rows or on which
- * outputs are wanted.  Values whose squares overflow f32 when summed give
- * infinities or NaN in their own row only.
+ * outputs are wanted.  A row whose squares do not add up to a finite f32 (it holds
+ * an infinity or NaN, or the sum passes 3.4e38) has NaN as its norm in every
+ * element; other rows do not change.
  * An output may be one of the inputs in place (same pointer and stride): h_out
  * may be h or y; normed may be y, or h where h_out is NULL.  Any other overlap
  * of an output with h, y, gate or another output is refused.

@@ -59,6 +59,12 @@ struct Stats {
   float mean, rstd;
 };
 
+// 1/sqrt of a mean square.  NaN where the squares did not add up in f32: the 0 that
+// 1/sqrt of infinity is would make clean zeros of such a row.
+__device__ __forceinline__ float inverse_root(float square) {
+  return square < __builtin_inff() ? rsqrtf(square) : __builtin_nanf("");
+}
+
 // Eight consecutive elements of a row in one thread.
 struct Oct {
   float4 a, b;
@@ -183,7 +189,7 @@ norm_kernel(qmm_norm a, int64_t t_pad, int n_tok, int id) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (e0 + v * step < id) s += squares(x[v], st.mean);
-    st.rstd = rsqrtf(group_sum(s, red.sums[at + 1]) * inv_id + a.eps);
+    st.rstd = inverse_root(group_sum(s, red.sums[at + 1]) * inv_id + a.eps);
     return st;
   };
 
@@ -269,7 +275,7 @@ norm_long_kernel(qmm_norm a, int64_t t_pad, int n_tok, int id) {
     }
     float s = 0.0f;
     for (int e = e0; e < id; e += step) s += squares(get(e), st.mean);
-    st.rstd = rsqrtf(group_sum(s, red.sums[at + 1]) * inv_id + a.eps);
+    st.rstd = inverse_root(group_sum(s, red.sums[at + 1]) * inv_id + a.eps);
     return st;
   };
   Stats post{0.0f, 0.0f};

@@ -56,3 +56,41 @@ def test_every_activation_keeps_nan_and_infinity(device, case):
         if act in ("none", "relu"):
             assert (got[:, 40] == (-INF if act == "none" else 0)).all(), act
     w.release()
+
+
+def overflowing(T, id_, dtype, dev):
+    """(rows, the same with rows 1 to 4 whose squares do not add up in f32: an infinity, 3e38, one of 3e19, NaN)"""
+    h = torch.randn((T, id_), device=dev, generator=torch.Generator(device=dev).manual_seed(id_)).to(dtype)
+    bad = h.clone()
+    bad[1, 7] = INF
+    bad[2] = torch.where(torch.arange(id_, device=dev) % 2 == 0, 3e38, -3e38).to(dtype)
+    bad[3, id_ - 1] = -3e19
+    bad[4, 100] = NAN
+    return h, bad
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("id_", [256, 768, 9216, 33024])
+def test_norm_of_a_row_whose_squares_overflow_is_nan(device, id_, dtype, kind):
+    """Every element of it, of the norm before the next block and of the one after the block; other rows keep their
+    bits, and a row whose squares just add up is right."""
+    T = 7
+    print(f"norm {id_} {dtype} {kind}", flush=True)
+    h, bad = overflowing(T, id_, dtype, device)
+    bad[6] = (bad[6].float() * (1.2e19 / id_ ** 0.5 / bad[6].float().abs().amax())).to(dtype)  # squares below 1.5e38
+    weight = 1 + torch.randn(id_, device=device, generator=torch.Generator(device=device).manual_seed(1)) * 0.1
+    ref, got = (qmm.norm_quantize(v, weight, kind=kind, normed=True) for v in (h, bad))
+    assert torch.equal(got.normed[[0, 5]], ref.normed[[0, 5]])
+    assert torch.isnan(got.normed[1:5]).all()
+    v = bad[6].double()
+    v = v - v.mean() if kind == "layer" else v
+    want = v / (v ** 2).mean().sqrt() * weight.double()
+    # a sum's roundings (below 120 units of 2^-24 of its terms, at most 10 of a layer norm's mean beside), then half a
+    # step of the type
+    half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    assert ((got.normed[6].double() - want).abs() <= 250 * 2.0 ** -24 * (want.abs() + 1) + half * want.abs()).all()
+    y = torch.randn((T, id_), device=device, generator=torch.Generator(device=device).manual_seed(2)).to(dtype)
+    ref, got = (qmm.norm_quantize(y, weight, y=v, post_weight=weight, kind=kind, normed=True) for v in (h, bad))
+    assert torch.equal(got.h[[0, 5]], ref.h[[0, 5]]) and torch.equal(got.normed[[0, 5]], ref.normed[[0, 5]])
+    assert torch.isnan(got.h[1:5]).all() and torch.isnan(got.normed[1:5]).all()
