@@ -63,7 +63,7 @@ __device__ __forceinline__ float gelu(float x) {
 
 __device__ __forceinline__ float activate(float x, int act) {
   switch (act) {
-    case QMM_ACT_RELU: return x < 0.0f ? 0.0f : x;  // NaN stays NaN
+    case QMM_ACT_RELU: return __builtin_elementwise_maximum(x, 0.0f);  // NaN stays NaN
     case QMM_ACT_SILU: return times_sigmoid(x, x);
     case QMM_ACT_GELU: return gelu(x);
     case QMM_ACT_GELU_TANH:  // 0.5*x*(1 + tanh(z)) = x*sigmoid(2z), z = sqrt(2/pi)*(x + 0.044715*x^3)
