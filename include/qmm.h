@@ -213,7 +213,9 @@ size_t qmm_qact_bytes(int64_t n_tok, int64_t id);
  * int8 values plus 4 bytes; r56 section 1: "d/ssum").
  *   x           device f32 [n_tok][id], row major, 16-byte aligned.  Values
  *               must be finite with |x| <= 2046 (so the scaled sum fits f16);
- *               other values give unspecified (but memory-safe) results.
+ *               other values give unspecified (but memory-safe) results in their
+ *               block: after NaN or an infinity its scale is not finite either, so
+ *               that a token which reads it has no finite product.
  *   qact        device buffer of exactly qact_bytes = qmm_qact_bytes(n_tok, id)
  *               bytes, 16-byte aligned, fully overwritten.
  * Per token t and block c of 32 activations x_k:

@@ -21,8 +21,12 @@ __device__ __forceinline__ int dpp(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
 }
 
-// Maximum of non-negative finite floats over the 8 lanes, on their bit patterns
-// (ordered like the values), so each step is one integer max.
+// The larger of two magnitudes, NaN where one is (fmaxf would drop it, and a block that
+// holds NaN would come out as numbers).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(fabsf(a), fabsf(b)); }
+
+// Maximum of non-negative floats over the 8 lanes, on their bit patterns (ordered
+// like the values, NaN last), so each step is one integer max.
 __device__ __forceinline__ float max8(float v) {
   uint32_t u = __builtin_bit_cast(uint32_t, v);
   u = max(u, (uint32_t)dpp<kDppQuadXor1>((int)u));
@@ -96,7 +100,7 @@ struct Q8Quad {
 };
 
 __device__ __forceinline__ Q8Quad quant_quad(const float4& v) {
-  const Q8Scale sc(max8(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)))));
+  const Q8Scale sc(max8(larger(larger(v.x, v.y), larger(v.z, v.w))));
   int q[4];
   quant4(v, sc.dhf, sc.inv, q);
   return {pack4(q), sc.pair(sum8(q[0] + q[1] + q[2] + q[3]))};
@@ -132,7 +136,7 @@ __device__ __forceinline__ Q8Part<N> quant_part(const float (&v)[N]) {
   constexpr float kHalfMin = 6.103515625e-5f;  // the smallest normal f16
   float top = fabsf(v[0]);
 #pragma unroll
-  for (int i = 1; i < N; ++i) top = fmaxf(top, fabsf(v[i]));
+  for (int i = 1; i < N; ++i) top = larger(top, v[i]);
   uint32_t u = __builtin_bit_cast(uint32_t, top);
   u = max(u, (uint32_t)dpp<kDppQuadXor1>((int)u));
   if (N == 8) u = max(u, (uint32_t)dpp<kDppQuadXor2>((int)u));

@@ -94,3 +94,69 @@ def test_norm_of_a_row_whose_squares_overflow_is_nan(device, id_, dtype, kind):
     ref, got = (qmm.norm_quantize(y, weight, y=v, post_weight=weight, kind=kind, normed=True) for v in (h, bad))
     assert torch.equal(got.h[[0, 5]], ref.h[[0, 5]]) and torch.equal(got.normed[[0, 5]], ref.normed[[0, 5]])
     assert torch.isnan(got.h[1:5]).all() and torch.isnan(got.normed[1:5]).all()
+
+
+def dequantized_blocks(qact, T, n):
+    return qmm.dequantize_activations(qact, T, n).reshape(T, -1, 32)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("id_", [256, 768, 9216, 33024])
+def test_norm_blocks_of_a_row_that_is_nan(device, id_, kind):
+    h, bad = overflowing(7, id_, torch.float32, device)
+    weight = torch.ones(id_, device=device)
+    ref, got = (dequantized_blocks(qmm.norm_quantize(v, weight, kind=kind).qact, 7, id_) for v in (h, bad))
+    assert not torch.isfinite(got[1:5]).any()
+    assert torch.equal(got[[0, 5, 6]], ref[[0, 5, 6]])
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF, 1e30], ids=["nan", "inf", "-inf", "1e30"])
+@pytest.mark.parametrize("id_", [256, 4096])
+def test_blocks_of_activations(device, id_, value):
+    """A block with a value that is not finite, or too large for its scale, has a scale that is not finite; the others
+    keep their bits; and so does a product of them, of every kernel."""
+    T = 13
+    x = torch.randn((T, id_), device=device, generator=torch.Generator(device=device).manual_seed(3))
+    bad = x.clone()
+    bad[4, 77] = value
+    bad[12, id_ - 1] = value
+    ref, got = (qmm.quantize_activations(v) for v in (x, bad))
+    a, b = dequantized_blocks(ref, T, id_), dequantized_blocks(got, T, id_)
+    hit = torch.zeros(a.shape[:2], dtype=torch.bool, device=device)
+    hit[4, 77 // 32] = hit[12, -1] = True
+    assert not torch.isfinite(b[hit]).any() and torch.equal(a[~hit], b[~hit])
+    keep = [t for t in range(T) if t not in (4, 12)]
+    for type_ in (synth.Q4_K, synth.Q6_K):
+        raw = synth.weights(np.random.default_rng(1), type_, 300, id_)
+        w, wr = qmm.register_weights(type_, 300, id_, raw), qmm.register_weights(ROWS[type_], 300, id_, raw)
+        for name, f in (("mmq", lambda q, v: qmm.mmq(w, q, T)), ("few", lambda q, v: qmm.mmq_epilogue(w, q, T)),
+                        ("rows, blocks", lambda q, v: qmm.mmv(wr, q, T)), ("rows", lambda q, v: qmm.mmv(wr, v)),
+                        ("rows, f32 of 5", lambda q, v: qmm.mmv(wr, v[8:])),
+                        ("rows, of 1", lambda q, v: qmm.mmv(wr, v[12:]))):
+            print(id_, value, synth.TYPE_NAMES[type_], name, flush=True)
+            r, g = f(ref, x), f(got, bad)
+            first = T - r.shape[0]
+            for t in range(first, T):
+                if t in keep:
+                    assert torch.equal(r[t - first], g[t - first]), (name, t)
+                else:
+                    assert not torch.isfinite(g[t - first]).any(), (name, t)
+        w.release()
+        wr.release()
+
+
+@pytest.mark.parametrize("case", [("few", synth.Q4_K, 256, 512, 40), ("tail", synth.Q6_K, 4352, 2048, 509),
+                                  ("tiles", synth.Q4_K, 8192, 512, 600), ("rows", synth.Q4_K, 256, 512, 3),
+                                  ("rows", synth.Q6_K, 512, 512, 11)], ids=IDS)
+def test_blocks_of_a_products_output(device, case):
+    """NaN and infinities that an epilogue brings into values kept as q8 blocks show in their blocks, and only there."""
+    run, w = product(device, *case)
+    od, T = case[2], case[4]
+    c = {"mul": torch.randn((T, od), device=device), "residual": torch.randn((T, od), device=device), "scale": 0.25}
+    ref = dequantized_blocks(run(dtype="q8", **c), T, od)
+    c["mul"][1, 40], c["residual"][T - 1, od - 1], c["residual"][0, 3] = NAN, INF, NAN
+    got = dequantized_blocks(run(dtype="q8", **c), T, od)
+    hit = torch.zeros(ref.shape[:2], dtype=torch.bool, device=device)
+    hit[1, 1] = hit[T - 1, -1] = hit[0, 0] = True
+    assert not torch.isfinite(got[hit]).any() and torch.equal(got[~hit], ref[~hit])
+    w.release()
