@@ -47,16 +47,12 @@ template <int TYPE>
 using elem_t = typename Elem<TYPE>::type;
 
 template <int TYPE>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  return (float)((const elem_t<TYPE>*)p)[i];
-}
-template <int TYPE>
 __device__ __forceinline__ void store1(void* p, int64_t i, float f) {
   ((elem_t<TYPE>*)p)[i] = (elem_t<TYPE>)f;
 }
 // Four consecutive elements at p[i] .. p[i + 3] as one access; p + i is aligned to
-// four of them (load4, store4) or only to one (load4_any, store4_any: the hardware
-// takes such addresses, and the compiler keeps the access whole).
+// four of them (load4, store4) or only to one (store4_any: the hardware takes such
+// addresses, and the compiler keeps the access whole).
 template <int TYPE>
 __device__ __forceinline__ float4 load4(const void* p, int64_t i) {
   typedef elem_t<TYPE> v4 __attribute__((ext_vector_type(4)));
@@ -70,14 +66,6 @@ __device__ __forceinline__ void store4(void* p, int64_t i, const float4& f) {
   *(v4*)((T*)p + i) = v4{(T)f.x, (T)f.y, (T)f.z, (T)f.w};
 }
 
-template <int TYPE>
-__device__ __forceinline__ float4 load4_any(const void* p, int64_t i) {
-  typedef elem_t<TYPE> T;
-  typedef T v4 __attribute__((ext_vector_type(4)));
-  typedef v4 any __attribute__((aligned(sizeof(T))));
-  const v4 v = *(const any*)((const T*)p + i);
-  return make_float4((float)v.x, (float)v.y, (float)v.z, (float)v.w);
-}
 template <int TYPE>
 __device__ __forceinline__ void store4_any(void* p, int64_t i, const float4& f) {
   typedef elem_t<TYPE> T;

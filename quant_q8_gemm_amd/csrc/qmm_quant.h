@@ -68,9 +68,6 @@ __device__ __forceinline__ void quant4(const float4& v, float dhf, float inv, in
   for (int i = 0; i < 4; ++i) q[i] = (int)__builtin_amdgcn_fmed3f(n[i], -127.0f, 127.0f);
 }
 
-// A float's magnitude as a bit pattern, ordered like the values (max8 above).
-__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
-
 // The scale of a block whose largest magnitude is amax.
 struct Q8Scale {
   _Float16 dh;
