@@ -341,8 +341,8 @@ def _empty(like, shape, dtype, stream):
     strides = (shape[1], 1) if len(shape) == 2 else (1,)
     if stream is None:
         return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    if isinstance(stream, int):  # 0 is the null stream, which ExternalStream does not know
+        stream = torch.cuda.ExternalStream(stream, device=like.device) if stream else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
         return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
 
