@@ -33,7 +33,9 @@ LIB_FLAGS = DEVICE_FLAGS + MAX_ILP
 
 def _flags(source: str):
     """The few-token kernels keep the default strategy: they need their registers for
-    the loads in flight, and max-ILP spills them."""
+    the loads in flight, and max-ILP spills them (the default one still spills a few of
+    the q4_K kernels: from f32 numbers with several tokens, and one register of the
+    one-block kernel on the planes)."""
     return DEVICE_FLAGS if os.path.basename(source) in ("qmm_mmv.hip", "qmm_mmq_few.hip") else LIB_FLAGS
 
 

@@ -29,7 +29,12 @@ namespace qmm {
 // tokens).  More of them, a wave each, read the weights once each, mostly from cache,
 // and win while the work-groups fit one round of the CUs (4096 x 11008 q6_K, 64
 // tokens: 18.3 / 27.3), with short rows two (4096 x 4096 q4_K, 128 tokens: 10.0 /
-// 15.7; 4096 x 11008 q6_K: 29.3 / 27.7).  Past one round two token blocks share a
+// 15.7).  Over two rounds the lead shrinks with the rows' length: 4096 rows, 128 tokens,
+// at 8, 16, 24, 28, 32, 36 and 43 super-blocks q4_K 7.9 / 13.7, 11.5 / 16.9, 15.5 / 17.9,
+// 18.8 / 19.5, 19.7 / 20.9, 22.5 / 22.4, 25.2 / 25.2, q6_K 8.8 / 14.8, 14.3 / 17.2, 19.1 /
+// 21.1, 23.3 / 23.2, 24.3 / 25.1, 28.1 / 27.3, 31.6 / 30.8; hence 32.  Other shapes lie a
+// few super-blocks to either side (2752 rows, 160 tokens, 32: q6_K 38.7 / 35.4, packed 19.9
+// / 30.2).  Past one round two token blocks share a
 // wave (11008 x 4096 q4_K, 64 tokens: 17.3 / 24.4, a wave each 22.9; 32000 x 4096
 // q6_K: 48.7 / 66.4); within one, a wave each is better (4096 x 4096: 8.1, shared
 // 10.2), and for more than two the tiled kernel is (11008 x 4096, 96 tokens: shared

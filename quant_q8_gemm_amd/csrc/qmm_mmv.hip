@@ -365,7 +365,10 @@ __device__ __forceinline__ void place_scales(uint8_t* lds, int sb_bytes, int slo
 // each other, as LDS has them; the next sixteen are loaded while these are quantized;
 // begin() loads the first ones, so that the caller can put other loads behind them.
 // Eight per thread repeat more of the shared work (4096 x 11008 q4_K, 16 tokens of bf16:
-// 26.1 instead of 20.7 us, 5 of f32: 11.7 and 11.1; one token of 2048: 3.7 and 3.8).
+// 26.1 instead of 20.7 us, 5 of f32: 11.7 and 11.1; one token of 2048: 3.7 and 3.8).  With
+// f32 the sixteen beside two super-blocks of q4_K weights are more than the registers
+// hold: 2 or 3 spill from two tokens on, 14 with more than eight (6 to q8 blocks; 4096 x
+// 4096, 16 tokens: 10.7 us, of bf16 9.3); from 16 bits, q8 blocks and for q6_K none do.
 template <bool Q6, int TOK, int XT>
 struct Quantizer {
   static constexpr int kPer = 16;
