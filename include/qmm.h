@@ -459,6 +459,212 @@ int qmm_mmq_epilogue(const qmm_weights *w, const void *qact, size_t qact_bytes, 
 int qmm_mmv(const qmm_weights *w, const void *x, int x_type, int64_t x_stride, int64_t n_tok,
             const qmm_epilogue *ep, int out_type, void *out, int64_t out_stride, void *stream);
 
+/* ---- between the q, k, v products and the output product: positions, a paged cache, attention ---- */
+
+/* A paged cache of keys and values.  A slot holds one token's key (in the pool k)
+ * and value (in the pool v) of every head, head_dim channels each; a page holds
+ * `page` slots, and each pool n_pages pages of qmm_cache_page_bytes bytes,
+ * 16-byte aligned.  The caller owns the pools; nothing in them needs clearing (what
+ * no sequence's slot in use holds is never part of a result).
+ *   type     QMM_F16, QMM_BF16, or QMM_Q8: blocks of 32 channels of a slot, int8
+ *            codes and an f16 scale as qmm_quantize_activations makes them (the
+ *            scaled sum left out; |values| <= 2046 as there), 1.0625 bytes a value
+ *   head_dim 64, 96, 128, 192 or 256
+ *   page     a power of two in [32, QMM_MAX_PAGE]
+ * Layout of a pool (the fragment order of the matrix instructions): pages, in a
+ * page heads, in a head tiles of 32 slots.  In a tile, of slot r and channel d,
+ * with D = head_dim and m(r) = r with its bits 2 and 3 exchanged,
+ *   16 bits  k: element ((d/16*2 + d%16/8)*32 + m(r))*8 + d%8
+ *            v: element ((d/32*4 + r/8)*32 + d%32)*8 + r%8
+ *   q8       k: byte d/32*1024 + ((d%16/8)*32 + m(r))*16 + d%32/16*8 + d%8
+ *            v: byte d/32*1024 + ((r%16/8)*32 + d%32)*16 + r/16*8 + r%8
+ *            each the code plus 128; both pools: the f16 scale of block d/32 at
+ *            byte 32*D + (d/32*32 + r)*2 */
+#define QMM_MAX_PAGE 65536
+#define QMM_MAX_HEADS 4096
+typedef struct {
+    int32_t type;
+    int32_t heads;    /* of keys and values, 1 .. QMM_MAX_HEADS */
+    int32_t head_dim;
+    int32_t page;
+    int64_t n_pages;  /* 1 .. 2^31 - 1 */
+    void *k, *v;      /* the pools, device memory */
+} qmm_cache;
+
+/* qmm_cache_page_bytes -- bytes of one page of one pool; 0 if an argument is out of
+ * range. */
+size_t qmm_cache_page_bytes(int type, int heads, int head_dim, int page);
+
+/* The sequences of a call.  Sequence s has the call's tokens (rows) starts[s] ..
+ * starts[s + 1] - 1, any number of them, none included, and lengths[s] slots in use
+ * of the cache, of which its tokens of this call are the last: token i of n has slot
+ * lengths[s] - n + i.  Slot j is slot j % page of page table[s][j / page].
+ * The arrays are device memory, read when the kernels run.  Whatever they hold,
+ * nothing outside the tensors and pools is read or written: starts are taken
+ * within [0, n_tok] and not to go down, lengths within the table's columns;
+ * tokens without a slot (more than lengths[s]) and pages outside the pool are not
+ * followed: nothing is stored to them, and their keys are not seen.
+ * max_new, max_length: the most tokens and the most slots of any sequence, to size
+ * the launch by; sequences that pass them are worked through all the same, only
+ * slower. */
+#define QMM_MAX_SEQS 65535
+typedef struct {
+    int32_t n_seq;         /* 1 .. QMM_MAX_SEQS */
+    int32_t columns;       /* of the table, >= 1; columns * page < 2^31 */
+    const int32_t *starts; /* [n_seq + 1] */
+    const int32_t *lengths;/* [n_seq] */
+    const int32_t *table;  /* [n_seq] rows of `columns` page numbers */
+    int64_t table_stride;  /* elements from row to row, >= columns */
+    int64_t max_new;       /* 0 .. QMM_MAX_TOKENS */
+    int64_t max_length;    /* 0 .. 2^31 - 1 */
+} qmm_batch;
+
+/* Rotary scalings for long contexts (qmm_rope_frequencies). */
+#define QMM_ROPE_PLAIN 0
+#define QMM_ROPE_LINEAR 1 /* every frequency divided by factor */
+#define QMM_ROPE_BASE 2   /* the base times factor^(n_rot / (n_rot - 2)): the fastest pair stays, the slowest is divided */
+#define QMM_ROPE_YARN 3   /* a ramp over the pairs from those that turn `fast` times in the original context, which
+                             stay, to those that turn `slow` times, which are divided by factor; its ends are whole
+                             pairs; magnitude 0.1 ln(factor) + 1 (1 where factor <= 1) */
+#define QMM_ROPE_TURNS 4  /* the same with the ramp over the turns themselves, magnitude 1 */
+
+/*
+ * qmm_rope_frequencies -- the angle per position, in radians, of each of the n_rot/2
+ * pairs: base^(-2i/n_rot), scaled.  Host arithmetic in 64 bits only; the caller
+ * copies them to the device once.
+ *   n_rot       a multiple of 16 in [16, 256]
+ *   base        > 1, finite
+ *   scaling     QMM_ROPE_*; factor > 0; YARN and TURNS: original > 0 (the context
+ *               before scaling), fast > slow > 0
+ *   frequencies host [n_rot / 2];  magnitude  host, or NULL
+ * Errors: QMM_EINVAL.
+ */
+int qmm_rope_frequencies(int64_t n_rot, double base, int scaling, double factor, double original, double fast,
+                         double slow, double *frequencies, float *magnitude);
+
+#define QMM_ROPE_HALF 0        /* pair i: channels i and i + n_rot/2 */
+#define QMM_ROPE_INTERLEAVED 1 /* pair i: channels 2i and 2i + 1 */
+
+/* What qmm_rope_cache works on.  Zero the struct, then set what is wanted.  q, k
+ * and v are device tensors [n_tok][heads][head_dim] with adjacent channels;
+ * strides in elements, of tokens and heads, multiples of 8 in [head_dim,
+ * QMM_MAX_STRIDE] (any value where there is one token or one head); 16-byte
+ * aligned. */
+typedef struct {
+    int32_t type;      /* QMM_F32, QMM_F16 or QMM_BF16: q, k, v */
+    int32_t out_type;  /* of q_out */
+    int32_t q_heads;   /* 1 .. QMM_MAX_HEADS, with q */
+    int32_t layout;    /* QMM_ROPE_HALF or QMM_ROPE_INTERLEAVED */
+    int32_t n_rot;     /* channels rotated, a multiple of 16 in [0, head_dim] */
+    float magnitude;   /* factor of the rotated channels, finite */
+    const double *frequencies;  /* device [n_rot / 2] (not with n_rot 0) */
+    const int32_t *positions;   /* device [n_tok], or NULL: a token's slot is its position */
+    const void *q;              /* queries, or NULL */
+    int64_t q_stride, q_head_stride;
+    void *q_out;                /* receives them rotated */
+    int64_t q_out_stride, q_out_head_stride;
+    const void *k;              /* keys, rotated and kept in the cache, or NULL */
+    int64_t k_stride, k_head_stride;
+    const void *v;              /* values, kept in the cache as they are, or NULL */
+    int64_t v_stride, v_head_stride;
+} qmm_rope;
+
+/*
+ * qmm_rope_cache -- the new tokens' queries and keys turned by their positions, and
+ * keys and values kept in their slots, in one pass:
+ *   pair (a, b) at position p with frequency f: t = p * f,
+ *   (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t)
+ * t is formed and reduced in 64 bits, the rest is f32; a result is rounded once to
+ * the type it is kept in (q8: the blocks of the f32 values).  Channels from n_rot on
+ * stay as they are.
+ *   cache     k and v, where given, go there; with q alone its head_dim counts
+ *   args      at least one of q, k and v
+ * q_out may be q in place (same type, pointer and strides); any other overlap of
+ * an output with an input is refused.  Rows of tokens of no sequence are left as
+ * they are, and slots of other tokens too.  Two tokens of a call never have one
+ * slot unless the table gives two sequences one page: which of them stays is then
+ * open.
+ * No workspace; can be captured into a graph.
+ * Errors: QMM_EINVAL, QMM_EHIP.  n_tok == 0 is an empty batch.
+ */
+int qmm_rope_cache(const qmm_rope *args, const qmm_cache *cache, const qmm_batch *batch, int64_t n_tok, void *stream);
+
+/*
+ * qmm_cache_read -- the keys and values that the cache holds for the batch's tokens
+ * (their slots as above), as numbers: with starts spaced by the lengths, whole
+ * sequences.
+ *   type        QMM_F32, QMM_F16 or QMM_BF16
+ *   k, v        device [n_tok][heads][head_dim], contiguous, 16-byte aligned; either
+ *               may be NULL.  Rows of tokens of no sequence are left as they are;
+ *               tokens without a slot, or in a page outside the pool, are zeros.
+ * Errors: QMM_EINVAL, QMM_EHIP.
+ */
+int qmm_cache_read(const qmm_cache *cache, const qmm_batch *batch, int64_t n_tok, int type, void *k, void *v,
+                   void *stream);
+
+/* What qmm_attention works on.  Zero the struct, then set what is wanted. */
+typedef struct {
+    int32_t heads;     /* of q: a multiple of the cache's */
+    int32_t causal;    /* 1: a token sees the slots up to its own; 0: all in use (an
+                          encoder's states, of a length that has nothing to do with
+                          the tokens') */
+    int32_t out_type;  /* q's type (QMM_F16, QMM_BF16) or QMM_Q8 */
+    float scale;       /* of the scores, > 0, finite */
+    int64_t window;    /* causal: of those only the last `window`; 0: all */
+    const void *q;     /* device [n_tok][heads][head_dim], adjacent channels, of the
+                          cache's type (QMM_F16 with a q8 cache), 16-byte aligned */
+    int64_t q_stride, q_head_stride;  /* as in qmm_rope */
+    void *out;         /* [n_tok] rows of heads * head_dim elements, out_stride from row
+                          to row, a multiple of 8; 16-byte aligned.  QMM_Q8: a qact buffer of
+                          qmm_qact_bytes(n_tok, heads * head_dim) bytes, and
+                          out_stride that number: the output product's input */
+    int64_t out_stride;
+} qmm_attn;
+
+/*
+ * qmm_attention -- attention of the batch's tokens over the cache: for token i,
+ * head h and the keys j that it sees, of cache head h / (heads / cache heads),
+ *   p_j = exp(scale * q.k_j - max_j),   out = sum_j p_j v_j / sum_j p_j
+ * Products are of 16-bit values summed in f32; maximum and sum are f32; p_j is
+ * rounded to q's type for the second product, q8 keys and values to f16.  A token
+ * that sees no key, or none whose score is above -infinity, gets zeros.  What a
+ * token does not see is no part of its result, whatever is stored there.  An output
+ * in q8 blocks has its padding tokens zero; rows of tokens of no sequence are
+ * left as they are.
+ *   work      device memory of at least the plan's work_bytes (qmm_attention_plan),
+ *             16-byte aligned; NULL with 0 where it needs none.  Calls that share it
+ *             have to be on one stream (or ordered otherwise); nothing in it needs
+ *             clearing.
+ * The output must not overlap an input or the work memory.  Deterministic: the
+ * same call gives the same bits.  Can be captured into a graph.
+ * Errors: QMM_EINVAL, QMM_EHIP.  n_tok == 0 is an empty batch.
+ */
+int qmm_attention(const qmm_attn *args, const qmm_cache *cache, const qmm_batch *batch, int64_t n_tok, void *work,
+                  size_t work_bytes, void *stream);
+
+/* How a qmm_attention is launched: the (token, head of its group) pairs of a
+ * sequence and a cache head are columns, taken `columns` at a time; the keys of
+ * such a tile are split into `splits` parts of whole 32-slot tiles, whose partial
+ * results a second kernel joins. */
+typedef struct {
+    size_t work_bytes;   /* partial results (0: none) */
+    int64_t work_groups;
+    int32_t few;         /* 1: few columns, the waves of a work-group take turns over
+                            the keys; 0: each takes columns of its own */
+    int32_t columns;
+    int32_t tiles;       /* column tiles of a sequence and cache head with max_new */
+    int32_t splits;
+} qmm_attn_plan;
+
+/*
+ * qmm_attention_plan -- the plan of qmm_attention for these sizes on a GPU with
+ * num_cus compute units; host arithmetic only.  Of `cache` type, heads and head_dim
+ * count, of `batch` n_seq, max_new and max_length.
+ * Errors: QMM_EINVAL.
+ */
+int qmm_attention_plan(const qmm_cache *cache, const qmm_batch *batch, int heads, int64_t n_tok, int num_cus,
+                       qmm_attn_plan *out);
+
 /* The launch plan of one MMQ (qmm_mmq, qmm_mmq_noalloc): how its output tiles
  * map onto work-groups on a GPU of a given size, and the tail partials it needs.
  * The slots are the work-groups resident at once (per_cu per compute unit).  The

@@ -57,13 +57,18 @@ BLOCK_BYTES = {Q4_K: 144, Q4_K_PACKED: 144, Q6_K: 210, Q4_K_ROWS: 144, Q6_K_ROWS
 EXPORTS = ("qmm_register_weights", "qmm_weights_info", "qmm_weights_export", "qmm_release_weights",
            "qmm_set_memory_cap", "qmm_qact_bytes", "qmm_quantize_activations", "qmm_mmq",
            "qmm_mmq_noalloc", "qmm_stream_release", "qmm_mmq_plan", "qmm_mmq_plan_work", "qmm_last_error",
-           "qmm_dequantize_activations", "qmm_norm_quantize", "qmm_mmq_epilogue", "qmm_mmv")
+           "qmm_dequantize_activations", "qmm_norm_quantize", "qmm_mmq_epilogue", "qmm_mmv",
+           "qmm_cache_page_bytes", "qmm_rope_frequencies", "qmm_rope_cache", "qmm_cache_read", "qmm_attention",
+           "qmm_attention_plan")
 MAX_CUS = 65536
 # element types of activation tensors
 F32, F16, BF16 = 0, 1, 2
 ELEM_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 NORM_KINDS = {"rms": 0, "layer": 1}
 Q8 = 3  # as the output of a product: q8 blocks
+MAX_TOKENS = 1 << 20
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "turns": 4}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
@@ -97,6 +102,39 @@ class Epilogue(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("act", ctypes.c_int32), ("type", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("residual_scale", ctypes.c_float), ("mul", ctypes.c_void_p),
                 ("mul_stride", ctypes.c_int64), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64)]
+
+
+class CacheStruct(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class BatchStruct(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("columns", ctypes.c_int32), ("starts", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_new", ctypes.c_int64), ("max_length", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("n_rot", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("frequencies", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("k_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64)]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("causal", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64)]
+
+
+class AttnPlan(ctypes.Structure):
+    _fields_ = [("work_bytes", ctypes.c_size_t), ("work_groups", ctypes.c_int64), ("few", ctypes.c_int32),
+                ("columns", ctypes.c_int32), ("tiles", ctypes.c_int32), ("splits", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -135,6 +173,20 @@ _lib.qmm_mmq_epilogue.argtypes = [_P, _P, _SZ, _I64, ctypes.POINTER(Epilogue), c
 _lib.qmm_mmq_epilogue.restype = ctypes.c_int
 _lib.qmm_mmv.argtypes = [_P, _P, ctypes.c_int, _I64, _I64, ctypes.POINTER(Epilogue), ctypes.c_int, _P, _I64, _P]
 _lib.qmm_mmv.restype = ctypes.c_int
+_D = ctypes.c_double
+_lib.qmm_cache_page_bytes.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+_lib.qmm_cache_page_bytes.restype = _SZ
+_lib.qmm_rope_frequencies.argtypes = [_I64, _D, ctypes.c_int, _D, _D, _D, _D, _P, _P]
+_lib.qmm_rope_frequencies.restype = ctypes.c_int
+_CB = [ctypes.POINTER(CacheStruct), ctypes.POINTER(BatchStruct)]
+_lib.qmm_rope_cache.argtypes = [ctypes.POINTER(Rope), *_CB, _I64, _P]
+_lib.qmm_rope_cache.restype = ctypes.c_int
+_lib.qmm_cache_read.argtypes = [*_CB, _I64, ctypes.c_int, _P, _P, _P]
+_lib.qmm_cache_read.restype = ctypes.c_int
+_lib.qmm_attention.argtypes = [ctypes.POINTER(Attn), *_CB, _I64, _P, _SZ, _P]
+_lib.qmm_attention.restype = ctypes.c_int
+_lib.qmm_attention_plan.argtypes = [*_CB, ctypes.c_int, _I64, ctypes.c_int, ctypes.POINTER(AttnPlan)]
+_lib.qmm_attention_plan.restype = ctypes.c_int
 _lib.qmm_last_error.argtypes = []
 _lib.qmm_last_error.restype = ctypes.c_char_p
 
@@ -510,3 +562,216 @@ def mmv(w: Weights, x, n_tok: int = None, *, bias=None, act: str = "none", mul=N
     _check(_lib.qmm_mmv(w.handle, x_ptr, x_type, x_stride, n_tok, ep, out_type, out_ptr, out_stride,
                         _raw_stream(stream, device)))
     return out
+
+
+# ---- between the q, k, v products and the output product: positions, a paged cache, attention ----
+
+def rope_frequencies(n_rot: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     original: float = 4096.0, fast: float = 32.0, slow: float = 1.0, device=None):
+    """(frequencies, magnitude) of rope_cache: the angle per position of each of the n_rot/2 pairs (float64, on the
+    device) and the factor of what is rotated.  scaling: "none", "linear", "base", "yarn" or "turns" (include/qmm.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise QmmError(EINVAL, f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    f = (ctypes.c_double * max(1, n_rot // 2))()
+    magnitude = ctypes.c_float()
+    _check(_lib.qmm_rope_frequencies(n_rot, base, ROPE_SCALINGS[scaling], factor, original, fast, slow, f,
+                                     ctypes.byref(magnitude)))
+    return torch.tensor(list(f), dtype=torch.float64).to("cuda" if device is None else device), magnitude.value
+
+
+class Cache:
+    """A paged cache of keys and values: n_pages pages of `page` slots (a power of two from 32 on) of `heads` heads of
+    head_dim channels, held as float16, bfloat16 or "q8" (blocks of 32 channels).  k and v are the pools, flat uint8
+    tensors, zero at first; give both to use memory of your own."""
+
+    def __init__(self, n_pages: int, heads: int, head_dim: int, *, page: int = 64, dtype=torch.float16, k=None, v=None,
+                 device=None):
+        type_ = Q8 if dtype == "q8" else ELEM_TYPES.get(dtype, -1)
+        nbytes = n_pages * int(_lib.qmm_cache_page_bytes(type_, heads, head_dim, page)) if n_pages > 0 else 0
+        if nbytes == 0:
+            raise QmmError(EINVAL, f"no cache of {n_pages} pages of {page} slots, {heads} heads of {head_dim}, {dtype}")
+        if (k is None) != (v is None):
+            raise QmmError(EINVAL, "k and v come together")
+        if k is None:
+            device = "cuda" if device is None else device
+            k, v = (torch.zeros(nbytes, dtype=torch.uint8, device=device) for _ in range(2))
+        for t in (k, v):
+            if t.dtype != torch.uint8 or t.shape != (nbytes,) or not t.is_contiguous() or t.get_device() != k.get_device():
+                raise QmmError(EINVAL, f"k and v must be contiguous uint8 tensors of {nbytes} bytes on one device")
+        self.k, self.v, self.dtype = k, v, dtype
+        self.n_pages, self.heads, self.head_dim, self.page = n_pages, heads, head_dim, page
+        self.device = k.get_device()
+        self.struct = CacheStruct(type_, heads, head_dim, page, n_pages, k.data_ptr(), v.data_ptr())
+
+    def views(self):
+        """What a float16 or bfloat16 cache holds, as strided views of its pools with the slots' and channels' indexes
+        split: k [n_pages][heads][page/32][2][2][2][4][head_dim/16][2][8], v [n_pages][heads][page/32][2][2][8]
+        [head_dim/32][32]; reshape(n_pages, heads, page, head_dim) of either is a copy in plain order."""
+        if self.dtype == "q8":
+            raise QmmError(EINVAL, "a q8 cache holds codes and scales: cache_read gives their numbers")
+        tiles, d = (self.n_pages, self.heads, self.page // 32), self.head_dim
+        k = self.k.view(self.dtype).view(*tiles, d // 16, 2, 2, 2, 2, 4, 8).permute(0, 1, 2, 5, 7, 6, 8, 3, 4, 9)
+        v = self.v.view(self.dtype).view(*tiles, d // 32, 2, 2, 32, 8).permute(0, 1, 2, 4, 5, 7, 3, 6)
+        return k, v
+
+
+class Batch:
+    """The sequences of a call: starts int32 [n_seq + 1] (sequence s has rows starts[s] .. starts[s + 1] - 1), lengths
+    int32 [n_seq] (slots in use, the call's tokens the last of them), table int32 [n_seq][columns] (page numbers), all
+    on the device and read there, so that a captured graph takes what they hold when it is replayed.  max_new and
+    max_length: the most tokens and slots of any sequence (None: what a sequence can have at most); they size
+    the launch, and sequences that pass them only take longer."""
+
+    def __init__(self, starts, lengths, table, *, max_new: int = None, max_length: int = None):
+        device = starts.get_device()
+        for t, what, dims in ((starts, "starts", 1), (lengths, "lengths", 1), (table, "table", 2)):
+            if t.get_device() != device or device < 0 or t.dtype != torch.int32 or t.dim() != dims or (
+                    t.numel() > 1 and t.stride(-1) != 1):
+                raise QmmError(EINVAL, f"{what} must be int32 with {dims} dimension(s) and adjacent elements, on starts' cuda device")
+        n = lengths.shape[0]
+        if starts.shape[0] != n + 1 or table.shape[0] != n:
+            raise QmmError(EINVAL, f"starts, lengths and table are of {starts.shape[0] - 1}, {n} and {table.shape[0]} sequences")
+        self.starts, self.lengths, self.table, self.device = starts, lengths, table, device
+        self.max_new = -1 if max_new is None else max_new
+        columns = table.shape[1]
+        self.max_length = -1 if max_length is None else max_length
+        self.struct = BatchStruct(n, columns, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
+                                  table.stride(0) if n > 1 else columns, 0, 0)
+
+    def _for(self, cache: Cache, n_tok: int) -> BatchStruct:
+        b = self.struct
+        b.max_new = min(n_tok, MAX_TOKENS) if self.max_new < 0 else self.max_new
+        b.max_length = min(b.columns * cache.page, 2 ** 31 - 1) if self.max_length < 0 else self.max_length
+        return b
+
+
+def _heads(t, what: str, n_tok: int, heads: int, dim: int, device: int, dtype=None):
+    """(address, token stride, head stride) of a tensor [n_tok][heads][dim]; the library checks the rest."""
+    if t.get_device() == device and t.shape == (n_tok, heads, dim) and (dtype is None or t.dtype == dtype):
+        strides = t.stride()
+        if strides[2] == 1:
+            return t.data_ptr(), strides[0], strides[1]
+        raise QmmError(EINVAL, f"{what} must have adjacent channels")
+    raise QmmError(EINVAL, f"{what} must be {[n_tok, heads, dim]} {dtype or ''} on device {device}, got {list(t.shape)} "
+                           f"{t.dtype} on {t.device}")
+
+
+def _same_device(cache: Cache, batch: Batch, device: int) -> None:
+    if cache.device != device or batch.device != device:
+        raise QmmError(EINVAL, f"the tensors are on device {device}, the cache on {cache.device} and the batch on {batch.device}")
+
+
+def rope_cache(cache: Cache, batch: Batch, *, q=None, k=None, v=None, frequencies=None, magnitude: float = 1.0,
+               layout: str = "half", positions=None, dtype=None, out=None, stream=None):
+    """The new tokens' queries and keys turned by their positions, and keys and values kept in their slots of the cache,
+    in one kernel.  q [n_tok][heads][head_dim], k and v [n_tok][cache.heads][head_dim] of one type, any of them; channels
+    adjacent, other strides free.  frequencies: float64 [n_rot/2] on the device (rope_frequencies); the first n_rot
+    channels of a head are rotated, "half" (i with i + n_rot/2) or "interleaved" (2i with 2i + 1), and times magnitude;
+    None: nothing turns.  positions: int32 [n_tok], or the tokens' slots.  Returns the queries, of `dtype` (None: that of
+    the cache where q is float32, else q's) or in `out` (which may be q), or None without q."""
+    x = q if q is not None else k if k is not None else v
+    if x is None:
+        raise QmmError(EINVAL, "rope_cache needs q, k or v")
+    if x.dim() != 3:
+        raise QmmError(EINVAL, "q, k and v must be [n_tok][heads][head_dim]")
+    device = _current(x, "q, k and v")
+    _same_device(cache, batch, device)
+    if layout not in ROPE_LAYOUTS:
+        raise QmmError(EINVAL, f"layout must be 'half' or 'interleaved', got {layout!r}")
+    n_tok, dim, kind = x.shape[0], cache.head_dim, x.dtype
+    a = Rope(_elem(kind, "q, k and v"), F16, 1, ROPE_LAYOUTS[layout], 0, magnitude)
+    if frequencies is not None:
+        if (frequencies.get_device() != device or frequencies.dtype != torch.float64 or frequencies.dim() != 1
+                or not frequencies.is_contiguous()):
+            raise QmmError(EINVAL, f"frequencies must be a contiguous float64 vector on device {device}")
+        a.n_rot, a.frequencies = 2 * frequencies.shape[0], frequencies.data_ptr()
+    if positions is not None:
+        if (positions.get_device() != device or positions.dtype != torch.int32 or positions.shape != (n_tok,)
+                or not positions.is_contiguous()):
+            raise QmmError(EINVAL, f"positions must be a contiguous int32 [{n_tok}] tensor on device {device}")
+        a.positions = positions.data_ptr()
+    if q is not None:
+        a.q_heads = q.shape[1]
+        a.q, a.q_stride, a.q_head_stride = _heads(q, "q", n_tok, q.shape[1], dim, device)
+        if out is None:
+            if dtype is None:
+                dtype = kind if kind != torch.float32 else torch.float16 if cache.dtype == "q8" else cache.dtype
+            a.out_type = _elem(dtype)
+            out = _empty(q, (n_tok * q.shape[1] * dim,), dtype, stream).view(n_tok, q.shape[1], dim)
+            a.q_out, a.q_out_stride, a.q_out_head_stride = out.data_ptr(), q.shape[1] * dim, dim
+        else:
+            a.out_type = _elem(out.dtype, "out")
+            a.q_out, a.q_out_stride, a.q_out_head_stride = _heads(out, "out", n_tok, q.shape[1], dim, device)
+    elif out is not None:
+        raise QmmError(EINVAL, "out is where the queries go: it needs q")
+    if k is not None:
+        a.k, a.k_stride, a.k_head_stride = _heads(k, "k", n_tok, cache.heads, dim, device, kind)
+    if v is not None:
+        a.v, a.v_stride, a.v_head_stride = _heads(v, "v", n_tok, cache.heads, dim, device, kind)
+    _check(_lib.qmm_rope_cache(a, cache.struct, batch._for(cache, n_tok), n_tok, _raw_stream(stream, device)))
+    return out
+
+
+def cache_read(cache: Cache, batch: Batch, n_tok: int, *, dtype=torch.float32, stream=None):
+    """(k, v), each [n_tok][cache.heads][head_dim] of dtype: what the cache holds for the batch's tokens.  Rows of
+    tokens of no sequence are not set."""
+    device = _current(cache.k, "the cache")
+    _same_device(cache, batch, device)
+    elem = _elem(dtype)
+    shape, n = (n_tok, cache.heads, cache.head_dim), n_tok * cache.heads * cache.head_dim
+    k, v = (_empty(cache.k, (n,), dtype, stream) for _ in range(2))
+    _check(_lib.qmm_cache_read(cache.struct, batch._for(cache, n_tok), n_tok, elem, k.data_ptr(), v.data_ptr(),
+                               _raw_stream(stream, device)))
+    return k.view(shape), v.view(shape)
+
+
+def attention_plan(cache: Cache, batch: Batch, heads: int, n_tok: int, num_cus: int) -> AttnPlan:
+    """How attention of these sizes is launched, and the work memory it needs (host arithmetic only)."""
+    plan = AttnPlan()
+    _check(_lib.qmm_attention_plan(cache.struct, batch._for(cache, n_tok), heads, n_tok, num_cus, plan))
+    return plan
+
+
+_cus = {}  # device -> its compute units
+
+
+def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: bool = True, window: int = 0, dtype=None,
+              out=None, work=None, stream=None):
+    """Attention of the batch's tokens over the cache: softmax(scale * q k^T) v for each head, keys and values those of
+    cache head h // (heads // cache.heads).
+
+    q: [n_tok][heads][head_dim] of the cache's type (float16 with a q8 cache), channels adjacent, other strides free.
+    causal: a token sees the slots up to its own, with window only the last `window` of them; else all in use (an
+    encoder's states).  scale: head_dim ** -0.5 if None.  The result is [n_tok][heads][head_dim] of q's type, or with
+    dtype "q8" the qact buffer of its rows (the output product's input), or `out`: [n_tok][heads * head_dim], rows may be
+    strided, or a qact buffer with dtype "q8".  A token that sees nothing gets zeros.  work: a uint8 tensor of
+    attention_plan's work_bytes; new memory without it."""
+    if q.dim() != 3:
+        raise QmmError(EINVAL, "q must be [n_tok][heads][head_dim]")
+    device = _current(q, "q")
+    _same_device(cache, batch, device)
+    n_tok, heads, dim = q.shape
+    kind = torch.float16 if cache.dtype == "q8" else cache.dtype
+    if dtype is not None and dtype != "q8" and dtype != kind:
+        raise QmmError(EINVAL, f"dtype must be None, 'q8' or {kind}, got {dtype}")
+    a = Attn(heads, 1 if causal else 0, Q8 if dtype == "q8" else ELEM_TYPES[kind], dim ** -0.5 if scale is None else scale,
+             window, *_heads(q, "q", n_tok, heads, cache.head_dim, device, kind))
+    result = out
+    if dtype == "q8":
+        if out is None:
+            result = out = _empty(q, (qact_bytes(n_tok, heads * dim),), torch.uint8, stream)
+        a.out, a.out_stride = _bytes(out, "out", device)
+    elif out is None:
+        out = _empty(q, (n_tok * heads * dim,), kind, stream)
+        a.out, a.out_stride, result = out.data_ptr(), heads * dim, out.view(n_tok, heads, dim)
+    else:
+        a.out, a.out_stride = _rows(out, "out", (n_tok, heads * dim), device, kind)
+    b = batch._for(cache, n_tok)
+    if work is None:
+        if device not in _cus:
+            _cus[device] = torch.cuda.get_device_properties(device).multi_processor_count
+        need = attention_plan(cache, batch, heads, n_tok, _cus[device]).work_bytes
+        work = _empty(q, (need,), torch.uint8, stream) if need else None
+    work_ptr, work_bytes = _bytes(work, "work", device) if work is not None and work.numel() else (None, 0)
+    _check(_lib.qmm_attention(a, cache.struct, b, n_tok, work_ptr, work_bytes, _raw_stream(stream, device)))
+    return result

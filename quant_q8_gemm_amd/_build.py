@@ -9,7 +9,9 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-KERNELS = ["qmm_repack.hip", "qmm_prepass.hip", "qmm_norm.hip", "qmm_mmq.hip", "qmm_mmq_few.hip", "qmm_mmv.hip"]
+KERNELS = ["qmm_repack.hip", "qmm_prepass.hip", "qmm_norm.hip", "qmm_mmq.hip", "qmm_mmq_few.hip", "qmm_mmv.hip",
+           "qmm_rope.hip", "qmm_attention.hip", "qmm_attention_f16.hip", "qmm_attention_bf16.hip",
+           "qmm_attention_q8.hip"]
 SOURCES = [os.path.join(CSRC, "qmm_api.cpp")] + [os.path.join(CSRC, k) for k in KERNELS]
 LIB = os.path.join(HERE, "libqmm.so")
 # calibration kernels for the benchmark's measured rooflines (not part of the ABI),
@@ -35,8 +37,9 @@ def _flags(source: str):
     """The few-token kernels keep the default strategy: they need their registers for
     the loads in flight, and max-ILP spills them (the default one still spills a few of
     the q4_K kernels: from f32 numbers with several tokens, and one register of the
-    one-block kernel on the planes)."""
-    return DEVICE_FLAGS if os.path.basename(source) in ("qmm_mmv.hip", "qmm_mmq_few.hip") else LIB_FLAGS
+    one-block kernel on the planes).  So do the attention kernels."""
+    name = os.path.basename(source)
+    return DEVICE_FLAGS if name in ("qmm_mmv.hip", "qmm_mmq_few.hip") or name.startswith("qmm_attention") else LIB_FLAGS
 
 
 def _hipcc(sources, out: str, verbose: bool, flags, shared: bool = True) -> str:

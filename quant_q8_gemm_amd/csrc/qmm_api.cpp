@@ -3,6 +3,7 @@
 // accounting, and the launches.  No compute happens here.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -13,8 +14,10 @@
 #include <vector>
 
 #include "../../include/qmm.h"
+#include "qmm_attention.h"
 #include "qmm_epilogue.h"
 #include "qmm_internal.h"
+#include "qmm_rope.h"
 
 struct qmm_weights {
   qmm::Planes p;
@@ -857,6 +860,385 @@ int qmm_mmq_plan_work(const qmm_plan* plan, int64_t wg, int32_t* row_tile, int32
   *tok_tile = tt;
   *sb_begin = s0;
   *sb_end = s1;
+  ok();
+  return QMM_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- qmm_rope_cache, qmm_cache_read, qmm_attention ----
+
+bool head_dim_ok(int dim) { return dim == 64 || dim == 96 || dim == 128 || dim == 192 || dim == 256; }
+
+int check_cache_shape(const qmm_cache& c) {
+  if (c.type != QMM_F16 && c.type != QMM_BF16 && c.type != QMM_Q8)
+    return fail(QMM_EINVAL, "a cache's type must be QMM_F16 (%d), QMM_BF16 (%d) or QMM_Q8 (%d), got %d", QMM_F16, QMM_BF16,
+                QMM_Q8, c.type);
+  if (c.heads < 1 || c.heads > QMM_MAX_HEADS)
+    return fail(QMM_EINVAL, "a cache's heads must be in [1, %d], got %d", QMM_MAX_HEADS, c.heads);
+  if (!head_dim_ok(c.head_dim)) return fail(QMM_EINVAL, "head_dim must be 64, 96, 128, 192 or 256, got %d", c.head_dim);
+  return QMM_OK;
+}
+
+bool page_ok(int page) { return page >= 32 && page <= QMM_MAX_PAGE && (page & (page - 1)) == 0; }
+
+// The cache and the batch, as the kernels take them.  Pools that a call does not use may be
+// NULL (use: 1 k, 2 v).
+int check_cache(const qmm_cache* cache, const qmm_batch* batch, int64_t n_tok, int use, qmm::Pools* p, qmm::Batch* b) {
+  if (cache == nullptr || batch == nullptr) return fail(QMM_EINVAL, "cache or batch is NULL");
+  const qmm_cache& c = *cache;
+  if (int rc = check_cache_shape(c)) return rc;
+  if (!page_ok(c.page)) return fail(QMM_EINVAL, "page must be a power of two in [32, %d], got %d", QMM_MAX_PAGE, c.page);
+  if (c.n_pages < 1 || c.n_pages > INT32_MAX)
+    return fail(QMM_EINVAL, "n_pages must be in [1, 2^31 - 1], got %lld", (long long)c.n_pages);
+  if (((use & 1) != 0 && c.k == nullptr) || ((use & 2) != 0 && c.v == nullptr))
+    return fail(QMM_EINVAL, "a pool of the cache is NULL");
+  if (!aligned(c.k, 16) || !aligned(c.v, 16)) return fail(QMM_EINVAL, "the cache's pools must be 16-byte aligned");
+  if (c.n_pages > (INT64_MAX >> 1) / (int64_t)qmm_cache_page_bytes(c.type, c.heads, c.head_dim, c.page))
+    return fail(QMM_EINVAL, "the pools' bytes pass 2^62");
+  const qmm_batch& q = *batch;
+  if (q.n_seq < 1 || q.n_seq > QMM_MAX_SEQS)
+    return fail(QMM_EINVAL, "n_seq must be in [1, %d], got %d", QMM_MAX_SEQS, q.n_seq);
+  if (q.columns < 1 || (int64_t)q.columns * c.page > INT32_MAX)
+    return fail(QMM_EINVAL, "columns must be at least 1 and columns * page below 2^31, got %d * %d", q.columns, c.page);
+  if (q.table_stride < q.columns || q.table_stride > INT32_MAX)
+    return fail(QMM_EINVAL, "table_stride must be in [%d, 2^31), got %lld", q.columns, (long long)q.table_stride);
+  if (q.max_new < 0 || q.max_new > QMM_MAX_TOKENS || q.max_length < 0 || q.max_length > INT32_MAX)
+    return fail(QMM_EINVAL, "max_new must be in [0, %d] and max_length in [0, 2^31), got %lld and %lld", QMM_MAX_TOKENS,
+                (long long)q.max_new, (long long)q.max_length);
+  if (q.starts == nullptr || q.lengths == nullptr || q.table == nullptr)
+    return fail(QMM_EINVAL, "starts, lengths or table is NULL");
+  if (!aligned(q.starts, 4) || !aligned(q.lengths, 4) || !aligned(q.table, 4))
+    return fail(QMM_EINVAL, "starts, lengths and table must be 4-byte aligned");
+  int shift = 0;
+  while ((1 << shift) < c.page) ++shift;
+  *p = {(uint8_t*)c.k, (uint8_t*)c.v, c.heads, c.head_dim, shift, c.type, (int32_t)c.n_pages};
+  *b = {q.starts, q.lengths, q.table, q.table_stride, q.n_seq, q.columns, (int32_t)n_tok};
+  return QMM_OK;
+}
+
+// A tensor [n_tok][heads][dim] with adjacent channels; *range: its bytes.
+int check_heads(const char* what, const void* p, int64_t stride, int64_t head_stride, int64_t n_tok, int64_t heads,
+                int64_t dim, size_t elem, qmm::Rows* rows, Range* range) {
+  if (!aligned(p, 16)) return fail(QMM_EINVAL, "%s must be 16-byte aligned", what);
+  if (n_tok == 1) stride = 0;
+  if (heads == 1) head_stride = 0;
+  const auto ok_stride = [&](int64_t s) { return s >= dim && s <= QMM_MAX_STRIDE && s % 8 == 0; };
+  if ((n_tok > 1 && !ok_stride(stride)) || (heads > 1 && !ok_stride(head_stride)))
+    return fail(QMM_EINVAL, "%s's strides must be multiples of 8 in [%lld, %d], got %lld and %lld", what, (long long)dim,
+                QMM_MAX_STRIDE, (long long)stride, (long long)head_stride);
+  *rows = {p, stride, head_stride};
+  *range = {what, p, 0, (size_t)((n_tok - 1) * stride + (heads - 1) * head_stride + dim) * elem};
+  return QMM_OK;
+}
+
+// Whether elements of a tensor fall on one another: one stride has to step over all that the other spans.
+bool folds(const qmm::Rows& r, int64_t n_tok, int64_t heads, int64_t dim) {
+  const int64_t row = (heads - 1) * r.head_stride + dim, column = (n_tok - 1) * r.stride + dim;
+  return n_tok > 1 && heads > 1 && r.stride < row && r.head_stride < column;
+}
+
+// Columns of one wider row, e.g. q, k and v of a joint product: rows of equal stride that
+// do not reach into each other.
+void as_rows(const qmm::Rows& r, int64_t n_tok, int64_t heads, int64_t dim, size_t elem, Range* range) {
+  const int64_t row = (heads - 1) * r.head_stride + dim;
+  if (n_tok > 1 && row <= r.stride) {
+    range->stride = r.stride * (int64_t)elem;
+    range->row = (size_t)row * elem;
+  }
+}
+
+Range pool_range(const char* what, const void* p, const qmm_cache& c) {
+  return {what, p, 0, p == nullptr ? 0 : (size_t)c.n_pages * qmm_cache_page_bytes(c.type, c.heads, c.head_dim, c.page)};
+}
+
+// The batch's arrays, which no output may overlap.
+struct BatchRanges {
+  Range r[3];
+  explicit BatchRanges(const qmm_batch& b)
+      : r{{"starts", b.starts, 0, (size_t)(b.n_seq + 1) * 4},
+          {"lengths", b.lengths, 0, (size_t)b.n_seq * 4},
+          {"table", b.table, 0, ((size_t)(b.n_seq - 1) * b.table_stride + b.columns) * 4}} {}
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t qmm_cache_page_bytes(int type, int heads, int head_dim, int page) {
+  if ((type != QMM_F16 && type != QMM_BF16 && type != QMM_Q8) || heads < 1 || heads > QMM_MAX_HEADS ||
+      !head_dim_ok(head_dim) || !page_ok(page))
+    return 0;
+  return (size_t)heads * (page / qmm::kTileSlots) * qmm::tile_bytes(type, head_dim);
+}
+
+int qmm_rope_frequencies(int64_t n_rot, double base, int scaling, double factor, double original, double fast, double slow,
+                         double* frequencies, float* magnitude) {
+  if (n_rot < 16 || n_rot > 256 || n_rot % 16 != 0)
+    return fail(QMM_EINVAL, "n_rot must be a multiple of 16 in [16, 256], got %lld", (long long)n_rot);
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(QMM_EINVAL, "base must be above 1 and finite");
+  if (scaling < QMM_ROPE_PLAIN || scaling > QMM_ROPE_TURNS)
+    return fail(QMM_EINVAL, "scaling must be one of QMM_ROPE_* (0 to %d), got %d", QMM_ROPE_TURNS, scaling);
+  if (scaling != QMM_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor)))
+    return fail(QMM_EINVAL, "factor must be positive and finite");
+  const bool ramp = scaling == QMM_ROPE_YARN || scaling == QMM_ROPE_TURNS;
+  if (ramp && (!(original > 0.0) || !std::isfinite(original) || !(slow > 0.0) || !(fast > slow) || !std::isfinite(fast)))
+    return fail(QMM_EINVAL, "original must be positive, and fast above slow above 0, all finite");
+  if (frequencies == nullptr) return fail(QMM_EINVAL, "frequencies is NULL");
+  const double n = (double)n_rot, kTurn = 6.283185307179586477;
+  if (scaling == QMM_ROPE_BASE) base *= std::pow(factor, n / (n - 2.0));
+  // the pair that turns `turns` times in the original context
+  const auto pair = [&](double turns) { return n * std::log(original / (turns * kTurn)) / (2.0 * std::log(base)); };
+  const double low = ramp ? std::fmax(0.0, std::floor(pair(fast))) : 0.0;
+  const double high = ramp ? std::fmin(n - 1.0, std::ceil(pair(slow))) : 0.0;
+  for (int64_t i = 0; i < n_rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * (double)i / n), keep = 1.0;
+    if (scaling == QMM_ROPE_LINEAR) keep = 0.0;
+    if (scaling == QMM_ROPE_YARN) keep = 1.0 - std::fmin(1.0, std::fmax(0.0, ((double)i - low) / std::fmax(high - low, 0.001)));
+    if (scaling == QMM_ROPE_TURNS) keep = std::fmin(1.0, std::fmax(0.0, (original * f / kTurn - slow) / (fast - slow)));
+    if (keep < 1.0) f = f / factor * (1.0 - keep) + f * keep;
+    frequencies[i] = f;
+  }
+  if (magnitude != nullptr) *magnitude = scaling == QMM_ROPE_YARN && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  ok();
+  return QMM_OK;
+}
+
+int qmm_rope_cache(const qmm_rope* args, const qmm_cache* cache, const qmm_batch* batch, int64_t n_tok, void* stream) {
+  if (args == nullptr) return fail(QMM_EINVAL, "args is NULL");
+  const qmm_rope& a = *args;
+  if (int rc = check_tokens(n_tok)) return rc;
+  if (int rc = check_elem("type", a.type)) return rc;
+  if (a.q != nullptr)
+    if (int rc = check_elem("out_type", a.out_type)) return rc;
+  qmm::Pools pools{};
+  qmm::Batch b{};
+  if (int rc = check_cache(cache, batch, n_tok, (a.k != nullptr ? 1 : 0) | (a.v != nullptr ? 2 : 0), &pools, &b)) return rc;
+  const int64_t dim = cache->head_dim;
+  if (a.layout != QMM_ROPE_HALF && a.layout != QMM_ROPE_INTERLEAVED)
+    return fail(QMM_EINVAL, "layout must be QMM_ROPE_HALF (%d) or QMM_ROPE_INTERLEAVED (%d), got %d", QMM_ROPE_HALF,
+                QMM_ROPE_INTERLEAVED, a.layout);
+  if (a.n_rot < 0 || a.n_rot > dim || a.n_rot % 16 != 0)
+    return fail(QMM_EINVAL, "n_rot must be a multiple of 16 in [0, %lld], got %d", (long long)dim, a.n_rot);
+  if (!std::isfinite(a.magnitude)) return fail(QMM_EINVAL, "magnitude must be finite");
+  if (a.q != nullptr && (a.q_heads < 1 || a.q_heads > QMM_MAX_HEADS))
+    return fail(QMM_EINVAL, "q_heads must be in [1, %d], got %d", QMM_MAX_HEADS, a.q_heads);
+  if (n_tok == 0) {  // empty batch: pointers are not used
+    ok();
+    return QMM_OK;
+  }
+  if (a.q == nullptr && a.k == nullptr && a.v == nullptr) return fail(QMM_EINVAL, "nothing to do: q, k and v are NULL");
+  if (a.n_rot > 0 && a.frequencies == nullptr) return fail(QMM_EINVAL, "frequencies is NULL");
+  if (!aligned(a.frequencies, 8) || !aligned(a.positions, 4))
+    return fail(QMM_EINVAL, "frequencies must be 8-byte aligned and positions 4-byte aligned");
+  qmm::RopeArgs r{};
+  r.frequencies = a.frequencies;
+  r.positions = a.positions;
+  r.type = a.type;
+  r.out_type = a.out_type;
+  r.layout = a.layout;
+  r.n_rot = a.n_rot;
+  r.magnitude = a.magnitude;
+  const size_t eb = elem_bytes(a.type);
+  Range q{}, q_out{}, k{}, v{};
+  if (a.q != nullptr) {
+    if (a.q_out == nullptr) return fail(QMM_EINVAL, "q_out is NULL");
+    r.q_heads = a.q_heads;
+    if (int rc = check_heads("q", a.q, a.q_stride, a.q_head_stride, n_tok, a.q_heads, dim, eb, &r.q, &q)) return rc;
+    if (int rc = check_heads("q_out", a.q_out, a.q_out_stride, a.q_out_head_stride, n_tok, a.q_heads, dim,
+                             elem_bytes(a.out_type), &r.q_out, &q_out))
+      return rc;
+    if (folds(r.q_out, n_tok, a.q_heads, dim)) return fail(QMM_EINVAL, "q_out's strides put rows on one another");
+    as_rows(r.q, n_tok, a.q_heads, dim, eb, &q);
+    as_rows(r.q_out, n_tok, a.q_heads, dim, elem_bytes(a.out_type), &q_out);
+  }
+  if (a.k != nullptr) {
+    if (int rc = check_heads("k", a.k, a.k_stride, a.k_head_stride, n_tok, pools.heads, dim, eb, &r.k, &k)) return rc;
+    as_rows(r.k, n_tok, pools.heads, dim, eb, &k);
+  }
+  if (a.v != nullptr) {
+    if (int rc = check_heads("v", a.v, a.v_stride, a.v_head_stride, n_tok, pools.heads, dim, eb, &r.v, &v)) return rc;
+    as_rows(r.v, n_tok, pools.heads, dim, eb, &v);
+  }
+  const bool in_place = a.q != nullptr && a.type == a.out_type && r.q.p == r.q_out.p && r.q.stride == r.q_out.stride &&
+                        r.q.head_stride == r.q_out.head_stride;
+  const Range outs[] = {q_out, pool_range("the cache's k", a.k != nullptr ? cache->k : nullptr, *cache),
+                        pool_range("the cache's v", a.v != nullptr ? cache->v : nullptr, *cache)};
+  const Range ins[] = {q, k, v, {"frequencies", a.frequencies, 0, (size_t)a.n_rot * 4},
+                       {"positions", a.positions, 0, (size_t)n_tok * 4}};
+  const BatchRanges fixed(*batch);
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (overlap(outs[i], ins[j]) && !(i == 0 && j == 0 && in_place)) return refuse_overlap(outs[i], ins[j]);
+    for (const Range& f : fixed.r)
+      if (overlap(outs[i], f)) return refuse_overlap(outs[i], f);
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return refuse_overlap(outs[i], outs[j]);
+  }
+  hipError_t e = qmm::launch_rope(r, pools, b, std::min(batch->max_new, n_tok), (hipStream_t)stream);
+  if (e != hipSuccess) return fail_hip(e, "rope launch");
+  ok();
+  return QMM_OK;
+}
+
+int qmm_cache_read(const qmm_cache* cache, const qmm_batch* batch, int64_t n_tok, int type, void* k, void* v, void* stream) {
+  if (int rc = check_tokens(n_tok)) return rc;
+  if (int rc = check_elem("type", type)) return rc;
+  qmm::Pools pools{};
+  qmm::Batch b{};
+  if (int rc = check_cache(cache, batch, n_tok, 3, &pools, &b)) return rc;
+  if (n_tok == 0) {
+    ok();
+    return QMM_OK;
+  }
+  if (k == nullptr && v == nullptr) return fail(QMM_EINVAL, "k and v are NULL");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(QMM_EINVAL, "k and v must be 16-byte aligned");
+  const size_t bytes = (size_t)n_tok * cache->heads * cache->head_dim * elem_bytes(type);
+  const Range outs[] = {{"k", k, 0, k == nullptr ? 0 : bytes}, {"v", v, 0, v == nullptr ? 0 : bytes}};
+  const BatchRanges fixed(*batch);
+  for (const Range& o : outs) {
+    for (const Range& f : {pool_range("the cache's k", cache->k, *cache), pool_range("the cache's v", cache->v, *cache),
+                           fixed.r[0], fixed.r[1], fixed.r[2]})
+      if (overlap(o, f)) return refuse_overlap(o, f);
+  }
+  if (overlap(outs[0], outs[1])) return refuse_overlap(outs[0], outs[1]);
+  hipError_t e = qmm::launch_cache_read(pools, b, std::min(batch->max_new, n_tok), type, k, v, (hipStream_t)stream);
+  if (e != hipSuccess) return fail_hip(e, "cache read launch");
+  ok();
+  return QMM_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the plan needs of an attention's sizes.
+int check_attention_sizes(const qmm_cache& c, int heads, int64_t n_tok) {
+  if (heads < 1 || heads > QMM_MAX_HEADS || heads % c.heads != 0)
+    return fail(QMM_EINVAL, "heads must be a multiple of the cache's %d up to %d, got %d", c.heads, QMM_MAX_HEADS, heads);
+  if (n_tok * heads > INT32_MAX / 2)
+    return fail(QMM_EINVAL, "n_tok * heads must be below 2^30, got %lld * %d", (long long)n_tok, heads);
+  return QMM_OK;
+}
+
+int check_attention_launch(const qmm::AttnPlan& plan) {
+  if (plan.work_groups > INT32_MAX) return fail(QMM_EINVAL, "%lld work-groups exceed one launch", (long long)plan.work_groups);
+  return QMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads, int64_t n_tok, int num_cus,
+                       qmm_attn_plan* out) {
+  if (out == nullptr) return fail(QMM_EINVAL, "out is NULL");
+  std::memset(out, 0, sizeof *out);
+  if (cache == nullptr || batch == nullptr) return fail(QMM_EINVAL, "cache or batch is NULL");
+  if (int rc = check_tokens(n_tok)) return rc;
+  if (int rc = check_cache_shape(*cache)) return rc;
+  if (int rc = check_attention_sizes(*cache, heads, n_tok)) return rc;
+  const qmm_batch& b = *batch;
+  if (b.n_seq < 1 || b.n_seq > QMM_MAX_SEQS)
+    return fail(QMM_EINVAL, "n_seq must be in [1, %d], got %d", QMM_MAX_SEQS, b.n_seq);
+  if (b.max_new < 0 || b.max_new > QMM_MAX_TOKENS || b.max_length < 0 || b.max_length > INT32_MAX)
+    return fail(QMM_EINVAL, "max_new must be in [0, %d] and max_length in [0, 2^31), got %lld and %lld", QMM_MAX_TOKENS,
+                (long long)b.max_new, (long long)b.max_length);
+  if (num_cus < 1 || num_cus > QMM_MAX_CUS)
+    return fail(QMM_EINVAL, "num_cus must be in [1, %d], got %d", QMM_MAX_CUS, num_cus);
+  if (n_tok > 0) {
+    const qmm::AttnPlan plan = qmm::plan_attention(cache->type, heads, cache->heads, cache->head_dim, b.n_seq, n_tok,
+                                                   b.max_new, b.max_length, num_cus);
+    if (int rc = check_attention_launch(plan)) return rc;
+    *out = {plan.work_bytes, plan.work_groups, plan.few ? 1 : 0, plan.columns, plan.tiles, plan.splits};
+  }
+  ok();
+  return QMM_OK;
+}
+
+int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch* batch, int64_t n_tok, void* work,
+                  size_t work_bytes, void* stream) {
+  if (args == nullptr) return fail(QMM_EINVAL, "args is NULL");
+  const qmm_attn& a = *args;
+  if (int rc = check_tokens(n_tok)) return rc;
+  qmm::Pools pools{};
+  qmm::Batch b{};
+  if (int rc = check_cache(cache, batch, n_tok, 3, &pools, &b)) return rc;
+  if (int rc = check_attention_sizes(*cache, a.heads, n_tok)) return rc;
+  const int type = cache->type == QMM_BF16 ? QMM_BF16 : QMM_F16;
+  const int64_t dim = cache->head_dim, id = dim * a.heads;
+  if (a.out_type != type && a.out_type != QMM_Q8)
+    return fail(QMM_EINVAL, "out_type must be that of q (%d with this cache) or QMM_Q8 (%d), got %d", type, QMM_Q8, a.out_type);
+  if (a.causal != 0 && a.causal != 1) return fail(QMM_EINVAL, "causal must be 0 or 1, got %d", a.causal);
+  if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return fail(QMM_EINVAL, "scale must be positive and finite");
+  if (a.window < 0 || (a.window > 0 && a.causal == 0))
+    return fail(QMM_EINVAL, "window must be 0, or positive with causal, got %lld", (long long)a.window);
+  if ((work == nullptr) != (work_bytes == 0) || !aligned(work, 16))
+    return fail(QMM_EINVAL, "work must be 16-byte aligned and come with its size (NULL with 0)");
+  const size_t need = a.out_type == QMM_Q8 ? qmm_qact_bytes(n_tok, id) : 0;
+  if (a.out_type == QMM_Q8) {
+    if (id % 256 != 0 || id > QMM_MAX_ID)
+      return fail(QMM_EINVAL, "a q8 output needs heads * head_dim %% 256 == 0 and at most %d, got %lld", QMM_MAX_ID, (long long)id);
+    if (a.out_stride < 0 || (size_t)a.out_stride != need)
+      return fail(QMM_EINVAL, "out_stride %lld != qmm_qact_bytes(%lld, %lld) = %zu", (long long)a.out_stride, (long long)n_tok,
+                  (long long)id, need);
+  }
+  if (n_tok == 0) {  // empty batch: pointers are not used
+    ok();
+    return QMM_OK;
+  }
+  if (a.q == nullptr || a.out == nullptr) return fail(QMM_EINVAL, "q or out is NULL");
+  if (!aligned(a.out, 16)) return fail(QMM_EINVAL, "out must be 16-byte aligned");
+  if (a.out_type != QMM_Q8 && (a.out_stride < id || a.out_stride > QMM_MAX_STRIDE || a.out_stride % 8 != 0))
+    return fail(QMM_EINVAL, "out_stride must be a multiple of 8 in [%lld, %d], got %lld", (long long)id, QMM_MAX_STRIDE,
+                (long long)a.out_stride);
+  qmm::Rows rows{};
+  Range q{};
+  if (int rc = check_heads("q", a.q, a.q_stride, a.q_head_stride, n_tok, a.heads, dim, 2, &rows, &q)) return rc;
+  as_rows(rows, n_tok, a.heads, dim, 2, &q);
+  const Range out = need > 0 ? Range{"out", a.out, 0, need} : rows_range("out", a.out, a.out_stride, n_tok, id, 2);
+  const Range own{"work", work, 0, work_bytes};
+  const BatchRanges fixed(*batch);
+  for (const Range& in : {q, pool_range("the cache's k", cache->k, *cache), pool_range("the cache's v", cache->v, *cache),
+                          fixed.r[0], fixed.r[1], fixed.r[2]}) {
+    if (overlap(out, in)) return refuse_overlap(out, in);
+    if (overlap(own, in)) return refuse_overlap(own, in);
+  }
+  if (overlap(own, out)) return refuse_overlap(own, out);
+  int device = -1, num_cus = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
+  e = hipDeviceGetAttribute(&num_cus, hipDeviceAttributeMultiprocessorCount, device);
+  if (e != hipSuccess) return fail_hip(e, "hipDeviceGetAttribute(multiprocessor count)");
+  const qmm::AttnPlan plan = qmm::plan_attention(cache->type, a.heads, cache->heads, cache->head_dim, batch->n_seq, n_tok,
+                                                 batch->max_new, batch->max_length, num_cus);
+  if (int rc = check_attention_launch(plan)) return rc;
+  if (work_bytes < plan.work_bytes)
+    return fail(QMM_EINVAL, "work_bytes %zu, but this launch needs %zu bytes of work memory (qmm_attention_plan)", work_bytes,
+                plan.work_bytes);
+  qmm::AttnArgs r{};
+  r.q = a.q;
+  r.q_stride = rows.stride;
+  r.q_head_stride = rows.head_stride;
+  r.out = a.out;
+  r.out_stride = a.out_type == QMM_Q8 ? 0 : a.out_stride;
+  r.part = (float*)work;
+  r.sums = (float2*)((float*)work + (plan.work_bytes > 0 ? (size_t)plan.splits * n_tok * id : 0));
+  r.window = a.window;
+  r.heads = a.heads;
+  r.group = a.heads / cache->heads;
+  r.causal = a.causal;
+  r.q8_out = a.out_type == QMM_Q8;
+  r.splits = plan.splits;
+  r.columns = plan.columns;
+  r.tiles = plan.tiles;
+  r.t_pad = token_pad(n_tok);
+  r.scale2 = (float)(a.scale * 1.4426950408889634074);
+  const auto turn = launch_turn((hipStream_t)stream, plan.work_bytes);
+  e = qmm::launch_attention(r, pools, b, plan, (hipStream_t)stream);
+  if (e != hipSuccess) return fail_hip(e, "attention launch");
   ok();
   return QMM_OK;
 }

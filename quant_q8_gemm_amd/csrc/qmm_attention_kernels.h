@@ -1,0 +1,455 @@
+// qmm_attention_kernels.h -- attention over the paged cache: the kernel for few
+// columns (decode steps) and the kernel for many (chunks and prompts), instantiated
+// per cache type in a source file each.
+#pragma once
+
+#include "qmm_attention_parts.h"
+#include "qmm_internal.h"
+
+namespace qmm {
+
+namespace {
+
+// ---- few columns ----
+//
+// The cache's bytes bound it.  The waves of a work-group take turns over a split's
+// 32-slot tiles, each with a running softmax of its own, straight from memory into the
+// operands' registers: a tile's keys are on their way while the one before is
+// worked on.  The waves' results are joined in LDS, the splits' by a second kernel.
+
+// A tile's keys or values as loaded.
+template <int TYPE, int DB>
+struct Loaded {
+  typedef typename Math<TYPE>::v8 v8;
+  v8 f[2 * DB];
+  __device__ __forceinline__ void load(const uint8_t* tile, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) f[i] = *(const v8*)(tile + i * 1024 + lane * 16);
+  }
+  __device__ __forceinline__ void load_keys(const uint8_t* tile, int lane) { load(tile, lane); }
+  __device__ __forceinline__ void load_values(const uint8_t* tile, int lane) { load(tile, lane); }
+  __device__ __forceinline__ bool odd() const {
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) r |= not_finite<TYPE>(f[i]);
+    return r;
+  }
+  __device__ __forceinline__ void clean() {
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) f[i] = finite<TYPE>(f[i]);
+  }
+  __device__ __forceinline__ v8 key(int i) const { return f[i]; }
+  __device__ __forceinline__ v8 value(int i) const { return f[i]; }
+};
+template <int DB>
+struct Loaded<QMM_Q8, DB> {
+  v4i w[DB];
+  _Float16 k[DB];      // keys: the scales of this lane's slot
+  f16x8 v[2 * DB];     // values: of the eight slots of each step
+  __device__ __forceinline__ void load(const uint8_t* tile, int lane) {
+#pragma unroll
+    for (int i = 0; i < DB; ++i) w[i] = *(const v4i*)(tile + i * 1024 + lane * 16);
+  }
+  __device__ __forceinline__ void load_keys(const uint8_t* tile, int lane) {
+    load(tile, lane);
+    const int r = key_row(lane & 31);  // its own inverse
+#pragma unroll
+    for (int i = 0; i < DB; ++i) k[i] = *(const _Float16*)(tile + scale_at(32 * DB, r, i));
+  }
+  __device__ __forceinline__ void load_values(const uint8_t* tile, int lane) {
+    load(tile, lane);
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i)
+      v[i] = *(const f16x8*)(tile + scale_at(32 * DB, 16 * (i & 1) + 8 * (lane >> 5), i >> 1));
+  }
+  __device__ __forceinline__ f16x8 codes(int i, const f16x8& s) const {
+    return (i & 1) ? codes8(w[i >> 1].z, w[i >> 1].w, s) : codes8(w[i >> 1].x, w[i >> 1].y, s);
+  }
+  // codes are finite: a value is where its scale is (products that pass 65504 aside, which
+  // blocks of numbers of up to 2046 do not have)
+  __device__ __forceinline__ bool odd() const {
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) r |= not_finite<QMM_Q8>(v[i]);
+    return r;
+  }
+  __device__ __forceinline__ void clean() {
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) v[i] = finite<QMM_Q8>(v[i]);
+  }
+  __device__ __forceinline__ f16x8 key(int i) const { return codes(i, splat8(k[i >> 1])); }
+  __device__ __forceinline__ f16x8 value(int i) const { return codes(i, v[i]); }
+};
+
+// (a tile's place in both pools, or -1) of the wave's tile t, in scalar registers
+__device__ __forceinline__ int64_t place(const Batch& b, const Pools& p, int s, int h, int t, int end) {
+  const int64_t at = t < end ? tile_offset(b, p, s, h, t) : -1;
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) << 32) |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)at));
+}
+
+template <int TYPE, int DB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void few_kernel(AttnArgs a, Pools pools, Batch batch) {
+  constexpr int kDim = 32 * DB, kRow = kDim + 4;
+  extern __shared__ float lds[];
+  typedef typename Math<TYPE>::v8 v8;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int h = blockIdx.x % pools.heads, rest = blockIdx.x / pools.heads, split = rest % a.splits, s = blockIdx.y;
+  if (a.q8_out && a.splits == 1)
+    zero_padding(a, kDim, batch.n_tok, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                 (int64_t)gridDim.x * gridDim.y * blockDim.x);
+  const Sequence seq = sequence(batch, pools.page_shift, s);
+  const int flats = seq.count * a.group;
+  float* const tops = lds;                    // [WAVES][32]
+  float* const sums = lds + WAVES * 32;       // [WAVES][32]
+  float* const parts = lds + 2 * WAVES * 32;  // [WAVES][columns][kRow]
+
+  for (int tile = rest / a.splits; (int64_t)tile * a.columns < flats; tile += a.tiles) {
+    const int first = tile * a.columns, last = min(first + a.columns, flats) - 1;
+    const Column c = column(a, seq, h, first + min(lane & 31, a.columns - 1));
+    int low, high, all_low, all_high, unused;
+    seen(a, seq, first / a.group, last / a.group, low, high);
+    seen(a, seq, first / a.group, first / a.group, unused, all_high);
+    seen(a, seq, last / a.group, last / a.group, all_low, unused);
+    const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin), share = (tiles + a.splits - 1) / a.splits;
+    const int from = begin + split * share, end = min(begin + tiles, from + share);
+
+    v8 q[2 * DB];
+    load_queries<TYPE, DB>(a, c, lane, q);
+    v16f o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] = v16f{};
+    Running run;
+    Loaded<TYPE, DB> keys, values;
+    bool odd = false;  // a value that is no finite number where not all columns see it
+    int t = from + wave;
+    int64_t at = place(batch, pools, s, h, t, end), next = place(batch, pools, s, h, t + WAVES, end);
+    if (at >= 0) keys.load_keys(pools.k + at, lane);
+    for (; t < end; t += WAVES) {
+      const int64_t now = at;
+      at = next;
+      next = place(batch, pools, s, h, t + 2 * WAVES, end);
+      if (now >= 0) {
+        values.load_values(pools.v + now, lane);
+        v16f score[1] = {v16f{}};
+#pragma unroll
+        for (int i = 0; i < 2 * DB; ++i) score[0] = Math<TYPE>::mma(keys.key(i), q[i], score[0]);
+        if (at >= 0) keys.load_keys(pools.k + at, lane);
+        const int slot0 = 32 * t;
+        const bool inside = slot0 >= all_low && slot0 + 32 <= all_high;
+        if (!inside) hide(score[0], slot0, half, c.low, c.high);
+        v8 p[2];
+        soften<TYPE, DB, 1>(score, a.scale2, run, o, p);
+        if (!inside && __any(values.odd())) {
+          values.clean();
+          odd = true;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * DB; ++i) o[i >> 1] = Math<TYPE>::mma(values.value(i), p[i & 1], o[i >> 1]);
+      } else if (at >= 0) {
+        keys.load_keys(pools.k + at, lane);
+      }
+    }
+
+    const float sum = run.sum + __shfl_xor(run.sum, 32);
+    if (lane < a.columns && lane < 32) tops[wave * 32 + lane] = run.top, sums[wave * 32 + lane] = sum;
+    if ((lane & 31) < a.columns) {
+      float* const to = parts + (wave * a.columns + (lane & 31)) * kRow + 4 * half;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *(float4*)(to + 32 * d + 8 * i) = make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
+    }
+    const bool mend = __syncthreads_or(odd);
+    for (int i = threadIdx.x; i < a.columns * (kDim / 4); i += 64 * WAVES) {
+      const int n = i / (kDim / 4), d = 4 * (i % (kDim / 4));
+      const Column to = column(a, seq, h, first + n);
+      if (!to.real) continue;
+      float top = tops[n];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) top = fmaxf(top, tops[w * 32 + n]);
+      float total = 0.0f;
+      float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const float mine = tops[w * 32 + n], by = mine == kNone ? 0.0f : __builtin_amdgcn_exp2f((mine - top) * a.scale2);
+        const float4 v = *(const float4*)(parts + (w * a.columns + n) * kRow + d);
+        total = fmaf(sums[w * 32 + n], by, total);
+        x.x = fmaf(v.x, by, x.x), x.y = fmaf(v.y, by, x.y), x.z = fmaf(v.z, by, x.z), x.w = fmaf(v.w, by, x.w);
+      }
+      if (mend) add_edges<TYPE>(pools, batch, s, h, {from, end, 1, all_low, all_high}, to, d, x);
+      store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, total);
+    }
+    __syncthreads();
+  }
+}
+
+// ---- many columns ----
+//
+// The matrix core and the softmax's vector instructions bound it.  A work-group's four
+// waves take 32 columns each and share the keys and values, which pass through LDS
+// in two stages of 32*KB slots: while one is worked on the next is copied, 16-bit tiles
+// straight from memory to LDS, q8 tiles through registers, where they become f16 once for
+// all waves.
+
+// N consecutive 1 KiB copies from base + 16*lane to LDS; M0 is set by each run itself, and
+// nothing else in these kernels reads it.
+template <int N>
+__device__ __forceinline__ void copy_run(const void* base, uint32_t lane_off, uint32_t lds) {
+  static_assert(N >= 1 && N <= 4, "13-bit offsets");
+  if constexpr (N == 1)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(lane_off), "s"(base), "s"(lds)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n\t"
+                 "global_load_lds_dwordx4 %0, %1 offset:1024" ::"v"(lane_off), "s"(base), "s"(lds)
+                 : "memory");
+  else if constexpr (N == 3)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n\t"
+                 "global_load_lds_dwordx4 %0, %1 offset:1024\n\tglobal_load_lds_dwordx4 %0, %1 offset:2048" ::"v"(lane_off),
+                 "s"(base), "s"(lds)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n\t"
+                 "global_load_lds_dwordx4 %0, %1 offset:1024\n\tglobal_load_lds_dwordx4 %0, %1 offset:2048\n\t"
+                 "global_load_lds_dwordx4 %0, %1 offset:3072" ::"v"(lane_off), "s"(base), "s"(lds)
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void copy_kib(const uint8_t* base, uint32_t lane_off, uint32_t lds) {
+  if constexpr (N > 4) {
+    copy_run<4>(base, lane_off, lds);
+    copy_kib<N - 4>(base + 4096, lane_off, lds + 4096);
+  } else {
+    copy_run<N>(base, lane_off, lds);
+  }
+}
+
+// Where the tiles of a stage are, by the waves' own table lookups.
+template <int KB>
+struct Places {
+  int64_t at[KB];
+  __device__ __forceinline__ void find(const Batch& b, const Pools& p, int s, int h, int t, int end) {
+#pragma unroll
+    for (int k = 0; k < KB; ++k) at[k] = place(b, p, s, h, t + k, end);
+  }
+};
+
+// A wave's part of staging: waves 0 and 1 the keys, 2 and 3 the values; of two tiles one
+// each, of one tile half each.
+template <int TYPE, int DB, int KB>
+struct Stager {
+  static __device__ __forceinline__ int64_t from(const Places<KB>& at, int wave) {
+    const int64_t first = at.at[0], second = at.at[KB - 1];
+    return KB == 2 && (wave & 1) ? second : first;
+  }
+  // a tile that is nowhere: the pool's first, whose numbers are then not used
+  __device__ __forceinline__ void load(const Pools& p, const Places<KB>& at, int wave, int lane, uint8_t* lds) {
+    const int64_t off = from(at, wave);
+    const uint8_t* const base = (const uint8_t*)uniform_ptr((wave < 2 ? p.k : p.v) + (off < 0 ? 0 : off) +
+                                                            (KB == 1 && (wave & 1) ? DB * 1024 : 0));
+    // the stage: keys of tile 0, of tile 1, values of tile 0, of tile 1
+    const uint32_t to = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)(lds + wave * (KB * DB * 1024)));
+    copy_kib<KB * DB>(base, lane * 16, to);
+  }
+  __device__ __forceinline__ void store(int, int, uint8_t*) {}
+};
+template <int DB, int KB>
+struct Stager<QMM_Q8, DB, KB> {
+  static constexpr int kBlocks = KB == 2 ? DB : DB / 2;  // blocks of 32 channels of a tile
+  v4i w[kBlocks];
+  f16x8 s[2 * kBlocks];
+  __device__ __forceinline__ void load(const Pools& p, const Places<KB>& at, int wave, int lane, uint8_t*) {
+    const int64_t off = Stager<QMM_F16, DB, KB>::from(at, wave);
+    const uint8_t* const tile = (wave < 2 ? p.k : p.v) + (off < 0 ? 0 : off);
+    const int block0 = KB == 1 && (wave & 1) ? kBlocks : 0;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) w[i] = *(const v4i*)(tile + (block0 + i) * 1024 + lane * 16);
+    if (wave < 2) {
+      const int r = key_row(lane & 31);
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i)
+        s[2 * i] = s[2 * i + 1] = splat8(*(const _Float16*)(tile + scale_at(32 * DB, r, block0 + i)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * kBlocks; ++i)
+        s[i] = *(const f16x8*)(tile + scale_at(32 * DB, 16 * (i & 1) + 8 * (lane >> 5), block0 + (i >> 1)));
+    }
+  }
+  __device__ __forceinline__ void store(int wave, int lane, uint8_t* lds) {
+    uint8_t* const to = lds + wave * (KB * DB * 1024) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      *(f16x8*)(to + 2 * i * 1024) = codes8(w[i].x, w[i].y, s[2 * i]);
+      *(f16x8*)(to + (2 * i + 1) * 1024) = codes8(w[i].z, w[i].w, s[2 * i + 1]);
+    }
+  }
+};
+
+template <int TYPE, int DB, int KB>
+__global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void many_kernel(AttnArgs a, Pools pools, Batch batch) {
+  constexpr int kDim = 32 * DB, kStage = 4 * KB * DB * 1024, kColumns = 128;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  typedef typename Math<TYPE>::v8 v8;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int h = blockIdx.x % pools.heads, rest = blockIdx.x / pools.heads, split = rest % a.splits, s = blockIdx.y;
+  if (a.q8_out && a.splits == 1)
+    zero_padding(a, kDim, batch.n_tok, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                 (int64_t)gridDim.x * gridDim.y * blockDim.x);
+  const Sequence seq = sequence(batch, pools.page_shift, s);
+  const int flats = seq.count * a.group;
+
+  // the last columns see the most keys: they start first
+  for (int tile = a.tiles - 1 - rest / a.splits; (int64_t)tile * kColumns < flats; tile += a.tiles) {
+    const int first = tile * kColumns, last = min(first + kColumns, flats) - 1;
+    int low, high, my_low, my_high, all_low, all_high, unused;
+    seen(a, seq, first / a.group, last / a.group, low, high);
+    // this wave's own columns; all_*: what all of them see
+    const int mine = min(first + 32 * wave, last), mine_end = min(first + 32 * wave + 31, last);
+    seen(a, seq, mine / a.group, mine_end / a.group, my_low, my_high);
+    seen(a, seq, mine / a.group, mine / a.group, unused, all_high);
+    seen(a, seq, mine_end / a.group, mine_end / a.group, all_low, unused);
+    const bool idle = first + 32 * wave > last;
+    const Column c = column(a, seq, h, first + 32 * wave + (lane & 31));
+    const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin);
+    const int share = (tiles + a.splits * KB - 1) / (a.splits * KB) * KB;
+    const int from = begin + split * share, end = min(begin + tiles, from + share);
+
+    v8 q[2 * DB];
+    load_queries<TYPE, DB>(a, c, lane, q);
+    v16f o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] = v16f{};
+    Running run;
+    Places<KB> at, next;
+    Stager<TYPE, DB, KB> stager;
+    at.find(batch, pools, s, h, from, end);
+    next.find(batch, pools, s, h, from + KB, end);
+    if (from < end) {
+      stager.load(pools, at, wave, lane, lds);
+      stager.store(wave, lane, lds);
+    }
+    bool odd = false;  // as in few_kernel
+    int stage = 0;
+    for (int t = from; t < end; t += KB, stage ^= 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      const Places<KB> now = at;
+      const bool more = t + KB < end;
+      uint8_t* const other = lds + (stage ^ 1) * kStage;
+      at = next;
+      if (more) stager.load(pools, at, wave, lane, other);
+      next.find(batch, pools, s, h, t + 2 * KB, end);
+      const int slot0 = 32 * t;
+      if (!idle && slot0 < my_high && slot0 + 32 * KB > my_low) {
+        const uint8_t* const keys = lds + stage * kStage + lane * 16;
+        const uint8_t* const values = keys + 2 * KB * DB * 1024;
+        v16f score[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          score[k] = v16f{};
+#pragma unroll
+          for (int i = 0; i < 2 * DB; ++i)
+            score[k] = Math<TYPE>::mma(*(const v8*)(keys + (k * 2 * DB + i) * 1024), q[i], score[k]);
+        }
+        bool inside = slot0 >= all_low && slot0 + 32 * KB <= all_high;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) inside &= now.at[k] >= 0;
+        bool clean = false;
+        if (!inside) {
+#pragma unroll
+          for (int k = 0; k < KB; ++k)  // a tile that is nowhere is seen by nobody
+            hide(score[k], slot0 + 32 * k, half, c.low, now.at[k] >= 0 ? c.high : 0);
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < 2 * DB * KB; ++i) any |= not_finite<TYPE>(*(const v8*)(values + i * 1024));
+          clean = __any(any);
+        }
+        v8 p[2 * KB];
+        soften<TYPE, DB, KB>(score, a.scale2, run, o, p);
+        if (!clean) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 2 * KB; ++i)
+              o[d] = Math<TYPE>::mma(*(const v8*)(values + ((i >> 1) * 2 * DB + 2 * d + (i & 1)) * 1024), p[i], o[d]);
+        } else {
+          odd = true;
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 2 * KB; ++i)
+              o[d] = Math<TYPE>::mma(finite<TYPE>(*(const v8*)(values + ((i >> 1) * 2 * DB + 2 * d + (i & 1)) * 1024)), p[i],
+                                     o[d]);
+        }
+      }
+      if (more) stager.store(wave, lane, other);
+    }
+    // The columns' results pass through the wave's quarter of the stages, kBlocks blocks of
+    // 32 channels at a time, so that they leave as runs of a row; 16-byte pieces are
+    // exchanged by column, or all columns' would be in the same banks.
+    constexpr int kBlocks = KB * DB / 2;
+    float* const out = (float*)(lds + wave * (kStage / 2));
+    const float total = run.sum + __shfl_xor(run.sum, 32);
+    const int swap = (lane & 31) & (kBlocks % 2 == 0 ? 15 : 7);
+#pragma unroll
+    for (int pass = 0; pass < DB; pass += kBlocks) {
+      __syncthreads();  // the stages, or the pass before, are read
+      if (idle) continue;
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *(float4*)(out + (lane & 31) * (32 * kBlocks) + 4 * ((8 * d + 2 * i + half) ^ swap)) =
+              make_float4(o[pass + d][4 * i], o[pass + d][4 * i + 1], o[pass + d][4 * i + 2], o[pass + d][4 * i + 3]);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll 1
+      for (int i = lane; i < 32 * 8 * kBlocks; i += 64) {  // whole groups of eight lanes have a column
+        const int n = i / (8 * kBlocks), piece = i % (8 * kBlocks);
+        const float top = __shfl(run.top, n), all = __shfl(total, n);
+        const Column to = column(a, seq, h, first + 32 * wave + n);
+        float4 x = *(const float4*)(out + n * (32 * kBlocks) + 4 * (piece ^ (n & (kBlocks % 2 == 0 ? 15 : 7))));
+        if (!to.real) continue;
+        const int d = 32 * pass + 4 * piece;
+        if (odd) add_edges<TYPE>(pools, batch, s, h, {from, end, KB, all_low, all_high}, to, d, x);
+        store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, all);
+      }
+    }
+    __syncthreads();  // the stages are free again
+  }
+}
+
+constexpr int few_waves(int db) { return db <= 4 ? 8 : 4; }
+
+template <int TYPE, int DB>
+hipError_t launch_dim(const AttnArgs& a, const Pools& p, const Batch& b, const AttnPlan& plan, hipStream_t s) {
+  const dim3 grid((unsigned)(plan.work_groups / b.n_seq), (unsigned)b.n_seq);
+  if (plan.few) {
+    constexpr int W = few_waves(DB);
+    const size_t lds = sizeof(float) * W * (64 + (size_t)plan.columns * (32 * DB + 4));
+    few_kernel<TYPE, DB, W><<<grid, 64 * W, lds, s>>>(a, p, b);
+  } else {
+    many_kernel<TYPE, DB, (DB <= 4 ? 2 : 1)><<<grid, 256, 0, s>>>(a, p, b);
+  }
+  return hipGetLastError();
+}
+
+template <int TYPE>
+hipError_t launch_type(const AttnArgs& a, const Pools& p, const Batch& b, const AttnPlan& plan, hipStream_t s) {
+  switch (p.dim) {
+    case 64: return launch_dim<TYPE, 2>(a, p, b, plan, s);
+    case 96: return launch_dim<TYPE, 3>(a, p, b, plan, s);
+    case 128: return launch_dim<TYPE, 4>(a, p, b, plan, s);
+    case 192: return launch_dim<TYPE, 6>(a, p, b, plan, s);
+    default: return launch_dim<TYPE, 8>(a, p, b, plan, s);
+  }
+}
+
+}  // namespace
+
+}  // namespace qmm

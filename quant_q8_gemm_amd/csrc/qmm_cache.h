@@ -1,0 +1,81 @@
+// qmm_cache.h -- where the paged cache keeps what, and which rows and slots a
+// sequence of a batch has: shared by the kernels that write and read it, and
+// compiled for the host too, where its bounds are tested.
+//
+// A head's 32 slots form a tile in the order in which the matrix instructions'
+// left operand (32 rows by 16, eight values a lane) wants it: keys with slots as
+// rows, values with channels as rows and slots along the sum.  One 16-byte load a
+// lane then moves a whole operand of 1 KiB, with nothing to transpose between
+// memory and the matrix core.  The keys' rows are slots with bits 2 and 3
+// exchanged, so that the scores leave the first product as a lane's eight
+// consecutive slots, which is how the second one wants its right operand.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/qmm.h"
+
+namespace qmm {
+
+constexpr int kTileSlots = 32;
+
+__host__ __device__ constexpr int tile_bytes(int type, int dim) { return type == QMM_Q8 ? 34 * dim : 64 * dim; }
+
+__host__ __device__ constexpr int key_row(int r) { return (r & ~12) | ((r & 4) << 1) | ((r & 8) >> 1); }
+
+// Element (16 bits) or byte (q8) of slot r and channel d in a tile.
+__host__ __device__ constexpr int key_at(int r, int d) {
+  return (((d >> 4) * 2 + ((d >> 3) & 1)) * 32 + key_row(r)) * 8 + (d & 7);
+}
+__host__ __device__ constexpr int value_at(int r, int d) { return (((d >> 5) * 4 + (r >> 3)) * 32 + (d & 31)) * 8 + (r & 7); }
+__host__ __device__ constexpr int key_code_at(int r, int d) {
+  return (d >> 5) * 1024 + (((d >> 3) & 1) * 32 + key_row(r)) * 16 + ((d >> 4) & 1) * 8 + (d & 7);
+}
+__host__ __device__ constexpr int value_code_at(int r, int d) {
+  return (d >> 5) * 1024 + (((r >> 3) & 1) * 32 + (d & 31)) * 16 + (r >> 4) * 8 + (r & 7);
+}
+// Byte of the scale of block d/32 of slot r.
+__host__ __device__ constexpr int scale_at(int dim, int r, int block) { return 32 * dim + (block * 32 + r) * 2; }
+
+// The sequences of a call as the kernels take them (qmm_batch, checked).
+struct Batch {
+  const int32_t* starts;
+  const int32_t* lengths;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t n_seq, columns, n_tok;
+};
+
+// The pools of a call; a page is 1 << page_shift slots.
+struct Pools {
+  uint8_t *k, *v;
+  int32_t heads, dim, page_shift, type;
+  int32_t n_pages;
+};
+
+// A sequence: its rows [first, first + count) and slots [0, length).  Whatever the
+// arrays hold, the rows are rows of the call and the slots have a column.
+struct Sequence {
+  int first, count, length;
+};
+
+__host__ __device__ inline int clamped(int v, int low, int high) { return v < low ? low : v > high ? high : v; }
+
+__host__ __device__ inline Sequence sequence(const Batch& b, int page_shift, int s) {
+  const int first = clamped(b.starts[s], 0, b.n_tok), end = clamped(b.starts[s + 1], first, b.n_tok);
+  return {first, end - first, clamped(b.lengths[s], 0, b.columns << page_shift)};
+}
+
+// Byte offset in a pool of the tile of head h that holds slots 32*tile .. of sequence
+// s; -1 where the page is none of the pool's.  0 <= 32*tile < columns * page.
+__host__ __device__ inline int64_t tile_offset(const Batch& b, const Pools& p, int s, int h, int tile) {
+  const int tiles_shift = p.page_shift - 5;
+  const int page = b.table[s * b.table_stride + (tile >> tiles_shift)];
+  if (page < 0 || page >= p.n_pages) return -1;
+  const int64_t at = (((int64_t)page * p.heads + h) << tiles_shift) + (tile & ((1 << tiles_shift) - 1));
+  return at * tile_bytes(p.type, p.dim);
+}
+
+}  // namespace qmm
