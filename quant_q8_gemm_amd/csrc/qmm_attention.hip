@@ -13,31 +13,81 @@ namespace qmm {
 
 namespace {
 
-template <int TYPE>
+// A work-group takes the rows (token, head) that its threads cover with dim/4 threads each
+// and LANES such sets for a row, which share its splits and are joined in LDS.  Loads go out
+// four splits at a time: there are few threads when this kernel matters, and a load after
+// the other would be all of its time.
+template <int TYPE, int LANES>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Batch batch, int dim) {
-  const int64_t thread = (int64_t)blockIdx.x * 256 + threadIdx.x, threads = (int64_t)gridDim.x * 256;
-  if (a.q8_out) zero_padding(a, dim, batch.n_tok, thread, threads);
-  const int first = clamped(batch.starts[0], 0, batch.n_tok), end = clamped(batch.starts[batch.n_seq], first, batch.n_tok);
-  const int per_head = dim >> 2;
-  const int64_t rows = (int64_t)batch.n_tok * a.heads, items = (int64_t)(end - first) * a.heads * per_head;
-  for (int64_t i = thread; i < items; i += threads) {
-    const int64_t row = (int64_t)first * a.heads + i / per_head;
-    const int d = 4 * (int)(i % per_head);
-    float top = kNone;
-    for (int k = 0; k < a.splits; ++k) top = fmaxf(top, a.sums[k * rows + row].x);
-    float total = 0.0f;
+  __shared__ float4 parts[256];
+  __shared__ float2 sums[256];
+  if (a.q8_out)
+    zero_padding(a, dim, batch.n_tok, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+  const int first = clamped(uniform_load(batch.starts, 0), 0, batch.n_tok);
+  const int end = clamped(uniform_load(batch.starts, batch.n_seq), first, batch.n_tok);
+  const int quads = dim >> 2, per_row = quads * LANES, rows_here = 256 / per_row;
+  const int lane = threadIdx.x / quads % LANES, d = 4 * (threadIdx.x % quads), mine = threadIdx.x / per_row;
+  const int64_t all = (int64_t)batch.n_tok * a.heads;
+  for (int64_t row0 = (int64_t)first * a.heads + (int64_t)blockIdx.x * rows_here; row0 < (int64_t)end * a.heads;
+       row0 += (int64_t)gridDim.x * rows_here) {
+    const int64_t row = row0 + mine;
+    const bool real = mine < rows_here && row < (int64_t)end * a.heads;
+    float top = kNone, total = 0.0f;
     float4 x = make_float4(0, 0, 0, 0);
-    for (int k = 0; k < a.splits; ++k) {
-      const float2 m = a.sums[k * rows + row];
-      const float by = m.x == kNone ? 0.0f : __builtin_amdgcn_exp2f((m.x - top) * a.scale2);
-      const float4 v = *(const float4*)(a.part + (k * rows + row) * dim + d);
-      total = fmaf(m.y, by, total);
-      x.x = fmaf(v.x, by, x.x), x.y = fmaf(v.y, by, x.y), x.z = fmaf(v.z, by, x.z), x.w = fmaf(v.w, by, x.w);
+    if (real) {
+      for (int k0 = lane; k0 < a.splits; k0 += 4 * LANES) {
+        float2 m[4];
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = k0 + j * LANES;
+          const int64_t at = (k < a.splits ? k : k0) * all + row;
+          m[j] = a.sums[at];
+          v[j] = *(const float4*)(a.part + at * dim + d);
+          if (k >= a.splits) m[j] = make_float2(kNone, 0.0f);
+        }
+        const float now = fmaxf(fmaxf(fmaxf(m[0].x, m[1].x), fmaxf(m[2].x, m[3].x)), top);
+        const float4 so_far = x;
+        const float sum = total;
+        x = make_float4(0, 0, 0, 0), total = 0.0f;
+        add_part(x, total, so_far, top, sum, now, a.scale2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k0 + j * LANES < a.splits) add_part(x, total, v[j], m[j].x, m[j].y, now, a.scale2);
+        top = now;
+      }
     }
-    const float by = total == 0.0f ? 0.0f : 1.0f / total;
-    store_four<TYPE>(a, dim, (int)(row / a.heads), (int)(row % a.heads), d,
-                     make_float4(x.x * by, x.y * by, x.z * by, x.w * by));
+    if (LANES > 1) {
+      parts[threadIdx.x] = x;
+      sums[threadIdx.x] = make_float2(top, total);
+      __syncthreads();
+      if (real && lane == 0) {
+        float now = top;
+#pragma unroll
+        for (int l = 1; l < LANES; ++l) now = fmaxf(now, sums[threadIdx.x + l * quads].x);
+        x = make_float4(0, 0, 0, 0), total = 0.0f;
+#pragma unroll
+        for (int l = 0; l < LANES; ++l) {
+          const float2 m = sums[threadIdx.x + l * quads];
+          add_part(x, total, parts[threadIdx.x + l * quads], m.x, m.y, now, a.scale2);
+        }
+      }
+    }
+    if (real && lane == 0) {
+      const float by = total == 0.0f ? 0.0f : 1.0f / total;
+      store_four<TYPE>(a, dim, (int)(row / a.heads), (int)(row % a.heads), d,
+                       make_float4(x.x * by, x.y * by, x.z * by, x.w * by));
+    }
+    if (LANES > 1) __syncthreads();
   }
+}
+
+template <int TYPE, int LANES>
+hipError_t launch_join(const AttnArgs& a, const Pools& p, const Batch& b, hipStream_t s) {
+  const int rows_here = 256 / (p.dim / 4 * LANES);
+  const int64_t blocks = ((int64_t)b.n_tok * a.heads + rows_here - 1) / rows_here;
+  join_kernel<TYPE, LANES><<<(unsigned)std::min<int64_t>(blocks, 1 << 16), 256, 0, s>>>(a, b, p.dim);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -63,11 +113,10 @@ hipError_t launch_attention(const AttnArgs& a, const Pools& p, const Batch& b, c
                         : p.type == QMM_F16 ? launch_attention_f16
                                             : launch_attention_bf16)(a, p, b, plan, s);
   if (e != hipSuccess || plan.splits == 1) return e;
-  const int64_t items = (int64_t)b.n_tok * a.heads * (p.dim / 4);
-  const unsigned grid = (unsigned)std::min<int64_t>((items + 255) / 256, 1 << 16);
-  if (p.type == QMM_BF16) join_kernel<QMM_BF16><<<grid, 256, 0, s>>>(a, b, p.dim);
-  else join_kernel<QMM_F16><<<grid, 256, 0, s>>>(a, b, p.dim);
-  return hipGetLastError();
+  // four splits in flight for each thread, as far as a row's threads go
+  const bool wide = plan.splits > 4;
+  if (p.type == QMM_BF16) return (wide ? launch_join<QMM_BF16, 4> : launch_join<QMM_BF16, 1>)(a, p, b, s);
+  return (wide ? launch_join<QMM_F16, 4> : launch_join<QMM_F16, 1>)(a, p, b, s);
 }
 
 }  // namespace qmm

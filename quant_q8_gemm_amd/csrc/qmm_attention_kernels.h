@@ -14,8 +14,8 @@ namespace {
 //
 // The cache's bytes bound it.  The waves of a work-group take turns over a split's
 // 32-slot tiles, each with a running softmax of its own, straight from memory into the
-// operands' registers: a tile's keys are on their way while the one before is
-// worked on.  The waves' results are joined in LDS, the splits' by a second kernel.
+// operands' registers: a tile's keys and values are on their way while the one before
+// is worked on.  The waves' results are joined in LDS, the splits' by a second kernel.
 
 // A tile's keys or values as loaded.
 template <int TYPE, int DB>
@@ -28,12 +28,6 @@ struct Loaded {
   }
   __device__ __forceinline__ void load_keys(const uint8_t* tile, int lane) { load(tile, lane); }
   __device__ __forceinline__ void load_values(const uint8_t* tile, int lane) { load(tile, lane); }
-  __device__ __forceinline__ bool odd() const {
-    bool r = false;
-#pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) r |= not_finite<TYPE>(f[i]);
-    return r;
-  }
   __device__ __forceinline__ void clean() {
 #pragma unroll
     for (int i = 0; i < 2 * DB; ++i) f[i] = finite<TYPE>(f[i]);
@@ -67,12 +61,6 @@ struct Loaded<QMM_Q8, DB> {
   }
   // codes are finite: a value is where its scale is (products that pass 65504 aside, which
   // blocks of numbers of up to 2046 do not have)
-  __device__ __forceinline__ bool odd() const {
-    bool r = false;
-#pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) r |= not_finite<QMM_Q8>(v[i]);
-    return r;
-  }
   __device__ __forceinline__ void clean() {
 #pragma unroll
     for (int i = 0; i < 2 * DB; ++i) v[i] = finite<QMM_Q8>(v[i]);
@@ -81,15 +69,14 @@ struct Loaded<QMM_Q8, DB> {
   __device__ __forceinline__ f16x8 value(int i) const { return codes(i, v[i]); }
 };
 
-// (a tile's place in both pools, or -1) of the wave's tile t, in scalar registers
+// Tile t's place in both pools, or -1; t is the same in every lane.
 __device__ __forceinline__ int64_t place(const Batch& b, const Pools& p, int s, int h, int t, int end) {
-  const int64_t at = t < end ? tile_offset(b, p, s, h, t) : -1;
-  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) << 32) |
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)at));
+  return t < end ? tile_offset<true>(b, p, s, h, t) : -1;
 }
 
 template <int TYPE, int DB, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void few_kernel(AttnArgs a, Pools pools, Batch batch) {
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2 : 1, DB <= 4 ? 2 : 1))) void few_kernel(
+    AttnArgs a, Pools pools, Batch batch) {
   constexpr int kDim = 32 * DB, kRow = kDim + 4;
   extern __shared__ float lds[];
   typedef typename Math<TYPE>::v8 v8;
@@ -114,74 +101,74 @@ __global__ __launch_bounds__(64 * WAVES) void few_kernel(AttnArgs a, Pools pools
     const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin), share = (tiles + a.splits - 1) / a.splits;
     const int from = begin + split * share, end = min(begin + tiles, from + share);
 
-    v8 q[2 * DB];
-    load_queries<TYPE, DB>(a, c, lane, q);
-    v16f o[DB];
+    for (bool safe = false;; safe = true) {
+      // A tile's loads are issued whether it is there or not (the pool's first instead, which
+      // then counts for nothing): behind a branch the wait for one tile would be one for
+      // the next as well.
+      Loaded<TYPE, DB> keys, values;
+      int t = from + wave;
+      int64_t at = place(batch, pools, s, h, t, end), next = place(batch, pools, s, h, t + WAVES, end);
+      keys.load_keys(pools.k + max(at, (int64_t)0), lane);
+      values.load_values(pools.v + max(at, (int64_t)0), lane);
+      v8 q[2 * DB];
+      load_queries<TYPE, DB>(a, c, lane, q);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) o[d] = v16f{};
-    Running run;
-    Loaded<TYPE, DB> keys, values;
-    bool odd = false;  // a value that is no finite number where not all columns see it
-    int t = from + wave;
-    int64_t at = place(batch, pools, s, h, t, end), next = place(batch, pools, s, h, t + WAVES, end);
-    if (at >= 0) keys.load_keys(pools.k + at, lane);
-    for (; t < end; t += WAVES) {
-      const int64_t now = at;
-      at = next;
-      next = place(batch, pools, s, h, t + 2 * WAVES, end);
-      if (now >= 0) {
-        values.load_values(pools.v + now, lane);
+      for (int i = 0; i < 2 * DB; ++i) pin(q[i]);
+      v16f o[DB];
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] = v16f{};
+      Running run;
+      for (; t < end; t += WAVES) {
+        const bool here = at >= 0;
+        at = next;
+        next = place(batch, pools, s, h, t + 2 * WAVES, end);
         v16f score[1] = {v16f{}};
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) score[0] = Math<TYPE>::mma(keys.key(i), q[i], score[0]);
-        if (at >= 0) keys.load_keys(pools.k + at, lane);
+        keys.load_keys(pools.k + max(at, (int64_t)0), lane);
         const int slot0 = 32 * t;
-        const bool inside = slot0 >= all_low && slot0 + 32 <= all_high;
-        if (!inside) hide(score[0], slot0, half, c.low, c.high);
+        const bool inside = here && slot0 >= all_low && slot0 + 32 <= all_high;
+        if (!inside) hide(score[0], slot0, half, c.low, here ? c.high : 0);
         v8 p[2];
         soften<TYPE, DB, 1>(score, a.scale2, run, o, p);
-        if (!inside && __any(values.odd())) {
-          values.clean();
-          odd = true;
-        }
+        if (safe && !inside) values.clean();
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) o[i >> 1] = Math<TYPE>::mma(values.value(i), p[i & 1], o[i >> 1]);
-      } else if (at >= 0) {
-        keys.load_keys(pools.k + at, lane);
+        values.load_values(pools.v + max(at, (int64_t)0), lane);
       }
-    }
 
-    const float sum = run.sum + __shfl_xor(run.sum, 32);
-    if (lane < a.columns && lane < 32) tops[wave * 32 + lane] = run.top, sums[wave * 32 + lane] = sum;
-    if ((lane & 31) < a.columns) {
-      float* const to = parts + (wave * a.columns + (lane & 31)) * kRow + 4 * half;
+      const float sum = both_sum(run.sum);
+      if (lane < a.columns && lane < 32) tops[wave * 32 + lane] = run.top, sums[wave * 32 + lane] = sum;
+      if ((lane & 31) < a.columns) {
+        float* const to = parts + (wave * a.columns + (lane & 31)) * kRow + 4 * half;
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *(float4*)(to + 32 * d + 8 * i) = make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
-    }
-    const bool mend = __syncthreads_or(odd);
-    for (int i = threadIdx.x; i < a.columns * (kDim / 4); i += 64 * WAVES) {
-      const int n = i / (kDim / 4), d = 4 * (i % (kDim / 4));
-      const Column to = column(a, seq, h, first + n);
-      if (!to.real) continue;
-      float top = tops[n];
-#pragma unroll
-      for (int w = 1; w < WAVES; ++w) top = fmaxf(top, tops[w * 32 + n]);
-      float total = 0.0f;
-      float4 x = make_float4(0, 0, 0, 0);
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
-        const float mine = tops[w * 32 + n], by = mine == kNone ? 0.0f : __builtin_amdgcn_exp2f((mine - top) * a.scale2);
-        const float4 v = *(const float4*)(parts + (w * a.columns + n) * kRow + d);
-        total = fmaf(sums[w * 32 + n], by, total);
-        x.x = fmaf(v.x, by, x.x), x.y = fmaf(v.y, by, x.y), x.z = fmaf(v.z, by, x.z), x.w = fmaf(v.w, by, x.w);
+          for (int i = 0; i < 4; ++i)
+            *(float4*)(to + 32 * d + 8 * i) = make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
       }
-      if (mend) add_edges<TYPE>(pools, batch, s, h, {from, end, 1, all_low, all_high}, to, d, x);
-      store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, total);
+      __syncthreads();
+      bool odd = false;
+      for (int i = threadIdx.x; i < a.columns * (kDim / 4); i += 64 * WAVES) {
+        const int n = i / (kDim / 4), d = 4 * (i % (kDim / 4));
+        const Column to = column(a, seq, h, first + n);
+        if (!to.real) continue;
+        float top = tops[n];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) top = fmaxf(top, tops[w * 32 + n]);
+        float total = 0.0f;
+        float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+          add_part(x, total, *(const float4*)(parts + (w * a.columns + n) * kRow + d), tops[w * 32 + n], sums[w * 32 + n], top,
+                   a.scale2);
+        odd |= !(fabsf(x.x + x.y) + fabsf(x.z + x.w) < __builtin_inff());
+        if (safe) add_edges<TYPE>(pools, batch, s, h, {from, end, 1, all_low, all_high}, to, d, x);
+        store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, total);
+      }
+      // again, safely, where a result is no finite number (a barrier that the next round needs too)
+      if (!__syncthreads_or(odd) || safe) break;
     }
-    __syncthreads();
   }
 }
 
@@ -225,6 +212,36 @@ __device__ __forceinline__ void copy_kib(const uint8_t* base, uint32_t lane_off,
   } else {
     copy_run<N>(base, lane_off, lds);
   }
+}
+
+// N products whose left operands come from LDS (1 KiB each, at(i) bytes from base), step by
+// step: while G of them run the next G operands are on their way.  The scheduling
+// barriers keep that order; by itself the compiler reads each operand right before its
+// product, which then waits for it.
+template <class V, int N, int G, class At, class Mma>
+__device__ __forceinline__ void products(const uint8_t* base, At&& at, Mma&& mma) {
+  static_assert(N % G == 0, "whole groups");
+  V buffer[2][G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) buffer[0][j] = *(const V*)(base + at(j));
+#pragma unroll
+  for (int g = 0; g < N / G; ++g) {
+    if (g + 1 < N / G) {
+#pragma unroll
+      for (int j = 0; j < G; ++j) buffer[(g + 1) & 1][j] = *(const V*)(base + at((g + 1) * G + j));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < G; ++j) mma(g * G + j, buffer[g & 1][j]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// What the lanes of a wave have written to LDS is there for all of them.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Where the tiles of a stage are, by the waves' own table lookups.
@@ -290,7 +307,8 @@ struct Stager<QMM_Q8, DB, KB> {
 };
 
 template <int TYPE, int DB, int KB>
-__global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void many_kernel(AttnArgs a, Pools pools, Batch batch) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2 : 1, DB <= 4 ? 2 : 1))) void many_kernel(
+    AttnArgs a, Pools pools, Batch batch) {
   constexpr int kDim = 32 * DB, kStage = 4 * KB * DB * 1024, kColumns = 128;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
   typedef typename Math<TYPE>::v8 v8;
@@ -305,13 +323,15 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void many_kernel(AttnArgs a, 
   // the last columns see the most keys: they start first
   for (int tile = a.tiles - 1 - rest / a.splits; (int64_t)tile * kColumns < flats; tile += a.tiles) {
     const int first = tile * kColumns, last = min(first + kColumns, flats) - 1;
-    int low, high, my_low, my_high, all_low, all_high, unused;
+    // what any and what all of the columns see, and the same of this wave's own
+    int low, high, all_low, all_high, my_low, my_high, my_all_low, my_all_high, unused;
+    const int mine = min(first + 32 * wave, last) / a.group, mine_end = min(first + 32 * wave + 31, last) / a.group;
     seen(a, seq, first / a.group, last / a.group, low, high);
-    // this wave's own columns; all_*: what all of them see
-    const int mine = min(first + 32 * wave, last), mine_end = min(first + 32 * wave + 31, last);
-    seen(a, seq, mine / a.group, mine_end / a.group, my_low, my_high);
-    seen(a, seq, mine / a.group, mine / a.group, unused, all_high);
-    seen(a, seq, mine_end / a.group, mine_end / a.group, all_low, unused);
+    seen(a, seq, first / a.group, first / a.group, unused, all_high);
+    seen(a, seq, last / a.group, last / a.group, all_low, unused);
+    seen(a, seq, mine, mine_end, my_low, my_high);
+    seen(a, seq, mine, mine, unused, my_all_high);
+    seen(a, seq, mine_end, mine_end, my_all_low, unused);
     const bool idle = first + 32 * wave > last;
     const Column c = column(a, seq, h, first + 32 * wave + (lane & 31));
     const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin);
@@ -320,111 +340,106 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void many_kernel(AttnArgs a, 
 
     v8 q[2 * DB];
     load_queries<TYPE, DB>(a, c, lane, q);
-    v16f o[DB];
 #pragma unroll
-    for (int d = 0; d < DB; ++d) o[d] = v16f{};
-    Running run;
-    Places<KB> at, next;
-    Stager<TYPE, DB, KB> stager;
-    at.find(batch, pools, s, h, from, end);
-    next.find(batch, pools, s, h, from + KB, end);
-    if (from < end) {
-      stager.load(pools, at, wave, lane, lds);
-      stager.store(wave, lane, lds);
-    }
-    bool odd = false;  // as in few_kernel
-    int stage = 0;
-    for (int t = from; t < end; t += KB, stage ^= 1) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      const Places<KB> now = at;
-      const bool more = t + KB < end;
-      uint8_t* const other = lds + (stage ^ 1) * kStage;
-      at = next;
-      if (more) stager.load(pools, at, wave, lane, other);
-      next.find(batch, pools, s, h, t + 2 * KB, end);
-      const int slot0 = 32 * t;
-      if (!idle && slot0 < my_high && slot0 + 32 * KB > my_low) {
-        const uint8_t* const keys = lds + stage * kStage + lane * 16;
-        const uint8_t* const values = keys + 2 * KB * DB * 1024;
-        v16f score[KB];
+    for (int i = 0; i < 2 * DB; ++i) pin(q[i]);  // here, not in the loop, where the wait would be for the loads ahead too
+    for (bool safe = false;; safe = true) {
+      v16f o[DB];
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-          score[k] = v16f{};
-#pragma unroll
-          for (int i = 0; i < 2 * DB; ++i)
-            score[k] = Math<TYPE>::mma(*(const v8*)(keys + (k * 2 * DB + i) * 1024), q[i], score[k]);
-        }
-        bool inside = slot0 >= all_low && slot0 + 32 * KB <= all_high;
-#pragma unroll
-        for (int k = 0; k < KB; ++k) inside &= now.at[k] >= 0;
-        bool clean = false;
-        if (!inside) {
-#pragma unroll
-          for (int k = 0; k < KB; ++k)  // a tile that is nowhere is seen by nobody
-            hide(score[k], slot0 + 32 * k, half, c.low, now.at[k] >= 0 ? c.high : 0);
-          bool any = false;
-#pragma unroll
-          for (int i = 0; i < 2 * DB * KB; ++i) any |= not_finite<TYPE>(*(const v8*)(values + i * 1024));
-          clean = __any(any);
-        }
-        v8 p[2 * KB];
-        soften<TYPE, DB, KB>(score, a.scale2, run, o, p);
-        if (!clean) {
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 2 * KB; ++i)
-              o[d] = Math<TYPE>::mma(*(const v8*)(values + ((i >> 1) * 2 * DB + 2 * d + (i & 1)) * 1024), p[i], o[d]);
-        } else {
-          odd = true;
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 2 * KB; ++i)
-              o[d] = Math<TYPE>::mma(finite<TYPE>(*(const v8*)(values + ((i >> 1) * 2 * DB + 2 * d + (i & 1)) * 1024)), p[i],
-                                     o[d]);
-        }
+      for (int d = 0; d < DB; ++d) o[d] = v16f{};
+      Running run;
+      Places<KB> at, next;
+      Stager<TYPE, DB, KB> stager;
+      at.find(batch, pools, s, h, from, end);
+      next.find(batch, pools, s, h, from + KB, end);
+      if (from < end) {
+        stager.load(pools, at, wave, lane, lds);
+        stager.store(wave, lane, lds);
       }
-      if (more) stager.store(wave, lane, other);
-    }
-    // The columns' results pass through the wave's quarter of the stages, kBlocks blocks of
-    // 32 channels at a time, so that they leave as runs of a row; 16-byte pieces are
-    // exchanged by column, or all columns' would be in the same banks.
-    constexpr int kBlocks = KB * DB / 2;
-    float* const out = (float*)(lds + wave * (kStage / 2));
-    const float total = run.sum + __shfl_xor(run.sum, 32);
-    const int swap = (lane & 31) & (kBlocks % 2 == 0 ? 15 : 7);
+      int stage = 0;
+      for (int t = from; t < end; t += KB, stage ^= 1) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        const Places<KB> now = at;
+        const bool more = t + KB < end;
+        uint8_t* const other = lds + (stage ^ 1) * kStage;
+        at = next;
+        if (more) stager.load(pools, at, wave, lane, other);
+        next.find(batch, pools, s, h, t + 2 * KB, end);
+        const int slot0 = 32 * t;
+        bool here = true;
 #pragma unroll
-    for (int pass = 0; pass < DB; pass += kBlocks) {
-      __syncthreads();  // the stages, or the pass before, are read
-      if (idle) continue;
+        for (int k = 0; k < KB; ++k) here &= now.at[k] >= 0;
+        if (safe && (!here || slot0 < all_low || slot0 + 32 * KB > all_high)) {
+          v8* const values = (v8*)(lds + stage * kStage + kStage / 2);
+          for (int i = threadIdx.x; i < kStage / 32; i += 256) values[i] = finite<TYPE>(values[i]);
+          __syncthreads();
+        }
+        if (!idle && slot0 < my_high && slot0 + 32 * KB > my_low) {
+          const uint8_t* const keys = lds + stage * kStage + lane * 16;
+          const uint8_t* const values = keys + kStage / 2;
+          v16f score[KB];
 #pragma unroll
-      for (int d = 0; d < kBlocks; ++d)
+          for (int k = 0; k < KB; ++k) score[k] = v16f{};
+          products<v8, 2 * DB * KB, 4>(
+              keys, [](int i) { return (i % KB * 2 * DB + i / KB) * 1024; },
+              [&](int i, const v8& k) { score[i % KB] = Math<TYPE>::mma(k, q[i / KB], score[i % KB]); });
+          if (!here || slot0 < my_all_low || slot0 + 32 * KB > my_all_high) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *(float4*)(out + (lane & 31) * (32 * kBlocks) + 4 * ((8 * d + 2 * i + half) ^ swap)) =
-              make_float4(o[pass + d][4 * i], o[pass + d][4 * i + 1], o[pass + d][4 * i + 2], o[pass + d][4 * i + 3]);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            for (int k = 0; k < KB; ++k)  // a tile that is nowhere is seen by nobody
+              hide(score[k], slot0 + 32 * k, half, c.low, now.at[k] >= 0 ? c.high : 0);
+          }
+          v8 p[2 * KB];
+          soften<TYPE, DB, KB>(score, a.scale2, run, o, p);
+          products<v8, 2 * DB * KB, 4>(
+              values, [](int i) { return (i / DB / 2 * 2 * DB + 2 * (i % DB) + i / DB % 2) * 1024; },
+              [&](int i, const v8& v) { o[i % DB] = Math<TYPE>::mma(v, p[i / DB], o[i % DB]); });
+        }
+        if (more) stager.store(wave, lane, other);
+      }
+      bool odd = false;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd |= !(fabsf(o[d][i]) < __builtin_inff());
+      // again, safely, where a result is no finite number; the stages are read
+      if (__syncthreads_or(odd) && !safe) continue;
+
+      // The columns' results pass through the wave's quarter of the stages, kBlocks blocks of
+      // 32 channels at a time, so that they leave as runs of a row; 16-byte pieces are
+      // exchanged by column, or all columns' would be in the same banks.
+      constexpr int kBlocks = KB * DB / 2, kSwap = kBlocks % 2 == 0 ? 15 : 7;
+      float* const out = (float*)(lds + wave * (kStage / 2));
+      const float total = both_sum(run.sum);
+#pragma unroll
+      for (int pass = 0; pass < DB; pass += kBlocks) {
+        if (idle) break;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *(float4*)(out + (lane & 31) * (32 * kBlocks) + 4 * ((8 * d + 2 * i + half) ^ (lane & kSwap))) =
+                make_float4(o[pass + d][4 * i], o[pass + d][4 * i + 1], o[pass + d][4 * i + 2], o[pass + d][4 * i + 3]);
+        wave_sync();
 #pragma unroll 1
-      for (int i = lane; i < 32 * 8 * kBlocks; i += 64) {  // whole groups of eight lanes have a column
-        const int n = i / (8 * kBlocks), piece = i % (8 * kBlocks);
-        const float top = __shfl(run.top, n), all = __shfl(total, n);
-        const Column to = column(a, seq, h, first + 32 * wave + n);
-        float4 x = *(const float4*)(out + n * (32 * kBlocks) + 4 * (piece ^ (n & (kBlocks % 2 == 0 ? 15 : 7))));
-        if (!to.real) continue;
-        const int d = 32 * pass + 4 * piece;
-        if (odd) add_edges<TYPE>(pools, batch, s, h, {from, end, KB, all_low, all_high}, to, d, x);
-        store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, all);
+        for (int i = lane; i < 32 * 8 * kBlocks; i += 64) {  // whole groups of eight lanes have a column
+          const int n = i / (8 * kBlocks), piece = i % (8 * kBlocks);
+          const float top = __shfl(run.top, n), all = __shfl(total, n);
+          const Column to = column(a, seq, h, first + 32 * wave + n);
+          float4 x = *(const float4*)(out + n * (32 * kBlocks) + 4 * (piece ^ (n & kSwap)));
+          if (!to.real) continue;
+          const int d = 32 * pass + 4 * piece;
+          if (safe) add_edges<TYPE>(pools, batch, s, h, {from, end, KB, all_low, all_high}, to, d, x);
+          store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, all);
+        }
+        wave_sync();
       }
+      __syncthreads();  // the stages are free again
+      break;
     }
-    __syncthreads();  // the stages are free again
   }
 }
 
-constexpr int few_waves(int db) { return db <= 4 ? 8 : 4; }
+constexpr int few_waves(int db) { return db <= 4 ? 4 : 2; }
 
 template <int TYPE, int DB>
 hipError_t launch_dim(const AttnArgs& a, const Pools& p, const Batch& b, const AttnPlan& plan, hipStream_t s) {

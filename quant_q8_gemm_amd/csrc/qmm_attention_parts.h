@@ -34,7 +34,7 @@ template <int TYPE>
 struct Math {
   typedef f16x8 v8;
   typedef _Float16 e;
-  static constexpr uint32_t kExponent = 0x7c007c00u, kOne = 0x04000400u;  // of two values; adding kOne carries where it is full
+  static constexpr uint16_t kExponent = 0x7c00;
   static __device__ __forceinline__ v16f mma(const v8& a, const v8& b, const v16f& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
@@ -43,7 +43,7 @@ template <>
 struct Math<QMM_BF16> {
   typedef bf16x8 v8;
   typedef __bf16 e;
-  static constexpr uint32_t kExponent = 0x7f807f80u, kOne = 0x00800080u;
+  static constexpr uint16_t kExponent = 0x7f80;
   static __device__ __forceinline__ v16f mma(const v8& a, const v8& b, const v16f& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -108,16 +108,36 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Column& c,
   for (int i = 0; i < 2 * DB; ++i) q[i] = *(const v8*)(p + 16 * i);
 }
 
-// A running softmax's state of a lane's column: the maximum (the same in both halves'
-// lanes) and this lane's part of the sum.
+// A value of this lane's column from both halves' lanes, without a trip through LDS:
+// v_permlane32_swap_b32 exchanges one register's upper lanes with another's lower.
+struct Halves {
+  float a, b;
+};
+__device__ __forceinline__ Halves halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return {__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+__device__ __forceinline__ float both_sum(float x) {
+  const Halves h = halves(x);
+  return h.a + h.b;
+}
+
+// A running softmax's state of a lane's column: what its scores are taken relative to (the
+// same in both halves' lanes) and this lane's part of the sum.
 struct Running {
   float top = kNone, sum = 0.0f;
 };
 
-// Scores (16 a lane and block of 32 slots) -> right operands of the second product; o is
-// scaled where the maximum moved.  A column without a score above -infinity stays at
-// sum 0.  exp(scale*(s - top)) is 2^(s*scale2 - top*scale2), one fma and one v_exp_f32;
-// NaN scores stay NaN, as a sum that is not a number shows.
+// Scores (16 a lane and block of 32 slots) -> right operands of the second product.
+// exp(scale*(s - top)) is 2^(s*scale2 - top*scale2), one fma and one v_exp_f32.  `top` only
+// follows the maximum once that is kSlack powers of two above it in some column, so that
+// the accumulators are scaled a few times a sequence and not with most tiles: a probability
+// may then be up to 2^kSlack, which f16 and bf16 hold as exactly as one below 1 (and an f32 sum of
+// 2^31 of them too), and what is small is no smaller than relative to the maximum itself.
+// A column without a score above -infinity stays at sum 0; NaN scores stay NaN, as a sum
+// that is not a number shows.
+constexpr float kSlack = 7.0f;
 template <int TYPE, int DB, int KB>
 __device__ __forceinline__ void soften(v16f (&s)[KB], float scale2, Running& run, v16f (&o)[DB],
                                        typename Math<TYPE>::v8 (&p)[2 * KB]) {
@@ -127,10 +147,11 @@ __device__ __forceinline__ void soften(v16f (&s)[KB], float scale2, Running& run
   for (int k = 0; k < KB; ++k)
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[k][i]);
-  top = fmaxf(top, __shfl_xor(top, 32));
-  top = fmaxf(top, run.top);
-  if (__any(top > run.top)) {
-    // -infinity minus -infinity is kept out: such a column has no sum and nothing to scale
+  const Halves t = halves(top);
+  top = fmaxf(t.a, t.b);
+  const bool far = (top - run.top) * scale2 > kSlack;  // -infinity minus itself is not
+  if (__any(far)) {
+    top = far ? top : run.top;  // a column's numbers do not go by its neighbours'
     const float by = run.top == kNone ? 0.0f : __builtin_amdgcn_exp2f((run.top - top) * scale2);
     run.top = top;
     run.sum *= by;
@@ -139,7 +160,7 @@ __device__ __forceinline__ void soften(v16f (&s)[KB], float scale2, Running& run
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] *= by;
   }
-  const float off = top == kNone ? 0.0f : -top * scale2;
+  const float off = run.top == kNone ? 0.0f : -run.top * scale2;
   float sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < KB; ++k)
@@ -161,22 +182,12 @@ __device__ __forceinline__ void hide(v16f& s, int slot0, int half, int low, int 
   }
 }
 
-// Whether an operand holds an infinity or NaN.
-template <int TYPE, class V>
-__device__ __forceinline__ bool not_finite(const V& v) {
-  const v4i w = __builtin_bit_cast(v4i, v);
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r |= ((uint32_t)w[i] & Math<TYPE>::kExponent) + Math<TYPE>::kOne;
-  return (r & 0x80008000u) != 0;
-}
-
 // The operand with zeros for what is no finite number.
 template <int TYPE, class V>
 __device__ __forceinline__ V finite(const V& v) {
   u16x8 u = __builtin_bit_cast(u16x8, v);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) u[j] = (u[j] & (uint16_t)Math<TYPE>::kExponent) == (uint16_t)Math<TYPE>::kExponent ? 0 : u[j];
+  for (int j = 0; j < 8; ++j) u[j] = (u[j] & Math<TYPE>::kExponent) == Math<TYPE>::kExponent ? 0 : u[j];
   return __builtin_bit_cast(V, u);
 }
 
@@ -189,10 +200,11 @@ __device__ __forceinline__ float value_of(const uint8_t* tile, int dim, int r, i
     return (float)((const elem_t<TYPE>*)tile)[value_at(r, d)];
 }
 
-// The slots of a split that only some of a wave's columns see: a value there that is no
-// finite number must not reach the others, and on the matrix core their 0 times
-// it would be NaN.  Such values are zero in the product (`finite`), and where there
-// were any, they are added here to the columns that see them, channel by channel.
+// The slots that only some columns of a work-group see, or none: a value there that is
+// no finite number must not reach the others, and on the matrix core their 0 times it
+// would be NaN.  A result that is no finite number may be such a one: the work-group then
+// does its tile again with zeros for those values in the product (`finite`), and they are
+// added here to the columns that see them, channel by channel.
 struct Edges {
   int from, end;  // tiles of the split
   int step;       // tiles taken at a time
@@ -235,6 +247,14 @@ __device__ __forceinline__ void store_four(const AttnArgs& a, int dim, int row, 
   uint8_t* const out = (uint8_t*)a.out;
   *(uint32_t*)(out + block * 1024 + ((k & 31) >> 4) * 512 + (row & 31) * 16 + (k & 15)) = q.codes;
   if ((k & 31) == 0) *(uint32_t*)(out + a.t_pad * id + block * 128 + (row & 31) * 4) = q.pair;
+}
+
+// Adds a part's sums, which are relative to `mine`, to sums relative to `top`.
+__device__ __forceinline__ void add_part(float4& x, float& total, const float4& part, float mine, float sum, float top,
+                                         float scale2) {
+  const float by = mine == kNone ? 0.0f : __builtin_amdgcn_exp2f((mine - top) * scale2);
+  total = fmaf(sum, by, total);
+  x.x = fmaf(part.x, by, x.x), x.y = fmaf(part.y, by, x.y), x.z = fmaf(part.z, by, x.z), x.w = fmaf(part.w, by, x.w);
 }
 
 // Four channels of a column's sums: to the split's partial results, or as the output.

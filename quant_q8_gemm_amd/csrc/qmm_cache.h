@@ -63,16 +63,31 @@ struct Sequence {
 
 __host__ __device__ inline int clamped(int v, int low, int high) { return v < low ? low : v > high ? high : v; }
 
+// One of the batch's numbers, at an index that is the same in every lane.  On the GPU a
+// scalar load: a vector load's wait would be one for every load before it, those of
+// the tiles ahead among them.
+__host__ __device__ inline int32_t uniform_load(const int32_t* p, int64_t i) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[i];
+#else
+  return p[i];
+#endif
+}
+
 __host__ __device__ inline Sequence sequence(const Batch& b, int page_shift, int s) {
-  const int first = clamped(b.starts[s], 0, b.n_tok), end = clamped(b.starts[s + 1], first, b.n_tok);
-  return {first, end - first, clamped(b.lengths[s], 0, b.columns << page_shift)};
+  const int first = clamped(uniform_load(b.starts, s), 0, b.n_tok);
+  const int end = clamped(uniform_load(b.starts, s + 1), first, b.n_tok);
+  return {first, end - first, clamped(uniform_load(b.lengths, s), 0, b.columns << page_shift)};
 }
 
 // Byte offset in a pool of the tile of head h that holds slots 32*tile .. of sequence
-// s; -1 where the page is none of the pool's.  0 <= 32*tile < columns * page.
+// s; -1 where the page is none of the pool's.  0 <= 32*tile < columns * page.  UNIFORM: s
+// and tile are the same in every lane.
+template <bool UNIFORM = false>
 __host__ __device__ inline int64_t tile_offset(const Batch& b, const Pools& p, int s, int h, int tile) {
   const int tiles_shift = p.page_shift - 5;
-  const int page = b.table[s * b.table_stride + (tile >> tiles_shift)];
+  const int64_t i = s * b.table_stride + (tile >> tiles_shift);
+  const int page = UNIFORM ? uniform_load(b.table, i) : b.table[i];
   if (page < 0 || page >= p.n_pages) return -1;
   const int64_t at = (((int64_t)page * p.heads + h) << tiles_shift) + (tile & ((1 << tiles_shift) - 1));
   return at * tile_bytes(p.type, p.dim);
