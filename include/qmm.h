@@ -644,8 +644,9 @@ int qmm_attention(const qmm_attn *args, const qmm_cache *cache, const qmm_batch 
 
 /* How a qmm_attention is launched: the (token, head of its group) pairs of a
  * sequence and a cache head are columns, taken `columns` at a time; the keys of
- * such a tile are split into `splits` parts of whole 32-slot tiles, whose partial
- * results a second kernel joins. */
+ * such a tile are split into up to `splits` parts of whole 32-slot tiles, `share` of
+ * them each (more where max_length is passed), whose partial results a second
+ * kernel joins. */
 typedef struct {
     size_t work_bytes;   /* partial results (0: none) */
     int64_t work_groups;
@@ -654,16 +655,17 @@ typedef struct {
     int32_t columns;
     int32_t tiles;       /* column tiles of a sequence and cache head with max_new */
     int32_t splits;
+    int32_t share;
 } qmm_attn_plan;
 
 /*
  * qmm_attention_plan -- the plan of qmm_attention for these sizes on a GPU with
  * num_cus compute units; host arithmetic only.  Of `cache` type, heads and head_dim
- * count, of `batch` n_seq, max_new and max_length.
+ * count, of `batch` n_seq, max_new and max_length; heads and window as in qmm_attn.
  * Errors: QMM_EINVAL.
  */
-int qmm_attention_plan(const qmm_cache *cache, const qmm_batch *batch, int heads, int64_t n_tok, int num_cus,
-                       qmm_attn_plan *out);
+int qmm_attention_plan(const qmm_cache *cache, const qmm_batch *batch, int heads, int64_t window, int64_t n_tok,
+                       int num_cus, qmm_attn_plan *out);
 
 /* The launch plan of one MMQ (qmm_mmq, qmm_mmq_noalloc): how its output tiles
  * map onto work-groups on a GPU of a given size, and the tail partials it needs.

@@ -134,7 +134,8 @@ class Attn(ctypes.Structure):
 
 class AttnPlan(ctypes.Structure):
     _fields_ = [("work_bytes", ctypes.c_size_t), ("work_groups", ctypes.c_int64), ("few", ctypes.c_int32),
-                ("columns", ctypes.c_int32), ("tiles", ctypes.c_int32), ("splits", ctypes.c_int32)]
+                ("columns", ctypes.c_int32), ("tiles", ctypes.c_int32), ("splits", ctypes.c_int32),
+                ("share", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -185,7 +186,7 @@ _lib.qmm_cache_read.argtypes = [*_CB, _I64, ctypes.c_int, _P, _P, _P]
 _lib.qmm_cache_read.restype = ctypes.c_int
 _lib.qmm_attention.argtypes = [ctypes.POINTER(Attn), *_CB, _I64, _P, _SZ, _P]
 _lib.qmm_attention.restype = ctypes.c_int
-_lib.qmm_attention_plan.argtypes = [*_CB, ctypes.c_int, _I64, ctypes.c_int, ctypes.POINTER(AttnPlan)]
+_lib.qmm_attention_plan.argtypes = [*_CB, ctypes.c_int, _I64, _I64, ctypes.c_int, ctypes.POINTER(AttnPlan)]
 _lib.qmm_attention_plan.restype = ctypes.c_int
 _lib.qmm_last_error.argtypes = []
 _lib.qmm_last_error.restype = ctypes.c_char_p
@@ -725,10 +726,10 @@ def cache_read(cache: Cache, batch: Batch, n_tok: int, *, dtype=torch.float32, s
     return k.view(shape), v.view(shape)
 
 
-def attention_plan(cache: Cache, batch: Batch, heads: int, n_tok: int, num_cus: int) -> AttnPlan:
+def attention_plan(cache: Cache, batch: Batch, heads: int, n_tok: int, num_cus: int, window: int = 0) -> AttnPlan:
     """How attention of these sizes is launched, and the work memory it needs (host arithmetic only)."""
     plan = AttnPlan()
-    _check(_lib.qmm_attention_plan(cache.struct, batch._for(cache, n_tok), heads, n_tok, num_cus, plan))
+    _check(_lib.qmm_attention_plan(cache.struct, batch._for(cache, n_tok), heads, window, n_tok, num_cus, plan))
     return plan
 
 
@@ -770,7 +771,7 @@ def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: boo
     if work is None:
         if device not in _cus:
             _cus[device] = torch.cuda.get_device_properties(device).multi_processor_count
-        need = attention_plan(cache, batch, heads, n_tok, _cus[device]).work_bytes
+        need = attention_plan(cache, batch, heads, n_tok, _cus[device], window).work_bytes
         work = _empty(q, (need,), torch.uint8, stream) if need else None
     work_ptr, work_bytes = _bytes(work, "work", device) if work is not None and work.numel() else (None, 0)
     _check(_lib.qmm_attention(a, cache.struct, b, n_tok, work_ptr, work_bytes, _raw_stream(stream, device)))

@@ -1132,7 +1132,7 @@ int check_attention_launch(const qmm::AttnPlan& plan) {
 
 extern "C" {
 
-int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads, int64_t n_tok, int num_cus,
+int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads, int64_t window, int64_t n_tok, int num_cus,
                        qmm_attn_plan* out) {
   if (out == nullptr) return fail(QMM_EINVAL, "out is NULL");
   std::memset(out, 0, sizeof *out);
@@ -1146,11 +1146,12 @@ int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads
   if (b.max_new < 0 || b.max_new > QMM_MAX_TOKENS || b.max_length < 0 || b.max_length > INT32_MAX)
     return fail(QMM_EINVAL, "max_new must be in [0, %d] and max_length in [0, 2^31), got %lld and %lld", QMM_MAX_TOKENS,
                 (long long)b.max_new, (long long)b.max_length);
+  if (window < 0) return fail(QMM_EINVAL, "window must not be negative, got %lld", (long long)window);
   if (num_cus < 1 || num_cus > QMM_MAX_CUS)
     return fail(QMM_EINVAL, "num_cus must be in [1, %d], got %d", QMM_MAX_CUS, num_cus);
   if (n_tok > 0) {
-    const qmm::AttnPlan plan = qmm::plan_attention(cache->type, heads, cache->heads, cache->head_dim, b.n_seq, n_tok,
-                                                   b.max_new, b.max_length, num_cus);
+    const qmm::AttnPlan plan = qmm::plan_attention(heads, cache->heads, cache->head_dim, b.n_seq, n_tok, b.max_new, b.max_length,
+                                                   window, num_cus);
     if (int rc = check_attention_launch(plan)) return rc;
     *out = {plan.work_bytes, plan.work_groups, plan.few ? 1 : 0, plan.columns, plan.tiles, plan.splits};
   }
@@ -1212,8 +1213,8 @@ int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch*
   if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
   e = hipDeviceGetAttribute(&num_cus, hipDeviceAttributeMultiprocessorCount, device);
   if (e != hipSuccess) return fail_hip(e, "hipDeviceGetAttribute(multiprocessor count)");
-  const qmm::AttnPlan plan = qmm::plan_attention(cache->type, a.heads, cache->heads, cache->head_dim, batch->n_seq, n_tok,
-                                                 batch->max_new, batch->max_length, num_cus);
+  const qmm::AttnPlan plan = qmm::plan_attention(a.heads, cache->heads, cache->head_dim, batch->n_seq, n_tok, batch->max_new,
+                                                 batch->max_length, a.window, num_cus);
   if (int rc = check_attention_launch(plan)) return rc;
   if (work_bytes < plan.work_bytes)
     return fail(QMM_EINVAL, "work_bytes %zu, but this launch needs %zu bytes of work memory (qmm_attention_plan)", work_bytes,
@@ -1232,6 +1233,7 @@ int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch*
   r.causal = a.causal;
   r.q8_out = a.out_type == QMM_Q8;
   r.splits = plan.splits;
+  r.share = plan.share;
   r.columns = plan.columns;
   r.tiles = plan.tiles;
   r.t_pad = token_pad(n_tok);

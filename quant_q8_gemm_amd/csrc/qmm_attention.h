@@ -16,6 +16,7 @@ struct AttnArgs {
   int64_t window;                   // 0: none
   int32_t heads, group;             // heads per head of the cache
   int32_t causal, q8_out, splits, columns, tiles;
+  int32_t share;                    // tiles of a split at least; splits * share cover max_length
   int64_t t_pad;                    // rows of the qact buffer
   float scale2;                     // scale / ln 2: the exponentials are powers of two
 };
@@ -23,12 +24,12 @@ struct AttnArgs {
 // Plan of a launch (qmm_attention_plan).
 struct AttnPlan {
   bool few;
-  int columns, tiles, splits;
+  int columns, tiles, splits, share;
   int64_t work_groups;
   size_t work_bytes;
 };
-AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new,
-                        int64_t max_length, int num_cus);
+AttnPlan plan_attention(int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new, int64_t max_length,
+                        int64_t window, int num_cus);
 
 // The product kernels of one cache type (a source file each), on a checked plan;
 // and the kernel that joins the splits.

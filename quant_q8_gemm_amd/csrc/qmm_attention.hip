@@ -8,6 +8,7 @@
 #include "qmm_internal.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace qmm {
 
@@ -44,7 +45,10 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Batch batch, int 
           const int64_t at = (k < a.splits ? k : k0) * all + row;
           m[j] = a.sums[at];
           v[j] = *(const float4*)(a.part + at * dim + d);
-          if (k >= a.splits) m[j] = make_float2(kNone, 0.0f);
+          if (k >= a.splits || m[j].y == 0.0f) {  // not there, or nothing was seen in it
+            m[j] = make_float2(kNone, 0.0f);
+            v[j] = make_float4(0, 0, 0, 0);
+          }
         }
         const float now = fmaxf(fmaxf(fmaxf(m[0].x, m[1].x), fmaxf(m[2].x, m[3].x)), top);
         const float4 so_far = x;
@@ -53,7 +57,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Batch batch, int 
         add_part(x, total, so_far, top, sum, now, a.scale2);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (k0 + j * LANES < a.splits) add_part(x, total, v[j], m[j].x, m[j].y, now, a.scale2);
+          add_part(x, total, v[j], m[j].x, m[j].y, now, a.scale2);
         top = now;
       }
     }
@@ -92,17 +96,25 @@ hipError_t launch_join(const AttnArgs& a, const Pools& p, const Batch& b, hipStr
 
 }  // namespace
 
-AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new,
-                        int64_t max_length, int num_cus) {
+AttnPlan plan_attention(int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new, int64_t max_length,
+                        int64_t window, int num_cus) {
   AttnPlan plan{};
   const int64_t group = heads / kv_heads, flats = std::clamp<int64_t>(max_new, 1, n_tok) * group;
   plan.few = flats <= 64;
   plan.columns = plan.few ? (int)std::min<int64_t>(flats, 32) : 128;
   plan.tiles = (int)((flats + plan.columns - 1) / plan.columns);
-  // Splits: enough work-groups for the compute units, each with some tiles for every wave.
-  const int64_t base = n_seq * kv_heads * plan.tiles, tiles = (max_length + kTileSlots - 1) / kTileSlots;
-  const int64_t want = (2 * (int64_t)num_cus + base - 1) / base, most = tiles / (plan.few ? 16 : 32);
-  plan.splits = (int)std::clamp<int64_t>(std::min(want, most), 1, 256);
+  // the most tiles of 32 slots that a tile of columns reads
+  int64_t keys = max_length;
+  if (window > 0) keys = std::min(keys, window + plan.columns / group + kTileSlots);
+  const int64_t tiles = std::max<int64_t>((keys + kTileSlots - 1) / kTileSlots, 1);
+  const int64_t base = n_seq * kv_heads * plan.tiles, slots = 2 * (int64_t)num_cus;
+  const int64_t least = plan.few ? 8 : 32, unit = plan.few ? 4 : 2;
+  int64_t share = std::max(least, (base * tiles + slots - 1) / slots);
+  share = (share + unit - 1) / unit * unit;
+  if (const char* e = getenv("XSHARE")) share = atoi(e);
+  share = std::max(share, (tiles + 255) / 256);
+  plan.splits = (int)((tiles + share - 1) / share);
+  plan.share = (int)share;
   plan.work_groups = base * plan.splits;
   plan.work_bytes = plan.splits == 1 ? 0 : (size_t)plan.splits * n_tok * heads * ((size_t)dim * 4 + 8);
   return plan;

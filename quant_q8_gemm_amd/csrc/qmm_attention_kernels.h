@@ -98,8 +98,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
     seen(a, seq, first / a.group, last / a.group, low, high);
     seen(a, seq, first / a.group, first / a.group, unused, all_high);
     seen(a, seq, last / a.group, last / a.group, all_low, unused);
-    const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin), share = (tiles + a.splits - 1) / a.splits;
+    const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin), share = max(a.share, (tiles + a.splits - 1) / a.splits);
     const int from = begin + split * share, end = min(begin + tiles, from + share);
+    if (split > 0 && from >= end) {  // nothing left for this split
+      no_part(a, seq, batch.n_tok, h, split, first, last);
+      continue;
+    }
 
     for (bool safe = false;; safe = true) {
       // A tile's loads are issued whether it is there or not (the pool's first instead, which
@@ -335,8 +339,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
     const bool idle = first + 32 * wave > last;
     const Column c = column(a, seq, h, first + 32 * wave + (lane & 31));
     const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin);
-    const int share = (tiles + a.splits * KB - 1) / (a.splits * KB) * KB;
+    const int share = max(a.share, (tiles + a.splits * KB - 1) / (a.splits * KB) * KB);
     const int from = begin + split * share, end = min(begin + tiles, from + share);
+    if (split > 0 && from >= end) {  // nothing left for this split
+      no_part(a, seq, batch.n_tok, h, split, first, last);
+      continue;
+    }
 
     v8 q[2 * DB];
     load_queries<TYPE, DB>(a, c, lane, q);

@@ -271,6 +271,16 @@ __device__ __forceinline__ void store_part(const AttnArgs& a, int dim, int n_tok
   }
 }
 
+// The columns from `first` to `last` have no part in this split: a sum of 0, whose numbers the
+// join does not read.
+__device__ __forceinline__ void no_part(const AttnArgs& a, const Sequence& seq, int n_tok, int kv_head, int split, int first,
+                                        int last) {
+  for (int flat = first + (int)threadIdx.x; flat <= last; flat += (int)blockDim.x) {
+    const Column c = column(a, seq, kv_head, flat);
+    a.sums[(int64_t)c.row * a.heads + c.head + (int64_t)split * n_tok * a.heads] = make_float2(kNone, 0.0f);
+  }
+}
+
 // Zeros in the padding tokens of a qact buffer, by `threads` threads together.
 __device__ __forceinline__ void zero_padding(const AttnArgs& a, int dim, int n_tok, int64_t thread, int64_t threads) {
   const int64_t id = (int64_t)a.heads * dim, blocks = id >> 5, tokens = a.t_pad - n_tok;

@@ -16,7 +16,7 @@ struct RopeArgs {
   const int32_t* positions;
   int32_t type, out_type, q_heads, layout, n_rot;
   float magnitude;
-  int32_t heads_per_job, q_jobs, k_jobs;  // set by the launcher
+  int32_t q_heads_per_job, heads_per_job, q_jobs, k_jobs;  // set by the launcher
 };
 
 hipError_t launch_rope(RopeArgs r, const Pools& p, const Batch& b, int64_t max_new, hipStream_t s);

@@ -53,6 +53,28 @@ __device__ __forceinline__ void store8_any(int type, void* p, int64_t i, const f
   else store8<QMM_BF16>(p, i, x);
 }
 
+// (cos, sin) of `turn` turns.  The nearest quarter turn is taken off in 64 bits; of the rest,
+// |x| <= pi/4 once in f32, the Taylor polynomials to x^9 and x^10 (their remainders are
+// below 3e-9 and 2e-10).  The sum of the roundings is below 4 * 2^-24.  A third of the
+// instructions of the library's sincospi, which with 256 rotated channels took most of
+// the time of a work-group with few heads (7 x 129 tokens, 16+4 heads of 256: 12.3 us).
+__device__ __forceinline__ float2 turned(double turn) {
+  const double y = 4.0 * (turn - __builtin_rint(turn)), n = __builtin_rint(y);
+  const float x = (float)(y - n) * 1.57079632679f, x2 = x * x;
+  const int quarter = (int)n;
+  float s = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);
+  s = fmaf(x2, s, 8.33333333e-3f);
+  s = fmaf(x2, s, -1.66666667e-1f);
+  s = fmaf(x * x2, s, x);
+  float c = fmaf(x2, -2.75573192e-7f, 2.48015873e-5f);
+  c = fmaf(x2, c, -1.38888889e-3f);
+  c = fmaf(x2, c, 4.16666667e-2f);
+  c = fmaf(x2, c, -0.5f);
+  c = fmaf(x2, c, 1.0f);
+  const float a = (quarter & 1) != 0 ? s : c, b = (quarter & 1) != 0 ? c : s;
+  return make_float2(((quarter + 1) & 2) != 0 ? -a : a, (quarter & 2) != 0 ? -b : b);
+}
+
 // What a thread rotates at a time: 16 channels of a token's head as two runs of
 // eight.  Half layout: the runs at `u`*8 in both halves; interleaved, and where
 // nothing turns: 16 channels in a row.
@@ -91,9 +113,25 @@ __device__ __forceinline__ void rotate(const RopeArgs& r, const float2* turn, fl
   }
 }
 
+// A thread's unit of a head as loaded: 16 values, still of their type.
+template <int IN>
+struct Loaded16 {
+  typedef elem_t<IN> v8 __attribute__((ext_vector_type(8)));
+  v8 a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t i, const Unit& at) {
+    a = *(const v8*)((const elem_t<IN>*)p + i + at.a);
+    b = *(const v8*)((const elem_t<IN>*)p + i + at.b);
+  }
+  __device__ __forceinline__ void get(float (&x)[8], float (&y)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)a[i], y[i] = (float)b[i];
+  }
+};
+
 // IN: type of q, k and v; CACHE: of the cache.  blockIdx: x the 16 slots (in steps of
-// the grid, where the sequence has more), y the job (heads_per_job heads of q, k or v),
-// z the sequence.
+// the grid, where the sequence has more), y the job (some heads of q, k or v), z the
+// sequence.  A thread keeps its token and channels and goes from head to head, the
+// next head's values on their way while it works on one.
 template <int IN, int CACHE>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools, Batch batch) {
   extern __shared__ float lds[];
@@ -102,8 +140,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools,
   if (seq.count == 0) return;
   // which tensor, and which of its heads
   const int kind = job < r.q_jobs ? 0 : job < r.q_jobs + r.k_jobs ? 1 : 2;
-  const int head0 = (job - (kind == 0 ? 0 : kind == 1 ? r.q_jobs : r.q_jobs + r.k_jobs)) * r.heads_per_job;
-  const int heads = min(r.heads_per_job, (kind == 0 ? r.q_heads : pools.heads) - head0);
+  const int per_job = kind == 0 ? r.q_heads_per_job : r.heads_per_job;
+  const int head0 = (job - (kind == 0 ? 0 : kind == 1 ? r.q_jobs : r.q_jobs + r.k_jobs)) * per_job;
+  const int head_end = min(head0 + per_job, kind == 0 ? r.q_heads : pools.heads);
   const int dim = pools.dim, units = dim >> 4, half = r.n_rot >> 1;
   const int slot0 = seq.length - seq.count;  // of the first new token; below 0: tokens without a slot
   float2* const turns = (float2*)lds;                               // [16][half]
@@ -115,121 +154,148 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools,
     if (base >= seq.length) break;
     const int from = max(0, slot0 - base), to = min(kSlots, seq.length - base), count = to - from;
     const int row0 = seq.first + base - slot0;  // row of slot `base`
+    if (kind > 0 && base < 0) continue;         // keys and values of slots below 0: there is none
+    const int in_tile = base & 31;
+    // the tile of head 0, and the bytes from head to head
+    const int64_t tile0 = kind > 0 ? tile_offset<true>(batch, pools, s, 0, base >> 5) : 0;
+    const int64_t tile_step = (int64_t)tile_bytes(CACHE, dim) << (pools.page_shift - 5);
+    if (tile0 < 0) continue;  // a page outside the pool
+    const Rows& x = kind == 0 ? r.q : kind == 1 ? r.k : r.v;
+    // Token and unit of a thread (at most 16 * 16 of them), and as many heads side by side
+    // as there are threads for.  The first head's values are on their way while the turns
+    // are computed.
+    const int places = count * units, side = kThreads / places;
+    int h = head0 + (int)threadIdx.x / places;
+    const bool turning = kind == 0 || (kind == 1 && CACHE != QMM_Q8), mine = (int)threadIdx.x < side * places;
+    const int t = from + (int)threadIdx.x % places / units;
+    const Unit at = unit(r, (int)threadIdx.x % places % units);
+    const int64_t in = (row0 + t) * x.stride;
+    Loaded16<IN> now;
+    if (turning && mine && h < head_end) now.load(x.p, in + h * x.head_stride, at);
     if (kind < 2) {
-      for (int i = threadIdx.x; i < count * half; i += kThreads) {
-        const int t = from + i / half, pair = i % half;
-        const int p = r.positions != nullptr ? r.positions[row0 + t] : base + t;
-        const double turn = (double)p * r.frequencies[pair] * 0.15915494309189533577;  // 1/(2 pi)
-        float sine, cosine;
-        sincospif(2.0f * (float)(turn - __builtin_rint(turn)), &sine, &cosine);
-        turns[t * half + pair] = make_float2(cosine * r.magnitude, sine * r.magnitude);
+      if (half > 0) {  // a thread keeps its pair and goes from token to token
+        const int abreast = kThreads / half, pair = (int)threadIdx.x % half;
+        int token = (int)threadIdx.x / half;
+        const auto position = [&](int i) {
+          return i >= count ? 0 : r.positions != nullptr ? r.positions[row0 + from + i] : base + from + i;
+        };
+        if (token < abreast) {
+          const double f = r.frequencies[pair] * 0.15915494309189533577;  // 1/(2 pi)
+          int p = position(token);
+          for (; token < count; token += abreast) {
+            const int next = position(token + abreast);
+            const float2 turn = turned((double)p * f);
+            turns[(from + token) * half + pair] = make_float2(turn.x * r.magnitude, turn.y * r.magnitude);
+            p = next;
+          }
+        }
       }
       __syncthreads();
     }
-    if (kind == 0) {
-      for (int i = threadIdx.x; i < count * heads * units; i += kThreads) {
-        const int u = i % units, j = i / units, t = from + j % count, h = head0 + j / count;
-        const Unit at = unit(r, u);
-        const int64_t in = (row0 + t) * r.q.stride + h * r.q.head_stride;
-        const int64_t out = (row0 + t) * r.q_out.stride + h * r.q_out.head_stride;
-        float a[8], b[8];
-        load8<IN>(r.q.p, in + at.a, a);
-        load8<IN>(r.q.p, in + at.b, b);
-        if (at.pair >= 0) rotate(r, turns + t * half + at.pair, a, b);
-        store8_any(r.out_type, (void*)r.q_out.p, out + at.a, a);
-        store8_any(r.out_type, (void*)r.q_out.p, out + at.b, b);
-      }
-    } else if (base >= 0) {  // keys and values; slots below 0 are none
-      const Rows& x = kind == 1 ? r.k : r.v;
-      const int tile = base >> 5, in_tile = base & 31;
-      if constexpr (CACHE != QMM_Q8) {
-        if (kind == 1) {
-          for (int i = threadIdx.x; i < count * heads * units; i += kThreads) {
-            const int u = i % units, j = i / units, t = from + j % count, h = head0 + j / count;
-            const Unit at = unit(r, u);
-            const int64_t in = (row0 + t) * x.stride + h * x.head_stride;
-            float a[8], b[8];
-            load8<IN>(x.p, in + at.a, a);
-            load8<IN>(x.p, in + at.b, b);
-            if (at.pair >= 0) rotate(r, turns + t * half + at.pair, a, b);
-            const int64_t to_tile = tile_offset(batch, pools, s, h, tile);
-            if (to_tile < 0) continue;
-            store8<CACHE>(pools.k + to_tile, key_at(in_tile + t, at.a), a);
-            store8<CACHE>(pools.k + to_tile, key_at(in_tile + t, at.b), b);
-          }
-        } else {
-          typedef elem_t<CACHE> T;
-          typedef T v8 __attribute__((ext_vector_type(8)));
-          for (int i = threadIdx.x; i < 2 * heads * dim; i += kThreads) {  // eight slots of a channel
-            const int d = i % dim, j = i / dim, g = 8 * (j & 1), h = head0 + (j >> 1);
-            if (g + 8 <= from || g >= to) continue;
-            const int64_t to_tile = tile_offset(batch, pools, s, h, tile);
-            if (to_tile < 0) continue;
-            v8 e;
+    if (turning) {
+      if (mine) {
+        float2 turn[8];
+        if (at.pair >= 0) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const bool is = g + n >= from && g + n < to;
-              e[n] = is ? (T)(float)((const elem_t<IN>*)x.p)[(row0 + g + n) * x.stride + h * x.head_stride + d] : (T)0.0f;
-            }
-            T* const p = (T*)(pools.v + to_tile) + value_at(in_tile + g, d);
-            if (g >= from && g + 8 <= to) {
-              *(v8*)p = e;
-            } else {
-#pragma unroll
-              for (int n = 0; n < 8; ++n)
-                if (g + n >= from && g + n < to) p[n] = e[n];
-            }
+          for (int i = 0; i < 8; ++i) turn[i] = turns[t * half + at.pair + i];
+        }
+        const int64_t out = (row0 + t) * r.q_out.stride;
+        for (; h < head_end; h += side) {
+          float a[8], b[8];
+          now.get(a, b);
+          if (h + side < head_end) now.load(x.p, in + (h + side) * x.head_stride, at);
+          if (at.pair >= 0) rotate(r, turn, a, b);
+          if (kind == 0) {
+            const int64_t o = out + h * r.q_out.head_stride;
+            store8_any(r.out_type, (void*)r.q_out.p, o + at.a, a);
+            store8_any(r.out_type, (void*)r.q_out.p, o + at.b, b);
+          } else if constexpr (CACHE != QMM_Q8) {
+            uint8_t* const to_tile = pools.k + tile0 + h * tile_step;
+            store8<CACHE>(to_tile, key_at(in_tile + t, at.a), a);
+            store8<CACHE>(to_tile, key_at(in_tile + t, at.b), b);
           }
         }
-      } else {
-        for (int h = head0; h < head0 + heads; ++h) {
-          __syncthreads();  // the head before is out of the stage
-          for (int i = threadIdx.x; i < count * units; i += kThreads) {
-            const int u = i % units, t = from + i / units;
-            const Unit at = kind == 1 ? unit(r, u) : Unit{16 * u, 16 * u + 8, -1};
-            const int64_t in = (row0 + t) * x.stride + h * x.head_stride;
-            float a[8], b[8];
-            load8<IN>(x.p, in + at.a, a);
-            load8<IN>(x.p, in + at.b, b);
-            if (at.pair >= 0) rotate(r, turns + t * half + at.pair, a, b);
-            store8<QMM_F32>(stage, t * (dim + 4) + at.a, a);
-            store8<QMM_F32>(stage, t * (dim + 4) + at.b, b);
-          }
-          __syncthreads();
-          const int64_t to_tile = tile_offset(batch, pools, s, h, tile);  // the same in every thread
-          if (to_tile < 0) continue;
-          uint8_t* const out = (kind == 1 ? pools.k : pools.v) + to_tile;
-          // four lanes quantize a block of 32 channels, eight each; dim/32 blocks times 4 lanes
-          // times the tokens, in whole groups of four lanes
-          for (int i = threadIdx.x; i < count * (dim >> 3); i += kThreads) {
-            const int d = 8 * (i % (dim >> 3)), t = from + i / (dim >> 3);
-            float x8[8];
-            load8<QMM_F32>(stage, t * (dim + 4) + d, x8);
-            const Q8Part<8> q = quant_part<8>(x8);
-            const uint2 c = make_uint2(q.codes[0] ^ 0x80808080u, q.codes[1] ^ 0x80808080u);
-            if (kind == 1) {
-              *(uint2*)(out + key_code_at(in_tile + t, d)) = c;
-            } else {
-              *(uint32_t*)(codes + t * (dim + 4) + d) = c.x;
-              *(uint32_t*)(codes + t * (dim + 4) + d + 4) = c.y;
-            }
-            if ((i & 3) == 0) *(uint16_t*)(out + scale_at(dim, in_tile + t, d >> 5)) = (uint16_t)q.pair;
-          }
-          if (kind == 2) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < 2 * dim; i += kThreads) {
-              const int d = i % dim, g = 8 * (i / dim);
-              if (g + 8 <= from || g >= to) continue;
-              uint8_t* const p = out + value_code_at(in_tile + g, d);
-              if (g >= from && g + 8 <= to) {
-                uint32_t w[2] = {0, 0};
+      }
+    } else if constexpr (CACHE != QMM_Q8) {
+      typedef elem_t<CACHE> T;
+      typedef T v8 __attribute__((ext_vector_type(8)));
+      // eight slots of a channel
+      const int runs = 2 * dim, beside = max(1, kThreads / runs);
+      for (int run = threadIdx.x % min(runs, kThreads); run < runs; run += kThreads) {
+        int h = head0 + (runs < kThreads ? (int)threadIdx.x / runs : 0);
+        if (runs < kThreads && (int)threadIdx.x >= beside * runs) break;
+        const int d = run % dim, g = run >= dim ? 8 : 0;
+        if (g + 8 <= from || g >= to) continue;
+        const elem_t<IN>* const in = (const elem_t<IN>*)x.p + (row0 + g) * x.stride + d;
+        elem_t<IN> now[8];
+        const auto load = [&](int head) {
 #pragma unroll
-                for (int n = 0; n < 8; ++n) w[n >> 2] |= (uint32_t)codes[(g + n) * (dim + 4) + d] << (8 * (n & 3));
-                *(uint2*)p = make_uint2(w[0], w[1]);
-              } else {
-                for (int n = 0; n < 8; ++n)
-                  if (g + n >= from && g + n < to) p[n] = codes[(g + n) * (dim + 4) + d];
-              }
+          for (int n = 0; n < 8; ++n)
+            if (g + n >= from && g + n < to) now[n] = in[n * x.stride + head * x.head_stride];
+        };
+#pragma unroll
+        for (int n = 0; n < 8; ++n) now[n] = (elem_t<IN>)0.0f;
+        if (h < head_end) load(h);
+        for (; h < head_end; h += beside) {
+          v8 e;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) e[n] = (T)(float)now[n];
+          if (h + beside < head_end) load(h + beside);
+          T* const p = (T*)(pools.v + tile0 + h * tile_step) + value_at(in_tile + g, d);
+          if (g >= from && g + 8 <= to) {
+            *(v8*)p = e;
+          } else {
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+              if (g + n >= from && g + n < to) p[n] = e[n];
+          }
+        }
+      }
+    } else {
+      for (int h = head0; h < head_end; ++h) {
+        __syncthreads();  // the head before is out of the stage
+        for (int i = threadIdx.x; i < count * units; i += kThreads) {
+          const int u = i % units, t = from + i / units;
+          const Unit at = kind == 1 ? unit(r, u) : Unit{16 * u, 16 * u + 8, -1};
+          float a[8], b[8];
+          Loaded16<IN> now;
+          now.load(x.p, (row0 + t) * x.stride + h * x.head_stride, at);
+          now.get(a, b);
+          if (at.pair >= 0) rotate(r, turns + t * half + at.pair, a, b);
+          store8<QMM_F32>(stage, t * (dim + 4) + at.a, a);
+          store8<QMM_F32>(stage, t * (dim + 4) + at.b, b);
+        }
+        __syncthreads();
+        uint8_t* const out = (kind == 1 ? pools.k : pools.v) + tile0 + h * tile_step;
+        // four lanes quantize a block of 32 channels, eight each
+        for (int i = threadIdx.x; i < count * (dim >> 3); i += kThreads) {
+          const int d = 8 * (i % (dim >> 3)), t = from + i / (dim >> 3);
+          float x8[8];
+          load8<QMM_F32>(stage, t * (dim + 4) + d, x8);
+          const Q8Part<8> q = quant_part<8>(x8);
+          const uint2 c = make_uint2(q.codes[0] ^ 0x80808080u, q.codes[1] ^ 0x80808080u);
+          if (kind == 1) {
+            *(uint2*)(out + key_code_at(in_tile + t, d)) = c;
+          } else {
+            *(uint32_t*)(codes + t * (dim + 4) + d) = c.x;
+            *(uint32_t*)(codes + t * (dim + 4) + d + 4) = c.y;
+          }
+          if ((i & 3) == 0) *(uint16_t*)(out + scale_at(dim, in_tile + t, d >> 5)) = (uint16_t)q.pair;
+        }
+        if (kind == 2) {
+          __syncthreads();
+          for (int i = threadIdx.x; i < 2 * dim; i += kThreads) {
+            const int d = i % dim, g = 8 * (i / dim);
+            if (g + 8 <= from || g >= to) continue;
+            uint8_t* const p = out + value_code_at(in_tile + g, d);
+            if (g >= from && g + 8 <= to) {
+              uint32_t w[2] = {0, 0};
+#pragma unroll
+              for (int n = 0; n < 8; ++n) w[n >> 2] |= (uint32_t)codes[(g + n) * (dim + 4) + d] << (8 * (n & 3));
+              *(uint2*)p = make_uint2(w[0], w[1]);
+            } else {
+              for (int n = 0; n < 8; ++n)
+                if (g + n >= from && g + n < to) p[n] = codes[(g + n) * (dim + 4) + d];
             }
           }
         }
@@ -244,38 +310,43 @@ __device__ __forceinline__ void put8(void* p, int64_t i, const float (&x)[8]) {
   if (p != nullptr) store8<TYPE>(p, i, x);
 }
 
+constexpr int kReadTokens = 4;  // of a work-group at a time
+
 // A thread reads eight channels of a token's head from both pools.
 template <int CACHE, int OUT>
 __global__ __launch_bounds__(kThreads) void read_kernel(Pools pools, Batch batch, void* k, void* v) {
-  const int s = blockIdx.z, runs = pools.dim >> 3;
+  const int s = blockIdx.z, runs = pools.dim >> 3, per_token = pools.heads * runs;
   const Sequence seq = sequence(batch, pools.page_shift, s);
   const int slot0 = seq.length - seq.count;
-  const int64_t all = (int64_t)seq.count * pools.heads * runs;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kThreads) {
-    const int d = 8 * (int)(i % runs), h = (int)(i / runs % pools.heads), t = (int)(i / runs / pools.heads);
-    const int slot = slot0 + t, r = slot & 31;
-    const int64_t tile = slot < 0 ? -1 : tile_offset(batch, pools, s, h, slot >> 5);
-    float a[8] = {}, b[8] = {};
-    if (tile >= 0) {
-      const uint8_t *tk = pools.k + tile, *tv = pools.v + tile;
-      if constexpr (CACHE == QMM_Q8) {
-        const float sk = (float)*(const _Float16*)(tk + scale_at(pools.dim, r, d >> 5));
-        const float sv = (float)*(const _Float16*)(tv + scale_at(pools.dim, r, d >> 5));
-        const uint2 c = *(const uint2*)(tk + key_code_at(r, d));
+  for (int t0 = blockIdx.x * kReadTokens; t0 < seq.count; t0 += gridDim.x * kReadTokens) {
+    const int tokens = min(kReadTokens, seq.count - t0);
+    for (int i = blockIdx.y * kThreads + threadIdx.x; i < per_token * tokens; i += gridDim.y * kThreads) {
+      // tokens side by side in a wave: eight of them share the pieces of a value tile
+      const int t = t0 + i % tokens, j = i / tokens, d = 8 * (j % runs), h = j / runs;
+      const int slot = slot0 + t, r = slot & 31;
+      const int64_t tile = slot < 0 ? -1 : tile_offset(batch, pools, s, h, slot >> 5);
+      float a[8] = {}, b[8] = {};
+      if (tile >= 0) {
+        const uint8_t *tk = pools.k + tile, *tv = pools.v + tile;
+        if constexpr (CACHE == QMM_Q8) {
+          const float sk = (float)*(const _Float16*)(tk + scale_at(pools.dim, r, d >> 5));
+          const float sv = (float)*(const _Float16*)(tv + scale_at(pools.dim, r, d >> 5));
+          const uint2 c = *(const uint2*)(tk + key_code_at(r, d));
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          a[n] = (float)((int)(((n < 4 ? c.x : c.y) >> (8 * (n & 3))) & 255) - 128) * sk;
-          b[n] = (float)((int)tv[value_code_at(r, d + n)] - 128) * sv;
+          for (int n = 0; n < 8; ++n) {
+            a[n] = (float)((int)(((n < 4 ? c.x : c.y) >> (8 * (n & 3))) & 255) - 128) * sk;
+            b[n] = (float)((int)tv[value_code_at(r, d + n)] - 128) * sv;
+          }
+        } else {
+          load8<CACHE>(tk, key_at(r, d), a);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) b[n] = (float)((const elem_t<CACHE>*)tv)[value_at(r, d + n)];
         }
-      } else {
-        load8<CACHE>(tk, key_at(r, d), a);
-#pragma unroll
-        for (int n = 0; n < 8; ++n) b[n] = (float)((const elem_t<CACHE>*)tv)[value_at(r, d + n)];
       }
+      const int64_t out = ((int64_t)(seq.first + t) * pools.heads + h) * pools.dim + d;
+      put8<OUT>(k, out, a);
+      put8<OUT>(v, out, b);
     }
-    const int64_t out = ((int64_t)(seq.first + t) * pools.heads + h) * pools.dim + d;
-    put8<OUT>(k, out, a);
-    put8<OUT>(v, out, b);
   }
 }
 
@@ -297,14 +368,16 @@ void launch_out(const Pools& p, const Batch& b, int type, void* k, void* v, dim3
 
 hipError_t launch_rope(RopeArgs r, const Pools& p, const Batch& b, int64_t max_new, hipStream_t s) {
   const int64_t blocks = std::min<int64_t>((std::max<int64_t>(max_new, 1) + 2 * kSlots - 2) / kSlots, 1 << 16);
-  // Turns cost about as much as four heads' rotation, so a work-group takes as many
-  // heads as leave some work-groups for every compute unit.
+  // Sine and cosine cost a work-group as much as some heads' rotation, so it takes as many
+  // heads as leave some work-groups for every compute unit.  A head of q8 blocks goes through
+  // LDS in three steps, which other work-groups' have to hide: few heads each.
   const int heads = r.q_heads + (r.k.p != nullptr ? p.heads : 0) + (r.v.p != nullptr ? p.heads : 0);
-  r.heads_per_job = (int)std::clamp<int64_t>(blocks * b.n_seq * heads / 1024, 2, 32);
-  const auto jobs = [&](const void* x, int n) { return x == nullptr ? 0 : (n + r.heads_per_job - 1) / r.heads_per_job; };
-  r.q_jobs = jobs(r.q.p, r.q_heads);
-  r.k_jobs = jobs(r.k.p, p.heads);
-  const dim3 grid((unsigned)blocks, (unsigned)(r.q_jobs + r.k_jobs + jobs(r.v.p, p.heads)), (unsigned)b.n_seq);
+  r.q_heads_per_job = (int)std::clamp<int64_t>(blocks * b.n_seq * heads / 2048, 2, 32);
+  r.heads_per_job = p.type == QMM_Q8 ? std::min(r.q_heads_per_job, 2) : r.q_heads_per_job;
+  const auto jobs = [](const void* x, int n, int per) { return x == nullptr ? 0 : (n + per - 1) / per; };
+  r.q_jobs = jobs(r.q.p, r.q_heads, r.q_heads_per_job);
+  r.k_jobs = jobs(r.k.p, p.heads, r.heads_per_job);
+  const dim3 grid((unsigned)blocks, (unsigned)(r.q_jobs + r.k_jobs + jobs(r.v.p, p.heads, r.heads_per_job)), (unsigned)b.n_seq);
   const size_t lds = kSlots * ((size_t)r.n_rot * 4 + (p.type == QMM_Q8 ? (size_t)(p.dim + 4) * 5 : 0));
   (r.type == QMM_F32 ? launch_in<QMM_F32> : r.type == QMM_F16 ? launch_in<QMM_F16> : launch_in<QMM_BF16>)(r, p, b, grid,
                                                                                                          lds, s);
@@ -312,8 +385,9 @@ hipError_t launch_rope(RopeArgs r, const Pools& p, const Batch& b, int64_t max_n
 }
 
 hipError_t launch_cache_read(const Pools& p, const Batch& b, int64_t max_new, int type, void* k, void* v, hipStream_t s) {
-  const int64_t work = std::max<int64_t>(max_new, 1) * p.heads * (p.dim / 8);
-  const dim3 grid((unsigned)std::min<int64_t>((work + kThreads - 1) / kThreads, 1 << 16), 1, (unsigned)b.n_seq);
+  const int64_t blocks = (std::max<int64_t>(max_new, 1) + kReadTokens - 1) / kReadTokens;
+  const int sides = (p.heads * (p.dim / 8) * kReadTokens + kThreads - 1) / kThreads;
+  const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 16), (unsigned)std::min(sides, 64), (unsigned)b.n_seq);
   (p.type == QMM_Q8 ? launch_out<QMM_Q8> : p.type == QMM_F16 ? launch_out<QMM_F16> : launch_out<QMM_BF16>)(p, b, type, k,
                                                                                                          v, grid, s);
   return hipGetLastError();

@@ -89,10 +89,10 @@ def test_null_structs_and_empty_batch():
     assert L.qmm_attention(attn_struct(q=None, out=None), cache_struct(), batch_struct(), 0, None, 0, None) == qmm.OK
 
 
-def _plan(heads, kv_heads, dim, n_seq, n_tok, max_new, max_length, cus=256, type_=1):
+def _plan(heads, kv_heads, dim, n_seq, n_tok, max_new, max_length, cus=256, type_=1, window=0):
     plan = qmm.AttnPlan()
     rc = qmm._lib.qmm_attention_plan(cache_struct(type=type_, heads=kv_heads, head_dim=dim), batch_struct(n_seq=n_seq, max_new=max_new,
-                                     max_length=max_length), heads, n_tok, cus, plan)
+                                     max_length=max_length), heads, window, n_tok, cus, plan)
     return rc, plan
 
 
