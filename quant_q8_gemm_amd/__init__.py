@@ -601,19 +601,20 @@ class Cache:
                 raise QmmError(EINVAL, f"k and v must be contiguous uint8 tensors of {nbytes} bytes on one device")
         self.k, self.v, self.dtype = k, v, dtype
         self.n_pages, self.heads, self.head_dim, self.page = n_pages, heads, head_dim, page
-        self.device = k.get_device()
+        self.device, self._views = k.get_device(), None
         self.struct = CacheStruct(type_, heads, head_dim, page, n_pages, k.data_ptr(), v.data_ptr())
 
     def views(self):
         """What a float16 or bfloat16 cache holds, as strided views of its pools with the slots' and channels' indexes
         split: k [n_pages][heads][page/32][2][2][2][4][head_dim/16][2][8], v [n_pages][heads][page/32][2][2][8]
         [head_dim/32][32]; reshape(n_pages, heads, page, head_dim) of either is a copy in plain order."""
-        if self.dtype == "q8":
-            raise QmmError(EINVAL, "a q8 cache holds codes and scales: cache_read gives their numbers")
-        tiles, d = (self.n_pages, self.heads, self.page // 32), self.head_dim
-        k = self.k.view(self.dtype).view(*tiles, d // 16, 2, 2, 2, 2, 4, 8).permute(0, 1, 2, 5, 7, 6, 8, 3, 4, 9)
-        v = self.v.view(self.dtype).view(*tiles, d // 32, 2, 2, 32, 8).permute(0, 1, 2, 4, 5, 7, 3, 6)
-        return k, v
+        if self._views is None:
+            if self.dtype == "q8":
+                raise QmmError(EINVAL, "a q8 cache holds codes and scales: cache_read gives their numbers")
+            tiles, d = (self.n_pages, self.heads, self.page // 32), self.head_dim
+            self._views = (self.k.view(self.dtype).view(*tiles, d // 16, 2, 2, 2, 2, 4, 8).permute(0, 1, 2, 5, 7, 6, 8, 3, 4, 9),
+                           self.v.view(self.dtype).view(*tiles, d // 32, 2, 2, 32, 8).permute(0, 1, 2, 4, 5, 7, 3, 6))
+        return self._views
 
 
 class Batch:

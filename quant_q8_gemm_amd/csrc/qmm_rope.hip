@@ -3,10 +3,9 @@
 //
 //   (a, b) at position p -> m*(a cos t - b sin t, a sin t + b cos t),  t = p*f
 //
-// t in turns is formed and reduced to half a turn in 64 bits: at position 10^6 the
-// product in 32 bits would be off by up to 0.03 radians.  Sine and cosine of what is left
-// (f32, within an ulp or two) are formed once for a work-group's tokens and used
-// for all of its heads.
+// t in turns is formed in 64 bits and modulo one: at position 10^6 the product in 32
+// bits would be off by up to 0.03 radians.  Sine and cosine of what is left (f32) are
+// formed once for a work-group's tokens and used for all of its heads.
 //
 // Memory bounds it: q, k and v are read once, q and the cache written once.  A
 // work-group takes 16 slots that lie in one tile of the cache, so that keys leave as runs of
@@ -53,15 +52,25 @@ __device__ __forceinline__ void store8_any(int type, void* p, int64_t i, const f
   else store8<QMM_BF16>(p, i, x);
 }
 
-// (cos, sin) of `turn` turns.  The nearest quarter turn is taken off in 64 bits; of the rest,
-// |x| <= pi/4 once in f32, the Taylor polynomials to x^9 and x^10 (their remainders are
-// below 3e-9 and 2e-10).  The sum of the roundings is below 4 * 2^-24.  A third of the
-// instructions of the library's sincospi, which with 256 rotated channels took most of
-// the time of a work-group with few heads (7 x 129 tokens, 16+4 heads of 256: 12.3 us).
-__device__ __forceinline__ float2 turned(double turn) {
-  const double y = 4.0 * (turn - __builtin_rint(turn)), n = __builtin_rint(y);
-  const float x = (float)(y - n) * 1.57079632679f, x2 = x * x;
-  const int quarter = (int)n;
+// A frequency as turns per position, whole ones left out (a position has whole numbers of
+// them), in units of 2^-64: a position times it, modulo 2^64, is the angle's place in its
+// turn, with nothing lost at any position but the rounding of the frequency itself.
+__device__ __forceinline__ uint64_t turns_of(double radians) {
+  const double t = fabs(radians) * 0.15915494309189533577;  // 1/(2 pi)
+  const double high = (t - floor(t)) * 4294967296.0, whole = floor(high);
+  const uint64_t step = ((uint64_t)(uint32_t)whole << 32) + (uint64_t)((high - whole) * 4294967296.0);
+  return radians < 0.0 ? 0 - step : step;
+}
+
+// (cos, sin) at a position.  The nearest quarter turn is taken off as an integer; of the
+// rest, |x| <= pi/4 once in f32, the Taylor polynomials to x^9 and x^10 (their remainders
+// are below 3e-9 and 2e-10).  The sum of the roundings is below 4 * 2^-24.  With the
+// angle in 64-bit floating point and the library's sincospi, sine and cosine took more of a
+// work-group's time than four heads' rotation.
+__device__ __forceinline__ float2 turned(int position, uint64_t step) {
+  const uint32_t at = (uint32_t)(((uint64_t)(int64_t)position * step) >> 32);
+  const uint32_t quarter = (at + (1u << 29)) >> 30;
+  const float x = (float)(int32_t)(at - (quarter << 30)) * 1.4629180792671596e-9f, x2 = x * x;  // 2 pi / 2^32
   float s = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);
   s = fmaf(x2, s, 8.33333333e-3f);
   s = fmaf(x2, s, -1.66666667e-1f);
@@ -128,12 +137,25 @@ struct Loaded16 {
   }
 };
 
+// Eight channels' codes of a q8 key, and the block's scale from the lane that has its first.
+__device__ __forceinline__ void store_codes(uint8_t* tile, int dim, int r, int d, bool first, const Q8Part<8>& q) {
+  *(uint2*)(tile + key_code_at(r, d)) = make_uint2(q.codes[0] ^ 0x80808080u, q.codes[1] ^ 0x80808080u);
+  if (first) *(uint16_t*)(tile + scale_at(dim, r, d >> 5)) = (uint16_t)q.pair;
+}
+
+__device__ __forceinline__ Q8Part<16> quant_sixteen(const float (&a)[8], const float (&b)[8]) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = a[i], v[8 + i] = b[i];
+  return quant_part<16>(v);
+}
+
 // IN: type of q, k and v; CACHE: of the cache.  blockIdx: x the 16 slots (in steps of
 // the grid, where the sequence has more), y the job (some heads of q, k or v), z the
 // sequence.  A thread keeps its token and channels and goes from head to head, the
 // next head's values on their way while it works on one.
 template <int IN, int CACHE>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools, Batch batch) {
+__global__ __launch_bounds__(kThreads, CACHE == QMM_Q8 ? 3 : 4) void rope_kernel(RopeArgs r, Pools pools, Batch batch) {
   extern __shared__ float lds[];
   const int s = blockIdx.z, job = blockIdx.y;
   const Sequence seq = sequence(batch, pools.page_shift, s);
@@ -146,8 +168,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools,
   const int dim = pools.dim, units = dim >> 4, half = r.n_rot >> 1;
   const int slot0 = seq.length - seq.count;  // of the first new token; below 0: tokens without a slot
   float2* const turns = (float2*)lds;                               // [16][half]
-  float* const stage = lds + (kind == 2 ? 0 : 2 * kSlots * half);   // q8: [16][dim + 4] values of a head
-  uint8_t* const codes = (uint8_t*)(stage + kSlots * (dim + 4));    // q8: [16][dim + 4] codes
+  float* const stage = lds + 2 * kSlots * half;                     // q8 keys: [16][dim + 4] values of a head
+  uint8_t* const codes = (uint8_t*)lds;                             // q8 values: [heads][16][dim + 4] codes
 
   for (int block = blockIdx.x;; block += gridDim.x) {
     const int base = ((slot0 >> 4) + block) * kSlots;
@@ -167,11 +189,15 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools,
     const int places = count * units, side = kThreads / places;
     int h = head0 + (int)threadIdx.x / places;
     const bool turning = kind == 0 || (kind == 1 && CACHE != QMM_Q8), mine = (int)threadIdx.x < side * places;
+    // q8 keys: whether the lanes of a token's units hold whole blocks of 32 channels
+    const bool whole_blocks =
+        r.n_rot == 0 || r.layout == QMM_ROPE_INTERLEAVED || (r.n_rot % 64 == 0 && units % 4 == 0);
     const int t = from + (int)threadIdx.x % places / units;
-    const Unit at = unit(r, (int)threadIdx.x % places % units);
+    const Unit at = kind == 2 ? Unit{16 * ((int)threadIdx.x % units), 16 * ((int)threadIdx.x % units) + 8, -1}
+                              : unit(r, (int)threadIdx.x % units);
     const int64_t in = (row0 + t) * x.stride;
     Loaded16<IN> now;
-    if (turning && mine && h < head_end) now.load(x.p, in + h * x.head_stride, at);
+    if ((turning || CACHE == QMM_Q8) && mine && h < head_end) now.load(x.p, in + h * x.head_stride, at);
     if (kind < 2) {
       if (half > 0) {  // a thread keeps its pair and goes from token to token
         const int abreast = kThreads / half, pair = (int)threadIdx.x % half;
@@ -180,11 +206,11 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools,
           return i >= count ? 0 : r.positions != nullptr ? r.positions[row0 + from + i] : base + from + i;
         };
         if (token < abreast) {
-          const double f = r.frequencies[pair] * 0.15915494309189533577;  // 1/(2 pi)
+          const uint64_t step = turns_of(r.frequencies[pair]);
           int p = position(token);
           for (; token < count; token += abreast) {
             const int next = position(token + abreast);
-            const float2 turn = turned((double)p * f);
+            const float2 turn = turned(p, step);
             turns[(from + token) * half + pair] = make_float2(turn.x * r.magnitude, turn.y * r.magnitude);
             p = next;
           }
@@ -251,52 +277,78 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools,
           }
         }
       }
-    } else {
-      for (int h = head0; h < head_end; ++h) {
+    } else if (kind == 1 && !whole_blocks) {
+      for (int head = head0; head < head_end; ++head) {
         __syncthreads();  // the head before is out of the stage
-        for (int i = threadIdx.x; i < count * units; i += kThreads) {
-          const int u = i % units, t = from + i / units;
-          const Unit at = kind == 1 ? unit(r, u) : Unit{16 * u, 16 * u + 8, -1};
+        if (threadIdx.x < places) {
           float a[8], b[8];
-          Loaded16<IN> now;
-          now.load(x.p, (row0 + t) * x.stride + h * x.head_stride, at);
+          now.load(x.p, in + head * x.head_stride, at);
           now.get(a, b);
           if (at.pair >= 0) rotate(r, turns + t * half + at.pair, a, b);
           store8<QMM_F32>(stage, t * (dim + 4) + at.a, a);
           store8<QMM_F32>(stage, t * (dim + 4) + at.b, b);
         }
         __syncthreads();
-        uint8_t* const out = (kind == 1 ? pools.k : pools.v) + tile0 + h * tile_step;
+        uint8_t* const out = pools.k + tile0 + head * tile_step;
         // four lanes quantize a block of 32 channels, eight each
         for (int i = threadIdx.x; i < count * (dim >> 3); i += kThreads) {
-          const int d = 8 * (i % (dim >> 3)), t = from + i / (dim >> 3);
+          const int d = 8 * (i % (dim >> 3)), token = from + i / (dim >> 3);
           float x8[8];
-          load8<QMM_F32>(stage, t * (dim + 4) + d, x8);
-          const Q8Part<8> q = quant_part<8>(x8);
-          const uint2 c = make_uint2(q.codes[0] ^ 0x80808080u, q.codes[1] ^ 0x80808080u);
-          if (kind == 1) {
-            *(uint2*)(out + key_code_at(in_tile + t, d)) = c;
-          } else {
-            *(uint32_t*)(codes + t * (dim + 4) + d) = c.x;
-            *(uint32_t*)(codes + t * (dim + 4) + d + 4) = c.y;
-          }
-          if ((i & 3) == 0) *(uint16_t*)(out + scale_at(dim, in_tile + t, d >> 5)) = (uint16_t)q.pair;
+          load8<QMM_F32>(stage, token * (dim + 4) + d, x8);
+          store_codes(out, dim, in_tile + token, d, (i & 3) == 0, quant_part<8>(x8));
         }
-        if (kind == 2) {
-          __syncthreads();
-          for (int i = threadIdx.x; i < 2 * dim; i += kThreads) {
-            const int d = i % dim, g = 8 * (i / dim);
-            if (g + 8 <= from || g >= to) continue;
-            uint8_t* const p = out + value_code_at(in_tile + g, d);
-            if (g >= from && g + 8 <= to) {
-              uint32_t w[2] = {0, 0};
+      }
+    } else if (kind == 1) {
+      // a block's values are in four lanes (the halves' runs) or two (16 in a row): nothing
+      // passes through LDS
+      if (mine) {
+        const bool in_halves = at.b != at.a + 8;
+        for (; h < head_end; h += side) {
+          float a[8], b[8];
+          now.get(a, b);
+          if (h + side < head_end) now.load(x.p, in + (h + side) * x.head_stride, at);
+          if (at.pair >= 0) rotate(r, turns + t * half + at.pair, a, b);
+          uint8_t* const out = pools.k + tile0 + h * tile_step;
+          if (in_halves) {
+            store_codes(out, dim, in_tile + t, at.a, (at.a & 31) == 0, quant_part<8>(a));
+            store_codes(out, dim, in_tile + t, at.b, (at.b & 31) == 0, quant_part<8>(b));
+          } else {
+            const Q8Part<16> q = quant_sixteen(a, b);
+            store_codes(out, dim, in_tile + t, at.a, (at.a & 31) == 0, Q8Part<8>{{q.codes[0], q.codes[1]}, q.pair});
+            store_codes(out, dim, in_tile + t, at.b, false, Q8Part<8>{{q.codes[2], q.codes[3]}, q.pair});
+          }
+        }
+      }
+    } else {
+      // values: blocks quantized where they are loaded, their codes turned in LDS, `side` heads at a time
+      for (int head = head0; head < head_end; head += side, h += side) {
+        const int heads = min(side, head_end - head), pitch = kSlots * (dim + 4);
+        __syncthreads();  // the heads before are out of LDS
+        if (mine && h < head_end) {
+          float a[8], b[8];
+          now.get(a, b);
+          if (h + side < head_end) now.load(x.p, in + (h + side) * x.head_stride, at);
+          const Q8Part<16> q = quant_sixteen(a, b);
+          uint32_t* const to_lds = (uint32_t*)(codes + (h - head) * pitch + t * (dim + 4) + at.a);
 #pragma unroll
-              for (int n = 0; n < 8; ++n) w[n >> 2] |= (uint32_t)codes[(g + n) * (dim + 4) + d] << (8 * (n & 3));
-              *(uint2*)p = make_uint2(w[0], w[1]);
-            } else {
-              for (int n = 0; n < 8; ++n)
-                if (g + n >= from && g + n < to) p[n] = codes[(g + n) * (dim + 4) + d];
-            }
+          for (int i = 0; i < 4; ++i) to_lds[i] = q.codes[i] ^ 0x80808080u;
+          if ((at.a & 31) == 0)
+            *(uint16_t*)(pools.v + tile0 + h * tile_step + scale_at(dim, in_tile + t, at.a >> 5)) = (uint16_t)q.pair;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < heads * 2 * dim; i += kThreads) {
+          const int d = i % dim, j = i / dim, g = 8 * (j & 1);
+          if (g + 8 <= from || g >= to) continue;
+          const uint8_t* const c = codes + (j >> 1) * pitch + g * (dim + 4) + d;
+          uint8_t* const p = pools.v + tile0 + (head + (j >> 1)) * tile_step + value_code_at(in_tile + g, d);
+          if (g >= from && g + 8 <= to) {
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int n = 0; n < 8; ++n) w[n >> 2] |= (uint32_t)c[n * (dim + 4)] << (8 * (n & 3));
+            *(uint2*)p = make_uint2(w[0], w[1]);
+          } else {
+            for (int n = 0; n < 8; ++n)
+              if (g + n >= from && g + n < to) p[n] = c[n * (dim + 4)];
           }
         }
       }
@@ -305,47 +357,59 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs r, Pools pools,
   }
 }
 
-template <int TYPE>
-__device__ __forceinline__ void put8(void* p, int64_t i, const float (&x)[8]) {
-  if (p != nullptr) store8<TYPE>(p, i, x);
-}
-
-constexpr int kReadTokens = 4;  // of a work-group at a time
-
-// A thread reads eight channels of a token's head from both pools.
+// The cache read back, 16 slots of some heads at a time: of keys a thread takes eight
+// channels of a slot, of values eight slots of a channel, as they lie in the tiles.
 template <int CACHE, int OUT>
-__global__ __launch_bounds__(kThreads) void read_kernel(Pools pools, Batch batch, void* k, void* v) {
-  const int s = blockIdx.z, runs = pools.dim >> 3, per_token = pools.heads * runs;
+__global__ __launch_bounds__(kThreads) void read_kernel(Pools pools, Batch batch, int heads_per_job, void* k, void* v) {
+  typedef elem_t<OUT> T;
+  const int s = blockIdx.z, dim = pools.dim, runs = dim >> 3;
   const Sequence seq = sequence(batch, pools.page_shift, s);
-  const int slot0 = seq.length - seq.count;
-  for (int t0 = blockIdx.x * kReadTokens; t0 < seq.count; t0 += gridDim.x * kReadTokens) {
-    const int tokens = min(kReadTokens, seq.count - t0);
-    for (int i = blockIdx.y * kThreads + threadIdx.x; i < per_token * tokens; i += gridDim.y * kThreads) {
-      // tokens side by side in a wave: eight of them share the pieces of a value tile
-      const int t = t0 + i % tokens, j = i / tokens, d = 8 * (j % runs), h = j / runs;
-      const int slot = slot0 + t, r = slot & 31;
-      const int64_t tile = slot < 0 ? -1 : tile_offset(batch, pools, s, h, slot >> 5);
-      float a[8] = {}, b[8] = {};
-      if (tile >= 0) {
-        const uint8_t *tk = pools.k + tile, *tv = pools.v + tile;
+  if (seq.count == 0) return;
+  const int slot0 = seq.length - seq.count, head0 = blockIdx.y * heads_per_job;
+  const int heads = min(heads_per_job, pools.heads - head0);
+  const int64_t tile_step = (int64_t)tile_bytes(CACHE, dim) << (pools.page_shift - 5);
+  for (int block = blockIdx.x;; block += gridDim.x) {
+    const int base = ((slot0 >> 4) + block) * kSlots;
+    if (base >= seq.length) break;
+    const int from = max(0, slot0 - base), to = min(kSlots, seq.length - base), count = to - from;
+    const int row0 = seq.first + base - slot0, in_tile = base & 31;
+    const int64_t tile0 = base < 0 ? -1 : tile_offset<true>(batch, pools, s, 0, base >> 5);
+    for (int i = threadIdx.x; k != nullptr && i < count * heads * runs; i += kThreads) {
+      const int d = 8 * (i % runs), j = i / runs, t = from + j % count, h = head0 + j / count, r = in_tile + t;
+      float x[8] = {};
+      if (tile0 >= 0) {
+        const uint8_t* const tile = pools.k + tile0 + h * tile_step;
         if constexpr (CACHE == QMM_Q8) {
-          const float sk = (float)*(const _Float16*)(tk + scale_at(pools.dim, r, d >> 5));
-          const float sv = (float)*(const _Float16*)(tv + scale_at(pools.dim, r, d >> 5));
-          const uint2 c = *(const uint2*)(tk + key_code_at(r, d));
+          const float scale = (float)*(const _Float16*)(tile + scale_at(dim, r, d >> 5));
+          const uint2 c = *(const uint2*)(tile + key_code_at(r, d));
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            a[n] = (float)((int)(((n < 4 ? c.x : c.y) >> (8 * (n & 3))) & 255) - 128) * sk;
-            b[n] = (float)((int)tv[value_code_at(r, d + n)] - 128) * sv;
-          }
+          for (int n = 0; n < 8; ++n) x[n] = (float)((int)(((n < 4 ? c.x : c.y) >> (8 * (n & 3))) & 255) - 128) * scale;
         } else {
-          load8<CACHE>(tk, key_at(r, d), a);
-#pragma unroll
-          for (int n = 0; n < 8; ++n) b[n] = (float)((const elem_t<CACHE>*)tv)[value_at(r, d + n)];
+          load8<CACHE>(tile, key_at(r, d), x);
         }
       }
-      const int64_t out = ((int64_t)(seq.first + t) * pools.heads + h) * pools.dim + d;
-      put8<OUT>(k, out, a);
-      put8<OUT>(v, out, b);
+      store8<OUT>(k, ((int64_t)(row0 + t) * pools.heads + h) * dim + d, x);
+    }
+    for (int i = threadIdx.x; v != nullptr && i < 2 * heads * dim; i += kThreads) {
+      const int d = i % dim, j = i / dim, g = 8 * (j & 1), h = head0 + (j >> 1), r = in_tile + g;
+      if (g + 8 <= from || g >= to) continue;
+      float x[8] = {};
+      if (tile0 >= 0) {
+        const uint8_t* const tile = pools.v + tile0 + h * tile_step;
+        if constexpr (CACHE == QMM_Q8) {
+          typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+          const v8 scale = *(const v8*)(tile + scale_at(dim, r, d >> 5));
+          const uint2 c = *(const uint2*)(tile + value_code_at(r, d));
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            x[n] = (float)((int)(((n < 4 ? c.x : c.y) >> (8 * (n & 3))) & 255) - 128) * (float)scale[n];
+        } else {
+          load8<CACHE>(tile, value_at(r, d), x);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        if (g + n >= from && g + n < to) ((T*)v)[((int64_t)(row0 + g + n) * pools.heads + h) * dim + d] = (T)x[n];
     }
   }
 }
@@ -358,38 +422,42 @@ void launch_in(const RopeArgs& r, const Pools& p, const Batch& b, dim3 grid, siz
 }
 
 template <int CACHE>
-void launch_out(const Pools& p, const Batch& b, int type, void* k, void* v, dim3 grid, hipStream_t s) {
-  if (type == QMM_F32) read_kernel<CACHE, QMM_F32><<<grid, kThreads, 0, s>>>(p, b, k, v);
-  else if (type == QMM_F16) read_kernel<CACHE, QMM_F16><<<grid, kThreads, 0, s>>>(p, b, k, v);
-  else read_kernel<CACHE, QMM_BF16><<<grid, kThreads, 0, s>>>(p, b, k, v);
+void launch_out(const Pools& p, const Batch& b, int type, int heads, void* k, void* v, dim3 grid, hipStream_t s) {
+  if (type == QMM_F32) read_kernel<CACHE, QMM_F32><<<grid, kThreads, 0, s>>>(p, b, heads, k, v);
+  else if (type == QMM_F16) read_kernel<CACHE, QMM_F16><<<grid, kThreads, 0, s>>>(p, b, heads, k, v);
+  else read_kernel<CACHE, QMM_BF16><<<grid, kThreads, 0, s>>>(p, b, heads, k, v);
 }
 
 }  // namespace
 
 hipError_t launch_rope(RopeArgs r, const Pools& p, const Batch& b, int64_t max_new, hipStream_t s) {
   const int64_t blocks = std::min<int64_t>((std::max<int64_t>(max_new, 1) + 2 * kSlots - 2) / kSlots, 1 << 16);
-  // Sine and cosine cost a work-group as much as some heads' rotation, so it takes as many
-  // heads as leave some work-groups for every compute unit.  A head of q8 blocks goes through
-  // LDS in three steps, which other work-groups' have to hide: few heads each.
+  // As many heads for a work-group as leave a few work-groups of 16-bit values, or twice that
+  // many of f32 ones, for every compute unit: of fewer, larger ones too few bytes are on
+  // their way, of more the turns and starts cost.  3314 tokens of 32+32 heads of 128: from f32
+  // 51.5 us with 9 heads, 56.7 with 19; q alone from f16 15.0 with 6, 17.3 with 3, 31 with 1.
   const int heads = r.q_heads + (r.k.p != nullptr ? p.heads : 0) + (r.v.p != nullptr ? p.heads : 0);
-  r.q_heads_per_job = (int)std::clamp<int64_t>(blocks * b.n_seq * heads / 2048, 2, 32);
-  r.heads_per_job = p.type == QMM_Q8 ? std::min(r.q_heads_per_job, 2) : r.q_heads_per_job;
+  r.q_heads_per_job = (int)std::clamp<int64_t>(blocks * b.n_seq * heads / (r.type == QMM_F32 ? 2048 : 1024), 2, 32);
+  r.heads_per_job = p.type == QMM_Q8 ? std::min(r.q_heads_per_job, 8) : r.q_heads_per_job;  // codes' LDS
   const auto jobs = [](const void* x, int n, int per) { return x == nullptr ? 0 : (n + per - 1) / per; };
   r.q_jobs = jobs(r.q.p, r.q_heads, r.q_heads_per_job);
   r.k_jobs = jobs(r.k.p, p.heads, r.heads_per_job);
   const dim3 grid((unsigned)blocks, (unsigned)(r.q_jobs + r.k_jobs + jobs(r.v.p, p.heads, r.heads_per_job)), (unsigned)b.n_seq);
-  const size_t lds = kSlots * ((size_t)r.n_rot * 4 + (p.type == QMM_Q8 ? (size_t)(p.dim + 4) * 5 : 0));
+  size_t lds = kSlots * (size_t)r.n_rot * 4;
+  if (p.type == QMM_Q8) {  // a key's values beside the turns, or the codes of a job's values
+    lds = std::max(lds + kSlots * (size_t)(p.dim + 4) * 4, (size_t)r.heads_per_job * kSlots * (p.dim + 4));
+  }
   (r.type == QMM_F32 ? launch_in<QMM_F32> : r.type == QMM_F16 ? launch_in<QMM_F16> : launch_in<QMM_BF16>)(r, p, b, grid,
                                                                                                          lds, s);
   return hipGetLastError();
 }
 
 hipError_t launch_cache_read(const Pools& p, const Batch& b, int64_t max_new, int type, void* k, void* v, hipStream_t s) {
-  const int64_t blocks = (std::max<int64_t>(max_new, 1) + kReadTokens - 1) / kReadTokens;
-  const int sides = (p.heads * (p.dim / 8) * kReadTokens + kThreads - 1) / kThreads;
-  const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 16), (unsigned)std::min(sides, 64), (unsigned)b.n_seq);
-  (p.type == QMM_Q8 ? launch_out<QMM_Q8> : p.type == QMM_F16 ? launch_out<QMM_F16> : launch_out<QMM_BF16>)(p, b, type, k,
-                                                                                                         v, grid, s);
+  const int64_t blocks = std::min<int64_t>((std::max<int64_t>(max_new, 1) + 2 * kSlots - 2) / kSlots, 1 << 16);
+  const int heads = (int)std::clamp<int64_t>(blocks * b.n_seq * p.heads / 1024, 1, 8);
+  const dim3 grid((unsigned)blocks, (unsigned)((p.heads + heads - 1) / heads), (unsigned)b.n_seq);
+  (p.type == QMM_Q8 ? launch_out<QMM_Q8> : p.type == QMM_F16 ? launch_out<QMM_F16> : launch_out<QMM_BF16>)(
+      p, b, type, heads, k, v, grid, s);
   return hipGetLastError();
 }
 
