@@ -1230,6 +1230,7 @@ int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch*
   r.window = a.window;
   r.heads = a.heads;
   r.group = a.heads / cache->heads;
+  r.by_group = qmm::Divisor(r.group);
   r.causal = a.causal;
   r.q8_out = a.out_type == QMM_Q8;
   r.splits = plan.splits;

@@ -6,6 +6,14 @@
 
 namespace qmm {
 
+// Division of numbers below 2^30 by a divisor of up to 2^12: with m = ceil(2^42 / d), n m 2^-42
+// is past n/d by less than n 2^-42 <= 2^-12, which does not reach the next whole number.
+struct Divisor {
+  uint64_t m;
+  Divisor(int d = 1) : m(((1ull << 42) + d - 1) / d) {}
+  __host__ __device__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> 42); }
+};
+
 struct AttnArgs {
   const void* q;
   int64_t q_stride, q_head_stride;  // elements
@@ -15,6 +23,7 @@ struct AttnArgs {
   float2* sums;                     // their (maximum, sum), [split][row * heads + head]
   int64_t window;                   // 0: none
   int32_t heads, group;             // heads per head of the cache
+  Divisor by_group;
   int32_t causal, q8_out, splits, columns, tiles;
   int32_t share;                    // tiles of a split at least; splits * share cover max_length
   int64_t t_pad;                    // rows of the qact buffer

@@ -8,6 +8,7 @@
 #include "qmm_internal.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace qmm {
 
@@ -110,6 +111,8 @@ AttnPlan plan_attention(int heads, int kv_heads, int dim, int64_t n_seq, int64_t
   const int64_t least = plan.few ? 8 : 32, unit = plan.few ? 4 : 2;
   int64_t share = std::max(least, (base * tiles + slots - 1) / slots);
   share = (share + unit - 1) / unit * unit;
+  if (!plan.few && base >= num_cus) share = tiles;
+  if (const char* e = getenv("XSHARE")) share = atoi(e);
   share = std::max(share, (tiles + 255) / 256);
   plan.splits = (int)((tiles + share - 1) / share);
   plan.share = (int)share;

@@ -69,10 +69,27 @@ struct Loaded<QMM_Q8, DB> {
   __device__ __forceinline__ f16x8 value(int i) const { return codes(i, v[i]); }
 };
 
-// Tile t's place in both pools, or -1; t is the same in every lane.
-__device__ __forceinline__ int64_t place(const Batch& b, const Pools& p, int s, int h, int t, int end) {
-  return t < end ? tile_offset<true>(b, p, s, h, t) : -1;
-}
+// A sequence's page numbers, 64 columns of its table at a time in a register of the wave: a
+// lookup is then a v_readlane, where a load would be waited for with every tile.
+struct Pages {
+  const int32_t* row;
+  int columns, base, held;
+  // (before anything else of a kernel, so that it is there when the lengths are)
+  __device__ __forceinline__ Pages(const Batch& b, int s) : row(b.table + s * b.table_stride), columns(b.columns), base(0) {
+    held = row[min((int)(threadIdx.x & 63), columns - 1)];
+  }
+  // Tile t's place in both pools, or -1; t is the same in every lane.
+  __device__ __forceinline__ int64_t place(const Pools& p, int h, int t, int end) {
+    if (t >= end) return -1;
+    const int i = t >> (p.page_shift - 5);
+    if ((unsigned)(i - base) >= 64u) {
+      base = i;
+      held = row[min(i + (int)(threadIdx.x & 63), columns - 1)];
+      pin(held);  // waited for here, and not where lookups without a load come by
+    }
+    return offset_on_page(p, __builtin_amdgcn_readlane(held, i - base), h, t);
+  }
+};
 
 template <int TYPE, int DB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2 : 1, DB <= 4 ? 2 : 1))) void few_kernel(
@@ -85,6 +102,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
   if (a.q8_out && a.splits == 1)
     zero_padding(a, kDim, batch.n_tok, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
                  (int64_t)gridDim.x * gridDim.y * blockDim.x);
+  Pages pages(batch, s);
   const Sequence seq = sequence(batch, pools.page_shift, s);
   const int flats = seq.count * a.group;
   float* const tops = lds;                    // [WAVES][32]
@@ -95,9 +113,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
     const int first = tile * a.columns, last = min(first + a.columns, flats) - 1;
     const Column c = column(a, seq, h, first + min(lane & 31, a.columns - 1));
     int low, high, all_low, all_high, unused;
-    seen(a, seq, first / a.group, last / a.group, low, high);
-    seen(a, seq, first / a.group, first / a.group, unused, all_high);
-    seen(a, seq, last / a.group, last / a.group, all_low, unused);
+    seen(a, seq, a.by_group.of(first), a.by_group.of(last), low, high);
+    seen(a, seq, a.by_group.of(first), a.by_group.of(first), unused, all_high);
+    seen(a, seq, a.by_group.of(last), a.by_group.of(last), all_low, unused);
     const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin), share = max(a.share, (tiles + a.splits - 1) / a.splits);
     const int from = begin + split * share, end = min(begin + tiles, from + share);
     if (split > 0 && from >= end) {  // nothing left for this split
@@ -111,7 +129,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
       // the next as well.
       Loaded<TYPE, DB> keys, values;
       int t = from + wave;
-      int64_t at = place(batch, pools, s, h, t, end), next = place(batch, pools, s, h, t + WAVES, end);
+      int64_t at = pages.place(pools, h, t, end), next = pages.place(pools, h, t + WAVES, end);
       keys.load_keys(pools.k + max(at, (int64_t)0), lane);
       values.load_values(pools.v + max(at, (int64_t)0), lane);
       v8 q[2 * DB];
@@ -125,7 +143,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
       for (; t < end; t += WAVES) {
         const bool here = at >= 0;
         at = next;
-        next = place(batch, pools, s, h, t + 2 * WAVES, end);
+        next = pages.place(pools, h, t + 2 * WAVES, end);
         v16f score[1] = {v16f{}};
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) score[0] = Math<TYPE>::mma(keys.key(i), q[i], score[0]);
@@ -248,20 +266,36 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Where the tiles of a stage are, by the waves' own table lookups.
+// Where the tiles of a stage are.
 template <int KB>
 struct Places {
   int64_t at[KB];
-  __device__ __forceinline__ void find(const Batch& b, const Pools& p, int s, int h, int t, int end) {
+  __device__ __forceinline__ void find(Pages& pages, const Pools& p, int h, int t, int end) {
 #pragma unroll
-    for (int k = 0; k < KB; ++k) at[k] = place(b, p, s, h, t + k, end);
+    for (int k = 0; k < KB; ++k) at[k] = pages.place(p, h, t + k, end);
+  }
+  // a bit for each tile that is somewhere
+  __device__ __forceinline__ uint32_t here() const {
+    uint32_t r = 0;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) r |= (uint32_t)(at[k] >= 0) << k;
+    return r;
   }
 };
+
+// Waits until at most N of the wave's loads are on their way: the copies to LDS, which the
+// compiler does not count.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "a 6-bit count");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 // A wave's part of staging: waves 0 and 1 the keys, 2 and 3 the values; of two tiles one
 // each, of one tile half each.
 template <int TYPE, int DB, int KB>
 struct Stager {
+  static constexpr int kLoads = KB * DB;  // of a stage, for each wave
   static __device__ __forceinline__ int64_t from(const Places<KB>& at, int wave) {
     const int64_t first = at.at[0], second = at.at[KB - 1];
     return KB == 2 && (wave & 1) ? second : first;
@@ -280,6 +314,7 @@ struct Stager {
 };
 template <int DB, int KB>
 struct Stager<QMM_Q8, DB, KB> {
+  static constexpr int kLoads = 0;
   static constexpr int kBlocks = KB == 2 ? DB : DB / 2;  // blocks of 32 channels of a tile
   v4i w[kBlocks];
   f16x8 s[2 * kBlocks];
@@ -310,17 +345,73 @@ struct Stager<QMM_Q8, DB, KB> {
   }
 };
 
-template <int TYPE, int DB, int KB>
+// A column's result from the lane's accumulators: 16 of each 32 channels, four in a row,
+// the others in the lane of the other half.
+template <int TYPE, int DB>
+__device__ __forceinline__ void store_column(const AttnArgs& a, const Column& c, int split, int n_tok, int half, float top,
+                                             float total, const v16f (&o)[DB]) {
+  constexpr int kDim = 32 * DB, T = TYPE == QMM_BF16 ? QMM_BF16 : QMM_F16;
+  if (!a.q8_out || a.splits > 1) {
+    if (!c.real) return;
+    if (a.splits > 1) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          store_part<TYPE>(a, kDim, n_tok, split, c, 32 * d + 8 * i + 4 * half,
+                           make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]), top, total);
+      return;
+    }
+    const float by = total == 0.0f ? 0.0f : 1.0f / total;
+    const int64_t to = c.row * a.out_stride + (int64_t)c.head * kDim + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        store4<T>(a.out, to + 32 * d + 8 * i, make_float4(o[d][4 * i] * by, o[d][4 * i + 1] * by, o[d][4 * i + 2] * by,
+                                                         o[d][4 * i + 3] * by));
+    return;
+  }
+  const float by = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t id = (int64_t)a.heads * kDim;
+#pragma unroll
+  for (int d = 0; d < DB; ++d) {
+    float largest = 0.0f;
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = make_float4(o[d][4 * i] * by, o[d][4 * i + 1] * by, o[d][4 * i + 2] * by, o[d][4 * i + 3] * by);
+      largest = larger(larger(largest, larger(x[i].x, x[i].y)), larger(x[i].z, x[i].w));
+    }
+    const Halves both = halves(largest);
+    const Q8Scale sc(larger(both.a, both.b));
+    const int64_t block = (int64_t)(c.row >> 5) * (id >> 5) + c.head * DB + d;
+    uint8_t* const to = (uint8_t*)a.out + block * 1024 + (c.row & 31) * 16 + 4 * half;
+    int S = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int q[4];
+      quant4(x[i], sc.dhf, sc.inv, q);
+      S += q[0] + q[1] + q[2] + q[3];
+      if (c.real) *(uint32_t*)(to + (i >> 1) * 512 + (i & 1) * 8) = pack4(q);
+    }
+    S += __shfl_xor(S, 32);
+    if (c.real && half == 0) *(uint32_t*)((uint8_t*)a.out + a.t_pad * id + block * 128 + (c.row & 31) * 4) = sc.pair(S);
+  }
+}
+
+template <int TYPE, int DB, int KB, int STAGES>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2 : 1, DB <= 4 ? 2 : 1))) void many_kernel(
     AttnArgs a, Pools pools, Batch batch) {
   constexpr int kDim = 32 * DB, kStage = 4 * KB * DB * 1024, kColumns = 128;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * kStage];
   typedef typename Math<TYPE>::v8 v8;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
   const int h = blockIdx.x % pools.heads, rest = blockIdx.x / pools.heads, split = rest % a.splits, s = blockIdx.y;
   if (a.q8_out && a.splits == 1)
     zero_padding(a, kDim, batch.n_tok, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
                  (int64_t)gridDim.x * gridDim.y * blockDim.x);
+  Pages pages(batch, s);
   const Sequence seq = sequence(batch, pools.page_shift, s);
   const int flats = seq.count * a.group;
 
@@ -329,10 +420,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
     const int first = tile * kColumns, last = min(first + kColumns, flats) - 1;
     // what any and what all of the columns see, and the same of this wave's own
     int low, high, all_low, all_high, my_low, my_high, my_all_low, my_all_high, unused;
-    const int mine = min(first + 32 * wave, last) / a.group, mine_end = min(first + 32 * wave + 31, last) / a.group;
-    seen(a, seq, first / a.group, last / a.group, low, high);
-    seen(a, seq, first / a.group, first / a.group, unused, all_high);
-    seen(a, seq, last / a.group, last / a.group, all_low, unused);
+    const int mine = a.by_group.of(min(first + 32 * wave, last)), mine_end = a.by_group.of(min(first + 32 * wave + 31, last));
+    seen(a, seq, a.by_group.of(first), a.by_group.of(last), low, high);
+    seen(a, seq, a.by_group.of(first), a.by_group.of(first), unused, all_high);
+    seen(a, seq, a.by_group.of(last), a.by_group.of(last), all_low, unused);
     seen(a, seq, mine, mine_end, my_low, my_high);
     seen(a, seq, mine, mine, unused, my_all_high);
     seen(a, seq, mine_end, mine_end, my_all_low, unused);
@@ -346,37 +437,49 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
       continue;
     }
 
-    v8 q[2 * DB];
-    load_queries<TYPE, DB>(a, c, lane, q);
-#pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) pin(q[i]);  // here, not in the loop, where the wait would be for the loads ahead too
     for (bool safe = false;; safe = true) {
+      v8 q[2 * DB];
+      load_queries<TYPE, DB>(a, c, lane, q);
       v16f o[DB];
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] = v16f{};
       Running run;
-      Places<KB> at, next;
+      // The stages are a ring: while tile t is worked on, the ones up to t + kAhead are on their
+      // way.  `here` of each, oldest first: whether its tiles are somewhere.
+      constexpr int kAhead = STAGES - 1;
+      Places<KB> next;
       Stager<TYPE, DB, KB> stager;
-      at.find(batch, pools, s, h, from, end);
-      next.find(batch, pools, s, h, from + KB, end);
-      if (from < end) {
-        stager.load(pools, at, wave, lane, lds);
-        stager.store(wave, lane, lds);
-      }
-      int stage = 0;
-      for (int t = from; t < end; t += KB, stage ^= 1) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        const Places<KB> now = at;
-        const bool more = t + KB < end;
-        uint8_t* const other = lds + (stage ^ 1) * kStage;
-        at = next;
-        if (more) stager.load(pools, at, wave, lane, other);
-        next.find(batch, pools, s, h, t + 2 * KB, end);
-        const int slot0 = 32 * t;
-        bool here = true;
+      uint32_t here_of[kAhead];
 #pragma unroll
-        for (int k = 0; k < KB; ++k) here &= now.at[k] >= 0;
+      for (int i = 0; i < kAhead; ++i) {
+        next.find(pages, pools, h, from + i * KB, end);
+        here_of[i] = next.here();
+        if (from + i * KB < end) {
+          stager.load(pools, next, wave, lane, lds + i * kStage);
+          stager.store(wave, lane, lds + i * kStage);
+        }
+      }
+      next.find(pages, pools, h, from + kAhead * KB, end);
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) pin(q[i]);  // here, not in the loop, where the wait would be for the loads ahead too
+      int stage = 0, free_stage = kAhead;
+      for (int t = from; t < end; t += KB) {
+        // this wave's loads of tile t, which are older than those of the tiles ahead
+        if (kAhead > 1 && t + (kAhead - 1) * KB < end)
+          wait_loads<(kAhead - 1) * Stager<TYPE, DB, KB>::kLoads>();
+        else
+          wait_loads<0>();
+        __syncthreads();
+        const uint32_t here_bits = here_of[0];
+        const bool more = t + kAhead * KB < end;
+        uint8_t* const other = lds + free_stage * kStage;
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) here_of[i] = here_of[i + 1];
+        here_of[kAhead - 1] = next.here();
+        if (more) stager.load(pools, next, wave, lane, other);
+        next.find(pages, pools, h, t + (kAhead + 1) * KB, end);
+        const int slot0 = 32 * t;
+        const bool here = here_bits == (1u << KB) - 1;
         if (safe && (!here || slot0 < all_low || slot0 + 32 * KB > all_high)) {
           v8* const values = (v8*)(lds + stage * kStage + kStage / 2);
           for (int i = threadIdx.x; i < kStage / 32; i += 256) values[i] = finite<TYPE>(values[i]);
@@ -394,7 +497,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
           if (!here || slot0 < my_all_low || slot0 + 32 * KB > my_all_high) {
 #pragma unroll
             for (int k = 0; k < KB; ++k)  // a tile that is nowhere is seen by nobody
-              hide(score[k], slot0 + 32 * k, half, c.low, now.at[k] >= 0 ? c.high : 0);
+              hide(score[k], slot0 + 32 * k, half, c.low, (here_bits >> k & 1) != 0 ? c.high : 0);
           }
           v8 p[2 * KB];
           soften<TYPE, DB, KB>(score, a.scale2, run, o, p);
@@ -403,6 +506,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
               [&](int i, const v8& v) { o[i % DB] = Math<TYPE>::mma(v, p[i / DB], o[i % DB]); });
         }
         if (more) stager.store(wave, lane, other);
+        free_stage = stage;
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
       }
       bool odd = false;
 #pragma unroll
@@ -412,12 +517,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
       // again, safely, where a result is no finite number; the stages are read
       if (__syncthreads_or(odd) && !safe) continue;
 
-      // The columns' results pass through the wave's quarter of the stages, kBlocks blocks of
-      // 32 channels at a time, so that they leave as runs of a row; 16-byte pieces are
-      // exchanged by column, or all columns' would be in the same banks.
+      const float total = both_sum(run.sum);
+      if (!safe) {
+        if (!idle) store_column<TYPE, DB>(a, c, split, batch.n_tok, half, run.top, total, o);
+        __syncthreads();  // the stages are free again
+        break;
+      }
+      // Where values are added that the product left out, the columns' results pass through
+      // the wave's quarter of the stages, kBlocks blocks of 32 channels at a time, so that this
+      // is one loop; 16-byte pieces are exchanged by column, or all columns' would be in the
+      // same banks.
       constexpr int kBlocks = KB * DB / 2, kSwap = kBlocks % 2 == 0 ? 15 : 7;
       float* const out = (float*)(lds + wave * (kStage / 2));
-      const float total = both_sum(run.sum);
 #pragma unroll
       for (int pass = 0; pass < DB; pass += kBlocks) {
         if (idle) break;
@@ -436,7 +547,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
           float4 x = *(const float4*)(out + n * (32 * kBlocks) + 4 * (piece ^ (n & kSwap)));
           if (!to.real) continue;
           const int d = 32 * pass + 4 * piece;
-          if (safe) add_edges<TYPE>(pools, batch, s, h, {from, end, KB, all_low, all_high}, to, d, x);
+          add_edges<TYPE>(pools, batch, s, h, {from, end, KB, all_low, all_high}, to, d, x);
           store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, all);
         }
         wave_sync();
@@ -449,6 +560,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
 
 constexpr int few_waves(int db) { return db <= 4 ? 4 : 2; }
 
+// Stages of many_kernel: as many as leave two work-groups on a CU (160 KiB of LDS) up to
+// heads of 128, and one beyond; q8 tiles pass through registers, one ahead.
+constexpr int stages(int type, int db) { return type == QMM_Q8 ? 2 : db == 2 ? 4 : db == 3 ? 3 : db == 4 ? 2 : 4; }
+
 template <int TYPE, int DB>
 hipError_t launch_dim(const AttnArgs& a, const Pools& p, const Batch& b, const AttnPlan& plan, hipStream_t s) {
   const dim3 grid((unsigned)(plan.work_groups / b.n_seq), (unsigned)b.n_seq);
@@ -457,7 +572,7 @@ hipError_t launch_dim(const AttnArgs& a, const Pools& p, const Batch& b, const A
     const size_t lds = sizeof(float) * W * (64 + (size_t)plan.columns * (32 * DB + 4));
     few_kernel<TYPE, DB, W><<<grid, 64 * W, lds, s>>>(a, p, b);
   } else {
-    many_kernel<TYPE, DB, (DB <= 4 ? 2 : 1)><<<grid, 256, 0, s>>>(a, p, b);
+    many_kernel<TYPE, DB, (DB <= 4 ? 2 : 1), stages(TYPE, DB)><<<grid, 256, 0, s>>>(a, p, b);
   }
   return hipGetLastError();
 }

@@ -78,7 +78,7 @@ __device__ __forceinline__ Column column(const AttnArgs& a, const Sequence& seq,
   const int last = seq.count * a.group - 1;
   const bool real = flat <= last;
   flat = min(flat, last);
-  const int token = flat / a.group;
+  const int token = a.by_group.of(flat);
   Column c = {real, seq.first + token, kv_head * a.group + flat - token * a.group, 0, seq.length};
   if (a.causal) {
     const int end = seq.length - seq.count + token + 1;

@@ -80,17 +80,21 @@ __host__ __device__ inline Sequence sequence(const Batch& b, int page_shift, int
   return {first, end - first, clamped(uniform_load(b.lengths, s), 0, b.columns << page_shift)};
 }
 
-// Byte offset in a pool of the tile of head h that holds slots 32*tile .. of sequence
-// s; -1 where the page is none of the pool's.  0 <= 32*tile < columns * page.  UNIFORM: s
-// and tile are the same in every lane.
-template <bool UNIFORM = false>
-__host__ __device__ inline int64_t tile_offset(const Batch& b, const Pools& p, int s, int h, int tile) {
+// Byte offset in a pool of the tile of head h that holds slots 32*tile .. on `page`; -1 where
+// the page is none of the pool's.
+__host__ __device__ inline int64_t offset_on_page(const Pools& p, int page, int h, int tile) {
   const int tiles_shift = p.page_shift - 5;
-  const int64_t i = s * b.table_stride + (tile >> tiles_shift);
-  const int page = UNIFORM ? uniform_load(b.table, i) : b.table[i];
   if (page < 0 || page >= p.n_pages) return -1;
   const int64_t at = (((int64_t)page * p.heads + h) << tiles_shift) + (tile & ((1 << tiles_shift) - 1));
   return at * tile_bytes(p.type, p.dim);
+}
+
+// The same by the table, of sequence s; 0 <= 32*tile < columns * page.  UNIFORM: s and tile
+// are the same in every lane.
+template <bool UNIFORM = false>
+__host__ __device__ inline int64_t tile_offset(const Batch& b, const Pools& p, int s, int h, int tile) {
+  const int64_t i = s * b.table_stride + (tile >> (p.page_shift - 5));
+  return offset_on_page(p, UNIFORM ? uniform_load(b.table, i) : b.table[i], h, tile);
 }
 
 }  // namespace qmm
