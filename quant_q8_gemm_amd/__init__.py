@@ -391,7 +391,7 @@ def _bytes(t, what: str, device: int):
 
 def _empty(like, shape, dtype, stream):
     """A new contiguous tensor on like's device that belongs to the stream it is written on."""
-    strides = (shape[1], 1) if len(shape) == 2 else (1,)
+    strides = (shape[1], 1) if len(shape) == 2 else (1,) if len(shape) == 1 else (shape[1] * shape[2], shape[2], 1)
     if stream is None:
         return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
     if isinstance(stream, int):  # 0 is the null stream, which ExternalStream does not know
@@ -637,13 +637,19 @@ class Batch:
         self.max_new = -1 if max_new is None else max_new
         columns = table.shape[1]
         self.max_length = -1 if max_length is None else max_length
+        self.work = {}  # bytes of work memory by a call's sizes
         self.struct = BatchStruct(n, columns, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
-                                  table.stride(0) if n > 1 else columns, 0, 0)
+                                  table.stride(0) if n > 1 else columns, max(self.max_new, 0), max(self.max_length, 0))
 
     def _for(self, cache: Cache, n_tok: int) -> BatchStruct:
-        b = self.struct
-        b.max_new = min(n_tok, MAX_TOKENS) if self.max_new < 0 else self.max_new
-        b.max_length = min(b.columns * cache.page, 2 ** 31 - 1) if self.max_length < 0 else self.max_length
+        if self.max_new >= 0 and self.max_length >= 0:
+            return self.struct
+        b = BatchStruct()  # of this call alone: other threads' may have other sizes
+        ctypes.pointer(b)[0] = self.struct
+        if self.max_new < 0:
+            b.max_new = min(n_tok, MAX_TOKENS)
+        if self.max_length < 0:
+            b.max_length = min(b.columns * cache.page, 2 ** 31 - 1)
         return b
 
 
@@ -659,7 +665,7 @@ def _heads(t, what: str, n_tok: int, heads: int, dim: int, device: int, dtype=No
 
 
 def _same_device(cache: Cache, batch: Batch, device: int) -> None:
-    if cache.device != device or batch.device != device:
+    if cache.device != device or batch.device != device:  # the tensors that they hold
         raise QmmError(EINVAL, f"the tensors are on device {device}, the cache on {cache.device} and the batch on {batch.device}")
 
 
@@ -693,17 +699,17 @@ def rope_cache(cache: Cache, batch: Batch, *, q=None, k=None, v=None, frequencie
             raise QmmError(EINVAL, f"positions must be a contiguous int32 [{n_tok}] tensor on device {device}")
         a.positions = positions.data_ptr()
     if q is not None:
-        a.q_heads = q.shape[1]
-        a.q, a.q_stride, a.q_head_stride = _heads(q, "q", n_tok, q.shape[1], dim, device)
+        a.q_heads = x.shape[1]
+        a.q, a.q_stride, a.q_head_stride = _heads(q, "q", n_tok, a.q_heads, dim, device)
         if out is None:
             if dtype is None:
                 dtype = kind if kind != torch.float32 else torch.float16 if cache.dtype == "q8" else cache.dtype
             a.out_type = _elem(dtype)
-            out = _empty(q, (n_tok * q.shape[1] * dim,), dtype, stream).view(n_tok, q.shape[1], dim)
-            a.q_out, a.q_out_stride, a.q_out_head_stride = out.data_ptr(), q.shape[1] * dim, dim
+            out = _empty(q, (n_tok, a.q_heads, dim), dtype, stream)
+            a.q_out, a.q_out_stride, a.q_out_head_stride = out.data_ptr(), a.q_heads * dim, dim
         else:
             a.out_type = _elem(out.dtype, "out")
-            a.q_out, a.q_out_stride, a.q_out_head_stride = _heads(out, "out", n_tok, q.shape[1], dim, device)
+            a.q_out, a.q_out_stride, a.q_out_head_stride = _heads(out, "out", n_tok, a.q_heads, dim, device)
     elif out is not None:
         raise QmmError(EINVAL, "out is where the queries go: it needs q")
     if k is not None:
@@ -720,11 +726,11 @@ def cache_read(cache: Cache, batch: Batch, n_tok: int, *, dtype=torch.float32, s
     device = _current(cache.k, "the cache")
     _same_device(cache, batch, device)
     elem = _elem(dtype)
-    shape, n = (n_tok, cache.heads, cache.head_dim), n_tok * cache.heads * cache.head_dim
-    k, v = (_empty(cache.k, (n,), dtype, stream) for _ in range(2))
+    shape = (n_tok, cache.heads, cache.head_dim)
+    k, v = (_empty(cache.k, shape, dtype, stream) for _ in range(2))
     _check(_lib.qmm_cache_read(cache.struct, batch._for(cache, n_tok), n_tok, elem, k.data_ptr(), v.data_ptr(),
                                _raw_stream(stream, device)))
-    return k.view(shape), v.view(shape)
+    return k, v
 
 
 def attention_plan(cache: Cache, batch: Batch, heads: int, n_tok: int, num_cus: int, window: int = 0) -> AttnPlan:
@@ -764,15 +770,18 @@ def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: boo
             result = out = _empty(q, (qact_bytes(n_tok, heads * dim),), torch.uint8, stream)
         a.out, a.out_stride = _bytes(out, "out", device)
     elif out is None:
-        out = _empty(q, (n_tok * heads * dim,), kind, stream)
-        a.out, a.out_stride, result = out.data_ptr(), heads * dim, out.view(n_tok, heads, dim)
+        result = out = _empty(q, (n_tok, heads, dim), kind, stream)
+        a.out, a.out_stride = out.data_ptr(), heads * dim
     else:
         a.out, a.out_stride = _rows(out, "out", (n_tok, heads * dim), device, kind)
     b = batch._for(cache, n_tok)
     if work is None:
-        if device not in _cus:
-            _cus[device] = torch.cuda.get_device_properties(device).multi_processor_count
-        need = attention_plan(cache, batch, heads, n_tok, _cus[device], window).work_bytes
+        sizes = (n_tok, heads, cache.heads, dim, cache.dtype, b.max_new, b.max_length, window)  # what the plan goes by
+        need = batch.work.get(sizes)
+        if need is None:
+            if device not in _cus:
+                _cus[device] = torch.cuda.get_device_properties(device).multi_processor_count
+            need = batch.work[sizes] = attention_plan(cache, batch, heads, n_tok, _cus[device], window).work_bytes
         work = _empty(q, (need,), torch.uint8, stream) if need else None
     work_ptr, work_bytes = _bytes(work, "work", device) if work is not None and work.numel() else (None, 0)
     _check(_lib.qmm_attention(a, cache.struct, b, n_tok, work_ptr, work_bytes, _raw_stream(stream, device)))

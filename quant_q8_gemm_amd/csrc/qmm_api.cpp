@@ -1150,8 +1150,8 @@ int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads
   if (num_cus < 1 || num_cus > QMM_MAX_CUS)
     return fail(QMM_EINVAL, "num_cus must be in [1, %d], got %d", QMM_MAX_CUS, num_cus);
   if (n_tok > 0) {
-    const qmm::AttnPlan plan = qmm::plan_attention(heads, cache->heads, cache->head_dim, b.n_seq, n_tok, b.max_new, b.max_length,
-                                                   window, num_cus);
+    const qmm::AttnPlan plan = qmm::plan_attention(cache->type, heads, cache->heads, cache->head_dim, b.n_seq, n_tok,
+                                                   b.max_new, b.max_length, window, num_cus);
     if (int rc = check_attention_launch(plan)) return rc;
     *out = {plan.work_bytes, plan.work_groups, plan.few ? 1 : 0, plan.columns, plan.tiles, plan.splits};
   }
@@ -1213,8 +1213,8 @@ int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch*
   if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
   e = hipDeviceGetAttribute(&num_cus, hipDeviceAttributeMultiprocessorCount, device);
   if (e != hipSuccess) return fail_hip(e, "hipDeviceGetAttribute(multiprocessor count)");
-  const qmm::AttnPlan plan = qmm::plan_attention(a.heads, cache->heads, cache->head_dim, batch->n_seq, n_tok, batch->max_new,
-                                                 batch->max_length, a.window, num_cus);
+  const qmm::AttnPlan plan = qmm::plan_attention(cache->type, a.heads, cache->heads, cache->head_dim, batch->n_seq, n_tok,
+                                                 batch->max_new, batch->max_length, a.window, num_cus);
   if (int rc = check_attention_launch(plan)) return rc;
   if (work_bytes < plan.work_bytes)
     return fail(QMM_EINVAL, "work_bytes %zu, but this launch needs %zu bytes of work memory (qmm_attention_plan)", work_bytes,

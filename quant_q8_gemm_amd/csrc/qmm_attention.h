@@ -37,8 +37,8 @@ struct AttnPlan {
   int64_t work_groups;
   size_t work_bytes;
 };
-AttnPlan plan_attention(int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new, int64_t max_length,
-                        int64_t window, int num_cus);
+AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new,
+                        int64_t max_length, int64_t window, int num_cus);
 
 // The product kernels of one cache type (a source file each), on a checked plan;
 // and the kernel that joins the splits.

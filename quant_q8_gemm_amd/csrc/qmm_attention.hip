@@ -8,7 +8,6 @@
 #include "qmm_internal.h"
 
 #include <algorithm>
-#include <cstdlib>
 
 namespace qmm {
 
@@ -96,8 +95,8 @@ hipError_t launch_join(const AttnArgs& a, const Pools& p, const Batch& b, hipStr
 
 }  // namespace
 
-AttnPlan plan_attention(int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new, int64_t max_length,
-                        int64_t window, int num_cus) {
+AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_seq, int64_t n_tok, int64_t max_new,
+                        int64_t max_length, int64_t window, int num_cus) {
   AttnPlan plan{};
   const int64_t group = heads / kv_heads, flats = std::clamp<int64_t>(max_new, 1, n_tok) * group;
   plan.few = flats <= 64;
@@ -108,11 +107,24 @@ AttnPlan plan_attention(int heads, int kv_heads, int dim, int64_t n_seq, int64_t
   if (window > 0) keys = std::min(keys, window + plan.columns / group + kTileSlots);
   const int64_t tiles = std::max<int64_t>((keys + kTileSlots - 1) / kTileSlots, 1);
   const int64_t base = n_seq * kv_heads * plan.tiles, slots = 2 * (int64_t)num_cus;
-  const int64_t least = plan.few ? 8 : 32, unit = plan.few ? 4 : 2;
-  int64_t share = std::max(least, (base * tiles + slots - 1) / slots);
-  share = (share + unit - 1) / unit * unit;
-  if (!plan.few && base >= num_cus) share = tiles;
-  if (const char* e = getenv("XSHARE")) share = atoi(e);
+  // The number of splits that needs the least time, in microseconds: rounds of work-groups over
+  // the GPU, each with a start and its share's tiles, and for more than one split the join
+  // and the partial results' way through memory.  A tile takes a work-group of many columns
+  // about 1 us; one of few what the active ones' tiles take from memory, 0.3 at least.  Measured:
+  // one token of 32 heads over 3314 slots with 1, 4, 16 splits 22.9, 15.8, 16.2 us; 16 sequences of
+  // 20 heads of 64 over up to 1500 with 1, 2, 4: 15.7, 18.3, 20.3; one token of 64/8 heads over 131072
+  // with 8, 16, 32: 167, 109, 105; 2048 tokens of 40/8 heads over 32768 with 1, 2, 4: 1524, 1347, 1353.
+  const double start = plan.few ? 3.0 : 8.0, join = plan.few ? 4.5 : 10.0, partial_mb = (double)n_tok * heads * dim * 8e-6;
+  const int64_t least = plan.few ? 4 : 32, unit = plan.few ? 4 : 2;
+  int64_t share = tiles;
+  double best = 0.0;
+  for (int64_t n = 1; n <= 256 && (n == 1 || tiles / n >= least); n += n < 16 ? 1 : n / 8) {
+    const int64_t each = ((tiles + n - 1) / n + unit - 1) / unit * unit, rounds = (base * n + slots - 1) / slots;
+    const double active = (double)std::clamp<int64_t>(base * n, 192, slots);  // fewer do not take all of the bandwidth
+    const double tile = plan.few ? std::max(0.3, active * 2.0 * tile_bytes(type, dim) / 5e6) : 1.0;
+    const double cost = (double)rounds * ((double)each * tile + start) + (n > 1 ? join + partial_mb * (double)n / 4.0 : 0.0);
+    if (n == 1 || cost < 0.97 * best) best = cost, share = each;
+  }
   share = std::max(share, (tiles + 255) / 256);
   plan.splits = (int)((tiles + share - 1) / share);
   plan.share = (int)share;

@@ -73,21 +73,28 @@ struct Loaded<QMM_Q8, DB> {
 // lookup is then a v_readlane, where a load would be waited for with every tile.
 struct Pages {
   const int32_t* row;
-  int columns, base, held;
+  int columns, base, held, shift, n_pages, tile;
+  int64_t page, head;  // bytes of a page, and to the head in it
   // (before anything else of a kernel, so that it is there when the lengths are)
-  __device__ __forceinline__ Pages(const Batch& b, int s) : row(b.table + s * b.table_stride), columns(b.columns), base(0) {
+  __device__ __forceinline__ Pages(const Batch& b, const Pools& p, int s, int h)
+      : row(b.table + s * b.table_stride), columns(b.columns), base(0), shift(p.page_shift - 5), n_pages(p.n_pages) {
     held = row[min((int)(threadIdx.x & 63), columns - 1)];
+    tile = tile_bytes(p.type, p.dim);
+    head = (int64_t)tile * (h << shift);
+    page = (int64_t)tile * (p.heads << shift);
   }
   // Tile t's place in both pools, or -1; t is the same in every lane.
-  __device__ __forceinline__ int64_t place(const Pools& p, int h, int t, int end) {
+  __device__ __forceinline__ int64_t place(int t, int end) {
     if (t >= end) return -1;
-    const int i = t >> (p.page_shift - 5);
+    const int i = t >> shift;
     if ((unsigned)(i - base) >= 64u) {
       base = i;
       held = row[min(i + (int)(threadIdx.x & 63), columns - 1)];
       pin(held);  // waited for here, and not where lookups without a load come by
     }
-    return offset_on_page(p, __builtin_amdgcn_readlane(held, i - base), h, t);
+    const uint32_t at = (uint32_t)__builtin_amdgcn_readlane(held, i - base);
+    if (at >= (uint32_t)n_pages) return -1;
+    return head + (int64_t)((uint64_t)at * (uint64_t)page) + (uint32_t)((t & ((1 << shift) - 1)) * tile);
   }
 };
 
@@ -102,7 +109,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
   if (a.q8_out && a.splits == 1)
     zero_padding(a, kDim, batch.n_tok, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
                  (int64_t)gridDim.x * gridDim.y * blockDim.x);
-  Pages pages(batch, s);
+  Pages pages(batch, pools, s, h);
   const Sequence seq = sequence(batch, pools.page_shift, s);
   const int flats = seq.count * a.group;
   float* const tops = lds;                    // [WAVES][32]
@@ -129,7 +136,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
       // the next as well.
       Loaded<TYPE, DB> keys, values;
       int t = from + wave;
-      int64_t at = pages.place(pools, h, t, end), next = pages.place(pools, h, t + WAVES, end);
+      int64_t at = pages.place(t, end), next = pages.place(t + WAVES, end);
       keys.load_keys(pools.k + max(at, (int64_t)0), lane);
       values.load_values(pools.v + max(at, (int64_t)0), lane);
       v8 q[2 * DB];
@@ -143,7 +150,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
       for (; t < end; t += WAVES) {
         const bool here = at >= 0;
         at = next;
-        next = pages.place(pools, h, t + 2 * WAVES, end);
+        next = pages.place(t + 2 * WAVES, end);
         v16f score[1] = {v16f{}};
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) score[0] = Math<TYPE>::mma(keys.key(i), q[i], score[0]);
@@ -270,9 +277,10 @@ __device__ __forceinline__ void wave_sync() {
 template <int KB>
 struct Places {
   int64_t at[KB];
-  __device__ __forceinline__ void find(Pages& pages, const Pools& p, int h, int t, int end) {
-#pragma unroll
-    for (int k = 0; k < KB; ++k) at[k] = pages.place(p, h, t + k, end);
+  // t is a multiple of KB: two tiles are on one page but for pages of 32 slots
+  __device__ __forceinline__ void find(Pages& pages, int t, int end) {
+    at[0] = pages.place(t, end);
+    if (KB > 1) at[KB - 1] = pages.shift == 0 ? pages.place(t + 1, end) : t + 1 < end && at[0] >= 0 ? at[0] + pages.tile : -1;
   }
   // a bit for each tile that is somewhere
   __device__ __forceinline__ uint32_t here() const {
@@ -411,7 +419,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
   if (a.q8_out && a.splits == 1)
     zero_padding(a, kDim, batch.n_tok, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
                  (int64_t)gridDim.x * gridDim.y * blockDim.x);
-  Pages pages(batch, s);
+  Pages pages(batch, pools, s, h);
   const Sequence seq = sequence(batch, pools.page_shift, s);
   const int flats = seq.count * a.group;
 
@@ -429,7 +437,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
     seen(a, seq, mine_end, mine_end, my_all_low, unused);
     const bool idle = first + 32 * wave > last;
     const Column c = column(a, seq, h, first + 32 * wave + (lane & 31));
-    const int begin = low >> 5, tiles = max(0, ((high + 31) >> 5) - begin);
+    const int begin = low >> 5 & -KB, tiles = max(0, ((high + 31) >> 5) - begin);
     const int share = max(a.share, (tiles + a.splits * KB - 1) / (a.splits * KB) * KB);
     const int from = begin + split * share, end = min(begin + tiles, from + share);
     if (split > 0 && from >= end) {  // nothing left for this split
@@ -452,14 +460,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
       uint32_t here_of[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        next.find(pages, pools, h, from + i * KB, end);
+        next.find(pages, from + i * KB, end);
         here_of[i] = next.here();
         if (from + i * KB < end) {
           stager.load(pools, next, wave, lane, lds + i * kStage);
           stager.store(wave, lane, lds + i * kStage);
         }
       }
-      next.find(pages, pools, h, from + kAhead * KB, end);
+      next.find(pages, from + kAhead * KB, end);
 #pragma unroll
       for (int i = 0; i < 2 * DB; ++i) pin(q[i]);  // here, not in the loop, where the wait would be for the loads ahead too
       int stage = 0, free_stage = kAhead;
@@ -477,7 +485,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
         for (int i = 0; i + 1 < kAhead; ++i) here_of[i] = here_of[i + 1];
         here_of[kAhead - 1] = next.here();
         if (more) stager.load(pools, next, wave, lane, other);
-        next.find(pages, pools, h, t + (kAhead + 1) * KB, end);
+        next.find(pages, t + (kAhead + 1) * KB, end);
         const int slot0 = 32 * t;
         const bool here = here_bits == (1u << KB) - 1;
         if (safe && (!here || slot0 < all_low || slot0 + 32 * KB > all_high)) {
