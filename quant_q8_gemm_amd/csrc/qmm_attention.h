@@ -33,7 +33,7 @@ struct AttnArgs {
 // Plan of a launch (qmm_attention_plan).
 struct AttnPlan {
   bool few;
-  int columns, tiles, splits, share;
+  int columns, tiles, splits, share, groups;
   int64_t work_groups;
   size_t work_bytes;
 };

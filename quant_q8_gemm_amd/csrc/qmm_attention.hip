@@ -121,7 +121,9 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   for (int64_t n = 1; n <= 256 && (n == 1 || tiles / n >= least); n += n < 16 ? 1 : n / 8) {
     const int64_t each = ((tiles + n - 1) / n + unit - 1) / unit * unit, rounds = (base * n + slots - 1) / slots;
     const double active = (double)std::clamp<int64_t>(base * n, 192, slots);  // fewer do not take all of the bandwidth
-    const double tile = plan.few ? std::max(0.3, active * 2.0 * tile_bytes(type, dim) / 5e6) : 1.0;
+    const double tile = plan.few           ? std::max(0.3, active * 2.0 * tile_bytes(type, dim) / 5e6)
+                        : base * n > num_cus ? 1.0
+                                             : 0.6;
     const double cost = (double)rounds * ((double)each * tile + start) + (n > 1 ? join + partial_mb * (double)n / 4.0 : 0.0);
     if (n == 1 || cost < 0.97 * best) best = cost, share = each;
   }
@@ -129,6 +131,7 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   plan.splits = (int)((tiles + share - 1) / share);
   plan.share = (int)share;
   plan.work_groups = base * plan.splits;
+  plan.groups = !plan.few && dim <= 128 && plan.work_groups <= num_cus ? 2 : 1;
   plan.work_bytes = plan.splits == 1 ? 0 : (size_t)plan.splits * n_tok * heads * ((size_t)dim * 4 + 8);
   return plan;
 }

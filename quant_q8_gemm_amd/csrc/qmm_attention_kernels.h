@@ -207,7 +207,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
 // waves take 32 columns each and share the keys and values, which pass through LDS
 // in two stages of 32*KB slots: while one is worked on the next is copied, 16-bit tiles
 // straight from memory to LDS, q8 tiles through registers, where they become f16 once for
-// all waves.
+// all waves.  Where there is at most one work-group for a compute unit it has two groups of
+// four waves, which take turns over the keys with stages of their own: a wave of a
+// SIMD by itself leaves it idle for half of the time (scores, powers and the second product
+// of a tile wait for each other), and a second one fills that.
 
 // N consecutive 1 KiB copies from base + 16*lane to LDS; M0 is set by each run itself, and
 // nothing else in these kernels reads it.
@@ -408,13 +411,15 @@ __device__ __forceinline__ void store_column(const AttnArgs& a, const Column& c,
   }
 }
 
-template <int TYPE, int DB, int KB, int STAGES>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2 : 1, DB <= 4 ? 2 : 1))) void many_kernel(
+template <int TYPE, int DB, int KB, int STAGES, int GROUPS>
+__global__ __launch_bounds__(256 * GROUPS) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2 : 1, DB <= 4 ? 2 : 1))) void many_kernel(
     AttnArgs a, Pools pools, Batch batch) {
   constexpr int kDim = 32 * DB, kStage = 4 * KB * DB * 1024, kColumns = 128;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t all_lds[GROUPS * STAGES * kStage];
   typedef typename Math<TYPE>::v8 v8;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, half = lane >> 5;
+  const int group = GROUPS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  uint8_t* const lds = all_lds + group * (STAGES * kStage);
   const int h = blockIdx.x % pools.heads, rest = blockIdx.x / pools.heads, split = rest % a.splits, s = blockIdx.y;
   if (a.q8_out && a.splits == 1)
     zero_padding(a, kDim, batch.n_tok, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
@@ -458,42 +463,47 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
       Places<KB> next;
       Stager<TYPE, DB, KB> stager;
       uint32_t here_of[kAhead];
+      constexpr int kStep = KB * GROUPS;  // a group's tiles are KB of every kStep
+      const int mine_from = from + group * KB;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        next.find(pages, from + i * KB, end);
+        next.find(pages, mine_from + i * kStep, end);
         here_of[i] = next.here();
-        if (from + i * KB < end) {
+        if (mine_from + i * kStep < end) {
           stager.load(pools, next, wave, lane, lds + i * kStage);
           stager.store(wave, lane, lds + i * kStage);
         }
       }
-      next.find(pages, from + kAhead * KB, end);
+      next.find(pages, mine_from + kAhead * kStep, end);
 #pragma unroll
       for (int i = 0; i < 2 * DB; ++i) pin(q[i]);  // here, not in the loop, where the wait would be for the loads ahead too
       int stage = 0, free_stage = kAhead;
-      for (int t = from; t < end; t += KB) {
+      for (int round = from; round < end; round += kStep) {
+        const int t = round + group * KB;  // may lie behind the end for the last group
         // this wave's loads of tile t, which are older than those of the tiles ahead
-        if (kAhead > 1 && t + (kAhead - 1) * KB < end)
+        if (kAhead > 1 && t + (kAhead - 1) * kStep < end)
           wait_loads<(kAhead - 1) * Stager<TYPE, DB, KB>::kLoads>();
         else
           wait_loads<0>();
         __syncthreads();
         const uint32_t here_bits = here_of[0];
-        const bool more = t + kAhead * KB < end;
+        const bool more = t + kAhead * kStep < end;
         uint8_t* const other = lds + free_stage * kStage;
 #pragma unroll
         for (int i = 0; i + 1 < kAhead; ++i) here_of[i] = here_of[i + 1];
         here_of[kAhead - 1] = next.here();
         if (more) stager.load(pools, next, wave, lane, other);
-        next.find(pages, t + (kAhead + 1) * KB, end);
+        next.find(pages, t + (kAhead + 1) * kStep, end);
         const int slot0 = 32 * t;
         const bool here = here_bits == (1u << KB) - 1;
-        if (safe && (!here || slot0 < all_low || slot0 + 32 * KB > all_high)) {
-          v8* const values = (v8*)(lds + stage * kStage + kStage / 2);
-          for (int i = threadIdx.x; i < kStage / 32; i += 256) values[i] = finite<TYPE>(values[i]);
+        if (safe) {
+          if (t < end && (!here || slot0 < all_low || slot0 + 32 * KB > all_high)) {
+            v8* const values = (v8*)(lds + stage * kStage + kStage / 2);
+            for (int i = threadIdx.x & 255; i < kStage / 32; i += 256) values[i] = finite<TYPE>(values[i]);
+          }
           __syncthreads();
         }
-        if (!idle && slot0 < my_high && slot0 + 32 * KB > my_low) {
+        if (!idle && t < end && slot0 < my_high && slot0 + 32 * KB > my_low) {
           const uint8_t* const keys = lds + stage * kStage + lane * 16;
           const uint8_t* const values = keys + kStage / 2;
           v16f score[KB];
@@ -517,6 +527,35 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
         free_stage = stage;
         stage = stage + 1 == STAGES ? 0 : stage + 1;
       }
+      if constexpr (GROUPS > 1) {
+        // the second group's sums join the first's, lane by lane through the second's stages
+        __syncthreads();
+        v4f* const moved = (v4f*)(all_lds + STAGES * kStage + wave * (DB * 4096)) + lane;
+        float2* const state = (float2*)(all_lds + wave * 512) + lane;
+        if (group == 1) {
+#pragma unroll
+          for (int i = 0; i < 4 * DB; ++i)
+            moved[64 * i] = v4f{o[i >> 2][4 * (i & 3)], o[i >> 2][4 * (i & 3) + 1], o[i >> 2][4 * (i & 3) + 2],
+                                o[i >> 2][4 * (i & 3) + 3]};
+          *state = make_float2(run.top, run.sum);
+        }
+        __syncthreads();
+        if (group == 0) {
+          const float2 m = *state;
+          const float top = fmaxf(run.top, m.x);
+          const float by = run.top == kNone ? 0.0f : __builtin_amdgcn_exp2f((run.top - top) * a.scale2);
+          const float by2 = m.x == kNone ? 0.0f : __builtin_amdgcn_exp2f((m.x - top) * a.scale2);
+          run.top = top;
+          run.sum = fmaf(m.y, by2, run.sum * by);
+#pragma unroll
+          for (int i = 0; i < 4 * DB; ++i) {
+            const v4f v = moved[64 * i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i >> 2][4 * (i & 3) + j] = fmaf(v[j], by2, o[i >> 2][4 * (i & 3) + j] * by);
+          }
+        }
+      }
+      const bool out_here = !idle && group == 0;
       bool odd = false;
 #pragma unroll
       for (int d = 0; d < DB; ++d)
@@ -527,7 +566,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
 
       const float total = both_sum(run.sum);
       if (!safe) {
-        if (!idle) store_column<TYPE, DB>(a, c, split, batch.n_tok, half, run.top, total, o);
+        if (out_here) store_column<TYPE, DB>(a, c, split, batch.n_tok, half, run.top, total, o);
         __syncthreads();  // the stages are free again
         break;
       }
@@ -539,7 +578,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2
       float* const out = (float*)(lds + wave * (kStage / 2));
 #pragma unroll
       for (int pass = 0; pass < DB; pass += kBlocks) {
-        if (idle) break;
+        if (!out_here) break;
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
@@ -575,13 +614,20 @@ constexpr int stages(int type, int db) { return type == QMM_Q8 ? 2 : db == 2 ? 4
 template <int TYPE, int DB>
 hipError_t launch_dim(const AttnArgs& a, const Pools& p, const Batch& b, const AttnPlan& plan, hipStream_t s) {
   const dim3 grid((unsigned)(plan.work_groups / b.n_seq), (unsigned)b.n_seq);
+  constexpr int KB = DB <= 4 ? 2 : 1;
   if (plan.few) {
     constexpr int W = few_waves(DB);
     const size_t lds = sizeof(float) * W * (64 + (size_t)plan.columns * (32 * DB + 4));
     few_kernel<TYPE, DB, W><<<grid, 64 * W, lds, s>>>(a, p, b);
-  } else {
-    many_kernel<TYPE, DB, (DB <= 4 ? 2 : 1), stages(TYPE, DB)><<<grid, 256, 0, s>>>(a, p, b);
+    return hipGetLastError();
   }
+  if constexpr (DB <= 4) {
+    if (plan.groups == 2) {
+      many_kernel<TYPE, DB, KB, stages(TYPE, DB), 2><<<grid, 512, 0, s>>>(a, p, b);
+      return hipGetLastError();
+    }
+  }
+  many_kernel<TYPE, DB, KB, stages(TYPE, DB), 1><<<grid, 256, 0, s>>>(a, p, b);
   return hipGetLastError();
 }
 
