@@ -508,15 +508,16 @@ size_t qmm_cache_page_bytes(int type, int heads, int head_dim, int page);
  * the launch by; sequences that pass them are worked through all the same, only
  * slower. */
 #define QMM_MAX_SEQS 65535
+#define QMM_MAX_SLOTS (1 << 30) /* of a sequence */
 typedef struct {
     int32_t n_seq;         /* 1 .. QMM_MAX_SEQS */
-    int32_t columns;       /* of the table, >= 1; columns * page < 2^31 */
+    int32_t columns;       /* of the table, >= 1; columns * page <= QMM_MAX_SLOTS */
     const int32_t *starts; /* [n_seq + 1] */
     const int32_t *lengths;/* [n_seq] */
     const int32_t *table;  /* [n_seq] rows of `columns` page numbers */
     int64_t table_stride;  /* elements from row to row, >= columns */
     int64_t max_new;       /* 0 .. QMM_MAX_TOKENS */
-    int64_t max_length;    /* 0 .. 2^31 - 1 */
+    int64_t max_length;    /* 0 .. QMM_MAX_SLOTS */
 } qmm_batch;
 
 /* Rotary scalings for long contexts (qmm_rope_frequencies). */
@@ -626,8 +627,9 @@ typedef struct {
  * head h and the keys j that it sees, of cache head h / (heads / cache heads),
  *   p_j = exp(scale * q.k_j - max_j),   out = sum_j p_j v_j / sum_j p_j
  * Products are of 16-bit values summed in f32; maximum and sum are f32; p_j is
- * rounded to q's type for the second product, q8 keys and values to f16.  A token
- * that sees no key, or none whose score is above -infinity, gets zeros.  What a
+ * rounded to q's type for the second product, q8 keys and values to f16.  Scores
+ * times scale stay below 2^126 in size, or are no numbers in what comes of them.  A
+ * token that sees no key, or none whose score is above -infinity, gets zeros.  What a
  * token does not see is no part of its result, whatever is stored there.  An output
  * in q8 blocks has its padding tokens zero; rows of tokens of no sequence are
  * left as they are.

@@ -67,6 +67,7 @@ ELEM_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 NORM_KINDS = {"rms": 0, "layer": 1}
 Q8 = 3  # as the output of a product: q8 blocks
 MAX_TOKENS = 1 << 20
+MAX_SLOTS = 1 << 30
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "turns": 4}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -188,6 +189,10 @@ _lib.qmm_attention.argtypes = [ctypes.POINTER(Attn), *_CB, _I64, _P, _SZ, _P]
 _lib.qmm_attention.restype = ctypes.c_int
 _lib.qmm_attention_plan.argtypes = [*_CB, ctypes.c_int, _I64, _I64, ctypes.c_int, ctypes.POINTER(AttnPlan)]
 _lib.qmm_attention_plan.restype = ctypes.c_int
+# the same two with their structs as addresses, for the calls below: a decode step makes them for every layer
+_rope_cache, _attention = _lib["qmm_rope_cache"], _lib["qmm_attention"]
+_rope_cache.argtypes, _rope_cache.restype = [_P, _P, _P, _I64, _P], ctypes.c_int
+_attention.argtypes, _attention.restype = [_P, _P, _P, _I64, _P, _SZ, _P], ctypes.c_int
 _lib.qmm_last_error.argtypes = []
 _lib.qmm_last_error.restype = ctypes.c_char_p
 
@@ -600,9 +605,11 @@ class Cache:
             if t.dtype != torch.uint8 or t.shape != (nbytes,) or not t.is_contiguous() or t.get_device() != k.get_device():
                 raise QmmError(EINVAL, f"k and v must be contiguous uint8 tensors of {nbytes} bytes on one device")
         self.k, self.v, self.dtype = k, v, dtype
+        self.kind = torch.float16 if dtype == "q8" else dtype  # of the queries that read it
         self.n_pages, self.heads, self.head_dim, self.page = n_pages, heads, head_dim, page
         self.device, self._views = k.get_device(), None
         self.struct = CacheStruct(type_, heads, head_dim, page, n_pages, k.data_ptr(), v.data_ptr())
+        self.address = ctypes.addressof(self.struct)
 
     def views(self):
         """What a float16 or bfloat16 cache holds, as strided views of its pools with the slots' and channels' indexes
@@ -649,16 +656,16 @@ class Batch:
         if self.max_new < 0:
             b.max_new = min(n_tok, MAX_TOKENS)
         if self.max_length < 0:
-            b.max_length = min(b.columns * cache.page, 2 ** 31 - 1)
+            b.max_length = min(b.columns * cache.page, MAX_SLOTS)
         return b
 
 
 def _heads(t, what: str, n_tok: int, heads: int, dim: int, device: int, dtype=None):
     """(address, token stride, head stride) of a tensor [n_tok][heads][dim]; the library checks the rest."""
     if t.get_device() == device and t.shape == (n_tok, heads, dim) and (dtype is None or t.dtype == dtype):
-        strides = t.stride()
-        if strides[2] == 1:
-            return t.data_ptr(), strides[0], strides[1]
+        row, head, one = t.stride()
+        if one == 1:
+            return t.data_ptr(), row, head
         raise QmmError(EINVAL, f"{what} must have adjacent channels")
     raise QmmError(EINVAL, f"{what} must be {[n_tok, heads, dim]} {dtype or ''} on device {device}, got {list(t.shape)} "
                            f"{t.dtype} on {t.device}")
@@ -703,7 +710,7 @@ def rope_cache(cache: Cache, batch: Batch, *, q=None, k=None, v=None, frequencie
         a.q, a.q_stride, a.q_head_stride = _heads(q, "q", n_tok, a.q_heads, dim, device)
         if out is None:
             if dtype is None:
-                dtype = kind if kind != torch.float32 else torch.float16 if cache.dtype == "q8" else cache.dtype
+                dtype = kind if kind != torch.float32 else cache.kind
             a.out_type = _elem(dtype)
             out = _empty(q, (n_tok, a.q_heads, dim), dtype, stream)
             a.q_out, a.q_out_stride, a.q_out_head_stride = out.data_ptr(), a.q_heads * dim, dim
@@ -716,7 +723,10 @@ def rope_cache(cache: Cache, batch: Batch, *, q=None, k=None, v=None, frequencie
         a.k, a.k_stride, a.k_head_stride = _heads(k, "k", n_tok, cache.heads, dim, device, kind)
     if v is not None:
         a.v, a.v_stride, a.v_head_stride = _heads(v, "v", n_tok, cache.heads, dim, device, kind)
-    _check(_lib.qmm_rope_cache(a, cache.struct, batch._for(cache, n_tok), n_tok, _raw_stream(stream, device)))
+    b = batch._for(cache, n_tok)
+    rc = _rope_cache(ctypes.addressof(a), cache.address, ctypes.addressof(b), n_tok, _raw_stream(stream, device))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -754,12 +764,13 @@ def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: boo
     dtype "q8" the qact buffer of its rows (the output product's input), or `out`: [n_tok][heads * head_dim], rows may be
     strided, or a qact buffer with dtype "q8".  A token that sees nothing gets zeros.  work: a uint8 tensor of
     attention_plan's work_bytes; new memory without it."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise QmmError(EINVAL, "q must be [n_tok][heads][head_dim]")
+    n_tok, heads, dim = shape
     device = _current(q, "q")
     _same_device(cache, batch, device)
-    n_tok, heads, dim = q.shape
-    kind = torch.float16 if cache.dtype == "q8" else cache.dtype
+    kind = cache.kind
     if dtype is not None and dtype != "q8" and dtype != kind:
         raise QmmError(EINVAL, f"dtype must be None, 'q8' or {kind}, got {dtype}")
     a = Attn(heads, 1 if causal else 0, Q8 if dtype == "q8" else ELEM_TYPES[kind], dim ** -0.5 if scale is None else scale,
@@ -770,7 +781,7 @@ def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: boo
             result = out = _empty(q, (qact_bytes(n_tok, heads * dim),), torch.uint8, stream)
         a.out, a.out_stride = _bytes(out, "out", device)
     elif out is None:
-        result = out = _empty(q, (n_tok, heads, dim), kind, stream)
+        result = out = _empty(q, shape, kind, stream)
         a.out, a.out_stride = out.data_ptr(), heads * dim
     else:
         a.out, a.out_stride = _rows(out, "out", (n_tok, heads * dim), device, kind)
@@ -783,6 +794,9 @@ def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: boo
                 _cus[device] = torch.cuda.get_device_properties(device).multi_processor_count
             need = batch.work[sizes] = attention_plan(cache, batch, heads, n_tok, _cus[device], window).work_bytes
         work = _empty(q, (need,), torch.uint8, stream) if need else None
-    work_ptr, work_bytes = _bytes(work, "work", device) if work is not None and work.numel() else (None, 0)
-    _check(_lib.qmm_attention(a, cache.struct, b, n_tok, work_ptr, work_bytes, _raw_stream(stream, device)))
+    work_ptr, work_bytes = (None, 0) if work is None or work.numel() == 0 else _bytes(work, "work", device)
+    rc = _attention(ctypes.addressof(a), cache.address, ctypes.addressof(b), n_tok, work_ptr, work_bytes,
+                    _raw_stream(stream, device))
+    if rc:
+        _check(rc)
     return result

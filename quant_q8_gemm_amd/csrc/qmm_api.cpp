@@ -901,13 +901,13 @@ int check_cache(const qmm_cache* cache, const qmm_batch* batch, int64_t n_tok, i
   const qmm_batch& q = *batch;
   if (q.n_seq < 1 || q.n_seq > QMM_MAX_SEQS)
     return fail(QMM_EINVAL, "n_seq must be in [1, %d], got %d", QMM_MAX_SEQS, q.n_seq);
-  if (q.columns < 1 || (int64_t)q.columns * c.page > INT32_MAX)
-    return fail(QMM_EINVAL, "columns must be at least 1 and columns * page below 2^31, got %d * %d", q.columns, c.page);
+  if (q.columns < 1 || (int64_t)q.columns * c.page > QMM_MAX_SLOTS)
+    return fail(QMM_EINVAL, "columns must be at least 1 and columns * page at most %d, got %d * %d", QMM_MAX_SLOTS, q.columns, c.page);
   if (q.table_stride < q.columns || q.table_stride > INT32_MAX)
     return fail(QMM_EINVAL, "table_stride must be in [%d, 2^31), got %lld", q.columns, (long long)q.table_stride);
-  if (q.max_new < 0 || q.max_new > QMM_MAX_TOKENS || q.max_length < 0 || q.max_length > INT32_MAX)
-    return fail(QMM_EINVAL, "max_new must be in [0, %d] and max_length in [0, 2^31), got %lld and %lld", QMM_MAX_TOKENS,
-                (long long)q.max_new, (long long)q.max_length);
+  if (q.max_new < 0 || q.max_new > QMM_MAX_TOKENS || q.max_length < 0 || q.max_length > QMM_MAX_SLOTS)
+    return fail(QMM_EINVAL, "max_new must be in [0, %d] and max_length in [0, %d], got %lld and %lld", QMM_MAX_TOKENS,
+                QMM_MAX_SLOTS, (long long)q.max_new, (long long)q.max_length);
   if (q.starts == nullptr || q.lengths == nullptr || q.table == nullptr)
     return fail(QMM_EINVAL, "starts, lengths or table is NULL");
   if (!aligned(q.starts, 4) || !aligned(q.lengths, 4) || !aligned(q.table, 4))
@@ -1123,8 +1123,8 @@ int check_attention_sizes(const qmm_cache& c, int heads, int64_t n_tok) {
   return QMM_OK;
 }
 
-int check_attention_launch(const qmm::AttnPlan& plan) {
-  if (plan.work_groups > INT32_MAX) return fail(QMM_EINVAL, "%lld work-groups exceed one launch", (long long)plan.work_groups);
+int check_attention_launch(const qmm::AttnPlan& plan, int64_t n_seq) {
+  if (plan.work_groups / n_seq > (int64_t)UINT32_MAX / 512 || plan.work_groups > INT32_MAX) return fail(QMM_EINVAL, "%lld work-groups exceed one launch", (long long)plan.work_groups);
   return QMM_OK;
 }
 
@@ -1143,16 +1143,16 @@ int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads
   const qmm_batch& b = *batch;
   if (b.n_seq < 1 || b.n_seq > QMM_MAX_SEQS)
     return fail(QMM_EINVAL, "n_seq must be in [1, %d], got %d", QMM_MAX_SEQS, b.n_seq);
-  if (b.max_new < 0 || b.max_new > QMM_MAX_TOKENS || b.max_length < 0 || b.max_length > INT32_MAX)
-    return fail(QMM_EINVAL, "max_new must be in [0, %d] and max_length in [0, 2^31), got %lld and %lld", QMM_MAX_TOKENS,
-                (long long)b.max_new, (long long)b.max_length);
+  if (b.max_new < 0 || b.max_new > QMM_MAX_TOKENS || b.max_length < 0 || b.max_length > QMM_MAX_SLOTS)
+    return fail(QMM_EINVAL, "max_new must be in [0, %d] and max_length in [0, %d], got %lld and %lld", QMM_MAX_TOKENS,
+                QMM_MAX_SLOTS, (long long)b.max_new, (long long)b.max_length);
   if (window < 0) return fail(QMM_EINVAL, "window must not be negative, got %lld", (long long)window);
   if (num_cus < 1 || num_cus > QMM_MAX_CUS)
     return fail(QMM_EINVAL, "num_cus must be in [1, %d], got %d", QMM_MAX_CUS, num_cus);
   if (n_tok > 0) {
     const qmm::AttnPlan plan = qmm::plan_attention(cache->type, heads, cache->heads, cache->head_dim, b.n_seq, n_tok,
                                                    b.max_new, b.max_length, window, num_cus);
-    if (int rc = check_attention_launch(plan)) return rc;
+    if (int rc = check_attention_launch(plan, b.n_seq)) return rc;
     *out = {plan.work_bytes, plan.work_groups, plan.few ? 1 : 0, plan.columns, plan.tiles, plan.splits};
   }
   ok();
@@ -1173,7 +1173,8 @@ int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch*
   if (a.out_type != type && a.out_type != QMM_Q8)
     return fail(QMM_EINVAL, "out_type must be that of q (%d with this cache) or QMM_Q8 (%d), got %d", type, QMM_Q8, a.out_type);
   if (a.causal != 0 && a.causal != 1) return fail(QMM_EINVAL, "causal must be 0 or 1, got %d", a.causal);
-  if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return fail(QMM_EINVAL, "scale must be positive and finite");
+  if (!(a.scale >= 1e-30f) || !(a.scale <= 1e30f))  // its multiples of a few stay normal numbers
+    return fail(QMM_EINVAL, "scale must be in [1e-30, 1e30]");
   if (a.window < 0 || (a.window > 0 && a.causal == 0))
     return fail(QMM_EINVAL, "window must be 0, or positive with causal, got %lld", (long long)a.window);
   if ((work == nullptr) != (work_bytes == 0) || !aligned(work, 16))
@@ -1215,7 +1216,7 @@ int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch*
   if (e != hipSuccess) return fail_hip(e, "hipDeviceGetAttribute(multiprocessor count)");
   const qmm::AttnPlan plan = qmm::plan_attention(cache->type, a.heads, cache->heads, cache->head_dim, batch->n_seq, n_tok,
                                                  batch->max_new, batch->max_length, a.window, num_cus);
-  if (int rc = check_attention_launch(plan)) return rc;
+  if (int rc = check_attention_launch(plan, batch->n_seq)) return rc;
   if (work_bytes < plan.work_bytes)
     return fail(QMM_EINVAL, "work_bytes %zu, but this launch needs %zu bytes of work memory (qmm_attention_plan)", work_bytes,
                 plan.work_bytes);

@@ -118,7 +118,7 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   const int64_t least = plan.few ? 4 : 32, unit = plan.few ? 4 : 2;
   int64_t share = tiles;
   double best = 0.0;
-  for (int64_t n = 1; n <= 256 && (n == 1 || tiles / n >= least); n += n < 16 ? 1 : n / 8) {
+  for (int64_t n = 1; n <= 256 && (n == 1 || (tiles / n >= least && base < 16 * slots)); n += n < 16 ? 1 : n / 8) {
     const int64_t each = ((tiles + n - 1) / n + unit - 1) / unit * unit, rounds = (base * n + slots - 1) / slots;
     const double active = (double)std::clamp<int64_t>(base * n, 192, slots);  // fewer do not take all of the bandwidth
     const double tile = plan.few           ? std::max(0.3, active * 2.0 * tile_bytes(type, dim) / 5e6)

@@ -45,7 +45,8 @@ def test_structs_match_header():
 
 REFUSED = [(dict(heads=0), "heads"), (dict(heads=3), "heads"), (dict(heads=8192), "heads"), (dict(causal=2), "causal"),
            (dict(out_type=0), "out_type"), (dict(out_type=2), "out_type"), (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"),
-           (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"), (dict(window=-1), "window"),
+           (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"), (dict(scale=1e-31), "scale"),
+           (dict(scale=2e30), "scale"), (dict(window=-1), "window"),
            (dict(window=4, causal=0), "window"), (dict(q=None), "NULL"), (dict(out=None), "NULL"), (dict(out=7 * BASE + 8), "aligned"),
            (dict(q=6 * BASE + 2), "aligned"), (dict(q_stride=60), "q's strides"), (dict(q_stride=H * 64 + 4), "q's strides"),
            (dict(q_head_stride=32), "q's strides"), (dict(out_stride=H * 64 - 8), "out_stride"), (dict(out_stride=H * 64 + 4), "out_stride"),
@@ -186,6 +187,47 @@ def test_one_sequence(device, dtype, dim, new, length):
 def test_heads(device, dtype, heads, kv_heads):
     for new, length in ((1, 130), (9, 50)):
         check(paged.Paged([new], [length], heads, kv_heads, 64, dtype))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("new", [1, 2, 3])
+def test_whole_tiles_of_few_columns(device, dtype, dim, new):
+    """32 heads of a cache head: 32 columns a token, in one, two and three tiles of the smallest kind; the last is the
+    kernel's of many columns."""
+    check(paged.Paged([new, 1], [300, 40], 32, 1, dim, dtype))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("page", [32, 64])
+def test_either_side_of_two_groups_of_waves(device, dtype, dim, page):
+    """Up to one work-group for a compute unit its keys are shared by two groups of waves, beyond by one: the same
+    sequence by itself and among others."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    news, lens = [70], [333]
+    check(paged.Paged(news, lens, 2, 2, dim, dtype, page))
+    n = cus // 4 + 1
+    many = paged.Paged(news + [65 + i % 9 for i in range(n)], lens + [90 + 3 * i for i in range(n)], 4, 4, dim, dtype, page)
+    cache, batch, q = many.cuda(qmm)
+    assert qmm.attention_plan(cache, batch, 4, q.shape[0], cus).work_groups > cus
+    check(many)
+    check(paged.Paged(news + [65] * n, lens + [90 + 3 * i for i in range(n)], 4, 4, dim, dtype, page), causal=False)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+def test_shared_pages(device, dtype):
+    """Two sequences whose tables begin with the same pages: a common prompt."""
+    for new in (1, 40):
+        p = paged.Paged([new, new], [150, 200], 4, 2, 64, dtype)
+        p.where[1][:3] = p.where[0][:3]
+        p.table[1, :3] = p.table[0, :3]
+        for x in (p.k, p.v):
+            x[1][:96] = x[0][:96]
+        check(p)
 
 
 @gpu

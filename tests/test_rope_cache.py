@@ -117,7 +117,7 @@ BATCH_REFUSED = [(dict(n_seq=0), "n_seq"), (dict(n_seq=1 << 16), "n_seq"), (dict
                  (dict(columns=1 << 26, table_stride=1 << 26), "columns"), (dict(table_stride=3), "table_stride"),
                  (dict(table_stride=-4), "table_stride"), (dict(starts=None), "NULL"), (dict(lengths=None), "NULL"),
                  (dict(table=None), "NULL"), (dict(lengths=3 * BASE + 66), "aligned"), (dict(max_new=-1), "max_new"),
-                 (dict(max_new=(1 << 20) + 1), "max_new"), (dict(max_length=-1), "max_length"), (dict(max_length=1 << 31), "max_length")]
+                 (dict(max_new=(1 << 20) + 1), "max_new"), (dict(max_length=-1), "max_length"), (dict(max_length=(1 << 30) + 1), "max_length")]
 N, H = 5, 4
 
 
