@@ -14,6 +14,11 @@ and what stands between the products of a layer:
     r = qmm.norm_quantize(h, weight, y=out)                     # r.h = h + out, r.qact = q8(norm(r.h))
     out = qmm.mmq_epilogue(w, r.qact, n_tok, act="silu", dtype=torch.float16)
     out = qmm.mmv(w_rows, x, residual=h)                        # up to 16 tokens, w_rows: a rows-form handle
+
+and between the q, k, v products and the output product:
+
+    q = qmm.rope_cache(cache, batch, q=q, k=k, v=v, frequencies=f)          # cache: Cache(...), batch: Batch(...)
+    qact = qmm.attention(q, cache, batch, dtype="q8")
 """
 from __future__ import annotations
 
