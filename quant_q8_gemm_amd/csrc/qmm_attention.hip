@@ -106,7 +106,10 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   int64_t keys = max_length;
   if (window > 0) keys = std::min(keys, window + plan.columns / group + kTileSlots);
   const int64_t tiles = std::max<int64_t>((keys + kTileSlots - 1) / kTileSlots, 1);
-  const int64_t base = n_seq * kv_heads * plan.tiles, slots = 2 * (int64_t)num_cus;
+  // work-groups of a split, and how many of them have columns at most: sequences with fewer
+  // tokens than max_new leave some without
+  const int64_t grid = n_seq * kv_heads * plan.tiles, slots = 2 * (int64_t)num_cus;
+  const int64_t base = std::min(grid, kv_heads * (n_tok * group / plan.columns + n_seq));
   // The number of splits that needs the least time, in microseconds: rounds of work-groups over
   // the GPU, each with a start and its share's tiles, and for more than one split the join
   // and the partial results' way through memory.  A tile takes a work-group of many columns
@@ -118,7 +121,7 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   const int64_t least = plan.few ? 4 : 32, unit = plan.few ? 4 : 2;
   int64_t share = tiles;
   double best = 0.0;
-  for (int64_t n = 1; n <= 256 && (n == 1 || (tiles / n >= least && base < 16 * slots)); n += n < 16 ? 1 : n / 8) {
+  for (int64_t n = 1; n <= 256 && (n == 1 || (tiles / n >= least && grid < 16 * slots)); n += n < 16 ? 1 : n / 8) {
     const int64_t each = ((tiles + n - 1) / n + unit - 1) / unit * unit, rounds = (base * n + slots - 1) / slots;
     const double active = (double)std::clamp<int64_t>(base * n, 192, slots);  // fewer do not take all of the bandwidth
     const double tile = plan.few           ? std::max(0.3, active * 2.0 * tile_bytes(type, dim) / 5e6)
@@ -130,8 +133,8 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   share = std::max(share, (tiles + 255) / 256);
   plan.splits = (int)((tiles + share - 1) / share);
   plan.share = (int)share;
-  plan.work_groups = base * plan.splits;
-  plan.groups = !plan.few && dim <= 128 && plan.work_groups <= num_cus ? 2 : 1;
+  plan.work_groups = grid * plan.splits;
+  plan.groups = !plan.few && base * plan.splits <= num_cus ? 2 : 1;
   plan.work_bytes = plan.splits == 1 ? 0 : (size_t)plan.splits * n_tok * heads * ((size_t)dim * 4 + 8);
   return plan;
 }

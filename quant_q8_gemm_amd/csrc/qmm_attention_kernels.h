@@ -205,7 +205,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
 //
 // The matrix core and the softmax's vector instructions bound it.  A work-group's four
 // waves take 32 columns each and share the keys and values, which pass through LDS
-// in two stages of 32*KB slots: while one is worked on the next is copied, 16-bit tiles
+// in a ring of stages of 32*KB slots: while one is worked on the next are copied, 16-bit tiles
 // straight from memory to LDS, q8 tiles through registers, where they become f16 once for
 // all waves.  Where there is at most one work-group for a compute unit it has two groups of
 // four waves, which take turns over the keys with stages of their own: a wave of a
@@ -232,7 +232,7 @@ __device__ __forceinline__ void copy_run(const void* base, uint32_t lane_off, ui
   else
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n\t"
                  "global_load_lds_dwordx4 %0, %1 offset:1024\n\tglobal_load_lds_dwordx4 %0, %1 offset:2048\n\t"
-                 "global_load_lds_dwordx4 %0, %1 offset:3072" ::"v"(lane_off), "s"(base), "s"(lds)
+                 "global_load_lds_dwordx4 %0, %1 offset:%3" ::"v"(lane_off), "s"(base), "s"(lds), "n"(3 * 1024)
                  : "memory");
 }
 
@@ -411,10 +411,19 @@ __device__ __forceinline__ void store_column(const AttnArgs& a, const Column& c,
   }
 }
 
+// Two waves a SIMD, but for q8 heads of 256: their accumulators, queries and the tile on its way
+// from q8 to f16 need more than 256 registers (a prompt of 4096, 32/8 heads: 568 us so, 675 with two
+// waves that reload some in every step).
+constexpr bool alone(int type, int db) { return type == QMM_Q8 && db == 8; }
+
 template <int TYPE, int DB, int KB, int STAGES, int GROUPS>
-__global__ __launch_bounds__(256 * GROUPS) __attribute__((amdgpu_waves_per_eu(DB <= 4 ? 2 : 1, DB <= 4 ? 2 : 1))) void many_kernel(
+__global__ __launch_bounds__(256 * GROUPS) __attribute__((
+    amdgpu_waves_per_eu(alone(TYPE, DB) ? 1 : 2, alone(TYPE, DB) ? 1 : 2))) void many_kernel(
     AttnArgs a, Pools pools, Batch batch) {
   constexpr int kDim = 32 * DB, kStage = 4 * KB * DB * 1024, kColumns = 128;
+  // operands read ahead: of heads of 256 two, as many as leave everything else in registers
+  // (the same prompt in f16: 303 us with four, 278 with two)
+  constexpr int kRead = DB == 8 && !alone(TYPE, DB) ? 2 : 4;
   __shared__ __attribute__((aligned(16))) uint8_t all_lds[GROUPS * STAGES * kStage];
   typedef typename Math<TYPE>::v8 v8;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, half = lane >> 5;
@@ -509,7 +518,7 @@ __global__ __launch_bounds__(256 * GROUPS) __attribute__((amdgpu_waves_per_eu(DB
           v16f score[KB];
 #pragma unroll
           for (int k = 0; k < KB; ++k) score[k] = v16f{};
-          products<v8, 2 * DB * KB, 4>(
+          products<v8, 2 * DB * KB, kRead>(
               keys, [](int i) { return (i % KB * 2 * DB + i / KB) * 1024; },
               [&](int i, const v8& k) { score[i % KB] = Math<TYPE>::mma(k, q[i / KB], score[i % KB]); });
           if (!here || slot0 < my_all_low || slot0 + 32 * KB > my_all_high) {
@@ -523,7 +532,7 @@ __global__ __launch_bounds__(256 * GROUPS) __attribute__((amdgpu_waves_per_eu(DB
           __builtin_amdgcn_s_setprio(1);
           soften<TYPE, DB, KB>(score, a.scale2, run, o, p);
           __builtin_amdgcn_s_setprio(0);
-          products<v8, 2 * DB * KB, 4>(
+          products<v8, 2 * DB * KB, kRead>(
               values, [](int i) { return (i / DB / 2 * 2 * DB + 2 * (i % DB) + i / DB % 2) * 1024; },
               [&](int i, const v8& v) { o[i % DB] = Math<TYPE>::mma(v, p[i / DB], o[i % DB]); });
         }
@@ -532,30 +541,41 @@ __global__ __launch_bounds__(256 * GROUPS) __attribute__((amdgpu_waves_per_eu(DB
         stage = stage + 1 == STAGES ? 0 : stage + 1;
       }
       if constexpr (GROUPS > 1) {
-        // the second group's sums join the first's, lane by lane through the second's stages
-        __syncthreads();
-        v4f* const moved = (v4f*)(all_lds + STAGES * kStage + wave * (DB * 4096)) + lane;
+        // the second group's sums join the first's, lane by lane through the second's stages, as
+        // many channels at a time as these hold
+        constexpr int kMoved = 16 * DB * 1024 <= STAGES * kStage ? DB : DB / 2;
+        static_assert(16 * kMoved * 1024 <= STAGES * kStage, "the sums fit the stages");
+        v4f* const moved = (v4f*)(all_lds + STAGES * kStage + wave * (kMoved * 4096)) + lane;
         float2* const state = (float2*)(all_lds + wave * 512) + lane;
-        if (group == 1) {
+        float by = 0.0f, by2 = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4 * DB; ++i)
-            moved[64 * i] = v4f{o[i >> 2][4 * (i & 3)], o[i >> 2][4 * (i & 3) + 1], o[i >> 2][4 * (i & 3) + 2],
-                                o[i >> 2][4 * (i & 3) + 3]};
-          *state = make_float2(run.top, run.sum);
-        }
-        __syncthreads();
-        if (group == 0) {
-          const float2 m = *state;
-          const float top = fmaxf(run.top, m.x);
-          const float by = run.top == kNone ? 0.0f : __builtin_amdgcn_exp2f((run.top - top) * a.scale2);
-          const float by2 = m.x == kNone ? 0.0f : __builtin_amdgcn_exp2f((m.x - top) * a.scale2);
-          run.top = top;
-          run.sum = fmaf(m.y, by2, run.sum * by);
+        for (int from_block = 0; from_block < DB; from_block += kMoved) {
+          __syncthreads();
+          if (group == 1) {
 #pragma unroll
-          for (int i = 0; i < 4 * DB; ++i) {
-            const v4f v = moved[64 * i];
+            for (int i = 0; i < 4 * kMoved; ++i) {
+              const v16f& x = o[from_block + (i >> 2)];
+              moved[64 * i] = v4f{x[4 * (i & 3)], x[4 * (i & 3) + 1], x[4 * (i & 3) + 2], x[4 * (i & 3) + 3]};
+            }
+            if (from_block == 0) *state = make_float2(run.top, run.sum);
+          }
+          __syncthreads();
+          if (group == 0) {
+            if (from_block == 0) {
+              const float2 m = *state;
+              const float top = fmaxf(run.top, m.x);
+              by = run.top == kNone ? 0.0f : __builtin_amdgcn_exp2f((run.top - top) * a.scale2);
+              by2 = m.x == kNone ? 0.0f : __builtin_amdgcn_exp2f((m.x - top) * a.scale2);
+              run.top = top;
+              run.sum = fmaf(m.y, by2, run.sum * by);
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[i >> 2][4 * (i & 3) + j] = fmaf(v[j], by2, o[i >> 2][4 * (i & 3) + j] * by);
+            for (int i = 0; i < 4 * kMoved; ++i) {
+              const v4f v = moved[64 * i];
+              v16f& x = o[from_block + (i >> 2)];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[4 * (i & 3) + j] = fmaf(v[j], by2, x[4 * (i & 3) + j] * by);
+            }
           }
         }
       }
@@ -611,9 +631,9 @@ __global__ __launch_bounds__(256 * GROUPS) __attribute__((amdgpu_waves_per_eu(DB
 
 constexpr int few_waves(int db) { return db <= 4 ? 4 : 2; }
 
-// Stages of many_kernel: as many as leave two work-groups on a CU (160 KiB of LDS) up to
-// heads of 128, and one beyond; q8 tiles pass through registers, one ahead.
-constexpr int stages(int type, int db) { return type == QMM_Q8 ? 2 : db == 2 ? 4 : db == 3 ? 3 : db == 4 ? 2 : 4; }
+// Stages of many_kernel: as many as leave two work-groups, or a group's two halves, on a CU
+// (160 KiB of LDS); q8 tiles pass through registers, one ahead.
+constexpr int stages(int type, int db) { return type == QMM_Q8 ? 2 : db == 2 ? 4 : db == 3 ? 3 : db == 4 ? 2 : db == 6 ? 3 : 2; }
 
 template <int TYPE, int DB>
 hipError_t launch_dim(const AttnArgs& a, const Pools& p, const Batch& b, const AttnPlan& plan, hipStream_t s) {
@@ -625,7 +645,7 @@ hipError_t launch_dim(const AttnArgs& a, const Pools& p, const Batch& b, const A
     few_kernel<TYPE, DB, W><<<grid, 64 * W, lds, s>>>(a, p, b);
     return hipGetLastError();
   }
-  if constexpr (DB <= 4) {
+  if constexpr (!alone(TYPE, DB)) {
     if (plan.groups == 2) {
       many_kernel<TYPE, DB, KB, stages(TYPE, DB), 2><<<grid, 512, 0, s>>>(a, p, b);
       return hipGetLastError();
