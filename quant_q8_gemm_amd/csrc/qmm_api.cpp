@@ -1153,7 +1153,7 @@ int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads
     const qmm::AttnPlan plan = qmm::plan_attention(cache->type, heads, cache->heads, cache->head_dim, b.n_seq, n_tok,
                                                    b.max_new, b.max_length, window, num_cus);
     if (int rc = check_attention_launch(plan, b.n_seq)) return rc;
-    *out = {plan.work_bytes, plan.work_groups, plan.few ? 1 : 0, plan.columns, plan.tiles, plan.splits};
+    *out = {plan.work_bytes, plan.work_groups, plan.few ? 1 : 0, plan.columns, plan.tiles, plan.splits, plan.share};
   }
   ok();
   return QMM_OK;

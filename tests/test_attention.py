@@ -114,6 +114,7 @@ def test_plans():
         assert p.work_groups == n_seq * kv * p.tiles * p.splits
         assert p.work_bytes == (0 if p.splits == 1 else p.splits * n_tok * kv * group * (dim * 4 + 8))
         assert p.splits == 1 or p.splits * 32 <= max(length, 32)
+        assert p.splits * p.share * 32 >= length and (p.splits - 1) * p.share * 32 < length
         lds = 4 * (8 if dim <= 128 else 4) * (64 + p.columns * (dim + 4)) if p.few else 0
         assert lds <= 160 * 1024
 
