@@ -655,7 +655,8 @@ typedef struct {
     int32_t few;         /* 1: few columns, the waves of a work-group take turns over
                             the keys; 0: each takes columns of its own */
     int32_t columns;
-    int32_t tiles;       /* column tiles of a sequence and cache head with max_new */
+    int32_t tiles;       /* column tiles of a sequence and cache head with max_new, or
+                            as many as work-groups take turns over (many sequences) */
     int32_t splits;
     int32_t share;
 } qmm_attn_plan;

@@ -1123,11 +1123,6 @@ int check_attention_sizes(const qmm_cache& c, int heads, int64_t n_tok) {
   return QMM_OK;
 }
 
-int check_attention_launch(const qmm::AttnPlan& plan, int64_t n_seq) {
-  if (plan.work_groups / n_seq > (int64_t)UINT32_MAX / 512 || plan.work_groups > INT32_MAX) return fail(QMM_EINVAL, "%lld work-groups exceed one launch", (long long)plan.work_groups);
-  return QMM_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -1152,7 +1147,6 @@ int qmm_attention_plan(const qmm_cache* cache, const qmm_batch* batch, int heads
   if (n_tok > 0) {
     const qmm::AttnPlan plan = qmm::plan_attention(cache->type, heads, cache->heads, cache->head_dim, b.n_seq, n_tok,
                                                    b.max_new, b.max_length, window, num_cus);
-    if (int rc = check_attention_launch(plan, b.n_seq)) return rc;
     *out = {plan.work_bytes, plan.work_groups, plan.few ? 1 : 0, plan.columns, plan.tiles, plan.splits, plan.share};
   }
   ok();
@@ -1216,7 +1210,6 @@ int qmm_attention(const qmm_attn* args, const qmm_cache* cache, const qmm_batch*
   if (e != hipSuccess) return fail_hip(e, "hipDeviceGetAttribute(multiprocessor count)");
   const qmm::AttnPlan plan = qmm::plan_attention(cache->type, a.heads, cache->heads, cache->head_dim, batch->n_seq, n_tok,
                                                  batch->max_new, batch->max_length, a.window, num_cus);
-  if (int rc = check_attention_launch(plan, batch->n_seq)) return rc;
   if (work_bytes < plan.work_bytes)
     return fail(QMM_EINVAL, "work_bytes %zu, but this launch needs %zu bytes of work memory (qmm_attention_plan)", work_bytes,
                 plan.work_bytes);

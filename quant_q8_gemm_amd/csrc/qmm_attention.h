@@ -30,7 +30,11 @@ struct AttnArgs {
   float scale2;                     // scale / ln 2: the exponentials are powers of two
 };
 
-// Plan of a launch (qmm_attention_plan).
+// Work-groups that a launch's tiles are given at most (but for one a sequence and head).
+constexpr int64_t kMostTiles = 1 << 18;
+
+// Plan of a launch (qmm_attention_plan).  Its work-groups are below 2^30: 65535 sequences of 4096
+// heads, two tiles each, and splits only where there are few.
 struct AttnPlan {
   bool few;
   int columns, tiles, splits, share, groups;

@@ -102,6 +102,9 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   plan.few = flats <= 64;
   plan.columns = plan.few ? (int)std::min<int64_t>(flats, 32) : 128;
   plan.tiles = (int)((flats + plan.columns - 1) / plan.columns);
+  // Work-groups without columns end at once, but thousands of sequences with max_new unknown would
+  // have millions of them, for some milliseconds: fewer take turns over a sequence's tiles then.
+  plan.tiles = (int)std::min<int64_t>(plan.tiles, std::max<int64_t>(kMostTiles / (n_seq * kv_heads), plan.few ? 2 : 1));
   // the most tiles of 32 slots that a tile of columns reads
   int64_t keys = max_length;
   if (window > 0) keys = std::min(keys, window + plan.columns / group + kTileSlots);

@@ -428,10 +428,17 @@ void launch_out(const Pools& p, const Batch& b, int type, int heads, void* k, vo
   else read_kernel<CACHE, QMM_BF16><<<grid, kThreads, 0, s>>>(p, b, heads, k, v);
 }
 
+// Groups of 16 slots of a sequence.  Thousands of sequences with max_new unknown would have
+// millions of them, most without a token: a work-group takes several then.
+int64_t slot_groups(int64_t max_new, int64_t n_seq) {
+  const int64_t most = std::max<int64_t>((1 << 18) / n_seq, 4);
+  return std::min<int64_t>((std::max<int64_t>(max_new, 1) + 2 * kSlots - 2) / kSlots, std::min<int64_t>(most, 1 << 16));
+}
+
 }  // namespace
 
 hipError_t launch_rope(RopeArgs r, const Pools& p, const Batch& b, int64_t max_new, hipStream_t s) {
-  const int64_t blocks = std::min<int64_t>((std::max<int64_t>(max_new, 1) + 2 * kSlots - 2) / kSlots, 1 << 16);
+  const int64_t blocks = slot_groups(max_new, b.n_seq);
   // As many heads for a work-group as leave a few work-groups of 16-bit values, or twice that
   // many of f32 ones, for every compute unit: of fewer, larger ones too few bytes are on
   // their way, of more the turns and starts cost.  3314 tokens of 32+32 heads of 128: from f32
@@ -453,7 +460,7 @@ hipError_t launch_rope(RopeArgs r, const Pools& p, const Batch& b, int64_t max_n
 }
 
 hipError_t launch_cache_read(const Pools& p, const Batch& b, int64_t max_new, int type, void* k, void* v, hipStream_t s) {
-  const int64_t blocks = std::min<int64_t>((std::max<int64_t>(max_new, 1) + 2 * kSlots - 2) / kSlots, 1 << 16);
+  const int64_t blocks = slot_groups(max_new, b.n_seq);
   const int heads = (int)std::clamp<int64_t>(blocks * b.n_seq * p.heads / 1024, 1, 8);
   const dim3 grid((unsigned)blocks, (unsigned)((p.heads + heads - 1) / heads), (unsigned)b.n_seq);
   (p.type == QMM_Q8 ? launch_out<QMM_Q8> : p.type == QMM_F16 ? launch_out<QMM_F16> : launch_out<QMM_BF16>)(

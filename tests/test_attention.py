@@ -110,7 +110,10 @@ def test_plans():
         rc, p = _plan(kv * group, kv, dim, n_seq, n_tok, max_new, length, cus, int(rng.choice([1, 2, 3])))
         assert rc == qmm.OK, qmm.last_error()
         flats = min(max_new, n_tok) * group
-        assert p.columns <= (32 if p.few else 128) and p.tiles * p.columns >= flats > (p.tiles - 1) * p.columns
+        assert p.columns <= (32 if p.few else 128) and flats > (p.tiles - 1) * p.columns
+        # every tile has a work-group, or there are very many and they take turns
+        assert p.tiles * p.columns >= flats or (not p.few and n_seq * kv * (p.tiles + 1) > 1 << 18)
+        assert p.work_groups < 1 << 30 and p.tiles * n_seq * kv <= max(1 << 18, 2 * n_seq * kv)
         assert p.work_groups == n_seq * kv * p.tiles * p.splits
         assert p.work_bytes == (0 if p.splits == 1 else p.splits * n_tok * kv * group * (dim * 4 + 8))
         assert p.splits == 1 or p.splits * 32 <= max(length, 32)
