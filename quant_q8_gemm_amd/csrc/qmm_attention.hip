@@ -16,7 +16,8 @@ namespace {
 // A work-group takes the rows (token, head) that its threads cover with dim/4 threads each
 // and LANES such sets for a row, which share its splits and are joined in LDS.  Loads go out
 // four splits at a time: there are few threads when this kernel matters, and a load after
-// the other would be all of its time.
+// the other would be all of its time.  Latency bounds it then: 64 rows of 24 splits 5.1 us, 32 of 13
+// 3.9 us; of many rows the partial results' bytes: 81920 rows of two splits 32.8 us (3.2 TB/s).
 template <int TYPE, int LANES>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Batch batch, int dim) {
   __shared__ float4 parts[256];
