@@ -205,7 +205,7 @@ def test_whole_tiles_of_few_columns(device, dtype, dim, new):
 
 @gpu
 @pytest.mark.parametrize("dtype", CACHES, ids=str)
-@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
 @pytest.mark.parametrize("page", [32, 64])
 def test_either_side_of_two_groups_of_waves(device, dtype, dim, page):
     """Up to one work-group for a compute unit its keys are shared by two groups of waves, beyond by one: the same
@@ -219,6 +219,39 @@ def test_either_side_of_two_groups_of_waves(device, dtype, dim, page):
     assert qmm.attention_plan(cache, batch, 4, q.shape[0], cus).work_groups > cus
     check(many)
     check(paged.Paged(news + [65] * n, lens + [90 + 3 * i for i in range(n)], 4, 4, dim, dtype, page), causal=False)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_many_work_groups(device, dtype, dim):
+    """More work-groups than compute units, one group of waves each: a window, an output in q8 blocks, and a value that is
+    no number, which reaches the tokens that see it and no others."""
+    n = torch.cuda.get_device_properties(0).multi_processor_count // 4 + 1
+    p = paged.Paged([150, 0] + [65 + i % 9 for i in range(n)], [333, 20] + [90 + 3 * i for i in range(n)], 4, 4, dim, dtype, 32)
+    check(p, window=77)
+    cache, batch, q = p.cuda(qmm)
+    clean = qmm.attention(q, cache, batch).clone()
+    if 4 * dim % 256 == 0:  # whole super-blocks
+        blocks = qmm.attention(q, cache, batch, dtype="q8")
+        torch.cuda.synchronize()
+        q8_close(p, blocks, *p.reference())
+    for slot in (200, 300):  # seen by all but 17 and by 33 of the 150 tokens
+        pool, page, at = cache.v.clone(), p.where[0][slot // 32], slot - 183
+        x = paged.unpacked(cache.v, dtype, "v", p.n_pages, 4, 32, dim) if dtype != "q8" else None
+        if dtype == "q8":  # the first block's scale
+            b, byte = cache.v.view(p.n_pages, 4, -1), 32 * dim + (slot % 32) * 2
+            b[page, 2, byte], b[page, 2, byte + 1] = 0, 0x7e
+        else:
+            x[page, 2, slot % 32, 3] = float("nan")
+            cache.v.copy_(paged.packed(x, dtype, "v").cuda())
+        out = qmm.attention(q, cache, batch)
+        torch.cuda.synchronize()
+        cache.v.copy_(pool)
+        width = slice(0, 32) if dtype == "q8" else slice(3, 4)
+        assert bool(out[at:150, 2, width].isnan().all())
+        out[at:150, 2, width] = clean[at:150, 2, width]
+        assert torch.equal(out, clean)
 
 
 @gpu
