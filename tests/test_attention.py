@@ -325,6 +325,17 @@ def test_splits(device, dtype, new):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+@pytest.mark.parametrize("dim", [96, 128, 192, 256])
+def test_splits_of_wide_heads(device, dtype, dim):
+    for news, lens in (([1], [4001]), ([200, 0, 33], [4001, 50, 70]), ([61, 64], [2048, 3001])):
+        p = paged.Paged(news, lens, 4, 2, dim, dtype, 64)
+        assert qmm.attention_plan(*p.cuda(qmm)[:2], 4, sum(news), 256).splits > 1
+        check(p)
+        check(p, window=700)
+
+
+@gpu
 @pytest.mark.parametrize("hints", [dict(max_new=1, max_length=1), dict(max_new=0, max_length=0), dict(max_new=None, max_length=None),
                                    dict(max_new=500, max_length=100000)], ids=str)
 def test_hints_only_size_the_launch(device, hints):
