@@ -117,20 +117,22 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   // The number of splits that needs the least time, in microseconds: rounds of work-groups over
   // the GPU, each with a start and its share's tiles, and for more than one split the join
   // and the partial results' way through memory.  A tile takes a work-group of many columns
-  // about 1 us; one of few what the active ones' tiles take from memory, 0.3 at least.  Measured:
+  // about 1 us, or 0.6 with two groups of waves, and of heads past 128 by as much more; one of few
+  // what the active ones' tiles take from memory, 0.3 at least.  Measured:
   // one token of 32 heads over 3314 slots with 1, 4, 16 splits 22.9, 15.8, 16.2 us; 16 sequences of
   // 20 heads of 64 over up to 1500 with 1, 2, 4: 15.7, 18.3, 20.3; one token of 64/8 heads over 131072
-  // with 8, 16, 32: 167, 109, 105; 2048 tokens of 40/8 heads over 32768 with 1, 2, 4: 1524, 1347, 1353.
+  // with 8, 16, 32: 167, 109, 105; 2048 tokens of 40/8 heads over 32768 with 1, 2, 4: 1524, 1347, 1353;
+  // 100 tokens of 16/4 heads over 3000 in q8 with 1, 2, 4, 8, 16: 64.8, 40.5, 28.8, 25.4, 25.9, of 256
+  // 196, 106, 62, 46, 39.
   const double start = plan.few ? 3.0 : 8.0, join = plan.few ? 4.5 : 10.0, partial_mb = (double)n_tok * heads * dim * 8e-6;
-  const int64_t least = plan.few ? 4 : 32, unit = plan.few ? 4 : 2;
+  const int64_t least = plan.few ? 4 : 8, unit = plan.few ? 4 : 2;
   int64_t share = tiles;
   double best = 0.0;
   for (int64_t n = 1; n <= 256 && (n == 1 || (tiles / n >= least && grid < 16 * slots)); n += n < 16 ? 1 : n / 8) {
     const int64_t each = ((tiles + n - 1) / n + unit - 1) / unit * unit, rounds = (base * n + slots - 1) / slots;
     const double active = (double)std::clamp<int64_t>(base * n, 192, slots);  // fewer do not take all of the bandwidth
-    const double tile = plan.few           ? std::max(0.3, active * 2.0 * tile_bytes(type, dim) / 5e6)
-                        : base * n > num_cus ? 1.0
-                                             : 0.6;
+    const double tile = plan.few ? std::max(0.3, active * 2.0 * tile_bytes(type, dim) / 5e6)
+                                 : (base * n > num_cus ? 1.0 : 0.6) * std::max(dim / 128.0, 1.0);
     const double cost = (double)rounds * ((double)each * tile + start) + (n > 1 ? join + partial_mb * (double)n / 4.0 : 0.0);
     if (n == 1 || cost < 0.97 * best) best = cost, share = each;
   }
