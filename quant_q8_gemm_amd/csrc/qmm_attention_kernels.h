@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
           add_part(x, total, *(const float4*)(parts + (w * a.columns + n) * kRow + d), tops[w * 32 + n], sums[w * 32 + n], top,
                    a.scale2);
         odd |= !(fabsf(x.x + x.y) + fabsf(x.z + x.w) < __builtin_inff());
-        if (safe) add_edges<TYPE>(pools, batch, s, h, {from, end, 1, all_low, all_high}, to, d, x);
+        if (safe) add_edges<TYPE>(pools, batch, s, h, {from, end, all_low, all_high}, to, d, x);
         store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, total);
       }
       // again, safely, where a result is no finite number (a barrier that the next round needs too)
@@ -513,9 +513,14 @@ __global__ __launch_bounds__(256 * GROUPS) __attribute__((
         const int slot0 = 32 * t;
         const bool here = here_bits == (1u << KB) - 1;
         if (safe) {
-          if (t < end && (!here || slot0 < all_low || slot0 + 32 * KB > all_high)) {
-            v8* const values = (v8*)(lds + stage * kStage + kStage / 2);
-            for (int i = threadIdx.x & 255; i < kStage / 32; i += 256) values[i] = finite<TYPE>(values[i]);
+          constexpr int kPieces = kStage / 32 / KB;  // of 16 bytes, of a tile's values
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            const int slot = slot0 + 32 * k;
+            if (t < end && ((here_bits >> k & 1) == 0 || slot < all_low || slot + 32 > all_high)) {
+              v8* const values = (v8*)(lds + stage * kStage + kStage / 2) + k * kPieces;
+              for (int i = threadIdx.x & 255; i < kPieces; i += 256) values[i] = finite<TYPE>(values[i]);
+            }
           }
           __syncthreads();
         }
@@ -625,7 +630,7 @@ __global__ __launch_bounds__(256 * GROUPS) __attribute__((
           float4 x = *(const float4*)(out + n * (32 * kBlocks) + 4 * (piece ^ (n & kSwap)));
           if (!to.real) continue;
           const int d = 32 * pass + 4 * piece;
-          add_edges<TYPE>(pools, batch, s, h, {from, end, KB, all_low, all_high}, to, d, x);
+          add_edges<TYPE>(pools, batch, s, h, {from, end, all_low, all_high}, to, d, x);
           store_part<TYPE>(a, kDim, batch.n_tok, split, to, d, x, top, all);
         }
         wave_sync();

@@ -204,10 +204,10 @@ __device__ __forceinline__ float value_of(const uint8_t* tile, int dim, int r, i
 // no finite number must not reach the others, and on the matrix core their 0 times it
 // would be NaN.  A result that is no finite number may be such a one: the work-group then
 // does its tile again with zeros for those values in the product (`finite`), and they are
-// added here to the columns that see them, channel by channel.
+// added here to the columns that see them, channel by channel.  Both go by the same 32 slots: in a
+// tile that every column sees nothing is taken out and nothing added.
 struct Edges {
   int from, end;  // tiles of the split
-  int step;       // tiles taken at a time
   int low, high;  // slots that every column sees
 };
 template <int TYPE>
@@ -215,8 +215,8 @@ __device__ __forceinline__ void add_edges(const Pools& pools, const Batch& batch
                                           int d, float4& x) {
 #pragma unroll 1
   for (int t = e.from; t < e.end; ++t) {
-    const int first = 32 * (t - (t - e.from) % e.step);  // of those taken together
-    if ((first >= e.low && first + 32 * e.step <= e.high) || 32 * t >= c.high || 32 * t + 32 <= c.low) continue;
+    // where every column sees the tile its values were left as they are
+    if ((32 * t >= e.low && 32 * t + 32 <= e.high) || 32 * t >= c.high || 32 * t + 32 <= c.low) continue;
     const int64_t at = tile_offset(batch, pools, s, h, t);
     if (at < 0) continue;
 #pragma unroll 1

@@ -1,0 +1,62 @@
+"""qmm_attention where tiles, types and masks end: values that are no numbers beside pages outside the pool, leftovers of
+a q8 pool, tokens whose scores are all -infinity, keys of small weight.  Tolerances: see each test."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quant_q8_gemm_amd as qmm  # noqa: E402
+from tests import paged  # noqa: E402
+from tests.test_attention import check  # noqa: E402
+
+gpu = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+CACHES = [F16, BF16, "q8"]
+
+
+@pytest.fixture
+def device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+    yield torch.device("cuda", 0)
+    torch.cuda.synchronize()
+
+
+def put(p, pool, which, slot, head, channel, value):
+    """Writes a number (q8: the scale of the channel's block) into the first sequence's slot; the channels it reaches."""
+    page, at = p.where[0][slot // p.page], slot % p.page
+    if p.dtype == "q8":
+        byte = at // 32 * 34 * p.dim + 32 * p.dim + (channel // 32 * 32 + at % 32) * 2
+        bits = int(np.float16(value).view(np.uint16))
+        b = pool.view(p.n_pages, p.kv_heads, -1)
+        b[page, head, byte], b[page, head, byte + 1] = bits & 255, bits >> 8
+        return slice(channel // 32 * 32, channel // 32 * 32 + 32)
+    x = paged.unpacked(pool, p.dtype, which, p.n_pages, p.kv_heads, p.page, p.dim)
+    x[page, head, at, channel] = value
+    pool.copy_(paged.packed(x, p.dtype, which).to(pool.device))
+    return slice(channel, channel + 1)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("new,causal", [(5, True), (70, True), (64, False), (300, True)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_not_finite_beside_a_page_outside_the_pool(device, dtype, dim, new, causal, bad):
+    """Of two neighbouring pages one is outside the pool, and the other holds a value that is no finite number, which every
+    token sees: no token has a finite result in its channel, and all the others are as without it."""
+    for missing in (0, 1, 2, 3):
+        p = paged.Paged([new], [500], 4, 2, dim, dtype, 32, junk=0.0)
+        cache, batch, q = p.cuda(qmm)
+        batch.table[0, missing] = p.n_pages
+        clean = qmm.attention(q, cache, batch, causal=causal).clone()
+        wide = put(p, cache.v, "v", 32 * (missing ^ 1) + 5, 1, 3, bad)
+        out = qmm.attention(q, cache, batch, causal=causal)
+        torch.cuda.synchronize()
+        assert bool(clean.isfinite().all())
+        assert not bool(out[:, 2:, wide].isfinite().any()), (missing, out[:, 2:, wide].isfinite().sum())
+        out[:, 2:, wide] = clean[:, 2:, wide]
+        assert torch.equal(out, clean)
