@@ -62,11 +62,19 @@ struct Loaded<QMM_Q8, DB> {
   __device__ __forceinline__ f16x8 codes(int i, const f16x8& s) const {
     return (i & 1) ? codes8(w[i >> 1].z, w[i >> 1].w, s) : codes8(w[i >> 1].x, w[i >> 1].y, s);
   }
-  // codes are finite: a value is where its scale is (products that pass 65504 aside, which
-  // blocks of numbers of up to 2046 do not have)
+  // A scale that is no finite number becomes zero, and with a finite one the codes whose
+  // product with it is none: leftovers of a pool may be any bits.
   __device__ __forceinline__ void clean() {
 #pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) v[i] = finite<QMM_Q8>(v[i]);
+    for (int i = 0; i < 2 * DB; ++i) {
+      const u16x8 u = __builtin_bit_cast(u16x8, codes(i, v[i]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int four = 2 * (i & 1) + (j >> 2), shift = 8 * (j & 3);
+        if ((u[j] & 0x7c00) == 0x7c00) w[i >> 1][four] = (w[i >> 1][four] & ~(255 << shift)) | (128 << shift);
+      }
+      v[i] = finite<QMM_Q8>(v[i]);
+    }
   }
   __device__ __forceinline__ f16x8 key(int i) const { return codes(i, splat8(k[i >> 1])); }
   __device__ __forceinline__ f16x8 value(int i) const { return codes(i, v[i]); }

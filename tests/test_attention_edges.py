@@ -60,3 +60,16 @@ def test_not_finite_beside_a_page_outside_the_pool(device, dtype, dim, new, caus
         assert not bool(out[:, 2:, wide].isfinite().any()), (missing, out[:, 2:, wide].isfinite().sum())
         out[:, 2:, wide] = clean[:, 2:, wide]
         assert torch.equal(out, clean)
+
+
+@gpu
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("junk", [60000.0, -600.0])
+def test_leftovers_of_a_q8_pool(device, dim, junk):
+    """Memory that nothing was stored to: scales whose products with the codes pass f16, in slots that no token sees.  The
+    tolerance is that of Paged.reference."""
+    for news, lens in (([1], [33]), ([1, 3, 1], [1, 40, 31]), ([1], [4001]), ([40], [90])):
+        p = paged.Paged(news, lens, 4, 2, dim, "q8", junk=junk)
+        check(p)
+        check(p, window=7)
+        check(p, causal=False)
