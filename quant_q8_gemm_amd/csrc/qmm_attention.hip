@@ -78,9 +78,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Batch batch, int 
       }
     }
     if (real && lane == 0) {
-      const float by = total == 0.0f ? 0.0f : 1.0f / total;
-      store_four<TYPE>(a, dim, (int)(row / a.heads), (int)(row % a.heads), d,
-                       make_float4(x.x * by, x.y * by, x.z * by, x.w * by));
+      store_four<TYPE>(a, dim, (int)(row / a.heads), (int)(row % a.heads), d, divided(x, total));
     }
     if (LANES > 1) __syncthreads();
   }

@@ -388,17 +388,15 @@ __device__ __forceinline__ void store_column(const AttnArgs& a, const Column& c,
                            make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]), top, total);
       return;
     }
-    const float by = total == 0.0f ? 0.0f : 1.0f / total;
     const int64_t to = c.row * a.out_stride + (int64_t)c.head * kDim + 4 * half;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        store4<T>(a.out, to + 32 * d + 8 * i, make_float4(o[d][4 * i] * by, o[d][4 * i + 1] * by, o[d][4 * i + 2] * by,
-                                                         o[d][4 * i + 3] * by));
+        store4<T>(a.out, to + 32 * d + 8 * i,
+                  divided(make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]), total));
     return;
   }
-  const float by = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t id = (int64_t)a.heads * kDim;
 #pragma unroll
   for (int d = 0; d < DB; ++d) {
@@ -406,7 +404,7 @@ __device__ __forceinline__ void store_column(const AttnArgs& a, const Column& c,
     float4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = make_float4(o[d][4 * i] * by, o[d][4 * i + 1] * by, o[d][4 * i + 2] * by, o[d][4 * i + 3] * by);
+      x[i] = divided(make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]), total);
       largest = larger(larger(largest, larger(x[i].x, x[i].y)), larger(x[i].z, x[i].w));
     }
     const Halves both = halves(largest);

@@ -257,6 +257,13 @@ __device__ __forceinline__ void add_part(float4& x, float& total, const float4& 
   x.x = fmaf(part.x, by, x.x), x.y = fmaf(part.y, by, x.y), x.z = fmaf(part.z, by, x.z), x.w = fmaf(part.w, by, x.w);
 }
 
+// Four channels' results from a column's sums.  Nothing seen, or no score above -infinity: zeros, and
+// not 0 times a value that is no number.
+__device__ __forceinline__ float4 divided(const float4& x, float total) {
+  const float by = 1.0f / total;
+  return total == 0.0f ? make_float4(0, 0, 0, 0) : make_float4(x.x * by, x.y * by, x.z * by, x.w * by);
+}
+
 // Four channels of a column's sums: to the split's partial results, or as the output.
 template <int TYPE>
 __device__ __forceinline__ void store_part(const AttnArgs& a, int dim, int n_tok, int split, const Column& c, int d,
@@ -266,8 +273,7 @@ __device__ __forceinline__ void store_part(const AttnArgs& a, int dim, int n_tok
     *(float4*)(a.part + row * dim + d) = x;
     if (d == 0) a.sums[row] = make_float2(top, total);
   } else {
-    const float by = total == 0.0f ? 0.0f : 1.0f / total;
-    store_four<TYPE>(a, dim, c.row, c.head, d, make_float4(x.x * by, x.y * by, x.z * by, x.w * by));
+    store_four<TYPE>(a, dim, c.row, c.head, d, divided(x, total));
   }
 }
 

@@ -73,3 +73,21 @@ def test_leftovers_of_a_q8_pool(device, dim, junk):
         check(p)
         check(p, window=7)
         check(p, causal=False)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 1.0])
+def test_no_score_above_minus_infinity(device, dtype, dim, bad):
+    """Every key that a token sees has a score of -infinity: zeros, whatever the values are, in every kernel."""
+    for new, length in ((1, 40), (5, 70), (70, 100), (150, 333), (1, 4001), (100, 4001)):
+        p = paged.Paged([new], [length], 4, 2, dim, dtype, junk=0.0)
+        p.k[0][:, :, 0] = -math.inf
+        p.q[:, :, 0] = p.q[:, :, 0].abs() + 0.25
+        p.v[0][1::3, :, 5] = bad
+        cache, batch, q = p.cuda(qmm)
+        for causal in (True, False):
+            assert not bool(qmm.attention(q, cache, batch, causal=causal).any())
+        if 4 * dim % 256 == 0:
+            assert not bool(qmm.attention(q, cache, batch, dtype="q8").any())
