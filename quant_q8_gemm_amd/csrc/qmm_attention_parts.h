@@ -35,6 +35,11 @@ struct Math {
   typedef f16x8 v8;
   typedef _Float16 e;
   static constexpr uint16_t kExponent = 0x7c00;
+  // Probabilities are 2^kRaise times what they stand for, and so is their sum.  f16's are whole numbers of
+  // 2^-24: with the largest, 2^kSlack, raised to 2^15, weights of 2^-22 of the largest one have all of
+  // their bits, and smaller ones are off by 2^-33 of it at most, 2^20 of them by 2^-13, a quarter of
+  // the result's own half step.  (At 2^0 weights below 2^-25 are lost: of 131072 keys 0.4%.)
+  static constexpr float kRaise = 8.0f;
   static __device__ __forceinline__ v16f mma(const v8& a, const v8& b, const v16f& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
@@ -44,6 +49,7 @@ struct Math<QMM_BF16> {
   typedef bf16x8 v8;
   typedef __bf16 e;
   static constexpr uint16_t kExponent = 0x7f80;
+  static constexpr float kRaise = 0.0f;  // f32's exponents
   static __device__ __forceinline__ v16f mma(const v8& a, const v8& b, const v16f& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -133,8 +139,8 @@ struct Running {
 // exp(scale*(s - top)) is 2^(s*scale2 - top*scale2), one fma and one v_exp_f32.  `top` only
 // follows the maximum once that is kSlack powers of two above it in some column, so that
 // the accumulators are scaled a few times a sequence and not with most tiles: a probability
-// may then be up to 2^kSlack, which f16 and bf16 hold as exactly as one below 1 (and an f32 sum of
-// 2^31 of them too), and what is small is no smaller than relative to the maximum itself.
+// may then be up to 2^kSlack (times 2^kRaise), which f16 and bf16 hold as exactly as one below 1 (and an
+// f32 sum of 2^31 of them too), and what is small is no smaller than relative to the maximum itself.
 // A column without a score above -infinity stays at sum 0; NaN scores stay NaN, as a sum
 // that is not a number shows.
 constexpr float kSlack = 7.0f;
@@ -160,7 +166,7 @@ __device__ __forceinline__ void soften(v16f (&s)[KB], float scale2, Running& run
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] *= by;
   }
-  const float off = run.top == kNone ? 0.0f : -run.top * scale2;
+  const float off = run.top == kNone ? 0.0f : Math<TYPE>::kRaise - run.top * scale2;
   float sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < KB; ++k)

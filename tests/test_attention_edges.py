@@ -91,3 +91,32 @@ def test_no_score_above_minus_infinity(device, dtype, dim, bad):
             assert not bool(qmm.attention(q, cache, batch, causal=causal).any())
         if 4 * dim % 256 == 0:
             assert not bool(qmm.attention(q, cache, batch, dtype="q8").any())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("max_length", [30000, 1])
+@pytest.mark.parametrize("far", [9.0, 13.0, 18.0, 71.4375, 142.875])
+def test_keys_of_small_weight(device, dtype, new, max_length, far):
+    """One key far above the many others, as the first of a long context often is, with values of zero: the result is the
+    others' weights, exp(-far) each.  With max_length 1 a work-group takes all of the keys.
+
+    Allowed, relative to the weight of the first key: half a step u of the products' type of each weight, and where the
+    type's numbers get no finer (f16 below 2^-14 of its range, of which the largest weight takes at least 2^8) 2^-33 for
+    each of the n keys; what is below f32's 2^-126 may be zero.  The scores are exact but for scale, its product with
+    1/ln 2 and with the score (4 f, f = 2^-24) and their power's rounding (2^-22), n + 64 sums in f32 add
+    (n + 64) f; then half a step of the stored result."""
+    n, dim = 30000, 64
+    p = paged.Paged([new], [n], 2, 1, dim, dtype, 64, junk=0.0)
+    p.q[:] = 0.0
+    p.q[:, :, 0] = 1.0
+    p.k[0][:], p.v[0][:] = 0.0, 127.0 / 128.0  # whole codes of blocks with a scale that f16 holds
+    p.k[0][0, :, 0], p.v[0][0] = 127.0 / 16.0, 0.0
+    cache, batch, q = p.cuda(qmm, max_length=max_length)
+    out = qmm.attention(q, cache, batch, scale=far * 16.0 / 127.0, causal=False).double().cpu()
+    rest = (n - 1) * math.exp(-far)
+    want, f, u = 127.0 / 128.0 * rest / (1.0 + rest), 2.0 ** -24, paged.HALF[p.type]
+    off = want * (u + 2 * (far * 4 * f + 2.0 ** -22) + 2 * (n + 64) * f) + n * (2.0 ** -33 if p.type == F16 else 2.0 ** -126)
+    off += paged.HALF[p.type] * (want + off) + (2.0 ** -25 if p.type == F16 else 0.0)
+    assert float((out - want).abs().max()) <= off, (float((out - want).abs().max()), off, want)
