@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Batch batch, int 
   if (a.q8_out)
     zero_padding(a, dim, batch.n_tok, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
   const int first = clamped(uniform_load(batch.starts, 0), 0, batch.n_tok);
-  const int end = clamped(uniform_load(batch.starts, batch.n_seq), first, batch.n_tok);
+  const int end = first_row(batch, batch.n_seq);
   const int quads = dim >> 2, per_row = quads * LANES, rows_here = 256 / per_row;
   const int lane = threadIdx.x / quads % LANES, d = 4 * (threadIdx.x % quads), mine = threadIdx.x / per_row;
   const int64_t all = (int64_t)batch.n_tok * a.heads;
