@@ -106,7 +106,7 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   plan.tiles = (int)std::min<int64_t>(plan.tiles, std::max<int64_t>(kMostTiles / (n_seq * kv_heads), plan.few ? 2 : 1));
   // the most tiles of 32 slots that a tile of columns reads
   int64_t keys = max_length;
-  if (window > 0) keys = std::min(keys, window + plan.columns / group + kTileSlots);
+  if (window > 0 && window < keys) keys = std::min(keys, window + plan.columns / group + kTileSlots);  // 2^63 - 1 is a window too
   const int64_t tiles = std::max<int64_t>((keys + kTileSlots - 1) / kTileSlots, 1);
   // work-groups of a split, and how many of them have columns at most: sequences with fewer
   // tokens than max_new leave some without
