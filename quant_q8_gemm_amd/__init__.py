@@ -637,6 +637,9 @@ class Batch:
     the launch, and sequences that pass them only take longer."""
 
     def __init__(self, starts, lengths, table, *, max_new: int = None, max_length: int = None):
+        for hint, what, most in ((max_new, "max_new", MAX_TOKENS), (max_length, "max_length", MAX_SLOTS)):
+            if hint is not None and not 0 <= hint <= most:
+                raise QmmError(EINVAL, f"{what} must be None or in [0, {most}], got {hint}")
         device = starts.get_device()
         for t, what, dims in ((starts, "starts", 1), (lengths, "lengths", 1), (table, "table", 2)):
             if t.get_device() != device or device < 0 or t.dtype != torch.int32 or t.dim() != dims or (
@@ -748,9 +751,16 @@ def cache_read(cache: Cache, batch: Batch, n_tok: int, *, dtype=torch.float32, s
     return k, v
 
 
+def _window(window: int) -> int:
+    if not 0 <= window < 1 << 63:  # ctypes would take other numbers modulo 2^64
+        raise QmmError(EINVAL, f"window must be in [0, 2^63), got {window}")
+    return window
+
+
 def attention_plan(cache: Cache, batch: Batch, heads: int, n_tok: int, num_cus: int, window: int = 0) -> AttnPlan:
     """How attention of these sizes is launched, and the work memory it needs (host arithmetic only)."""
     plan = AttnPlan()
+    window = _window(window)
     _check(_lib.qmm_attention_plan(cache.struct, batch._for(cache, n_tok), heads, window, n_tok, num_cus, plan))
     return plan
 
@@ -779,7 +789,7 @@ def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: boo
     if dtype is not None and dtype != "q8" and dtype != kind:
         raise QmmError(EINVAL, f"dtype must be None, 'q8' or {kind}, got {dtype}")
     a = Attn(heads, 1 if causal else 0, Q8 if dtype == "q8" else ELEM_TYPES[kind], dim ** -0.5 if scale is None else scale,
-             window, *_heads(q, "q", n_tok, heads, cache.head_dim, device, kind))
+             _window(window), *_heads(q, "q", n_tok, heads, cache.head_dim, device, kind))
     result = out
     if dtype == "q8":
         if out is None:

@@ -19,3 +19,26 @@ def test_windows_past_the_length_plan_as_none(sizes, type_):
     for window in (sizes[-1], sizes[-1] + 1, 1 << 31, 1 << 62, (1 << 63) - 200, (1 << 63) - 1):
         rc, p = _plan(*sizes, type_=type_, window=window)
         assert rc == qmm.OK and bytes(p) == bytes(want), (window, p.splits, want.splits)
+
+
+@pytest.mark.parametrize("kw", [dict(max_new=-1), dict(max_new=(1 << 20) + 1), dict(max_new=(1 << 64) + 1), dict(max_length=-7),
+                                dict(max_length=(1 << 30) + 1), dict(max_length=1 << 64)], ids=str)
+def test_hints_out_of_range_are_refused(kw):
+    t = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(qmm.QmmError, match=next(iter(kw))):
+        qmm.Batch(t, t[:1], t[None, :1], **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [-1, 1 << 63, (1 << 64) + 3])
+def test_windows_out_of_range_are_refused(window):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    t = torch.tensor([0, 1], dtype=torch.int32).cuda()
+    cache, batch = qmm.Cache(1, 2, 64, page=32), qmm.Batch(t, t[1:], t[None, :1])
+    q = torch.zeros(1, 2, 64, dtype=torch.float16, device="cuda")
+    for call in (lambda: qmm.attention(q, cache, batch, window=window),
+                 lambda: qmm.attention_plan(cache, batch, 2, 1, 256, window)):
+        with pytest.raises(qmm.QmmError, match="window"):
+            call()
+    assert not bool(qmm.attention(q, cache, batch, window=(1 << 63) - 1).any())
