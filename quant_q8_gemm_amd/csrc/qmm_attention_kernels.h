@@ -5,6 +5,7 @@
 
 #include "qmm_attention_parts.h"
 #include "qmm_internal.h"
+#include "qmm_pages.h"
 
 namespace qmm {
 
@@ -78,35 +79,6 @@ struct Loaded<QMM_Q8, DB> {
   }
   __device__ __forceinline__ f16x8 key(int i) const { return codes(i, splat8(k[i >> 1])); }
   __device__ __forceinline__ f16x8 value(int i) const { return codes(i, v[i]); }
-};
-
-// A sequence's page numbers, 64 columns of its table at a time in a register of the wave: a
-// lookup is then a v_readlane, where a load would be waited for with every tile.
-struct Pages {
-  const int32_t* row;
-  int columns, base, held, shift, n_pages, tile;
-  int64_t page, head;  // bytes of a page, and to the head in it
-  // (before anything else of a kernel, so that it is there when the lengths are)
-  __device__ __forceinline__ Pages(const Batch& b, const Pools& p, int s, int h)
-      : row(b.table + s * b.table_stride), columns(b.columns), base(0), shift(p.page_shift - 5), n_pages(p.n_pages) {
-    held = row[min((int)(threadIdx.x & 63), columns - 1)];
-    tile = tile_bytes(p.type, p.dim);
-    head = (int64_t)tile * (h << shift);
-    page = (int64_t)tile * (p.heads << shift);
-  }
-  // Tile t's place in both pools, or -1; t is the same in every lane.
-  __device__ __forceinline__ int64_t place(int t, int end) {
-    if (t >= end) return -1;
-    const int i = t >> shift;
-    if ((unsigned)(i - base) >= 64u) {
-      base = i;
-      held = row[min(i + (int)(threadIdx.x & 63), columns - 1)];
-      pin(held);  // waited for here, and not where lookups without a load come by
-    }
-    const uint32_t at = (uint32_t)__builtin_amdgcn_readlane(held, i - base);
-    if (at >= (uint32_t)n_pages) return -1;
-    return head + (int64_t)((uint64_t)at * (uint64_t)page) + (uint32_t)((t & ((1 << shift) - 1)) * tile);
-  }
 };
 
 template <int TYPE, int DB, int WAVES>
@@ -290,24 +262,6 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
-
-// Where the tiles of a stage are.
-template <int KB>
-struct Places {
-  int64_t at[KB];
-  // t is a multiple of KB: two tiles are on one page but for pages of 32 slots
-  __device__ __forceinline__ void find(Pages& pages, int t, int end) {
-    at[0] = pages.place(t, end);
-    if (KB > 1) at[KB - 1] = pages.shift == 0 ? pages.place(t + 1, end) : t + 1 < end && at[0] >= 0 ? at[0] + pages.tile : -1;
-  }
-  // a bit for each tile that is somewhere
-  __device__ __forceinline__ uint32_t here() const {
-    uint32_t r = 0;
-#pragma unroll
-    for (int k = 0; k < KB; ++k) r |= (uint32_t)(at[k] >= 0) << k;
-    return r;
-  }
-};
 
 // Waits until at most N of the wave's loads are on their way: the copies to LDS, which the
 // compiler does not count.
