@@ -465,7 +465,10 @@ int qmm_mmv(const qmm_weights *w, const void *x, int x_type, int64_t x_stride, i
  * and value (in the pool v) of every head, head_dim channels each; a page holds
  * `page` slots, and each pool n_pages pages of qmm_cache_page_bytes bytes,
  * 16-byte aligned.  The caller owns the pools; nothing in them needs clearing (what
- * no sequence's slot in use holds is never part of a result).
+ * no sequence's slot in use holds is never part of a result).  Leftovers that are no
+ * finite numbers, in values of tiles that are partly in use, cost time though: attention
+ * does such work again (decode steps took up to 2 times as long, prompts and chunks 6 to
+ * 20 times), which a pool that was cleared once does not meet.
  *   type     QMM_F16, QMM_BF16, or QMM_Q8: blocks of 32 channels of a slot, int8
  *            codes and an f16 scale as qmm_quantize_activations makes them (the
  *            scaled sum left out; |values| <= 2046 as there), 1.0625 bytes a value
@@ -500,13 +503,16 @@ size_t qmm_cache_page_bytes(int type, int heads, int head_dim, int page);
  * of the cache, of which its tokens of this call are the last: token i of n has slot
  * lengths[s] - n + i.  Slot j is slot j % page of page table[s][j / page].
  * The arrays are device memory, read when the kernels run.  Whatever they hold,
- * nothing outside the tensors and pools is read or written: starts are taken
- * within [0, n_tok] and not to go down, lengths within the table's columns;
- * tokens without a slot (more than lengths[s]) and pages outside the pool are not
+ * nothing outside the tensors and pools is read or written: a start is taken
+ * within [0, n_tok] and as the highest up to it, so that no token has two
+ * sequences, lengths within the table's columns; tokens without a slot (more than lengths[s]) and pages outside the pool are not
  * followed: nothing is stored to them, and their keys are not seen.
  * max_new, max_length: the most tokens and the most slots of any sequence, to size
- * the launch by; sequences that pass them are worked through all the same, only
- * slower. */
+ * the launch by.  They do not change which keys are seen.  Sequences that pass them
+ * are worked through all the same, only slower; a max_length far above the lengths is
+ * slower too, since attention takes a part of the keys to be of the size that it
+ * would have in a sequence of max_length (one token of 32/8 heads of 128 over 3314
+ * slots: 11.2 us with 3314, 12.9 with 8192, 17.1 with 32768, 25.8 with 131072). */
 #define QMM_MAX_SEQS 65535
 #define QMM_MAX_SLOTS (1 << 30) /* of a sequence */
 typedef struct {
@@ -583,8 +589,8 @@ typedef struct {
  * q_out may be q in place (same type, pointer and strides); any other overlap of
  * an output with an input is refused.  Rows of tokens of no sequence are left as
  * they are, and slots of other tokens too.  Two tokens of a call never have one
- * slot unless the table gives two sequences one page: which of them stays is then
- * open.
+ * slot unless the table names a page twice, in two sequences or in one: what such a
+ * slot then holds is open (in q8, codes of one and the scale of the other).
  * No workspace; can be captured into a graph.
  * Errors: QMM_EINVAL, QMM_EHIP.  n_tok == 0 is an empty batch.
  */
@@ -610,7 +616,7 @@ typedef struct {
                           encoder's states, of a length that has nothing to do with
                           the tokens') */
     int32_t out_type;  /* q's type (QMM_F16, QMM_BF16) or QMM_Q8 */
-    float scale;       /* of the scores, > 0, finite */
+    float scale;       /* of the scores, in [1e-30, 1e30] */
     int64_t window;    /* causal: of those only the last `window`; 0: all */
     const void *q;     /* device [n_tok][heads][head_dim], adjacent channels, of the
                           cache's type (QMM_F16 with a q8 cache), 16-byte aligned */
@@ -627,10 +633,12 @@ typedef struct {
  * head h and the keys j that it sees, of cache head h / (heads / cache heads),
  *   p_j = exp(scale * q.k_j - max_j),   out = sum_j p_j v_j / sum_j p_j
  * Products are of 16-bit values summed in f32; maximum and sum are f32; p_j is
- * rounded to q's type for the second product, q8 keys and values to f16.  Scores
- * times scale stay below 2^126 in size, or are no numbers in what comes of them.  A
- * token that sees no key, or none whose score is above -infinity, gets zeros.  What a
- * token does not see is no part of its result, whatever is stored there.  An output
+ * rounded to q's type for the second product (f16: with weights down to 2^-22 of the
+ * largest one in full, smaller ones to 2^-33 of it), q8 keys and values to f16.
+ * Scores times scale stay below 2^126 in size, and values times the number of keys
+ * below 2^120 (bf16), or are no numbers in what comes of them.  A token that sees no
+ * key, or none whose score is above -infinity, gets zeros, whatever the values are.
+ * What a token does not see is no part of its result, whatever is stored there.  An output
  * in q8 blocks has its padding tokens zero; rows of tokens of no sequence are
  * left as they are.
  *   work      device memory of at least the plan's work_bytes (qmm_attention_plan),

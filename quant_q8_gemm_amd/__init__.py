@@ -634,7 +634,8 @@ class Batch:
     int32 [n_seq] (slots in use, the call's tokens the last of them), table int32 [n_seq][columns] (page numbers), all
     on the device and read there, so that a captured graph takes what they hold when it is replayed.  max_new and
     max_length: the most tokens and slots of any sequence (None: what a sequence can have at most); they size
-    the launch, and sequences that pass them only take longer."""
+    the launch and change no result.  Sequences that pass them take longer, and so does attention over ones far shorter than
+    max_length, None among them: give the longest length where it is known."""
 
     def __init__(self, starts, lengths, table, *, max_new: int = None, max_length: int = None):
         for hint, what, most in ((max_new, "max_new", MAX_TOKENS), (max_length, "max_length", MAX_SLOTS)):
@@ -691,7 +692,8 @@ def rope_cache(cache: Cache, batch: Batch, *, q=None, k=None, v=None, frequencie
     adjacent, other strides free.  frequencies: float64 [n_rot/2] on the device (rope_frequencies); the first n_rot
     channels of a head are rotated, "half" (i with i + n_rot/2) or "interleaved" (2i with 2i + 1), and times magnitude;
     None: nothing turns.  positions: int32 [n_tok], or the tokens' slots.  Returns the queries, of `dtype` (None: that of
-    the cache where q is float32, else q's) or in `out` (which may be q), or None without q."""
+    the cache where q is float32, else q's) or in `out` (which may be q), or None without q.  Rows of tokens of no
+    sequence are not set."""
     x = q if q is not None else k if k is not None else v
     if x is None:
         raise QmmError(EINVAL, "rope_cache needs q, k or v")
@@ -777,8 +779,8 @@ def attention(q, cache: Cache, batch: Batch, *, scale: float = None, causal: boo
     causal: a token sees the slots up to its own, with window only the last `window` of them; else all in use (an
     encoder's states).  scale: head_dim ** -0.5 if None.  The result is [n_tok][heads][head_dim] of q's type, or with
     dtype "q8" the qact buffer of its rows (the output product's input), or `out`: [n_tok][heads * head_dim], rows may be
-    strided, or a qact buffer with dtype "q8".  A token that sees nothing gets zeros.  work: a uint8 tensor of
-    attention_plan's work_bytes; new memory without it."""
+    strided, or a qact buffer with dtype "q8".  A token that sees nothing gets zeros; rows of tokens of no sequence are not
+    set.  work: a uint8 tensor of attention_plan's work_bytes; new memory without it."""
     shape = q.shape
     if len(shape) != 3:
         raise QmmError(EINVAL, "q must be [n_tok][heads][head_dim]")

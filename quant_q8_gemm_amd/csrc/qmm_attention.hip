@@ -17,7 +17,7 @@ namespace {
 // and LANES such sets for a row, which share its splits and are joined in LDS.  Loads go out
 // four splits at a time: there are few threads when this kernel matters, and a load after
 // the other would be all of its time.  Latency bounds it then: 64 rows of 24 splits 5.1 us, 32 of 13
-// 3.9 us; of many rows the partial results' bytes: 81920 rows of two splits 32.8 us (3.2 TB/s).
+// 4.0 us; of many rows the partial results' bytes: 81920 rows of two splits 34.4 us (3.0 TB/s).
 template <int TYPE, int LANES>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Batch batch, int dim) {
   __shared__ float4 parts[256];
@@ -117,11 +117,11 @@ AttnPlan plan_attention(int type, int heads, int kv_heads, int dim, int64_t n_se
   // and the partial results' way through memory.  A tile takes a work-group of many columns
   // about 1 us, or 0.6 with two groups of waves, and of heads past 128 by as much more; one of few
   // what the active ones' tiles take from memory, 0.3 at least.  Measured:
-  // one token of 32 heads over 3314 slots with 1, 4, 16 splits 22.9, 15.8, 16.2 us; 16 sequences of
-  // 20 heads of 64 over up to 1500 with 1, 2, 4: 15.7, 18.3, 20.3; one token of 64/8 heads over 131072
-  // with 8, 16, 32: 167, 109, 105; 2048 tokens of 40/8 heads over 32768 with 1, 2, 4: 1524, 1347, 1353;
-  // 100 tokens of 16/4 heads over 3000 in q8 with 1, 2, 4, 8, 16: 64.8, 40.5, 28.8, 25.4, 25.9, of 256
-  // 196, 106, 62, 46, 39.
+  // one token of 32 heads over 3314 slots with 1, 4, 16 splits 21.6, 15.9, 16.5 us; 16 sequences of
+  // 20 heads of 64 over up to 1500 with 1, 2, 4: 15.4, 17.8, 19.7; one token of 64/8 heads over 131072
+  // with 8, 16, 32: 167, 109, 106; 2048 tokens of 40/8 heads over 32768 with 1, 2, 4: 1605, 1339, 1301;
+  // 100 tokens of 16/4 heads over 3000 in q8 with 1, 2, 4, 8, 16: 65.1, 40.8, 29.2, 25.9, 26.3, of 256
+  // 196, 106, 62, 46, 41.
   const double start = plan.few ? 3.0 : 8.0, join = plan.few ? 4.5 : 10.0, partial_mb = (double)n_tok * heads * dim * 8e-6;
   const int64_t least = plan.few ? 4 : 8, unit = plan.few ? 4 : 2;
   int64_t share = tiles;

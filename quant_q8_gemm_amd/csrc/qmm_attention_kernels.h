@@ -17,8 +17,8 @@ namespace {
 // 32-slot tiles, each with a running softmax of its own, straight from memory into the
 // operands' registers: a tile's keys and values are on their way while the one before
 // is worked on.  The waves' results are joined in LDS, the splits' by a second kernel.
-// Measured: one token of 64/8 heads of 128 over 131072 bf16 slots 91.8 us (5.8 TB/s); of 32/32 over
-// 3314 f16 slots 13.0 us (4.2 TB/s); 32 sequences of up to 8192 q8 slots, 32/8 heads, 79.8 us (4.1 TB/s;
+// Measured: one token of 64/8 heads of 128 over 131072 bf16 slots 91.4 us (5.9 TB/s); of 32/32 over
+// 3314 f16 slots 12.6 us (4.3 TB/s); 32 sequences of up to 8192 q8 slots, 32/8 heads, 78.3 us (4.2 TB/s;
 // of 8192 each 5.2).
 
 // A tile's keys or values as loaded.
@@ -194,9 +194,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DB <
 // four waves, which take turns over the keys with stages of their own: a wave of a
 // SIMD by itself leaves it idle for half of the time (scores, powers and the second product
 // of a tile wait for each other), and a second one fills that.
-// Measured: 2048 tokens of 40/8 heads of 128 over 32768 bf16 slots 1,233 us (1.08 PFLOP/s, the matrix core
+// Measured: 2048 tokens of 40/8 heads of 128 over 32768 bf16 slots 1,262 us (1.05 PFLOP/s, the matrix core
 // busy for 54% of the cycles; the softmax's vector instructions add to its time); a prompt of 4096 of
-// 32/8 heads of 256 in f16 278 us (0.99), of 3314 of 32/32 of 128 113 us (0.79); with two groups
+// 32/8 heads of 256 in f16 278 us (0.99), of 3314 of 32/32 of 128 115 us (0.79); with two groups
 // 4 x 448 tokens over 1501 states, 16 heads of 96, 36.5 -> 31 us.
 
 // N consecutive 1 KiB copies from base + 16*lane to LDS; M0 is set by each run itself, and

@@ -12,8 +12,8 @@
 // 256 bytes (a lane's eight channels are one piece of the tile) and values as
 // runs of 512 (a lane gathers eight tokens of a channel, so that only the first
 // and last slots of a chunk are written one by one).
-// Measured: 3314 tokens of 32 + 32 heads of 128 from f32 49.7 us (4.9 TB/s, a copy's rate); 24 chunks of
-// 1674 tokens, 40 + 8 heads, into q8 15.8 us (2.6 TB/s), where work-groups' starts bound it; one token
+// Measured: 3314 tokens of 32 + 32 heads of 128 from f32 50.1 us (4.9 TB/s, a copy's rate); 24 chunks of
+// 1674 tokens, 40 + 8 heads, into q8 16.2 us (2.5 TB/s), where work-groups' starts bound it; one token
 // 4.9 us, all of it a work-group's path.
 #include "qmm_cache.h"
 #include "qmm_common.h"
@@ -362,7 +362,7 @@ __global__ __launch_bounds__(kThreads, CACHE == QMM_Q8 ? 3 : 4) void rope_kernel
 
 // The cache read back, 16 slots of some heads at a time: of keys a thread takes eight
 // channels of a slot, of values eight slots of a channel, as they lie in the tiles.  Of few
-// tokens a work-group's path bounds it: 1674 of 8 heads of 128 from q8 7.5 us (10 MB).
+// tokens a work-group's path bounds it: 1674 of 8 heads of 128 from q8 7.3 us (10 MB).
 template <int CACHE, int OUT>
 __global__ __launch_bounds__(kThreads) void read_kernel(Pools pools, Batch batch, int heads_per_job, void* k, void* v) {
   typedef elem_t<OUT> T;
