@@ -505,14 +505,16 @@ size_t qmm_cache_page_bytes(int type, int heads, int head_dim, int page);
  * The arrays are device memory, read when the kernels run.  Whatever they hold,
  * nothing outside the tensors and pools is read or written: a start is taken
  * within [0, n_tok] and as the highest up to it, so that no token has two
- * sequences, lengths within the table's columns; tokens without a slot (more than lengths[s]) and pages outside the pool are not
- * followed: nothing is stored to them, and their keys are not seen.
+ * sequences, lengths within the table's columns; tokens without a slot (more than
+ * lengths[s]) and pages outside the pool are not followed: nothing is stored to
+ * them, and their keys are not seen.
  * max_new, max_length: the most tokens and the most slots of any sequence, to size
- * the launch by.  They do not change which keys are seen.  Sequences that pass them
- * are worked through all the same, only slower; a max_length far above the lengths is
- * slower too, since attention takes a part of the keys to be of the size that it
- * would have in a sequence of max_length (one token of 32/8 heads of 128 over 3314
- * slots: 11.2 us with 3314, 12.9 with 8192, 17.1 with 32768, 25.8 with 131072). */
+ * the launch by; a result does not go by them, but for its roundings.  Sequences
+ * that pass them are worked through all the same, only slower; a max_length far above
+ * the lengths is slower too, since attention's parts of the keys are then of the size
+ * that they have in a sequence of max_length (one token of 32/8 heads of 128 over
+ * 3314 slots: 11.2 us with 3314, 12.9 with 8192, 17.1 with 32768, 25.8 with
+ * 131072). */
 #define QMM_MAX_SEQS 65535
 #define QMM_MAX_SLOTS (1 << 30) /* of a sequence */
 typedef struct {
@@ -638,8 +640,8 @@ typedef struct {
  * Scores times scale stay below 2^126 in size, and values times the number of keys
  * below 2^120 (bf16), or are no numbers in what comes of them.  A token that sees no
  * key, or none whose score is above -infinity, gets zeros, whatever the values are.
- * What a token does not see is no part of its result, whatever is stored there.  An output
- * in q8 blocks has its padding tokens zero; rows of tokens of no sequence are
+ * What a token does not see is no part of its result, whatever is stored there.  An
+ * output in q8 blocks has its padding tokens zero; rows of tokens of no sequence are
  * left as they are.
  *   work      device memory of at least the plan's work_bytes (qmm_attention_plan),
  *             16-byte aligned; NULL with 0 where it needs none.  Calls that share it

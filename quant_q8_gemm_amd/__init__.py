@@ -634,7 +634,7 @@ class Batch:
     int32 [n_seq] (slots in use, the call's tokens the last of them), table int32 [n_seq][columns] (page numbers), all
     on the device and read there, so that a captured graph takes what they hold when it is replayed.  max_new and
     max_length: the most tokens and slots of any sequence (None: what a sequence can have at most); they size
-    the launch and change no result.  Sequences that pass them take longer, and so does attention over ones far shorter than
+    the launch, and change a result in its roundings at most.  Sequences that pass them take longer, and so does attention over ones far shorter than
     max_length, None among them: give the longest length where it is known."""
 
     def __init__(self, starts, lengths, table, *, max_new: int = None, max_length: int = None):

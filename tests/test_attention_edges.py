@@ -120,3 +120,25 @@ def test_keys_of_small_weight(device, dtype, new, max_length, far):
     off = want * (u + 2 * (far * 4 * f + 2.0 ** -22) + 2 * (n + 64) * f) + n * (2.0 ** -33 if p.type == F16 else 2.0 ** -126)
     off += paged.HALF[p.type] * (want + off) + (2.0 ** -25 if p.type == F16 else 0.0)
     assert float((out - want).abs().max()) <= off, (float((out - want).abs().max()), off, want)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", CACHES, ids=str)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_queries_that_are_no_numbers(device, dtype, dim, bad):
+    """One query with a channel that is no finite number: its own row is no number, and all others keep their bits."""
+    for news, lens in (([1, 3], [40, 33]), ([70], [75]), ([40, 5], [90, 3001])):
+        p = paged.Paged(news, lens, 4, 2, dim, dtype, junk=3.0)
+        cache, batch, q = p.cuda(qmm)
+        clean = qmm.attention(q, cache, batch).clone()
+        for row in (0, sum(news) - 1):
+            x = q.clone()
+            x[row, 2, 5] = bad
+            out = qmm.attention(x, cache, batch)
+            torch.cuda.synchronize()
+            own = out[row, 2].clone()
+            if bad != bad:
+                assert bool(own.isnan().all())
+            out[row, 2] = clean[row, 2]
+            assert torch.equal(out, clean)
